@@ -114,6 +114,13 @@ def load(build_if_missing: bool = True):
         "moe_quantize_rows_fp8": ([P, ctypes.c_longlong, I, P, P], I),
         "moe_layer_forward_fp8": ([ctypes.POINTER(MoeShape), ctypes.POINTER(MoeWeightsFp8),
                                    ctypes.POINTER(MoeRouting), P, P, P, P, P, P, P, Z, P], I),
+        "moe_layer_norm": ([P, I, P, P, I, I, ctypes.c_float, P, P, P, P], I),
+        "moe_layer_norm_backward_workspace_bytes": ([I, I], Z),
+        "moe_layer_norm_backward": ([P, P, I, P, P, P, P, I, I, P, P, P, P, Z, P], I),
+        "moe_route_logits": ([P, I, P, I, I, I, ctypes.POINTER(MoeRouting), P, P, P], I),
+        "moe_route_logits_backward": ([P, I, I, I, I, ctypes.POINTER(MoeRouting), P, P, P, P], I),
+        "moe_checkpoint_pack": ([P, ctypes.c_longlong, I, P, P, P], I),
+        "moe_checkpoint_unpack": ([P, P, ctypes.c_longlong, I, P, P], I),
         "moe_grace_metrics": ([P, I, P, I, P, P], I),
         "moe_grace_group": ([P, I, I, ctypes.c_double, P], I),
         "moe_grace_choose_r": ([P, I, I, P, I, P, P, P, P], I),
@@ -129,6 +136,7 @@ def load(build_if_missing: bool = True):
 
 
 BF16, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+I8 = torch.int8
 
 
 def _chk(t, dtype=None, numel=None, name="tensor"):
@@ -387,6 +395,79 @@ def moe_layer_forward_fp8(shape: MoeShape, weights8: dict, routing, X, Y, topk_i
     _check("moe_layer_forward_fp8", load().moe_layer_forward_fp8(
         ctypes.byref(shape), ctypes.byref(w), _routing(routing), *_ptrs(*io), _ptr(ws),
         ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# -------------------------------------------------------------- training around the layer
+def _fp32_flag(t, name):
+    if t.dtype not in (BF16, F32):
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {BF16} or {F32}")
+    return 1 if t.dtype == F32 else 0
+
+
+def moe_layer_norm(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
+    """x bf16 or fp32 [T, H] -> y bf16; beta, mean and rstd may be None."""
+    T, H = x.shape
+    f = _fp32_flag(x, "x")
+    xp, g, b, yp, m, r = _ptrs((x, x.dtype, T * H, "x"), (gamma, F32, H, "gamma"), (beta, F32, H, "beta"),
+                               (y, BF16, T * H, "y"), (mean, F32, T, "mean"), (rstd, F32, T, "rstd"))
+    _check("moe_layer_norm", load().moe_layer_norm(xp, f, g, b, T, H, float(eps), yp, m, r,
+                                                   _stream(stream)))
+
+
+def moe_layer_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return int(load().moe_layer_norm_backward_workspace_bytes(int(T), int(H)))
+
+
+def moe_layer_norm_backward(dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream=None):
+    """dres: a gradient of x's type to add to dx, or None."""
+    T, H = x.shape
+    f = _fp32_flag(x, "x")
+    d, xp, g, m, r, e, o, dg, db = _ptrs(
+        (dy, BF16, T * H, "dy"), (x, x.dtype, T * H, "x"), (gamma, F32, H, "gamma"), (mean, F32, T, "mean"),
+        (rstd, F32, T, "rstd"), (dres, x.dtype, T * H, "dres"), (dx, x.dtype, T * H, "dx"),
+        (dgamma, F32, H, "dgamma"), (dbeta, F32, H, "dbeta"))
+    _check("moe_layer_norm_backward", load().moe_layer_norm_backward(
+        d, xp, f, g, m, r, e, T, H, o, dg, db, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_route_logits(logits, bias, K, routing, topk_idx, topk_w, stream=None):
+    """logits bf16 or fp32 [T, E]; bias may be None; routing as in moe_router_topk_ex."""
+    T, E = logits.shape
+    K, f = int(K), _fp32_flag(logits, "logits")
+    l, b, i, w = _ptrs((logits, logits.dtype, T * E, "logits"), (bias, F32, E, "bias"),
+                       (topk_idx, I32, T * K, "topk_idx"), (topk_w, F32, T * K, "topk_w"))
+    _check("moe_route_logits", load().moe_route_logits(l, f, b, T, E, K, _routing(routing), i, w,
+                                                       _stream(stream)))
+
+
+def moe_route_logits_backward(logits, routing, topk_idx, d_topk_w, d_logits, stream=None):
+    T, E = logits.shape
+    K, f = topk_idx.shape[1], _fp32_flag(logits, "logits")
+    l, i, w, d = _ptrs((logits, logits.dtype, T * E, "logits"), (topk_idx, I32, T * K, "topk_idx"),
+                       (d_topk_w, F32, T * K, "d_topk_w"), (d_logits, logits.dtype, T * E, "d_logits"))
+    _check("moe_route_logits_backward", load().moe_route_logits_backward(
+        l, f, T, E, K, _routing(routing), i, w, d, _stream(stream)))
+
+
+def moe_checkpoint_pack(x, q=None, scale=None, stream=None):
+    """x bf16 [rows, n] -> (E4M3 bytes uint8 [rows, n], scale exponents int8
+    [rows, ceil(n / 128)]), into q and scale where given."""
+    rows, n = x.shape
+    nb = (n + 127) // 128
+    q = torch.empty(rows, n, dtype=U8, device=x.device) if q is None else q
+    scale = torch.empty(rows, nb, dtype=I8, device=x.device) if scale is None else scale
+    xp, qp, sp = _ptrs((x, BF16, rows * n, "x"), (q, U8, rows * n, "q"), (scale, I8, rows * nb, "scale"))
+    _check("moe_checkpoint_pack", load().moe_checkpoint_pack(xp, rows, n, qp, sp, _stream(stream)))
+    return q, scale
+
+
+def moe_checkpoint_unpack(q, scale, out=None, stream=None):
+    rows, n = q.shape
+    out = torch.empty(rows, n, dtype=BF16, device=q.device) if out is None else out
+    qp, sp, o = _ptrs((q, U8, rows * n, "q"), (scale, I8, rows * ((n + 127) // 128), "scale"),
+                      (out, BF16, rows * n, "out"))
+    _check("moe_checkpoint_unpack", load().moe_checkpoint_unpack(qp, sp, rows, n, o, _stream(stream)))
+    return out
 
 
 # ------------------------------------------------------------------- convenience wrapper

@@ -663,4 +663,102 @@ int moe_quantize_rows_fp8(const void *in, long long rows, int n, void *out, void
     return cuda_status(launch_quant_rows(in, rows, n, out, static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------- training around the layer
+static int check_norm(int T, int H)
+{
+    if (T < 0 || H <= 0) return MOE_ERR_INVALID_ARG;
+    return H % 64 || H > 16384 ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+}
+
+int moe_layer_norm(const void *x, int x_fp32, const float *gamma, const float *beta, int T, int H,
+                   float eps, void *y, float *mean, float *rstd, void *stream)
+{
+    int rc = check_norm(T, H);
+    if (rc) return rc;
+    if ((x_fp32 != 0 && x_fp32 != 1) || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((rc = check_ptrs({x, gamma, y}))) return rc;
+    if ((rc = check_opt(beta)) || (rc = check_opt(mean)) || (rc = check_opt(rstd))) return rc;
+    return cuda_status(launch_norm(x, x_fp32, gamma, beta, T, H, eps, y, mean, rstd,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_layer_norm_backward_workspace_bytes(int T, int H)
+{
+    if (check_norm(T, H) != MOE_OK) return 0;
+    return kHeader + al256(static_cast<size_t>(norm_bwd_ctas(T, H)) * 2 * H * sizeof(float));
+}
+
+int moe_layer_norm_backward(const void *dy, const void *x, int x_fp32, const float *gamma,
+                            const float *mean, const float *rstd, const void *dres, int T, int H,
+                            void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                            void *stream)
+{
+    int rc = check_norm(T, H);
+    if (rc) return rc;
+    if (x_fp32 != 0 && x_fp32 != 1) return MOE_ERR_INVALID_ARG;
+    if ((rc = check_ptrs({dgamma, dbeta}))) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {    // the sums over no rows
+        if (cudaMemsetAsync(dgamma, 0, H * sizeof(float), st) != cudaSuccess) return MOE_ERR_CUDA;
+        return cuda_status(cudaMemsetAsync(dbeta, 0, H * sizeof(float), st));
+    }
+    if ((rc = check_ptrs({dy, x, gamma, mean, rstd, dx})) || (rc = check_opt(dres))) return rc;
+    if ((rc = check_ws(ws, ws_bytes, moe_layer_norm_backward_workspace_bytes(T, H)))) return rc;
+    return cuda_status(launch_norm_bwd(dy, x, x_fp32, gamma, mean, rstd, dres, T, H, dx, dgamma, dbeta,
+                                       reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeader), st));
+}
+
+int moe_route_logits(const void *logits, int logits_fp32, const float *bias, int T, int E, int K,
+                     const moe_routing_t *routing, int32_t *topk_idx, float *topk_w, void *stream)
+{
+    int rc = check_common(T, 64, E, K);
+    if (rc) return rc;
+    RoutingOpts ro;
+    if ((rc = check_routing(routing, E, K, ro))) return rc;
+    if (logits_fp32 != 0 && logits_fp32 != 1) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((rc = check_ptrs({logits, topk_idx, topk_w})) || (rc = check_opt(bias))) return rc;
+    return cuda_status(launch_route(logits, logits_fp32, bias, T, E, K, ro, topk_idx, topk_w,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+int moe_route_logits_backward(const void *logits, int logits_fp32, int T, int E, int K,
+                              const moe_routing_t *routing, const int32_t *topk_idx,
+                              const float *d_topk_w, void *d_logits, void *stream)
+{
+    int rc = check_common(T, 64, E, K);
+    if (rc) return rc;
+    RoutingOpts ro;
+    if ((rc = check_routing(routing, E, K, ro))) return rc;
+    if (logits_fp32 != 0 && logits_fp32 != 1) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((rc = check_ptrs({logits, topk_idx, d_topk_w, d_logits}))) return rc;
+    return cuda_status(launch_route_bwd(logits, logits_fp32, T, E, K, ro, topk_idx, d_topk_w, d_logits,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+static int check_ckpt(long long rows, int n)
+{
+    if (rows < 0 || n <= 0) return MOE_ERR_INVALID_ARG;
+    if (n % 64 || rows > 0x7fffffffll / ((n + 127) / 128)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+int moe_checkpoint_pack(const void *x, long long rows, int n, void *q, int8_t *scale, void *stream)
+{
+    int rc = check_ckpt(rows, n);
+    if (rc || rows == 0) return rc;
+    if ((rc = check_ptrs({x, q, scale}))) return rc;
+    return cuda_status(launch_ckpt_pack(x, rows, n, q, scale, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_checkpoint_unpack(const void *q, const int8_t *scale, long long rows, int n, void *x, void *stream)
+{
+    int rc = check_ckpt(rows, n);
+    if (rc || rows == 0) return rc;
+    if ((rc = check_ptrs({q, scale, x}))) return rc;
+    return cuda_status(launch_ckpt_unpack(q, scale, rows, n, x, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

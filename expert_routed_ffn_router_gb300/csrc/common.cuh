@@ -98,6 +98,22 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float hi, float lo)
     return d;
 }
 
+// Scale exponent of a checkpoint block: fp8_scale_exp, and the largest for a block that
+// holds an infinity (frexp gives it no exponent), so that it comes back infinite.
+__device__ __forceinline__ int ckpt_scale_exp(float amax)
+{
+    return amax > 3.402823466e38f ? kFp8MaxExp : fp8_scale_exp(amax);
+}
+
+// Eight E4M3 bytes times a power-of-two scale -> eight bf16 (exact).
+__device__ __forceinline__ uint4 e4m3x8_to_bf16x8(uint2 u, float s)
+{
+    const float2 a = e4m3x2_to_f32x2(static_cast<uint16_t>(u.x)), b = e4m3x2_to_f32x2(static_cast<uint16_t>(u.x >> 16));
+    const float2 c = e4m3x2_to_f32x2(static_cast<uint16_t>(u.y)), d = e4m3x2_to_f32x2(static_cast<uint16_t>(u.y >> 16));
+    return make_uint4(f32x2_to_bf16x2(a.y * s, a.x * s), f32x2_to_bf16x2(b.y * s, b.x * s),
+                      f32x2_to_bf16x2(c.y * s, c.x * s), f32x2_to_bf16x2(d.y * s, d.x * s));
+}
+
 // ------------------------------------------------------------------------ status word
 // The first int of every workspace records device-side conditions (bounded waits that ran
 // out, indices out of range).  The first error wins.

@@ -80,6 +80,29 @@ cudaError_t launch_quant_rows_e4m3(const void *in, long long rows, int n, void *
 cudaError_t launch_combine(const void *Yp, const int32_t *slot_pos, const float *topk_w,
                            const float *Ysh, int T, int H, int K, float *Y, cudaStream_t s);
 
+// ------------------------------------------------------------------------- layer norm
+// Rows x [T][H] (bf16, or fp32) -> y bf16; mean and rstd [T] (nullable) for the backward pass.
+cudaError_t launch_norm(const void *x, int x_fp32, const float *gamma, const float *beta, int T, int H,
+                        float eps, void *y, float *mean, float *rstd, cudaStream_t s);
+// CTAs of the backward launch; each leaves 2 H partial sums in `part`.
+int norm_bwd_ctas(int T, int H);
+cudaError_t launch_norm_bwd(const void *dy, const void *x, int x_fp32, const float *gamma, const float *mean,
+                            const float *rstd, const void *dres, int T, int H, void *dx, float *dgamma,
+                            float *dbeta, float *part, cudaStream_t s);
+
+// --------------------------------------------------------------- routing from given logits
+cudaError_t launch_route(const void *logits, int fp32, const float *bias, int T, int E, int K,
+                         const RoutingOpts &ro, int32_t *idx, float *w, cudaStream_t s);
+cudaError_t launch_route_bwd(const void *logits, int fp32, int T, int E, int K, const RoutingOpts &ro,
+                             const int32_t *idx, const float *dw, void *dl, cudaStream_t s);
+
+// ------------------------------------------------------------------ 8-bit checkpoint rows
+// bf16 rows [rows][n] (n a multiple of 64) <-> E4M3 bytes and int8 exponents
+// [rows][ceil(n / 128)]; rows * ceil(n / 128) < 2^31.
+cudaError_t launch_ckpt_pack(const void *in, long long rows, int n, void *q, int8_t *sc, cudaStream_t s);
+cudaError_t launch_ckpt_unpack(const void *q, const int8_t *sc, long long rows, int n, void *out,
+                               cudaStream_t s);
+
 // ------------------------------------------------------------------------------ FFN
 // One grouped problem of the expert FFN: rows of group g are [offsets[g], offsets[g+1])
 // (or one dense group of `dense_rows` rows when offsets == nullptr).

@@ -378,6 +378,71 @@ int moe_layer_forward_fp8(const moe_shape_t *shape, const moe_weights_fp8_t *wei
                           void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------------------
+ * Training around the layer.  The pages describe inference only: these entry points are
+ * additions of this library, in its conventions.  They differentiate the layer's readings
+ * above (scores, renormalised weights, SwiGLU).  For an empty batch (T or rows == 0) the
+ * pointers of arrays that it leaves empty may be NULL.
+ * ------------------------------------------------------------------------------------ */
+
+/* Layer norm of the token rows (the norm in front of the layer): per row
+ *     y = gamma * (x - mu) * rstd + beta,  mu = mean(x), rstd = (mean((x - mu)^2) + eps)^-1/2
+ *   x      [T, H], bf16 (x_fp32 == 0) or fp32 (x_fp32 == 1: an fp32 residual stream)
+ *   gamma  fp32 [H], beta fp32 [H] or NULL (no shift)
+ *   out y  bf16 [T, H]; mean, rstd fp32 [T] (each nullable: kept for the backward pass)
+ * Sums are fp32, the variance is that of the centred row.  H a multiple of 64, at most 16384
+ * (else MOE_ERR_UNSUPPORTED_SHAPE); eps < 0 or NaN: MOE_ERR_INVALID_ARG. */
+int moe_layer_norm(const void *x, int x_fp32, const float *gamma, const float *beta, int T, int H,
+                   float eps, void *y, float *mean, float *rstd, void *stream);
+
+/* Backward pass of moe_layer_norm.  With xh = (x - mean) rstd and a = gamma dy:
+ *     dx = rstd (a - mean(a) - xh mean(a xh)) (+ dres),  dgamma = sum_t dy xh,  dbeta = sum_t dy
+ *   dy bf16 [T, H]; x, gamma as in the forward call, mean and rstd as it left them
+ *   dres   [T, H] in the type of x, or NULL: a gradient that bypasses the norm (the residual
+ *          branch's), added in fp32 before dx is rounded; it may be dx's own buffer
+ *   out dx [T, H] in the type of x; dgamma, dbeta fp32 [H]
+ *   ws     at least moe_layer_norm_backward_workspace_bytes(T, H) bytes (0 for an invalid
+ *          shape): partial sums of the weight gradients, added in a fixed order
+ * T == 0 sets dgamma and dbeta to 0 (ws and the row arrays may then be NULL). */
+size_t moe_layer_norm_backward_workspace_bytes(int T, int H);
+int moe_layer_norm_backward(const void *dy, const void *x, int x_fp32, const float *gamma,
+                            const float *mean, const float *rstd, const void *dres, int T, int H,
+                            void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* Routing from given gate logits (a gate the caller computes: fp32, masked, with noise): the
+ * scoring, selection and weights of moe_router_topk_ex, without its gate GEMM.
+ *   logits [T, E], bf16 (logits_fp32 == 0) or fp32 (logits_fp32 == 1)
+ *   bias   fp32 [E] or NULL (selection only)
+ *   out topk_idx int32 [T, K], topk_w fp32 [T, K] as moe_router_topk_ex; options and errors
+ *   as there.  The selection is the one exact arithmetic gives on these logits.
+ * A logit at or below bf16's lowest finite value (-3.3895e38: -inf, either type's lowest)
+ * masks its expert: score 0, and chosen only when its kept groups hold nothing else, lowest
+ * index first.  Weights whose sum is 0 (a row with nothing left) are 0.  A row with a NaN
+ * still gets K distinct experts in [0, E); its weights may be NaN. */
+int moe_route_logits(const void *logits, int logits_fp32, const float *bias, int T, int E, int K,
+                     const moe_routing_t *routing, int32_t *topk_idx, float *topk_w, void *stream);
+
+/* Gradient of topk_w with respect to the logits (the selection is held fixed; the bias has
+ * none).  Of `routing`, scoring and renorm matter.
+ *   logits, topk_idx as in the forward call; d_topk_w fp32 [T, K]
+ *   out d_logits [T, E] in the type of the logits, every entry written
+ * An index outside [0, E) contributes nothing; the indices of a token are distinct.  Rows
+ * whose weights are 0 get a zero gradient. */
+int moe_route_logits_backward(const void *logits, int logits_fp32, int T, int E, int K,
+                              const moe_routing_t *routing, const int32_t *topk_idx,
+                              const float *d_topk_w, void *d_logits, void *stream);
+
+/* 8-bit checkpoint of activation rows: x bf16 [rows, n] -> q E4M3 bytes [rows, n] and scale
+ * int8 [rows, ceil(n / 128)], the exponents k of the blocks' scales 2^k (the FP8 section's
+ * format: k the smallest integer with amax <= 448 * 2^k, in [-124, 127]; round to nearest
+ * even).  n a multiple of 64, rows * ceil(n / 128) < 2^31 (else MOE_ERR_UNSUPPORTED_SHAPE).
+ * A NaN stays a NaN; a block with an infinity has k = 127 and comes back infinite there.
+ * moe_checkpoint_unpack writes the values q * 2^k (exact in bf16) to x bf16 [rows, n]. */
+int moe_checkpoint_pack(const void *x, long long rows, int n, void *q, int8_t *scale, void *stream);
+int moe_checkpoint_unpack(const void *q, const int8_t *scale, long long rows, int n, void *x,
+                          void *stream);
+
+/* ------------------------------------------------------------------------------------
  * GRACE-MoE placement planner ("GRACE-MoE" notes, Core Idea 1-3).  Host code on HOST
  * pointers: it consumes the counts and the affinity matrix moe_layer_forward produces
  * (copied to the host by the caller) and plans where experts go for expert parallelism
