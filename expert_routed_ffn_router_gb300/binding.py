@@ -121,6 +121,8 @@ def load(build_if_missing: bool = True):
         "moe_route_logits_backward": ([P, I, I, I, I, ctypes.POINTER(MoeRouting), P, P, P, P], I),
         "moe_checkpoint_pack": ([P, ctypes.c_longlong, I, P, P, P], I),
         "moe_checkpoint_unpack": ([P, P, ctypes.c_longlong, I, P, P], I),
+        "moe_expert_ffn_backward_workspace_bytes": ([I, I, I, I, I], Z),
+        "moe_expert_ffn_backward": ([P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P, P, P, Z, P], I),
         "moe_grace_metrics": ([P, I, P, I, P, P], I),
         "moe_grace_group": ([P, I, I, ctypes.c_double, P], I),
         "moe_grace_choose_r": ([P, I, I, P, I, P, P, P, P], I),
@@ -468,6 +470,28 @@ def moe_checkpoint_unpack(q, scale, out=None, stream=None):
                       (out, BF16, rows * n, "out"))
     _check("moe_checkpoint_unpack", load().moe_checkpoint_unpack(qp, sp, rows, n, o, _stream(stream)))
     return out
+
+
+def moe_expert_ffn_backward_workspace_bytes(T, H, E, K, I) -> int:
+    return int(load().moe_expert_ffn_backward_workspace_bytes(T, H, E, K, I))
+
+
+def moe_expert_ffn_backward(x, x_scale, dY, offsets, slot_pos, topk_w, W1, W3, W2, dX, d_topk_w,
+                            dW1, dW3, dW2, ws, stream=None):
+    """x bf16 with x_scale None, or a checkpoint's (q, scale); topk_w (all 1) and d_topk_w (not
+    wanted) may be None."""
+    T, H = x.shape
+    E, _, I = W1.shape
+    K, n = slot_pos.shape[1], E * H * I
+    xp, xs, dy, o, sp, w, w1, w3, w2, dx, dw, d1, d3, d2 = _ptrs(
+        (x, BF16 if x_scale is None else U8, T * H, "x"), (x_scale, I8, T * ((H + 127) // 128), "x_scale"),
+        (dY, BF16, T * H, "dY"), (offsets, I32, E + 1, "offsets"), (slot_pos, I32, T * K, "slot_pos"),
+        (topk_w, F32, T * K, "topk_w"), (W1, BF16, n, "W1"), (W3, BF16, n, "W3"), (W2, BF16, n, "W2"),
+        (dX, BF16, T * H, "dX"), (d_topk_w, F32, T * K, "d_topk_w"), (dW1, BF16, n, "dW1"),
+        (dW3, BF16, n, "dW3"), (dW2, BF16, n, "dW2"))
+    _check("moe_expert_ffn_backward", load().moe_expert_ffn_backward(
+        xp, xs, dy, o, sp, w, T, H, E, K, I, w1, w3, w2, dx, dw, d1, d3, d2, _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
 
 
 # ------------------------------------------------------------------- convenience wrapper

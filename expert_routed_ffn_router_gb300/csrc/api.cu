@@ -761,4 +761,46 @@ int moe_checkpoint_unpack(const void *q, const int8_t *scale, long long rows, in
     return cuda_status(launch_ckpt_unpack(q, scale, rows, n, x, static_cast<cudaStream_t>(stream)));
 }
 
+static int check_ffn_bwd(int T, int H, int E, int K, int I)
+{
+    const int rc = check_common(T, H, E, K);
+    if (rc) return rc;
+    if (I <= 0) return MOE_ERR_INVALID_ARG;
+    if (I % 64 || ffn_bwd_rows(T, E, K) >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+size_t moe_expert_ffn_backward_workspace_bytes(int T, int H, int E, int K, int I)
+{
+    if (check_ffn_bwd(T, H, E, K, I) != MOE_OK) return 0;
+    return kHeader + ffn_bwd_bytes(T, H, E, K, I);
+}
+
+int moe_expert_ffn_backward(const void *x, const int8_t *x_scale, const void *dY,
+                            const int32_t *offsets, const int32_t *slot_pos, const float *topk_w,
+                            int T, int H, int E, int K, int I, const void *W1, const void *W3,
+                            const void *W2, void *dX, float *d_topk_w, void *dW1, void *dW3, void *dW2,
+                            void *ws, size_t ws_bytes, void *stream)
+{
+    int rc = check_ffn_bwd(T, H, E, K, I);
+    if (rc) return rc;
+    if ((rc = check_ptrs({dW1, dW3, dW2}))) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {    // the sums over no rows
+        const size_t n = static_cast<size_t>(E) * H * I * 2;
+        for (void *d : {dW1, dW3, dW2})
+            if (cudaMemsetAsync(d, 0, n, st) != cudaSuccess) return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    if ((rc = check_ptrs({x, dY, offsets, slot_pos, W1, W3, W2, dX}))) return rc;
+    if ((rc = check_opt(x_scale)) || (rc = check_opt(topk_w)) || (rc = check_opt(d_topk_w))) return rc;
+    if ((rc = check_ws(ws, ws_bytes, kHeader + ffn_bwd_bytes(T, H, E, K, I)))) return rc;
+    const FfnBwd f{x, x_scale, dY, offsets, slot_pos, topk_w, T, H, E, K, I, W1, W3, W2, dX, d_topk_w,
+                   dW1, dW3, dW2};
+    return debug_status(cuda_status(launch_ffn_bwd(f, static_cast<unsigned char *>(ws) + kHeader,
+                                                   static_cast<int *>(ws), g_wait_limit_ns,
+                                                   g_inject_stall, st)),
+                        ws, stream);
+}
+
 }  // extern "C"

@@ -186,6 +186,26 @@ cudaError_t launch_ffn(const FfnProblem *probs, int n_probs, int H, const int *I
 // over all its problems.
 size_t ffn_ready_slots(long long rows, int n_groups);
 
+// Backward pass of the routed expert FFN (with its dispatch and combine): the public
+// moe_expert_ffn_backward's arguments, validated.
+struct FfnBwd {
+    const void *x;             // token rows [T][H]: bf16, or E4M3 with x_scale
+    const int8_t *x_scale;     // [T][ceil(H / 128)] or nullptr
+    const void *dY;            // bf16 [T][H]
+    const int32_t *offsets;    // [E + 1]
+    const int32_t *slot_pos;   // [T][K]
+    const float *topk_w;       // [T][K] or nullptr (all 1)
+    int T, H, E, K, I;
+    const void *W1, *W3, *W2;
+    void *dX;                  // bf16 [T][H]
+    float *d_topk_w;           // [T][K] or nullptr
+    void *dW1, *dW3, *dW2;     // bf16
+};
+size_t ffn_bwd_bytes(int T, int H, int E, int K, int I);   // scratch of the launches
+long long ffn_bwd_rows(int T, int E, int K);               // padded rows at most
+cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned long long timeout_ns,
+                           int inject, cudaStream_t s);
+
 // Raises the dynamic shared-memory limit of `func` to `bytes` once per process and size
 // (a no-op afterwards, so launches stay capturable).
 cudaError_t ensure_smem(const void *func, size_t bytes);

@@ -442,6 +442,37 @@ int moe_checkpoint_pack(const void *x, long long rows, int n, void *q, int8_t *s
 int moe_checkpoint_unpack(const void *q, const int8_t *scale, long long rows, int n, void *x,
                           void *stream);
 
+/* Backward pass of the routed experts, from dispatch to combine: of
+ *     Y[t] = sum_j topk_w[t, j] ( silu(X[t] W1[e]) * (X[t] W3[e]) ) W2[e],  e = expert of (t, j)
+ * given the gradient dY of Y.  Nothing of the forward pass is kept but the token rows: the
+ * activations are computed again.
+ *   x        the token rows [T, H]: bf16 (x_scale == NULL), or a checkpoint of
+ *            moe_checkpoint_pack (E4M3 bytes, x_scale int8 [T, ceil(H / 128)])
+ *   dY       bf16 [T, H]
+ *   offsets int32 [E + 1], slot_pos int32 [T, K]: as moe_dispatch left them for the same
+ *            routing (rows of a slot_pos outside every group -- -1, a pair the dispatch
+ *            rejected -- have no gradient)
+ *   topk_w   fp32 [T, K] or NULL (all 1)
+ *   W1, W3   bf16 [E, H, I];  W2 bf16 [E, I, H]
+ *   out dX   bf16 [T, H], through the experts (not through the router)
+ *   out d_topk_w fp32 [T, K] (nullable)
+ *   out dW1, dW3 bf16 [E, H, I], dW2 bf16 [E, I, H]: every entry written, zeros for an
+ *            expert without rows
+ *   ws       at least moe_expert_ffn_backward_workspace_bytes(T, H, E, K, I) bytes (0 for an
+ *            invalid shape); about (T K + 63 E) (8 H + 6 I) bytes
+ * bf16 products with fp32 sums on the tensor cores; the gradients of g = X W1 and u = X W3 and
+ * the weighted activation are rounded to bf16 once, as operands of the second products.  The
+ * results repeat bit for bit.  Offsets that decrease or leave [0, T*K] are recorded as
+ * MOE_ERR_INVALID_ARG in the status word and nothing is written.  T == 0 sets dW1, dW3 and dW2
+ * to 0.  The shared expert is the case E = K = 1, offsets = {0, T}, slot_pos = 0..T-1,
+ * topk_w = NULL. */
+size_t moe_expert_ffn_backward_workspace_bytes(int T, int H, int E, int K, int I);
+int moe_expert_ffn_backward(const void *x, const int8_t *x_scale, const void *dY,
+                            const int32_t *offsets, const int32_t *slot_pos, const float *topk_w,
+                            int T, int H, int E, int K, int I, const void *W1, const void *W3,
+                            const void *W2, void *dX, float *d_topk_w, void *dW1, void *dW3, void *dW2,
+                            void *ws, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------------------------------
  * GRACE-MoE placement planner ("GRACE-MoE" notes, Core Idea 1-3).  Host code on HOST
  * pointers: it consumes the counts and the affinity matrix moe_layer_forward produces

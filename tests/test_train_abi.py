@@ -96,3 +96,29 @@ def test_binding_checks_types_and_sizes():
         B.moe_checkpoint_pack(torch.zeros(T, 192, dtype=torch.bfloat16), None, torch.zeros(T, 1, dtype=torch.int8))
     with pytest.raises(ValueError, match="device tensors"):
         B.moe_checkpoint_pack(y)
+
+
+def test_expert_backward_refusals(lib):
+    def call(x=OK, xs=None, dY=OK, off=OK, slot=OK, w=OK, T=4, H=128, E=4, K=2, I=64, dX=OK, dw=None, d1=OK,
+             ws=WS, n=BIG):
+        return lib.moe_expert_ffn_backward(x, xs, dY, off, slot, w, T, H, E, K, I, OK, OK, OK, dX, dw, d1, OK, OK,
+                                           ws, n, None)
+    assert call(T=-1) == -1 and call(K=5) == -1 and call(I=0) == -1 and call(H=0) == -1
+    assert call(H=96) == -2 and call(I=96) == -2 and call(E=1025) == -2 and call(E=64, K=33) == -2
+    assert call(T=1 << 30, K=2) == -2
+    for name in ("x", "dY", "off", "slot", "dX", "d1", "ws"):
+        assert call(**{name: None}) == -1, name
+    for name in ("x", "xs", "dY", "off", "slot", "w", "dX", "dw", "d1"):
+        assert call(**{name: BAD}) == -3, name
+    need = B.moe_expert_ffn_backward_workspace_bytes(4, 128, 4, 2, 64)
+    assert call(n=need - 1) == -4 and call(ws=P(0x100080)) == -3
+    assert B.moe_expert_ffn_backward_workspace_bytes(4, 100, 4, 2, 64) == 0
+    x = torch.zeros(4, 128, dtype=torch.uint8)
+    i = torch.zeros(4, 2, dtype=torch.int32)
+    W = torch.zeros(4, 128, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x: dtype"):       # bytes without their exponents
+        B.moe_expert_ffn_backward(x, None, x.bfloat16(), torch.zeros(5, dtype=torch.int32), i, None, W, W, W,
+                                  x.bfloat16(), None, W, W, W, x)
+    with pytest.raises(ValueError, match="offsets: 4 elements"):
+        B.moe_expert_ffn_backward(x.bfloat16(), None, x.bfloat16(), torch.zeros(4, dtype=torch.int32), i, None,
+                                  W, W, W, x.bfloat16(), None, W, W, W, x)
