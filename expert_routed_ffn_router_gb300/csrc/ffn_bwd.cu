@@ -42,17 +42,18 @@ namespace moe {
 namespace {
 
 constexpr int PADR = 64;                  // groups start at multiples of this many rows
-constexpr int TM = 256;                   // rows of a tile (a cluster)
+constexpr int TM = 256, TN = 256;         // tile of a cluster
 constexpr int BK = 64;                    // depth of a stage
 constexpr int N_EPI = 8;                  // epilogue warps
-constexpr int NT = 64 + 32 * N_EPI;
+constexpr int NT = 64 + 32 * N_EPI;        // at most 168 registers a thread
 constexpr int MAXG = 1024;
 constexpr int HALF = 8192;                // one 64 x 64 bf16 box
-constexpr int STAGE_GATES = 2 * 16384 + 3 * HALF;   // X, dY rows; W1, W3, W2 boxes
-constexpr int STAGE_GRADS = 2 * 16384;
-constexpr int S_GATES = 4, S_GRADS = 6;
-constexpr int GN = 128;                   // "gates": columns of a tile
-constexpr int DN = 256;                   // "grads": columns of a tile
+constexpr int STAGE = 4 * HALF;           // A: 128 rows of this CTA; B: 128 of the tile's columns
+constexpr int STAGES = 6;
+constexpr int SLAB = 4096;                // an epilogue warp's store buffer: 32 rows of 128 bytes
+// Stages of one sum in tensor memory in the products that d topk_w comes from (see above).
+constexpr int CHUNK = 8;
+constexpr int STASH = 32 * N_EPI * 128;   // floats of a CTA's stash: p of a unit
 
 // What the plan kernel leaves in the workspace.
 struct Plan {
@@ -64,18 +65,16 @@ struct Plan {
 };
 
 struct GemmArgs {
-    CUtensorMap xa, da;              // gates: X, dY rows, boxes of 128 rows
-    CUtensorMap w1, w3, w2;          // weights, 64 x 64 boxes
-    CUtensorMap ga, ua;              // grads: dg, du rows, boxes of 128 rows
-    CUtensorMap xb, db, gb, ub, hb;  // grads: X, dY, dg, du, hw, 64 x 64 boxes
+    // loads: token rows (boxes of 128 rows; of 64 x 64), weights (64 x 64)
+    CUtensorMap xa, da, ga, ua, xb, db, gb, ub, hb, w1, w3, w2;
+    // stores: dg, du, hw (64 columns x 32 rows), rows of dX (32 fp32 x 32), weight gradients
+    CUtensorMap gs, us, hs, xs, s1, s3, s2;
     Plan plan;
     int E, H, I;
     const float *wrow;               // [padded rows] slot weights
-    uint16_t *dg, *du, *hw;          // [padded rows][I]
-    float *dwp;                      // [I / 64][padded rows] partial sums of <p, h>
+    float *dwp;                      // [2 ceil(I / 128)][padded rows] partial sums of <p, h>
     long long ld_dwp;
-    float *dxp;                      // [padded rows][H]
-    uint16_t *dW1, *dW3, *dW2;
+    float *stash;                    // [CTAs][STASH]
     int *status;
     unsigned long long timeout_ns;
     int inject;
@@ -199,24 +198,72 @@ __global__ void __launch_bounds__(GT) gather_kernel(const void *__restrict__ x, 
 }
 
 // ------------------------------------------------------------------------- products
+enum { GU, PR, ROWS, DW1, DW3, DW2, END };     // g and u; p; rows of dX; weight gradients
+
 struct Tile {
-    int kind;       // 0 gates; 1 rows of dX; 2, 3, 4 dW1, dW3, dW2
-    int g, row0, live, col0, kb, m0;
-    // gates, dX rows: row0 the tile's first padded row, live its rows from there to the end
-    // of the group (padded), col0 the first column; weight gradients: m0, col0 the tile's
-    // first output row and column, row0 the group's first padded row
+    int kind, g;
+    int row0;       // first padded row of the tile (weight gradients: of the group)
+    int live;       // padded rows of the group from row0 on
+    int m0;         // weight gradients: first output row
+    int col0;       // first output column
+    int kb, chunk;  // stages, and stages of one sum in tensor memory
 };
 
+__device__ __forceinline__ void tma_store_2d(const void *tmap, const void *src, int c0, int c1)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(smem_u32(src)) : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src)) : "memory");
+}
+
+// The warp's slab may be written again: the store before it has read it.
+__device__ __forceinline__ void slab_free(int lane)
+{
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+
+// 16 bytes to chunk c (of 8) of the lane's row, in the 128-byte swizzle
+__device__ __forceinline__ void slab_put(unsigned char *slab, int lane, int c, uint4 v)
+{
+    *reinterpret_cast<uint4 *>(slab + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+}
+
+// The slab is written: order it before the store that lane 0 issues next.
+__device__ __forceinline__ void slab_ready()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
+__device__ __forceinline__ void slab_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+// 64 fp32 -> the lane's row of 64 bf16
+__device__ __forceinline__ void slab_bf16(unsigned char *slab, int lane, const float *v, int c0)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        slab_put(slab, lane, c0 + i,
+                 make_uint4(f32x2_to_bf16x2(v[8 * i + 1], v[8 * i]), f32x2_to_bf16x2(v[8 * i + 3], v[8 * i + 2]),
+                            f32x2_to_bf16x2(v[8 * i + 5], v[8 * i + 4]), f32x2_to_bf16x2(v[8 * i + 7], v[8 * i + 6])));
+}
+
+// GATES: units of (p of 256 columns; g and u of 128 of them, twice); else: tiles of dX's
+// rows, then of the weight gradients.
 template <bool GATES>
 __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__ GemmArgs p)
 {
-    constexpr int S = GATES ? S_GATES : S_GRADS;
-    constexpr int STAGE = GATES ? STAGE_GATES : STAGE_GRADS;
     constexpr int TCOLS = 512;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    __shared__ uint64_t full[S], empty[S], tfull[2], tempty[2], drain;
+    unsigned char *slabs = ring + STAGES * STAGE;
+    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     volatile int *abort_flag = &abort_s;
@@ -226,7 +273,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
     const bool leader = rank == 0;
     const uint64_t tmo = p.timeout_ns;
     if (tid == 0) {
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -252,47 +299,69 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
     const int E = p.E, H = p.H, I = p.I;
     const int ok = *p.plan.ok;
     const int row_tiles = ok ? p.plan.tiles[E] : 0;
-    const int nI = GATES ? (I + GN - 1) / GN : (I + DN - 1) / DN;      // tiles along I
-    const int nH = (H + DN - 1) / DN;
+    const int nI = (I + TN - 1) / TN, nH = (H + TN - 1) / TN;
     const int n_rows = row_tiles * (GATES ? nI : nH);
-    const int per_w = nH * nI;                                         // tiles of one weight matrix
-    const int n_tiles = GATES ? n_rows : (ok ? n_rows + 3 * E * per_w : 0);
-    const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
+    const int per_w = nH * nI;                       // tiles of one weight gradient
+    const int n_units = GATES ? n_rows : (ok ? n_rows + 3 * E * per_w : 0);
+    const int step = gridDim.x >> 1;
 
-    auto decode = [&](int t) -> Tile {
+    // The tiles of this cluster, in order: `next` takes (unit, part of the unit) on.
+    struct Walk { int unit, part, g; };
+    auto start = [&]() -> Walk { return Walk{static_cast<int>(blockIdx.x >> 1), 0, 0}; };
+    auto tile_of = [&](Walk &w) -> Tile {
         Tile T{};
-        if (GATES || t < n_rows) {
-            // a group's tiles: column by column, its row tiles innermost (they share the
-            // weights)
+        T.kind = END;
+        bool last = true;                            // of its unit
+        if (w.unit >= n_units) return T;
+        if (w.unit < n_rows) {
+            // column by column, a group's row tiles innermost (they share the weights)
             const int nc = GATES ? nI : nH;
-            int lo = 0, hi = E - 1;      // last group with tiles[g] * nc <= t
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (p.plan.tiles[mid] * nc <= t) lo = mid; else hi = mid - 1;
+            // the group with tiles[g] * nc <= unit < tiles[g + 1] * nc: mostly the last tile's or
+            // one of the next
+            int lo = w.g, near = 0;
+            while (near < 8 && p.plan.tiles[lo + 1] * nc <= w.unit) { ++lo; ++near; }
+            if (near == 8) {
+                int hi = E - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (p.plan.tiles[mid] * nc <= w.unit) lo = mid; else hi = mid - 1;
+                }
             }
+            w.g = lo;
             const int mt = p.plan.tiles[lo + 1] - p.plan.tiles[lo];
-            const int l = t - p.plan.tiles[lo] * nc;
+            const int l = w.unit - p.plan.tiles[lo] * nc;
             const int c = l / mt, m = l - c * mt;
-            T.kind = GATES ? 0 : 1;
             T.g = lo;
             T.row0 = p.plan.pos[lo] + m * TM;
-            T.live = (GATES ? pad_rows(p.plan.cnt[lo]) : p.plan.cnt[lo]) - m * TM;
-            T.col0 = c * (GATES ? GN : DN);
-            T.kb = GATES ? H / BK : 2 * (I / BK);
+            T.live = pad_rows(p.plan.cnt[lo]) - m * TM;
+            T.col0 = c * TN;
+            if (GATES) {
+                // p of 256 columns, then g and u of the first 128 and (where there are any) of
+                // the other 128
+                T.kind = w.part == 0 ? PR : GU;
+                if (w.part == 2) T.col0 += 128;
+                last = w.part == 2 || (w.part == 1 && T.col0 + 128 >= I);
+                T.kb = H / BK;
+                T.chunk = CHUNK;
+            } else {
+                T.kind = ROWS;
+                T.kb = T.chunk = 2 * (I / BK);
+            }
         } else {
-            int v = t - n_rows;
-            const int g = v / (3 * per_w);
-            v -= g * 3 * per_w;
-            const int w = v / per_w;
-            v -= w * per_w;
-            const int nc = w < 2 ? nI : nH;
-            T.kind = 2 + w;
-            T.g = g;
+            int v = w.unit - n_rows;
+            T.g = v / (3 * per_w);
+            v -= T.g * 3 * per_w;
+            const int m = v / per_w;
+            v -= m * per_w;
+            const int nc = m < 2 ? nI : nH;
+            T.kind = DW1 + m;
             T.m0 = v / nc * TM;
-            T.col0 = (v - v / nc * nc) * DN;
-            T.row0 = p.plan.pos[g];
-            T.kb = pad_rows(p.plan.cnt[g]) / BK;
+            T.col0 = (v - v / nc * nc) * TN;
+            T.row0 = p.plan.pos[T.g];
+            T.kb = T.chunk = pad_rows(p.plan.cnt[T.g]) / BK;
         }
+        if (!last) ++w.part;
+        else { w.unit += step; w.part = 0; }
         return T;
     };
 
@@ -301,48 +370,57 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         if (lane == 0 && !p.inject) {
             uint32_t s = 0, ph = 0, it = 0;
             const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+            const int r = static_cast<int>(rank);
             bool good = true;
-            for (int t = unit; t < n_tiles && good; t += units) {
-                const Tile T = decode(t);
-                const int r = static_cast<int>(rank);
+            Walk w = start();
+            while (good) {
+                const Tile T = tile_of(w);
+                if (T.kind == END) break;
                 for (int kb = 0; kb < T.kb; ++kb, ++it) {
                     if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
-                    unsigned char *a = ring + s * STAGE;
+                    unsigned char *a = ring + s * STAGE, *b = a + 2 * HALF;
                     const uint32_t fb = full0 + 8u * s;
                     if (leader) mbar_arrive_expect_tx(&full[s], 2u * STAGE);
+                    const int k = kb * BK;
                     if (GATES) {
-                        const int row = T.row0 + 128 * r, col = T.col0 + 64 * r, k = kb * BK;
-                        tma_load_2d_pair(a, &p.xa, fb, k, row);
-                        tma_load_2d_pair(a + 16384, &p.da, fb, k, row);
-                        tma_load_3d_pair(a + 32768, &p.w1, fb, col, k, T.g);
-                        tma_load_3d_pair(a + 32768 + HALF, &p.w3, fb, col, k, T.g);
-                        tma_load_3d_pair(a + 32768 + 2 * HALF, &p.w2, fb, k, col, T.g);
-                    } else if (T.kind == 1) {
+                        const int row = T.row0 + 128 * r, col = T.col0 + 64 * r;
+                        if (T.kind == GU) {
+                            // this CTA's 128 of the tile's columns: 64 of W1, the same 64 of W3
+                            tma_load_2d_pair(a, &p.xa, fb, k, row);
+                            tma_load_3d_pair(b, &p.w1, fb, col, k, T.g);
+                            tma_load_3d_pair(b + HALF, &p.w3, fb, col, k, T.g);
+                        } else {
+                            // ... the columns whose g and u this CTA's half came from
+                            tma_load_2d_pair(a, &p.da, fb, k, row);
+                            tma_load_3d_pair(b, &p.w2, fb, k, col, T.g);
+                            tma_load_3d_pair(b + HALF, &p.w2, fb, k, col + 128, T.g);
+                        }
+                    } else if (T.kind == ROWS) {
                         const bool second = kb >= I / BK;
-                        const int k = (second ? kb - I / BK : kb) * BK, col = T.col0 + 128 * r;
-                        tma_load_2d_pair(a, second ? &p.ua : &p.ga, fb, k, T.row0 + 128 * r);
-                        const CUtensorMap *w = second ? &p.w3 : &p.w1;
-                        tma_load_3d_pair(a + 16384, w, fb, k, col, T.g);
-                        tma_load_3d_pair(a + 16384 + HALF, w, fb, k, col + 64, T.g);
+                        const int c = second ? k - I : k, col = T.col0 + 128 * r;
+                        const CUtensorMap *wm = second ? &p.w3 : &p.w1;
+                        tma_load_2d_pair(a, second ? &p.ua : &p.ga, fb, c, T.row0 + 128 * r);
+                        tma_load_3d_pair(b, wm, fb, c, col, T.g);
+                        tma_load_3d_pair(b + HALF, wm, fb, c, col + 64, T.g);
                     } else {
-                        const CUtensorMap *ma = T.kind == 4 ? &p.hb : &p.xb;
-                        const CUtensorMap *mb = T.kind == 4 ? &p.db : (T.kind == 3 ? &p.ub : &p.gb);
-                        const int k = T.row0 + kb * BK, m = T.m0 + 128 * r, n = T.col0 + 128 * r;
-                        tma_load_2d_pair(a, ma, fb, m, k);
-                        tma_load_2d_pair(a + HALF, ma, fb, m + 64, k);
-                        tma_load_2d_pair(a + 16384, mb, fb, n, k);
-                        tma_load_2d_pair(a + 16384 + HALF, mb, fb, n + 64, k);
+                        const CUtensorMap *ma = T.kind == DW2 ? &p.hb : &p.xb;
+                        const CUtensorMap *mb = T.kind == DW2 ? &p.db : (T.kind == DW3 ? &p.ub : &p.gb);
+                        const int row = T.row0 + k, m = T.m0 + 128 * r, n = T.col0 + 128 * r;
+                        tma_load_2d_pair(a, ma, fb, m, row);
+                        tma_load_2d_pair(a + HALF, ma, fb, m + 64, row);
+                        tma_load_2d_pair(b, mb, fb, n, row);
+                        tma_load_2d_pair(b + HALF, mb, fb, n + 64, row);
                     }
-                    if (++s == S) { s = 0; ph ^= 1u; }
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
             }
             // every copy issued lands before the CTAs can exit (the even CTA's barriers
             // count both CTAs' copies)
             if (leader) {
-                const uint32_t n = it < S ? it : S;
+                const uint32_t n = it < STAGES ? it : STAGES;
                 for (uint32_t j = it - n; j < it; ++j) {
                     int dummy = 0;
-                    mbar_wait(&full[j % S], (j / S) & 1u, &dummy, nullptr, 20000000ull);
+                    mbar_wait(&full[j % STAGES], (j / STAGES) & 1u, &dummy, nullptr, 20000000ull);
                 }
             }
         }
@@ -350,50 +428,42 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         // -------------------------------------------------------------- MMA issuer
         if (lane == 0 && leader) {
             const uint32_t ring0 = smem_u32(ring);
-            uint32_t s = 0, ph = 0, tc = 0;
+            uint32_t s = 0, ph = 0, b = 0, tph = 0;
             bool good = true;
-            for (int t = unit; t < n_tiles && good; t += units, ++tc) {
-                const Tile T = decode(t);
-                const uint32_t b = GATES ? 0u : tc & 1u, tph = GATES ? tc & 1u : (tc >> 1) & 1u;
-                if (!mbar_wait_cluster(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
-                tc_fence_after();
-                for (int kb = 0; kb < T.kb; ++kb) {
-                    if (!mbar_wait(&full[s], ph, abort_flag, p.status, tmo)) { good = false; break; }
+            Walk w = start();
+            while (good) {
+                const Tile T = tile_of(w);
+                if (T.kind == END) break;
+                // A: rows K-major, or (weight gradients) rows as the depth, MN-major; B: columns
+                // of W1 and W3 as they lie (g, u) and rows as the depth are MN-major
+                const bool amn = T.kind >= DW1, bmn = T.kind >= DW1 || T.kind == GU;
+                const uint64_t ad0 = smem_desc_sw128(ring0, amn ? HALF : 16, 1024);
+                const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, bmn ? HALF : 16, 1024);
+                const uint32_t as = amn ? 128u : 2u, bs = bmn ? 128u : 2u;
+                const uint32_t id = idesc_bf16_f32(TM, TN, amn, bmn);
+                int kb = 0;
+                do {
+                    if (!mbar_wait_cluster(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
                     tc_fence_after();
-                    const uint32_t a = ring0 + s * STAGE;
-                    if (GATES) {
-                        // rows K-major; W1 and W3 boxes are columns of I (MN-major), W2's K-major
-                        const uint64_t xd = smem_desc_sw128(a, 16, 1024), dd = smem_desc_sw128(a + 16384, 16, 1024);
-                        const uint64_t b1 = smem_desc_sw128(a + 32768, HALF, 1024);
-                        const uint64_t b3 = smem_desc_sw128(a + 32768 + HALF, HALF, 1024);
-                        const uint64_t b2 = smem_desc_sw128(a + 32768 + 2 * HALF, 16, 1024);
-                        constexpr uint32_t iw = idesc_bf16_f32(TM, GN, false, true);
-                        constexpr uint32_t ik = idesc_bf16_f32(TM, GN, false, false);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t acc = kb | k ? 1u : 0u;
-                            tc_mma_bf16_pair(tmem, xd + 2 * k, b1 + 128 * k, iw, acc);
-                            tc_mma_bf16_pair(tmem + GN, xd + 2 * k, b3 + 128 * k, iw, acc);
-                            tc_mma_bf16_pair(tmem + 2 * GN, dd + 2 * k, b2 + 2 * k, ik, acc);
-                        }
-                    } else {
-                        const uint32_t d = tmem + b * DN;
-                        const bool rows = T.kind == 1;
-                        const uint64_t ad = rows ? smem_desc_sw128(a, 16, 1024) : smem_desc_sw128(a, HALF, 1024);
-                        const uint64_t bd = rows ? smem_desc_sw128(a + 16384, 16, 1024)
-                                                 : smem_desc_sw128(a + 16384, HALF, 1024);
-                        const uint32_t step = rows ? 2u : 128u;
-                        const uint32_t id = rows ? idesc_bf16_f32(TM, DN, false, false)
-                                                 : idesc_bf16_f32(TM, DN, true, true);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc_mma_bf16_pair(d, ad + step * k, bd + step * k, id, kb | k ? 1u : 0u);
+                    const uint32_t d = tmem + b * TN;
+                    const int end = min(kb + T.chunk, T.kb);
+                    for (int k0 = kb; kb < end; ++kb) {
+                        if (!mbar_wait(&full[s], ph, abort_flag, p.status, tmo)) { good = false; break; }
+                        tc_fence_after();
+                        const uint64_t o = static_cast<uint64_t>(s * (STAGE >> 4));
+                        const uint64_t ad = ad0 + o, bd = bd0 + o;
+                        tc_mma_bf16_pair(d, ad, bd, id, kb > k0 ? 1u : 0u);
+                        tc_mma_bf16_pair(d, ad + as, bd + bs, id, 1u);
+                        tc_mma_bf16_pair(d, ad + 2 * as, bd + 2 * bs, id, 1u);
+                        tc_mma_bf16_pair(d, ad + 3 * as, bd + 3 * bs, id, 1u);
+                        tc_commit_pair_mc(&empty[s], 3);
+                        if (++s == STAGES) { s = 0; ph ^= 1u; }
                     }
-                    tc_commit_pair_mc(&empty[s], 3);
-                    if (++s == S) { s = 0; ph ^= 1u; }
-                }
-                if (!good) break;
-                tc_commit_pair_mc(&tfull[b], 3);
+                    if (!good) break;
+                    tc_commit_pair_mc(&tfull[b], 3);
+                    b ^= 1u;
+                    if (b == 0) tph ^= 1u;
+                } while (kb < T.kb);
             }
             tc_commit_pair_mc(&drain, 1);
             int dummy = 0;
@@ -402,100 +472,161 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
     } else {
         // ---------------------------------------------------------------- epilogue
         const int q = warp & 3, half = (warp - 2) >> 2;   // lane quarter, column half
-        const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+        const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128u * half;
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
-        uint32_t tc = 0;
-        for (int t = unit; t < n_tiles; t += units, ++tc) {
-            const Tile T = decode(t);
-            const uint32_t b = GATES ? 0u : tc & 1u, tph = GATES ? tc & 1u : (tc >> 1) & 1u;
+        unsigned char *slab = slabs + (warp - 2) * SLAB;
+        uint32_t b = 0, tph = 0;
+        // the sums of buffer b are complete (every lane observes the phase itself)
+        auto sums_ready = [&]() -> bool {
             bool good = true;
             if (lane == 0) good = mbar_wait(&tfull[b], tph, abort_flag, p.status, tmo);
             good = __shfl_sync(kFullMask, good, 0);
-            if (!good) break;
-            // (every lane observes the completed phase itself before it reads tensor memory)
-            mbar_try_wait(&tfull[b], tph);
-            tc_fence_after();
-            const int lrow = 128 * static_cast<int>(rank) + 32 * q + lane;   // row of the tile
-            if (GATES) {
-                const bool on = lrow < T.live;
-                const size_t row = static_cast<size_t>(T.row0 + lrow);
-                const float w = on ? p.wrow[row] : 0.f;
-                const int c0 = T.col0 + 64 * half;
-                const bool cols = c0 < I;
-                float dw = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    const uint32_t at = tmem + lanes + 64 * half + 32 * c;
-                    float g[32], u[32], pv[32];
-                    __syncwarp();
-                    tmem_ld32(at, g);
-                    tmem_ld32(at + GN, u);
-                    tmem_ld32(at + 2 * GN, pv);
-                    uint32_t og[16], ou[16], oh[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float a[2], bb[2], cc[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float gi = g[i + k], ui = u[i + k], pi = pv[i + k];
-                            const float s = fast_sigmoid(gi), gs = gi * s, h = gs * ui;
-                            dw = fmaf(pi, h, dw);
-                            const float pw = pi * w;
-                            a[k] = pw * ui * s * fmaf(gi, 1.f - s, 1.f);
-                            bb[k] = pw * gs;
-                            cc[k] = w * h;
-                        }
-                        og[i / 2] = f32x2_to_bf16x2(a[1], a[0]);
-                        ou[i / 2] = f32x2_to_bf16x2(bb[1], bb[0]);
-                        oh[i / 2] = f32x2_to_bf16x2(cc[1], cc[0]);
-                    }
-                    if (on && cols) {
-                        const size_t o = row * I + c0 + 32 * c;
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            *reinterpret_cast<uint4 *>(p.dg + o + 2 * i) = make_uint4(og[i], og[i + 1], og[i + 2], og[i + 3]);
-                            *reinterpret_cast<uint4 *>(p.du + o + 2 * i) = make_uint4(ou[i], ou[i + 1], ou[i + 2], ou[i + 3]);
-                            *reinterpret_cast<uint4 *>(p.hw + o + 2 * i) = make_uint4(oh[i], oh[i + 1], oh[i + 2], oh[i + 3]);
-                        }
-                    }
-                }
-                if (on && cols) p.dwp[static_cast<size_t>(c0 / 64) * p.ld_dwp + row] = dw;
-            } else {
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    const int lc = 128 * half + 32 * c;
-                    float v[32];
-                    __syncwarp();
-                    tmem_ld32(tmem + b * DN + lanes + lc, v);
-                    const int col = T.col0 + lc;
-                    if (T.kind == 1) {
-                        if (lrow < T.live && col < H) {
-                            float4 *o = reinterpret_cast<float4 *>(p.dxp + static_cast<size_t>(T.row0 + lrow) * H + col);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        }
-                    } else {
-                        const int M = T.kind == 4 ? I : H, N = T.kind == 4 ? H : I, m = T.m0 + lrow;
-                        if (m < M && col < N) {
-                            uint16_t *base = T.kind == 2 ? p.dW1 : (T.kind == 3 ? p.dW3 : p.dW2);
-                            uint4 *o = reinterpret_cast<uint4 *>(base + (static_cast<size_t>(T.g) * M + m) * N + col);
-                            if (T.kb == 0) {       // an expert without rows
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) o[i] = make_uint4(0, 0, 0, 0);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    o[i] = make_uint4(f32x2_to_bf16x2(v[8 * i + 1], v[8 * i]), f32x2_to_bf16x2(v[8 * i + 3], v[8 * i + 2]),
-                                                      f32x2_to_bf16x2(v[8 * i + 5], v[8 * i + 4]), f32x2_to_bf16x2(v[8 * i + 7], v[8 * i + 6]));
-                            }
-                        }
-                    }
-                }
+            if (good) {
+                mbar_try_wait(&tfull[b], tph);
+                tc_fence_after();
             }
+            return good;
+        };
+        auto sums_read = [&]() {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0 + 8u * b);
+            b ^= 1u;
+            if (b == 0) tph ^= 1u;
+        };
+        // float4 i of this thread's stash (256 threads side by side)
+        float4 *stash = reinterpret_cast<float4 *>(p.stash + static_cast<size_t>(blockIdx.x) * STASH) + (tid - 64);
+        constexpr int SROW = 32 * N_EPI;
+        int part = 0;                                // of the unit: its tiles of g and u so far
+        float dw = 0.f;
+        Walk w = start();
+        bool good = true;
+        while (good) {
+            const Tile T = tile_of(w);
+            if (T.kind == END) break;
+            const int r0 = 128 * static_cast<int>(rank) + 32 * q;   // the warp's first row of the tile
+            if (GATES) {
+                const bool rows = r0 < T.live;
+                const size_t row = static_cast<size_t>(T.row0 + r0 + lane);
+                // sums over the chunks, in registers
+                float acc[128];
+#pragma unroll
+                for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+#pragma unroll 1
+                for (int kb = 0; kb < T.kb; kb += CHUNK) {
+                    if (!sums_ready()) { good = false; break; }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float v[16];
+                        __syncwarp();
+                        tmem_ld16(tm0 + b * TN + 16 * c, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[16 * c + i] += v[i];
+                    }
+                    sums_read();
+                }
+                if (!good) break;
+                if (T.kind == PR) {
+                    // kept for the unit's next tiles: acc[0..63] are columns of the first 128,
+                    // acc[64..127] of the second
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        stash[i * SROW] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                    part = 0;
+                    dw = 0.f;
+                } else {
+                    // g of 64 columns in acc[0..63], u of the same in acc[64..127], p in the stash.
+                    // In their place: dg and du (bf16 pair), hw.
+                    const float wr = rows ? p.wrow[row] : 0.f;
+                    const float4 *st = stash + part * 16 * SROW;
+                    const int col = T.col0 + 64 * half;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 p4 = st[i / 4 * SROW];
+                        const float pp[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float g = acc[i + k], u = acc[64 + i + k];
+                            const float s = fast_sigmoid(g), gs = g * s, h = gs * u, pw = pp[k] * wr;
+                            dw = fmaf(pp[k], h, dw);
+                            acc[i + k] = __uint_as_float(f32x2_to_bf16x2(pw * gs, pw * u * s * fmaf(g, 1.f - s, 1.f)));
+                            acc[64 + i + k] = wr * h;
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {    // dg, du, hw
+                        slab_free(lane);
+#pragma unroll
+                        for (int i = 0; i < 64; i += 8) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                o[k] = x < 2 ? __byte_perm(__float_as_uint(acc[i + 2 * k]), __float_as_uint(acc[i + 2 * k + 1]),
+                                                           x == 0 ? 0x5410 : 0x7632)
+                                             : f32x2_to_bf16x2(acc[64 + i + 2 * k + 1], acc[64 + i + 2 * k]);
+                            slab_put(slab, lane, i / 8, make_uint4(o[0], o[1], o[2], o[3]));
+                        }
+                        slab_ready();
+                        if (lane == 0 && rows && col < I) {
+                            tma_store_2d(x == 0 ? &p.gs : (x == 1 ? &p.us : &p.hs), slab, col, T.row0 + r0);
+                            slab_commit();
+                        }
+                    }
+                    // (each of the unit's tiles leaves its own partial sum)
+                    if (rows) p.dwp[static_cast<size_t>(2 * (T.col0 / 128) + half) * p.ld_dwp + row] = dw;
+                    dw = 0.f;
+                    ++part;
+                }
+            } else {
+                if (!sums_ready()) { good = false; break; }
+                const uint32_t at = tm0 + b * TN;
+                if (T.kind == ROWS) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const int col = T.col0 + 128 * half + 32 * c;
+                        float v[32];
+                        __syncwarp();
+                        tmem_ld32(at + 32 * c, v);
+                        slab_free(lane);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            slab_put(slab, lane, i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                                               __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+                        slab_ready();
+                        if (lane == 0 && r0 < T.live && col < H) {
+                            tma_store_2d(&p.xs, slab, col, T.row0 + r0);
+                            slab_commit();
+                        }
+                    }
+                } else {
+                    const int M = T.kind == DW2 ? I : H, N = T.kind == DW2 ? H : I;
+                    const CUtensorMap *sm = T.kind == DW1 ? &p.s1 : (T.kind == DW3 ? &p.s3 : &p.s2);
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        const int col = T.col0 + 128 * half + 64 * c;
+                        float v[32], u[32];
+                        __syncwarp();
+                        tmem_ld32(at + 64 * c, v);
+                        tmem_ld32(at + 64 * c + 32, u);
+                        if (T.kb == 0) {             // an expert without rows
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = u[i] = 0.f;
+                        }
+                        slab_free(lane);
+                        slab_bf16(slab, lane, v, 0);
+                        slab_bf16(slab, lane, u, 4);
+                        slab_ready();
+                        if (lane == 0 && T.m0 + r0 < M && col < N) {
+                            tma_store_3d(sm, slab, col, T.m0 + r0, T.g);
+                            slab_commit();
+                        }
+                    }
+                }
+                sums_read();
+            }
         }
+        // the last stores have left shared memory and reached global memory
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncwarp();
@@ -570,26 +701,33 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// bf16 [groups][rows][cols] (groups == 0: [rows][cols]), boxes of 64 columns x box_rows rows
-// in the 128-byte swizzle.
-bool encode(CUtensorMap *m, const void *base, int groups, long long rows, int cols, int box_rows)
+// [groups][rows][cols] (groups == 0: [rows][cols]) of bf16, or fp32, in boxes of 128 bytes x
+// box_rows rows in the 128-byte swizzle.
+bool encode(CUtensorMap *m, const void *base, int groups, long long rows, int cols, int box_rows,
+            bool fp32 = false)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
+    const cuuint64_t es = fp32 ? 4 : 2;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(groups)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * rows * 2};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups ? 3 : 2, const_cast<void *>(base), dims, strides,
-              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t strides[2] = {cols * es, cols * es * static_cast<cuuint64_t>(rows)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups ? 3 : 2,
+              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t al256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
+int gemm_ctas() { return num_sms() / 2 * 2; }
+int dw_parts(int I) { return 2 * ((I + 127) / 128); }    // partial sums of <p, h>
+
 struct Layout {
     long long rows;        // padded rows at most
-    size_t plan, wrow, prow, X, D, dg, du, hw, dwp, dxp, bytes;
+    size_t plan, wrow, prow, X, D, dg, du, hw, dwp, dxp, stash, bytes;
 };
 Layout layout(int T, int H, int E, int K, int I)
 {
@@ -608,8 +746,9 @@ Layout layout(int T, int H, int E, int K, int I)
     L.dg = take(R * I * 2);
     L.du = take(R * I * 2);
     L.hw = take(R * I * 2);
-    L.dwp = take(R * (I / 64) * 4);
+    L.dwp = take(R * dw_parts(I) * 4);
     L.dxp = take(R * H * 4);
+    L.stash = take(static_cast<size_t>(gemm_ctas()) * STASH * 4);
     L.bytes = o;
     return L;
 }
@@ -633,27 +772,26 @@ cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned
     float *dxp = reinterpret_cast<float *>(w + L.dxp);
     int *prow = reinterpret_cast<int *>(w + L.prow);
 
+    void *dg = w + L.dg, *du = w + L.du, *hw = w + L.hw;
     GemmArgs a;
     memset(&a, 0, sizeof a);
-    a.dg = reinterpret_cast<uint16_t *>(w + L.dg);
-    a.du = reinterpret_cast<uint16_t *>(w + L.du);
-    a.hw = reinterpret_cast<uint16_t *>(w + L.hw);
     if (!encode(&a.xa, X, 0, L.rows, H, 128) || !encode(&a.da, D, 0, L.rows, H, 128) ||
+        !encode(&a.ga, dg, 0, L.rows, I, 128) || !encode(&a.ua, du, 0, L.rows, I, 128) ||
         !encode(&a.xb, X, 0, L.rows, H, 64) || !encode(&a.db, D, 0, L.rows, H, 64) ||
-        !encode(&a.ga, a.dg, 0, L.rows, I, 128) || !encode(&a.ua, a.du, 0, L.rows, I, 128) ||
-        !encode(&a.gb, a.dg, 0, L.rows, I, 64) || !encode(&a.ub, a.du, 0, L.rows, I, 64) ||
-        !encode(&a.hb, a.hw, 0, L.rows, I, 64) || !encode(&a.w1, f.W1, E, H, I, 64) ||
-        !encode(&a.w3, f.W3, E, H, I, 64) || !encode(&a.w2, f.W2, E, I, H, 64))
+        !encode(&a.gb, dg, 0, L.rows, I, 64) || !encode(&a.ub, du, 0, L.rows, I, 64) ||
+        !encode(&a.hb, hw, 0, L.rows, I, 64) || !encode(&a.w1, f.W1, E, H, I, 64) ||
+        !encode(&a.w3, f.W3, E, H, I, 64) || !encode(&a.w2, f.W2, E, I, H, 64) ||
+        !encode(&a.gs, dg, 0, L.rows, I, 32) || !encode(&a.us, du, 0, L.rows, I, 32) ||
+        !encode(&a.hs, hw, 0, L.rows, I, 32) || !encode(&a.xs, dxp, 0, L.rows, H, 32, true) ||
+        !encode(&a.s1, f.dW1, E, H, I, 32) || !encode(&a.s3, f.dW3, E, H, I, 32) ||
+        !encode(&a.s2, f.dW2, E, I, H, 32))
         return cudaErrorInvalidValue;
     a.plan = plan;
     a.E = E; a.H = H; a.I = I;
     a.wrow = wrow;
     a.dwp = dwp;
     a.ld_dwp = L.rows;
-    a.dxp = dxp;
-    a.dW1 = static_cast<uint16_t *>(f.dW1);
-    a.dW3 = static_cast<uint16_t *>(f.dW3);
-    a.dW2 = static_cast<uint16_t *>(f.dW2);
+    a.stash = reinterpret_cast<float *>(w + L.stash);
     a.status = status;
     a.timeout_ns = timeout_ns;
     a.inject = inject;
@@ -664,14 +802,14 @@ cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned
     e = launch_pdl(gather_kernel, dim3(T + E, parts), dim3(GT), 0, s, 1, f.x, f.x_scale,
                    static_cast<const uint16_t *>(f.dY), f.slot_pos, f.topk_w, T, H, E, K, plan, X, D, wrow, prow);
     if (e != cudaSuccess) return e;
-    const unsigned ctas = num_sms() / 2 * 2;
-    const size_t sm1 = 1024 + static_cast<size_t>(S_GATES) * STAGE_GATES, sm2 = 1024 + static_cast<size_t>(S_GRADS) * STAGE_GRADS;
-    if ((e = ensure_smem(reinterpret_cast<const void *>(bwd_gemm_kernel<true>), sm1)) != cudaSuccess) return e;
-    if ((e = ensure_smem(reinterpret_cast<const void *>(bwd_gemm_kernel<false>), sm2)) != cudaSuccess) return e;
-    if ((e = launch_pdl(bwd_gemm_kernel<true>, dim3(ctas), dim3(NT), sm1, s, 2, a)) != cudaSuccess) return e;
-    if ((e = launch_pdl(bwd_gemm_kernel<false>, dim3(ctas), dim3(NT), sm2, s, 2, a)) != cudaSuccess) return e;
+    const unsigned ctas = gemm_ctas();
+    const size_t smem = 1024 + STAGES * STAGE + N_EPI * SLAB;
+    if ((e = ensure_smem(reinterpret_cast<const void *>(bwd_gemm_kernel<true>), smem)) != cudaSuccess) return e;
+    if ((e = ensure_smem(reinterpret_cast<const void *>(bwd_gemm_kernel<false>), smem)) != cudaSuccess) return e;
+    if ((e = launch_pdl(bwd_gemm_kernel<true>, dim3(ctas), dim3(NT), smem, s, 2, a)) != cudaSuccess) return e;
+    if ((e = launch_pdl(bwd_gemm_kernel<false>, dim3(ctas), dim3(NT), smem, s, 2, a)) != cudaSuccess) return e;
     return launch_pdl(finish_kernel, dim3(T, parts), dim3(GT), 0, s, 1, static_cast<const float *>(dxp),
-                      static_cast<const int *>(prow), static_cast<const float *>(dwp), L.rows, I / 64,
+                      static_cast<const int *>(prow), static_cast<const float *>(dwp), L.rows, dw_parts(I),
                       static_cast<const int *>(plan.ok), H, K, static_cast<uint16_t *>(f.dX), f.d_topk_w);
 }
 
