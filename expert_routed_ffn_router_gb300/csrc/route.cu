@@ -8,10 +8,18 @@
 //   group score (sum of the 1 or 2 largest sel), the K largest sel among their experts,
 //   equal values by index; w = s / sum of the selected s, or s.
 //
-// One warp per token.  The selection is exact: without a bias sel is ordered as the logits
-// are, and those are compared as they stand; otherwise sel is held in fp32 with a bound on
-// its error, and a token with two neighbours in the order closer than their bounds (and not
-// equal in logit and bias) is selected again in fp64.
+// One warp per token, NV consecutive experts a lane.  Selection without a loop over K: the
+// K-th largest of the 32 lanes' maxima bounds the K-th largest value from below, so only the
+// values at or above it (a dozen for K = 8) are candidates; they go to one lane each, in
+// expert order, and every lane counts the candidates ahead of its own.  (Taking the maximum K
+// times measured 26.6 us for 16384 tokens of 256 experts, K = 8, without groups or bias; this
+// NEWT us.)  More than 32 candidates (many equal values) take that loop.
+//
+// The selection is exact: without a bias sel is ordered as the logits are, and those are
+// compared as they stand.  Otherwise sel is held in fp32 with a bound on its error; the
+// candidates reach down by twice that bound, and where two of them are closer than it, they
+// are evaluated again in fp64, one a lane (a softmax, or group scores too close: the whole
+// row, rare).
 //
 // Gradient (D = sum_k w_k dw_k over the selected):
 //   sigmoid, renormalised  dl_j = w_j (1 - s_j) (dw_j - D)
@@ -26,7 +34,7 @@
 namespace moe {
 namespace {
 
-constexpr int WPC = 4;                    // warps (tokens) a CTA
+constexpr int WPC = 8;                    // warps (tokens) a CTA
 constexpr float kMaskedLogit = -3.38953139e38f;   // bf16's lowest value: at or below it, masked
 constexpr double kMaskedSel = -1e300;     // fp64 order: a masked expert of a kept group
 
@@ -35,6 +43,11 @@ __device__ __forceinline__ uint32_t order_key(float v)
 {
     const uint32_t u = __float_as_uint(v);
     return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
 }
 
 __device__ __forceinline__ float warp_max(float v)
@@ -75,117 +88,158 @@ struct RouteArgs {
     float *w;
 };
 
-// Groups kept (bit g) by their scores, from the warp's sel values in shared memory; *gap: the
-// smallest kept score less the largest one not kept.
+// Rank of each lane's score among those of the first n lanes: descending, equal scores by lane.
 template <typename F>
-__device__ __forceinline__ uint32_t keep_groups(const RouteArgs &a, const F *sel, int lane, F lowest, F *gap)
+__device__ __forceinline__ int lane_rank(F score, int lane, int n)
 {
-    const int G = a.E / a.n_group;
-    F s1 = lowest, s2 = lowest;
-    if (lane < a.n_group)
-        for (int i = 0; i < G; ++i) push2(sel[lane * G + i], s1, s2);
-    F score = a.group_top == 2 ? s1 + s2 : s1;
-    if (!(score >= lowest)) score = lowest;     // (-inf, NaN)
-    bool open = lane < a.n_group;
-    uint32_t kept = 0;
-    F last = 0, next = lowest;
-    for (int r = 0; r <= a.topk_group && r < a.n_group; ++r) {
-        F best = open ? score : lowest;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const F v = __shfl_xor_sync(kFullMask, best, o);
-            best = v > best ? v : best;
-        }
-        const uint32_t at = __ballot_sync(kFullMask, open && score == best);
-        const int g = __ffs(at) - 1;
-        if (r == a.topk_group) { next = best; break; }
-        last = best;
-        kept |= 1u << g;
-        if (lane == g) open = false;
+    int rank = 0;
+    for (int h = 0; h < n; ++h) {
+        const F v = __shfl_sync(kFullMask, score, h);
+        rank += v > score || (v == score && h < lane);
     }
-    *gap = last - next;
-    return kept;
+    return rank;
 }
 
-// The selection in fp64 (lane j ends up with the j-th expert).  sel: E doubles of this warp.
-template <int NV>
-__device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lane, double *sel)
+template <typename F>
+__device__ __forceinline__ void merge2(F &a, F &b, int off)
 {
-    double m = 0.0, z = 1.0;
-    if (a.softmax) {
-        m = -DBL_MAX;
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = logit_at(a.logits, a.fp32, base + e);
-            if (l > kMaskedLogit) m = fmax(m, static_cast<double>(l));
+    const F oa = __shfl_xor_sync(kFullMask, a, off), ob = __shfl_xor_sync(kFullMask, b, off);
+    push2(oa, a, b);
+    push2(ob, a, b);
+}
+
+// Lane g: the two largest of the values of group g (NV consecutive experts a lane).
+template <typename F, int NV>
+__device__ __forceinline__ void group_top2(const RouteArgs &a, const F (&v)[NV], int lane, F lowest, F &s1, F &s2)
+{
+    const int G = a.E / a.n_group, per = G / NV;
+    F x = lowest, y = lowest;
+    s1 = s2 = lowest;
+    if (G % NV == 0 && (per & (per - 1)) == 0) {
+        // whole lanes hold a group
+#pragma unroll
+        for (int i = 0; i < NV; ++i) push2(v[i], x, y);
+        for (int o = 1; o < per; o <<= 1) merge2(x, y, o);
+        s1 = __shfl_sync(kFullMask, x, lane * per & 31);
+        s2 = __shfl_sync(kFullMask, y, lane * per & 31);
+        return;
+    }
+    for (int g = 0; g < a.n_group; ++g) {
+        x = y = lowest;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane * NV + i;
+            if (e >= g * G && e < (g + 1) * G) push2(v[i], x, y);
         }
 #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) merge2(x, y, o);
+        if (lane == g) { s1 = x; s2 = y; }
+    }
+}
+
+// The selection in fp64, row by row as written down: lane j ends up with the j-th expert.
+template <int NV>
+__device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lane)
+{
+    double v[NV], m = -DBL_MAX, z = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane * NV + i;
+        const float l = e < a.E ? logit_at(a.logits, a.fp32, base + e) : -INFINITY;
+        v[i] = l > kMaskedLogit ? static_cast<double>(l) : (l <= kMaskedLogit ? -INFINITY : NAN);
+        if (l > kMaskedLogit) m = fmax(m, v[i]);
+    }
+    if (a.softmax) {
+#pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFullMask, m, o));
-        z = 0.0;
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = logit_at(a.logits, a.fp32, base + e);
-            if (l > kMaskedLogit) z += exp(static_cast<double>(l) - m);
-        }
+        for (int i = 0; i < NV; ++i) z += exp(v[i] - m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFullMask, z, o);
     }
-    for (int e = lane; e < a.E; e += 32) {
-        const double l = static_cast<double>(logit_at(a.logits, a.fp32, base + e));
-        double v = a.softmax ? exp(l - m) / z : 1.0 / (1.0 + exp(-l));
-        if (a.bias) v += static_cast<double>(a.bias[e]);
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane * NV + i;
+        const bool on = v[i] > -INFINITY;
+        double s = a.softmax ? exp(v[i] - m) / z : 1.0 / (1.0 + exp(-v[i]));
+        if (a.bias && e < a.E) s += static_cast<double>(a.bias[e]);
         // (a bias of -inf ranks above a mask, and every entry stays above what is taken out)
-        sel[e] = l > kMaskedLogit && v == v ? fmax(v, 0.1 * kMaskedSel) : kMaskedSel;
+        v[i] = e >= a.E ? -DBL_MAX : (on && s == s ? fmax(s, 0.1 * kMaskedSel) : kMaskedSel);
     }
-    __syncwarp();
-    uint32_t kept = kFullMask;
-    const int G = a.E / a.n_group;
     if (a.n_group > 1) {
-        double gap;
-        kept = keep_groups<double>(a, sel, lane, 2 * kMaskedSel, &gap);
+        const int G = a.E / a.n_group;
+        double s1, s2;
+        group_top2<double, NV>(a, v, lane, 2 * kMaskedSel, s1, s2);
+        const double score = a.group_top == 2 ? s1 + s2 : s1;
+        const int rank = lane_rank(score, lane, a.n_group);
+        const uint32_t kept = __ballot_sync(kFullMask, lane < a.n_group && rank < a.topk_group);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane * NV + i;
+            if (e < a.E && !((kept >> (e / G)) & 1u)) v[i] = -DBL_MAX;
+        }
     }
-    for (int e = lane; e < a.E; e += 32)
-        if (a.n_group > 1 && !((kept >> (e / G)) & 1u)) sel[e] = -DBL_MAX;
-    __syncwarp();
     int mine = 0;
     for (int k = 0; k < a.K; ++k) {
         double best = -DBL_MAX;
-        int at = a.E;
-        for (int e = lane; e < a.E; e += 32)
-            if (sel[e] > best) { best = sel[e]; at = e; }
+        int at = a.E - 1;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (v[i] > best) { best = v[i]; at = lane * NV + i; }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const double v = __shfl_xor_sync(kFullMask, best, o);
-            const int i = __shfl_xor_sync(kFullMask, at, o);
-            if (v > best || (v == best && i < at)) { best = v; at = i; }
+            const double w = __shfl_xor_sync(kFullMask, best, o);
+            const int j = __shfl_xor_sync(kFullMask, at, o);
+            if (w > best || (w == best && j < at)) { best = w; at = j; }
         }
         if (lane == k) mine = at;
-        if (lane == (at & 31)) sel[at] = -DBL_MAX;
-        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (lane * NV + i == at) v[i] = -DBL_MAX;
     }
     return mine;
 }
 
-template <int NV>
+template <int NV, bool F32>
 __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
 {
-    extern __shared__ double sm_sel[];      // [WPC][E] (fp32 for the group scores, fp64 again)
-    pdl_wait();
+    __shared__ uint2 cand[WPC][32];          // key and expert, in expert order
     const int lane = threadIdx.x, t = blockIdx.x * WPC + threadIdx.y;
+    pdl_wait();
     if (t >= a.T) return;
     const size_t base = static_cast<size_t>(t) * a.E;
-    double *sel64 = sm_sel + static_cast<size_t>(threadIdx.y) * a.E;
-    float *sel32 = reinterpret_cast<float *>(sel64);
+    const int e0 = lane * NV;
 
-    float l[NV], v[NV];        // logit; then score
-    uint32_t key[NV];
+    float l[NV];
+    if (F32 && NV % 4 == 0 && a.E % 4 == 0) {
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + base + e0);
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+            const float4 v = e0 + i < a.E ? src[i / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
+            l[i] = v.x; l[(i + 1) % NV] = v.y; l[(i + 2) % NV] = v.z; l[(i + 3) % NV] = v.w;
+        }
+    } else if (!F32 && NV % 8 == 0 && a.E % 8 == 0) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + base + e0);
+#pragma unroll
+        for (int i = 0; i < NV; i += 8) {
+            const uint4 v = e0 + i < a.E ? src[i / 8] : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) l[(i + k) % NV] = k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) l[i] = e0 + i < a.E ? logit_at(a.logits, F32, base + e0 + i) : 0.f;
+    }
     float m = -FLT_MAX;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < a.E ? logit_at(a.logits, a.fp32, base + e) : -INFINITY;
-        if (l[i] > kMaskedLogit) m = fmaxf(m, l[i]);
-        else if (l[i] <= kMaskedLogit) l[i] = -INFINITY;     // (NaN stays)
+        if (e0 + i >= a.E || l[i] <= kMaskedLogit) l[i] = -INFINITY;     // (NaN stays)
+        else if (l[i] > kMaskedLogit) m = fmaxf(m, l[i]);
     }
-    float z = 1.f;
+    // Order keys.  No bias and no sum of two scores: the logits themselves, exactly.
+    const bool scored = a.bias || (a.n_group > 1 && a.group_top == 2);
+    float z = 1.f, bound = 0.f;
+    uint32_t key[NV];
+    float v[NV];                             // what the groups are scored by
     if (a.softmax) {
         m = warp_max(m);
         z = 0.f;
@@ -195,98 +249,162 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
             z += v[i];
         }
         z = warp_sum(z);
+    }
+    if (scored) {
+        // Relative error of a score: fp32 exp, sum and division (softmax: also the rounding of
+        // l - m and of up to 1024 sums); then the rounding of s + bias.
+        const float inv = a.softmax ? (z == 0.f ? 0.f : 1.f / z) : 0.f;
+        float top = 0.f, most = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = z > 0.f || z != z ? v[i] / z : 0.f;
+        for (int i = 0; i < NV; ++i) {
+            v[i] = a.softmax ? v[i] * inv : sigmoid(l[i]);
+            const float s = v[i] + (a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f);
+            const bool on = l[i] > -INFINITY && s == s;
+            if (on) {
+                top = fmaxf(top, v[i]);
+                if (fabsf(s) < INFINITY) most = fmaxf(most, fabsf(s));
+            }
+            key[i] = e0 + i >= a.E ? 0u : (on ? order_key(a.bias ? s : l[i] + 0.f) : 1u);
+            // (masked: below every sel, and the sum of two above the lowest float)
+            v[i] = e0 + i >= a.E ? -FLT_MAX : (on ? s : -1e38f);
+        }
+        bound = (a.softmax ? 3e-6f : 3e-7f) * warp_max(top) + 1.5e-7f * warp_max(most);
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = sigmoid(l[i]);
+        for (int i = 0; i < NV; ++i) {
+            const bool on = l[i] > -INFINITY;
+            key[i] = e0 + i >= a.E ? 0u : (on ? order_key(l[i] + 0.f) : 1u);     // (-0 ranks as +0)
+            v[i] = e0 + i >= a.E ? -FLT_MAX : (on ? l[i] : -3.395e38f);
+        }
     }
-    // Order keys.  No bias and no sum of two scores: the logits themselves, exactly.
-    const bool scored = a.bias || (a.n_group > 1 && a.group_top == 2);
-    float most = 0.f;          // largest |sel| (scales the error bound)
-    float bv[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        bv[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
-        const float s = a.bias ? v[i] + bv[i] : l[i] + 0.f;     // (-0 ranks as +0)
-        const bool ok = l[i] > -INFINITY && s == s;
-        key[i] = e >= a.E ? 0u : (ok ? order_key(s) : 1u);
-        if (scored && ok && fabsf(s) < INFINITY) most = fmaxf(most, fabsf(v[i] + bv[i]));
-    }
-    // Error of sel: fp32 exp, sum and division of s <= 1, and the rounding of s + bias.  For
-    // the softmax an error of the argument l - m and of the sum of up to 1024 terms comes in.
-    float bound = 0.f;
-    if (scored) bound = 6e-7f + 1.5e-7f * warp_max(most) + (a.softmax ? 2.5e-6f : 0.f);
     bool sure = true;
     if (a.n_group > 1) {
+        float s1, s2;
+        group_top2<float, NV>(a, v, lane, -FLT_MAX, s1, s2);
+        float score = a.group_top == 2 ? s1 + s2 : s1;
+        if (!(score >= -FLT_MAX)) score = -FLT_MAX;      // (-inf, NaN)
+        const int rank = lane_rank(score, lane, a.n_group);      // (every lane takes part)
+        const bool mine = lane < a.n_group, in = mine && rank < a.topk_group;
+        const uint32_t kept = __ballot_sync(kFullMask, in);
+        if (scored && a.topk_group < a.n_group) {
+            const uint32_t k = order_key(score);
+            const uint32_t lo = __reduce_min_sync(kFullMask, in ? k : 0xffffffffu);
+            const uint32_t hi = __reduce_max_sync(kFullMask, mine && !in ? k : 0u);
+            sure = key_value(lo) - key_value(hi) > 4.f * bound;
+        }
         const int G = a.E / a.n_group;
+        if (G % NV == 0) {
+            if (e0 < a.E && !((kept >> (e0 / G)) & 1u))
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E) {
-                // (masked: below every sel, their sum above `lowest`; below every logit)
-                sel32[e] = key[i] <= 1u ? (scored ? -1e38f : -3.395e38f) : (scored ? v[i] + bv[i] : l[i]);
+                for (int i = 0; i < NV; ++i) key[i] = 0u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (e0 + i < a.E && !((kept >> ((e0 + i) / G)) & 1u)) key[i] = 0u;
+        }
+    }
+    int expert = 0, place = 32;              // this lane's expert and its place in the order
+    if (sure) {
+        // K-th largest of the lanes' maxima (bitonic sort, descending)
+        uint32_t x = 0u;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x = key[i] > x ? key[i] : x;
+#pragma unroll
+        for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                const uint32_t o = __shfl_xor_sync(kFullMask, x, j);
+                x = ((lane & k) == 0) == ((lane & j) == 0) ? max(x, o) : min(x, o);
+            }
+        uint32_t least = __shfl_sync(kFullMask, x, a.K - 1);
+        if (least > 1u && a.bias) {
+            const float f = key_value(least) - 2.f * bound;
+            least = f == f ? order_key(f) : 1u;
+        }
+        if (least == 0u) least = 1u;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) n += key[i] >= least;
+        int at = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(kFullMask, at, o);
+            if (lane >= o) at += w;
+        }
+        const int C = __shfl_sync(kFullMask, at, 31);
+        if (C <= 32) {
+            at -= n;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (key[i] >= least) cand[threadIdx.y][at++] = make_uint2(key[i], static_cast<uint32_t>(e0 + i));
+            __syncwarp();
+            uint32_t k = 0u;
+            if (lane < C) {
+                const uint2 c = cand[threadIdx.y][lane];
+                k = c.x;
+                expert = static_cast<int>(c.y);
+            }
+            const float f = key_value(k);
+            int rank = 0;
+            bool close = false;
+            for (int j = 0; j < C; ++j) {
+                const uint32_t o = __shfl_sync(kFullMask, k, j);
+                rank += o > k || (o == k && j < lane);
+                // (masked experts, key 1, are equal among themselves)
+                if (a.bias) close |= j != lane && k > 1u && o > 1u && !(fabsf(key_value(o) - f) > 2.f * bound);
+            }
+            place = lane < C ? rank : 32;
+            if (a.bias && __any_sync(kFullMask, close && lane < C)) {
+                if (a.softmax) {
+                    sure = false;
+                } else {
+                    double d = -DBL_MAX;
+                    if (lane < C) {
+                        const double x64 = static_cast<double>(logit_at(a.logits, F32, base + expert));
+                        d = 1.0 / (1.0 + exp(-x64)) + static_cast<double>(a.bias[expert]);
+                        d = k <= 1u ? kMaskedSel : fmax(d, 0.1 * kMaskedSel);
+                    }
+                    const int r64 = lane_rank(d, lane, C);
+                    if (lane < C) place = r64;
+                }
+            }
+        } else if (a.bias) {
+            sure = false;
+        } else {
+            for (int r = 0; r < a.K; ++r) {
+                uint32_t best = 0u;
+                int e = 1 << 30;
+#pragma unroll
+                for (int i = NV - 1; i >= 0; --i)
+                    if (key[i] >= best) { best = key[i]; e = e0 + i; }
+                const uint32_t top = __reduce_max_sync(kFullMask, best);
+                const int win = __reduce_min_sync(kFullMask, best == top ? e : 1 << 30);
+                if (lane == r) { expert = win; place = r; }
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (e0 + i == win) key[i] = 0u;
             }
         }
-        __syncwarp();
-        float gap;
-        const uint32_t kept = keep_groups<float>(a, sel32, lane, -FLT_MAX, &gap);
-        if (scored && a.topk_group < a.n_group) sure = gap > 4.f * bound;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E && !((kept >> (e / G)) & 1u)) key[i] = 0u;
-        }
-    }
-    int mine = 0;
-    float prev = 0.f, prev_l = 0.f, prev_b = 0.f;
-    uint32_t prev_key = 0u;
-    for (int k = 0; k <= a.K && sure; ++k) {
-        uint32_t best = 0u;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) best = key[i] > best ? key[i] : best;
-        const uint32_t top = __reduce_max_sync(kFullMask, best);
-        if (top == 0u || (k == a.K && !a.bias)) break;
-        int at = 1 << 30;
-        float wl = 0.f, wb = 0.f;
-#pragma unroll
-        for (int i = NV - 1; i >= 0; --i)
-            if (key[i] == top) { at = lane + 32 * i; wl = l[i]; wb = bv[i]; }
-        const int win = __reduce_min_sync(kFullMask, at);
-        if (a.bias) {
-            // certified against the one before it
-            wl = __shfl_sync(kFullMask, wl, win & 31);
-            wb = __shfl_sync(kFullMask, wb, win & 31);
-            const float cur = top > 1u ? __uint_as_float((top >> 31) ? top & 0x7fffffffu : ~top) : -INFINITY;
-            if (k > 0 && top > 1u && prev_key > 1u && !(prev - cur > 2.f * bound) && !(prev_l == wl && prev_b == wb))
-                sure = false;
-            prev = cur; prev_l = wl; prev_b = wb; prev_key = top;
-        }
-        if (k == a.K) break;
-        if (lane == k) mine = win;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (lane + 32 * i == win) key[i] = 0u;
     }
     if (!sure) {
-        __syncwarp();
-        mine = select_fp64<NV>(a, base, lane, sel64);
+        expert = select_fp64<NV>(a, base, lane);
+        place = lane;
     }
     // weights: the selected scores (a masked expert's is 0), over their sum
+    const bool on = place < a.K;
     float s = 0.f;
-    if (lane < a.K) {
-        float lj = logit_at(a.logits, a.fp32, base + mine);
+    if (on) {
+        float lj = logit_at(a.logits, F32, base + expert);
         if (lj <= kMaskedLogit) lj = -INFINITY;
-        s = !a.softmax ? sigmoid(lj) : (z > 0.f || z != z ? expf(lj - m) / z : 0.f);
+        s = !a.softmax ? sigmoid(lj) : (z == 0.f ? 0.f : expf(lj - m) / z);
     }
     if (a.renorm) {
         const float sum = warp_sum(s);
         s = sum == 0.f ? 0.f : s / sum;
     }
-    if (lane < a.K) {
-        a.idx[static_cast<size_t>(t) * a.K + lane] = mine;
-        a.w[static_cast<size_t>(t) * a.K + lane] = s;
+    if (on) {
+        a.idx[static_cast<size_t>(t) * a.K + place] = expert;
+        a.w[static_cast<size_t>(t) * a.K + place] = s;
     }
 }
 
@@ -368,10 +486,9 @@ __global__ void __launch_bounds__(32 * WPC) route_bwd_kernel(const RouteBwdArgs 
 template <int NV>
 cudaError_t fwd(const RouteArgs &a, cudaStream_t s)
 {
-    const size_t smem = static_cast<size_t>(WPC) * a.E * sizeof(double);
-    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(route_fwd_kernel<NV>), smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(route_fwd_kernel<NV>, dim3((a.T + WPC - 1) / WPC), dim3(32, WPC), smem, s, 1, a);
+    const dim3 grid((a.T + WPC - 1) / WPC), block(32, WPC);
+    return a.fp32 ? launch_pdl(route_fwd_kernel<NV, true>, grid, block, 0, s, 1, a)
+                  : launch_pdl(route_fwd_kernel<NV, false>, grid, block, 0, s, 1, a);
 }
 
 }  // namespace
