@@ -79,6 +79,14 @@ __device__ __forceinline__ void push2(F v, F &a, F &b)
     else if (v > b) b = v;
 }
 
+// sigmoid from the hardware exp2 and reciprocal, for the selection (its error is in the bound)
+__device__ __forceinline__ float rough_sigmoid(float l)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-l)));
+    return r;
+}
+
 struct RouteArgs {
     const void *logits;
     const float *bias;      // nullable
@@ -198,6 +206,45 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
     return mine;
 }
 
+// The groups kept, by scores in fp64 of every lane's two largest values (v: sel within `bound`):
+// where lanes hold whole groups, the score is a sigmoid and no lane's third value comes close
+// to its second.  False where that does not hold.
+template <int NV>
+__device__ __noinline__ bool groups_fp64(const RouteArgs &a, const float (&l)[NV], const float (&v)[NV], int lane,
+                                         float bound, uint32_t &kept)
+{
+    const int G = a.E / a.n_group, per = G / NV;
+    if (a.softmax || G % NV || (per & (per - 1))) return false;
+    float v1 = -FLT_MAX, v2 = -FLT_MAX, v3 = -FLT_MAX, l1 = 0.f, l2 = 0.f;
+    int e1 = 0, e2 = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane * NV + i;
+        if (v[i] > v1) {
+            v3 = v2; v2 = v1; l2 = l1; e2 = e1;
+            v1 = v[i]; l1 = l[i]; e1 = e;
+        } else if (v[i] > v2) {
+            v3 = v2; v2 = v[i]; l2 = l[i]; e2 = e;
+        } else {
+            v3 = fmaxf(v3, v[i]);
+        }
+    }
+    if (__any_sync(kFullMask, v3 > -1e37f && !(v2 - v3 > 2.f * bound))) return false;
+    auto exact = [&](float s, float x, int e) -> double {
+        if (!(s > -1e37f)) return kMaskedSel;
+        const double d = 1.0 / (1.0 + exp(-static_cast<double>(x)));
+        return fmax(a.bias ? d + static_cast<double>(a.bias[e]) : d, 0.1 * kMaskedSel);
+    };
+    const double d1 = exact(v1, l1, e1), d2 = exact(v2, l2, e2);
+    double x = fmax(d1, d2), y = fmin(d1, d2);
+    for (int o = 1; o < per; o <<= 1) merge2(x, y, o);
+    x = __shfl_sync(kFullMask, x, lane * per & 31);
+    y = __shfl_sync(kFullMask, y, lane * per & 31);
+    const int rank = lane_rank(a.group_top == 2 ? x + y : x, lane, a.n_group);
+    kept = __ballot_sync(kFullMask, lane < a.n_group && rank < a.topk_group);
+    return true;
+}
+
 template <int NV, bool F32>
 __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
 {
@@ -251,14 +298,26 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
         z = warp_sum(z);
     }
     if (scored) {
-        // Relative error of a score: fp32 exp, sum and division (softmax: also the rounding of
-        // l - m and of up to 1024 sums); then the rounding of s + bias.
+        // Error of a score: the sigmoid's is below 3e-7, and below (6e-8 |l| + 5e-7) of its value,
+        // from exp2, its argument's rounding and the reciprocal; the softmax's below 3e-6 of the
+        // largest (fp32 exp, the rounding of l - m, up to 1024 sums).  Then the rounding of s + bias.
         const float inv = a.softmax ? (z == 0.f ? 0.f : 1.f / z) : 0.f;
+        float bv[NV];
+        if (a.bias && NV % 4 == 0 && a.E % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < NV; i += 4) {
+                const float4 x = e0 + i < a.E ? *reinterpret_cast<const float4 *>(a.bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                bv[i] = x.x; bv[(i + 1) % NV] = x.y; bv[(i + 2) % NV] = x.z; bv[(i + 3) % NV] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) bv[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
+        }
         float top = 0.f, most = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            v[i] = a.softmax ? v[i] * inv : sigmoid(l[i]);
-            const float s = v[i] + (a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f);
+            v[i] = a.softmax ? v[i] * inv : rough_sigmoid(l[i]);
+            const float s = v[i] + bv[i];
             const bool on = l[i] > -INFINITY && s == s;
             if (on) {
                 top = fmaxf(top, v[i]);
@@ -268,7 +327,9 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
             // (masked: below every sel, and the sum of two above the lowest float)
             v[i] = e0 + i >= a.E ? -FLT_MAX : (on ? s : -1e38f);
         }
-        bound = (a.softmax ? 3e-6f : 3e-7f) * warp_max(top) + 1.5e-7f * warp_max(most);
+        top = key_value(__reduce_max_sync(kFullMask, order_key(top)));
+        most = key_value(__reduce_max_sync(kFullMask, order_key(most)));
+        bound = (a.softmax ? 3e-6f * top : fminf(4e-7f, 8e-6f * top)) + 1.5e-7f * most;
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -285,12 +346,13 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
         if (!(score >= -FLT_MAX)) score = -FLT_MAX;      // (-inf, NaN)
         const int rank = lane_rank(score, lane, a.n_group);      // (every lane takes part)
         const bool mine = lane < a.n_group, in = mine && rank < a.topk_group;
-        const uint32_t kept = __ballot_sync(kFullMask, in);
+        uint32_t kept = __ballot_sync(kFullMask, in);
         if (scored && a.topk_group < a.n_group) {
             const uint32_t k = order_key(score);
             const uint32_t lo = __reduce_min_sync(kFullMask, in ? k : 0xffffffffu);
             const uint32_t hi = __reduce_max_sync(kFullMask, mine && !in ? k : 0u);
             sure = key_value(lo) - key_value(hi) > 4.f * bound;
+            if (!sure) sure = groups_fp64<NV>(a, l, v, lane, bound, kept);
         }
         const int G = a.E / a.n_group;
         if (G % NV == 0) {
