@@ -38,16 +38,17 @@ constexpr int WPC = 8;                    // warps (tokens) a CTA
 constexpr float kMaskedLogit = -3.38953139e38f;   // bf16's lowest value: at or below it, masked
 constexpr double kMaskedSel = -1e300;     // fp64 order: a masked expert of a kept group
 
-// Keys that order as the floats do; 0: not selectable, 1: masked or NaN.
+// Values that rank below every sel or logit: masked ones (sums of two of them stay above
+// the lowest float), and ones out of the running.
+constexpr float kMaskedRank = -1e38f, kLeastRank = -9e37f;    // sel is kept at or above the latter
+constexpr float kMaskedRankLogit = -3.395e38f;
+constexpr float kOut = -INFINITY;
+
+// Integers that order as the floats do (for the warp-wide integer maximum).
 __device__ __forceinline__ uint32_t order_key(float v)
 {
     const uint32_t u = __float_as_uint(v);
     return (u >> 31) ? ~u : (u | 0x80000000u);
-}
-
-__device__ __forceinline__ float key_value(uint32_t k)
-{
-    return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
 }
 
 __device__ __forceinline__ float warp_max(float v)
@@ -72,8 +73,12 @@ __device__ __forceinline__ float logit_at(const void *p, int fp32, size_t i)
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
 
-template <typename F>
-__device__ __forceinline__ void push2(F v, F &a, F &b)
+__device__ __forceinline__ void push2(float v, float &a, float &b)
+{
+    b = fmaxf(b, fminf(a, v));
+    a = fmaxf(a, v);
+}
+__device__ __forceinline__ void push2(double v, double &a, double &b)
 {
     if (v > a) { b = a; a = v; }
     else if (v > b) b = v;
@@ -229,9 +234,9 @@ __device__ __noinline__ bool groups_fp64(const RouteArgs &a, const float (&l)[NV
             v3 = fmaxf(v3, v[i]);
         }
     }
-    if (__any_sync(kFullMask, v3 > -1e37f && !(v2 - v3 > 2.f * bound))) return false;
+    if (__any_sync(kFullMask, v3 > kMaskedRank && !(v2 - v3 > 2.f * bound))) return false;
     auto exact = [&](float s, float x, int e) -> double {
-        if (!(s > -1e37f)) return kMaskedSel;
+        if (!(s > kMaskedRank)) return kMaskedSel;
         const double d = 1.0 / (1.0 + exp(-static_cast<double>(x)));
         return fmax(a.bias ? d + static_cast<double>(a.bias[e]) : d, 0.1 * kMaskedSel);
     };
@@ -248,145 +253,127 @@ __device__ __noinline__ bool groups_fp64(const RouteArgs &a, const float (&l)[NV
 template <int NV, bool F32>
 __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
 {
-    __shared__ uint2 cand[WPC][32];          // key and expert, in expert order
-    const int lane = threadIdx.x, t = blockIdx.x * WPC + threadIdx.y;
+    __shared__ __align__(16) float cand_f[WPC][36];      // candidates in expert order
+    __shared__ int cand_e[WPC][32];
+    const int lane = threadIdx.x, wy = threadIdx.y, t = blockIdx.x * WPC + wy;
     pdl_wait();
     if (t >= a.T) return;
     const size_t base = static_cast<size_t>(t) * a.E;
     const int e0 = lane * NV;
+    const int live = a.E - e0;               // experts i < live of this lane exist
 
     float l[NV];
     if (F32 && NV % 4 == 0 && a.E % 4 == 0) {
         const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + base + e0);
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
-            const float4 v = e0 + i < a.E ? src[i / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = i < live ? src[i / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
             l[i] = v.x; l[(i + 1) % NV] = v.y; l[(i + 2) % NV] = v.z; l[(i + 3) % NV] = v.w;
         }
     } else if (!F32 && NV % 8 == 0 && a.E % 8 == 0) {
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + base + e0);
 #pragma unroll
         for (int i = 0; i < NV; i += 8) {
-            const uint4 v = e0 + i < a.E ? src[i / 8] : make_uint4(0, 0, 0, 0);
+            const uint4 v = i < live ? src[i / 8] : make_uint4(0, 0, 0, 0);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) l[(i + k) % NV] = k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) l[i] = e0 + i < a.E ? logit_at(a.logits, F32, base + e0 + i) : 0.f;
+        for (int i = 0; i < NV; ++i) l[i] = i < live ? logit_at(a.logits, F32, base + e0 + i) : 0.f;
     }
-    float m = -FLT_MAX;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (e0 + i >= a.E || l[i] <= kMaskedLogit) l[i] = -INFINITY;     // (NaN stays)
-        else if (l[i] > kMaskedLogit) m = fmaxf(m, l[i]);
-    }
-    // Order keys.  No bias and no sum of two scores: the logits themselves, exactly.
-    const bool scored = a.bias || (a.n_group > 1 && a.group_top == 2);
-    float z = 1.f, bound = 0.f;
-    uint32_t key[NV];
-    float v[NV];                             // what the groups are scored by
+    float m = -FLT_MAX, z = 1.f;
     if (a.softmax) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i < live && l[i] > kMaskedLogit) m = fmaxf(m, l[i]);
         m = warp_max(m);
         z = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            v[i] = expf(l[i] - m);
-            z += v[i];
-        }
+        for (int i = 0; i < NV; ++i) z += i < live && !(l[i] <= kMaskedLogit) ? expf(l[i] - m) : 0.f;
         z = warp_sum(z);
     }
+    // What the experts are ranked by.  No bias and no sum of two scores: the logits, exactly.
+    const bool scored = a.bias || (a.n_group > 1 && a.group_top == 2);
+    float f[NV], bound = 0.f;
     if (scored) {
-        // Error of a score: the sigmoid's is below 3e-7, and below (6e-8 |l| + 5e-7) of its value,
-        // from exp2, its argument's rounding and the reciprocal; the softmax's below 3e-6 of the
-        // largest (fp32 exp, the rounding of l - m, up to 1024 sums).  Then the rounding of s + bias.
-        const float inv = a.softmax ? (z == 0.f ? 0.f : 1.f / z) : 0.f;
         float bv[NV];
         if (a.bias && NV % 4 == 0 && a.E % 4 == 0) {
 #pragma unroll
             for (int i = 0; i < NV; i += 4) {
-                const float4 x = e0 + i < a.E ? *reinterpret_cast<const float4 *>(a.bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 x = i < live ? *reinterpret_cast<const float4 *>(a.bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
                 bv[i] = x.x; bv[(i + 1) % NV] = x.y; bv[(i + 2) % NV] = x.z; bv[(i + 3) % NV] = x.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) bv[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
+            for (int i = 0; i < NV; ++i) bv[i] = a.bias && i < live ? a.bias[e0 + i] : 0.f;
         }
-        float top = 0.f, most = 0.f;
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+        float most = 0.f;                    // largest |sel|
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            v[i] = a.softmax ? v[i] * inv : rough_sigmoid(l[i]);
-            const float s = v[i] + bv[i];
-            const bool on = l[i] > -INFINITY && s == s;
-            if (on) {
-                top = fmaxf(top, v[i]);
-                if (fabsf(s) < INFINITY) most = fmaxf(most, fabsf(s));
-            }
-            key[i] = e0 + i >= a.E ? 0u : (on ? order_key(a.bias ? s : l[i] + 0.f) : 1u);
-            // (masked: below every sel, and the sum of two above the lowest float)
-            v[i] = e0 + i >= a.E ? -FLT_MAX : (on ? s : -1e38f);
+            const float s = (a.softmax ? __expf(l[i] - m) * inv : rough_sigmoid(l[i])) + bv[i];
+            f[i] = l[i] <= kMaskedLogit ? kMaskedRank : fmaxf(s, kLeastRank);
+            if (f[i] > kLeastRank && f[i] < INFINITY) most = fmaxf(most, fabsf(f[i]));
         }
-        top = key_value(__reduce_max_sync(kFullMask, order_key(top)));
-        most = key_value(__reduce_max_sync(kFullMask, order_key(most)));
-        bound = (a.softmax ? 3e-6f * top : fminf(4e-7f, 8e-6f * top)) + 1.5e-7f * most;
+        // Error of a score: the sigmoid's is below 4e-7 (exp2, its argument's rounding, the
+        // reciprocal), the softmax's below 4e-6 of the largest, which is 1 / z (also the rounding
+        // of l - m, up to 1024 sums).  Then the rounding of s + bias.
+        bound = (a.softmax ? 4e-6f * inv : 4e-7f) +
+                1.5e-7f * __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(most)));
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool on = l[i] > -INFINITY;
-            key[i] = e0 + i >= a.E ? 0u : (on ? order_key(l[i] + 0.f) : 1u);     // (-0 ranks as +0)
-            v[i] = e0 + i >= a.E ? -FLT_MAX : (on ? l[i] : -3.395e38f);
-        }
+        for (int i = 0; i < NV; ++i)     // (-0 ranks as +0, NaN as the lowest)
+            f[i] = fmaxf(l[i] <= kMaskedLogit ? kMaskedRankLogit : l[i] + 0.f, kMaskedRankLogit);
     }
-    bool sure = true;
+    bool sure = true, out = live <= 0;       // out: nothing of this lane is in the running
+    float x;                                 // the lane's maximum
+    const int G = a.E / a.n_group;
     if (a.n_group > 1) {
         float s1, s2;
-        group_top2<float, NV>(a, v, lane, -FLT_MAX, s1, s2);
-        float score = a.group_top == 2 ? s1 + s2 : s1;
-        if (!(score >= -FLT_MAX)) score = -FLT_MAX;      // (-inf, NaN)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i >= live) f[i] = kOut;
+        group_top2<float, NV>(a, f, lane, -FLT_MAX, s1, s2);
+        const float score = a.group_top == 2 ? s1 + s2 : s1;
         const int rank = lane_rank(score, lane, a.n_group);      // (every lane takes part)
         const bool mine = lane < a.n_group, in = mine && rank < a.topk_group;
         uint32_t kept = __ballot_sync(kFullMask, in);
         if (scored && a.topk_group < a.n_group) {
-            const uint32_t k = order_key(score);
-            const uint32_t lo = __reduce_min_sync(kFullMask, in ? k : 0xffffffffu);
-            const uint32_t hi = __reduce_max_sync(kFullMask, mine && !in ? k : 0u);
-            sure = key_value(lo) - key_value(hi) > 4.f * bound;
-            if (!sure) sure = groups_fp64<NV>(a, l, v, lane, bound, kept);
+            const float lo = __shfl_sync(kFullMask, score, __ffs(__ballot_sync(kFullMask, mine && rank == a.topk_group - 1)) - 1);
+            const float hi = __shfl_sync(kFullMask, score, __ffs(__ballot_sync(kFullMask, mine && rank == a.topk_group)) - 1);
+            sure = lo - hi > 4.f * bound;
+            if (!sure) sure = groups_fp64<NV>(a, l, f, lane, bound, kept);
         }
-        const int G = a.E / a.n_group;
         if (G % NV == 0) {
-            if (e0 < a.E && !((kept >> (e0 / G)) & 1u))
-#pragma unroll
-                for (int i = 0; i < NV; ++i) key[i] = 0u;
+            out = out || !((kept >> (e0 / G)) & 1u);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (e0 + i < a.E && !((kept >> ((e0 + i) / G)) & 1u)) key[i] = 0u;
+                if (i < live && !((kept >> ((e0 + i) / G)) & 1u)) f[i] = kOut;
         }
     }
     int expert = 0, place = 32;              // this lane's expert and its place in the order
     if (sure) {
-        // K-th largest of the lanes' maxima (bitonic sort, descending)
-        uint32_t x = 0u;
+        x = kOut;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) x = key[i] > x ? key[i] : x;
+        for (int i = 0; i < NV; ++i) x = fmaxf(x, i < live ? f[i] : kOut);
+        if (out) x = kOut;
+        // K-th largest of the lanes' maxima (bitonic sort, descending)
 #pragma unroll
         for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
             for (int j = k >> 1; j > 0; j >>= 1) {
-                const uint32_t o = __shfl_xor_sync(kFullMask, x, j);
-                x = ((lane & k) == 0) == ((lane & j) == 0) ? max(x, o) : min(x, o);
+                const float o = __shfl_xor_sync(kFullMask, x, j);
+                x = ((lane & k) == 0) == ((lane & j) == 0) ? fmaxf(x, o) : fminf(x, o);
             }
-        uint32_t least = __shfl_sync(kFullMask, x, a.K - 1);
-        if (least > 1u && a.bias) {
-            const float f = key_value(least) - 2.f * bound;
-            least = f == f ? order_key(f) : 1u;
-        }
-        if (least == 0u) least = 1u;
+        float least = __shfl_sync(kFullMask, x, a.K - 1);
+        if (a.bias) least -= 2.f * bound;
+        least = fmaxf(least, -FLT_MAX);      // (fewer lanes than K hold anything)
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) n += key[i] >= least;
+        for (int i = 0; i < NV; ++i) n += !out && i < live && f[i] >= least;
         int at = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -398,53 +385,65 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
             at -= n;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (key[i] >= least) cand[threadIdx.y][at++] = make_uint2(key[i], static_cast<uint32_t>(e0 + i));
+                if (!out && i < live && f[i] >= least) {
+                    cand_f[wy][at] = f[i];
+                    cand_e[wy][at] = e0 + i;
+                    ++at;
+                }
+            if (lane < 4) cand_f[wy][C + lane] = kOut;
             __syncwarp();
-            uint32_t k = 0u;
+            float mine = kOut;
             if (lane < C) {
-                const uint2 c = cand[threadIdx.y][lane];
-                k = c.x;
-                expert = static_cast<int>(c.y);
+                mine = cand_f[wy][lane];
+                expert = cand_e[wy][lane];
             }
-            const float f = key_value(k);
             int rank = 0;
-            bool close = false;
-            for (int j = 0; j < C; ++j) {
-                const uint32_t o = __shfl_sync(kFullMask, k, j);
-                rank += o > k || (o == k && j < lane);
-                // (masked experts, key 1, are equal among themselves)
-                if (a.bias) close |= j != lane && k > 1u && o > 1u && !(fabsf(key_value(o) - f) > 2.f * bound);
+            for (int j = 0; j < C; j += 4) {
+                const float4 o = *reinterpret_cast<const float4 *>(&cand_f[wy][j]);
+                rank += j < lane ? o.x >= mine : o.x > mine;
+                rank += j + 1 < lane ? o.y >= mine : o.y > mine;
+                rank += j + 2 < lane ? o.z >= mine : o.z > mine;
+                rank += j + 3 < lane ? o.w >= mine : o.w > mine;
             }
             place = lane < C ? rank : 32;
-            if (a.bias && __any_sync(kFullMask, close && lane < C)) {
-                if (a.softmax) {
-                    sure = false;
-                } else {
-                    double d = -DBL_MAX;
-                    if (lane < C) {
-                        const double x64 = static_cast<double>(logit_at(a.logits, F32, base + expert));
-                        d = 1.0 / (1.0 + exp(-x64)) + static_cast<double>(a.bias[expert]);
-                        d = k <= 1u ? kMaskedSel : fmax(d, 0.1 * kMaskedSel);
+            if (a.bias) {
+                // neighbours in the order that the bound does not tell apart (masked experts
+                // and biases of -inf are equal among themselves)
+                __syncwarp();
+                if (lane < C) cand_f[wy][rank] = mine;
+                __syncwarp();
+                const float next = lane < C ? cand_f[wy][rank + 1] : kOut;
+                const bool close = mine > kLeastRank && next > kLeastRank && !(mine - next > 2.f * bound);
+                if (__any_sync(kFullMask, close)) {
+                    if (a.softmax) {
+                        sure = false;
+                    } else {
+                        double d = -DBL_MAX;
+                        if (lane < C) {
+                            const double x64 = static_cast<double>(logit_at(a.logits, F32, base + expert));
+                            d = 1.0 / (1.0 + exp(-x64)) + static_cast<double>(a.bias[expert]);
+                            d = mine <= kMaskedRank ? kMaskedSel : fmax(d, 0.1 * kMaskedSel);
+                        }
+                        const int r64 = lane_rank(d, lane, C);
+                        if (lane < C) place = r64;
                     }
-                    const int r64 = lane_rank(d, lane, C);
-                    if (lane < C) place = r64;
                 }
             }
         } else if (a.bias) {
             sure = false;
         } else {
             for (int r = 0; r < a.K; ++r) {
-                uint32_t best = 0u;
+                float best = kOut;
                 int e = 1 << 30;
 #pragma unroll
                 for (int i = NV - 1; i >= 0; --i)
-                    if (key[i] >= best) { best = key[i]; e = e0 + i; }
-                const uint32_t top = __reduce_max_sync(kFullMask, best);
-                const int win = __reduce_min_sync(kFullMask, best == top ? e : 1 << 30);
+                    if (!out && i < live && f[i] >= best && f[i] > kOut) { best = f[i]; e = e0 + i; }
+                const uint32_t key = order_key(best), top = __reduce_max_sync(kFullMask, key);
+                const int win = __reduce_min_sync(kFullMask, key == top ? e : 1 << 30);
                 if (lane == r) { expert = win; place = r; }
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
-                    if (e0 + i == win) key[i] = 0u;
+                    if (e0 + i == win) f[i] = kOut;
             }
         }
     }
