@@ -211,30 +211,34 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
     return mine;
 }
 
-// The groups kept, by scores in fp64 of every lane's two largest values (v: sel within `bound`):
-// where lanes hold whole groups, the score is a sigmoid and no lane's third value comes close
-// to its second.  False where that does not hold.
+// The groups kept (a bit each), by scores in fp64 of every lane's two largest values (sel within
+// `bound`): where lanes hold whole groups, the score is a sigmoid and no lane's third value
+// comes close to its second.  0 where that does not hold.  (Out of line, on values of its own:
+// it is rare, and arrays handed to it would keep the caller's in local memory.)
 template <int NV>
-__device__ __noinline__ bool groups_fp64(const RouteArgs &a, const float (&l)[NV], const float (&v)[NV], int lane,
-                                         float bound, uint32_t &kept)
+__device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, int lane, float bound)
 {
     const int G = a.E / a.n_group, per = G / NV;
-    if (a.softmax || G % NV || (per & (per - 1))) return false;
+    if (a.softmax || G % NV || (per & (per - 1))) return 0u;
     float v1 = -FLT_MAX, v2 = -FLT_MAX, v3 = -FLT_MAX, l1 = 0.f, l2 = 0.f;
     int e1 = 0, e2 = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = lane * NV + i;
-        if (v[i] > v1) {
+        if (e >= a.E) break;
+        const float l = logit_at(a.logits, a.fp32, base + e);
+        const float v = l <= kMaskedLogit ? kMaskedRank
+                                          : fmaxf(rough_sigmoid(l) + (a.bias ? a.bias[e] : 0.f), kLeastRank);
+        if (v > v1) {
             v3 = v2; v2 = v1; l2 = l1; e2 = e1;
-            v1 = v[i]; l1 = l[i]; e1 = e;
-        } else if (v[i] > v2) {
-            v3 = v2; v2 = v[i]; l2 = l[i]; e2 = e;
+            v1 = v; l1 = l; e1 = e;
+        } else if (v > v2) {
+            v3 = v2; v2 = v; l2 = l; e2 = e;
         } else {
-            v3 = fmaxf(v3, v[i]);
+            v3 = fmaxf(v3, v);
         }
     }
-    if (__any_sync(kFullMask, v3 > kMaskedRank && !(v2 - v3 > 2.f * bound))) return false;
+    if (__any_sync(kFullMask, v3 > kMaskedRank && !(v2 - v3 > 2.f * bound))) return 0u;
     auto exact = [&](float s, float x, int e) -> double {
         if (!(s > kMaskedRank)) return kMaskedSel;
         const double d = 1.0 / (1.0 + exp(-static_cast<double>(x)));
@@ -246,12 +250,11 @@ __device__ __noinline__ bool groups_fp64(const RouteArgs &a, const float (&l)[NV
     x = __shfl_sync(kFullMask, x, lane * per & 31);
     y = __shfl_sync(kFullMask, y, lane * per & 31);
     const int rank = lane_rank(a.group_top == 2 ? x + y : x, lane, a.n_group);
-    kept = __ballot_sync(kFullMask, lane < a.n_group && rank < a.topk_group);
-    return true;
+    return __ballot_sync(kFullMask, lane < a.n_group && rank < a.topk_group);
 }
 
 template <int NV, bool F32>
-__global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
+__global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const __grid_constant__ RouteArgs a)
 {
     __shared__ __align__(16) float cand_f[WPC][36];      // candidates in expert order
     __shared__ int cand_e[WPC][32];
@@ -344,7 +347,10 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const RouteArgs a)
             const float lo = __shfl_sync(kFullMask, score, __ffs(__ballot_sync(kFullMask, mine && rank == a.topk_group - 1)) - 1);
             const float hi = __shfl_sync(kFullMask, score, __ffs(__ballot_sync(kFullMask, mine && rank == a.topk_group)) - 1);
             sure = lo - hi > 4.f * bound;
-            if (!sure) sure = groups_fp64<NV>(a, l, f, lane, bound, kept);
+            if (!sure) {
+                kept = groups_fp64<NV>(a, base, lane, bound);
+                sure = kept != 0u;
+            }
         }
         if (G % NV == 0) {
             out = out || !((kept >> (e0 / G)) & 1u);
