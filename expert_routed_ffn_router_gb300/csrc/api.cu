@@ -705,8 +705,11 @@ int moe_layer_norm_backward(const void *dy, const void *x, int x_fp32, const flo
     }
     if ((rc = check_ptrs({dy, x, gamma, mean, rstd, dx})) || (rc = check_opt(dres))) return rc;
     if ((rc = check_ws(ws, ws_bytes, moe_layer_norm_backward_workspace_bytes(T, H)))) return rc;
-    return cuda_status(launch_norm_bwd(dy, x, x_fp32, gamma, mean, rstd, dres, T, H, dx, dgamma, dbeta,
-                                       reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeader), st));
+    return debug_status(cuda_status(launch_norm_bwd(
+                            dy, x, x_fp32, gamma, mean, rstd, dres, T, H, dx, dgamma, dbeta,
+                            reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeader),
+                            static_cast<int *>(ws), g_wait_limit_ns, st)),
+                        ws, stream);
 }
 
 int moe_route_logits(const void *logits, int logits_fp32, const float *bias, int T, int E, int K,

@@ -88,7 +88,8 @@ cudaError_t launch_norm(const void *x, int x_fp32, const float *gamma, const flo
 int norm_bwd_ctas(int T, int H);
 cudaError_t launch_norm_bwd(const void *dy, const void *x, int x_fp32, const float *gamma, const float *mean,
                             const float *rstd, const void *dres, int T, int H, void *dx, float *dgamma,
-                            float *dbeta, float *part, cudaStream_t s);
+                            float *dbeta, float *part, int *status, unsigned long long timeout_ns,
+                            cudaStream_t s);
 
 // --------------------------------------------------------------- routing from given logits
 cudaError_t launch_route(const void *logits, int fp32, const float *bias, int T, int E, int K,

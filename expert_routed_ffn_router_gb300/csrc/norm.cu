@@ -149,97 +149,220 @@ struct NormBwd {
     void *dx;
     float *part;           // [gridDim.x][2][H]
     int T, H;
+    // rows longer than WARP_COLS: stages of the ring, whether they hold dres, the offsets of
+    // dy and dres in a stage, its bytes
+    int stages, res_staged, off_dy, off_res, stage_bytes;
+    int *status;
+    unsigned long long timeout_ns;
 };
 
-// One row of the backward pass from this thread's columns; adds to its weight sums.
-template <bool XF32, int VPT, bool ONE>
-__device__ __forceinline__ void norm_bwd_row(const NormBwd &p, int row, const float (&g)[VPT][8],
-                                             float (&dg)[VPT][8], float (&db)[VPT][8], float (*red)[32])
+// Rows of up to WARP_COLS columns: a warp per row, its weight sums in registers; the CTA's
+// warps' sums are added in warp order.
+template <bool XF32, int VPT>
+__global__ void __launch_bounds__(32 * ROWS_PER_CTA) norm_bwd_warp_kernel(const NormBwd p)
 {
-    const size_t base = static_cast<size_t>(row) * p.H;
-    const float mu = p.mean[row], r = p.rstd[row];
-    float xh[VPT][8], a[VPT][8];
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (threadIdx.x + i * blockDim.x);
-        if (c < p.H) {
-            load8<XF32>(p.x, base + c, xh[i]);
-            load8<false>(p.dy, base + c, a[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                xh[i][j] = (xh[i][j] - mu) * r;
-                dg[i][j] = fmaf(a[i][j], xh[i][j], dg[i][j]);
-                db[i][j] += a[i][j];
-                a[i][j] *= g[i][j];
-                s0 += a[i][j];
-                s1 = fmaf(a[i][j], xh[i][j], s1);
-            }
-        }
-    }
-    const float inv = 1.f / static_cast<float>(p.H);
-    s0 = row_sum<ONE>(s0, red[0]) * inv;
-    s1 = row_sum<ONE>(s1, red[1]) * inv;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (threadIdx.x + i * blockDim.x);
-        if (c < p.H) {
-            float e[8];
-            if (p.dres) load8<XF32>(p.dres, base + c, e);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a[i][j] = r * (a[i][j] - s0 - xh[i][j] * s1);
-                if (p.dres) a[i][j] += e[j];
-            }
-            store8<XF32>(p.dx, base + c, a[i]);
-        }
-    }
-}
-
-template <bool XF32, int VPT, bool ONE, int MAXT = 32 * ROWS_PER_CTA>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p)
-{
-    __shared__ float red[4][32];
-    __shared__ float comb[ONE ? ROWS_PER_CTA : 1][ONE ? 32 * 8 : 1];
+    __shared__ float comb[ROWS_PER_CTA][32 * 8];
     pdl_wait();
+    const int lane = threadIdx.x;
     float g[VPT][8], dg[VPT][8], db[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (threadIdx.x + i * blockDim.x);
+        const int c = 8 * (lane + 32 * i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[i][j] = dg[i][j] = db[i][j] = 0.f;
         if (c < p.H) load8<true>(p.gamma, c, g[i]);
     }
-    if (ONE) {
-        for (int row = blockIdx.x * ROWS_PER_CTA + threadIdx.y; row < p.T; row += gridDim.x * ROWS_PER_CTA)
-            norm_bwd_row<XF32, VPT, ONE>(p, row, g, dg, db, red);
-    } else {
-        int k = 0;
-        for (int row = blockIdx.x; row < p.T; row += gridDim.x, k ^= 2)
-            norm_bwd_row<XF32, VPT, ONE>(p, row, g, dg, db, red + k);
+    const float inv = 1.f / static_cast<float>(p.H);
+    for (int row = blockIdx.x * ROWS_PER_CTA + threadIdx.y; row < p.T; row += gridDim.x * ROWS_PER_CTA) {
+        const size_t base = static_cast<size_t>(row) * p.H;
+        const float mu = p.mean[row], r = p.rstd[row];
+        float xh[VPT][8], a[VPT][8];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = 8 * (lane + 32 * i);
+            if (c < p.H) {
+                load8<XF32>(p.x, base + c, xh[i]);
+                load8<false>(p.dy, base + c, a[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    xh[i][j] = (xh[i][j] - mu) * r;
+                    dg[i][j] = fmaf(a[i][j], xh[i][j], dg[i][j]);
+                    db[i][j] += a[i][j];
+                    a[i][j] *= g[i][j];
+                    s0 += a[i][j];
+                    s1 = fmaf(a[i][j], xh[i][j], s1);
+                }
+            }
+        }
+        s0 = warp_sum(s0) * inv;
+        s1 = warp_sum(s1) * inv;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = 8 * (lane + 32 * i);
+            if (c < p.H) {
+                float e[8];
+                if (p.dres) load8<XF32>(p.dres, base + c, e);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    a[i][j] = r * (a[i][j] - s0 - xh[i][j] * s1);
+                    if (p.dres) a[i][j] += e[j];
+                }
+                store8<XF32>(p.dx, base + c, a[i]);
+            }
+        }
     }
-    // the CTA's sums (ONE: its warps' sums added in warp order)
     float *part = p.part + static_cast<size_t>(blockIdx.x) * 2 * p.H;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = 8 * (threadIdx.x + i * blockDim.x);
-            float(&v)[8] = w ? db[i] : dg[i];
-            if (ONE) {
-                __syncthreads();
+            const int c = 8 * (lane + 32 * i);
+            __syncthreads();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) comb[threadIdx.y][j * 32 + threadIdx.x] = v[j];
-                __syncthreads();
-                // thread (lane, warp y) adds element y of every warp's vector
-                float t = 0.f;
+            for (int j = 0; j < 8; ++j) comb[threadIdx.y][j * 32 + lane] = w ? db[i][j] : dg[i][j];
+            __syncthreads();
+            // thread (lane, warp y) adds element y of every warp's vector
+            float t = 0.f;
 #pragma unroll
-                for (int y = 0; y < ROWS_PER_CTA; ++y) t += comb[y][threadIdx.y * 32 + threadIdx.x];
-                if (c < p.H) part[w * p.H + c + threadIdx.y] = t;
-            } else if (c < p.H) {
-                store8<true>(part, static_cast<size_t>(w) * p.H + c, v);
-            }
+            for (int y = 0; y < ROWS_PER_CTA; ++y) t += comb[y][threadIdx.y * 32 + lane];
+            if (c < p.H) part[w * p.H + c + threadIdx.y] = t;
         }
+    }
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+template <bool F32>
+__device__ __forceinline__ float4 load4(const void *p, int c)
+{
+    if (F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c);
+    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + c);
+    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+}
+
+// Longer rows: a CTA per row, 4 x VPT columns a thread.  The rows x, dy (and dres) of the CTA
+// arrive by bulk copies in a ring of shared-memory stages, so that loads never wait for a
+// row's two sums (plain loads before and after the barriers of two CTAs an SM: 402 us for
+// 16384 rows of 7168 in fp32 with dres, 4.1 TB/s; this: NEWT).  One barrier a row: its sums;
+// a row's stage is filled again behind the next row's.  GREG: gamma stays in registers.
+template <bool XF32, int VPT, bool GREG, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_bwd_ring_kernel(const NormBwd p)
+{
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ float2 red[2][32];
+    __shared__ uint64_t full[4];
+    __shared__ int abort_s;
+    volatile int *abort_flag = &abort_s;
+    const int tid = threadIdx.x, S = p.stages, H = p.H;
+    const int nw = blockDim.x >> 5;
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+        abort_s = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    constexpr int XB = XF32 ? 4 : 2;
+    auto fill = [&](int row, int s) {
+        unsigned char *st = ring + static_cast<size_t>(s) * p.stage_bytes;
+        const size_t base = static_cast<size_t>(row) * H;
+        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(H) * (2 + XB + (p.res_staged ? XB : 0)));
+        bulk_load(st, static_cast<const unsigned char *>(p.x) + base * XB, H * XB, &full[s]);
+        bulk_load(st + p.off_dy, p.dy + base, H * 2, &full[s]);
+        if (p.res_staged) bulk_load(st + p.off_res, static_cast<const unsigned char *>(p.dres) + base * XB, H * XB, &full[s]);
+    };
+    const int first = blockIdx.x, step = gridDim.x;
+    int ahead = first;                       // next row to fill (thread 0)
+    if (tid == 0)
+        for (int s = 0; s < S && ahead < p.T; ++s, ahead += step) fill(ahead, s);
+    float4 g[GREG ? VPT : 1], dg[VPT], db[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = 4 * (tid + i * blockDim.x);
+        if (GREG) g[i % (GREG ? VPT : 1)] = c < H ? load4<true>(p.gamma, c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        dg[i] = db[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float inv = 1.f / static_cast<float>(H);
+    int s = 0, prev = -1, k = 0;
+    uint32_t ph = 0;
+    for (int row = first; row < p.T; row += step, k ^= 1) {
+        const float mu = p.mean[row], r = p.rstd[row];
+        // (a wait that runs out is recorded; the row's results are then void)
+        mbar_wait(&full[s], ph, abort_flag, p.status, p.timeout_ns);
+        const unsigned char *st = ring + static_cast<size_t>(s) * p.stage_bytes;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = 4 * (tid + i * blockDim.x);
+            if (c >= H) continue;
+            const float4 x = load4<XF32>(st, c), d = load4<false>(st + p.off_dy, c);
+            const float4 gm = GREG ? g[i % (GREG ? VPT : 1)] : load4<true>(p.gamma, c);
+            const float4 h = make_float4((x.x - mu) * r, (x.y - mu) * r, (x.z - mu) * r, (x.w - mu) * r);
+            dg[i].x = fmaf(d.x, h.x, dg[i].x); dg[i].y = fmaf(d.y, h.y, dg[i].y);
+            dg[i].z = fmaf(d.z, h.z, dg[i].z); dg[i].w = fmaf(d.w, h.w, dg[i].w);
+            db[i].x += d.x; db[i].y += d.y; db[i].z += d.z; db[i].w += d.w;
+            const float4 a = make_float4(gm.x * d.x, gm.y * d.y, gm.z * d.z, gm.w * d.w);
+            s0 += (a.x + a.y) + (a.z + a.w);
+            s1 += fmaf(a.x, h.x, a.y * h.y) + fmaf(a.z, h.z, a.w * h.w);
+        }
+        s0 = warp_sum(s0);
+        s1 = warp_sum(s1);
+        if ((tid & 31) == 0) red[k][tid >> 5] = make_float2(s0, s1);
+        __syncthreads();
+        // every thread is done with the row before: its stage takes a row further on
+        if (tid == 0 && prev >= 0 && ahead < p.T) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            fill(ahead, prev);
+            ahead += step;
+        }
+        const float2 q = (tid & 31) < nw ? red[k][tid & 31] : make_float2(0.f, 0.f);
+        s0 = warp_sum(q.x) * inv;
+        s1 = warp_sum(q.y) * inv;
+        const size_t base = static_cast<size_t>(row) * H;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = 4 * (tid + i * blockDim.x);
+            if (c >= H) continue;
+            const float4 x = load4<XF32>(st, c), d = load4<false>(st + p.off_dy, c);
+            const float4 gm = GREG ? g[i % (GREG ? VPT : 1)] : load4<true>(p.gamma, c);
+            float4 o;
+            o.x = r * (gm.x * d.x - s0 - (x.x - mu) * r * s1);
+            o.y = r * (gm.y * d.y - s0 - (x.y - mu) * r * s1);
+            o.z = r * (gm.z * d.z - s0 - (x.z - mu) * r * s1);
+            o.w = r * (gm.w * d.w - s0 - (x.w - mu) * r * s1);
+            if (p.dres) {
+                const float4 e = p.res_staged ? load4<XF32>(st + p.off_res, c)
+                                              : load4<XF32>(static_cast<const unsigned char *>(p.dres) + base * XB, c);
+                o.x += e.x; o.y += e.y; o.z += e.z; o.w += e.w;
+            }
+            if (XF32)
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.dx) + base + c) = o;
+            else
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.dx) + base + c) =
+                    make_uint2(f32x2_to_bf16x2(o.y, o.x), f32x2_to_bf16x2(o.w, o.z));
+        }
+        prev = s;
+        if (++s == S) { s = 0; ph ^= 1u; }
+    }
+    // (after a wait that ran out: copies in flight land before the CTA leaves)
+    __syncthreads();
+    if (*abort_flag && tid == 0) {
+        int dummy = 0;
+        for (int j = 0; j < S; ++j) mbar_wait(&full[j], ph, &dummy, nullptr, 20000000ull);
+    }
+    float *part = p.part + static_cast<size_t>(blockIdx.x) * 2 * H;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = 4 * (tid + i * blockDim.x);
+        if (c >= H) continue;
+        *reinterpret_cast<float4 *>(part + c) = dg[i];
+        *reinterpret_cast<float4 *>(part + H + c) = db[i];
     }
 }
 
@@ -276,26 +399,62 @@ cudaError_t fwd(const void *x, const float *gamma, const float *beta, int T, int
     return launch_pdl(norm_fwd_kernel<XF32, 2, false>, dim3(T), dim3(cta_threads(H, 2)), 0, s, 1, x, gamma, beta, T, H, eps, y, mean, rstd);
 }
 
+constexpr size_t RING_BYTES = 220 * 1024;     // shared memory of an SM for the rings
+
+// Rows longer than WARP_COLS: the ring's stages (two at least; three and four where they fit
+// with dres, which is otherwise loaded directly) and its shared memory.
+size_t plan_ring(NormBwd &p, int xb, bool res)
+{
+    auto stage = [&](bool with) { return static_cast<size_t>(p.H) * (xb + 2 + (with ? xb : 0)); };
+    const bool staged = res && 3 * stage(true) <= RING_BYTES;
+    const size_t b = stage(staged);
+    p.res_staged = staged ? 1 : 0;
+    p.stages = static_cast<int>(RING_BYTES / b < 4 ? RING_BYTES / b : 4);
+    p.off_dy = p.H * xb;
+    p.off_res = p.H * (xb + 2);
+    p.stage_bytes = static_cast<int>(b);
+    return b * p.stages;
+}
+
+// CTAs that share an SM in the longest-row launch
+int ring_ctas(int H)
+{
+    NormBwd p{};
+    p.H = H;
+    const int n = static_cast<int>(RING_BYTES / plan_ring(p, 4, true));
+    return n < 1 ? 1 : (n > 4 ? 4 : n);
+}
+
+template <bool XF32, int VPT, bool GREG, int MAXT>
+cudaError_t ring(NormBwd &p, int n, cudaStream_t s)
+{
+    const size_t smem = plan_ring(p, XF32 ? 4 : 2, p.dres != nullptr);
+    const void *fn = reinterpret_cast<const void *>(norm_bwd_ring_kernel<XF32, VPT, GREG, MAXT>);
+    const cudaError_t e = ensure_smem(fn, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(norm_bwd_ring_kernel<XF32, VPT, GREG, MAXT>, dim3(n),
+                      dim3((p.H / 4 + VPT * 32 - 1) / (VPT * 32) * 32), smem, s, 1, p);
+}
+
 template <bool XF32>
-cudaError_t bwd(const NormBwd &p, int n, cudaStream_t s)
+cudaError_t bwd(NormBwd &p, int n, cudaStream_t s)
 {
     const dim3 warps(32, ROWS_PER_CTA), g(n);
-    if (p.H <= 256) return launch_pdl(norm_bwd_kernel<XF32, 1, true>, g, warps, 0, s, 1, p);
-    if (p.H <= 512) return launch_pdl(norm_bwd_kernel<XF32, 2, true>, g, warps, 0, s, 1, p);
-    if (p.H <= WARP_COLS) return launch_pdl(norm_bwd_kernel<XF32, 4, true>, g, warps, 0, s, 1, p);
-    // (up to 8192 columns 512 threads of at most 128 registers; the longest rows spill)
-    if (p.H <= 8192) return launch_pdl(norm_bwd_kernel<XF32, 2, false, 512>, g, dim3(cta_threads(p.H, 2)), 0, s, 1, p);
-    return launch_pdl(norm_bwd_kernel<XF32, 2, false, 1024>, g, dim3(cta_threads(p.H, 2)), 0, s, 1, p);
+    if (p.H <= 256) return launch_pdl(norm_bwd_warp_kernel<XF32, 1>, g, warps, 0, s, 1, p);
+    if (p.H <= 512) return launch_pdl(norm_bwd_warp_kernel<XF32, 2>, g, warps, 0, s, 1, p);
+    if (p.H <= WARP_COLS) return launch_pdl(norm_bwd_warp_kernel<XF32, 4>, g, warps, 0, s, 1, p);
+    if (p.H <= 2048) return ring<XF32, 2, true, 256>(p, n, s);
+    if (p.H <= 8192) return ring<XF32, 4, true, 512>(p, n, s);
+    return ring<XF32, 4, false, 1024>(p, n, s);
 }
 
 }  // namespace
 
-// CTAs of the backward launch: as many rows in flight as fit, so that the partial sums (8 H
-// bytes a CTA) stay small beside the rows.
+// CTAs of the backward launch (their partial sums take 8 H bytes each).
 int norm_bwd_ctas(int T, int H)
 {
     const int units = H <= WARP_COLS ? (T + ROWS_PER_CTA - 1) / ROWS_PER_CTA : T;
-    const int most = 2 * num_sms();
+    const int most = (H <= WARP_COLS ? 2 : ring_ctas(H)) * num_sms();
     return units < most ? (units > 0 ? units : 1) : most;
 }
 
@@ -309,9 +468,11 @@ cudaError_t launch_norm(const void *x, int x_fp32, const float *gamma, const flo
 
 cudaError_t launch_norm_bwd(const void *dy, const void *x, int x_fp32, const float *gamma, const float *mean,
                             const float *rstd, const void *dres, int T, int H, void *dx, float *dgamma,
-                            float *dbeta, float *part, cudaStream_t s)
+                            float *dbeta, float *part, int *status, unsigned long long timeout_ns,
+                            cudaStream_t s)
 {
-    NormBwd p{static_cast<const uint16_t *>(dy), x, gamma, mean, rstd, dres, dx, part, T, H};
+    NormBwd p{static_cast<const uint16_t *>(dy), x, gamma, mean, rstd, dres, dx, part, T, H, 0, 0, 0, 0, 0,
+              status, timeout_ns};
     const int n = norm_bwd_ctas(T, H);
     const cudaError_t e = x_fp32 ? bwd<true>(p, n, s) : bwd<false>(p, n, s);
     if (e != cudaSuccess) return e;
