@@ -18,7 +18,8 @@
 namespace moe {
 namespace {
 
-constexpr int WARP_COLS = 1024;       // longest row that one warp takes
+constexpr int WARP_COLS = 1024;       // longest row that one warp takes (forward)
+constexpr int WARP_COLS_BWD = 512;    // ... backward (at 1024, 198 registers: 86 us for 16384 rows, ring NEWT)
 constexpr int ROWS_PER_CTA = 8;       // ... with this many warps a CTA
 
 __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8])
@@ -141,6 +142,122 @@ __global__ void __launch_bounds__(ONE ? 32 * ROWS_PER_CTA : 1024)
     }
 }
 
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+template <bool F32>
+__device__ __forceinline__ float4 load4(const void *p, int c)
+{
+    if (F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c);
+    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + c);
+    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+}
+
+// Longer rows of a batch that gives every CTA several: the rows of x arrive by bulk copies in a
+// ring of shared-memory stages, 4 x VPT columns a thread in registers from there.  A row's
+// stage is filled again behind the barrier of its mean.  (A CTA per row, 448 threads of plain
+// loads, took 154 us for 16384 rows of 7168 in fp32 and 163 us in bf16; this: NEWT.)
+struct NormFwd {
+    const void *x;
+    const float *gamma, *beta;     // beta nullable
+    int T, H;
+    float eps;
+    uint16_t *y;
+    float *mean, *rstd;            // nullable
+    int stages, stage_bytes;
+    unsigned long long timeout_ns;
+};
+
+template <bool XF32, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kernel(const NormFwd p)
+{
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ float red[2][32];
+    __shared__ uint64_t full[4];
+    __shared__ int abort_s;
+    volatile int *abort_flag = &abort_s;
+    const int tid = threadIdx.x, S = p.stages, H = p.H;
+    const int nw = blockDim.x >> 5;
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+        abort_s = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    constexpr int XB = XF32 ? 4 : 2;
+    auto fill = [&](int row, int s) {
+        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(H) * XB);
+        bulk_load(ring + static_cast<size_t>(s) * p.stage_bytes,
+                  static_cast<const unsigned char *>(p.x) + static_cast<size_t>(row) * H * XB, H * XB, &full[s]);
+    };
+    const int step = gridDim.x;
+    int ahead = blockIdx.x;                  // next row to fill (thread 0)
+    if (tid == 0)
+        for (int s = 0; s < S && ahead < p.T; ++s, ahead += step) fill(ahead, s);
+    const float inv = 1.f / static_cast<float>(H);
+    int s = 0;
+    uint32_t ph = 0;
+    auto sum = [&](float v, float *r) {      // over the CTA; one barrier
+        v = warp_sum(v);
+        if ((tid & 31) == 0) r[tid >> 5] = v;
+        __syncthreads();
+        return warp_sum((tid & 31) < nw ? r[tid & 31] : 0.f);
+    };
+    for (int row = blockIdx.x; row < p.T; row += step) {
+        mbar_wait(&full[s], ph, abort_flag, nullptr, p.timeout_ns);
+        const unsigned char *st = ring + static_cast<size_t>(s) * p.stage_bytes;
+        float4 v[VPT];
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = 4 * (tid + i * blockDim.x);
+            v[i] = c < H ? load4<XF32>(st, c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            a += (v[i].x + v[i].y) + (v[i].z + v[i].w);
+        }
+        const float mu = sum(a, red[0]) * inv;
+        // (every thread has read the row: its stage takes a row further on)
+        if (tid == 0 && ahead < p.T) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            fill(ahead, s);
+            ahead += step;
+        }
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (4 * (tid + i * blockDim.x) >= H) continue;
+            v[i] = make_float4(v[i].x - mu, v[i].y - mu, v[i].z - mu, v[i].w - mu);
+            a += fmaf(v[i].x, v[i].x, v[i].y * v[i].y) + fmaf(v[i].z, v[i].z, v[i].w * v[i].w);
+        }
+        const float r = 1.f / sqrtf(sum(a, red[1]) * inv + p.eps);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = 4 * (tid + i * blockDim.x);
+            if (c >= H) continue;
+            const float4 g = load4<true>(p.gamma, c);
+            const float4 b = p.beta ? load4<true>(p.beta, c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<uint2 *>(p.y + static_cast<size_t>(row) * H + c) =
+                make_uint2(f32x2_to_bf16x2(v[i].y * r * g.y + b.y, v[i].x * r * g.x + b.x),
+                           f32x2_to_bf16x2(v[i].w * r * g.w + b.w, v[i].z * r * g.z + b.z));
+        }
+        if (tid == 0) {
+            if (p.mean) p.mean[row] = mu;
+            if (p.rstd) p.rstd[row] = r;
+        }
+        if (++s == S) { s = 0; ph ^= 1u; }
+    }
+    // (after a wait that ran out: copies in flight land before the CTA leaves)
+    __syncthreads();
+    if (*abort_flag && tid == 0) {
+        int dummy = 0;
+        for (int j = 0; j < S; ++j) mbar_wait(&full[j], ph, &dummy, nullptr, 20000000ull);
+    }
+}
+
 struct NormBwd {
     const uint16_t *dy;
     const void *x;
@@ -149,14 +266,14 @@ struct NormBwd {
     void *dx;
     float *part;           // [gridDim.x][2][H]
     int T, H;
-    // rows longer than WARP_COLS: stages of the ring, whether they hold dres, the offsets of
+    // rows longer than WARP_COLS_BWD: stages of the ring, whether they hold dres, the offsets of
     // dy and dres in a stage, its bytes
     int stages, res_staged, off_dy, off_res, stage_bytes;
     int *status;
     unsigned long long timeout_ns;
 };
 
-// Rows of up to WARP_COLS columns: a warp per row, its weight sums in registers; the CTA's
+// Rows of up to WARP_COLS_BWD columns: a warp per row, its weight sums in registers; the CTA's
 // warps' sums are added in warp order.
 template <bool XF32, int VPT>
 __global__ void __launch_bounds__(32 * ROWS_PER_CTA) norm_bwd_warp_kernel(const NormBwd p)
@@ -231,28 +348,13 @@ __global__ void __launch_bounds__(32 * ROWS_PER_CTA) norm_bwd_warp_kernel(const 
     }
 }
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-template <bool F32>
-__device__ __forceinline__ float4 load4(const void *p, int c)
-{
-    if (F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c);
-    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + c);
-    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-}
-
 // Longer rows: a CTA per row, 4 x VPT columns a thread.  The rows x, dy (and dres) of the CTA
 // arrive by bulk copies in a ring of shared-memory stages, so that loads never wait for a
 // row's two sums (plain loads before and after the barriers of two CTAs an SM: 402 us for
 // 16384 rows of 7168 in fp32 with dres, 4.1 TB/s; this: NEWT).  One barrier a row: its sums;
 // a row's stage is filled again behind the next row's.  GREG: gamma stays in registers.
-template <bool XF32, int VPT, bool GREG, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_ring_kernel(const NormBwd p)
+template <bool XF32, int VPT, bool GREG, int MAXT, int CTAS>
+__global__ void __launch_bounds__(MAXT, CTAS) norm_bwd_ring_kernel(const NormBwd p)
 {
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ float2 red[2][32];
@@ -388,6 +490,28 @@ __global__ void __launch_bounds__(256) norm_wgrad_kernel(const float *__restrict
 
 int cta_threads(int H, int vpt) { return (H / 8 + vpt * 32 - 1) / (vpt * 32) * 32; }
 
+constexpr size_t RING_BYTES = 220 * 1024;     // shared memory of an SM for the rings
+
+int ring_threads(int H, int vpt) { return (H / 4 + vpt * 32 - 1) / (vpt * 32) * 32; }
+
+// Persistent CTAs of the forward ring: as many an SM as threads and two stages a CTA allow
+int fwd_ctas(int H, int xb)
+{
+    const int by_room = static_cast<int>(RING_BYTES / (2 * static_cast<size_t>(H) * xb)), by_threads = 1536 / ring_threads(H, 4);
+    const int n = by_room < by_threads ? by_room : by_threads;
+    return num_sms() * (n < 1 ? 1 : n);
+}
+
+template <bool XF32, int VPT, int MAXT>
+cudaError_t fwd_ring(const NormFwd &p, int ctas, cudaStream_t s)
+{
+    const size_t smem = static_cast<size_t>(p.stages) * p.stage_bytes;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(norm_fwd_ring_kernel<XF32, VPT, MAXT>), smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(norm_fwd_ring_kernel<XF32, VPT, MAXT>, dim3(ctas), dim3(ring_threads(p.H, VPT)),
+                      smem, s, 1, p);
+}
+
 template <bool XF32>
 cudaError_t fwd(const void *x, const float *gamma, const float *beta, int T, int H, float eps, uint16_t *y,
                 float *mean, float *rstd, cudaStream_t s)
@@ -396,65 +520,79 @@ cudaError_t fwd(const void *x, const float *gamma, const float *beta, int T, int
     if (H <= 256) return launch_pdl(norm_fwd_kernel<XF32, 1, true>, gw, warps, 0, s, 1, x, gamma, beta, T, H, eps, y, mean, rstd);
     if (H <= 512) return launch_pdl(norm_fwd_kernel<XF32, 2, true>, gw, warps, 0, s, 1, x, gamma, beta, T, H, eps, y, mean, rstd);
     if (H <= WARP_COLS) return launch_pdl(norm_fwd_kernel<XF32, 4, true>, gw, warps, 0, s, 1, x, gamma, beta, T, H, eps, y, mean, rstd);
+    // (up to eight rows a CTA of the ring, the plain launch's parallel rows are as fast)
+    const int ctas = fwd_ctas(H, XF32 ? 4 : 2);
+    if (T >= 8 * ctas) {
+        NormFwd p{x, gamma, beta, T, H, eps, y, mean, rstd, 0, H * (XF32 ? 4 : 2), 1000000000ull};
+        const size_t room = RING_BYTES / (ctas / num_sms());
+        p.stages = static_cast<int>(room / p.stage_bytes < 4 ? room / p.stage_bytes : 4);
+        return H <= 8192 ? fwd_ring<XF32, 4, 512>(p, ctas, s) : fwd_ring<XF32, 4, 1024>(p, ctas, s);
+    }
     return launch_pdl(norm_fwd_kernel<XF32, 2, false>, dim3(T), dim3(cta_threads(H, 2)), 0, s, 1, x, gamma, beta, T, H, eps, y, mean, rstd);
 }
 
-constexpr size_t RING_BYTES = 220 * 1024;     // shared memory of an SM for the rings
-
-// Rows longer than WARP_COLS: the ring's stages (two at least; three and four where they fit
+// Rows longer than WARP_COLS_BWD: the ring's stages (two at least; three and four where they fit
 // with dres, which is otherwise loaded directly) and its shared memory.
-size_t plan_ring(NormBwd &p, int xb, bool res)
+size_t plan_ring(NormBwd &p, int xb, bool res, int per_sm)
 {
+    const size_t room = RING_BYTES / per_sm;
     auto stage = [&](bool with) { return static_cast<size_t>(p.H) * (xb + 2 + (with ? xb : 0)); };
-    const bool staged = res && 3 * stage(true) <= RING_BYTES;
+    const bool staged = res && 2 * stage(true) <= room;
     const size_t b = stage(staged);
     p.res_staged = staged ? 1 : 0;
-    p.stages = static_cast<int>(RING_BYTES / b < 4 ? RING_BYTES / b : 4);
+    p.stages = static_cast<int>(room / b < 4 ? room / b : 4);
     p.off_dy = p.H * xb;
     p.off_res = p.H * (xb + 2);
     p.stage_bytes = static_cast<int>(b);
     return b * p.stages;
 }
 
-// CTAs that share an SM in the longest-row launch
-int ring_ctas(int H)
+// CTAs of the ring that share an SM: 1024 threads, where two stages of their rows fit.  One CTA a row of 7168 leaves the SM idle between a row's barriers (bf16 without
+// dres, 16384 rows: 190 us with one, NEWT with two).
+int ring_ctas(int H, int row_bytes)
 {
-    NormBwd p{};
-    p.H = H;
-    const int n = static_cast<int>(RING_BYTES / plan_ring(p, 4, true));
-    return n < 1 ? 1 : (n > 4 ? 4 : n);
+    const int most = 1024 / ring_threads(H, H <= 2048 ? 2 : 4);
+    const int n = static_cast<int>(RING_BYTES / (2 * static_cast<size_t>(row_bytes)));
+    return n < 1 ? 1 : (n < most ? n : most);
 }
 
-template <bool XF32, int VPT, bool GREG, int MAXT>
-cudaError_t ring(NormBwd &p, int n, cudaStream_t s)
+template <bool XF32, int VPT, bool GREG, int MAXT, int CTAS>
+cudaError_t ring(NormBwd &p, int per_sm, int n, cudaStream_t s)
 {
-    const size_t smem = plan_ring(p, XF32 ? 4 : 2, p.dres != nullptr);
-    const void *fn = reinterpret_cast<const void *>(norm_bwd_ring_kernel<XF32, VPT, GREG, MAXT>);
+    const size_t smem = plan_ring(p, XF32 ? 4 : 2, p.dres != nullptr, per_sm);
+    const void *fn = reinterpret_cast<const void *>(norm_bwd_ring_kernel<XF32, VPT, GREG, MAXT, CTAS>);
     const cudaError_t e = ensure_smem(fn, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(norm_bwd_ring_kernel<XF32, VPT, GREG, MAXT>, dim3(n),
-                      dim3((p.H / 4 + VPT * 32 - 1) / (VPT * 32) * 32), smem, s, 1, p);
+    return launch_pdl(norm_bwd_ring_kernel<XF32, VPT, GREG, MAXT, CTAS>, dim3(n), dim3(ring_threads(p.H, VPT)),
+                      smem, s, 1, p);
 }
 
+// n: CTAs launched
 template <bool XF32>
-cudaError_t bwd(NormBwd &p, int n, cudaStream_t s)
+cudaError_t bwd(NormBwd &p, int &n, cudaStream_t s)
 {
-    const dim3 warps(32, ROWS_PER_CTA), g(n);
-    if (p.H <= 256) return launch_pdl(norm_bwd_warp_kernel<XF32, 1>, g, warps, 0, s, 1, p);
-    if (p.H <= 512) return launch_pdl(norm_bwd_warp_kernel<XF32, 2>, g, warps, 0, s, 1, p);
-    if (p.H <= WARP_COLS) return launch_pdl(norm_bwd_warp_kernel<XF32, 4>, g, warps, 0, s, 1, p);
-    if (p.H <= 2048) return ring<XF32, 2, true, 256>(p, n, s);
-    if (p.H <= 8192) return ring<XF32, 4, true, 512>(p, n, s);
-    return ring<XF32, 4, false, 1024>(p, n, s);
+    const dim3 warps(32, ROWS_PER_CTA);
+    if (p.H <= WARP_COLS_BWD) {
+        n = norm_bwd_ctas(p.T, p.H);
+        if (p.H <= 256) return launch_pdl(norm_bwd_warp_kernel<XF32, 1>, dim3(n), warps, 0, s, 1, p);
+        return launch_pdl(norm_bwd_warp_kernel<XF32, 2>, dim3(n), warps, 0, s, 1, p);
+    }
+    constexpr int XB = XF32 ? 4 : 2;
+    const int per_sm = ring_ctas(p.H, p.H * (2 + XB + (p.dres ? XB : 0)));
+    n = per_sm * num_sms();
+    if (n > p.T) n = p.T;
+    if (p.H <= 2048) return ring<XF32, 2, true, 256, 4>(p, per_sm, n, s);
+    if (p.H > 8192) return ring<XF32, 4, false, 1024, 1>(p, per_sm, n, s);
+    return per_sm > 1 ? ring<XF32, 4, false, 512, 2>(p, per_sm, n, s) : ring<XF32, 4, true, 512, 1>(p, per_sm, n, s);
 }
 
 }  // namespace
 
-// CTAs of the backward launch (their partial sums take 8 H bytes each).
+// CTAs of the backward launch at most, for any type (their partial sums take 8 H bytes each).
 int norm_bwd_ctas(int T, int H)
 {
-    const int units = H <= WARP_COLS ? (T + ROWS_PER_CTA - 1) / ROWS_PER_CTA : T;
-    const int most = (H <= WARP_COLS ? 2 : ring_ctas(H)) * num_sms();
+    const int units = H <= WARP_COLS_BWD ? (T + ROWS_PER_CTA - 1) / ROWS_PER_CTA : T;
+    const int most = (H <= WARP_COLS_BWD ? 2 : ring_ctas(H, 4 * H)) * num_sms();
     return units < most ? (units > 0 ? units : 1) : most;
 }
 
@@ -473,7 +611,7 @@ cudaError_t launch_norm_bwd(const void *dy, const void *x, int x_fp32, const flo
 {
     NormBwd p{static_cast<const uint16_t *>(dy), x, gamma, mean, rstd, dres, dx, part, T, H, 0, 0, 0, 0, 0,
               status, timeout_ns};
-    const int n = norm_bwd_ctas(T, H);
+    int n = 0;
     const cudaError_t e = x_fp32 ? bwd<true>(p, n, s) : bwd<false>(p, n, s);
     if (e != cudaSuccess) return e;
     return launch_pdl(norm_wgrad_kernel, dim3(2 * H / 32), dim3(32, 8), 0, s, 1, static_cast<const float *>(part),
