@@ -42,18 +42,19 @@ namespace moe {
 namespace {
 
 constexpr int PADR = 64;                  // groups start at multiples of this many rows
-constexpr int TM = 256, TN = 256;         // tile of a cluster
+constexpr int TM = 256, TN = 256;         // tile of a cluster (TN: at most)
 constexpr int BK = 64;                    // depth of a stage
 constexpr int N_EPI = 8;                  // epilogue warps
-constexpr int NT = 64 + 32 * N_EPI;        // at most 168 registers a thread
+constexpr int NT = 64 + 32 * N_EPI;       // at most 168 registers a thread
 constexpr int MAXG = 1024;
 constexpr int HALF = 8192;                // one 64 x 64 bf16 box
-constexpr int STAGE = 4 * HALF;           // A: 128 rows of this CTA; B: 128 of the tile's columns
+constexpr int STAGE = 4 * HALF;           // A: 128 of the tile's rows; B: 128 of its columns
 constexpr int STAGES = 6;
-constexpr int SLAB = 4096;                // an epilogue warp's store buffer: 32 rows of 128 bytes
+constexpr int SLAB = 4096;                // an epilogue warp's store buffer
+constexpr int TQ = 4;                     // slots that hand claimed units to the roles
 // Stages of one sum in tensor memory in the products that d topk_w comes from (see above).
-constexpr int CHUNK = 8;
-constexpr int STASH = 32 * N_EPI * 128;   // floats of a CTA's stash: p of a unit
+constexpr int CHUNK = 6;
+constexpr int STASH = 32 * N_EPI * 2 * 128;   // floats of a CTA's stash: p and u of a unit
 
 // What the plan kernel leaves in the workspace.
 struct Plan {
@@ -62,17 +63,20 @@ struct Plan {
     int *src;       // [E] first row in the caller's order
     int *pos;       // [E + 1] first padded row
     int *tiles;     // [E + 1] 256-row tiles before the group
+    int *ready;     // [E] epilogue warps that are done with a unit of the group (zeroed)
+    int *next;      // the next unit to be claimed (zeroed)
 };
 
 struct GemmArgs {
-    // loads: token rows (boxes of 128 rows; of 64 x 64), weights (64 x 64)
-    CUtensorMap xa, da, ga, ua, xb, db, gb, ub, hb, w1, w3, w2;
-    // stores: dg, du, hw (64 columns x 32 rows), rows of dX (32 fp32 x 32), weight gradients
+    // loads: rows of X, dY, dg, du in boxes of 128 and of 32; the same and hw, and the weights,
+    // in boxes of 64 x 64
+    CUtensorMap x128, d128, g128, u128, x32, d32, g32, u32, xb, db, gb, ub, hb, w1, w3, w2;
+    // stores: dg, du, hw (32 columns x 32 rows), rows of dX (32 fp32 x 32), weight gradients
     CUtensorMap gs, us, hs, xs, s1, s3, s2;
     Plan plan;
     int E, H, I;
     const float *wrow;               // [padded rows] slot weights
-    float *dwp;                      // [2 ceil(I / 128)][padded rows] partial sums of <p, h>
+    float *dwp;                      // [I / 32][padded rows] partial sums of <p, h>
     long long ld_dwp;
     float *stash;                    // [CTAs][STASH]
     int *status;
@@ -115,6 +119,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t *__restrict__ 
         p.src[g] = lo;
         p.pos[g] = ip - np;
         p.tiles[g] = it - nt;
+        p.ready[g] = 0;
     }
     if (g == E - 1) {
         p.pos[E] = ip;
@@ -122,6 +127,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t *__restrict__ 
     }
     if (g == 0) {
         *p.ok = ok ? 1 : 0;
+        *p.next = 0;
         if (!ok) report(status, MOE_ERR_INVALID_ARG);
     }
 }
@@ -198,14 +204,14 @@ __global__ void __launch_bounds__(GT) gather_kernel(const void *__restrict__ x, 
 }
 
 // ------------------------------------------------------------------------- products
-enum { GU, PR, ROWS, DW1, DW3, DW2, END };     // g and u; p; rows of dX; weight gradients
+enum { P, U, G, ROWS, DW1, DW3, DW2 };     // p, u, g; rows of dX; weight gradients
 
 struct Tile {
     int kind, g;
-    int row0;       // first padded row of the tile (weight gradients: of the group)
-    int live;       // padded rows of the group from row0 on
-    int m0;         // weight gradients: first output row
-    int col0;       // first output column
+    int row0;       // P .. ROWS: first padded row of the tile's token rows (its columns); weight
+                    // gradients: first padded row of the group (the depth)
+    int m0;         // first row of the tile: of I (P, U, G), H (ROWS), the gradient's rows
+    int n0, n;      // weight gradients: first column; columns of the tile (a multiple of 64)
     int kb, chunk;  // stages, and stages of one sum in tensor memory
 };
 
@@ -221,17 +227,11 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, 
                  ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src)) : "memory");
 }
 
-// The warp's slab may be written again: the store before it has read it.
+// The warp's slab may be written again: the stores before it have read it.
 __device__ __forceinline__ void slab_free(int lane)
 {
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
-}
-
-// 16 bytes to chunk c (of 8) of the lane's row, in the 128-byte swizzle
-__device__ __forceinline__ void slab_put(unsigned char *slab, int lane, int c, uint4 v)
-{
-    *reinterpret_cast<uint4 *>(slab + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
 }
 
 // The slab is written: order it before the store that lane 0 issues next.
@@ -243,19 +243,28 @@ __device__ __forceinline__ void slab_ready()
 
 __device__ __forceinline__ void slab_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
-// 64 fp32 -> the lane's row of 64 bf16
-__device__ __forceinline__ void slab_bf16(unsigned char *slab, int lane, const float *v, int c0)
+// 32 fp32 -> 32 bf16 of the lane's row of 64, from chunk c0 (of 8), in the 128-byte swizzle
+__device__ __forceinline__ void slab_bf16(unsigned char *slab, int lane, const float (&v)[32], int c0)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        slab_put(slab, lane, c0 + i,
-                 make_uint4(f32x2_to_bf16x2(v[8 * i + 1], v[8 * i]), f32x2_to_bf16x2(v[8 * i + 3], v[8 * i + 2]),
-                            f32x2_to_bf16x2(v[8 * i + 5], v[8 * i + 4]), f32x2_to_bf16x2(v[8 * i + 7], v[8 * i + 6])));
+        *reinterpret_cast<uint4 *>(slab + lane * 128 + (((c0 + i) ^ (lane & 7)) << 4)) =
+            make_uint4(f32x2_to_bf16x2(v[8 * i + 1], v[8 * i]), f32x2_to_bf16x2(v[8 * i + 3], v[8 * i + 2]),
+                       f32x2_to_bf16x2(v[8 * i + 5], v[8 * i + 4]), f32x2_to_bf16x2(v[8 * i + 7], v[8 * i + 6]));
 }
 
-// GATES: units of (p of 256 columns; g and u of 128 of them, twice); else: tiles of dX's
-// rows, then of the weight gradients.
-template <bool GATES>
+__device__ __forceinline__ int ld_acquire(const int *p)
+{
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void fence_proxy_async_global()
+{
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__ GemmArgs p)
 {
     constexpr int TCOLS = 512;
@@ -263,7 +272,8 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
     unsigned char *ring = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *slabs = ring + STAGES * STAGE;
-    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
+    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], drain;
+    __shared__ int tq[TQ];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     volatile int *abort_flag = &abort_s;
@@ -280,6 +290,10 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 2 * N_EPI);
+        }
+        for (int q = 0; q < TQ; ++q) {
+            mbar_init(&tqf[q], 1);
+            mbar_init(&tqe[q], 2 * N_EPI + 2);   // both epilogues, the MMA issuer, the odd producer
         }
         mbar_init(&drain, 1);
         abort_s = 0;
@@ -299,119 +313,165 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
     const int E = p.E, H = p.H, I = p.I;
     const int ok = *p.plan.ok;
     const int row_tiles = ok ? p.plan.tiles[E] : 0;
-    const int nI = (I + TN - 1) / TN, nH = (H + TN - 1) / TN;
-    const int n_rows = row_tiles * (GATES ? nI : nH);
+    const int nI = (I + TM - 1) / TM, nH = (H + TM - 1) / TM;
     const int per_w = nH * nI;                       // tiles of one weight gradient
-    const int n_units = GATES ? n_rows : (ok ? n_rows + 3 * E * per_w : 0);
-    const int step = gridDim.x >> 1;
+    const int n_gates = row_tiles * nI;
+    const int n_units = ok ? n_gates + row_tiles * nH + 3 * E * per_w : 0;
 
-    // The tiles of this cluster, in order: `next` takes (unit, part of the unit) on.
-    struct Walk { int unit, part, g; };
-    auto start = [&]() -> Walk { return Walk{static_cast<int>(blockIdx.x >> 1), 0, 0}; };
-    auto tile_of = [&](Walk &w) -> Tile {
+    // Part `part` of a unit; *g: a group at or before the unit's (the search starts there).
+    auto decode = [&](int unit, int part, int &from) -> Tile {
         Tile T{};
-        T.kind = END;
-        bool last = true;                            // of its unit
-        if (w.unit >= n_units) return T;
-        if (w.unit < n_rows) {
-            // column by column, a group's row tiles innermost (they share the weights)
-            const int nc = GATES ? nI : nH;
-            // the group with tiles[g] * nc <= unit < tiles[g + 1] * nc: mostly the last tile's or
-            // one of the next
-            int lo = w.g, near = 0;
-            while (near < 8 && p.plan.tiles[lo + 1] * nc <= w.unit) { ++lo; ++near; }
-            if (near == 8) {
-                int hi = E - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (p.plan.tiles[mid] * nc <= w.unit) lo = mid; else hi = mid - 1;
-                }
+        const bool gates = unit < n_gates;
+        const int v = gates ? unit : unit - n_gates;
+        const int nr = gates ? nI : nH, nw = gates ? 0 : 3 * per_w;
+        auto first = [&](int g) -> int { return p.plan.tiles[g] * nr + g * nw; };   // units before group g
+        int lo = from;
+        if (first(lo) > v) lo = 0;
+        int near = 0;
+        while (near < 8 && first(lo + 1) <= v) { ++lo; ++near; }
+        if (near == 8) {
+            int hi = E - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (first(mid) <= v) lo = mid; else hi = mid - 1;
             }
-            w.g = lo;
-            const int mt = p.plan.tiles[lo + 1] - p.plan.tiles[lo];
-            const int l = w.unit - p.plan.tiles[lo] * nc;
-            const int c = l / mt, m = l - c * mt;
-            T.g = lo;
-            T.row0 = p.plan.pos[lo] + m * TM;
-            T.live = pad_rows(p.plan.cnt[lo]) - m * TM;
-            T.col0 = c * TN;
-            if (GATES) {
-                // p of 256 columns, then g and u of the first 128 and (where there are any) of
-                // the other 128
-                T.kind = w.part == 0 ? PR : GU;
-                if (w.part == 2) T.col0 += 128;
-                last = w.part == 2 || (w.part == 1 && T.col0 + 128 >= I);
-                T.kb = H / BK;
-                T.chunk = CHUNK;
-            } else {
-                T.kind = ROWS;
-                T.kb = T.chunk = 2 * (I / BK);
-            }
-        } else {
-            int v = w.unit - n_rows;
-            T.g = v / (3 * per_w);
-            v -= T.g * 3 * per_w;
-            const int m = v / per_w;
-            v -= m * per_w;
-            const int nc = m < 2 ? nI : nH;
-            T.kind = DW1 + m;
-            T.m0 = v / nc * TM;
-            T.col0 = (v - v / nc * nc) * TN;
-            T.row0 = p.plan.pos[T.g];
-            T.kb = T.chunk = pad_rows(p.plan.cnt[T.g]) / BK;
         }
-        if (!last) ++w.part;
-        else { w.unit += step; w.part = 0; }
+        from = lo;
+        T.g = lo;
+        T.row0 = p.plan.pos[lo];
+        const int rows = pad_rows(p.plan.cnt[lo]);
+        int l = v - first(lo);
+        const int mt = (rows + TN - 1) / TN;         // tiles of token rows, innermost: they share the weights
+        if (gates || l < mt * nH) {
+            const int c = l / mt, m = l - c * mt;
+            T.kind = gates ? part : ROWS;
+            T.m0 = c * TM;
+            T.row0 += m * TN;
+            T.n = min(TN, rows - m * TN);
+            T.kb = gates ? H / BK : 2 * (I / BK);
+            T.chunk = gates ? CHUNK : T.kb;
+        } else {
+            l -= mt * nH;
+            const int w = l / per_w;
+            l -= w * per_w;
+            const int nc = w < 2 ? nI : nH, cols = w < 2 ? I : H;
+            T.kind = DW1 + w;
+            T.m0 = l / nc * TM;
+            T.n0 = (l - l / nc * nc) * TN;
+            T.n = min(TN, cols - T.n0);
+            T.kb = T.chunk = rows / BK;
+        }
         return T;
+    };
+    // Units are claimed from a counter by the even CTA's producer, in order, and handed to
+    // every role of both CTAs through TQ slots (unit -1 ends).  All of a group's gates come
+    // before the tiles that need them, so a cluster that waits holds nothing they need.
+    auto slot_done = [&](int q) {
+        if (leader) mbar_arrive(&tqe[q]);
+        else mbar_arrive_cluster(mapa_shared(smem_u32(&tqe[q]), 0));
     };
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0 && !p.inject) {
-            uint32_t s = 0, ph = 0, it = 0;
+            uint32_t s = 0, ph = 0, it = 0, qs = 0, qph = 0;
             const uint32_t full0 = mapa_shared(smem_u32(full), 0);
             const int r = static_cast<int>(rank);
             bool good = true;
-            Walk w = start();
+            int from = 0;
+            auto claim = [&](int &unit) -> bool {
+                if (!mbar_wait_cluster(&tqe[qs], qph ^ 1u, abort_flag, p.status, tmo)) return false;
+                const int t = atomicAdd(p.plan.next, 1);
+                unit = t < n_units ? t : -1;
+                tq[qs] = unit;
+                mbar_arrive(&tqf[qs]);
+                st_shared_cluster(mapa_shared(smem_u32(&tq[qs]), 1), unit);
+                mbar_arrive_cluster(mapa_shared(smem_u32(&tqf[qs]), 1));
+                if (++qs == TQ) { qs = 0; qph ^= 1u; }
+                return true;
+            };
+            int unit = -1, after = -1;
+            if (leader) good = claim(after);
             while (good) {
-                const Tile T = tile_of(w);
-                if (T.kind == END) break;
-                for (int kb = 0; kb < T.kb; ++kb, ++it) {
-                    if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
-                    unsigned char *a = ring + s * STAGE, *b = a + 2 * HALF;
-                    const uint32_t fb = full0 + 8u * s;
-                    if (leader) mbar_arrive_expect_tx(&full[s], 2u * STAGE);
-                    const int k = kb * BK;
-                    if (GATES) {
-                        const int row = T.row0 + 128 * r, col = T.col0 + 64 * r;
-                        if (T.kind == GU) {
-                            // this CTA's 128 of the tile's columns: 64 of W1, the same 64 of W3
-                            tma_load_2d_pair(a, &p.xa, fb, k, row);
-                            tma_load_3d_pair(b, &p.w1, fb, col, k, T.g);
-                            tma_load_3d_pair(b + HALF, &p.w3, fb, col, k, T.g);
-                        } else {
-                            // ... the columns whose g and u this CTA's half came from
-                            tma_load_2d_pair(a, &p.da, fb, k, row);
-                            tma_load_3d_pair(b, &p.w2, fb, k, col, T.g);
-                            tma_load_3d_pair(b + HALF, &p.w2, fb, k, col + 128, T.g);
+                if (leader) {
+                    unit = after;
+                    if (unit < 0) break;
+                    if (!claim(after)) break;        // one ahead: the hand-over overlaps the loads
+                } else {
+                    if (!mbar_wait_cluster(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
+                    unit = tq[qs];
+                    slot_done(qs);
+                    if (++qs == TQ) { qs = 0; qph ^= 1u; }
+                    if (unit < 0) break;
+                }
+                const int parts = unit < n_gates ? 3 : 1;
+                for (int part = 0; part < parts && good; ++part) {
+                    const Tile T = decode(unit, part, from);
+                    if (T.kind >= ROWS && T.kb > 0) {
+                        // dg, du and hw of the group: every epilogue warp of its units is done
+                        const int need = (p.plan.tiles[T.g + 1] - p.plan.tiles[T.g]) * nI * 2 * N_EPI;
+                        const int *flag = p.plan.ready + T.g;
+                        if (ld_acquire(flag) < need) {
+                            const uint64_t t0 = globaltimer_ns();
+                            while (ld_acquire(flag) < need) {
+                                if (*abort_flag) { good = false; break; }
+                                if (globaltimer_ns() - t0 > tmo) {
+                                    *abort_flag = 1;
+                                    report(p.status, MOE_ERR_DEVICE_TIMEOUT);
+                                    good = false;
+                                    break;
+                                }
+                                __nanosleep(64);
+                            }
+                            if (!good) break;
                         }
-                    } else if (T.kind == ROWS) {
-                        const bool second = kb >= I / BK;
-                        const int c = second ? k - I : k, col = T.col0 + 128 * r;
-                        const CUtensorMap *wm = second ? &p.w3 : &p.w1;
-                        tma_load_2d_pair(a, second ? &p.ua : &p.ga, fb, c, T.row0 + 128 * r);
-                        tma_load_3d_pair(b, wm, fb, c, col, T.g);
-                        tma_load_3d_pair(b + HALF, wm, fb, c, col + 64, T.g);
-                    } else {
-                        const CUtensorMap *ma = T.kind == DW2 ? &p.hb : &p.xb;
-                        const CUtensorMap *mb = T.kind == DW2 ? &p.db : (T.kind == DW3 ? &p.ub : &p.gb);
-                        const int row = T.row0 + k, m = T.m0 + 128 * r, n = T.col0 + 128 * r;
-                        tma_load_2d_pair(a, ma, fb, m, row);
-                        tma_load_2d_pair(a + HALF, ma, fb, m + 64, row);
-                        tma_load_2d_pair(b, mb, fb, n, row);
-                        tma_load_2d_pair(b + HALF, mb, fb, n + 64, row);
+                        fence_proxy_async_global();
                     }
-                    if (++s == STAGES) { s = 0; ph ^= 1u; }
+                    const bool dw = T.kind >= DW1;
+                    const int nb = T.n / 2;          // this CTA's columns
+                    const uint32_t bytes = 2 * HALF + (dw ? (nb > 64 ? 2 : 1) * HALF : nb * 128);
+                    const int m = T.m0 + 128 * r;
+                    const int brow = T.row0 + nb * r;
+                    const CUtensorMap *b128 = T.kind == P ? &p.d128 : &p.x128, *b32 = T.kind == P ? &p.d32 : &p.x32;
+                    const CUtensorMap *wm = T.kind == U ? &p.w3 : &p.w1;
+                    for (int kb = 0; kb < T.kb; ++kb, ++it) {
+                        if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
+                        unsigned char *a = ring + s * STAGE, *b = a + 2 * HALF;
+                        const uint32_t fb = full0 + 8u * s;
+                        if (leader) mbar_arrive_expect_tx(&full[s], 2u * bytes);
+                        int k = kb * BK;
+                        if (dw) {
+                            const CUtensorMap *ma = T.kind == DW2 ? &p.hb : &p.xb;
+                            const CUtensorMap *mb = T.kind == DW2 ? &p.db : (T.kind == DW3 ? &p.ub : &p.gb);
+                            const int n = T.n0 + nb * r;
+                            k += T.row0;
+                            tma_load_2d_pair(a, ma, fb, m, k);
+                            tma_load_2d_pair(a + HALF, ma, fb, m + 64, k);
+                            tma_load_2d_pair(b, mb, fb, n, k);
+                            if (nb > 64) tma_load_2d_pair(b + HALF, mb, fb, n + 64, k);
+                        } else {
+                            if (T.kind == P) {           // rows of W2: depth along H
+                                tma_load_3d_pair(a, &p.w2, fb, k, m, T.g);
+                                tma_load_3d_pair(a + HALF, &p.w2, fb, k, m + 64, T.g);
+                            } else if (T.kind != ROWS) { // columns of W1, W3: depth along H
+                                tma_load_3d_pair(a, wm, fb, m, k, T.g);
+                                tma_load_3d_pair(a + HALF, wm, fb, m + 64, k, T.g);
+                            } else {                     // rows of W1, then of W3: depth along I
+                                const bool second = k >= I;
+                                if (second) k -= I;
+                                wm = second ? &p.w3 : &p.w1;
+                                b128 = second ? &p.u128 : &p.g128;
+                                b32 = second ? &p.u32 : &p.g32;
+                                tma_load_3d_pair(a, wm, fb, k, m, T.g);
+                                tma_load_3d_pair(a + HALF, wm, fb, k, m + 64, T.g);
+                            }
+                            if (nb == 128)
+                                tma_load_2d_pair(b, b128, fb, k, brow);
+                            else
+                                for (int j = 0; j < nb; j += 32) tma_load_2d_pair(b + j * 128, b32, fb, k, brow + j);
+                        }
+                        if (++s == STAGES) { s = 0; ph ^= 1u; }
+                    }
                 }
             }
             // every copy issued lands before the CTAs can exit (the even CTA's barriers
@@ -428,42 +488,49 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         // -------------------------------------------------------------- MMA issuer
         if (lane == 0 && leader) {
             const uint32_t ring0 = smem_u32(ring);
-            uint32_t s = 0, ph = 0, b = 0, tph = 0;
+            uint32_t s = 0, ph = 0, b = 0, tph = 0, qs = 0, qph = 0;
             bool good = true;
-            Walk w = start();
+            int from = 0;
             while (good) {
-                const Tile T = tile_of(w);
-                if (T.kind == END) break;
-                // A: rows K-major, or (weight gradients) rows as the depth, MN-major; B: columns
-                // of W1 and W3 as they lie (g, u) and rows as the depth are MN-major
-                const bool amn = T.kind >= DW1, bmn = T.kind >= DW1 || T.kind == GU;
-                const uint64_t ad0 = smem_desc_sw128(ring0, amn ? HALF : 16, 1024);
-                const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, bmn ? HALF : 16, 1024);
-                const uint32_t as = amn ? 128u : 2u, bs = bmn ? 128u : 2u;
-                const uint32_t id = idesc_bf16_f32(TM, TN, amn, bmn);
-                int kb = 0;
-                do {
-                    if (!mbar_wait_cluster(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
-                    tc_fence_after();
-                    const uint32_t d = tmem + b * TN;
-                    const int end = min(kb + T.chunk, T.kb);
-                    for (int k0 = kb; kb < end; ++kb) {
-                        if (!mbar_wait(&full[s], ph, abort_flag, p.status, tmo)) { good = false; break; }
+                if (!mbar_wait(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
+                const int unit = tq[qs];
+                slot_done(qs);
+                if (++qs == TQ) { qs = 0; qph ^= 1u; }
+                if (unit < 0) break;
+                const int parts = unit < n_gates ? 3 : 1;
+                for (int part = 0; part < parts && good; ++part) {
+                    const Tile T = decode(unit, part, from);
+                    // rows K-major; columns of W1, W3 as the tile's rows, and (weight gradients)
+                    // rows as the depth, MN-major
+                    const bool bmn = T.kind >= DW1, amn = bmn || T.kind == U || T.kind == G;
+                    const uint64_t ad0 = smem_desc_sw128(ring0, amn ? HALF : 16, 1024);
+                    const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, bmn ? HALF : 16, 1024);
+                    const uint32_t as = amn ? 128u : 2u, bs = bmn ? 128u : 2u;
+                    const uint32_t id = idesc_bf16_f32(TM, static_cast<uint32_t>(T.n), amn, bmn);
+                    int kb = 0;
+                    do {
+                        if (!mbar_wait_cluster(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
                         tc_fence_after();
-                        const uint64_t o = static_cast<uint64_t>(s * (STAGE >> 4));
-                        const uint64_t ad = ad0 + o, bd = bd0 + o;
-                        tc_mma_bf16_pair(d, ad, bd, id, kb > k0 ? 1u : 0u);
-                        tc_mma_bf16_pair(d, ad + as, bd + bs, id, 1u);
-                        tc_mma_bf16_pair(d, ad + 2 * as, bd + 2 * bs, id, 1u);
-                        tc_mma_bf16_pair(d, ad + 3 * as, bd + 3 * bs, id, 1u);
-                        tc_commit_pair_mc(&empty[s], 3);
-                        if (++s == STAGES) { s = 0; ph ^= 1u; }
-                    }
-                    if (!good) break;
-                    tc_commit_pair_mc(&tfull[b], 3);
-                    b ^= 1u;
-                    if (b == 0) tph ^= 1u;
-                } while (kb < T.kb);
+                        const uint32_t d = tmem + b * TN;
+                        const int end = min(kb + T.chunk, T.kb);
+                        for (int k0 = kb; kb < end; ++kb) {
+                            if (!mbar_wait(&full[s], ph, abort_flag, p.status, tmo)) { good = false; break; }
+                            tc_fence_after();
+                            const uint64_t o = static_cast<uint64_t>(s * (STAGE >> 4));
+                            const uint64_t ad = ad0 + o, bd = bd0 + o;
+                            tc_mma_bf16_pair(d, ad, bd, id, kb > k0 ? 1u : 0u);
+                            tc_mma_bf16_pair(d, ad + as, bd + bs, id, 1u);
+                            tc_mma_bf16_pair(d, ad + 2 * as, bd + 2 * bs, id, 1u);
+                            tc_mma_bf16_pair(d, ad + 3 * as, bd + 3 * bs, id, 1u);
+                            tc_commit_pair_mc(&empty[s], 3);
+                            if (++s == STAGES) { s = 0; ph ^= 1u; }
+                        }
+                        if (!good) break;
+                        tc_commit_pair_mc(&tfull[b], 3);
+                        b ^= 1u;
+                        if (b == 0) tph ^= 1u;
+                    } while (kb < T.kb);
+                }
             }
             tc_commit_pair_mc(&drain, 1);
             int dummy = 0;
@@ -471,20 +538,23 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         }
     } else {
         // ---------------------------------------------------------------- epilogue
-        const int q = warp & 3, half = (warp - 2) >> 2;   // lane quarter, column half
-        const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128u * half;
+        const int q = warp & 3, half = (warp - 2) >> 2;   // lane quarter, half of the columns
+        const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+        const int r0 = 128 * static_cast<int>(rank) + 32 * q;   // the warp's first row of a tile
         unsigned char *slab = slabs + (warp - 2) * SLAB;
-        uint32_t b = 0, tph = 0;
-        // the sums of buffer b are complete (every lane observes the phase itself)
-        auto sums_ready = [&]() -> bool {
+        uint32_t b = 0, tph = 0, qs = 0, qph = 0;
+        // a wait by one lane (every lane then observes the phase itself)
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
             bool good = true;
-            if (lane == 0) good = mbar_wait(&tfull[b], tph, abort_flag, p.status, tmo);
+            if (lane == 0) good = mbar_wait_cluster(bar, parity, abort_flag, p.status, tmo);
             good = __shfl_sync(kFullMask, good, 0);
-            if (good) {
-                mbar_try_wait(&tfull[b], tph);
-                tc_fence_after();
-            }
+            if (good) mbar_try_wait_cluster(bar, parity);
+            return good;
+        };
+        auto sums_ready = [&]() -> bool {
+            const bool good = wait_all(&tfull[b], tph);
+            tc_fence_after();
             return good;
         };
         auto sums_read = [&]() {
@@ -494,136 +564,168 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
             b ^= 1u;
             if (b == 0) tph ^= 1u;
         };
-        // float4 i of this thread's stash (256 threads side by side)
+        // this thread's stash: p, then u, of its row, float4 i at i * SROW (256 threads side by side)
         float4 *stash = reinterpret_cast<float4 *>(p.stash + static_cast<size_t>(blockIdx.x) * STASH) + (tid - 64);
         constexpr int SROW = 32 * N_EPI;
-        int part = 0;                                // of the unit: its tiles of g and u so far
-        float dw = 0.f;
-        Walk w = start();
+        int from = 0;
         bool good = true;
         while (good) {
-            const Tile T = tile_of(w);
-            if (T.kind == END) break;
-            const int r0 = 128 * static_cast<int>(rank) + 32 * q;   // the warp's first row of the tile
-            if (GATES) {
-                const bool rows = r0 < T.live;
-                const size_t row = static_cast<size_t>(T.row0 + r0 + lane);
-                // sums over the chunks, in registers
-                float acc[128];
-#pragma unroll
-                for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+            if (!wait_all(&tqf[qs], qph)) break;
+            const int unit = tq[qs];
+            __syncwarp();
+            if (lane == 0) slot_done(qs);
+            if (++qs == TQ) { qs = 0; qph ^= 1u; }
+            if (unit < 0) break;
+            if (unit < n_gates) {
+                Tile T{};
+                int nc = 0;                          // 32-column pieces of this warp's half
+                float acc[128];                      // row i of the tile, its half of the token rows
 #pragma unroll 1
-                for (int kb = 0; kb < T.kb; kb += CHUNK) {
-                    if (!sums_ready()) { good = false; break; }
+                for (int part = P; part <= G && good; ++part) {
+                    T = decode(unit, part, from);
+                    nc = T.n / 64;
+                    const uint32_t at = tm0 + static_cast<uint32_t>(half * (T.n / 2));
+                    // sums over the chunks, in registers
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        float v[16];
-                        __syncwarp();
-                        tmem_ld16(tm0 + b * TN + 16 * c, v);
+                    for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+#pragma unroll 1
+                    for (int kb = 0; kb < T.kb; kb += CHUNK) {
+                        if (!sums_ready()) { good = false; break; }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[16 * c + i] += v[i];
+                        for (int c = 0; c < 8; ++c) {
+                            if (c >= 2 * nc) continue;
+                            float v[16];
+                            __syncwarp();
+                            tmem_ld16(at + b * TN + 16 * c, v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) acc[16 * c + i] += v[i];
+                        }
+                        sums_read();
                     }
-                    sums_read();
+                    if (good && part != G) {
+                        float4 *st = stash + part * 32 * SROW;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < 8 * nc) st[i * SROW] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                    }
                 }
                 if (!good) break;
-                if (T.kind == PR) {
-                    // kept for the unit's next tiles: acc[0..63] are columns of the first 128,
-                    // acc[64..127] of the second
+                // g in acc; p and u in the stash.  32 token rows at a time: dg, du, hw and the
+                // terms of <p, h>
+                const int col = T.m0 + r0;           // the warp's columns of I
+                const int tok = T.row0 + half * (T.n / 2);
+                float *dwp = p.dwp + static_cast<size_t>((T.m0 + r0) / 32) * p.ld_dwp + tok + lane;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        stash[i * SROW] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-                    part = 0;
-                    dw = 0.f;
-                } else {
-                    // g of 64 columns in acc[0..63], u of the same in acc[64..127], p in the stash.
-                    // In their place: dg and du (bf16 pair), hw.
-                    const float wr = rows ? p.wrow[row] : 0.f;
-                    const float4 *st = stash + part * 16 * SROW;
-                    const int col = T.col0 + 64 * half;
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= nc) continue;
+                    const float4 *wv = reinterpret_cast<const float4 *>(p.wrow + tok + 32 * c);
+                    uint16_t *sl = reinterpret_cast<uint16_t *>(slab);
+                    uint32_t hw[16];
+                    slab_free(lane);
 #pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const float4 p4 = st[i / 4 * SROW];
-                        const float pp[4] = {p4.x, p4.y, p4.z, p4.w};
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 p4 = stash[(8 * c + i / 4) * SROW], u4 = stash[(32 + 8 * c + i / 4) * SROW], w4 = wv[i / 4];
+                        const float pp[4] = {p4.x, p4.y, p4.z, p4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
+                        const float ww[4] = {w4.x, w4.y, w4.z, w4.w};
+                        float hv[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float g = acc[i + k], u = acc[64 + i + k];
-                            const float s = fast_sigmoid(g), gs = g * s, h = gs * u, pw = pp[k] * wr;
-                            dw = fmaf(pp[k], h, dw);
-                            acc[i + k] = __uint_as_float(f32x2_to_bf16x2(pw * gs, pw * u * s * fmaf(g, 1.f - s, 1.f)));
-                            acc[64 + i + k] = wr * h;
+                            const float g = acc[32 * c + i + k], u = uu[k];
+                            const float s = fast_sigmoid(g), gs = g * s, h = gs * u, pw = pp[k] * ww[k];
+                            const uint32_t o = f32x2_to_bf16x2(pw * gs, pw * u * s * fmaf(g, 1.f - s, 1.f));
+                            sl[(i + k) * 32 + lane] = static_cast<uint16_t>(o);
+                            sl[1024 + (i + k) * 32 + lane] = static_cast<uint16_t>(o >> 16);
+                            hv[k] = ww[k] * h;
+                            acc[32 * c + i + k] = pp[k] * h;
                         }
+                        hw[i / 2] = f32x2_to_bf16x2(hv[1], hv[0]);
+                        hw[i / 2 + 1] = f32x2_to_bf16x2(hv[3], hv[2]);
                     }
-#pragma unroll
-                    for (int x = 0; x < 3; ++x) {    // dg, du, hw
-                        slab_free(lane);
-#pragma unroll
-                        for (int i = 0; i < 64; i += 8) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                o[k] = x < 2 ? __byte_perm(__float_as_uint(acc[i + 2 * k]), __float_as_uint(acc[i + 2 * k + 1]),
-                                                           x == 0 ? 0x5410 : 0x7632)
-                                             : f32x2_to_bf16x2(acc[64 + i + 2 * k + 1], acc[64 + i + 2 * k]);
-                            slab_put(slab, lane, i / 8, make_uint4(o[0], o[1], o[2], o[3]));
-                        }
-                        slab_ready();
-                        if (lane == 0 && rows && col < I) {
-                            tma_store_2d(x == 0 ? &p.gs : (x == 1 ? &p.us : &p.hs), slab, col, T.row0 + r0);
-                            slab_commit();
-                        }
+                    slab_ready();
+                    if (lane == 0 && col < I) {
+                        tma_store_2d(&p.gs, slab, col, tok + 32 * c);
+                        tma_store_2d(&p.us, slab + 2048, col, tok + 32 * c);
+                        slab_commit();
                     }
-                    // (each of the unit's tiles leaves its own partial sum)
-                    if (rows) p.dwp[static_cast<size_t>(2 * (T.col0 / 128) + half) * p.ld_dwp + row] = dw;
-                    dw = 0.f;
-                    ++part;
+                    // sum over the warp's 32 columns: lane j ends up with token row j
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                        for (int k = 0; k < o; ++k) {
+                            const bool up = lane & o;
+                            const float send = up ? acc[32 * c + k] : acc[32 * c + k + o];
+                            const float keep = up ? acc[32 * c + k + o] : acc[32 * c + k];
+                            acc[32 * c + k] = keep + __shfl_xor_sync(kFullMask, send, o);
+                        }
+                    if (col < I) dwp[32 * c] = acc[32 * c];
+                    slab_free(lane);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        sl[2 * i * 32 + lane] = static_cast<uint16_t>(hw[i]);
+                        sl[(2 * i + 1) * 32 + lane] = static_cast<uint16_t>(hw[i] >> 16);
+                    }
+                    slab_ready();
+                    if (lane == 0 && col < I) {
+                        tma_store_2d(&p.hs, slab, col, tok + 32 * c);
+                        slab_commit();
+                    }
+                }
+                // the unit's dg, du and hw are in global memory: tell the group
+                if (lane == 0) {
+                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                    fence_proxy_async_global();
+                    __threadfence();
+                    atomicAdd(p.plan.ready + T.g, 1);
+                }
+                __syncwarp();
+                continue;
+            }
+            const Tile T = decode(unit, 0, from);
+            if (!sums_ready()) break;
+            if (T.kind == ROWS) {
+                const int col = T.m0 + r0, tok = T.row0 + half * (T.n / 2);
+                const uint32_t at = tm0 + b * TN + static_cast<uint32_t>(half * (T.n / 2));
+                float *sl = reinterpret_cast<float *>(slab);
+#pragma unroll 1
+                for (int c = 0; c < T.n / 64; ++c) {
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld32(at + 32 * c, v);
+                    slab_free(lane);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sl[i * 32 + lane] = v[i];
+                    slab_ready();
+                    if (lane == 0 && col < H) {
+                        tma_store_2d(&p.xs, slab, col, tok + 32 * c);
+                        slab_commit();
+                    }
                 }
             } else {
-                if (!sums_ready()) { good = false; break; }
-                const uint32_t at = tm0 + b * TN;
-                if (T.kind == ROWS) {
+                const int M = T.kind == DW2 ? I : H;
+                const CUtensorMap *sm = T.kind == DW1 ? &p.s1 : (T.kind == DW3 ? &p.s3 : &p.s2);
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        const int col = T.col0 + 128 * half + 32 * c;
-                        float v[32];
-                        __syncwarp();
-                        tmem_ld32(at + 32 * c, v);
-                        slab_free(lane);
+                for (int c = 0; c < 2; ++c) {
+                    const int lc = 128 * half + 64 * c;
+                    if (lc >= T.n) break;
+                    float v[32], u[32];
+                    __syncwarp();
+                    tmem_ld32(tm0 + b * TN + lc, v);
+                    tmem_ld32(tm0 + b * TN + lc + 32, u);
+                    if (T.kb == 0) {             // an expert without rows
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            slab_put(slab, lane, i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                                               __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
-                        slab_ready();
-                        if (lane == 0 && r0 < T.live && col < H) {
-                            tma_store_2d(&p.xs, slab, col, T.row0 + r0);
-                            slab_commit();
-                        }
+                        for (int i = 0; i < 32; ++i) v[i] = u[i] = 0.f;
                     }
-                } else {
-                    const int M = T.kind == DW2 ? I : H, N = T.kind == DW2 ? H : I;
-                    const CUtensorMap *sm = T.kind == DW1 ? &p.s1 : (T.kind == DW3 ? &p.s3 : &p.s2);
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        const int col = T.col0 + 128 * half + 64 * c;
-                        float v[32], u[32];
-                        __syncwarp();
-                        tmem_ld32(at + 64 * c, v);
-                        tmem_ld32(at + 64 * c + 32, u);
-                        if (T.kb == 0) {             // an expert without rows
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = u[i] = 0.f;
-                        }
-                        slab_free(lane);
-                        slab_bf16(slab, lane, v, 0);
-                        slab_bf16(slab, lane, u, 4);
-                        slab_ready();
-                        if (lane == 0 && T.m0 + r0 < M && col < N) {
-                            tma_store_3d(sm, slab, col, T.m0 + r0, T.g);
-                            slab_commit();
-                        }
+                    slab_free(lane);
+                    slab_bf16(slab, lane, v, 0);
+                    slab_bf16(slab, lane, u, 4);
+                    slab_ready();
+                    if (lane == 0 && T.m0 + r0 < M) {
+                        tma_store_3d(sm, slab, T.n0 + lc, T.m0 + r0, T.g);
+                        slab_commit();
                     }
                 }
-                sums_read();
             }
+            sums_read();
         }
         // the last stores have left shared memory and reached global memory
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -701,10 +803,11 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// [groups][rows][cols] (groups == 0: [rows][cols]) of bf16, or fp32, in boxes of 128 bytes x
-// box_rows rows in the 128-byte swizzle.
+// [groups][rows][cols] (groups == 0: [rows][cols]) of bf16, or fp32, in boxes of box_cols columns
+// x box_rows rows: 128 bytes wide in the 128-byte swizzle (an operand, or a slab written so),
+// or 32 columns as they stand.
 bool encode(CUtensorMap *m, const void *base, int groups, long long rows, int cols, int box_rows,
-            bool fp32 = false)
+            int box_cols = 64, bool fp32 = false)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
@@ -712,18 +815,18 @@ bool encode(CUtensorMap *m, const void *base, int groups, long long rows, int co
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(groups)};
     const cuuint64_t strides[2] = {cols * es, cols * es * static_cast<cuuint64_t>(rows)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups ? 3 : 2,
               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t al256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 int gemm_ctas() { return num_sms() / 2 * 2; }
-int dw_parts(int I) { return 2 * ((I + 127) / 128); }    // partial sums of <p, h>
+int dw_parts(int I) { return I / 32; }    // partial sums of <p, h>
 
 struct Layout {
     long long rows;        // padded rows at most
@@ -738,7 +841,7 @@ Layout layout(int T, int H, int E, int K, int I)
     const size_t R = static_cast<size_t>(L.rows);
     size_t o = 0;
     auto take = [&](size_t b) { const size_t at = o; o += al256(b); return at; };
-    L.plan = take((4 * (MAXG + 1) + 1) * sizeof(int));
+    L.plan = take((5 * (MAXG + 1) + 2) * sizeof(int));
     L.wrow = take(R * 4);
     L.prow = take(static_cast<size_t>(TK) * 4);
     L.X = take(R * H * 2);
@@ -766,7 +869,7 @@ cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned
     const Layout L = layout(T, H, E, K, I);
     unsigned char *w = static_cast<unsigned char *>(scratch);
     int *pl = reinterpret_cast<int *>(w + L.plan);
-    Plan plan{pl, pl + 1, pl + 1 + MAXG, pl + 1 + 2 * MAXG, pl + 2 + 3 * MAXG};
+    Plan plan{pl, pl + 2, pl + 2 + MAXG, pl + 2 + 2 * MAXG, pl + 3 + 3 * MAXG, pl + 4 + 4 * MAXG, pl + 1};
     uint16_t *X = reinterpret_cast<uint16_t *>(w + L.X), *D = reinterpret_cast<uint16_t *>(w + L.D);
     float *wrow = reinterpret_cast<float *>(w + L.wrow), *dwp = reinterpret_cast<float *>(w + L.dwp);
     float *dxp = reinterpret_cast<float *>(w + L.dxp);
@@ -775,14 +878,16 @@ cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned
     void *dg = w + L.dg, *du = w + L.du, *hw = w + L.hw;
     GemmArgs a;
     memset(&a, 0, sizeof a);
-    if (!encode(&a.xa, X, 0, L.rows, H, 128) || !encode(&a.da, D, 0, L.rows, H, 128) ||
-        !encode(&a.ga, dg, 0, L.rows, I, 128) || !encode(&a.ua, du, 0, L.rows, I, 128) ||
+    if (!encode(&a.x128, X, 0, L.rows, H, 128) || !encode(&a.d128, D, 0, L.rows, H, 128) ||
+        !encode(&a.g128, dg, 0, L.rows, I, 128) || !encode(&a.u128, du, 0, L.rows, I, 128) ||
+        !encode(&a.x32, X, 0, L.rows, H, 32) || !encode(&a.d32, D, 0, L.rows, H, 32) ||
+        !encode(&a.g32, dg, 0, L.rows, I, 32) || !encode(&a.u32, du, 0, L.rows, I, 32) ||
         !encode(&a.xb, X, 0, L.rows, H, 64) || !encode(&a.db, D, 0, L.rows, H, 64) ||
         !encode(&a.gb, dg, 0, L.rows, I, 64) || !encode(&a.ub, du, 0, L.rows, I, 64) ||
         !encode(&a.hb, hw, 0, L.rows, I, 64) || !encode(&a.w1, f.W1, E, H, I, 64) ||
         !encode(&a.w3, f.W3, E, H, I, 64) || !encode(&a.w2, f.W2, E, I, H, 64) ||
-        !encode(&a.gs, dg, 0, L.rows, I, 32) || !encode(&a.us, du, 0, L.rows, I, 32) ||
-        !encode(&a.hs, hw, 0, L.rows, I, 32) || !encode(&a.xs, dxp, 0, L.rows, H, 32, true) ||
+        !encode(&a.gs, dg, 0, L.rows, I, 32, 32) || !encode(&a.us, du, 0, L.rows, I, 32, 32) ||
+        !encode(&a.hs, hw, 0, L.rows, I, 32, 32) || !encode(&a.xs, dxp, 0, L.rows, H, 32, 32, true) ||
         !encode(&a.s1, f.dW1, E, H, I, 32) || !encode(&a.s3, f.dW3, E, H, I, 32) ||
         !encode(&a.s2, f.dW2, E, I, H, 32))
         return cudaErrorInvalidValue;
@@ -804,10 +909,8 @@ cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned
     if (e != cudaSuccess) return e;
     const unsigned ctas = gemm_ctas();
     const size_t smem = 1024 + STAGES * STAGE + N_EPI * SLAB;
-    if ((e = ensure_smem(reinterpret_cast<const void *>(bwd_gemm_kernel<true>), smem)) != cudaSuccess) return e;
-    if ((e = ensure_smem(reinterpret_cast<const void *>(bwd_gemm_kernel<false>), smem)) != cudaSuccess) return e;
-    if ((e = launch_pdl(bwd_gemm_kernel<true>, dim3(ctas), dim3(NT), smem, s, 2, a)) != cudaSuccess) return e;
-    if ((e = launch_pdl(bwd_gemm_kernel<false>, dim3(ctas), dim3(NT), smem, s, 2, a)) != cudaSuccess) return e;
+    if ((e = ensure_smem(reinterpret_cast<const void *>(bwd_gemm_kernel), smem)) != cudaSuccess) return e;
+    if ((e = launch_pdl(bwd_gemm_kernel, dim3(ctas), dim3(NT), smem, s, 2, a)) != cudaSuccess) return e;
     return launch_pdl(finish_kernel, dim3(T, parts), dim3(GT), 0, s, 1, static_cast<const float *>(dxp),
                       static_cast<const int *>(prow), static_cast<const float *>(dwp), L.rows, dw_parts(I),
                       static_cast<const int *>(plan.ok), H, K, static_cast<uint16_t *>(f.dX), f.d_topk_w);
