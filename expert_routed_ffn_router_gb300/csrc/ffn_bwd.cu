@@ -68,10 +68,10 @@ struct Plan {
 };
 
 struct GemmArgs {
-    // loads: rows of X, dY, dg, du in boxes of 128 and of 32; the same and hw, and the weights,
-    // in boxes of 64 x 64
-    CUtensorMap x128, d128, g128, u128, x32, d32, g32, u32, xb, db, gb, ub, hb, w1, w3, w2;
-    // stores: dg, du, hw (32 columns x 32 rows), rows of dX (32 fp32 x 32), weight gradients
+    // loads: rows of X and dY in boxes of 128 and of 32; those, dg, du, hw (transposed) and the
+    // weights in boxes of 64 x 64
+    CUtensorMap x128, d128, x32, d32, xb, db, gb, ub, hb, w1, w3, w2;
+    // stores: dg, du, hw (32 token rows x 32 of I), rows of dX (32 fp32 x 32), weight gradients
     CUtensorMap gs, us, hs, xs, s1, s3, s2;
     Plan plan;
     int E, H, I;
@@ -206,14 +206,20 @@ __global__ void __launch_bounds__(GT) gather_kernel(const void *__restrict__ x, 
 // ------------------------------------------------------------------------- products
 enum { P, U, G, ROWS, DW1, DW3, DW2 };     // p, u, g; rows of dX; weight gradients
 
-struct Tile {
+// What a cluster claims at a time: a tile's three products (P, U, G), or a run of tiles of one
+// kind side by side (ROWS along H, weight gradients along their columns).
+struct Unit {
     int kind, g;
-    int row0;       // P .. ROWS: first padded row of the tile's token rows (its columns); weight
+    int row0;       // P, ROWS: first padded row of the tile's token rows (its columns); weight
                     // gradients: first padded row of the group (the depth)
-    int m0;         // first row of the tile: of I (P, U, G), H (ROWS), the gradient's rows
-    int n0, n;      // weight gradients: first column; columns of the tile (a multiple of 64)
-    int kb, chunk;  // stages, and stages of one sum in tensor memory
+    int m0;         // first row of the first tile: of I (P, U, G), H (ROWS), the gradient
+    int n0, n;      // weight gradients: first column; the others: columns of a tile
+    int kb;         // stages of a tile
+    int parts;      // tiles
 };
+constexpr int RUN_DW = 4;     // weight-gradient tiles of a unit at most
+
+struct Tile { int kind, m0, n0, n; };
 
 __device__ __forceinline__ void tma_store_2d(const void *tmap, const void *src, int c0, int c1)
 {
@@ -253,6 +259,12 @@ __device__ __forceinline__ void slab_bf16(unsigned char *slab, int lane, const f
                        f32x2_to_bf16x2(v[8 * i + 5], v[8 * i + 4]), f32x2_to_bf16x2(v[8 * i + 7], v[8 * i + 6]));
 }
 
+// 16 bytes to chunk c (of 4) of the lane's row of 64 bytes, in the 64-byte swizzle
+__device__ __forceinline__ void slab_row64(unsigned char *slab, int lane, int c, uint4 v)
+{
+    *reinterpret_cast<uint4 *>(slab + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v;
+}
+
 __device__ __forceinline__ int ld_acquire(const int *p)
 {
     int v;
@@ -273,7 +285,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *slabs = ring + STAGES * STAGE;
     __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], drain;
-    __shared__ int tq[TQ];
+    __shared__ int tq[TQ][8];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     volatile int *abort_flag = &abort_s;
@@ -314,16 +326,20 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
     const int ok = *p.plan.ok;
     const int row_tiles = ok ? p.plan.tiles[E] : 0;
     const int nI = (I + TM - 1) / TM, nH = (H + TM - 1) / TM;
-    const int per_w = nH * nI;                       // tiles of one weight gradient
+    // units of a group beside its gates: ROWS per tile of token rows, DW1 or DW3, DW2
+    const int rr = max(1, min(8, 32 / (I / BK)));    // H tiles of a ROWS unit
+    const int u_rows = (nH + rr - 1) / rr;
+    const int r13 = (nI + RUN_DW - 1) / RUN_DW, r2 = (nH + RUN_DW - 1) / RUN_DW;
+    const int u_dw13 = nH * r13, u_dw = 2 * u_dw13 + nI * r2;
     const int n_gates = row_tiles * nI;
-    const int n_units = ok ? n_gates + row_tiles * nH + 3 * E * per_w : 0;
+    const int n_units = ok ? n_gates + row_tiles * u_rows + E * u_dw : 0;
 
-    // Part `part` of a unit; *g: a group at or before the unit's (the search starts there).
-    auto decode = [&](int unit, int part, int &from) -> Tile {
-        Tile T{};
-        const bool gates = unit < n_gates;
-        const int v = gates ? unit : unit - n_gates;
-        const int nr = gates ? nI : nH, nw = gates ? 0 : 3 * per_w;
+    // Unit `t` of the list; from: a group at or before its own (the search starts there).
+    auto decode = [&](int t, int &from) -> Unit {
+        Unit T{};
+        const bool gates = t < n_gates;
+        const int v = gates ? t : t - n_gates;
+        const int nr = gates ? nI : u_rows, nw = gates ? 0 : u_dw;
         auto first = [&](int g) -> int { return p.plan.tiles[g] * nr + g * nw; };   // units before group g
         int lo = from;
         if (first(lo) > v) lo = 0;
@@ -342,29 +358,51 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         const int rows = pad_rows(p.plan.cnt[lo]);
         int l = v - first(lo);
         const int mt = (rows + TN - 1) / TN;         // tiles of token rows, innermost: they share the weights
-        if (gates || l < mt * nH) {
+        if (l < mt * nr) {
             const int c = l / mt, m = l - c * mt;
-            T.kind = gates ? part : ROWS;
-            T.m0 = c * TM;
             T.row0 += m * TN;
             T.n = min(TN, rows - m * TN);
-            T.kb = gates ? H / BK : 2 * (I / BK);
-            T.chunk = gates ? CHUNK : T.kb;
+            if (gates) {
+                T.kind = P;
+                T.m0 = c * TM;
+                T.kb = H / BK;
+                T.parts = 3;
+            } else {
+                T.kind = ROWS;
+                T.m0 = c * rr * TM;
+                T.kb = 2 * (I / BK);
+                T.parts = min(rr, nH - c * rr);
+            }
         } else {
-            l -= mt * nH;
-            const int w = l / per_w;
-            l -= w * per_w;
-            const int nc = w < 2 ? nI : nH, cols = w < 2 ? I : H;
+            l -= mt * nr;
+            int w = 0;
+            while (w < 2 && l >= u_dw13) { l -= u_dw13; ++w; }
+            const int nc = w < 2 ? nI : nH, runs = w < 2 ? r13 : r2;
+            const int m = l / runs, c = (l - m * runs) * RUN_DW;
             T.kind = DW1 + w;
-            T.m0 = l / nc * TM;
-            T.n0 = (l - l / nc * nc) * TN;
-            T.n = min(TN, cols - T.n0);
-            T.kb = T.chunk = rows / BK;
+            T.m0 = m * TM;
+            T.n0 = c * TN;
+            T.kb = rows / BK;
+            T.parts = min(RUN_DW, nc - c);
         }
         return T;
     };
+    auto tile_of = [&](const Unit &u, int part) -> Tile {
+        Tile T{u.kind, u.m0, u.n0, u.n};
+        if (u.kind == P) T.kind = P + part;
+        else if (u.kind == ROWS) T.m0 += part * TM;
+        else {
+            T.n0 += part * TN;
+            T.n = min(TN, (u.kind == DW2 ? H : I) - T.n0);
+        }
+        return T;
+    };
+    auto slot_read = [&](int q) -> Unit {
+        const int *e = tq[q];
+        return Unit{e[0], e[1], e[2], e[3], e[4], e[5], e[6], e[7]};
+    };
     // Units are claimed from a counter by the even CTA's producer, in order, and handed to
-    // every role of both CTAs through TQ slots (unit -1 ends).  All of a group's gates come
+    // every role of both CTAs through TQ slots (kind -1 ends).  All of a group's gates come
     // before the tiles that need them, so a cluster that waits holds nothing they need.
     auto slot_done = [&](int q) {
         if (leader) mbar_arrive(&tqe[q]);
@@ -379,96 +417,107 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
             const int r = static_cast<int>(rank);
             bool good = true;
             int from = 0;
-            auto claim = [&](int &unit) -> bool {
+            auto claim = [&](Unit &u) -> bool {
                 if (!mbar_wait_cluster(&tqe[qs], qph ^ 1u, abort_flag, p.status, tmo)) return false;
                 const int t = atomicAdd(p.plan.next, 1);
-                unit = t < n_units ? t : -1;
-                tq[qs] = unit;
+                if (t < n_units) u = decode(t, from);
+                else u.kind = -1;
+                const int vals[8] = {u.kind, u.g, u.row0, u.m0, u.n0, u.n, u.kb, u.parts};
+                const uint32_t other = mapa_shared(smem_u32(tq[qs]), 1);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    tq[qs][j] = vals[j];
+                    st_shared_cluster(other + 4u * j, vals[j]);
+                }
                 mbar_arrive(&tqf[qs]);
-                st_shared_cluster(mapa_shared(smem_u32(&tq[qs]), 1), unit);
                 mbar_arrive_cluster(mapa_shared(smem_u32(&tqf[qs]), 1));
                 if (++qs == TQ) { qs = 0; qph ^= 1u; }
                 return true;
             };
-            int unit = -1, after = -1;
+            Unit u{}, after{};
             if (leader) good = claim(after);
             while (good) {
                 if (leader) {
-                    unit = after;
-                    if (unit < 0) break;
+                    u = after;
+                    if (u.kind < 0) break;
                     if (!claim(after)) break;        // one ahead: the hand-over overlaps the loads
                 } else {
                     if (!mbar_wait_cluster(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
-                    unit = tq[qs];
+                    u = slot_read(qs);
                     slot_done(qs);
                     if (++qs == TQ) { qs = 0; qph ^= 1u; }
-                    if (unit < 0) break;
+                    if (u.kind < 0) break;
                 }
-                const int parts = unit < n_gates ? 3 : 1;
-                for (int part = 0; part < parts && good; ++part) {
-                    const Tile T = decode(unit, part, from);
-                    if (T.kind >= ROWS && T.kb > 0) {
-                        // dg, du and hw of the group: every epilogue warp of its units is done
-                        const int need = (p.plan.tiles[T.g + 1] - p.plan.tiles[T.g]) * nI * 2 * N_EPI;
-                        const int *flag = p.plan.ready + T.g;
-                        if (ld_acquire(flag) < need) {
-                            const uint64_t t0 = globaltimer_ns();
-                            while (ld_acquire(flag) < need) {
-                                if (*abort_flag) { good = false; break; }
-                                if (globaltimer_ns() - t0 > tmo) {
-                                    *abort_flag = 1;
-                                    report(p.status, MOE_ERR_DEVICE_TIMEOUT);
-                                    good = false;
-                                    break;
-                                }
-                                __nanosleep(64);
+                if (u.kind >= ROWS && u.kb > 0) {
+                    // dg, du and hw of the group: every epilogue warp of its units is done
+                    const int need = (p.plan.tiles[u.g + 1] - p.plan.tiles[u.g]) * nI * 2 * N_EPI;
+                    const int *flag = p.plan.ready + u.g;
+                    if (ld_acquire(flag) < need) {
+                        const uint64_t t0 = globaltimer_ns();
+                        while (ld_acquire(flag) < need) {
+                            if (*abort_flag) { good = false; break; }
+                            if (globaltimer_ns() - t0 > tmo) {
+                                *abort_flag = 1;
+                                report(p.status, MOE_ERR_DEVICE_TIMEOUT);
+                                good = false;
+                                break;
                             }
-                            if (!good) break;
+                            __nanosleep(64);
                         }
-                        fence_proxy_async_global();
+                        if (!good) break;
                     }
-                    const bool dw = T.kind >= DW1;
+                    fence_proxy_async_global();
+                }
+                for (int part = 0; part < u.parts && good; ++part) {
+                    const Tile T = tile_of(u, part);
                     const int nb = T.n / 2;          // this CTA's columns
-                    const uint32_t bytes = 2 * HALF + (dw ? (nb > 64 ? 2 : 1) * HALF : nb * 128);
+                    const bool boxes = T.kind >= ROWS;   // B in boxes of 64 x 64
+                    const uint32_t bytes = 2 * HALF + (boxes ? (nb > 64 ? 2 : 1) * HALF : nb * 128);
                     const int m = T.m0 + 128 * r;
-                    const int brow = T.row0 + nb * r;
-                    const CUtensorMap *b128 = T.kind == P ? &p.d128 : &p.x128, *b32 = T.kind == P ? &p.d32 : &p.x32;
-                    const CUtensorMap *wm = T.kind == U ? &p.w3 : &p.w1;
-                    for (int kb = 0; kb < T.kb; ++kb, ++it) {
+                    const int n = (T.kind >= DW1 ? T.n0 : u.row0) + nb * r;
+                    for (int kb = 0; kb < u.kb; ++kb, ++it) {
                         if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
                         unsigned char *a = ring + s * STAGE, *b = a + 2 * HALF;
                         const uint32_t fb = full0 + 8u * s;
                         if (leader) mbar_arrive_expect_tx(&full[s], 2u * bytes);
                         int k = kb * BK;
-                        if (dw) {
-                            const CUtensorMap *ma = T.kind == DW2 ? &p.hb : &p.xb;
-                            const CUtensorMap *mb = T.kind == DW2 ? &p.db : (T.kind == DW3 ? &p.ub : &p.gb);
-                            const int n = T.n0 + nb * r;
-                            k += T.row0;
-                            tma_load_2d_pair(a, ma, fb, m, k);
-                            tma_load_2d_pair(a + HALF, ma, fb, m + 64, k);
-                            tma_load_2d_pair(b, mb, fb, n, k);
-                            if (nb > 64) tma_load_2d_pair(b + HALF, mb, fb, n + 64, k);
-                        } else {
-                            if (T.kind == P) {           // rows of W2: depth along H
-                                tma_load_3d_pair(a, &p.w2, fb, k, m, T.g);
-                                tma_load_3d_pair(a + HALF, &p.w2, fb, k, m + 64, T.g);
-                            } else if (T.kind != ROWS) { // columns of W1, W3: depth along H
-                                tma_load_3d_pair(a, wm, fb, m, k, T.g);
-                                tma_load_3d_pair(a + HALF, wm, fb, m + 64, k, T.g);
-                            } else {                     // rows of W1, then of W3: depth along I
-                                const bool second = k >= I;
-                                if (second) k -= I;
-                                wm = second ? &p.w3 : &p.w1;
-                                b128 = second ? &p.u128 : &p.g128;
-                                b32 = second ? &p.u32 : &p.g32;
-                                tma_load_3d_pair(a, wm, fb, k, m, T.g);
-                                tma_load_3d_pair(a + HALF, wm, fb, k, m + 64, T.g);
+                        if (T.kind < ROWS) {
+                            if (T.kind == P) {           // rows of W2
+                                tma_load_3d_pair(a, &p.w2, fb, k, m, u.g);
+                                tma_load_3d_pair(a + HALF, &p.w2, fb, k, m + 64, u.g);
+                            } else {                     // columns of W3, W1
+                                const CUtensorMap *wm = T.kind == U ? &p.w3 : &p.w1;
+                                tma_load_3d_pair(a, wm, fb, m, k, u.g);
+                                tma_load_3d_pair(a + HALF, wm, fb, m + 64, k, u.g);
                             }
-                            if (nb == 128)
-                                tma_load_2d_pair(b, b128, fb, k, brow);
-                            else
-                                for (int j = 0; j < nb; j += 32) tma_load_2d_pair(b + j * 128, b32, fb, k, brow + j);
+                            if (nb == 128) {
+                                tma_load_2d_pair(b, T.kind == P ? &p.d128 : &p.x128, fb, k, n);
+                            } else {
+                                const CUtensorMap *bm = T.kind == P ? &p.d32 : &p.x32;
+                                for (int j = 0; j < nb; j += 32) tma_load_2d_pair(b + j * 128, bm, fb, k, n + j);
+                            }
+                        } else if (T.kind == ROWS) {     // rows of W1, then of W3; dg, then du
+                            const bool second = k >= I;
+                            if (second) k -= I;
+                            const CUtensorMap *wm = second ? &p.w3 : &p.w1, *bm = second ? &p.ub : &p.gb;
+                            tma_load_3d_pair(a, wm, fb, k, m, u.g);
+                            tma_load_3d_pair(a + HALF, wm, fb, k, m + 64, u.g);
+                            tma_load_2d_pair(b, bm, fb, n, k);
+                            if (nb > 64) tma_load_2d_pair(b + HALF, bm, fb, n + 64, k);
+                        } else {
+                            k += u.row0;
+                            if (T.kind == DW2) {         // hw as it lies; columns of dY
+                                tma_load_2d_pair(a, &p.hb, fb, k, m);
+                                tma_load_2d_pair(a + HALF, &p.hb, fb, k, m + 64);
+                                tma_load_2d_pair(b, &p.db, fb, n, k);
+                                if (nb > 64) tma_load_2d_pair(b + HALF, &p.db, fb, n + 64, k);
+                            } else {                     // columns of X; dg or du as it lies
+                                const CUtensorMap *bm = T.kind == DW3 ? &p.ub : &p.gb;
+                                tma_load_2d_pair(a, &p.xb, fb, m, k);
+                                tma_load_2d_pair(a + HALF, &p.xb, fb, m + 64, k);
+                                tma_load_2d_pair(b, bm, fb, k, n);
+                                if (nb > 64) tma_load_2d_pair(b + HALF, bm, fb, k, n + 64);
+                            }
                         }
                         if (++s == STAGES) { s = 0; ph ^= 1u; }
                     }
@@ -490,19 +539,18 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
             const uint32_t ring0 = smem_u32(ring);
             uint32_t s = 0, ph = 0, b = 0, tph = 0, qs = 0, qph = 0;
             bool good = true;
-            int from = 0;
             while (good) {
                 if (!mbar_wait(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
-                const int unit = tq[qs];
+                const Unit un = slot_read(qs);
                 slot_done(qs);
                 if (++qs == TQ) { qs = 0; qph ^= 1u; }
-                if (unit < 0) break;
-                const int parts = unit < n_gates ? 3 : 1;
-                for (int part = 0; part < parts && good; ++part) {
-                    const Tile T = decode(unit, part, from);
-                    // rows K-major; columns of W1, W3 as the tile's rows, and (weight gradients)
-                    // rows as the depth, MN-major
-                    const bool bmn = T.kind >= DW1, amn = bmn || T.kind == U || T.kind == G;
+                if (un.kind < 0) break;
+                const int chunk = un.kind == P ? CHUNK : un.kb;
+                for (int part = 0; part < un.parts && good; ++part) {
+                    const Tile T = tile_of(un, part);
+                    // MN-major where the operand lies with the tile's rows (columns) contiguous
+                    const bool amn = T.kind == U || T.kind == G || T.kind == DW1 || T.kind == DW3;
+                    const bool bmn = T.kind == ROWS || T.kind == DW2;
                     const uint64_t ad0 = smem_desc_sw128(ring0, amn ? HALF : 16, 1024);
                     const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, bmn ? HALF : 16, 1024);
                     const uint32_t as = amn ? 128u : 2u, bs = bmn ? 128u : 2u;
@@ -512,7 +560,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                         if (!mbar_wait_cluster(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
                         tc_fence_after();
                         const uint32_t d = tmem + b * TN;
-                        const int end = min(kb + T.chunk, T.kb);
+                        const int end = min(kb + chunk, un.kb);
                         for (int k0 = kb; kb < end; ++kb) {
                             if (!mbar_wait(&full[s], ph, abort_flag, p.status, tmo)) { good = false; break; }
                             tc_fence_after();
@@ -529,7 +577,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                         tc_commit_pair_mc(&tfull[b], 3);
                         b ^= 1u;
                         if (b == 0) tph ^= 1u;
-                    } while (kb < T.kb);
+                    } while (kb < un.kb);
                 }
             }
             tc_commit_pair_mc(&drain, 1);
@@ -567,29 +615,25 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         // this thread's stash: p, then u, of its row, float4 i at i * SROW (256 threads side by side)
         float4 *stash = reinterpret_cast<float4 *>(p.stash + static_cast<size_t>(blockIdx.x) * STASH) + (tid - 64);
         constexpr int SROW = 32 * N_EPI;
-        int from = 0;
         bool good = true;
         while (good) {
             if (!wait_all(&tqf[qs], qph)) break;
-            const int unit = tq[qs];
+            const Unit u = slot_read(qs);
             __syncwarp();
             if (lane == 0) slot_done(qs);
             if (++qs == TQ) { qs = 0; qph ^= 1u; }
-            if (unit < 0) break;
-            if (unit < n_gates) {
-                Tile T{};
-                int nc = 0;                          // 32-column pieces of this warp's half
+            if (u.kind < 0) break;
+            if (u.kind == P) {
+                const int nc = u.n / 64;             // 32-column pieces of this warp's half
+                const uint32_t at = tm0 + static_cast<uint32_t>(half * (u.n / 2));
                 float acc[128];                      // row i of the tile, its half of the token rows
 #pragma unroll 1
-                for (int part = P; part <= G && good; ++part) {
-                    T = decode(unit, part, from);
-                    nc = T.n / 64;
-                    const uint32_t at = tm0 + static_cast<uint32_t>(half * (T.n / 2));
+                for (int part = P; part <= G; ++part) {
                     // sums over the chunks, in registers
 #pragma unroll
                     for (int i = 0; i < 128; ++i) acc[i] = 0.f;
 #pragma unroll 1
-                    for (int kb = 0; kb < T.kb; kb += CHUNK) {
+                    for (int kb = 0; kb < u.kb; kb += CHUNK) {
                         if (!sums_ready()) { good = false; break; }
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
@@ -602,7 +646,8 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                         }
                         sums_read();
                     }
-                    if (good && part != G) {
+                    if (!good) break;
+                    if (part != G) {
                         float4 *st = stash + part * 32 * SROW;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -612,42 +657,51 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                 if (!good) break;
                 // g in acc; p and u in the stash.  32 token rows at a time: dg, du, hw and the
                 // terms of <p, h>
-                const int col = T.m0 + r0;           // the warp's columns of I
-                const int tok = T.row0 + half * (T.n / 2);
-                float *dwp = p.dwp + static_cast<size_t>((T.m0 + r0) / 32) * p.ld_dwp + tok + lane;
+                const int col = u.m0 + r0;           // the warp's columns of I
+                const int tok = u.row0 + half * (u.n / 2);
+                float *dwp = p.dwp + static_cast<size_t>(col / 32) * p.ld_dwp + tok + lane;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (c >= nc) continue;
                     const float4 *wv = reinterpret_cast<const float4 *>(p.wrow + tok + 32 * c);
-                    uint16_t *sl = reinterpret_cast<uint16_t *>(slab);
                     uint32_t hw[16];
                     slab_free(lane);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 p4 = stash[(8 * c + i / 4) * SROW], u4 = stash[(32 + 8 * c + i / 4) * SROW], w4 = wv[i / 4];
-                        const float pp[4] = {p4.x, p4.y, p4.z, p4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
-                        const float ww[4] = {w4.x, w4.y, w4.z, w4.w};
-                        float hv[4];
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t og[4], ou[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float g = acc[32 * c + i + k], u = uu[k];
-                            const float s = fast_sigmoid(g), gs = g * s, h = gs * u, pw = pp[k] * ww[k];
-                            const uint32_t o = f32x2_to_bf16x2(pw * gs, pw * u * s * fmaf(g, 1.f - s, 1.f));
-                            sl[(i + k) * 32 + lane] = static_cast<uint16_t>(o);
-                            sl[1024 + (i + k) * 32 + lane] = static_cast<uint16_t>(o >> 16);
-                            hv[k] = ww[k] * h;
-                            acc[32 * c + i + k] = pp[k] * h;
+                        for (int y = 0; y < 8; y += 4) {
+                            const int j = i + y;
+                            const float4 p4 = stash[(8 * c + j / 4) * SROW], u4 = stash[(32 + 8 * c + j / 4) * SROW], w4 = wv[j / 4];
+                            const float pp[4] = {p4.x, p4.y, p4.z, p4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
+                            const float ww[4] = {w4.x, w4.y, w4.z, w4.w};
+                            float a[4], e[4], hv[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float g = acc[32 * c + j + k];
+                                const float s = fast_sigmoid(g), gs = g * s, h = gs * uu[k], pw = pp[k] * ww[k];
+                                a[k] = pw * uu[k] * s * fmaf(g, 1.f - s, 1.f);
+                                e[k] = pw * gs;
+                                hv[k] = ww[k] * h;
+                                acc[32 * c + j + k] = pp[k] * h;
+                            }
+                            og[y / 2] = f32x2_to_bf16x2(a[1], a[0]);
+                            og[y / 2 + 1] = f32x2_to_bf16x2(a[3], a[2]);
+                            ou[y / 2] = f32x2_to_bf16x2(e[1], e[0]);
+                            ou[y / 2 + 1] = f32x2_to_bf16x2(e[3], e[2]);
+                            hw[j / 2] = f32x2_to_bf16x2(hv[1], hv[0]);
+                            hw[j / 2 + 1] = f32x2_to_bf16x2(hv[3], hv[2]);
                         }
-                        hw[i / 2] = f32x2_to_bf16x2(hv[1], hv[0]);
-                        hw[i / 2 + 1] = f32x2_to_bf16x2(hv[3], hv[2]);
+                        slab_row64(slab, lane, i / 8, make_uint4(og[0], og[1], og[2], og[3]));
+                        slab_row64(slab + 2048, lane, i / 8, make_uint4(ou[0], ou[1], ou[2], ou[3]));
                     }
                     slab_ready();
                     if (lane == 0 && col < I) {
-                        tma_store_2d(&p.gs, slab, col, tok + 32 * c);
-                        tma_store_2d(&p.us, slab + 2048, col, tok + 32 * c);
+                        tma_store_2d(&p.gs, slab, tok + 32 * c, col);
+                        tma_store_2d(&p.us, slab + 2048, tok + 32 * c, col);
                         slab_commit();
                     }
-                    // sum over the warp's 32 columns: lane j ends up with token row j
+                    // sum over the warp's 32 columns of I: lane j ends up with token row j
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -660,13 +714,11 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                     if (col < I) dwp[32 * c] = acc[32 * c];
                     slab_free(lane);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        sl[2 * i * 32 + lane] = static_cast<uint16_t>(hw[i]);
-                        sl[(2 * i + 1) * 32 + lane] = static_cast<uint16_t>(hw[i] >> 16);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        slab_row64(slab, lane, i, make_uint4(hw[4 * i], hw[4 * i + 1], hw[4 * i + 2], hw[4 * i + 3]));
                     slab_ready();
                     if (lane == 0 && col < I) {
-                        tma_store_2d(&p.hs, slab, col, tok + 32 * c);
+                        tma_store_2d(&p.hs, slab, tok + 32 * c, col);
                         slab_commit();
                     }
                 }
@@ -675,57 +727,60 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
                     fence_proxy_async_global();
                     __threadfence();
-                    atomicAdd(p.plan.ready + T.g, 1);
+                    atomicAdd(p.plan.ready + u.g, 1);
                 }
                 __syncwarp();
                 continue;
             }
-            const Tile T = decode(unit, 0, from);
-            if (!sums_ready()) break;
-            if (T.kind == ROWS) {
-                const int col = T.m0 + r0, tok = T.row0 + half * (T.n / 2);
-                const uint32_t at = tm0 + b * TN + static_cast<uint32_t>(half * (T.n / 2));
-                float *sl = reinterpret_cast<float *>(slab);
 #pragma unroll 1
-                for (int c = 0; c < T.n / 64; ++c) {
-                    float v[32];
-                    __syncwarp();
-                    tmem_ld32(at + 32 * c, v);
-                    slab_free(lane);
+            for (int part = 0; part < u.parts; ++part) {
+                const Tile T = tile_of(u, part);
+                if (!sums_ready()) { good = false; break; }
+                if (T.kind == ROWS) {
+                    const int col = T.m0 + r0, tok = u.row0 + half * (T.n / 2);
+                    const uint32_t at = tm0 + b * TN + static_cast<uint32_t>(half * (T.n / 2));
+                    float *sl = reinterpret_cast<float *>(slab);
+#pragma unroll 1
+                    for (int c = 0; c < T.n / 64; ++c) {
+                        float v[32];
+                        __syncwarp();
+                        tmem_ld32(at + 32 * c, v);
+                        slab_free(lane);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sl[i * 32 + lane] = v[i];
-                    slab_ready();
-                    if (lane == 0 && col < H) {
-                        tma_store_2d(&p.xs, slab, col, tok + 32 * c);
-                        slab_commit();
+                        for (int i = 0; i < 32; ++i) sl[i * 32 + lane] = v[i];
+                        slab_ready();
+                        if (lane == 0 && col < H) {
+                            tma_store_2d(&p.xs, slab, col, tok + 32 * c);
+                            slab_commit();
+                        }
+                    }
+                } else {
+                    const int M = T.kind == DW2 ? I : H;
+                    const CUtensorMap *sm = T.kind == DW1 ? &p.s1 : (T.kind == DW3 ? &p.s3 : &p.s2);
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        const int lc = 128 * half + 64 * c;
+                        if (lc >= T.n) break;
+                        float v[32], y[32];
+                        __syncwarp();
+                        tmem_ld32(tm0 + b * TN + lc, v);
+                        tmem_ld32(tm0 + b * TN + lc + 32, y);
+                        if (u.kb == 0) {             // an expert without rows
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = y[i] = 0.f;
+                        }
+                        slab_free(lane);
+                        slab_bf16(slab, lane, v, 0);
+                        slab_bf16(slab, lane, y, 4);
+                        slab_ready();
+                        if (lane == 0 && T.m0 + r0 < M) {
+                            tma_store_3d(sm, slab, T.n0 + lc, T.m0 + r0, u.g);
+                            slab_commit();
+                        }
                     }
                 }
-            } else {
-                const int M = T.kind == DW2 ? I : H;
-                const CUtensorMap *sm = T.kind == DW1 ? &p.s1 : (T.kind == DW3 ? &p.s3 : &p.s2);
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    const int lc = 128 * half + 64 * c;
-                    if (lc >= T.n) break;
-                    float v[32], u[32];
-                    __syncwarp();
-                    tmem_ld32(tm0 + b * TN + lc, v);
-                    tmem_ld32(tm0 + b * TN + lc + 32, u);
-                    if (T.kb == 0) {             // an expert without rows
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = u[i] = 0.f;
-                    }
-                    slab_free(lane);
-                    slab_bf16(slab, lane, v, 0);
-                    slab_bf16(slab, lane, u, 4);
-                    slab_ready();
-                    if (lane == 0 && T.m0 + r0 < M) {
-                        tma_store_3d(sm, slab, T.n0 + lc, T.m0 + r0, T.g);
-                        slab_commit();
-                    }
-                }
+                sums_read();
             }
-            sums_read();
         }
         // the last stores have left shared memory and reached global memory
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -804,8 +859,9 @@ EncodeTiledFn encode_fn()
 }
 
 // [groups][rows][cols] (groups == 0: [rows][cols]) of bf16, or fp32, in boxes of box_cols columns
-// x box_rows rows: 128 bytes wide in the 128-byte swizzle (an operand, or a slab written so),
-// or 32 columns as they stand.
+// x box_rows rows: 64 bf16 in the 128-byte swizzle, 32 bf16 in the 64-byte one, 32 fp32 as they
+// stand.  (A box narrower than its swizzle's span is stored from rows of the whole span: it
+// would read past a slab.)
 bool encode(CUtensorMap *m, const void *base, int groups, long long rows, int cols, int box_rows,
             int box_cols = 64, bool fp32 = false)
 {
@@ -819,7 +875,7 @@ bool encode(CUtensorMap *m, const void *base, int groups, long long rows, int co
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups ? 3 : 2,
               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              fp32 ? CU_TENSOR_MAP_SWIZZLE_NONE : (box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B),
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -879,15 +935,13 @@ cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned
     GemmArgs a;
     memset(&a, 0, sizeof a);
     if (!encode(&a.x128, X, 0, L.rows, H, 128) || !encode(&a.d128, D, 0, L.rows, H, 128) ||
-        !encode(&a.g128, dg, 0, L.rows, I, 128) || !encode(&a.u128, du, 0, L.rows, I, 128) ||
         !encode(&a.x32, X, 0, L.rows, H, 32) || !encode(&a.d32, D, 0, L.rows, H, 32) ||
-        !encode(&a.g32, dg, 0, L.rows, I, 32) || !encode(&a.u32, du, 0, L.rows, I, 32) ||
         !encode(&a.xb, X, 0, L.rows, H, 64) || !encode(&a.db, D, 0, L.rows, H, 64) ||
-        !encode(&a.gb, dg, 0, L.rows, I, 64) || !encode(&a.ub, du, 0, L.rows, I, 64) ||
-        !encode(&a.hb, hw, 0, L.rows, I, 64) || !encode(&a.w1, f.W1, E, H, I, 64) ||
+        !encode(&a.gb, dg, 0, I, static_cast<int>(L.rows), 64) || !encode(&a.ub, du, 0, I, static_cast<int>(L.rows), 64) ||
+        !encode(&a.hb, hw, 0, I, static_cast<int>(L.rows), 64) || !encode(&a.w1, f.W1, E, H, I, 64) ||
         !encode(&a.w3, f.W3, E, H, I, 64) || !encode(&a.w2, f.W2, E, I, H, 64) ||
-        !encode(&a.gs, dg, 0, L.rows, I, 32, 32) || !encode(&a.us, du, 0, L.rows, I, 32, 32) ||
-        !encode(&a.hs, hw, 0, L.rows, I, 32, 32) || !encode(&a.xs, dxp, 0, L.rows, H, 32, 32, true) ||
+        !encode(&a.gs, dg, 0, I, static_cast<int>(L.rows), 32, 32) || !encode(&a.us, du, 0, I, static_cast<int>(L.rows), 32, 32) ||
+        !encode(&a.hs, hw, 0, I, static_cast<int>(L.rows), 32, 32) || !encode(&a.xs, dxp, 0, L.rows, H, 32, 32, true) ||
         !encode(&a.s1, f.dW1, E, H, I, 32) || !encode(&a.s3, f.dW3, E, H, I, 32) ||
         !encode(&a.s2, f.dW2, E, I, H, 32))
         return cudaErrorInvalidValue;
