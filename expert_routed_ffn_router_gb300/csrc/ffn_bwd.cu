@@ -45,7 +45,8 @@ constexpr int PADR = 64;                  // groups start at multiples of this m
 constexpr int TM = 256, TN = 256;         // tile of a cluster (TN: at most)
 constexpr int BK = 64;                    // depth of a stage
 constexpr int N_EPI = 8;                  // epilogue warps
-constexpr int NT = 64 + 32 * N_EPI;       // at most 168 registers a thread
+constexpr int CLAIM_WARP = 2 + N_EPI;
+constexpr int NT = 32 * (CLAIM_WARP + 1); // at most 168 registers a thread
 constexpr int MAXG = 1024;
 constexpr int HALF = 8192;                // one 64 x 64 bf16 box
 constexpr int STAGE = 4 * HALF;           // A: 128 of the tile's rows; B: 128 of its columns
@@ -68,8 +69,8 @@ struct Plan {
 };
 
 struct GemmArgs {
-    // loads: rows of X and dY in boxes of 128 and of 32; those, dg, du, hw (transposed) and the
-    // weights in boxes of 64 x 64
+    // loads: rows of X and dY in boxes of 128 and of 32; those, the weights and blocks of dg, du
+    // and hw ([rows / 64][I][64]) in boxes of 64 x 64
     CUtensorMap x128, d128, x32, d32, xb, db, gb, ub, hb, w1, w3, w2;
     // stores: dg, du, hw (32 token rows x 32 of I), rows of dX (32 fp32 x 32), weight gradients
     CUtensorMap gs, us, hs, xs, s1, s3, s2;
@@ -213,7 +214,7 @@ struct Unit {
     int row0;       // P, ROWS: first padded row of the tile's token rows (its columns); weight
                     // gradients: first padded row of the group (the depth)
     int m0;         // first row of the first tile: of I (P, U, G), H (ROWS), the gradient
-    int n0, n;      // weight gradients: first column; the others: columns of a tile
+    int n0, n;      // columns in the group, columns of a tile; weight gradients: first column, -
     int kb;         // stages of a tile
     int parts;      // tiles
 };
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         }
         for (int q = 0; q < TQ; ++q) {
             mbar_init(&tqf[q], 1);
-            mbar_init(&tqe[q], 2 * N_EPI + 2);   // both epilogues, the MMA issuer, the odd producer
+            mbar_init(&tqe[q], 2 * N_EPI + 3);   // both epilogues and producers, the MMA issuer
         }
         mbar_init(&drain, 1);
         abort_s = 0;
@@ -361,7 +362,8 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         if (l < mt * nr) {
             const int c = l / mt, m = l - c * mt;
             T.row0 += m * TN;
-            T.n = min(TN, rows - m * TN);
+            T.n0 = min(TN, rows - m * TN);
+            T.n = T.n0 == 192 ? 256 : T.n0;          // (its halves: whole blocks of 64, or half of one)
             if (gates) {
                 T.kind = P;
                 T.m0 = c * TM;
@@ -401,8 +403,9 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         const int *e = tq[q];
         return Unit{e[0], e[1], e[2], e[3], e[4], e[5], e[6], e[7]};
     };
-    // Units are claimed from a counter by the even CTA's producer, in order, and handed to
-    // every role of both CTAs through TQ slots (kind -1 ends).  All of a group's gates come
+    // Units are claimed from a counter by a warp of the even CTA, in order, and handed to every
+    // role of both CTAs through TQ slots (kind -1 ends): the counter's round trip and the search
+    // for the group stay off the producer's thread, whose pause empties the ring.  All of a group's gates come
     // before the tiles that need them, so a cluster that waits holds nothing they need.
     auto slot_done = [&](int q) {
         if (leader) mbar_arrive(&tqe[q]);
@@ -416,38 +419,12 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
             const uint32_t full0 = mapa_shared(smem_u32(full), 0);
             const int r = static_cast<int>(rank);
             bool good = true;
-            int from = 0;
-            auto claim = [&](Unit &u) -> bool {
-                if (!mbar_wait_cluster(&tqe[qs], qph ^ 1u, abort_flag, p.status, tmo)) return false;
-                const int t = atomicAdd(p.plan.next, 1);
-                if (t < n_units) u = decode(t, from);
-                else u.kind = -1;
-                const int vals[8] = {u.kind, u.g, u.row0, u.m0, u.n0, u.n, u.kb, u.parts};
-                const uint32_t other = mapa_shared(smem_u32(tq[qs]), 1);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    tq[qs][j] = vals[j];
-                    st_shared_cluster(other + 4u * j, vals[j]);
-                }
-                mbar_arrive(&tqf[qs]);
-                mbar_arrive_cluster(mapa_shared(smem_u32(&tqf[qs]), 1));
-                if (++qs == TQ) { qs = 0; qph ^= 1u; }
-                return true;
-            };
-            Unit u{}, after{};
-            if (leader) good = claim(after);
             while (good) {
-                if (leader) {
-                    u = after;
-                    if (u.kind < 0) break;
-                    if (!claim(after)) break;        // one ahead: the hand-over overlaps the loads
-                } else {
-                    if (!mbar_wait_cluster(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
-                    u = slot_read(qs);
-                    slot_done(qs);
-                    if (++qs == TQ) { qs = 0; qph ^= 1u; }
-                    if (u.kind < 0) break;
-                }
+                if (!mbar_wait_cluster(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
+                const Unit u = slot_read(qs);
+                slot_done(qs);
+                if (++qs == TQ) { qs = 0; qph ^= 1u; }
+                if (u.kind < 0) break;
                 if (u.kind >= ROWS && u.kb > 0) {
                     // dg, du and hw of the group: every epilogue warp of its units is done
                     const int need = (p.plan.tiles[u.g + 1] - p.plan.tiles[u.g]) * nI * 2 * N_EPI;
@@ -502,21 +479,21 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                             const CUtensorMap *wm = second ? &p.w3 : &p.w1, *bm = second ? &p.ub : &p.gb;
                             tma_load_3d_pair(a, wm, fb, k, m, u.g);
                             tma_load_3d_pair(a + HALF, wm, fb, k, m + 64, u.g);
-                            tma_load_2d_pair(b, bm, fb, n, k);
-                            if (nb > 64) tma_load_2d_pair(b + HALF, bm, fb, n + 64, k);
+                            tma_load_3d_pair(b, bm, fb, n & 63, k, n >> 6);
+                            if (nb > 64) tma_load_3d_pair(b + HALF, bm, fb, 0, k, (n >> 6) + 1);
                         } else {
                             k += u.row0;
                             if (T.kind == DW2) {         // hw as it lies; columns of dY
-                                tma_load_2d_pair(a, &p.hb, fb, k, m);
-                                tma_load_2d_pair(a + HALF, &p.hb, fb, k, m + 64);
+                                tma_load_3d_pair(a, &p.hb, fb, 0, m, k >> 6);
+                                tma_load_3d_pair(a + HALF, &p.hb, fb, 0, m + 64, k >> 6);
                                 tma_load_2d_pair(b, &p.db, fb, n, k);
                                 if (nb > 64) tma_load_2d_pair(b + HALF, &p.db, fb, n + 64, k);
                             } else {                     // columns of X; dg or du as it lies
                                 const CUtensorMap *bm = T.kind == DW3 ? &p.ub : &p.gb;
                                 tma_load_2d_pair(a, &p.xb, fb, m, k);
                                 tma_load_2d_pair(a + HALF, &p.xb, fb, m + 64, k);
-                                tma_load_2d_pair(b, bm, fb, k, n);
-                                if (nb > 64) tma_load_2d_pair(b + HALF, bm, fb, k, n + 64);
+                                tma_load_3d_pair(b, bm, fb, 0, n, k >> 6);
+                                if (nb > 64) tma_load_3d_pair(b + HALF, bm, fb, 0, n + 64, k >> 6);
                             }
                         }
                         if (++s == STAGES) { s = 0; ph ^= 1u; }
@@ -584,6 +561,30 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
             int dummy = 0;
             mbar_wait(&drain, 0, &dummy, nullptr, 20000000ull);
         }
+    } else if (warp == CLAIM_WARP) {
+        // ------------------------------------------------------------------ claims
+        if (lane == 0 && leader) {
+            uint32_t qs = 0, qph = 0;
+            int from = 0;
+            int t = 0;
+            do {
+                if (!mbar_wait_cluster(&tqe[qs], qph ^ 1u, abort_flag, p.status, tmo)) break;
+                t = atomicAdd(p.plan.next, 1);
+                Unit u{};
+                if (t < n_units) u = decode(t, from);
+                else u.kind = -1;
+                const int vals[8] = {u.kind, u.g, u.row0, u.m0, u.n0, u.n, u.kb, u.parts};
+                const uint32_t other = mapa_shared(smem_u32(tq[qs]), 1);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    tq[qs][j] = vals[j];
+                    st_shared_cluster(other + 4u * j, vals[j]);
+                }
+                mbar_arrive(&tqf[qs]);
+                mbar_arrive_cluster(mapa_shared(smem_u32(&tqf[qs]), 1));
+                if (++qs == TQ) { qs = 0; qph ^= 1u; }
+            } while (t < n_units);
+        }
     } else {
         // ---------------------------------------------------------------- epilogue
         const int q = warp & 3, half = (warp - 2) >> 2;   // lane quarter, half of the columns
@@ -624,7 +625,8 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
             if (++qs == TQ) { qs = 0; qph ^= 1u; }
             if (u.kind < 0) break;
             if (u.kind == P) {
-                const int nc = u.n / 64;             // 32-column pieces of this warp's half
+                // 32-column pieces of this warp's half that are in the group
+                const int nc = max(0, min(u.n / 2, u.n0 - half * (u.n / 2))) / 32;
                 const uint32_t at = tm0 + static_cast<uint32_t>(half * (u.n / 2));
                 float acc[128];                      // row i of the tile, its half of the token rows
 #pragma unroll 1
@@ -697,8 +699,9 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                     }
                     slab_ready();
                     if (lane == 0 && col < I) {
-                        tma_store_2d(&p.gs, slab, tok + 32 * c, col);
-                        tma_store_2d(&p.us, slab + 2048, tok + 32 * c, col);
+                        const int t0 = tok + 32 * c;
+                        tma_store_3d(&p.gs, slab, t0 & 63, col, t0 >> 6);
+                        tma_store_3d(&p.us, slab + 2048, t0 & 63, col, t0 >> 6);
                         slab_commit();
                     }
                     // sum over the warp's 32 columns of I: lane j ends up with token row j
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                         slab_row64(slab, lane, i, make_uint4(hw[4 * i], hw[4 * i + 1], hw[4 * i + 2], hw[4 * i + 3]));
                     slab_ready();
                     if (lane == 0 && col < I) {
-                        tma_store_2d(&p.hs, slab, tok + 32 * c, col);
+                        tma_store_3d(&p.hs, slab, (tok + 32 * c) & 63, col, (tok + 32 * c) >> 6);
                         slab_commit();
                     }
                 }
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                     const uint32_t at = tm0 + b * TN + static_cast<uint32_t>(half * (T.n / 2));
                     float *sl = reinterpret_cast<float *>(slab);
 #pragma unroll 1
-                    for (int c = 0; c < T.n / 64; ++c) {
+                    for (int c = 0; c < max(0, min(T.n / 2, u.n0 - half * (T.n / 2))) / 32; ++c) {
                         float v[32];
                         __syncwarp();
                         tmem_ld32(at + 32 * c, v);
@@ -931,17 +934,19 @@ cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned
     float *dxp = reinterpret_cast<float *>(w + L.dxp);
     int *prow = reinterpret_cast<int *>(w + L.prow);
 
+    // dg, du and hw lie in blocks of 64 token rows: [rows / 64][I][64]
     void *dg = w + L.dg, *du = w + L.du, *hw = w + L.hw;
+    const int blocks = static_cast<int>(L.rows / 64);
     GemmArgs a;
     memset(&a, 0, sizeof a);
     if (!encode(&a.x128, X, 0, L.rows, H, 128) || !encode(&a.d128, D, 0, L.rows, H, 128) ||
         !encode(&a.x32, X, 0, L.rows, H, 32) || !encode(&a.d32, D, 0, L.rows, H, 32) ||
         !encode(&a.xb, X, 0, L.rows, H, 64) || !encode(&a.db, D, 0, L.rows, H, 64) ||
-        !encode(&a.gb, dg, 0, I, static_cast<int>(L.rows), 64) || !encode(&a.ub, du, 0, I, static_cast<int>(L.rows), 64) ||
-        !encode(&a.hb, hw, 0, I, static_cast<int>(L.rows), 64) || !encode(&a.w1, f.W1, E, H, I, 64) ||
+        !encode(&a.gb, dg, blocks, I, 64, 64) || !encode(&a.ub, du, blocks, I, 64, 64) ||
+        !encode(&a.hb, hw, blocks, I, 64, 64) || !encode(&a.w1, f.W1, E, H, I, 64) ||
         !encode(&a.w3, f.W3, E, H, I, 64) || !encode(&a.w2, f.W2, E, I, H, 64) ||
-        !encode(&a.gs, dg, 0, I, static_cast<int>(L.rows), 32, 32) || !encode(&a.us, du, 0, I, static_cast<int>(L.rows), 32, 32) ||
-        !encode(&a.hs, hw, 0, I, static_cast<int>(L.rows), 32, 32) || !encode(&a.xs, dxp, 0, L.rows, H, 32, 32, true) ||
+        !encode(&a.gs, dg, blocks, I, 64, 32, 32) || !encode(&a.us, du, blocks, I, 64, 32, 32) ||
+        !encode(&a.hs, hw, blocks, I, 64, 32, 32) || !encode(&a.xs, dxp, 0, L.rows, H, 32, 32, true) ||
         !encode(&a.s1, f.dW1, E, H, I, 32) || !encode(&a.s3, f.dW3, E, H, I, 32) ||
         !encode(&a.s2, f.dW2, E, I, H, 32))
         return cudaErrorInvalidValue;
