@@ -45,16 +45,21 @@ constexpr int PADR = 64;                  // groups start at multiples of this m
 constexpr int TM = 256, TN = 256;         // tile of a cluster (TN: at most)
 constexpr int BK = 64;                    // depth of a stage
 constexpr int N_EPI = 8;                  // epilogue warps
-constexpr int CLAIM_WARP = 2 + N_EPI;
-constexpr int NT = 32 * (CLAIM_WARP + 1); // at most 168 registers a thread
+constexpr int CLAIM_WARP = 2;
+constexpr int EPI0 = 4;                   // first epilogue warp (its warpgroup's start)
+constexpr int NT = 32 * (EPI0 + N_EPI);
+// Registers: 384 threads launch with 168 each; the first warpgroup hands its share on
+// (128 x 88 + 256 x 208 = 384 x 168) for the sums that an epilogue thread holds.
+constexpr int REGS_FEW = 88, REGS_MANY = 208;
 constexpr int MAXG = 1024;
 constexpr int HALF = 8192;                // one 64 x 64 bf16 box
 constexpr int STAGE = 4 * HALF;           // A: 128 of the tile's rows; B: 128 of its columns
-constexpr int STAGES = 6;
-constexpr int SLAB = 4096;                // an epilogue warp's store buffer
+constexpr int STAGES = 5;
+constexpr int SLAB = 8192;                // an epilogue warp's store buffer
 constexpr int TQ = 4;                     // slots that hand claimed units to the roles
-// Stages of one sum in tensor memory in the products that d topk_w comes from (see above).
-constexpr int CHUNK = 6;
+// Stages of one sum in tensor memory in the products that d topk_w comes from (see above): a
+// token row from an 8-bit checkpoint makes shorter products, which lose less.
+constexpr int CHUNK_E4M3 = 8, CHUNK_BF16 = 6;
 constexpr int STASH = 32 * N_EPI * 2 * 128;   // floats of a CTA's stash: p and u of a unit
 
 // What the plan kernel leaves in the workspace.
@@ -75,7 +80,7 @@ struct GemmArgs {
     // stores: dg, du, hw (32 token rows x 32 of I), rows of dX (32 fp32 x 32), weight gradients
     CUtensorMap gs, us, hs, xs, s1, s3, s2;
     Plan plan;
-    int E, H, I;
+    int E, H, I, chunk;
     const float *wrow;               // [padded rows] slot weights
     float *dwp;                      // [I / 32][padded rows] partial sums of <p, h>
     long long ld_dwp;
@@ -412,6 +417,8 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         else mbar_arrive_cluster(mapa_shared(smem_u32(&tqe[q]), 0));
     };
 
+    if (warp < EPI0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FEW));
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0 && !p.inject) {
@@ -522,7 +529,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                 slot_done(qs);
                 if (++qs == TQ) { qs = 0; qph ^= 1u; }
                 if (un.kind < 0) break;
-                const int chunk = un.kind == P ? CHUNK : un.kb;
+                const int chunk = un.kind == P ? p.chunk : un.kb;
                 for (int part = 0; part < un.parts && good; ++part) {
                     const Tile T = tile_of(un, part);
                     // MN-major where the operand lies with the tile's rows (columns) contiguous
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                     const uint32_t id = idesc_bf16_f32(TM, static_cast<uint32_t>(T.n), amn, bmn);
                     int kb = 0;
                     do {
-                        if (!mbar_wait_cluster(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
+                        if (!mbar_wait(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
                         tc_fence_after();
                         const uint32_t d = tmem + b * TN;
                         const int end = min(kb + chunk, un.kb);
@@ -585,13 +592,15 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                 if (++qs == TQ) { qs = 0; qph ^= 1u; }
             } while (t < n_units);
         }
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_MANY));
         // ---------------------------------------------------------------- epilogue
-        const int q = warp & 3, half = (warp - 2) >> 2;   // lane quarter, half of the columns
+        const int q = warp & 3, half = (warp - EPI0) >> 2;   // lane quarter, half of the columns
         const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
         const int r0 = 128 * static_cast<int>(rank) + 32 * q;   // the warp's first row of a tile
-        unsigned char *slab = slabs + (warp - 2) * SLAB;
+        unsigned char *slab = slabs + (warp - EPI0) * SLAB;
         uint32_t b = 0, tph = 0, qs = 0, qph = 0;
         // a wait by one lane (every lane then observes the phase itself)
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -602,7 +611,10 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
             return good;
         };
         auto sums_ready = [&]() -> bool {
-            const bool good = wait_all(&tfull[b], tph);
+            bool good = true;
+            if (lane == 0) good = mbar_wait(&tfull[b], tph, abort_flag, p.status, tmo);
+            good = __shfl_sync(kFullMask, good, 0);
+            if (good) mbar_try_wait(&tfull[b], tph);
             tc_fence_after();
             return good;
         };
@@ -613,8 +625,16 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
             b ^= 1u;
             if (b == 0) tph ^= 1u;
         };
+        // the slab's halves in turn: the store before the last has read its own
+        uint32_t turn = 0;
+        auto slab_turn = [&](int ln) -> unsigned char * {
+            if (ln == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+            turn ^= 1u;
+            return slab + (turn ? SLAB / 2 : 0);
+        };
         // this thread's stash: p, then u, of its row, float4 i at i * SROW (256 threads side by side)
-        float4 *stash = reinterpret_cast<float4 *>(p.stash + static_cast<size_t>(blockIdx.x) * STASH) + (tid - 64);
+        float4 *stash = reinterpret_cast<float4 *>(p.stash + static_cast<size_t>(blockIdx.x) * STASH) + (tid - 32 * EPI0);
         constexpr int SROW = 32 * N_EPI;
         bool good = true;
         while (good) {
@@ -635,16 +655,16 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
 #pragma unroll
                     for (int i = 0; i < 128; ++i) acc[i] = 0.f;
 #pragma unroll 1
-                    for (int kb = 0; kb < u.kb; kb += CHUNK) {
+                    for (int kb = 0; kb < u.kb; kb += p.chunk) {
                         if (!sums_ready()) { good = false; break; }
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            if (c >= 2 * nc) continue;
-                            float v[16];
+                        for (int c = 0; c < 4; ++c) {
+                            if (c >= nc) continue;
+                            float v[32];
                             __syncwarp();
-                            tmem_ld16(at + b * TN + 16 * c, v);
+                            tmem_ld32(at + b * TN + 32 * c, v);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[16 * c + i] += v[i];
+                            for (int i = 0; i < 32; ++i) acc[32 * c + i] += v[i];
                         }
                         sums_read();
                     }
@@ -666,11 +686,10 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                 for (int c = 0; c < 4; ++c) {
                     if (c >= nc) continue;
                     const float4 *wv = reinterpret_cast<const float4 *>(p.wrow + tok + 32 * c);
-                    uint32_t hw[16];
                     slab_free(lane);
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
-                        uint32_t og[4], ou[4];
+                        uint32_t og[4], ou[4], hw[4];
 #pragma unroll
                         for (int y = 0; y < 8; y += 4) {
                             const int j = i + y;
@@ -691,17 +710,19 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                             og[y / 2 + 1] = f32x2_to_bf16x2(a[3], a[2]);
                             ou[y / 2] = f32x2_to_bf16x2(e[1], e[0]);
                             ou[y / 2 + 1] = f32x2_to_bf16x2(e[3], e[2]);
-                            hw[j / 2] = f32x2_to_bf16x2(hv[1], hv[0]);
-                            hw[j / 2 + 1] = f32x2_to_bf16x2(hv[3], hv[2]);
+                            hw[y / 2] = f32x2_to_bf16x2(hv[1], hv[0]);
+                            hw[y / 2 + 1] = f32x2_to_bf16x2(hv[3], hv[2]);
                         }
                         slab_row64(slab, lane, i / 8, make_uint4(og[0], og[1], og[2], og[3]));
                         slab_row64(slab + 2048, lane, i / 8, make_uint4(ou[0], ou[1], ou[2], ou[3]));
+                        slab_row64(slab + 4096, lane, i / 8, make_uint4(hw[0], hw[1], hw[2], hw[3]));
                     }
                     slab_ready();
                     if (lane == 0 && col < I) {
                         const int t0 = tok + 32 * c;
                         tma_store_3d(&p.gs, slab, t0 & 63, col, t0 >> 6);
                         tma_store_3d(&p.us, slab + 2048, t0 & 63, col, t0 >> 6);
+                        tma_store_3d(&p.hs, slab + 4096, t0 & 63, col, t0 >> 6);
                         slab_commit();
                     }
                     // sum over the warp's 32 columns of I: lane j ends up with token row j
@@ -715,15 +736,6 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                             acc[32 * c + k] = keep + __shfl_xor_sync(kFullMask, send, o);
                         }
                     if (col < I) dwp[32 * c] = acc[32 * c];
-                    slab_free(lane);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        slab_row64(slab, lane, i, make_uint4(hw[4 * i], hw[4 * i + 1], hw[4 * i + 2], hw[4 * i + 3]));
-                    slab_ready();
-                    if (lane == 0 && col < I) {
-                        tma_store_3d(&p.hs, slab, (tok + 32 * c) & 63, col, (tok + 32 * c) >> 6);
-                        slab_commit();
-                    }
                 }
                 // the unit's dg, du and hw are in global memory: tell the group
                 if (lane == 0) {
@@ -742,18 +754,18 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                 if (T.kind == ROWS) {
                     const int col = T.m0 + r0, tok = u.row0 + half * (T.n / 2);
                     const uint32_t at = tm0 + b * TN + static_cast<uint32_t>(half * (T.n / 2));
-                    float *sl = reinterpret_cast<float *>(slab);
 #pragma unroll 1
                     for (int c = 0; c < max(0, min(T.n / 2, u.n0 - half * (T.n / 2))) / 32; ++c) {
                         float v[32];
                         __syncwarp();
                         tmem_ld32(at + 32 * c, v);
-                        slab_free(lane);
+                        unsigned char *buf = slab_turn(lane);
+                        float *sl = reinterpret_cast<float *>(buf);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) sl[i * 32 + lane] = v[i];
                         slab_ready();
-                        if (lane == 0 && col < H) {
-                            tma_store_2d(&p.xs, slab, col, tok + 32 * c);
+                        if (lane == 0) {
+                            if (col < H) tma_store_2d(&p.xs, buf, col, tok + 32 * c);
                             slab_commit();
                         }
                     }
@@ -772,12 +784,12 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = y[i] = 0.f;
                         }
-                        slab_free(lane);
-                        slab_bf16(slab, lane, v, 0);
-                        slab_bf16(slab, lane, y, 4);
+                        unsigned char *buf = slab_turn(lane);
+                        slab_bf16(buf, lane, v, 0);
+                        slab_bf16(buf, lane, y, 4);
                         slab_ready();
-                        if (lane == 0 && T.m0 + r0 < M) {
-                            tma_store_3d(sm, slab, T.n0 + lc, T.m0 + r0, u.g);
+                        if (lane == 0) {
+                            if (T.m0 + r0 < M) tma_store_3d(sm, buf, T.n0 + lc, T.m0 + r0, u.g);
                             slab_commit();
                         }
                     }
@@ -952,6 +964,7 @@ cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned
         return cudaErrorInvalidValue;
     a.plan = plan;
     a.E = E; a.H = H; a.I = I;
+    a.chunk = f.x_scale ? CHUNK_E4M3 : CHUNK_BF16;
     a.wrow = wrow;
     a.dwp = dwp;
     a.ld_dwp = L.rows;
