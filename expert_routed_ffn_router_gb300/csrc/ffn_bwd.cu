@@ -57,6 +57,7 @@ constexpr int STAGE = 4 * HALF;           // A: 128 of the tile's rows; B: 128 o
 constexpr int STAGES = 5;
 constexpr int SLAB = 8192;                // an epilogue warp's store buffer
 constexpr int TQ = 4;                     // slots that hand claimed units to the roles
+constexpr int AHEAD = 24;                 // stages left to load of a unit when the next one is claimed
 // Stages of one sum in tensor memory in the products that d topk_w comes from (see above): a
 // token row from an 8-bit checkpoint makes shorter products, which lose less.
 constexpr int CHUNK_E4M3 = 8, CHUNK_BF16 = 6;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
     unsigned char *ring = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *slabs = ring + STAGES * STAGE;
-    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], drain;
+    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], want, drain;
     __shared__ int tq[TQ][8];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
@@ -313,6 +314,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
             mbar_init(&tqf[q], 1);
             mbar_init(&tqe[q], 2 * N_EPI + 3);   // both epilogues and producers, the MMA issuer
         }
+        mbar_init(&want, 1);
         mbar_init(&drain, 1);
         abort_s = 0;
         fence_mbar_init();
@@ -410,7 +412,10 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
     };
     // Units are claimed from a counter by a warp of the even CTA, in order, and handed to every
     // role of both CTAs through TQ slots (kind -1 ends): the counter's round trip and the search
-    // for the group stay off the producer's thread, whose pause empties the ring.  All of a group's gates come
+    // for the group stay off the producer's thread, whose pause empties the ring.  A unit is
+    // claimed when the one before it has AHEAD stages left to load: claimed as early as the slots
+    // allow, a few units would go to the first clusters alone (one expert of 7168 x 2048, one
+    // token: 176 us, now NEWA).  All of a group's gates come
     // before the tiles that need them, so a cluster that waits holds nothing they need.
     auto slot_done = [&](int q) {
         if (leader) mbar_arrive(&tqe[q]);
@@ -452,6 +457,9 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                     }
                     fence_proxy_async_global();
                 }
+                int left = u.parts * u.kb;           // stages
+                bool asked = !leader;
+                if (!asked && left <= AHEAD) { mbar_arrive(&want); asked = true; }
                 for (int part = 0; part < u.parts && good; ++part) {
                     const Tile T = tile_of(u, part);
                     const int nb = T.n / 2;          // this CTA's columns
@@ -504,6 +512,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                             }
                         }
                         if (++s == STAGES) { s = 0; ph ^= 1u; }
+                        if (--left <= AHEAD && !asked) { mbar_arrive(&want); asked = true; }
                     }
                 }
             }
@@ -572,9 +581,12 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
         // ------------------------------------------------------------------ claims
         if (lane == 0 && leader) {
             uint32_t qs = 0, qph = 0;
+            uint32_t wph = 1;                        // (the first claim waits for nothing)
             int from = 0;
             int t = 0;
             do {
+                if (!mbar_wait(&want, wph, abort_flag, p.status, tmo)) break;
+                wph ^= 1u;
                 if (!mbar_wait_cluster(&tqe[qs], qph ^ 1u, abort_flag, p.status, tmo)) break;
                 t = atomicAdd(p.plan.next, 1);
                 Unit u{};
