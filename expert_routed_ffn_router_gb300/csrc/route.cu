@@ -51,6 +51,11 @@ __device__ __forceinline__ uint32_t order_key(float v)
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
+}
+
 __device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll
@@ -97,6 +102,8 @@ struct RouteArgs {
     const float *bias;      // nullable
     int fp32, T, E, K;
     int softmax, n_group, topk_group, group_top, renorm;
+    int G;           // experts of a group
+    int lane_shift;  // a group fills 2^lane_shift whole lanes; -1: groups and lanes do not align
     int32_t *idx;
     float *w;
 };
@@ -113,6 +120,21 @@ __device__ __forceinline__ int lane_rank(F score, int lane, int n)
     return rank;
 }
 
+// The same of the first n of a warp's values in shared memory (36 of them, kOut past n), which
+// every lane reads four at a time.
+__device__ __forceinline__ int rank_of(const float *f, float mine, int lane, int n)
+{
+    int rank = 0;
+    for (int j = 0; j < n; j += 4) {
+        const float4 o = *reinterpret_cast<const float4 *>(f + j);
+        rank += j < lane ? o.x >= mine : o.x > mine;
+        rank += j + 1 < lane ? o.y >= mine : o.y > mine;
+        rank += j + 2 < lane ? o.z >= mine : o.z > mine;
+        rank += j + 3 < lane ? o.w >= mine : o.w > mine;
+    }
+    return rank;
+}
+
 template <typename F>
 __device__ __forceinline__ void merge2(F &a, F &b, int off)
 {
@@ -125,16 +147,16 @@ __device__ __forceinline__ void merge2(F &a, F &b, int off)
 template <typename F, int NV>
 __device__ __forceinline__ void group_top2(const RouteArgs &a, const F (&v)[NV], int lane, F lowest, F &s1, F &s2)
 {
-    const int G = a.E / a.n_group, per = G / NV;
+    const int G = a.G;
     F x = lowest, y = lowest;
     s1 = s2 = lowest;
-    if (G % NV == 0 && (per & (per - 1)) == 0) {
+    if (a.lane_shift >= 0) {
         // whole lanes hold a group
 #pragma unroll
         for (int i = 0; i < NV; ++i) push2(v[i], x, y);
-        for (int o = 1; o < per; o <<= 1) merge2(x, y, o);
-        s1 = __shfl_sync(kFullMask, x, lane * per & 31);
-        s2 = __shfl_sync(kFullMask, y, lane * per & 31);
+        for (int o = 1; o < 1 << a.lane_shift; o <<= 1) merge2(x, y, o);
+        s1 = __shfl_sync(kFullMask, x, (lane << a.lane_shift) & 31);
+        s2 = __shfl_sync(kFullMask, y, (lane << a.lane_shift) & 31);
         return;
     }
     for (int g = 0; g < a.n_group; ++g) {
@@ -218,8 +240,8 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
 template <int NV>
 __device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, int lane, float bound)
 {
-    const int G = a.E / a.n_group, per = G / NV;
-    if (a.softmax || G % NV || (per & (per - 1))) return 0u;
+    const int per = 1 << a.lane_shift;
+    if (a.softmax || a.lane_shift < 0) return 0u;
     float v1 = -FLT_MAX, v2 = -FLT_MAX, v3 = -FLT_MAX, l1 = 0.f, l2 = 0.f;
     int e1 = 0, e2 = 0;
 #pragma unroll
@@ -253,8 +275,9 @@ __device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, in
     return __ballot_sync(kFullMask, lane < a.n_group && rank < a.topk_group);
 }
 
-template <int NV, bool F32>
-__global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const __grid_constant__ RouteArgs a)
+// FULL: every lane holds NV experts (E == 32 NV).
+template <int NV, bool F32, bool FULL>
+__global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(const __grid_constant__ RouteArgs a)
 {
     __shared__ __align__(16) float cand_f[WPC][36];      // candidates in expert order
     __shared__ int cand_e[WPC][32];
@@ -263,123 +286,137 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const __grid_consta
     if (t >= a.T) return;
     const size_t base = static_cast<size_t>(t) * a.E;
     const int e0 = lane * NV;
-    const int live = a.E - e0;               // experts i < live of this lane exist
+    const int live = FULL ? NV : a.E - e0;   // experts i < live of this lane exist
+    auto has = [&](int i) -> bool { return FULL || i < live; };
 
     float l[NV];
     if (F32 && NV % 4 == 0 && a.E % 4 == 0) {
         const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + base + e0);
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
-            const float4 v = i < live ? src[i / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = has(i) ? src[i / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
             l[i] = v.x; l[(i + 1) % NV] = v.y; l[(i + 2) % NV] = v.z; l[(i + 3) % NV] = v.w;
         }
     } else if (!F32 && NV % 8 == 0 && a.E % 8 == 0) {
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + base + e0);
 #pragma unroll
         for (int i = 0; i < NV; i += 8) {
-            const uint4 v = i < live ? src[i / 8] : make_uint4(0, 0, 0, 0);
+            const uint4 v = has(i) ? src[i / 8] : make_uint4(0, 0, 0, 0);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) l[(i + k) % NV] = k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) l[i] = i < live ? logit_at(a.logits, F32, base + e0 + i) : 0.f;
+        for (int i = 0; i < NV; ++i) l[i] = has(i) ? logit_at(a.logits, F32, base + e0 + i) : 0.f;
     }
     float m = -FLT_MAX, z = 1.f;
     if (a.softmax) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (i < live && l[i] > kMaskedLogit) m = fmaxf(m, l[i]);
+            if (has(i) && l[i] > kMaskedLogit) m = fmaxf(m, l[i]);
         m = warp_max(m);
         z = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) z += i < live && !(l[i] <= kMaskedLogit) ? expf(l[i] - m) : 0.f;
+        for (int i = 0; i < NV; ++i) z += has(i) && !(l[i] <= kMaskedLogit) ? expf(l[i] - m) : 0.f;
         z = warp_sum(z);
     }
     // What the experts are ranked by.  No bias and no sum of two scores: the logits, exactly.
     const bool scored = a.bias || (a.n_group > 1 && a.group_top == 2);
-    float f[NV], bound = 0.f;
-    if (scored) {
-        float bv[NV];
-        if (a.bias && NV % 4 == 0 && a.E % 4 == 0) {
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    auto rank_by = [&](float lg, float bv) -> float {
+        if (!scored)                         // (-0 ranks as +0, NaN as the lowest)
+            return fmaxf(lg <= kMaskedLogit ? kMaskedRankLogit : lg + 0.f, kMaskedRankLogit);
+        const float s = (a.softmax ? __expf(lg - m) * inv : rough_sigmoid(lg)) + bv;
+        return lg <= kMaskedLogit ? kMaskedRank : fmaxf(s, kLeastRank);
+    };
+    // Error of a score: the sigmoid's is below 4e-7 (exp2, its argument's rounding, the
+    // reciprocal), the softmax's below 4e-6 of the largest, which is 1 / z (also the rounding of
+    // l - m, up to 1024 sums).  The rounding of s + bias comes to it: 1.5e-7 |sel|.
+    const float error = scored ? (a.softmax ? 4e-6f * inv : 4e-7f) : 0.f;
+    float f[NV];
+    if (a.bias && NV % 4 == 0 && a.E % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < NV; i += 4) {
-                const float4 x = i < live ? *reinterpret_cast<const float4 *>(a.bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                bv[i] = x.x; bv[(i + 1) % NV] = x.y; bv[(i + 2) % NV] = x.z; bv[(i + 3) % NV] = x.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) bv[i] = a.bias && i < live ? a.bias[e0 + i] : 0.f;
+        for (int i = 0; i < NV; i += 4) {
+            const float4 x = has(i) ? *reinterpret_cast<const float4 *>(a.bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            f[i] = rank_by(l[i], x.x);
+            f[(i + 1) % NV] = rank_by(l[(i + 1) % NV], x.y);
+            f[(i + 2) % NV] = rank_by(l[(i + 2) % NV], x.z);
+            f[(i + 3) % NV] = rank_by(l[(i + 3) % NV], x.w);
         }
-        const float inv = z == 0.f ? 0.f : 1.f / z;
-        float most = 0.f;                    // largest |sel|
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const float s = (a.softmax ? __expf(l[i] - m) * inv : rough_sigmoid(l[i])) + bv[i];
-            f[i] = l[i] <= kMaskedLogit ? kMaskedRank : fmaxf(s, kLeastRank);
-            if (f[i] > kLeastRank && f[i] < INFINITY) most = fmaxf(most, fabsf(f[i]));
-        }
-        // Error of a score: the sigmoid's is below 4e-7 (exp2, its argument's rounding, the
-        // reciprocal), the softmax's below 4e-6 of the largest, which is 1 / z (also the rounding
-        // of l - m, up to 1024 sums).  Then the rounding of s + bias.
-        bound = (a.softmax ? 4e-6f * inv : 4e-7f) +
-                1.5e-7f * __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(most)));
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)     // (-0 ranks as +0, NaN as the lowest)
-            f[i] = fmaxf(l[i] <= kMaskedLogit ? kMaskedRankLogit : l[i] + 0.f, kMaskedRankLogit);
+        for (int i = 0; i < NV; ++i) f[i] = rank_by(l[i], a.bias && has(i) ? a.bias[e0 + i] : 0.f);
     }
-    bool sure = true, out = live <= 0;       // out: nothing of this lane is in the running
-    float x;                                 // the lane's maximum
-    const int G = a.E / a.n_group;
-    if (a.n_group > 1) {
-        float s1, s2;
+    if (!FULL) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (i >= live) f[i] = kOut;
+            if (!has(i)) f[i] = kOut;
+    }
+    bool sure = true, out = false;           // out: nothing of this lane is in the running
+    if (a.n_group > 1) {
+        float s1, s2;
         group_top2<float, NV>(a, f, lane, -FLT_MAX, s1, s2);
         const float score = a.group_top == 2 ? s1 + s2 : s1;
-        const int rank = lane_rank(score, lane, a.n_group);      // (every lane takes part)
-        const bool mine = lane < a.n_group, in = mine && rank < a.topk_group;
-        uint32_t kept = __ballot_sync(kFullMask, in);
+        const bool mine = lane < a.n_group;
+        cand_f[wy][lane] = mine ? score : kOut;
+        __syncwarp();
+        const int rank = rank_of(cand_f[wy], score, lane, a.n_group);
+        __syncwarp();
+        uint32_t kept = __ballot_sync(kFullMask, mine && rank < a.topk_group);
         if (scored && a.topk_group < a.n_group) {
             const float lo = __shfl_sync(kFullMask, score, __ffs(__ballot_sync(kFullMask, mine && rank == a.topk_group - 1)) - 1);
             const float hi = __shfl_sync(kFullMask, score, __ffs(__ballot_sync(kFullMask, mine && rank == a.topk_group)) - 1);
+            // (a score is the sum of two values, each within the bound at its size)
+            const float bound = error + 1.5e-7f * fmaxf(fabsf(lo), fabsf(hi));
             sure = lo - hi > 4.f * bound;
             if (!sure) {
                 kept = groups_fp64<NV>(a, base, lane, bound);
                 sure = kept != 0u;
             }
         }
-        if (G % NV == 0) {
-            out = out || !((kept >> (e0 / G)) & 1u);
+        if (a.lane_shift >= 0) {
+            out = live <= 0 || !((kept >> (lane >> a.lane_shift)) & 1u);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (i < live && !((kept >> ((e0 + i) / G)) & 1u)) f[i] = kOut;
+                if (has(i) && !((kept >> ((e0 + i) / a.G)) & 1u)) f[i] = kOut;
         }
     }
     int expert = 0, place = 32;              // this lane's expert and its place in the order
+    float lg = 0.f;                          // ... and its logit
     if (sure) {
-        x = kOut;
+        float x = kOut;                      // the lane's maximum
+        if (!out)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) x = fmaxf(x, i < live ? f[i] : kOut);
-        if (out) x = kOut;
-        // K-th largest of the lanes' maxima (bitonic sort, descending)
+            for (int i = 0; i < NV; ++i) x = fmaxf(x, f[i]);
+        // A value that K lanes' maxima reach (so K experts do), close to the K-th largest of them:
+        // six halvings between the smallest and the largest maximum.
+        float least = -FLT_MAX;
+        const uint32_t some = __ballot_sync(kFullMask, x > kOut);
+        const float top = key_value(__reduce_max_sync(kFullMask, order_key(x)));
+        if (__popc(some) >= a.K) {
+            float lo = key_value(__reduce_min_sync(kFullMask, x > kOut ? order_key(x) : 0xffffffffu)), hi = top;
 #pragma unroll
-        for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-            for (int j = k >> 1; j > 0; j >>= 1) {
-                const float o = __shfl_xor_sync(kFullMask, x, j);
-                x = ((lane & k) == 0) == ((lane & j) == 0) ? fmaxf(x, o) : fminf(x, o);
+            for (int r = 0; r < 6; ++r) {
+                const float mid = 0.5f * lo + 0.5f * hi;
+                const bool enough = __popc(__ballot_sync(kFullMask, x >= mid)) >= a.K;
+                lo = enough ? mid : lo;
+                hi = enough ? hi : mid;
             }
-        float least = __shfl_sync(kFullMask, x, a.K - 1);
-        if (a.bias) least -= 2.f * bound;
-        least = fmaxf(least, -FLT_MAX);      // (fewer lanes than K hold anything)
-        int n = 0;
+            least = lo;
+        }
+        float bound = 0.f;
+        if (a.bias) {
+            bound = error + 1.5e-7f * fmaxf(fabsf(top), fabsf(fmaxf(least, kLeastRank)));
+            least -= 2.f * bound;
+        }
+        least = fmaxf(least, -FLT_MAX);
+        uint32_t chosen = 0u;
+        if (!out)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) n += !out && i < live && f[i] >= least;
+            for (int i = 0; i < NV; ++i) chosen |= f[i] >= least ? 1u << i : 0u;
+        const int n = __popc(chosen);
         int at = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -389,28 +426,21 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const __grid_consta
         const int C = __shfl_sync(kFullMask, at, 31);
         if (C <= 32) {
             at -= n;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (!out && i < live && f[i] >= least) {
-                    cand_f[wy][at] = f[i];
-                    cand_e[wy][at] = e0 + i;
-                    ++at;
-                }
-            if (lane < 4) cand_f[wy][C + lane] = kOut;
+            while (chosen) {
+                cand_e[wy][at++] = e0 + __ffs(chosen) - 1;
+                chosen &= chosen - 1u;
+            }
             __syncwarp();
             float mine = kOut;
             if (lane < C) {
-                mine = cand_f[wy][lane];
                 expert = cand_e[wy][lane];
+                lg = logit_at(a.logits, F32, base + expert);
+                mine = rank_by(lg, a.bias ? a.bias[expert] : 0.f);     // (the value ranked by above)
             }
-            int rank = 0;
-            for (int j = 0; j < C; j += 4) {
-                const float4 o = *reinterpret_cast<const float4 *>(&cand_f[wy][j]);
-                rank += j < lane ? o.x >= mine : o.x > mine;
-                rank += j + 1 < lane ? o.y >= mine : o.y > mine;
-                rank += j + 2 < lane ? o.z >= mine : o.z > mine;
-                rank += j + 3 < lane ? o.w >= mine : o.w > mine;
-            }
+            cand_f[wy][lane] = mine;
+            if (lane < 4) cand_f[wy][32 + lane] = kOut;
+            __syncwarp();
+            const int rank = rank_of(cand_f[wy], mine, lane, C);
             place = lane < C ? rank : 32;
             if (a.bias) {
                 // neighbours in the order that the bound does not tell apart (masked experts
@@ -426,8 +456,7 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const __grid_consta
                     } else {
                         double d = -DBL_MAX;
                         if (lane < C) {
-                            const double x64 = static_cast<double>(logit_at(a.logits, F32, base + expert));
-                            d = 1.0 / (1.0 + exp(-x64)) + static_cast<double>(a.bias[expert]);
+                            d = 1.0 / (1.0 + exp(-static_cast<double>(lg))) + static_cast<double>(a.bias[expert]);
                             d = mine <= kMaskedRank ? kMaskedSel : fmax(d, 0.1 * kMaskedSel);
                         }
                         const int r64 = lane_rank(d, lane, C);
@@ -443,27 +472,28 @@ __global__ void __launch_bounds__(32 * WPC) route_fwd_kernel(const __grid_consta
                 int e = 1 << 30;
 #pragma unroll
                 for (int i = NV - 1; i >= 0; --i)
-                    if (!out && i < live && f[i] >= best && f[i] > kOut) { best = f[i]; e = e0 + i; }
-                const uint32_t key = order_key(best), top = __reduce_max_sync(kFullMask, key);
-                const int win = __reduce_min_sync(kFullMask, key == top ? e : 1 << 30);
+                    if (!out && f[i] >= best && f[i] > kOut) { best = f[i]; e = e0 + i; }
+                const uint32_t key = order_key(best), most = __reduce_max_sync(kFullMask, key);
+                const int win = __reduce_min_sync(kFullMask, key == most ? e : 1 << 30);
                 if (lane == r) { expert = win; place = r; }
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if (e0 + i == win) f[i] = kOut;
             }
+            if (place < a.K) lg = logit_at(a.logits, F32, base + expert);
         }
     }
     if (!sure) {
         expert = select_fp64<NV>(a, base, lane);
         place = lane;
+        if (place < a.K) lg = logit_at(a.logits, F32, base + expert);
     }
     // weights: the selected scores (a masked expert's is 0), over their sum
     const bool on = place < a.K;
     float s = 0.f;
     if (on) {
-        float lj = logit_at(a.logits, F32, base + expert);
-        if (lj <= kMaskedLogit) lj = -INFINITY;
-        s = !a.softmax ? sigmoid(lj) : (z == 0.f ? 0.f : expf(lj - m) / z);
+        if (lg <= kMaskedLogit) lg = -INFINITY;
+        s = !a.softmax ? sigmoid(lg) : (z == 0.f ? 0.f : expf(lg - m) / z);
     }
     if (a.renorm) {
         const float sum = warp_sum(s);
@@ -551,11 +581,18 @@ __global__ void __launch_bounds__(32 * WPC) route_bwd_kernel(const RouteBwdArgs 
 }
 
 template <int NV>
-cudaError_t fwd(const RouteArgs &a, cudaStream_t s)
+cudaError_t fwd(RouteArgs a, cudaStream_t s)
 {
+    const int per = a.G / NV;
+    a.lane_shift = -1;
+    if (a.G % NV == 0 && (per & (per - 1)) == 0)
+        for (a.lane_shift = 0; 1 << a.lane_shift < per;) ++a.lane_shift;
     const dim3 grid((a.T + WPC - 1) / WPC), block(32, WPC);
-    return a.fp32 ? launch_pdl(route_fwd_kernel<NV, true>, grid, block, 0, s, 1, a)
-                  : launch_pdl(route_fwd_kernel<NV, false>, grid, block, 0, s, 1, a);
+    if (a.E == 32 * NV)
+        return a.fp32 ? launch_pdl(route_fwd_kernel<NV, true, true>, grid, block, 0, s, 1, a)
+                      : launch_pdl(route_fwd_kernel<NV, false, true>, grid, block, 0, s, 1, a);
+    return a.fp32 ? launch_pdl(route_fwd_kernel<NV, true, false>, grid, block, 0, s, 1, a)
+                  : launch_pdl(route_fwd_kernel<NV, false, false>, grid, block, 0, s, 1, a);
 }
 
 }  // namespace
@@ -564,7 +601,7 @@ cudaError_t launch_route(const void *logits, int fp32, const float *bias, int T,
                          const RoutingOpts &ro, int32_t *idx, float *w, cudaStream_t s)
 {
     const RouteArgs a{logits, bias, fp32, T, E, K, ro.scoring, ro.n_group, ro.topk_group, ro.group_top,
-                      ro.renorm, idx, w};
+                      ro.renorm, E / ro.n_group, -1, idx, w};
     if (E <= 32) return fwd<1>(a, s);
     if (E <= 64) return fwd<2>(a, s);
     if (E <= 128) return fwd<4>(a, s);
