@@ -76,7 +76,14 @@ __device__ __forceinline__ float logit_at(const void *p, int fp32, size_t i)
                 : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
 }
 
-__device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+__device__ __forceinline__ float fast_rcp(float v)      // within one step (0 for +inf, +inf for 0)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float sigmoid(float l) { return fast_rcp(1.f + expf(-l)); }
 
 __device__ __forceinline__ void push2(float v, float &a, float &b)
 {
@@ -90,12 +97,7 @@ __device__ __forceinline__ void push2(double v, double &a, double &b)
 }
 
 // sigmoid from the hardware exp2 and reciprocal, for the selection (its error is in the bound)
-__device__ __forceinline__ float rough_sigmoid(float l)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-l)));
-    return r;
-}
+__device__ __forceinline__ float rough_sigmoid(float l) { return fast_rcp(1.f + __expf(-l)); }
 
 struct RouteArgs {
     const void *logits;
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
     }
     // What the experts are ranked by.  No bias and no sum of two scores: the logits, exactly.
     const bool scored = a.bias || (a.n_group > 1 && a.group_top == 2);
-    const float inv = z == 0.f ? 0.f : 1.f / z;
+    const float inv = a.softmax && z != 0.f ? fast_rcp(z) : 0.f;
     auto rank_by = [&](float lg, float bv) -> float {
         if (!scored)                         // (-0 ranks as +0, NaN as the lowest)
             return fmaxf(lg <= kMaskedLogit ? kMaskedRankLogit : lg + 0.f, kMaskedRankLogit);
@@ -493,11 +495,11 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
     float s = 0.f;
     if (on) {
         if (lg <= kMaskedLogit) lg = -INFINITY;
-        s = !a.softmax ? sigmoid(lg) : (z == 0.f ? 0.f : expf(lg - m) / z);
+        s = a.softmax ? expf(lg - m) * inv : sigmoid(lg);
     }
     if (a.renorm) {
         const float sum = warp_sum(s);
-        s = sum == 0.f ? 0.f : s / sum;
+        s = sum < 1e-30f ? (sum == 0.f ? 0.f : s / sum) : s * fast_rcp(sum);
     }
     if (on) {
         a.idx[static_cast<size_t>(t) * a.K + place] = expert;
