@@ -9,7 +9,7 @@
 // Bound by memory: 3 + 1/128 bytes an element each way.  8 lanes hold a block, 16 columns (32
 // bytes of bf16, 16 of E4M3) a lane, so its maximum takes three shuffles and every access is
 // 16 bytes wide (8 columns a lane, with 8-byte accesses to the bytes, measured 129 us for 16384
-// rows of 7168 packed and taken back; this: NEWT).
+// rows of 7168 packed and taken back; this: 107.5 us, 6.57 TB/s).
 #include "common.cuh"
 #include "kernels.h"
 

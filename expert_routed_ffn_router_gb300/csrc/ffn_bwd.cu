@@ -14,21 +14,40 @@
 //   plan     padded row offsets of the groups (multiples of 64 rows), offsets checked
 //   gather   the rows of X (taken back from 8 bits) and dY in padded group order, bf16; the
 //            rows up to the next multiple of 64 are zeros, so no product needs a mask
-//   gates    three products per tile in tensor memory (g, u, p), the formulas above in the
-//            epilogue; writes dg, du, hw (bf16) and partial sums of <p, h>
-//   grads    dg W1^T + du W3^T (fp32 rows) and the three weight gradients, one tile list
+//   products one persistent launch over a list of units:
+//     gates   a tile of 256 columns of I x up to 256 token rows: p, u and g one after the other
+//             in tensor memory, the formulas above in the epilogue; dg, du, hw (bf16, in blocks
+//             of 64 token rows: [rows / 64][I][64]) and partial sums of <p, h>
+//     rows    dg W1^T + du W3^T: tiles of 256 columns of H x up to 256 token rows, fp32
+//     dW1, dW3, dW2   tiles of 256 x 256, the expert's padded rows as the depth
 //   finish   dX and d topk_w: sums over the slots, over the partials, in a fixed order
 // No atomics on results: they repeat bit for bit.
 //
-// Rounding.  dg, du and hw are operands of bf16 products and are rounded to bf16 once each;
-// products are summed in fp32 (tensor memory), the rows of dX stay fp32 until their sum over
-// the slots is rounded.  d topk_w is fp32 throughout.
+// Rounding.  dg, du and hw are operands of bf16 products and are rounded to bf16 once each; the
+// rows of dX stay fp32 until their sum over the slots is rounded.  (Stored in bf16, they would
+// add a third rounding to dX's two.)
 //
-// Tiles.  Clusters of two CTAs issue 2-SM MMAs of M = 256.  "gates": 256 token rows x 128
-// columns of I, 3 x 128 columns of tensor memory.  "grads": 256 x 256, two buffers of 256
-// columns.  Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (even CTA), warps 2..9
-// epilogue (two per lane quarter, each half of the columns).  Tiles are dealt to the clusters
-// in turn; every role walks the same list.
+// d topk_w is fp32, and the tensor core's sums are not quite: at every MMA (16 products) it cuts
+// the sum towards zero, so that a sum of n MMAs comes out 1 to 1.5 n 2^-26 short (7e-6 at a depth
+// of 7168), and <p, h> inherits that three times.  The sums of p, u and g therefore leave
+// tensor memory every few stages and are continued in fp32 registers (two buffers in turn):
+// d topk_w is then off by 5 to 9e-7, and a batch of 4096 tokens takes 6.0 ms; without, 1.3e-5
+// and 5.7 ms.
+//
+// Tiles.  Clusters of two CTAs issue 2-SM MMAs of M = 256: the weights' columns (or rows) are the
+// MMA's rows, the token rows its columns, N = 64 .. 256, so a group's last tile costs what it
+// holds.  (Token rows as M, in tiles of 256, multiplied 11% more zeros at 1024 rows a group.)
+// The epilogue of the gates has a row of I per lane and token rows in its registers: dg, du and
+// hw are stored as they lie there, and read as MN- or K-major operands.
+// Roles per CTA: warp 0 TMA producer (5 stages of 32 KB), warp 1 MMA issuer (even CTA), warp 2
+// claims units (even CTA), warps 4..11 epilogue (two per lane quarter, each half of the
+// columns).  A weight gradient's tiles are stored by TMA from 4 KB slabs: whole 128-byte lines.
+// (Plain 16-byte stores of rows: 1.55 ms for rows and weight gradients of 32 tokens, slabs 0.94.)
+//
+// What bounds it.  Many rows an expert: the tensor cores (19 experts of 1024 rows, 7168 x 2048:
+// 1615 TFLOP/s in this launch; measured peak 1936 in a burst, 1713 sustained).  Few rows: memory
+// -- the gates stream the weights at 6.9 TB/s, the weight gradients are written at 4.5 TB/s (a
+// plain fill reaches 4.0), W1 and W3 are read twice.
 //
 // Every wait is bounded as in ffn_tc.cu (MOE_ERR_DEVICE_TIMEOUT in the status word).
 #include <cuda.h>
@@ -415,7 +434,7 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
     // for the group stay off the producer's thread, whose pause empties the ring.  A unit is
     // claimed when the one before it has AHEAD stages left to load: claimed as early as the slots
     // allow, a few units would go to the first clusters alone (one expert of 7168 x 2048, one
-    // token: 176 us, now NEWA).  All of a group's gates come
+    // token: 176 us, now 161).  All of a group's gates come
     // before the tiles that need them, so a cluster that waits holds nothing they need.
     auto slot_done = [&](int q) {
         if (leader) mbar_arrive(&tqe[q]);
@@ -550,6 +569,9 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                     const uint32_t id = idesc_bf16_f32(TM, static_cast<uint32_t>(T.n), amn, bmn);
                     int kb = 0;
                     do {
+                        // (what this orders is tensor memory, by the tcgen05 fences on both
+                        // sides: an acquire of wider scope, 3.24 instead of 3.13 ms for 19 x
+                        // 1024 rows, would add nothing)
                         if (!mbar_wait(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
                         tc_fence_after();
                         const uint32_t d = tmem + b * TN;

@@ -8,18 +8,22 @@
 //   group score (sum of the 1 or 2 largest sel), the K largest sel among their experts,
 //   equal values by index; w = s / sum of the selected s, or s.
 //
-// One warp per token, NV consecutive experts a lane.  Selection without a loop over K: the
-// K-th largest of the 32 lanes' maxima bounds the K-th largest value from below, so only the
-// values at or above it (a dozen for K = 8) are candidates; they go to one lane each, in
-// expert order, and every lane counts the candidates ahead of its own.  (Taking the maximum K
+// One warp per token, NV consecutive experts a lane.  Selection without a loop over K: a value
+// that K of the 32 lanes' maxima reach (six halvings from their range come close to the K-th
+// largest) is reached by K experts, so only the values at or above it, a dozen for K = 8, are
+// candidates; they go to one lane each, in expert order, and every lane counts the candidates
+// ahead of its own.  (Taking the maximum K
 // times measured 26.6 us for 16384 tokens of 256 experts, K = 8, without groups or bias; this
-// NEWT us.)  More than 32 candidates (many equal values) take that loop.
+// 10.1 us.)  More than 32 candidates (many equal values) take that loop.
 //
 // The selection is exact: without a bias sel is ordered as the logits are, and those are
 // compared as they stand.  Otherwise sel is held in fp32 with a bound on its error; the
 // candidates reach down by twice that bound, and where two of them are closer than it, they
 // are evaluated again in fp64, one a lane (a softmax, or group scores too close: the whole
 // row, rare).
+//
+// The batch above with 8 groups (4 kept, two values each) and a bias takes 19 us: about 800
+// instructions a token, where its bytes would take 2.6 us.  Two tokens take the launch's time.
 //
 // Gradient (D = sum_k w_k dw_k over the selected):
 //   sigmoid, renormalised  dl_j = w_j (1 - s_j) (dw_j - D)
@@ -193,10 +197,11 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFullMask, z, o);
     }
+    const double inv = a.softmax ? 1.0 / z : 0.0;
     for (int i = 0; i < NV; ++i) {
         const int e = lane * NV + i;
         const bool on = v[i] > -INFINITY;
-        double s = a.softmax ? exp(v[i] - m) / z : 1.0 / (1.0 + exp(-v[i]));
+        double s = a.softmax ? exp(v[i] - m) * inv : 1.0 / (1.0 + exp(-v[i]));
         if (a.bias && e < a.E) s += static_cast<double>(a.bias[e]);
         // (a bias of -inf ranks above a mask, and every entry stays above what is taken out)
         v[i] = e >= a.E ? -DBL_MAX : (on && s == s ? fmax(s, 0.1 * kMaskedSel) : kMaskedSel);
@@ -235,13 +240,35 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
     return mine;
 }
 
-// The groups kept (a bit each), by scores in fp64 of every lane's two largest values (sel within
-// `bound`): where lanes hold whole groups, the score is a sigmoid and no lane's third value
-// comes close to its second.  0 where that does not hold.  (Out of line, on values of its own:
+// The groups kept (a bit each), by scores in fp64.  With a bias, of every lane's two largest
+// values (sel within `bound`), where lanes hold whole groups, the score is a sigmoid and no
+// lane's third value comes close to its second; 0 where that does not hold.  (Out of line, on values of its own:
 // it is rare, and arrays handed to it would keep the caller's in local memory.)
 template <int NV>
 __device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, int lane, float bound)
 {
+    if (!a.bias) {
+        // the logits order a group's values exactly: its two largest logits, then their scores
+        // (a softmax's up to a factor)
+        float l[NV], m = -FLT_MAX, s1, s2;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane * NV + i;
+            l[i] = e < a.E ? logit_at(a.logits, a.fp32, base + e) : kOut;
+            if (e < a.E) l[i] = fmaxf(l[i] <= kMaskedLogit ? kMaskedRankLogit : l[i], kMaskedRankLogit);
+            m = fmaxf(m, l[i]);
+        }
+        m = warp_max(m);
+        group_top2<float, NV>(a, l, lane, -FLT_MAX, s1, s2);
+        auto score = [&](float x) -> double {
+            if (!(x > kMaskedLogit)) return kMaskedSel;
+            const double d = static_cast<double>(x);
+            return a.softmax ? exp(d - static_cast<double>(m)) : 1.0 / (1.0 + exp(-d));
+        };
+        const double two = score(s1) + (a.group_top == 2 ? score(s2) : 0.0);
+        const int rank = lane_rank(two, lane, a.n_group);
+        return __ballot_sync(kFullMask, lane < a.n_group && rank < a.topk_group);
+    }
     const int per = 1 << a.lane_shift;
     if (a.softmax || a.lane_shift < 0) return 0u;
     float v1 = -FLT_MAX, v2 = -FLT_MAX, v3 = -FLT_MAX, l1 = 0.f, l2 = 0.f;
@@ -323,32 +350,38 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
         for (int i = 0; i < NV; ++i) z += has(i) && !(l[i] <= kMaskedLogit) ? expf(l[i] - m) : 0.f;
         z = warp_sum(z);
     }
-    // What the experts are ranked by.  No bias and no sum of two scores: the logits, exactly.
+    // What the experts are ranked by: sel where there is a bias, else the logits, exactly.  The
+    // groups are by sums of two scores even then.
     const bool scored = a.bias || (a.n_group > 1 && a.group_top == 2);
     const float inv = a.softmax && z != 0.f ? fast_rcp(z) : 0.f;
-    auto rank_by = [&](float lg, float bv) -> float {
-        if (!scored)                         // (-0 ranks as +0, NaN as the lowest)
-            return fmaxf(lg <= kMaskedLogit ? kMaskedRankLogit : lg + 0.f, kMaskedRankLogit);
+    auto by_logit = [&](float lg) -> float {     // (-0 ranks as +0, NaN as the lowest)
+        return fmaxf(lg <= kMaskedLogit ? kMaskedRankLogit : lg + 0.f, kMaskedRankLogit);
+    };
+    auto by_score = [&](float lg, float bv) -> float {
         const float s = (a.softmax ? __expf(lg - m) * inv : rough_sigmoid(lg)) + bv;
         return lg <= kMaskedLogit ? kMaskedRank : fmaxf(s, kLeastRank);
     };
     // Error of a score: the sigmoid's is below 4e-7 (exp2, its argument's rounding, the
-    // reciprocal), the softmax's below 4e-6 of the largest, which is 1 / z (also the rounding of
-    // l - m, up to 1024 sums).  The rounding of s + bias comes to it: 1.5e-7 |sel|.
-    const float error = scored ? (a.softmax ? 4e-6f * inv : 4e-7f) : 0.f;
+    // reciprocal).  The softmax's largest score is 1 / z; a score e^-x / z is off by 4 steps and
+    // 2 x steps of 2^-24 of itself, and all by what z is: NV + 6 roundings of its sum and 3 of
+    // its terms.  The rounding of s + bias comes to it: 1.5e-7 |sel|.
+    const float error = scored ? (a.softmax ? (9e-7f + 6e-8f * NV) * inv : 4e-7f) : 0.f;
     float f[NV];
     if (a.bias && NV % 4 == 0 && a.E % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
             const float4 x = has(i) ? *reinterpret_cast<const float4 *>(a.bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-            f[i] = rank_by(l[i], x.x);
-            f[(i + 1) % NV] = rank_by(l[(i + 1) % NV], x.y);
-            f[(i + 2) % NV] = rank_by(l[(i + 2) % NV], x.z);
-            f[(i + 3) % NV] = rank_by(l[(i + 3) % NV], x.w);
+            f[i] = by_score(l[i], x.x);
+            f[(i + 1) % NV] = by_score(l[(i + 1) % NV], x.y);
+            f[(i + 2) % NV] = by_score(l[(i + 2) % NV], x.z);
+            f[(i + 3) % NV] = by_score(l[(i + 3) % NV], x.w);
         }
+    } else if (scored) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) f[i] = by_score(l[i], a.bias && has(i) ? a.bias[e0 + i] : 0.f);
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) f[i] = rank_by(l[i], a.bias && has(i) ? a.bias[e0 + i] : 0.f);
+        for (int i = 0; i < NV; ++i) f[i] = by_logit(l[i]);
     }
     if (!FULL) {
 #pragma unroll
@@ -376,6 +409,10 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
                 kept = groups_fp64<NV>(a, base, lane, bound);
                 sure = kept != 0u;
             }
+        }
+        if (scored && !a.bias) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) f[i] = has(i) ? by_logit(l[i]) : kOut;
         }
         if (a.lane_shift >= 0) {
             out = live <= 0 || !((kept >> (lane >> a.lane_shift)) & 1u);
@@ -407,6 +444,29 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
                 hi = enough ? hi : mid;
             }
             least = lo;
+        } else {
+            // fewer lanes than K hold anything (few groups kept): the experts themselves
+            const float floor_rank = a.bias ? kLeastRank : kMaskedRankLogit;
+            uint32_t low = 0xffffffffu;
+            int some_n = 0;
+            if (!out)
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (f[i] > floor_rank) { low = min(low, order_key(f[i])); ++some_n; }
+            if (static_cast<int>(__reduce_add_sync(kFullMask, some_n)) >= a.K) {
+                float lo = key_value(__reduce_min_sync(kFullMask, low)), hi = top;
+                for (int r = 0; r < 8; ++r) {
+                    const float mid = 0.5f * lo + 0.5f * hi;
+                    int n = 0;
+                    if (!out)
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) n += f[i] >= mid;
+                    const bool enough = static_cast<int>(__reduce_add_sync(kFullMask, n)) >= a.K;
+                    lo = enough ? mid : lo;
+                    hi = enough ? hi : mid;
+                }
+                least = lo;
+            }
         }
         float bound = 0.f;
         if (a.bias) {
@@ -437,7 +497,7 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
             if (lane < C) {
                 expert = cand_e[wy][lane];
                 lg = logit_at(a.logits, F32, base + expert);
-                mine = rank_by(lg, a.bias ? a.bias[expert] : 0.f);     // (the value ranked by above)
+                mine = a.bias ? by_score(lg, a.bias[expert]) : by_logit(lg);     // (as above)
             }
             cand_f[wy][lane] = mine;
             if (lane < 4) cand_f[wy][32 + lane] = kOut;
@@ -454,7 +514,22 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
                 const bool close = mine > kLeastRank && next > kLeastRank && !(mine - next > 2.f * bound);
                 if (__any_sync(kFullMask, close)) {
                     if (a.softmax) {
-                        sure = false;
+                        // z is known to (NV + 9) 2^-24 of it, so differences of the scores are
+                        // to as much of themselves; closer than that, the whole row
+                        double q = 0.0, d = -DBL_MAX;
+                        if (lane < C) {
+                            q = mine <= kMaskedRank ? 0.0 : exp(static_cast<double>(lg) - static_cast<double>(m)) / static_cast<double>(z);
+                            d = mine <= kMaskedRank ? kMaskedSel : fmax(q + static_cast<double>(a.bias[expert]), 0.1 * kMaskedSel);
+                        }
+                        int r64 = 0;
+                        bool tie = false;
+                        for (int h = 0; h < C; ++h) {
+                            const double od = __shfl_sync(kFullMask, d, h), oq = __shfl_sync(kFullMask, q, h);
+                            r64 += od > d || (od == d && h < lane);
+                            tie = tie || (h != lane && fabs(od - d) <= (5e-7 + 1e-7 * NV) * fabs(oq - q) && oq != q);
+                        }
+                        if (lane < C) place = r64;
+                        sure = !__any_sync(kFullMask, lane < C && (tie || !(q == q)));
                     } else {
                         double d = -DBL_MAX;
                         if (lane < C) {

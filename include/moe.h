@@ -41,7 +41,7 @@
  *     returns a negative moe_status_t and has no effect.  A failing launch returns
  *     MOE_ERR_CUDA.  Conditions found on the device (a bounded wait that ran out, an
  *     expert index outside [0, E) given to moe_dispatch, group offsets outside [0, rows]
- *     given to moe_expert_ffn) are recorded in the workspace's status word and never lead
+ *     given to moe_expert_ffn or moe_expert_ffn_backward) are recorded in the workspace's status word and never lead
  *     to an access out of bounds; read them with moe_read_status().
  *   - Supported shapes: 1 <= E <= 1024, 1 <= K <= min(E, 32), H and I multiples of 64,
  *     T >= 0 (T == 0 enqueues nothing and returns MOE_OK), T*K < 2^31.
@@ -141,8 +141,8 @@ int moe_read_status(void *ws, void *stream);
 
 /* Debugging hook: with on = 1, every later call that records device-side conditions in a
  * workspace status word (moe_router_topk, moe_router_topk_ex, moe_dispatch,
- * moe_expert_ffn, moe_layer_forward, moe_layer_forward_ex, moe_layer_forward_fp8)
- * synchronises its stream after enqueueing its work and returns that word, read and reset
+ * moe_expert_ffn, moe_layer_forward, moe_layer_forward_ex, moe_layer_forward_fp8,
+ * moe_layer_norm_backward, moe_expert_ffn_backward) synchronises its stream after enqueueing its work and returns that word, read and reset
  * as by moe_read_status, in place of MOE_OK -- except for an empty batch and inside a stream
  * capture (a capture cannot be synchronised).  on = 0 (the default) restores the
  * asynchronous calls.  Process-wide; not for production use: it serialises the host with
@@ -150,10 +150,10 @@ int moe_read_status(void *ws, void *stream);
 void moe_debug_set_sync_status(int on);
 
 /* Testing hook: sets the limit of the bounded device-side waits of the tensor-core FFN
- * kernels (0 restores the default of one second) and, with inject_stall = 1, makes their
+ * kernels (forward and backward) (0 restores the default of one second) and, with inject_stall = 1, makes their
  * TMA producer skip its work so that the waits run out and MOE_ERR_DEVICE_TIMEOUT is
- * recorded in the status word (no fault, no hang).  Affects later moe_expert_ffn and
- * moe_layer_forward calls of the process; not for production use. */
+ * recorded in the status word (no fault, no hang).  Affects later moe_expert_ffn,
+ * moe_expert_ffn_backward and moe_layer_forward calls of the process; not for production use. */
 void moe_debug_set_wait_limit(unsigned long long limit_ns, int inject_stall);
 
 /* Profiling hook: with `events` pointing at n >= 6 cudaEvent_t handles, every later
@@ -459,7 +459,7 @@ int moe_checkpoint_unpack(const void *q, const int8_t *scale, long long rows, in
  *   out dW1, dW3 bf16 [E, H, I], dW2 bf16 [E, I, H]: every entry written, zeros for an
  *            expert without rows
  *   ws       at least moe_expert_ffn_backward_workspace_bytes(T, H, E, K, I) bytes (0 for an
- *            invalid shape); about (T K + 63 E) (8 H + 6 I) bytes
+ *            invalid shape); about (T K + 63 min(E, T K)) (8 H + 6.2 I) bytes and 40 MB
  * bf16 products with fp32 sums on the tensor cores; the gradients of g = X W1 and u = X W3 and
  * the weighted activation are rounded to bf16 once, as operands of the second products.  The
  * results repeat bit for bit.  Offsets that decrease or leave [0, T*K] are recorded as

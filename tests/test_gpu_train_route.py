@@ -87,6 +87,9 @@ CASES = [
     (64, 512, 32, dict(renorm=False)),
     (40, 1000, 31, dict(scoring="softmax")),
     (33, 1024, 32, dict(n_group=2, topk_group=1, group_top=2)),
+    (90, 274, 15, dict(scoring="softmax", n_group=2, topk_group=1, group_top=2, renorm=False)),
+    (70, 512, 16, dict(n_group=8, topk_group=1, group_top=2)),
+    (50, 960, 20, dict(scoring="softmax", n_group=32, topk_group=2, group_top=1)),
 ]
 
 
@@ -114,6 +117,7 @@ def test_ties_and_near_ties(scoring, opts):
     near = (1.0 + 2.0 ** -22 * rng.integers(0, 40, (T, E))).astype(np.float32)
     const = torch.full((E,), 0.07, device=DEV)
     _check(torch.from_numpy(near).to(DEV), const, K, scoring=scoring, **opts)
+    _check(torch.from_numpy(near).to(DEV), None, K, scoring=scoring, **opts)
     # opposite zeros are equal
     z = torch.zeros(2, E, device=DEV)
     z[:, ::2] = -0.0
