@@ -109,10 +109,26 @@ struct RouteArgs {
     int fp32, T, E, K;
     int softmax, n_group, topk_group, group_top, renorm;
     int G;           // experts of a group
-    int lane_shift;  // a group fills 2^lane_shift whole lanes; -1: groups and lanes do not align
+    // Experts of a lane: with lane_shift >= 0 a group has 2^lane_shift lanes, `per` consecutive
+    // experts each (the last fewer); else the lanes take NV consecutive experts each.
+    int lane_shift, per;
+    int vec;         // lanes' experts start at multiples of 16 bytes of logits (and of 4 experts)
     int32_t *idx;
     float *w;
 };
+
+// The lane's experts: the first, and how many.
+template <int NV>
+__device__ __forceinline__ int lane_experts(const RouteArgs &a, int lane, int &live)
+{
+    if (a.lane_shift < 0) {
+        live = a.E - lane * NV;
+        return lane * NV;
+    }
+    const int g = lane >> a.lane_shift, r = (lane & ((1 << a.lane_shift) - 1)) * a.per;
+    live = g < a.n_group ? min(a.per, a.G - r) : 0;
+    return g * a.G + r;
+}
 
 // Rank of each lane's score among those of the first n lanes: descending, equal scores by lane.
 template <typename F>
@@ -149,7 +165,7 @@ __device__ __forceinline__ void merge2(F &a, F &b, int off)
     push2(ob, a, b);
 }
 
-// Lane g: the two largest of the values of group g (NV consecutive experts a lane).
+// Lane g: the two largest of the values of group g (v: the lane's experts, `lowest` past them).
 template <typename F, int NV>
 __device__ __forceinline__ void group_top2(const RouteArgs &a, const F (&v)[NV], int lane, F lowest, F &s1, F &s2)
 {
@@ -165,7 +181,7 @@ __device__ __forceinline__ void group_top2(const RouteArgs &a, const F (&v)[NV],
         s2 = __shfl_sync(kFullMask, y, (lane << a.lane_shift) & 31);
         return;
     }
-    for (int g = 0; g < a.n_group; ++g) {
+    for (int g = 0; g < a.n_group; ++g) {       // (lanes of NV experts)
         x = y = lowest;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -183,10 +199,12 @@ template <int NV>
 __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lane)
 {
     double v[NV], m = -DBL_MAX, z = 0.0;
+    int live;
+    const int e0 = lane_experts<NV>(a, lane, live);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = lane * NV + i;
-        const float l = e < a.E ? logit_at(a.logits, a.fp32, base + e) : -INFINITY;
+        const int e = e0 + i;
+        const float l = i < live ? logit_at(a.logits, a.fp32, base + e) : -INFINITY;
         v[i] = l > kMaskedLogit ? static_cast<double>(l) : (l <= kMaskedLogit ? -INFINITY : NAN);
         if (l > kMaskedLogit) m = fmax(m, v[i]);
     }
@@ -199,12 +217,12 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
     }
     const double inv = a.softmax ? 1.0 / z : 0.0;
     for (int i = 0; i < NV; ++i) {
-        const int e = lane * NV + i;
+        const int e = e0 + i;
         const bool on = v[i] > -INFINITY;
         double s = a.softmax ? exp(v[i] - m) * inv : 1.0 / (1.0 + exp(-v[i]));
-        if (a.bias && e < a.E) s += static_cast<double>(a.bias[e]);
+        if (a.bias && i < live) s += static_cast<double>(a.bias[e]);
         // (a bias of -inf ranks above a mask, and every entry stays above what is taken out)
-        v[i] = e >= a.E ? -DBL_MAX : (on && s == s ? fmax(s, 0.1 * kMaskedSel) : kMaskedSel);
+        v[i] = i >= live ? -DBL_MAX : (on && s == s ? fmax(s, 0.1 * kMaskedSel) : kMaskedSel);
     }
     if (a.n_group > 1) {
         const int G = a.E / a.n_group;
@@ -214,10 +232,8 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
         const int rank = lane_rank(score, lane, a.n_group);
         const uint32_t kept = __ballot_sync(kFullMask, lane < a.n_group && rank < a.topk_group);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = lane * NV + i;
-            if (e < a.E && !((kept >> (e / G)) & 1u)) v[i] = -DBL_MAX;
-        }
+        for (int i = 0; i < NV; ++i)
+            if (i < live && !((kept >> ((e0 + i) / G)) & 1u)) v[i] = -DBL_MAX;
     }
     int mine = 0;
     for (int k = 0; k < a.K; ++k) {
@@ -225,7 +241,7 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
         int at = a.E - 1;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (v[i] > best) { best = v[i]; at = lane * NV + i; }
+            if (v[i] > best) { best = v[i]; at = e0 + i; }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const double w = __shfl_xor_sync(kFullMask, best, o);
@@ -235,7 +251,7 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
         if (lane == k) mine = at;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (lane * NV + i == at) v[i] = -DBL_MAX;
+            if (i < live && e0 + i == at) v[i] = -DBL_MAX;
     }
     return mine;
 }
@@ -247,15 +263,16 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
 template <int NV>
 __device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, int lane, float bound)
 {
+    int live;
+    const int e0 = lane_experts<NV>(a, lane, live);
     if (!a.bias) {
         // the logits order a group's values exactly: its two largest logits, then their scores
         // (a softmax's up to a factor)
         float l[NV], m = -FLT_MAX, s1, s2;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = lane * NV + i;
-            l[i] = e < a.E ? logit_at(a.logits, a.fp32, base + e) : kOut;
-            if (e < a.E) l[i] = fmaxf(l[i] <= kMaskedLogit ? kMaskedRankLogit : l[i], kMaskedRankLogit);
+            l[i] = i < live ? logit_at(a.logits, a.fp32, base + e0 + i) : kOut;
+            if (i < live) l[i] = fmaxf(l[i] <= kMaskedLogit ? kMaskedRankLogit : l[i], kMaskedRankLogit);
             m = fmaxf(m, l[i]);
         }
         m = warp_max(m);
@@ -275,8 +292,8 @@ __device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, in
     int e1 = 0, e2 = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = lane * NV + i;
-        if (e >= a.E) break;
+        const int e = e0 + i;
+        if (i >= live) break;
         const float l = logit_at(a.logits, a.fp32, base + e);
         const float v = l <= kMaskedLogit ? kMaskedRank
                                           : fmaxf(rough_sigmoid(l) + (a.bias ? a.bias[e] : 0.f), kLeastRank);
@@ -304,7 +321,7 @@ __device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, in
     return __ballot_sync(kFullMask, lane < a.n_group && rank < a.topk_group);
 }
 
-// FULL: every lane holds NV experts (E == 32 NV).
+// FULL: every lane holds NV experts.
 template <int NV, bool F32, bool FULL>
 __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(const __grid_constant__ RouteArgs a)
 {
@@ -314,19 +331,19 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
     pdl_wait();
     if (t >= a.T) return;
     const size_t base = static_cast<size_t>(t) * a.E;
-    const int e0 = lane * NV;
-    const int live = FULL ? NV : a.E - e0;   // experts i < live of this lane exist
+    int live;                                // experts i < live of this lane exist
+    const int e0 = lane_experts<NV>(a, lane, live);
     auto has = [&](int i) -> bool { return FULL || i < live; };
 
     float l[NV];
-    if (F32 && NV % 4 == 0 && a.E % 4 == 0) {
+    if (F32 && NV % 4 == 0 && a.vec) {
         const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + base + e0);
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
             const float4 v = has(i) ? src[i / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
             l[i] = v.x; l[(i + 1) % NV] = v.y; l[(i + 2) % NV] = v.z; l[(i + 3) % NV] = v.w;
         }
-    } else if (!F32 && NV % 8 == 0 && a.E % 8 == 0) {
+    } else if (!F32 && NV % 8 == 0 && a.vec) {
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + base + e0);
 #pragma unroll
         for (int i = 0; i < NV; i += 8) {
@@ -367,7 +384,7 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
     // its terms.  The rounding of s + bias comes to it: 1.5e-7 |sel|.
     const float error = scored ? (a.softmax ? (9e-7f + 6e-8f * NV) * inv : 4e-7f) : 0.f;
     float f[NV];
-    if (a.bias && NV % 4 == 0 && a.E % 4 == 0) {
+    if (a.bias && NV % 4 == 0 && a.vec) {
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
             const float4 x = has(i) ? *reinterpret_cast<const float4 *>(a.bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -658,14 +675,11 @@ __global__ void __launch_bounds__(32 * WPC) route_bwd_kernel(const RouteBwdArgs 
 }
 
 template <int NV>
-cudaError_t fwd(RouteArgs a, cudaStream_t s)
+cudaError_t fwd(const RouteArgs &a, cudaStream_t s)
 {
-    const int per = a.G / NV;
-    a.lane_shift = -1;
-    if (a.G % NV == 0 && (per & (per - 1)) == 0)
-        for (a.lane_shift = 0; 1 << a.lane_shift < per;) ++a.lane_shift;
     const dim3 grid((a.T + WPC - 1) / WPC), block(32, WPC);
-    if (a.E == 32 * NV)
+    const bool full = a.lane_shift >= 0 && a.per == NV && a.n_group << a.lane_shift == 32 && a.G == NV << a.lane_shift;
+    if (full)
         return a.fp32 ? launch_pdl(route_fwd_kernel<NV, true, true>, grid, block, 0, s, 1, a)
                       : launch_pdl(route_fwd_kernel<NV, false, true>, grid, block, 0, s, 1, a);
     return a.fp32 ? launch_pdl(route_fwd_kernel<NV, true, false>, grid, block, 0, s, 1, a)
@@ -677,13 +691,25 @@ cudaError_t fwd(RouteArgs a, cudaStream_t s)
 cudaError_t launch_route(const void *logits, int fp32, const float *bias, int T, int E, int K,
                          const RoutingOpts &ro, int32_t *idx, float *w, cudaStream_t s)
 {
-    const RouteArgs a{logits, bias, fp32, T, E, K, ro.scoring, ro.n_group, ro.topk_group, ro.group_top,
-                      ro.renorm, E / ro.n_group, -1, idx, w};
-    if (E <= 32) return fwd<1>(a, s);
-    if (E <= 64) return fwd<2>(a, s);
-    if (E <= 128) return fwd<4>(a, s);
-    if (E <= 256) return fwd<8>(a, s);
-    if (E <= 512) return fwd<16>(a, s);
+    RouteArgs a{logits, bias, fp32, T, E, K, ro.scoring, ro.n_group, ro.topk_group, ro.group_top,
+                ro.renorm, E / ro.n_group, 0, 0, 0, idx, w};
+    // 2^lane_shift lanes a group, whole vectors of experts a lane where that fits
+    while (ro.n_group << (a.lane_shift + 1) <= 32) ++a.lane_shift;
+    const int lanes = 1 << a.lane_shift, v = fp32 ? 4 : 8;
+    a.per = (a.G + lanes - 1) / lanes;
+    if ((a.per + v - 1) / v * v <= 32) a.per = a.per > v / 2 ? (a.per + v - 1) / v * v : a.per;
+    a.vec = a.G % v == 0 && a.per % v == 0;
+    int nv = a.per;
+    if (nv > 32) {                  // many groups of many experts: lanes and groups do not align
+        a.lane_shift = -1;
+        nv = (E + 31) / 32;
+        a.vec = 0;
+    }
+    if (nv <= 1) return fwd<1>(a, s);
+    if (nv <= 2) return fwd<2>(a, s);
+    if (nv <= 4) return fwd<4>(a, s);
+    if (nv <= 8) return fwd<8>(a, s);
+    if (nv <= 16) return fwd<16>(a, s);
     return fwd<32>(a, s);
 }
 

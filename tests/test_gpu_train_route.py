@@ -76,6 +76,9 @@ def _logits(T, E, dtype, seed=0):
 
 
 CASES = [
+    (60, 200, 8, dict(n_group=8, topk_group=3, group_top=2)),
+    (40, 1020, 9, dict(n_group=17, topk_group=4, group_top=2)),
+    (40, 72, 4, dict(n_group=12, topk_group=2, group_top=2)),
     (1, 1, 1, dict()),
     (3, 8, 8, dict(scoring="softmax")),
     (45, 16, 2, dict()),
