@@ -39,6 +39,7 @@ namespace moe {
 namespace {
 
 constexpr int WPC = 8;                    // warps (tokens) a CTA
+constexpr int MANY = 28;                  // candidates that are more than wanted (32 have a lane)
 constexpr float kMaskedLogit = -3.38953139e38f;   // bf16's lowest value: at or below it, masked
 constexpr double kMaskedSel = -1e300;     // fp64 order: a masked expert of a kept group
 
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
         for (int i = 0; i < NV; ++i)
             if (!has(i)) f[i] = kOut;
     }
-    bool sure = true, out = false;           // out: nothing of this lane is in the running
+    bool sure = true;
     if (a.n_group > 1) {
         float s1, s2;
         group_top2<float, NV>(a, f, lane, -FLT_MAX, s1, s2);
@@ -432,7 +433,10 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
             for (int i = 0; i < NV; ++i) f[i] = has(i) ? by_logit(l[i]) : kOut;
         }
         if (a.lane_shift >= 0) {
-            out = live <= 0 || !((kept >> (lane >> a.lane_shift)) & 1u);
+            // (by selection: a branch on the lane would split the warp for all that follows)
+            const bool in = live > 0 && ((kept >> (lane >> a.lane_shift)) & 1u);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) f[i] = in ? f[i] : kOut;
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -443,9 +447,8 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
     float lg = 0.f;                          // ... and its logit
     if (sure) {
         float x = kOut;                      // the lane's maximum
-        if (!out)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) x = fmaxf(x, f[i]);
+        for (int i = 0; i < NV; ++i) x = fmaxf(x, f[i]);
         // A value that K lanes' maxima reach (so K experts do), close to the K-th largest of them:
         // six halvings between the smallest and the largest maximum.
         float least = -FLT_MAX;
@@ -461,26 +464,29 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
                 hi = enough ? hi : mid;
             }
             least = lo;
-        } else {
-            // fewer lanes than K hold anything (few groups kept): the experts themselves
+        }
+        // Where that leaves many candidates (few lanes hold what is in the running), halvings
+        // over the experts themselves, from the lowest unmasked one.
+        auto reach = [&](float v) -> int {       // experts at or above v
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) n += f[i] >= v;
+            return static_cast<int>(__reduce_add_sync(kFullMask, n));
+        };
+        if (reach(least) > MANY) {
             const float floor_rank = a.bias ? kLeastRank : kMaskedRankLogit;
             uint32_t low = 0xffffffffu;
-            int some_n = 0;
-            if (!out)
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (f[i] > floor_rank) { low = min(low, order_key(f[i])); ++some_n; }
-            if (static_cast<int>(__reduce_add_sync(kFullMask, some_n)) >= a.K) {
-                float lo = key_value(__reduce_min_sync(kFullMask, low)), hi = top;
-                for (int r = 0; r < 8; ++r) {
+            for (int i = 0; i < NV; ++i) low = min(low, f[i] > floor_rank ? order_key(f[i]) : 0xffffffffu);
+            low = __reduce_min_sync(kFullMask, low);
+            float lo = fmaxf(least, low == 0xffffffffu ? -FLT_MAX : key_value(low)), hi = top;
+            int n = reach(lo);
+            if (n >= a.K) {
+                for (int r = 0; r < 12 && n > MANY; ++r) {
                     const float mid = 0.5f * lo + 0.5f * hi;
-                    int n = 0;
-                    if (!out)
-#pragma unroll
-                        for (int i = 0; i < NV; ++i) n += f[i] >= mid;
-                    const bool enough = static_cast<int>(__reduce_add_sync(kFullMask, n)) >= a.K;
-                    lo = enough ? mid : lo;
-                    hi = enough ? hi : mid;
+                    const int c = reach(mid);
+                    if (c >= a.K) { lo = mid; n = c; }
+                    else hi = mid;
                 }
                 least = lo;
             }
@@ -492,9 +498,8 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
         }
         least = fmaxf(least, -FLT_MAX);
         uint32_t chosen = 0u;
-        if (!out)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) chosen |= f[i] >= least ? 1u << i : 0u;
+        for (int i = 0; i < NV; ++i) chosen |= f[i] >= least ? 1u << i : 0u;
         const int n = __popc(chosen);
         int at = n;
 #pragma unroll
@@ -566,7 +571,7 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
                 int e = 1 << 30;
 #pragma unroll
                 for (int i = NV - 1; i >= 0; --i)
-                    if (!out && f[i] >= best && f[i] > kOut) { best = f[i]; e = e0 + i; }
+                    if (f[i] >= best && f[i] > kOut) { best = f[i]; e = e0 + i; }
                 const uint32_t key = order_key(best), most = __reduce_max_sync(kFullMask, key);
                 const int win = __reduce_min_sync(kFullMask, key == most ? e : 1 << 30);
                 if (lane == r) { expert = win; place = r; }
