@@ -20,7 +20,8 @@ namespace moe {
 namespace {
 
 constexpr int WARP_COLS = 1024;       // longest row that one warp takes (forward)
-constexpr int WARP_COLS_BWD = 512;    // ... backward (1024 columns take 198 registers: 86 us for 16384 fp32 rows with dres, the ring 45)
+constexpr int WARP_COLS_BWD = 512;    // ... backward (1024 columns take 198 registers: 86 us for
+                                      // 16384 fp32 rows with dres, the ring 45)
 constexpr int ROWS_PER_CTA = 8;       // ... with this many warps a CTA
 
 __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8])
@@ -161,9 +162,10 @@ __device__ __forceinline__ float4 load4(const void *p, int c)
 // Longer rows of a batch that gives every CTA several: the rows of x arrive by bulk copies in a
 // ring of shared-memory stages, 4 x VPT columns a thread in registers from there.  A row's
 // stage is filled again behind the barrier of its mean.  (A CTA per row, 448 threads of plain
-// loads, took 154 us for 16384 rows of 7168 in fp32 and 163 us in bf16; this: 130 and 115 us, 5.4 and 4.1 TB/s.  Two barriers a row bound it,
-// not the loads: more CTAs an SM would need fewer registers.  A wait that runs out leaves the
-// CTA's later rows void; the entry point has no status word to record it in.)
+// loads, took 154 us for 16384 rows of 7168 in fp32 and 163 us in bf16; this: 130 and 115 us, 5.4
+// and 4.1 TB/s.  Two barriers a row bound it, not the loads: more CTAs an SM would need fewer
+// registers.  A wait that runs out leaves the CTA's later rows void; the entry point has no status
+// word to record it in.)
 struct NormFwd {
     const void *x;
     const float *gamma, *beta;     // beta nullable
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kerne
         }
         const float mu = sum(a, red[0]) * inv;
         // (every thread has read the row: its stage takes a row further on)
-        if (tid == 0 && ahead < p.T) {
+        if (tid == 0 && ahead < p.T && !*abort_flag) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             fill(ahead, s);
             ahead += step;
@@ -354,8 +356,9 @@ __global__ void __launch_bounds__(32 * ROWS_PER_CTA) norm_bwd_warp_kernel(const 
 // Longer rows: a CTA per row, 4 x VPT columns a thread.  The rows x, dy (and dres) of the CTA
 // arrive by bulk copies in a ring of shared-memory stages, so that loads never wait for a
 // row's two sums (plain loads before and after the barriers of two CTAs an SM: 402 us for
-// 16384 rows of 7168 in fp32 with dres, 4.1 TB/s; this: 242 us, 6.8 TB/s, the copy bandwidth).  One barrier a row: its sums;
-// a row's stage is filled again behind the next row's.  GREG: gamma stays in registers.
+// 16384 rows of 7168 in fp32 with dres, 4.1 TB/s; this: 242 us, 6.8 TB/s, the copy bandwidth).
+// One barrier a row: its sums; a row's stage is filled again behind the next row's.  GREG: gamma
+// stays in registers.
 template <bool XF32, int VPT, bool GREG, int MAXT, int CTAS>
 __global__ void __launch_bounds__(MAXT, CTAS) norm_bwd_ring_kernel(const NormBwd p)
 {
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_bwd_ring_kernel(const NormBwd
         if ((tid & 31) == 0) red[k][tid >> 5] = make_float2(s0, s1);
         __syncthreads();
         // every thread is done with the row before: its stage takes a row further on
-        if (tid == 0 && prev >= 0 && ahead < p.T) {
+        if (tid == 0 && prev >= 0 && ahead < p.T && !*abort_flag) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             fill(ahead, prev);
             ahead += step;
@@ -550,8 +553,9 @@ size_t plan_ring(NormBwd &p, int xb, bool res, int per_sm)
     return b * p.stages;
 }
 
-// CTAs of the ring that share an SM: 1024 threads, where two stages of their rows fit.  One CTA a row of 7168 leaves the SM idle between a row's barriers (bf16 without
-// dres, 16384 rows: 190 us with one, 165 us with two).
+// CTAs of the ring that share an SM: 1024 threads, where two stages of their rows fit.  One CTA a
+// row of 7168 leaves the SM idle between a row's barriers (bf16 without dres, 16384 rows: 190 us
+// with one, 165 us with two).
 int ring_ctas(int H, int row_bytes)
 {
     const int most = 1024 / ring_threads(H, H <= 2048 ? 2 : 4);

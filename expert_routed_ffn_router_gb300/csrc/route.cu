@@ -12,9 +12,9 @@
 // that K of the 32 lanes' maxima reach (six halvings from their range come close to the K-th
 // largest) is reached by K experts, so only the values at or above it, a dozen for K = 8, are
 // candidates; they go to one lane each, in expert order, and every lane counts the candidates
-// ahead of its own.  (Taking the maximum K
-// times measured 26.6 us for 16384 tokens of 256 experts, K = 8, without groups or bias; this
-// 10.1 us.)  More than 32 candidates (many equal values) take that loop.
+// ahead of its own.  (Taking the maximum K times measured 26.6 us for 16384 tokens of 256
+// experts, K = 8, without groups or bias; this 10.8 us.)  More than 32 candidates (many equal
+// values) take that loop.
 //
 // The selection is exact: without a bias sel is ordered as the logits are, and those are
 // compared as they stand.  Otherwise sel is held in fp32 with a bound on its error; the
@@ -22,7 +22,7 @@
 // are evaluated again in fp64, one a lane (a softmax, or group scores too close: the whole
 // row, rare).
 //
-// The batch above with 8 groups (4 kept, two values each) and a bias takes 19 us: about 800
+// The batch above with 8 groups (4 kept, two values each) and a bias takes 18 us: about 800
 // instructions a token, where its bytes would take 2.6 us.  Two tokens take the launch's time.
 //
 // Gradient (D = sum_k w_k dw_k over the selected):
@@ -259,8 +259,8 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
 
 // The groups kept (a bit each), by scores in fp64.  With a bias, of every lane's two largest
 // values (sel within `bound`), where lanes hold whole groups, the score is a sigmoid and no
-// lane's third value comes close to its second; 0 where that does not hold.  (Out of line, on values of its own:
-// it is rare, and arrays handed to it would keep the caller's in local memory.)
+// lane's third value comes close to its second; 0 where that does not hold.  (Out of line, on
+// values of its own: it is rare, and arrays handed to it would keep the caller's in local memory.)
 template <int NV>
 __device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, int lane, float bound)
 {
@@ -287,8 +287,8 @@ __device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, in
         const int rank = lane_rank(two, lane, a.n_group);
         return __ballot_sync(kFullMask, lane < a.n_group && rank < a.topk_group);
     }
-    const int per = 1 << a.lane_shift;
     if (a.softmax || a.lane_shift < 0) return 0u;
+    const int per = 1 << a.lane_shift;
     float v1 = -FLT_MAX, v2 = -FLT_MAX, v3 = -FLT_MAX, l1 = 0.f, l2 = 0.f;
     int e1 = 0, e2 = 0;
 #pragma unroll

@@ -41,10 +41,12 @@
  *     returns a negative moe_status_t and has no effect.  A failing launch returns
  *     MOE_ERR_CUDA.  Conditions found on the device (a bounded wait that ran out, an
  *     expert index outside [0, E) given to moe_dispatch, group offsets outside [0, rows]
- *     given to moe_expert_ffn or moe_expert_ffn_backward) are recorded in the workspace's status word and never lead
- *     to an access out of bounds; read them with moe_read_status().
+ *     given to moe_expert_ffn or moe_expert_ffn_backward) are recorded in the workspace's
+ *     status word and never lead to an access out of bounds; read them with
+ *     moe_read_status().
  *   - Supported shapes: 1 <= E <= 1024, 1 <= K <= min(E, 32), H and I multiples of 64,
- *     T >= 0 (T == 0 enqueues nothing and returns MOE_OK), T*K < 2^31.
+ *     T >= 0 (T == 0 enqueues nothing and returns MOE_OK, except that the backward calls
+ *     set the weight gradients to 0), T*K < 2^31.
  */
 #ifndef MOE_GB300_H
 #define MOE_GB300_H
@@ -122,8 +124,9 @@ size_t moe_workspace_bytes(const moe_shape_t *shape);
  * moe_workspace_bytes(shape).  They hold what the last layer call on that workspace left
  * there, once its stream has reached the end of the call (with FP8 experts, h and Yp hold
  * the bf16 activations and outputs the FP8 GEMMs read and wrote; their E4M3 operands live
- * elsewhere in the workspace).  For inspection and testing; not on the pages.  Returns MOE_OK, or MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED_SHAPE for a
- * shape moe_workspace_bytes rejects. */
+ * elsewhere in the workspace).  For inspection and testing; not on the pages.  Returns
+ * MOE_OK, or MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED_SHAPE for a shape
+ * moe_workspace_bytes rejects. */
 typedef struct moe_workspace_layout {
     size_t offsets, perm, slot_pos, Xp, h, Yp, Ysh, bytes;
 } moe_workspace_layout_t;
@@ -142,18 +145,19 @@ int moe_read_status(void *ws, void *stream);
 /* Debugging hook: with on = 1, every later call that records device-side conditions in a
  * workspace status word (moe_router_topk, moe_router_topk_ex, moe_dispatch,
  * moe_expert_ffn, moe_layer_forward, moe_layer_forward_ex, moe_layer_forward_fp8,
- * moe_layer_norm_backward, moe_expert_ffn_backward) synchronises its stream after enqueueing its work and returns that word, read and reset
- * as by moe_read_status, in place of MOE_OK -- except for an empty batch and inside a stream
- * capture (a capture cannot be synchronised).  on = 0 (the default) restores the
- * asynchronous calls.  Process-wide; not for production use: it serialises the host with
- * the GPU. */
+ * moe_layer_norm_backward, moe_expert_ffn_backward) synchronises its stream after enqueueing
+ * its work and returns that word, read and reset as by moe_read_status, in place of MOE_OK
+ * -- except for an empty batch and inside a stream capture (a capture cannot be
+ * synchronised).  on = 0 (the default) restores the asynchronous calls.  Process-wide; not
+ * for production use: it serialises the host with the GPU. */
 void moe_debug_set_sync_status(int on);
 
 /* Testing hook: sets the limit of the bounded device-side waits of the tensor-core FFN
- * kernels (forward and backward) (0 restores the default of one second) and, with inject_stall = 1, makes their
- * TMA producer skip its work so that the waits run out and MOE_ERR_DEVICE_TIMEOUT is
- * recorded in the status word (no fault, no hang).  Affects later moe_expert_ffn,
- * moe_expert_ffn_backward and moe_layer_forward calls of the process; not for production use. */
+ * kernels, forward and backward, and of moe_layer_norm_backward (0 restores the default of
+ * one second) and, with inject_stall = 1, makes the TMA producer of the FFN kernels skip its
+ * work so that the waits run out and MOE_ERR_DEVICE_TIMEOUT is recorded in the status word
+ * (no fault, no hang).  Affects later calls of these and of moe_layer_forward in the process;
+ * not for production use. */
 void moe_debug_set_wait_limit(unsigned long long limit_ns, int inject_stall);
 
 /* Profiling hook: with `events` pointing at n >= 6 cudaEvent_t handles, every later
