@@ -11,7 +11,8 @@
 // applied after the product with W2, so <p, h> needs no expert output.
 //
 // Launches, in stream order:
-//   plan     padded row offsets of the groups (multiples of 64 rows), offsets checked
+//   plan     padded row offsets of the groups (multiples of 64 rows), offsets checked (few tokens:
+//            within gather)
 //   gather   the rows of X (taken back from 8 bits) and dY in padded group order, bf16; the
 //            rows up to the next multiple of 64 are zeros, so no product needs a mask
 //   products one persistent launch over a list of units:
@@ -120,17 +121,28 @@ __device__ __forceinline__ float fast_sigmoid(float g)
 }
 
 // ----------------------------------------------------------------------------- plan
-__global__ void __launch_bounds__(1024) plan_kernel(const int32_t *__restrict__ offsets, int E, int rows,
-                                                    Plan p, int *status)
+// By a whole CTA: rows, first row and first padded row of each group to cnt, src and pos, and with
+// `out` the rest of the plan; whether the offsets are valid (cnt is 0 throughout if not).
+__device__ __forceinline__ bool plan_groups(const int32_t *__restrict__ offsets, int E, int rows, const Plan &p,
+                                            bool out, int *cnt, int *src, int *pos, int *status)
 {
     __shared__ int a[32], b[32];
-    pdl_wait();
-    const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
-    const int lo = g < E ? offsets[g] : 0, hi = g < E ? offsets[g + 1] : 0;
-    const int bad = lo < 0 || hi < lo || hi > rows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (E + blockDim.x - 1) / blockDim.x, g0 = threadIdx.x * per, g1 = min(E, g0 + per);
+    int bad = 0;
+    for (int g = g0; g < g1; ++g) {
+        const int lo = offsets[g], hi = offsets[g + 1];
+        bad |= lo < 0 || hi < lo || hi > rows;
+        src[g] = lo;
+        cnt[g] = hi - lo;
+    }
     const bool ok = !__syncthreads_or(bad);
-    const int m = ok ? hi - lo : 0;
-    const int np = pad_rows(m), nt = (m + TM - 1) / TM;
+    int np = 0, nt = 0;
+    for (int g = g0; g < g1; ++g) {
+        if (!ok) cnt[g] = 0;
+        np += pad_rows(cnt[g]);
+        nt += (cnt[g] + TM - 1) / TM;
+    }
     int ip = np, it = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -140,22 +152,37 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t *__restrict__ 
     if (lane == 31) { a[warp] = ip; b[warp] = it; }
     __syncthreads();
     for (int w = 0; w < warp; ++w) { ip += a[w]; it += b[w]; }
-    if (g < E) {
-        p.cnt[g] = m;
-        p.src[g] = lo;
-        p.pos[g] = ip - np;
-        p.tiles[g] = it - nt;
-        p.ready[g] = 0;
-    }
-    if (g == E - 1) {
+    if (out && g0 < g1 && g1 == E) {
         p.pos[E] = ip;
         p.tiles[E] = it;
     }
-    if (g == 0) {
+    ip -= np;
+    it -= nt;
+    for (int g = g0; g < g1; ++g) {
+        pos[g] = ip;
+        if (out) {
+            p.cnt[g] = cnt[g];
+            p.src[g] = src[g];
+            p.pos[g] = ip;
+            p.tiles[g] = it;
+            p.ready[g] = 0;
+        }
+        ip += pad_rows(cnt[g]);
+        it += (cnt[g] + TM - 1) / TM;
+    }
+    if (out && threadIdx.x == 0) {
         *p.ok = ok ? 1 : 0;
         *p.next = 0;
         if (!ok) report(status, MOE_ERR_INVALID_ARG);
     }
+    return ok;
+}
+
+__global__ void __launch_bounds__(1024) plan_kernel(const int32_t *__restrict__ offsets, int E, int rows,
+                                                    Plan p, int *status)
+{
+    pdl_wait();
+    plan_groups(offsets, E, rows, p, true, p.cnt, p.src, p.pos, status);
 }
 
 // --------------------------------------------------------------------------- gather
@@ -163,24 +190,41 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t *__restrict__ 
 // slots.  CTA (T + g, y): the zero rows at the end of group g.
 constexpr int GT = 128;
 constexpr int GCOLS = GT * 8;
+// With at most this many CTAs each makes the plan for itself (PLAN), which saves a launch; the
+// first of them leaves it to the products.
+// (16 x 256, 16 experts: 27.5 us with the launch, 25.9 without; 1000 tokens 36.3 and 34.5; 2000
+// tokens, 2016 CTAs, 39.8 and 40.0; 1024 experts 148.8 and 150.5.)
+constexpr unsigned PLAN_CTAS = 1024;
+constexpr int PLAN_E = 256;
 
+template <bool PLAN>
 __global__ void __launch_bounds__(GT) gather_kernel(const void *__restrict__ x, const int8_t *__restrict__ xs,
                                                     const uint16_t *__restrict__ dY,
+                                                    const int32_t *__restrict__ offsets,
                                                     const int32_t *__restrict__ slot_pos,
                                                     const float *__restrict__ topk_w, int T, int H, int E,
                                                     int K, Plan p, uint16_t *__restrict__ X,
                                                     uint16_t *__restrict__ D, float *__restrict__ wrow,
-                                                    int *__restrict__ prow)
+                                                    int *__restrict__ prow, int *__restrict__ status)
 {
     __shared__ int dst[32];
+    __shared__ int own[PLAN ? 3 * PLAN_E : 1];
     pdl_wait();
-    if (!*p.ok) return;
+    const int *cnt = p.cnt, *src = p.src, *pos = p.pos;
+    if (PLAN) {
+        int *c = own, *f = own + PLAN_E, *q = own + 2 * PLAN_E;
+        if (!plan_groups(offsets, E, T * K, p, (blockIdx.x | blockIdx.y) == 0, c, f, q, status)) return;
+        __syncthreads();
+        cnt = c; src = f; pos = q;
+    } else if (!*p.ok) {
+        return;
+    }
     const int c = blockIdx.y * GCOLS + threadIdx.x * 8;
     if (blockIdx.x >= static_cast<unsigned>(T)) {
         const int g = blockIdx.x - T;
-        const int m = p.cnt[g], n = pad_rows(m);
+        const int m = cnt[g], n = pad_rows(m);
         for (int r = m; r < n; ++r) {
-            const size_t row = static_cast<size_t>(p.pos[g] + r);
+            const size_t row = static_cast<size_t>(pos[g] + r);
             if (c < H) {
                 *reinterpret_cast<uint4 *>(X + row * H + c) = make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4 *>(D + row * H + c) = make_uint4(0, 0, 0, 0);
@@ -194,14 +238,14 @@ __global__ void __launch_bounds__(GT) gather_kernel(const void *__restrict__ x, 
         const size_t pair = static_cast<size_t>(t) * K + threadIdx.x;
         const int r = slot_pos[pair];
         int q = -1;
-        if (r >= 0 && r < p.src[E - 1] + p.cnt[E - 1]) {
+        if (r >= 0 && r < src[E - 1] + cnt[E - 1]) {
             int lo = 0, hi = E - 1;        // last group whose first row is <= r
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (p.src[mid] <= r) lo = mid; else hi = mid - 1;
+                if (src[mid] <= r) lo = mid; else hi = mid - 1;
             }
-            const int k = r - p.src[lo];
-            if (k >= 0 && k < p.cnt[lo]) q = p.pos[lo] + k;
+            const int k = r - src[lo];
+            if (k >= 0 && k < cnt[lo]) q = pos[lo] + k;
         }
         dst[threadIdx.x] = q;
         if (blockIdx.y == 0) {
@@ -1007,11 +1051,14 @@ cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned
     a.timeout_ns = timeout_ns;
     a.inject = inject;
 
-    cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(1024), 0, s, 1, f.offsets, E, T * K, plan, status);
-    if (e != cudaSuccess) return e;
     const unsigned parts = (H + GCOLS - 1) / GCOLS;
-    e = launch_pdl(gather_kernel, dim3(T + E, parts), dim3(GT), 0, s, 1, f.x, f.x_scale,
-                   static_cast<const uint16_t *>(f.dY), f.slot_pos, f.topk_w, T, H, E, K, plan, X, D, wrow, prow);
+    const bool fused = E <= PLAN_E && static_cast<size_t>(T + E) * parts <= PLAN_CTAS;
+    cudaError_t e = cudaSuccess;
+    if (!fused) e = launch_pdl(plan_kernel, dim3(1), dim3(1024), 0, s, 1, f.offsets, E, T * K, plan, status);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(fused ? gather_kernel<true> : gather_kernel<false>, dim3(T + E, parts), dim3(GT), 0, s, 1, f.x,
+                   f.x_scale, static_cast<const uint16_t *>(f.dY), f.offsets, f.slot_pos, f.topk_w, T, H, E, K,
+                   plan, X, D, wrow, prow, status);
     if (e != cudaSuccess) return e;
     const unsigned ctas = gemm_ctas();
     const size_t smem = 1024 + STAGES * STAGE + N_EPI * SLAB;

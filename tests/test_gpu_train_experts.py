@@ -252,3 +252,21 @@ def test_empty_batch():
     B.moe_expert_ffn_backward(e(0, 64), None, e(0, 64), torch.zeros(3, dtype=I32, device=DEV), e(0, 1, t=I32), None,
                               W, W, W, e(0, 64), None, d[0], d[1], d[2], ws)
     assert not any(bool(v.any()) for v in d)
+
+
+@pytest.mark.parametrize("shape", [(16, 64, 256, 4, 64), (16, 64, 257, 4, 64), (1016, 64, 8, 1, 64), (1017, 64, 8, 1, 64)])
+def test_both_sides_of_the_rule_on_where_the_plan_is_made(shape):
+    p = _problem(*shape, False)
+    o, ws = backward(p)
+    assert B.moe_read_status(ws) == 0
+    check(o, *reference(p))
+    off = p["offsets"].cpu().numpy()
+    off[-1] = shape[0] * shape[3] + 1
+    good, p["offsets"] = p["offsets"], torch.from_numpy(off).to(DEV)
+    o, _ = backward(p, ws=ws)
+    assert B.moe_read_status(ws) == -1
+    assert all(bool((v == 7).all()) for v in o.values())
+    p["offsets"] = good
+    o, _ = backward(p, ws=ws)
+    assert B.moe_read_status(ws) == 0
+    check(o, *reference(p))
