@@ -420,8 +420,11 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
         if (scored && a.topk_group < a.n_group) {
             const float lo = __shfl_sync(kFullMask, score, __ffs(__ballot_sync(kFullMask, mine && rank == a.topk_group - 1)) - 1);
             const float hi = __shfl_sync(kFullMask, score, __ffs(__ballot_sync(kFullMask, mine && rank == a.topk_group)) - 1);
-            // (a score is the sum of two values, each within the bound at its size)
-            const float bound = error + 1.5e-7f * fmaxf(fabsf(lo), fabsf(hi));
+            // (a score is the sum of two values, each within the bound at its own size, which the
+            // sum need not have: values of opposite sign cancel; any group may be out of place)
+            auto size = [](float v) -> float { return v > kLeastRank ? fabsf(v) : 0.f; };
+            const float most = mine ? size(s1) + (a.group_top == 2 ? size(s2) : 0.f) : 0.f;
+            const float bound = error + 1.5e-7f * __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(most)));
             sure = lo - hi > 4.f * bound;
             if (!sure) {
                 kept = groups_fp64<NV>(a, base, lane, bound);

@@ -1,0 +1,26 @@
+"""Routing from given logits where sums cancel, underflow or saturate: the selection has to be
+the definition's in 64 bits, weights and gradients right relative to their own size."""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_train_route as R
+from expert_routed_ffn_router_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = R.DEV
+F32 = torch.float32
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [1e4, 1e5])
+def test_group_sums_that_cancel(scoring, size):
+    # one expert of each group with bias +size, the others -size (and a spread of 0.2): a group's
+    # two largest values cancel in their sum, their roundings (2^-24 size) do not
+    T, E = 20000, 256
+    rng = np.random.default_rng(0)
+    b = (0.2 * rng.random(E)).astype(np.float32) - np.float32(size)
+    for g in range(8):
+        b[g * 32 + int(rng.integers(32))] += np.float32(2 * size)
+    R._check(R._logits(T, E, F32, seed=11), torch.from_numpy(b).to(DEV), 8, scoring=scoring, n_group=8, topk_group=4,
+             group_top=2)
