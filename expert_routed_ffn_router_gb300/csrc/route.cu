@@ -41,12 +41,13 @@ namespace {
 constexpr int WPC = 8;                    // warps (tokens) a CTA
 constexpr int MANY = 28;                  // candidates that are more than wanted (32 have a lane)
 constexpr float kMaskedLogit = -3.38953139e38f;   // bf16's lowest value: at or below it, masked
-constexpr double kMaskedSel = -1e300;     // fp64 order: a masked expert of a kept group
 
 // Values that rank below every sel or logit: masked ones (sums of two of them stay above
 // the lowest float), and ones out of the running.
 constexpr float kMaskedRank = -1e38f, kLeastRank = -9e37f;    // sel is kept at or above the latter
 constexpr float kMaskedRankLogit = -3.395e38f;
+// The same in fp64: values and sums of two of them in the same order as in fp32.
+constexpr double kMaskedSel = -1e300, kLeastSel = 0.9 * kMaskedSel;
 constexpr float kOut = -INFINITY;
 
 // Integers that order as the floats do (for the warp-wide integer maximum).
@@ -223,7 +224,7 @@ __device__ __noinline__ int select_fp64(const RouteArgs &a, size_t base, int lan
         double s = a.softmax ? exp(v[i] - m) * inv : 1.0 / (1.0 + exp(-v[i]));
         if (a.bias && i < live) s += static_cast<double>(a.bias[e]);
         // (a bias of -inf ranks above a mask, and every entry stays above what is taken out)
-        v[i] = i >= live ? -DBL_MAX : (on && s == s ? fmax(s, 0.1 * kMaskedSel) : kMaskedSel);
+        v[i] = i >= live ? -DBL_MAX : (on && s == s ? fmax(s, kLeastSel) : kMaskedSel);
     }
     if (a.n_group > 1) {
         const int G = a.E / a.n_group;
@@ -311,7 +312,7 @@ __device__ __noinline__ uint32_t groups_fp64(const RouteArgs &a, size_t base, in
     auto exact = [&](float s, float x, int e) -> double {
         if (!(s > kMaskedRank)) return kMaskedSel;
         const double d = 1.0 / (1.0 + exp(-static_cast<double>(x)));
-        return fmax(a.bias ? d + static_cast<double>(a.bias[e]) : d, 0.1 * kMaskedSel);
+        return fmax(a.bias ? d + static_cast<double>(a.bias[e]) : d, kLeastSel);
     };
     const double d1 = exact(v1, l1, e1), d2 = exact(v2, l2, e2);
     double x = fmax(d1, d2), y = fmin(d1, d2);
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
                         double q = 0.0, d = -DBL_MAX;
                         if (lane < C) {
                             q = mine <= kMaskedRank ? 0.0 : exp(static_cast<double>(lg) - static_cast<double>(m)) / static_cast<double>(z);
-                            d = mine <= kMaskedRank ? kMaskedSel : fmax(q + static_cast<double>(a.bias[expert]), 0.1 * kMaskedSel);
+                            d = mine <= kMaskedRank ? kMaskedSel : fmax(q + static_cast<double>(a.bias[expert]), kLeastSel);
                         }
                         int r64 = 0;
                         bool tie = false;
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
                         double d = -DBL_MAX;
                         if (lane < C) {
                             d = 1.0 / (1.0 + exp(-static_cast<double>(lg))) + static_cast<double>(a.bias[expert]);
-                            d = mine <= kMaskedRank ? kMaskedSel : fmax(d, 0.1 * kMaskedSel);
+                            d = mine <= kMaskedRank ? kMaskedSel : fmax(d, kLeastSel);
                         }
                         const int r64 = lane_rank(d, lane, C);
                         if (lane < C) place = r64;

@@ -24,3 +24,17 @@ def test_group_sums_that_cancel(scoring, size):
         b[g * 32 + int(rng.integers(32))] += np.float32(2 * size)
     R._check(R._logits(T, E, F32, seed=11), torch.from_numpy(b).to(DEV), 8, scoring=scoring, n_group=8, topk_group=4,
              group_top=2)
+
+
+@pytest.mark.parametrize("E,group_top", [(16, 2), (256, 2), (256, 1)])
+def test_groups_of_masked_and_of_excluded_experts(E, group_top):
+    # group 0 holds experts with a bias of -inf, group 1 one unmasked expert and masked ones: the
+    # order of the two does not depend on how many experts there are
+    l = torch.full((3, E), -float("inf"), device=DEV)
+    l[:, :E // 2] = 0.25
+    l[:, E // 2 + 5] = torch.tensor([0.5, -3.0, 20.0], device=DEV)
+    b = torch.zeros(E, device=DEV)
+    b[:E // 2] = -float("inf")
+    for scoring in ("sigmoid", "softmax"):
+        idx, _ = R._check(l, b, 8, scoring=scoring, n_group=2, topk_group=1, group_top=group_top)
+        assert bool((idx[:, 0] == E // 2 + 5).all())
