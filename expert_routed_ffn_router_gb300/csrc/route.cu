@@ -102,6 +102,26 @@ __device__ __forceinline__ void push2(double v, double &a, double &b)
     else if (v > b) b = v;
 }
 
+// The lanes' scores up to a common factor, the largest near 1, where their sum is all that they
+// are divided by: a softmax of the selected logits alone.  (The row's maximum need not be among
+// them: 95 below it, where a bias chose them, their scores are denormal, and 0 from 104 on.)
+// Masked logits are -inf here and give 0.
+__device__ __forceinline__ float selected_exp(float l, bool on)
+{
+    const float top = key_value(__reduce_max_sync(kFullMask, order_key(on && l > -INFINITY ? l : -FLT_MAX)));
+    return on ? expf(l - top) : 0.f;
+}
+
+// Sigmoids whose sum is below kSmallSum are e^l to 1e-12 of themselves, and below 2^-126 fp32 does
+// not hold them: the same.  (0 where they are 0 in 64 bits too.)
+constexpr float kSmallSum = 1e-12f, kNoScore = -708.f;
+
+__device__ __forceinline__ float small_scores(float l, bool on)
+{
+    const float s = selected_exp(l, on);
+    return __any_sync(kFullMask, on && l > kNoScore) ? s : 0.f;
+}
+
 // sigmoid from the hardware exp2 and reciprocal, for the selection (its error is in the bound)
 __device__ __forceinline__ float rough_sigmoid(float l) { return fast_rcp(1.f + __expf(-l)); }
 
@@ -593,14 +613,18 @@ __global__ void __launch_bounds__(32 * WPC, NV <= 8 ? 4 : 1) route_fwd_kernel(co
     }
     // weights: the selected scores (a masked expert's is 0), over their sum
     const bool on = place < a.K;
+    if (on && lg <= kMaskedLogit) lg = -INFINITY;
     float s = 0.f;
-    if (on) {
-        if (lg <= kMaskedLogit) lg = -INFINITY;
-        s = a.softmax ? expf(lg - m) * inv : sigmoid(lg);
-    }
     if (a.renorm) {
-        const float sum = warp_sum(s);
-        s = sum < 1e-30f ? (sum == 0.f ? 0.f : s / sum) : s * fast_rcp(sum);
+        s = a.softmax ? selected_exp(lg, on) : (on ? sigmoid(lg) : 0.f);
+        float sum = warp_sum(s);
+        if (!a.softmax && sum < kSmallSum) {
+            s = small_scores(lg, on);
+            sum = warp_sum(s);
+        }
+        s = sum == 0.f ? 0.f : s * fast_rcp(sum);
+    } else if (on) {
+        s = a.softmax ? expf(lg - m) * inv : sigmoid(lg);
     }
     if (on) {
         a.idx[static_cast<size_t>(t) * a.K + place] = expert;
@@ -659,18 +683,17 @@ __global__ void __launch_bounds__(32 * WPC) route_bwd_kernel(const RouteBwdArgs 
     } else {
         for (int i = lane; i < a.E; i += 32) row[i] = 0.f;
         __syncwarp();
-        float s, w;
-        if (a.softmax) {     // renormalised: a softmax of the selected logits
-            m = warp_max(l > -INFINITY || l != l ? l : -FLT_MAX);
-            s = e >= 0 ? expf(l - m) : 0.f;
-        } else {
-            s = e >= 0 ? sigmoid(l) : 0.f;
-        }
+        // (a softmax is renormalised here)
+        float s = a.softmax ? selected_exp(l, e >= 0) : (e >= 0 ? sigmoid(l) : 0.f);
         if (a.renorm) {
-            const float sum = warp_sum(s);
-            w = sum == 0.f ? 0.f : s / sum;
-            d = w * (dw - warp_sum(w * dw));
-            if (!a.softmax) d *= 1.f - s;
+            const float rest = a.softmax ? 1.f : 1.f - s;
+            float sum = warp_sum(s);
+            if (!a.softmax && sum < kSmallSum) {
+                s = small_scores(l, e >= 0);
+                sum = warp_sum(s);
+            }
+            const float w = sum == 0.f ? 0.f : s / sum;
+            d = w * (dw - warp_sum(w * dw)) * rest;
         } else {
             d = s * (1.f - s) * dw;
         }

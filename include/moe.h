@@ -421,8 +421,10 @@ int moe_layer_norm_backward(const void *dy, const void *x, int x_fp32, const flo
  *   as there.  The selection is the one exact arithmetic gives on these logits.
  * A logit at or below bf16's lowest finite value (-3.3895e38: -inf, either type's lowest)
  * masks its expert: score 0, and chosen only when its kept groups hold nothing else, lowest
- * index first.  Weights whose sum is 0 (a row with nothing left) are 0.  A row with a NaN
- * still gets K distinct experts in [0, E); its weights may be NaN. */
+ * index first.  Renormalised weights hold for scores too small for fp32 as well; a sum of 0 (a
+ * row with nothing left, or sigmoids of logits that are all below -708, 0 in 64 bits too) gives
+ * weights 0.  A row with a NaN still gets K distinct experts in [0, E); its weights may be
+ * NaN. */
 int moe_route_logits(const void *logits, int logits_fp32, const float *bias, int T, int E, int K,
                      const moe_routing_t *routing, int32_t *topk_idx, float *topk_w, void *stream);
 

@@ -38,3 +38,61 @@ def test_groups_of_masked_and_of_excluded_experts(E, group_top):
     for scoring in ("sigmoid", "softmax"):
         idx, _ = R._check(l, b, 8, scoring=scoring, n_group=2, topk_group=1, group_top=group_top)
         assert bool((idx[:, 0] == E // 2 + 5).all())
+
+
+# A weight is a score over a sum of K scores: each a handful of fp32 roundings (exp, its
+# argument's rounding of up to 128 x 2^-24, sum, reciprocal).
+REL = (128 + 32) * 2.0 ** -24
+
+
+def _selected_weights(l, idx):
+    """softmax of the selected logits, 64 bits."""
+    v = np.take_along_axis(l.double().cpu().numpy(), idx.cpu().numpy().astype(np.int64), 1)
+    e = np.exp(v - v.max(1, keepdims=True))
+    return e / e.sum(1, keepdims=True)
+
+
+@pytest.mark.parametrize("depth", [95.0, 120.0])
+def test_softmax_weights_of_experts_far_below_the_maximum(depth):
+    # a bias that keeps the row's largest logits out: the weights are a softmax of the selected
+    T, E, K = 64, 40, 6
+    l = R._logits(T, E, F32, seed=12)
+    l[:, 3] = l[:, 3] + depth
+    b = torch.zeros(E, device=DEV)
+    b[3] = -10.0
+    l[1, 7] = -float("inf")
+    idx, w = R._route(l, b, K, scoring="softmax")
+    assert not bool((idx == 3).any())
+    ref = _selected_weights(l, idx)
+    assert bool((np.abs(w.double().cpu().numpy() - ref) <= REL * ref).all())
+    # ... and the gradient is that of these weights
+    dw = torch.linspace(-1, 1, K, device=DEV).expand(T, K).contiguous()
+    out = torch.empty_like(l)
+    B.moe_route_logits_backward(l, dict(scoring="softmax"), idx, dw, out)
+    d = dw.double().cpu().numpy()
+    want = ref * (d - (ref * d).sum(1, keepdims=True))
+    got = out.gather(1, idx.long()).double().cpu().numpy()
+    assert bool((np.abs(got - want) <= 4 * REL * ref).all())
+
+
+@pytest.mark.parametrize("at", [-60.0, -90.0, -300.0])
+def test_sigmoid_weights_of_small_scores(at):
+    # scores that fp32 cannot hold, whose ratios it can: sigmoid(l) is e^l to e^l of itself
+    T, E, K = 64, 40, 6
+    l = R._logits(T, E, F32, seed=13) + at
+    l[1, :20] = -float("inf")
+    l[2] = -float("inf")
+    l[3] = -1e35                                    # a score of 0 in 64 bits too
+    idx, w = R._route(l, None, K)
+    live = [t for t in range(T) if t not in (2, 3)]
+    ref = _selected_weights(l[live], idx[live])
+    assert bool((np.abs(w[live].double().cpu().numpy() - ref) <= REL * ref).all())
+    assert not bool(w[[2, 3]].any())
+    dw = torch.linspace(-1, 1, K, device=DEV).expand(T, K).contiguous()
+    out = torch.empty_like(l)
+    B.moe_route_logits_backward(l, None, idx, dw, out)
+    d = dw[live].double().cpu().numpy()
+    want = ref * (d - (ref * d).sum(1, keepdims=True))
+    got = out.gather(1, idx.long())[live].double().cpu().numpy()
+    assert bool((np.abs(got - want) <= 4 * REL * ref).all())
+    assert not bool(out[[2, 3]].any())
