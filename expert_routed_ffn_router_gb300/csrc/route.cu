@@ -30,6 +30,8 @@
 //   sigmoid                dl_j = s_j (1 - s_j) dw_j
 //   softmax, renormalised  dl_j = w_j (dw_j - D)            (a softmax of the selected logits)
 //   softmax                dl_e = s_e ([e selected] dw_e - sum_k s_k dw_k)    for every e
+// (1 - s is taken as sigmoid(-l): the difference would lose what a saturated gate has left, 1e-3
+// of it at a logit of 10 and all of it from 17 on.)
 #include <cfloat>
 
 #include "common.cuh"
@@ -686,16 +688,15 @@ __global__ void __launch_bounds__(32 * WPC) route_bwd_kernel(const RouteBwdArgs 
         // (a softmax is renormalised here)
         float s = a.softmax ? selected_exp(l, e >= 0) : (e >= 0 ? sigmoid(l) : 0.f);
         if (a.renorm) {
-            const float rest = a.softmax ? 1.f : 1.f - s;
             float sum = warp_sum(s);
             if (!a.softmax && sum < kSmallSum) {
                 s = small_scores(l, e >= 0);
                 sum = warp_sum(s);
             }
             const float w = sum == 0.f ? 0.f : s / sum;
-            d = w * (dw - warp_sum(w * dw)) * rest;
+            d = w * (dw - warp_sum(w * dw)) * (a.softmax ? 1.f : sigmoid(-l));
         } else {
-            d = s * (1.f - s) * dw;
+            d = s * sigmoid(-l) * dw;
         }
     }
     if (e >= 0) row[e] += d;

@@ -96,3 +96,24 @@ def test_sigmoid_weights_of_small_scores(at):
     got = out.gather(1, idx.long())[live].double().cpu().numpy()
     assert bool((np.abs(got - want) <= 4 * REL * ref).all())
     assert not bool(out[[2, 3]].any())
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_of_saturated_gates(renorm):
+    # 1 - s of a logit of 10 to 80 is e^-l: relative to its size
+    T, E = 71, 8
+    l = torch.full((T, E), -5.0, device=DEV)
+    l[:, 2] = torch.arange(10, 81, device=DEV).float()
+    l[:, 5] = torch.arange(10, 81, device=DEV).float() + 0.5
+    idx = torch.tensor([[5, 2]], dtype=torch.int32, device=DEV).expand(T, 2).contiguous()
+    dw = torch.tensor([[1.0, -0.5]], device=DEV).expand(T, 2).contiguous()
+    out = torch.empty_like(l)
+    B.moe_route_logits_backward(l, dict(renorm=renorm), idx, dw, out)
+    x = l.double().cpu().gather(1, idx.long().cpu()).numpy()
+    s, q, d = 1 / (1 + np.exp(-x)), 1 / (1 + np.exp(x)), dw.double().cpu().numpy()
+    w = s / s.sum(1, keepdims=True)
+    want = w * (d - (w * d).sum(1, keepdims=True)) * q if renorm else s * q * d
+    got = out.gather(1, idx.long()).double().cpu().numpy()
+    assert bool((np.abs(got - want) <= REL * np.abs(want)).all())
+    out[:, [2, 5]] = 0
+    assert not bool(out.any())
