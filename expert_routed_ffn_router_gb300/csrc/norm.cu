@@ -151,6 +151,14 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
+// After a wait that ran out, by the thread that issued the copies, fill f to stage f % S: those
+// in flight land (the last S at most, each its stage's last) before the CTA leaves.
+__device__ __forceinline__ void drain(uint64_t *full, int S, int fills)
+{
+    int dummy = 0;
+    for (int f = max(0, fills - S); f < fills; ++f) mbar_wait(&full[f % S], (f / S) & 1u, &dummy, nullptr, 20000000ull);
+}
+
 template <bool F32>
 __device__ __forceinline__ float4 load4(const void *p, int c)
 {
@@ -195,10 +203,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kerne
     __syncthreads();
     pdl_wait();
     constexpr int XB = XF32 ? 4 : 2;
+    int fills = 0;                           // (thread 0)
     auto fill = [&](int row, int s) {
         mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(H) * XB);
         bulk_load(ring + static_cast<size_t>(s) * p.stage_bytes,
                   static_cast<const unsigned char *>(p.x) + static_cast<size_t>(row) * H * XB, H * XB, &full[s]);
+        ++fills;
     };
     const int step = gridDim.x;
     int ahead = blockIdx.x;                  // next row to fill (thread 0)
@@ -255,12 +265,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kerne
         }
         if (++s == S) { s = 0; ph ^= 1u; }
     }
-    // (after a wait that ran out: copies in flight land before the CTA leaves)
     __syncthreads();
-    if (*abort_flag && tid == 0) {
-        int dummy = 0;
-        for (int j = 0; j < S; ++j) mbar_wait(&full[j], ph, &dummy, nullptr, 20000000ull);
-    }
+    if (*abort_flag && tid == 0) drain(full, S, fills);
 }
 
 struct NormBwd {
@@ -377,6 +383,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_bwd_ring_kernel(const NormBwd
     __syncthreads();
     pdl_wait();
     constexpr int XB = XF32 ? 4 : 2;
+    int fills = 0;                           // (thread 0)
     auto fill = [&](int row, int s) {
         unsigned char *st = ring + static_cast<size_t>(s) * p.stage_bytes;
         const size_t base = static_cast<size_t>(row) * H;
@@ -384,6 +391,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_bwd_ring_kernel(const NormBwd
         bulk_load(st, static_cast<const unsigned char *>(p.x) + base * XB, H * XB, &full[s]);
         bulk_load(st + p.off_dy, p.dy + base, H * 2, &full[s]);
         if (p.res_staged) bulk_load(st + p.off_res, static_cast<const unsigned char *>(p.dres) + base * XB, H * XB, &full[s]);
+        ++fills;
     };
     const int first = blockIdx.x, step = gridDim.x;
     int ahead = first;                       // next row to fill (thread 0)
@@ -458,12 +466,8 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_bwd_ring_kernel(const NormBwd
         prev = s;
         if (++s == S) { s = 0; ph ^= 1u; }
     }
-    // (after a wait that ran out: copies in flight land before the CTA leaves)
     __syncthreads();
-    if (*abort_flag && tid == 0) {
-        int dummy = 0;
-        for (int j = 0; j < S; ++j) mbar_wait(&full[j], ph, &dummy, nullptr, 20000000ull);
-    }
+    if (*abort_flag && tid == 0) drain(full, S, fills);
     float *part = p.part + static_cast<size_t>(blockIdx.x) * 2 * H;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
