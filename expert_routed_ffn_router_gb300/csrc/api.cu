@@ -679,7 +679,7 @@ int moe_layer_norm(const void *x, int x_fp32, const float *gamma, const float *b
     if (T == 0) return MOE_OK;
     if ((rc = check_ptrs({x, gamma, y}))) return rc;
     if ((rc = check_opt(beta)) || (rc = check_opt(mean)) || (rc = check_opt(rstd))) return rc;
-    return cuda_status(launch_norm(x, x_fp32, gamma, beta, T, H, eps, y, mean, rstd,
+    return cuda_status(launch_norm(x, x_fp32, gamma, beta, T, H, eps, y, mean, rstd, g_wait_limit_ns, g_inject_stall,
                                    static_cast<cudaStream_t>(stream)));
 }
 
@@ -708,7 +708,7 @@ int moe_layer_norm_backward(const void *dy, const void *x, int x_fp32, const flo
     return debug_status(cuda_status(launch_norm_bwd(
                             dy, x, x_fp32, gamma, mean, rstd, dres, T, H, dx, dgamma, dbeta,
                             reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeader),
-                            static_cast<int *>(ws), g_wait_limit_ns, st)),
+                            static_cast<int *>(ws), g_wait_limit_ns, g_inject_stall, st)),
                         ws, stream);
 }
 

@@ -83,13 +83,14 @@ cudaError_t launch_combine(const void *Yp, const int32_t *slot_pos, const float 
 // ------------------------------------------------------------------------- layer norm
 // Rows x [T][H] (bf16, or fp32) -> y bf16; mean and rstd [T] (nullable) for the backward pass.
 cudaError_t launch_norm(const void *x, int x_fp32, const float *gamma, const float *beta, int T, int H,
-                        float eps, void *y, float *mean, float *rstd, cudaStream_t s);
+                        float eps, void *y, float *mean, float *rstd, unsigned long long timeout_ns, int inject,
+                        cudaStream_t s);
 // CTAs of the backward launch; each leaves 2 H partial sums in `part`.
 int norm_bwd_ctas(int T, int H);
 cudaError_t launch_norm_bwd(const void *dy, const void *x, int x_fp32, const float *gamma, const float *mean,
                             const float *rstd, const void *dres, int T, int H, void *dx, float *dgamma,
                             float *dbeta, float *part, int *status, unsigned long long timeout_ns,
-                            cudaStream_t s);
+                            int inject, cudaStream_t s);
 
 // --------------------------------------------------------------- routing from given logits
 cudaError_t launch_route(const void *logits, int fp32, const float *bias, int T, int E, int K,

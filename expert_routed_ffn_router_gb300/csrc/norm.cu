@@ -172,8 +172,8 @@ __device__ __forceinline__ float4 load4(const void *p, int c)
 // stage is filled again behind the barrier of its mean.  (A CTA per row, 448 threads of plain
 // loads, took 154 us for 16384 rows of 7168 in fp32 and 163 us in bf16; this: 130 and 115 us, 5.4
 // and 4.1 TB/s.  Two barriers a row bound it, not the loads: more CTAs an SM would need fewer
-// registers.  A wait that runs out leaves the CTA's later rows void; the entry point has no status
-// word to record it in.)
+// registers.)  The entry point has no status word: a CTA whose wait runs out takes its rows from
+// there on by plain loads, so the results hold.
 struct NormFwd {
     const void *x;
     const float *gamma, *beta;     // beta nullable
@@ -183,10 +183,47 @@ struct NormFwd {
     float *mean, *rstd;            // nullable
     int stages, stage_bytes;
     unsigned long long timeout_ns;
+    int inject;                    // no copies: every wait runs out (testing)
 };
 
+// Rows `row`, + step, ... of the forward ring without it, by the whole CTA (out of line: rare).
+template <bool XF32>
+__device__ __noinline__ void norm_rows(const NormFwd &p, int row, int step, float (*red)[32])
+{
+    constexpr int XB = XF32 ? 4 : 2;
+    const float inv = 1.f / static_cast<float>(p.H);
+    for (; row < p.T; row += step) {
+        const size_t base = static_cast<size_t>(row) * p.H;
+        const unsigned char *x = static_cast<const unsigned char *>(p.x) + base * XB;
+        float a = 0.f;
+        for (int c = 4 * threadIdx.x; c < p.H; c += 4 * blockDim.x) {
+            const float4 v = load4<XF32>(x, c);
+            a += (v.x + v.y) + (v.z + v.w);
+        }
+        const float mu = row_sum<false>(a, red[0]) * inv;
+        a = 0.f;
+        for (int c = 4 * threadIdx.x; c < p.H; c += 4 * blockDim.x) {
+            float4 v = load4<XF32>(x, c);
+            v = make_float4(v.x - mu, v.y - mu, v.z - mu, v.w - mu);
+            a += fmaf(v.x, v.x, v.y * v.y) + fmaf(v.z, v.z, v.w * v.w);
+        }
+        const float r = 1.f / sqrtf(row_sum<false>(a, red[1]) * inv + p.eps);
+        for (int c = 4 * threadIdx.x; c < p.H; c += 4 * blockDim.x) {
+            const float4 v = load4<XF32>(x, c), g = load4<true>(p.gamma, c);
+            const float4 b = p.beta ? load4<true>(p.beta, c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<uint2 *>(p.y + base + c) =
+                make_uint2(f32x2_to_bf16x2((v.y - mu) * r * g.y + b.y, (v.x - mu) * r * g.x + b.x),
+                           f32x2_to_bf16x2((v.w - mu) * r * g.w + b.w, (v.z - mu) * r * g.z + b.z));
+        }
+        if (threadIdx.x == 0) {
+            if (p.mean) p.mean[row] = mu;
+            if (p.rstd) p.rstd[row] = r;
+        }
+    }
+}
+
 template <bool XF32, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kernel(const NormFwd p)
+__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kernel(const __grid_constant__ NormFwd p)
 {
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ float red[2][32];
@@ -203,16 +240,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kerne
     __syncthreads();
     pdl_wait();
     constexpr int XB = XF32 ? 4 : 2;
-    int fills = 0;                           // (thread 0)
     auto fill = [&](int row, int s) {
         mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(H) * XB);
         bulk_load(ring + static_cast<size_t>(s) * p.stage_bytes,
                   static_cast<const unsigned char *>(p.x) + static_cast<size_t>(row) * H * XB, H * XB, &full[s]);
-        ++fills;
     };
     const int step = gridDim.x;
     int ahead = blockIdx.x;                  // next row to fill (thread 0)
-    if (tid == 0)
+    if (tid == 0 && !p.inject)
         for (int s = 0; s < S && ahead < p.T; ++s, ahead += step) fill(ahead, s);
     const float inv = 1.f / static_cast<float>(H);
     int s = 0;
@@ -223,7 +258,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kerne
         __syncthreads();
         return warp_sum((tid & 31) < nw ? r[tid & 31] : 0.f);
     };
-    for (int row = blockIdx.x; row < p.T; row += step) {
+    int row = blockIdx.x;
+    for (; row < p.T; row += step) {
         mbar_wait(&full[s], ph, abort_flag, nullptr, p.timeout_ns);
         const unsigned char *st = ring + static_cast<size_t>(s) * p.stage_bytes;
         float4 v[VPT];
@@ -235,8 +271,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kerne
             a += (v[i].x + v[i].y) + (v[i].z + v[i].w);
         }
         const float mu = sum(a, red[0]) * inv;
+        // a wait of this row ran out for some thread (the flag of a later one's comes behind the
+        // second barrier, so all threads leave together)
+        if (*abort_flag) break;
         // (every thread has read the row: its stage takes a row further on)
-        if (tid == 0 && ahead < p.T && !*abort_flag) {
+        if (tid == 0 && ahead < p.T) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             fill(ahead, s);
             ahead += step;
@@ -265,8 +304,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 3 : 1) norm_fwd_ring_kerne
         }
         if (++s == S) { s = 0; ph ^= 1u; }
     }
-    __syncthreads();
-    if (*abort_flag && tid == 0) drain(full, S, fills);
+    if (row < p.T) {
+        if (tid == 0) drain(full, S, (ahead - static_cast<int>(blockIdx.x)) / step);
+        norm_rows<XF32>(p, row, step, red);
+    }
 }
 
 struct NormBwd {
@@ -282,6 +323,7 @@ struct NormBwd {
     int stages, res_staged, off_dy, off_res, stage_bytes;
     int *status;
     unsigned long long timeout_ns;
+    int inject;            // no copies: every wait runs out (testing)
 };
 
 // Rows of up to WARP_COLS_BWD columns: a warp per row, its weight sums in registers; the CTA's
@@ -383,7 +425,6 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_bwd_ring_kernel(const NormBwd
     __syncthreads();
     pdl_wait();
     constexpr int XB = XF32 ? 4 : 2;
-    int fills = 0;                           // (thread 0)
     auto fill = [&](int row, int s) {
         unsigned char *st = ring + static_cast<size_t>(s) * p.stage_bytes;
         const size_t base = static_cast<size_t>(row) * H;
@@ -391,11 +432,10 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_bwd_ring_kernel(const NormBwd
         bulk_load(st, static_cast<const unsigned char *>(p.x) + base * XB, H * XB, &full[s]);
         bulk_load(st + p.off_dy, p.dy + base, H * 2, &full[s]);
         if (p.res_staged) bulk_load(st + p.off_res, static_cast<const unsigned char *>(p.dres) + base * XB, H * XB, &full[s]);
-        ++fills;
     };
     const int first = blockIdx.x, step = gridDim.x;
     int ahead = first;                       // next row to fill (thread 0)
-    if (tid == 0)
+    if (tid == 0 && !p.inject)
         for (int s = 0; s < S && ahead < p.T; ++s, ahead += step) fill(ahead, s);
     float4 g[GREG ? VPT : 1], dg[VPT], db[VPT];
 #pragma unroll
@@ -467,7 +507,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_bwd_ring_kernel(const NormBwd
         if (++s == S) { s = 0; ph ^= 1u; }
     }
     __syncthreads();
-    if (*abort_flag && tid == 0) drain(full, S, fills);
+    if (*abort_flag && tid == 0) drain(full, S, (ahead - first) / step);
     float *part = p.part + static_cast<size_t>(blockIdx.x) * 2 * H;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -524,7 +564,7 @@ cudaError_t fwd_ring(const NormFwd &p, int ctas, cudaStream_t s)
 
 template <bool XF32>
 cudaError_t fwd(const void *x, const float *gamma, const float *beta, int T, int H, float eps, uint16_t *y,
-                float *mean, float *rstd, cudaStream_t s)
+                float *mean, float *rstd, unsigned long long timeout_ns, int inject, cudaStream_t s)
 {
     const dim3 warps(32, ROWS_PER_CTA), gw((T + ROWS_PER_CTA - 1) / ROWS_PER_CTA);
     if (H <= 256) return launch_pdl(norm_fwd_kernel<XF32, 1, true>, gw, warps, 0, s, 1, x, gamma, beta, T, H, eps, y, mean, rstd);
@@ -533,7 +573,7 @@ cudaError_t fwd(const void *x, const float *gamma, const float *beta, int T, int
     // (up to eight rows a CTA of the ring, the plain launch's parallel rows are as fast)
     const int ctas = fwd_ctas(H, XF32 ? 4 : 2);
     if (T >= 8 * ctas) {
-        NormFwd p{x, gamma, beta, T, H, eps, y, mean, rstd, 0, H * (XF32 ? 4 : 2), 1000000000ull};
+        NormFwd p{x, gamma, beta, T, H, eps, y, mean, rstd, 0, H * (XF32 ? 4 : 2), timeout_ns, inject};
         const size_t room = RING_BYTES / (ctas / num_sms());
         p.stages = static_cast<int>(room / p.stage_bytes < 4 ? room / p.stage_bytes : 4);
         return H <= 8192 ? fwd_ring<XF32, 4, 512>(p, ctas, s) : fwd_ring<XF32, 4, 1024>(p, ctas, s);
@@ -608,20 +648,21 @@ int norm_bwd_ctas(int T, int H)
 }
 
 cudaError_t launch_norm(const void *x, int x_fp32, const float *gamma, const float *beta, int T, int H,
-                        float eps, void *y, float *mean, float *rstd, cudaStream_t s)
+                        float eps, void *y, float *mean, float *rstd, unsigned long long timeout_ns, int inject,
+                        cudaStream_t s)
 {
     uint16_t *o = static_cast<uint16_t *>(y);
-    return x_fp32 ? fwd<true>(x, gamma, beta, T, H, eps, o, mean, rstd, s)
-                  : fwd<false>(x, gamma, beta, T, H, eps, o, mean, rstd, s);
+    return x_fp32 ? fwd<true>(x, gamma, beta, T, H, eps, o, mean, rstd, timeout_ns, inject, s)
+                  : fwd<false>(x, gamma, beta, T, H, eps, o, mean, rstd, timeout_ns, inject, s);
 }
 
 cudaError_t launch_norm_bwd(const void *dy, const void *x, int x_fp32, const float *gamma, const float *mean,
                             const float *rstd, const void *dres, int T, int H, void *dx, float *dgamma,
                             float *dbeta, float *part, int *status, unsigned long long timeout_ns,
-                            cudaStream_t s)
+                            int inject, cudaStream_t s)
 {
     NormBwd p{static_cast<const uint16_t *>(dy), x, gamma, mean, rstd, dres, dx, part, T, H, 0, 0, 0, 0, 0,
-              status, timeout_ns};
+              status, timeout_ns, inject};
     int n = 0;
     const cudaError_t e = x_fp32 ? bwd<true>(p, n, s) : bwd<false>(p, n, s);
     if (e != cudaSuccess) return e;

@@ -153,11 +153,12 @@ int moe_read_status(void *ws, void *stream);
 void moe_debug_set_sync_status(int on);
 
 /* Testing hook: sets the limit of the bounded device-side waits of the tensor-core FFN
- * kernels, forward and backward, and of moe_layer_norm_backward (0 restores the default of
- * one second) and, with inject_stall = 1, makes the TMA producer of the FFN kernels skip its
- * work so that the waits run out and MOE_ERR_DEVICE_TIMEOUT is recorded in the status word
- * (no fault, no hang).  Affects later calls of these and of moe_layer_forward in the process;
- * not for production use. */
+ * kernels, forward and backward, and of moe_layer_norm and moe_layer_norm_backward (0 restores
+ * the default of one second) and, with inject_stall = 1, makes the TMA producers of the FFN
+ * kernels and the norms' copies of rows skip their work so that the waits run out and
+ * MOE_ERR_DEVICE_TIMEOUT is recorded in the status word (no fault, no hang; moe_layer_norm has
+ * none and reads the rows another way).  Affects later calls of these and of moe_layer_forward
+ * in the process; not for production use. */
 void moe_debug_set_wait_limit(unsigned long long limit_ns, int inject_stall);
 
 /* Profiling hook: with `events` pointing at n >= 6 cudaEvent_t handles, every later
@@ -394,7 +395,8 @@ int moe_layer_forward_fp8(const moe_shape_t *shape, const moe_weights_fp8_t *wei
  *   gamma  fp32 [H], beta fp32 [H] or NULL (no shift)
  *   out y  bf16 [T, H]; mean, rstd fp32 [T] (each nullable: kept for the backward pass)
  * Sums are fp32, the variance is that of the centred row.  H a multiple of 64, at most 16384
- * (else MOE_ERR_UNSUPPORTED_SHAPE); eps < 0 or NaN: MOE_ERR_INVALID_ARG. */
+ * (else MOE_ERR_UNSUPPORTED_SHAPE); eps < 0 or NaN: MOE_ERR_INVALID_ARG.  No status word: the
+ * results hold even where a bounded wait ran out. */
 int moe_layer_norm(const void *x, int x_fp32, const float *gamma, const float *beta, int T, int H,
                    float eps, void *y, float *mean, float *rstd, void *stream);
 
