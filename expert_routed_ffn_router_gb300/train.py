@@ -157,8 +157,9 @@ def fit(steps=30, T=512, H=256, E=16, K=2, I=128, Is=128, lr=2.0, seed=0, device
         for n, v in grads.items():
             master[n] -= lr * v.float()
             weights[n].copy_(master[n])
-    if block.status() != 0:
-        raise B.MoeError("training step", block.status())
+    status = block.status()                      # (reading it resets it)
+    if status != 0:
+        raise B.MoeError("training step", status)
     return losses
 
 
