@@ -4,8 +4,9 @@
 
 with the routing weights w of a gate that is trained: logits = n W_gate^T in fp32.  Between the
 forward and the backward pass the block keeps x, the norm's statistics, the logits, the routing
-and its dispatch, and n as an 8-bit checkpoint (E4M3 bytes and exponents, about half of bf16;
-``packed=False`` keeps it in bf16); the experts' activations are computed again.
+and its dispatch, and n in bf16, or with ``packed=True`` as an 8-bit checkpoint (E4M3 bytes and
+exponents, half the memory; the gradients are then those of rows with a 3-bit mantissa); the
+experts' activations are computed again.
 
     block = MoETrainBlock(weights, T=4096, K=8)
     out = block.forward(x)                  # x fp32 or bf16 [T, H]
@@ -37,7 +38,7 @@ class MoETrainBlock:
     [H, Is], W2s [Is, H].  routing: as for moe_route_logits."""
 
     def __init__(self, weights: dict, T: int, K: int, routing=None, eps: float = 1e-5,
-                 packed: bool = True, x_dtype=F32):
+                 packed: bool = False, x_dtype=F32):
         self.w, self.T, self.K, self.eps, self.packed = weights, T, K, eps, packed
         self.routing = B.MoeRouting.make(**routing) if isinstance(routing, dict) else routing
         self.E, self.H, self.I = weights["W1"].shape
@@ -141,7 +142,7 @@ def random_weights(H, E, I, Is, device, seed=0) -> dict:
     return w
 
 
-def fit(steps=30, T=512, H=256, E=16, K=2, I=128, Is=128, lr=2.0, seed=0, device="cuda", packed=True):
+def fit(steps=30, T=512, H=256, E=16, K=2, I=128, Is=128, lr=2.0, seed=0, device="cuda", packed=False):
     """Plain gradient descent on mean (out - target)^2 over one fixed batch; the losses."""
     g = torch.Generator(device=device).manual_seed(seed + 1)
     x = torch.randn(T, H, generator=g, device=device)
@@ -168,9 +169,11 @@ def main(argv=None):
     ap.add_argument("--steps", type=int, default=30)
     ap.add_argument("--T", type=int, default=512)
     ap.add_argument("--lr", type=float, default=2.0)
-    ap.add_argument("--bf16-rows", action="store_true", help="keep the token rows in bf16, not in 8 bits")
+    rows = ap.add_mutually_exclusive_group()
+    rows.add_argument("--packed", action="store_true", help="keep the token rows in 8 bits for the backward pass")
+    rows.add_argument("--bf16-rows", action="store_true", help="keep them in bf16 (the default)")
     a = ap.parse_args(argv)
-    for i, v in enumerate(fit(steps=a.steps, T=a.T, lr=a.lr, packed=not a.bf16_rows)):
+    for i, v in enumerate(fit(steps=a.steps, T=a.T, lr=a.lr, packed=a.packed)):
         print(f"step {i:3d}  loss {v:.6f}")
 
 
