@@ -170,7 +170,7 @@ __device__ __forceinline__ float4 load4(const void *p, int c)
 // Longer rows of a batch that gives every CTA several: the rows of x arrive by bulk copies in a
 // ring of shared-memory stages, 4 x VPT columns a thread in registers from there.  A row's
 // stage is filled again behind the barrier of its mean.  (A CTA per row, 448 threads of plain
-// loads, took 154 us for 16384 rows of 7168 in fp32 and 163 us in bf16; this: 130 and 115 us, 5.4
+// loads, took 154 us for 16384 rows of 7168 in fp32 and 163 us in bf16; this: 129 and 113 us, 5.5
 // and 4.1 TB/s.  Two barriers a row bound it, not the loads: more CTAs an SM would need fewer
 // registers.)  The entry point has no status word: a CTA whose wait runs out takes its rows from
 // there on by plain loads, so the results hold.
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(32 * ROWS_PER_CTA) norm_bwd_warp_kernel(const 
 // Longer rows: a CTA per row, 4 x VPT columns a thread.  The rows x, dy (and dres) of the CTA
 // arrive by bulk copies in a ring of shared-memory stages, so that loads never wait for a
 // row's two sums (plain loads before and after the barriers of two CTAs an SM: 402 us for
-// 16384 rows of 7168 in fp32 with dres, 4.1 TB/s; this: 242 us, 6.8 TB/s, the copy bandwidth).
+// 16384 rows of 7168 in fp32 with dres, 4.1 TB/s; this: 247 us, 6.7 TB/s, 98% of the copy bandwidth).
 // One barrier a row: its sums; a row's stage is filled again behind the next row's.  GREG: gamma
 // stays in registers.
 template <bool XF32, int VPT, bool GREG, int MAXT, int CTAS>

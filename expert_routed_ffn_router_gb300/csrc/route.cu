@@ -22,7 +22,7 @@
 // are evaluated again in fp64, one a lane (a softmax, or group scores too close: the whole
 // row, rare).
 //
-// The batch above with 8 groups (4 kept, two values each) and a bias takes 18 us: about 800
+// The batch above with 8 groups (4 kept, two values each) and a bias takes 19 us: about 800
 // instructions a token, where its bytes would take 2.6 us.  Two tokens take the launch's time.
 //
 // Gradient (D = sum_k w_k dw_k over the selected):

@@ -12,9 +12,15 @@ experts' activations are computed again.
     out = block.forward(x)                  # x fp32 or bf16 [T, H]
     dx, grads = block.backward(dout)        # dout of x's type
 
-Buffers and workspaces are allocated once; both passes only enqueue work on the current stream
-and can be captured in a CUDA graph.  The two products with the gate are plain library
-products (torch.mm); everything else runs in the library's kernels.
+Outputs, what is kept and the workspace are allocated once; the gate's products, in fp32, and the
+sum of the branches' gradients take temporaries of torch's allocator in each pass (fp32 copies of
+n and dn, T x H each).  Both passes only enqueue work on the current stream and can be captured in
+a CUDA graph.  The three products with the gate are plain library products (torch.mm); the
+additions and casts around them are torch's, everything else runs in the library's kernels.
+
+Roundings of the gradient that reaches the norm: the experts' dX and the shared expert's are bf16
+as the kernels leave them; they are added to the gate's part in fp32, and the sum is rounded to
+bf16 once, the type moe_layer_norm_backward takes.
 
     python -m expert_routed_ffn_router_gb300.train --steps 30
 
@@ -101,7 +107,8 @@ class MoETrainBlock:
         return self.out
 
     def backward(self, dout: torch.Tensor):
-        """Gradient of the last forward call's output -> (dx, gradients by weight name)."""
+        """Gradient of the last forward call's output -> (dx, gradients by weight name): the
+        block's own buffers, which the next call overwrites."""
         if self.x is None:
             raise RuntimeError("backward() before forward()")
         w, g = self.w, self.grads
