@@ -579,8 +579,14 @@ __global__ void __launch_bounds__(NT, 1) bwd_gemm_kernel(const __grid_constant__
                     }
                 }
             }
-            // every copy issued lands before the CTAs can exit (the even CTA's barriers
-            // count both CTAs' copies)
+            // Every copy issued lands before the CTAs can exit: the even CTA's barriers count both
+            // CTAs' copies.  After a wait that ran out the odd CTA may have issued stages that the
+            // even one has not, whose barriers then say nothing: it stays as long as the even one
+            // waits for a stage at most.
+            if (!leader && *abort_flag) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 20000000ull) __nanosleep(1000);
+            }
             if (leader) {
                 const uint32_t n = it < STAGES ? it : STAGES;
                 for (uint32_t j = it - n; j < it; ++j) {
