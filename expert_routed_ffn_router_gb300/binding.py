@@ -59,6 +59,20 @@ class MoeWeightsFp8(ctypes.Structure):
                                                "S2", "W1s", "W3s", "W2s", "S1s", "S3s", "S2s")]
 
 
+class MoeResidual(ctypes.Structure):
+    """moe_residual_t."""
+    _fields_ = [("post", ctypes.c_int32), ("pre", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("eps_post", ctypes.c_float), ("eps_pre", ctypes.c_float)] + [
+                    (n, ctypes.c_void_p) for n in ("gamma_post", "beta_post", "gate", "gate_token", "gamma_pre",
+                                                   "beta_pre")]
+
+
+class MoeResidualGrads(ctypes.Structure):
+    """moe_residual_grads_t."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gamma_post", "beta_post", "gate", "gate_token", "gamma_pre",
+                                               "beta_pre")]
+
+
 class MoeGraceReplication(ctypes.Structure):
     _fields_ = [("heaviest", ctypes.c_int32), ("n_replica", ctypes.c_int32),
                 ("n_hot", ctypes.c_int32), ("rho", ctypes.c_double), ("W_mean", ctypes.c_double),
@@ -123,6 +137,12 @@ def load(build_if_missing: bool = True):
         "moe_checkpoint_unpack": ([P, P, ctypes.c_longlong, I, P, P], I),
         "moe_expert_ffn_backward_workspace_bytes": ([I, I, I, I, I], Z),
         "moe_expert_ffn_backward": ([P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P, P, P, Z, P], I),
+        "moe_combine_backward": ([P, I, P, P, P, I, I, I, P, P, P], I),
+        "moe_dispatch_backward": ([P, P, P, I, I, I, P, I, P], I),
+        "moe_residual_norm": ([P, I, P, I, ctypes.POINTER(MoeResidual), I, I, P, P, P, P], I),
+        "moe_residual_norm_backward_workspace_bytes": ([I, I], Z),
+        "moe_residual_norm_backward": ([P, P, P, I, P, I, P, ctypes.POINTER(MoeResidual), I, I, P, P,
+                                        ctypes.POINTER(MoeResidualGrads), P, Z, P], I),
         "moe_grace_metrics": ([P, I, P, I, P, P], I),
         "moe_grace_group": ([P, I, I, ctypes.c_double, P], I),
         "moe_grace_choose_r": ([P, I, I, P, I, P, P, P, P], I),
@@ -517,6 +537,76 @@ def moe_expert_ffn_backward(x, x_scale, dY, offsets, slot_pos, topk_w, W1, W3, W
         (dW3, BF16, n, "dW3"), (dW2, BF16, n, "dW2"))
     _check("moe_expert_ffn_backward", load().moe_expert_ffn_backward(
         xp, xs, dy, o, sp, w, T, H, E, K, I, w1, w3, w2, dx, dw, d1, d3, d2, *_ws(ws), _stream(stream)))
+
+
+def moe_combine_backward(dY, Yp, slot_pos, topk_w, dYp, d_topk_w=None, stream=None):
+    """dY bf16 or fp32 [T, H]; topk_w (all 1), d_topk_w (not wanted) and with it Yp may be None."""
+    T, K = slot_pos.shape
+    H, f = dY.shape[1], _fp32_flag(dY, "dY")
+    d, y, s, w, o, dw = _ptrs((dY, dY.dtype, T * H, "dY"), (Yp, BF16, T * K * H, "Yp"), (slot_pos, I32, T * K, "slot_pos"),
+                              (topk_w, F32, T * K, "topk_w"), (dYp, BF16, T * K * H, "dYp"),
+                              (d_topk_w, F32, T * K, "d_topk_w"))
+    _check("moe_combine_backward", load().moe_combine_backward(d, f, y, s, w, T, H, K, o, dw, _stream(stream)))
+
+
+def moe_dispatch_backward(dXp, slot_pos, dres, dX, stream=None):
+    """dX bf16 or fp32 [T, H]; dres of its type, or None."""
+    T, K = slot_pos.shape
+    H, f = dX.shape[1], _fp32_flag(dX, "dX")
+    p, s, r, o = _ptrs((dXp, BF16, T * K * H, "dXp"), (slot_pos, I32, T * K, "slot_pos"),
+                       (dres, dX.dtype, T * H, "dres"), (dX, dX.dtype, T * H, "dX"))
+    _check("moe_dispatch_backward", load().moe_dispatch_backward(p, s, r, T, H, K, o, f, _stream(stream)))
+
+
+_NORMS = {"none": 0, "layer": 1, "rms": 2}
+_RESIDUAL_SCALARS = ("post", "pre", "alpha", "eps_post", "eps_pre")
+_RESIDUAL_COLUMNS = ("gamma_post", "beta_post", "gate", "gate_token", "gamma_pre", "beta_pre")
+
+
+def _column_specs(d, T, H, scalars=(), prefix=""):
+    for n in d:
+        if n not in _RESIDUAL_COLUMNS and n not in scalars:
+            raise ValueError(f"{prefix}{n}: unknown, expected some of {_RESIDUAL_COLUMNS}")
+    for n in ("post", "pre"):
+        if d.get(n, "none") not in _NORMS:
+            raise ValueError(f"{n}: {d[n]}, expected one of {tuple(_NORMS)}")
+    return [(d.get(n), F32, T if n == "gate_token" else H, prefix + n) for n in _RESIDUAL_COLUMNS]
+
+
+def _residual(p, columns):
+    return MoeResidual(_NORMS[p.get("post", "none")], _NORMS[p.get("pre", "none")], float(p.get("alpha", 1.0)),
+                       float(p.get("eps_post", 1e-5)), float(p.get("eps_pre", 1e-5)), *columns)
+
+
+def moe_residual_norm(x, y, p, r, n=None, stats=None, stream=None):
+    """p: dict with post and pre ("none", "layer" or "rms"; default "none"), alpha (default 1),
+    eps_post, eps_pre (default 1e-5) and the fp32 parameters gamma_post, beta_post, gate, gamma_pre,
+    beta_pre [H] and gate_token [T], each of which may be missing or None."""
+    T, H = x.shape
+    fx, fy = _fp32_flag(x, "x"), _fp32_flag(y, "y")
+    xp, yp, rp, np_, sp, *cols = _ptrs(
+        (x, x.dtype, T * H, "x"), (y, y.dtype, T * H, "y"), (r, x.dtype, T * H, "r"), (n, BF16, T * H, "n"),
+        (stats, F32, 4 * T, "stats"), *_column_specs(p, T, H, _RESIDUAL_SCALARS))
+    _check("moe_residual_norm", load().moe_residual_norm(xp, fx, yp, fy, ctypes.byref(_residual(p, cols)), T, H, rp,
+                                                         np_, sp, _stream(stream)))
+
+
+def moe_residual_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return int(load().moe_residual_norm_backward_workspace_bytes(int(T), int(H)))
+
+
+def moe_residual_norm_backward(dn, dr, y, r, stats, p, dx, dy, grads, ws, stream=None):
+    """p as in the forward call; grads: dict of the wanted parameters' gradients by the
+    parameters' names.  dn (without pre), dr, y and r (see the header) may be None."""
+    T, H = dx.shape
+    fx, fy = _fp32_flag(dx, "dx"), 0 if y is None else _fp32_flag(y, "y")
+    d, e, yp, rp, sp, dxp, dyp, *cols = _ptrs(
+        (dn, BF16, T * H, "dn"), (dr, dx.dtype, T * H, "dr"), (y, F32 if fy else BF16, T * H, "y"),
+        (r, dx.dtype, T * H, "r"), (stats, F32, 4 * T, "stats"), (dx, dx.dtype, T * H, "dx"), (dy, BF16, T * H, "dy"),
+        *_column_specs(p, T, H, _RESIDUAL_SCALARS), *_column_specs(grads, T, H, prefix="gradient of "))
+    _check("moe_residual_norm_backward", load().moe_residual_norm_backward(
+        d, e, yp, fy, rp, fx, sp, ctypes.byref(_residual(p, cols[:6])), T, H, dxp, dyp,
+        ctypes.byref(MoeResidualGrads(*cols[6:])), *_ws(ws), _stream(stream)))
 
 
 # ------------------------------------------------------------------- convenience wrapper

@@ -741,6 +741,123 @@ int moe_route_logits_backward(const void *logits, int logits_fp32, int T, int E,
                                         static_cast<cudaStream_t>(stream)));
 }
 
+// Numbers of rows up to this leave room for a launch's steps beyond the last one in an int.
+constexpr int kMaxRows = 0x7fffffff - (1 << 20);
+
+static int check_rows(int T, int H, int K)
+{
+    if (T < 0 || H <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+    if (H % 64 || K > 32 || static_cast<long long>(T) * K >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+int moe_combine_backward(const void *dY, int dY_fp32, const void *Yp, const int32_t *slot_pos,
+                         const float *topk_w, int T, int H, int K, void *dYp, float *d_topk_w, void *stream)
+{
+    int rc = check_rows(T, H, K);
+    if (rc) return rc;
+    if (dY_fp32 != 0 && dY_fp32 != 1) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((rc = check_ptrs({dY, slot_pos, dYp})) || (rc = check_opt(topk_w)) || (rc = check_opt(d_topk_w))) return rc;
+    if (d_topk_w && (rc = check_ptrs({Yp}))) return rc;
+    return cuda_status(launch_combine_bwd(dY, dY_fp32, Yp, slot_pos, topk_w, T, H, K, dYp, d_topk_w,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+int moe_dispatch_backward(const void *dXp, const int32_t *slot_pos, const void *dres, int T, int H, int K,
+                          void *dX, int dX_fp32, void *stream)
+{
+    int rc = check_rows(T, H, K);
+    if (rc) return rc;
+    if (dX_fp32 != 0 && dX_fp32 != 1) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((rc = check_ptrs({dXp, slot_pos, dX})) || (rc = check_opt(dres))) return rc;
+    return cuda_status(launch_dispatch_bwd(dXp, slot_pos, dres, T, H, K, dX, dX_fp32,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+// moe_residual_t -> validated options, with nothing in the place of what a missing norm has not
+static int check_residual(const moe_residual_t *p, int T, int H, ResidualOpts &o)
+{
+    if (!p) return MOE_ERR_INVALID_ARG;
+    int rc = check_norm(T, H);
+    if (rc) return rc;
+    if (T > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (p->post < 0 || p->post > 2 || p->pre < 0 || p->pre > 2) return MOE_ERR_INVALID_ARG;
+    if (!(p->alpha == p->alpha)) return MOE_ERR_INVALID_ARG;
+    o = ResidualOpts{p->post, p->pre, p->alpha, 0.f, 0.f, nullptr, nullptr, p->gate, p->gate_token, nullptr, nullptr};
+    if (p->post) {
+        if (!(p->eps_post >= 0.f)) return MOE_ERR_INVALID_ARG;
+        if ((rc = check_ptrs({p->gamma_post})) || (rc = check_opt(p->beta_post))) return rc;
+        o.eps_post = p->eps_post;
+        o.gamma_post = p->gamma_post;
+        o.beta_post = p->beta_post;
+    }
+    if (p->pre) {
+        if (!(p->eps_pre >= 0.f)) return MOE_ERR_INVALID_ARG;
+        if ((rc = check_ptrs({p->gamma_pre})) || (rc = check_opt(p->beta_pre))) return rc;
+        o.eps_pre = p->eps_pre;
+        o.gamma_pre = p->gamma_pre;
+        o.beta_pre = p->beta_pre;
+    }
+    if ((rc = check_opt(p->gate)) || (rc = check_opt(p->gate_token))) return rc;
+    return MOE_OK;
+}
+
+int moe_residual_norm(const void *x, int x_fp32, const void *y, int y_fp32, const moe_residual_t *p, int T,
+                      int H, void *r, void *n, float *stats, void *stream)
+{
+    ResidualOpts o;
+    int rc = check_residual(p, T, H, o);
+    if (rc) return rc;
+    if ((x_fp32 != 0 && x_fp32 != 1) || (y_fp32 != 0 && y_fp32 != 1)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((rc = check_ptrs({x, y, r})) || (rc = check_opt(stats))) return rc;
+    if (o.pre && (rc = check_ptrs({n}))) return rc;
+    return cuda_status(launch_join(o, x, x_fp32, y, y_fp32, T, H, r, n, stats, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_residual_norm_backward_workspace_bytes(int T, int H)
+{
+    if (check_norm(T, H) != MOE_OK || T > kMaxRows) return 0;
+    return kHeader + al256(static_cast<size_t>(join_bwd_ctas(T, H)) * 4 * H * sizeof(float));
+}
+
+int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, int y_fp32, const void *r,
+                               int x_fp32, const float *stats, const moe_residual_t *p, int T, int H,
+                               void *dx, void *dy, const moe_residual_grads_t *grads, void *ws,
+                               size_t ws_bytes, void *stream)
+{
+    ResidualOpts o;
+    int rc = check_residual(p, T, H, o);
+    if (rc) return rc;
+    if ((x_fp32 != 0 && x_fp32 != 1) || (y_fp32 != 0 && y_fp32 != 1)) return MOE_ERR_INVALID_ARG;
+    ResidualGrads g{};
+    if (grads) {
+        // a gradient of what the call does not have is refused
+        if ((grads->gamma_post && !o.gamma_post) || (grads->beta_post && !o.beta_post) || (grads->gate && !o.gate) ||
+            (grads->gate_token && !o.gate_token) || (grads->gamma_pre && !o.gamma_pre) || (grads->beta_pre && !o.beta_pre))
+            return MOE_ERR_INVALID_ARG;
+        g = ResidualGrads{grads->gamma_post, grads->beta_post, grads->gate, grads->gate_token, grads->gamma_pre,
+                          grads->beta_pre};
+        for (const float *q : {g.gamma_post, g.beta_post, g.gate, g.gate_token, g.gamma_pre, g.beta_pre})
+            if ((rc = check_opt(q))) return rc;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {    // the sums over no rows
+        for (float *q : {g.gamma_post, g.beta_post, g.gate, g.gamma_pre, g.beta_pre})
+            if (q && cudaMemsetAsync(q, 0, H * sizeof(float), st) != cudaSuccess) return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    if (!o.pre && !dr) return MOE_ERR_INVALID_ARG;
+    if (o.pre && (rc = check_ptrs({dn, r}))) return rc;
+    if ((o.post || g.gate || g.gate_token) && (rc = check_ptrs({y}))) return rc;
+    if ((rc = check_ptrs({stats, dx, dy})) || (rc = check_opt(dr))) return rc;
+    if ((rc = check_ws(ws, ws_bytes, moe_residual_norm_backward_workspace_bytes(T, H)))) return rc;
+    return cuda_status(launch_join_bwd(o, dn, dr, y, y_fp32, r, x_fp32, stats, T, H, dx, dy, g,
+                                       reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeader), st));
+}
+
 static int check_ckpt(long long rows, int n)
 {
     if (rows < 0 || n <= 0) return MOE_ERR_INVALID_ARG;

@@ -92,6 +92,30 @@ cudaError_t launch_norm_bwd(const void *dy, const void *x, int x_fp32, const flo
                             float *dbeta, float *part, int *status, unsigned long long timeout_ns,
                             int inject, cudaStream_t s);
 
+// ------------------------------------------------- gradients of the combine and the dispatch
+cudaError_t launch_combine_bwd(const void *dY, int dY_fp32, const void *Yp, const int32_t *slot_pos,
+                               const float *topk_w, int T, int H, int K, void *dYp, float *d_topk_w, cudaStream_t s);
+cudaError_t launch_dispatch_bwd(const void *dXp, const int32_t *slot_pos, const void *dres, int T, int H, int K,
+                                void *dX, int dX_fp32, cudaStream_t s);
+
+// ----------------------------------------------------- a branch joined to the residual stream
+// moe_residual_t of the public header, validated.
+struct ResidualOpts {
+    int post, pre;                 // 0 none, 1 layer norm, 2 RMS norm
+    float alpha, eps_post, eps_pre;
+    const float *gamma_post, *beta_post, *gate, *gate_token, *gamma_pre, *beta_pre;
+};
+struct ResidualGrads {             // each nullable
+    float *gamma_post, *beta_post, *gate, *gate_token, *gamma_pre, *beta_pre;
+};
+cudaError_t launch_join(const ResidualOpts &o, const void *x, int x_fp32, const void *y, int y_fp32, int T, int H,
+                        void *r, void *n, float *stats, cudaStream_t s);
+// CTAs of the backward launch; each leaves 4 H partial sums in `part`.
+int join_bwd_ctas(int T, int H);
+cudaError_t launch_join_bwd(const ResidualOpts &o, const void *dn, const void *dr, const void *y, int y_fp32,
+                            const void *r, int x_fp32, const float *stats, int T, int H, void *dx, void *dy,
+                            const ResidualGrads &g, float *part, cudaStream_t s);
+
 // --------------------------------------------------------------- routing from given logits
 cudaError_t launch_route(const void *logits, int fp32, const float *bias, int T, int E, int K,
                          const RoutingOpts &ro, int32_t *idx, float *w, cudaStream_t s);

@@ -481,6 +481,86 @@ int moe_expert_ffn_backward(const void *x, const int8_t *x_scale, const void *dY
                             const void *W2, void *dX, float *d_topk_w, void *dW1, void *dW3, void *dW2,
                             void *ws, size_t ws_bytes, void *stream);
 
+/* Gradients of the layer's two row movements, for experts whose own backward pass the caller has
+ * (moe_expert_ffn_backward holds both for the library's experts).  slot_pos as moe_dispatch left
+ * it, its rows distinct; an entry outside [0, T*K) -- -1, a pair without a row -- contributes
+ * nothing.  K <= 32.  No sum crosses tokens: the results repeat bit for bit.
+ *
+ * Of moe_combine's Y[t] = sum_j topk_w[t, j] Yp[slot_pos[t, j]] (+ Ysh[t], whose gradient is dY):
+ *     dYp[slot_pos[t, j]] = topk_w[t, j] dY[t],   d_topk_w[t, j] = <dY[t], Yp[slot_pos[t, j]]>
+ *   dY       [T, H], bf16 (dY_fp32 == 0) or fp32 (dY_fp32 == 1)
+ *   Yp       bf16 [T*K, H]: the rows the combine read; may be NULL without d_topk_w
+ *   topk_w   fp32 [T, K] or NULL (all 1)
+ *   out dYp  bf16 [T*K, H] (may be Yp's own memory); rows that no pair has are left as they were
+ *   out d_topk_w fp32 [T, K] (nullable); 0 for a pair without a row */
+int moe_combine_backward(const void *dY, int dY_fp32, const void *Yp, const int32_t *slot_pos,
+                         const float *topk_w, int T, int H, int K, void *dYp, float *d_topk_w,
+                         void *stream);
+
+/* Of moe_dispatch's Xp[slot_pos[t, j]] = X[t]:  dX[t] = sum_j dXp[slot_pos[t, j]] (+ dres[t])
+ *   dXp      bf16 [T*K, H]
+ *   dres     [T, H] in the type of dX, or NULL: a gradient that bypasses the experts (the shared
+ *            expert's), added in fp32 before dX is rounded; it may be dX's own memory
+ *   out dX   [T, H], bf16 (dX_fp32 == 0) or fp32 (dX_fp32 == 1); j ascending, then dres */
+int moe_dispatch_backward(const void *dXp, const int32_t *slot_pos, const void *dres, int T, int H,
+                          int K, void *dX, int dX_fp32, void *stream);
+
+/* A block's branch joined to the residual stream, and the next block's norm of the result:
+ *     b = post(y),   r = alpha x + gate_token[t] gate[h] b,   n = pre(r)
+ * with a norm behind the branch (post), gates for channels and for tokens, the stream's scale
+ * alpha, and the norm in front of the next block (pre).  A norm is
+ *     gamma (v - mu) rstd + beta,  rstd = (mean((v - mu)^2) + eps)^-1/2
+ * with mu = mean(v) (layer norm) or 0 (RMS norm). */
+typedef struct moe_residual {
+    int post, pre;             /* 0 no norm, 1 layer norm, 2 RMS norm                       */
+    float alpha;               /* scale of the stream                                       */
+    float eps_post, eps_pre;
+    const float *gamma_post;   /* fp32 [H]; read where post != 0                            */
+    const float *beta_post;    /* fp32 [H] or NULL (no shift); read where post != 0         */
+    const float *gate;         /* fp32 [H] or NULL (1)                                      */
+    const float *gate_token;   /* fp32 [T] or NULL (1)                                      */
+    const float *gamma_pre;    /* as for post                                               */
+    const float *beta_pre;
+} moe_residual_t;
+
+/* Forward.
+ *   x        [T, H], bf16 (x_fp32 == 0) or fp32 (x_fp32 == 1): the stream
+ *   y        [T, H], bf16 or fp32 (y_fp32): the branch's output (moe_combine's Y)
+ *   out r    [T, H] in the type of x (may be x's own memory)
+ *   out n    bf16 [T, H]: the norm of r as it is stored; unused (may be NULL) where pre == 0
+ *   out stats fp32 [T, 4] or NULL: mean and rstd of y, then of r, for the backward pass (0 and 1
+ *            where there is no norm; mean 0 of an RMS norm)
+ * Sums are fp32, variances those of centred rows.  H a multiple of 64, at most 16384, T <= 2^31 -
+ * 2^20 - 1 (else MOE_ERR_UNSUPPORTED_SHAPE); eps < 0, alpha NaN: MOE_ERR_INVALID_ARG. */
+int moe_residual_norm(const void *x, int x_fp32, const void *y, int y_fp32, const moe_residual_t *p,
+                      int T, int H, void *r, void *n, float *stats, void *stream);
+
+/* Gradients of moe_residual_norm's parameters, each nullable (not wanted); a gradient of a
+ * parameter that the call does not have is MOE_ERR_INVALID_ARG. */
+typedef struct moe_residual_grads {
+    float *gamma_post, *beta_post, *gate;   /* fp32 [H] */
+    float *gate_token;                      /* fp32 [T] */
+    float *gamma_pre, *beta_pre;            /* fp32 [H] */
+} moe_residual_grads_t;
+
+/* Backward pass.
+ *   dn       bf16 [T, H]: gradient of n; unused where pre == 0
+ *   dr       [T, H] in the type of x, or NULL: gradient of r (what reaches the stream behind this
+ *            call); required where pre == 0
+ *   y        as in the forward call; may be NULL with post == 0 and no gradient of a gate wanted
+ *   r, stats as the forward call left them (r unused where pre == 0)
+ *   out dx   [T, H] in the type of x (may be dr's own memory); dy bf16 [T, H] (the type
+ *            moe_expert_ffn_backward takes)
+ *   grads    or NULL (none wanted)
+ *   ws       at least moe_residual_norm_backward_workspace_bytes(T, H) bytes (0 for an invalid
+ *            shape): partial sums of the parameters' gradients, added in a fixed order
+ * T == 0 sets the gradients of [H] to 0. */
+size_t moe_residual_norm_backward_workspace_bytes(int T, int H);
+int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, int y_fp32, const void *r,
+                               int x_fp32, const float *stats, const moe_residual_t *p, int T, int H,
+                               void *dx, void *dy, const moe_residual_grads_t *grads, void *ws,
+                               size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------------------------------
  * GRACE-MoE placement planner ("GRACE-MoE" notes, Core Idea 1-3).  Host code on HOST
  * pointers: it consumes the counts and the affinity matrix moe_layer_forward produces
