@@ -143,6 +143,8 @@ def load(build_if_missing: bool = True):
         "moe_residual_norm_backward_workspace_bytes": ([I, I], Z),
         "moe_residual_norm_backward": ([P, P, P, I, P, I, P, ctypes.POINTER(MoeResidual), I, I, P, P,
                                         ctypes.POINTER(MoeResidualGrads), P, Z, P], I),
+        "moe_orthogonalize_workspace_bytes": ([I, I, I], Z),
+        "moe_orthogonalize": ([P, I, P, ctypes.c_float, I, I, I, I, I, P, ctypes.c_float, P, P, Z, P], I),
         "moe_grace_metrics": ([P, I, P, I, P, P], I),
         "moe_grace_group": ([P, I, I, ctypes.c_double, P], I),
         "moe_grace_choose_r": ([P, I, I, P, I, P, P, P, P], I),
@@ -607,6 +609,28 @@ def moe_residual_norm_backward(dn, dr, y, r, stats, p, dx, dy, grads, ws, stream
     _check("moe_residual_norm_backward", load().moe_residual_norm_backward(
         d, e, yp, fy, rp, fx, sp, ctypes.byref(_residual(p, cols[:6])), T, H, dxp, dyp,
         ctypes.byref(MoeResidualGrads(*cols[6:])), *_ws(ws), _stream(stream)))
+
+
+def moe_orthogonalize_workspace_bytes(B: int, R: int, C: int) -> int:
+    return int(load().moe_orthogonalize_workspace_bytes(int(B), int(R), int(C)))
+
+
+def moe_orthogonalize(g, out, ws, momentum=None, mu=0.95, nesterov=False, steps=5, coeffs=None, scale=1.0,
+                      stream=None):
+    """g bf16 or fp32 [B, R, C] or [R, C] -> out bf16; momentum fp32, updated, or None; coeffs: a
+    sequence of `steps` triples (a, b, c), or None (the default in every step)."""
+    b, R, C = ((1,) + tuple(g.shape))[-3:]
+    n, f = b * R * C, _fp32_flag(g, "g")
+    arr = None
+    if coeffs is not None:
+        flat = [float(v) for step in coeffs for v in step]
+        if len(flat) != 3 * int(steps):
+            raise ValueError(f"coeffs: {len(flat)} values, expected {3 * int(steps)}")
+        arr = (ctypes.c_float * len(flat))(*flat)
+    gp, m, o = _ptrs((g, g.dtype, n, "g"), (momentum, F32, n, "momentum"), (out, BF16, n, "out"))
+    _check("moe_orthogonalize", load().moe_orthogonalize(
+        gp, f, m, float(mu), 1 if nesterov else 0, b, R, C, int(steps), arr, float(scale), o, *_ws(ws),
+        _stream(stream)))
 
 
 # ------------------------------------------------------------------- convenience wrapper

@@ -33,7 +33,8 @@ cudaError_t ensure_smem(const void *func, size_t bytes)
     static Entry tab[64];
     static int n = 0;
     static std::mutex mu;
-    if (bytes <= 48 * 1024) return cudaSuccess;
+    // 48 KB need no attribute, a kernel's static arrays among them (at most 8 KB)
+    if (bytes <= 40 * 1024) return cudaSuccess;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -856,6 +857,43 @@ int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, in
     if ((rc = check_ws(ws, ws_bytes, moe_residual_norm_backward_workspace_bytes(T, H)))) return rc;
     return cuda_status(launch_join_bwd(o, dn, dr, y, y_fp32, r, x_fp32, stats, T, H, dx, dy, g,
                                        reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeader), st));
+}
+
+static int check_ortho(int B, int R, int C)
+{
+    if (B < 0 || R <= 0 || C <= 0) return MOE_ERR_INVALID_ARG;
+    return B > 65535 || R > 32768 || C > 32768 ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+}
+
+size_t moe_orthogonalize_workspace_bytes(int B, int R, int C)
+{
+    if (check_ortho(B, R, C) != MOE_OK) return 0;
+    return kHeader + ortho_bytes(B, R, C);
+}
+
+int moe_orthogonalize(const void *g, int g_fp32, float *momentum, float mu, int nesterov, int B, int R, int C,
+                      int steps, const float *coeffs, float scale, void *out, void *ws, size_t ws_bytes,
+                      void *stream)
+{
+    constexpr int kMost = 32;
+    int rc = check_ortho(B, R, C);
+    if (rc) return rc;
+    if ((g_fp32 != 0 && g_fp32 != 1) || (nesterov != 0 && nesterov != 1)) return MOE_ERR_INVALID_ARG;
+    if (steps < 1 || (nesterov && !momentum) || !(mu == mu) || !(scale == scale)) return MOE_ERR_INVALID_ARG;
+    if (steps > kMost) return MOE_ERR_UNSUPPORTED_SHAPE;
+    float c[3 * kMost];
+    for (int i = 0; i < 3 * steps; ++i) {
+        constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
+        c[i] = coeffs ? coeffs[i] : kDefault[i % 3];
+        if (!(c[i] == c[i])) return MOE_ERR_INVALID_ARG;
+    }
+    if (B == 0) return MOE_OK;
+    if ((rc = check_ptrs({g, out})) || (rc = check_opt(momentum))) return rc;
+    if ((rc = check_ws(ws, ws_bytes, kHeader + ortho_bytes(B, R, C)))) return rc;
+    const Ortho f{g, g_fp32, momentum, mu, nesterov, B, R, C, steps, c, scale, out};
+    return debug_status(cuda_status(launch_ortho(f, static_cast<unsigned char *>(ws) + kHeader, static_cast<int *>(ws),
+                                                 g_wait_limit_ns, g_inject_stall, static_cast<cudaStream_t>(stream))),
+                        ws, stream);
 }
 
 static int check_ckpt(long long rows, int n)

@@ -232,6 +232,22 @@ long long ffn_bwd_rows(int T, int E, int K);               // padded rows at mos
 cudaError_t launch_ffn_bwd(const FfnBwd &f, void *scratch, int *status, unsigned long long timeout_ns,
                            int inject, cudaStream_t s);
 
+// Orthogonalised updates: the public moe_orthogonalize's arguments, validated.
+struct Ortho {
+    const void *g;             // [B][R][C] bf16 or fp32
+    int g_fp32;
+    float *momentum;           // [B][R][C] or nullptr
+    float mu;
+    int nesterov;
+    int B, R, C, steps;
+    const float *coeffs;       // host [steps][3]
+    float scale;
+    void *out;                 // bf16 [B][R][C]
+};
+size_t ortho_bytes(int B, int R, int C);
+cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned long long timeout_ns, int inject,
+                         cudaStream_t s);
+
 // Raises the dynamic shared-memory limit of `func` to `bytes` once per process and size
 // (a no-op afterwards, so launches stay capturable).
 cudaError_t ensure_smem(const void *func, size_t bytes);

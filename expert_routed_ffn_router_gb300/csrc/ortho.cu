@@ -1,0 +1,713 @@
+// ortho.cu -- orthogonalised updates of a batch of matrices by Newton-Schulz products (the update
+// of the Muon optimiser), on the 5th-generation tensor cores.
+//
+//   m <- mu m + g,  u = m or g + mu m (with momentum), else g
+//   X = u / |u|_F;  every step:  A = X X^T,  P = b A + c A A,  X <- a X + P X;   out = scale X
+//
+// with A on the smaller side (for matrices with more rows than columns A = X^T X and X <- a X +
+// X P: A and P are symmetric, so the matrices stay as they lie).  A step's polynomial a s + b s^3 +
+// c s^5 acts on every singular value s of X.
+//
+// Launches: the momentum, partial square sums; X from them; three products a step:
+//   gram     A: the tiles on and below the diagonal, each stored twice (the mirror image too)
+//   square   P: likewise, with b A added as the tile leaves tensor memory
+//   apply    X: with a X added likewise; the last step's writes `out`
+//
+// Numbers.  The products take fp16 operands (11 bits; entries of X are at most 1.2 and typically
+// (rows columns)^-1/2, so a fixed power of two keeps them normal) with fp32 sums.  What is carried
+// from step to step is X in two fp16 numbers, 22 bits: a direction with a small singular value
+// is multiplied by a = 3.4 in every step, 485 over five, and a rounding of X with it.  (Rounded to
+// fp16 once a step, gradients of rank 16 come out 3e-2 off, in bf16 0.2; so they are 4e-4 off.)
+// A and P are rounded to fp16 once each: their error acts through products with X alone, and
+// what X has not is not amplified.  In all 2e-4 to 1.8e-3 off, the largest for flat spectra; the
+// rounding of the bf16 result is 1.7e-3.
+//
+// Tiles, roles and waits as in ffn_bwd.cu: clusters of two CTAs, 2-SM MMAs of 256 x 256, 64 deep
+// stages of 32 KB a CTA, two accumulators in tensor memory, eight epilogue warps, all waits
+// bounded (MOE_ERR_DEVICE_TIMEOUT in the status word).  A cluster's tiles are known beforehand
+// (tile, + clusters, ...), tiles of one matrix side by side.
+#include <cuda.h>
+
+#include <cstring>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+// Powers of two that X, A and P are stored with: |X|_2 <= 1.2 (default coefficients), room for 16;
+// |A| <= 1.5, |P| <= 7, room for 128.  An entry of 2^-26 (X), 2^-23 (A, P) is still normal.
+constexpr float SX = 4096.f, SA = 512.f;
+constexpr float SLO = 2048.f;             // the second number of X: its own power of two on top
+
+constexpr int TM = 256, TN = 256, BK = 64;
+constexpr int N_EPI = 8, EPI0 = 4;
+constexpr int NT = 32 * (EPI0 + N_EPI);
+constexpr int HALF = 8192;                // 64 x 64 fp16
+constexpr int STAGE = 4 * HALF;
+constexpr int STAGES = 5;
+constexpr int SLAB = 8192;
+
+enum { GRAM, SQUARE, APPLY, LAST };
+
+struct Args {
+    // loads: K-major operands in boxes of 128 x 64, MN-major ones in boxes of 64 x 64
+    CUtensorMap a, b;
+    // stores: tiles of 32 x 64 (and of X's second numbers), mirror images of 64 x 32
+    CUtensorMap s, s2, sm;
+    int mode, amn, bmn;           // operand rows (columns) contiguous
+    int B, M, N, K;               // products [M][K] x [K][N] of each matrix
+    int nM, nN, tiles;            // tiles of a matrix in each direction, in all
+    const uint16_t *add, *add2;   // SQUARE: A; APPLY: X's numbers; rows of `ld`
+    int ld;
+    float ca, cb, cc;             // coefficients
+    float scale;
+    uint16_t *out;                // LAST: bf16 [B][M][N]
+    int *status;
+    unsigned long long timeout_ns;
+    int inject;
+};
+
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float hi, float lo)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float f16_lo(uint32_t v)
+{
+    float f;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(v));
+    return f;
+}
+__device__ __forceinline__ float f16_hi(uint32_t v)
+{
+    float f;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(f) : "r"(v));
+    return f;
+}
+
+// fp16 operands (formats 0 in bits 7-9 and 10-12), else as idesc_bf16_f32
+__device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool a_mn, bool b_mn)
+{
+    return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((7u << 7) | (7u << 10));
+}
+
+__device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src)) : "memory");
+}
+
+struct Tile { int b, m0, n0; };
+
+__device__ __forceinline__ Tile tile_at(const Args &p, int t)
+{
+    const int per = p.mode <= SQUARE ? p.nM * (p.nM + 1) / 2 : p.nM * p.nN;
+    const int b = t / per;
+    int l = t - b * per, i, j;
+    if (p.mode <= SQUARE) {
+        i = static_cast<int>((sqrtf(8.f * l + 1.f) - 1.f) * 0.5f);
+        while (i * (i + 1) / 2 > l) --i;
+        while ((i + 1) * (i + 2) / 2 <= l) ++i;
+        j = l - i * (i + 1) / 2;
+    } else {
+        j = l / p.nM;              // the rows of tiles innermost: they share columns of the larger operand
+        i = l - j * p.nM;
+    }
+    return Tile{b, i * TM, j * TN};
+}
+
+__global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant__ Args p)
+{
+    constexpr int TCOLS = 512;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *ring = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char *slabs = ring + STAGES * STAGE;
+    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_s;
+    volatile int *abort_flag = &abort_s;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const uint64_t tmo = p.timeout_ns;
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 2 * N_EPI);
+        }
+        mbar_init(&drain, 1);
+        abort_s = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&tmem_slot, TCOLS);
+        tmem_relinquish_pair();
+    }
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+    const int kbs = (p.K + BK - 1) / BK;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0 && !p.inject) {
+            uint32_t s = 0, ph = 0, it = 0;
+            const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+            const int r = static_cast<int>(rank);
+            bool good = true;
+            for (int t = cluster; t < p.tiles && good; t += clusters) {
+                const Tile T = tile_at(p, t);
+                const int m = T.m0 + 128 * r, n = T.n0 + 128 * r;
+                for (int kb = 0; kb < kbs; ++kb, ++it) {
+                    if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
+                    unsigned char *a = ring + s * STAGE, *b = a + 2 * HALF;
+                    const uint32_t fb = full0 + 8u * s;
+                    if (leader) mbar_arrive_expect_tx(&full[s], 2u * STAGE);
+                    const int k = kb * BK;
+                    if (p.amn) {
+                        tma_load_3d_pair(a, &p.a, fb, m, k, T.b);
+                        tma_load_3d_pair(a + HALF, &p.a, fb, m + 64, k, T.b);
+                    } else {
+                        tma_load_3d_pair(a, &p.a, fb, k, m, T.b);
+                    }
+                    if (p.bmn) {
+                        tma_load_3d_pair(b, &p.b, fb, n, k, T.b);
+                        tma_load_3d_pair(b + HALF, &p.b, fb, n + 64, k, T.b);
+                    } else {
+                        tma_load_3d_pair(b, &p.b, fb, k, n, T.b);
+                    }
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+            // Every copy issued lands before the CTAs can exit: the even CTA's barriers count both
+            // CTAs' copies.  After a wait that ran out the odd CTA may have issued stages that the
+            // even one has not: it stays as long as the even one waits for a stage at most.
+            if (!leader && *abort_flag) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 20000000ull) __nanosleep(1000);
+            }
+            if (leader) {
+                const uint32_t n = it < STAGES ? it : STAGES;
+                for (uint32_t j = it - n; j < it; ++j) {
+                    int dummy = 0;
+                    mbar_wait(&full[j % STAGES], (j / STAGES) & 1u, &dummy, nullptr, 20000000ull);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------------- MMA issuer
+        if (lane == 0 && leader) {
+            const uint32_t ring0 = smem_u32(ring);
+            const uint64_t ad0 = smem_desc_sw128(ring0, p.amn ? HALF : 16, 1024);
+            const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, p.bmn ? HALF : 16, 1024);
+            const uint32_t as = p.amn ? 128u : 2u, bs = p.bmn ? 128u : 2u;
+            const uint32_t id = idesc_f16_f32(TM, TN, p.amn, p.bmn);
+            uint32_t s = 0, ph = 0, b = 0, tph = 0;
+            bool good = true;
+            for (int t = cluster; t < p.tiles && good; t += clusters) {
+                if (!mbar_wait(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + b * TN;
+                for (int kb = 0; kb < kbs; ++kb) {
+                    if (!mbar_wait(&full[s], ph, abort_flag, p.status, tmo)) { good = false; break; }
+                    tc_fence_after();
+                    const uint64_t o = static_cast<uint64_t>(s * (STAGE >> 4));
+                    const uint64_t ad = ad0 + o, bd = bd0 + o;
+                    tc_mma_bf16_pair(d, ad, bd, id, kb > 0 ? 1u : 0u);
+                    tc_mma_bf16_pair(d, ad + as, bd + bs, id, 1u);
+                    tc_mma_bf16_pair(d, ad + 2 * as, bd + 2 * bs, id, 1u);
+                    tc_mma_bf16_pair(d, ad + 3 * as, bd + 3 * bs, id, 1u);
+                    tc_commit_pair_mc(&empty[s], 3);
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
+                }
+                if (!good) break;
+                tc_commit_pair_mc(&tfull[b], 3);
+                b ^= 1u;
+                if (b == 0) tph ^= 1u;
+            }
+            tc_commit_pair_mc(&drain, 1);
+            int dummy = 0;
+            mbar_wait(&drain, 0, &dummy, nullptr, 20000000ull);
+        }
+    } else if (warp >= EPI0) {
+        // ---------------------------------------------------------------- epilogue
+        const int q = warp & 3, half = (warp - EPI0) >> 2;   // lane quarter, half of the columns
+        const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+        const int r0 = 128 * static_cast<int>(rank) + 32 * q;
+        unsigned char *slab = slabs + (warp - EPI0) * SLAB;
+        uint32_t b = 0, tph = 0;
+        for (int t = cluster; t < p.tiles; t += clusters) {
+            const Tile T = tile_at(p, t);
+            bool good = true;
+            if (lane == 0) good = mbar_wait(&tfull[b], tph, abort_flag, p.status, tmo);
+            good = __shfl_sync(kFullMask, good, 0);
+            if (!good) break;
+            mbar_try_wait(&tfull[b], tph);
+            tc_fence_after();
+            const int m0 = T.m0 + r0, row = m0 + lane;
+            const bool mirror = p.mode <= SQUARE && T.m0 != T.n0;
+            const size_t at = (static_cast<size_t>(T.b) * p.M + row) * p.ld;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                const int lc = 128 * half + 32 * c, col = T.n0 + lc;
+                if (col >= p.N) break;
+                if (m0 >= p.M) break;
+                float v[32];
+                __syncwarp();
+                tmem_ld32(tm0 + b * TN + lc, v);
+                uint4 h[4], l[4];
+                if (p.mode != GRAM && row < p.M) {
+                    // (the last columns of a row end within ld, a multiple of 8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = col + 8 * i < p.N;
+                        h[i] = in ? *reinterpret_cast<const uint4 *>(p.add + at + col + 8 * i) : make_uint4(0, 0, 0, 0);
+                        if (p.mode >= APPLY)
+                            l[i] = in ? *reinterpret_cast<const uint4 *>(p.add2 + at + col + 8 * i) : make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (p.mode == GRAM) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= SA / (SX * SX);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint4 hv = h[i / 4], lv = p.mode >= APPLY ? l[i / 4] : make_uint4(0, 0, 0, 0);
+                        const uint32_t hw = (i & 3) == 0 ? hv.x : (i & 3) == 1 ? hv.y : (i & 3) == 2 ? hv.z : hv.w;
+                        const uint32_t lw = (i & 3) == 0 ? lv.x : (i & 3) == 1 ? lv.y : (i & 3) == 2 ? lv.z : lv.w;
+                        float x0 = f16_lo(hw), x1 = f16_hi(hw);
+                        if (p.mode >= APPLY) {
+                            x0 = fmaf(f16_lo(lw), 1.f / SLO, x0);
+                            x1 = fmaf(f16_hi(lw), 1.f / SLO, x1);
+                            v[2 * i] = fmaf(p.ca, x0, v[2 * i] * (1.f / SA));
+                            v[2 * i + 1] = fmaf(p.ca, x1, v[2 * i + 1] * (1.f / SA));
+                        } else {
+                            v[2 * i] = fmaf(p.cb, x0, v[2 * i] * (p.cc / SA));
+                            v[2 * i + 1] = fmaf(p.cb, x1, v[2 * i + 1] * (p.cc / SA));
+                        }
+                    }
+                }
+                if (p.mode == LAST) {
+                    if (row < p.M) {
+                        const float f = p.scale / SX;
+                        uint16_t *o = p.out + (static_cast<size_t>(T.b) * p.M + row) * p.N + col;
+                        if (p.N % 8 == 0) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (col + 8 * i < p.N)
+                                    reinterpret_cast<uint4 *>(o)[i] =
+                                        make_uint4(f32x2_to_bf16x2(v[8 * i + 1] * f, v[8 * i] * f), f32x2_to_bf16x2(v[8 * i + 3] * f, v[8 * i + 2] * f),
+                                                   f32x2_to_bf16x2(v[8 * i + 5] * f, v[8 * i + 4] * f), f32x2_to_bf16x2(v[8 * i + 7] * f, v[8 * i + 6] * f));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (col + i < p.N) o[i] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * f));
+                        }
+                    }
+                    continue;
+                }
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+                // 32 columns of the lane's row, 64 bytes: the first numbers, and the second ones or
+                // the mirror image, each as 32 rows of 64 bytes in the 64-byte swizzle
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = f32x2_to_f16x2(v[2 * i + 1], v[2 * i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(slab + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                if (p.mode == APPLY) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = f32x2_to_f16x2((v[8 * i + 2 * k + 1] - f16_hi(w[4 * i + k])) * SLO,
+                                                  (v[8 * i + 2 * k] - f16_lo(w[4 * i + k])) * SLO);
+                        *reinterpret_cast<uint4 *>(slab + 2048 + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                } else if (mirror) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        *reinterpret_cast<uint16_t *>(slab + 2048 + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2) =
+                            static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&p.s, slab, col, m0, T.b);
+                    if (p.mode == APPLY) tma_store_3d(&p.s2, slab + 2048, col, m0, T.b);
+                    else if (mirror) tma_store_3d(&p.sm, slab + 2048, m0, col, T.b);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + 8u * b);
+            b ^= 1u;
+            if (b == 0) tph ^= 1u;
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, TCOLS);
+    }
+}
+
+// ------------------------------------------------------------------ momentum, norm, X
+constexpr int PT = 256;               // threads
+constexpr int MAX_PARTS = 256;        // chunks of a matrix
+
+struct Prepare {
+    const void *g;
+    int g_fp32;
+    float *m;                         // nullable
+    float mu;
+    int nesterov;
+    int R, C, ld;
+    long long chunk;                  // elements, a multiple of 8
+    int parts;
+    float4 *part;                     // [B][parts]: square sums at three scales
+    uint16_t *hi, *lo;                // [B][R][ld]
+};
+
+template <bool VEC>
+struct Elements { static constexpr int N = VEC ? 8 : 1; };
+
+template <bool VEC>
+__device__ __forceinline__ void load_g(const Prepare &p, size_t i, float (&v)[Elements<VEC>::N])
+{
+    if constexpr (VEC) {
+        if (p.g_fp32) {
+            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.g) + i);
+            const float4 a = q[0], b = q[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.g) + i);
+            v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+            v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
+        }
+    } else {
+        v[0] = p.g_fp32 ? static_cast<const float *>(p.g)[i] : bf16_lo(static_cast<const uint16_t *>(p.g)[i]);
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load_m(const float *m, size_t i, float (&v)[Elements<VEC>::N])
+{
+    if constexpr (VEC) {
+        const float4 *q = reinterpret_cast<const float4 *>(m + i);
+        const float4 a = q[0], b = q[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        v[0] = m[i];
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+
+// Square sums of u, of 2^60 u and of 2^-80 u: one of them holds |u| to fp32's precision whatever the
+// size of the entries.
+constexpr float UP = 1152921504606846976.f, DOWN = 1.f / (UP * 1048576.f);
+
+// VEC: R C and C are multiples of 8.  CTA (part, matrix): the momentum, and the chunk's square sums.
+template <bool VEC>
+__global__ void __launch_bounds__(PT) ortho_momentum_kernel(const Prepare p)
+{
+    constexpr int N = Elements<VEC>::N;
+    __shared__ float red[3][PT / 32];
+    pdl_wait();
+    const long long n = static_cast<long long>(p.R) * p.C;
+    const size_t base = static_cast<size_t>(blockIdx.y) * n;
+    const long long lo = blockIdx.x * p.chunk, hi = min(n, lo + p.chunk);
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f;
+    for (long long i = lo + threadIdx.x * N; i < hi; i += PT * N) {
+        float u[N];
+        load_g<VEC>(p, base + i, u);
+        if (p.m) {
+            float m[N];
+            load_m<VEC>(p.m, base + i, m);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                m[k] = fmaf(p.mu, m[k], u[k]);
+                u[k] = p.nesterov ? fmaf(p.mu, m[k], u[k]) : m[k];
+            }
+            if constexpr (VEC) {
+                float4 *q = reinterpret_cast<float4 *>(p.m + base + i);
+                q[0] = make_float4(m[0], m[1], m[2], m[3]);
+                q[1] = make_float4(m[4], m[5], m[6], m[7]);
+            } else {
+                p.m[base + i] = m[0];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            s0 = fmaf(u[k], u[k], s0);
+            const float a = u[k] * UP, b = u[k] * DOWN;
+            s1 = fmaf(a, a, s1);
+            s2 = fmaf(b, b, s2);
+        }
+    }
+    s0 = warp_sum(s0); s1 = warp_sum(s1); s2 = warp_sum(s2);
+    const int w = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) { red[0][w] = s0; red[1][w] = s1; red[2][w] = s2; }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < PT / 32; ++k) { s0 += red[0][k]; s1 += red[1][k]; s2 += red[2][k]; }
+        p.part[static_cast<size_t>(blockIdx.y) * p.parts + blockIdx.x] = make_float4(s0, s1, s2, 0.f);
+    }
+}
+
+// CTA (part, matrix): X = u / |u| of the chunk, as two fp16 numbers.
+template <bool VEC>
+__global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
+{
+    constexpr int N = Elements<VEC>::N;
+    __shared__ float red[3][PT / 32];
+    pdl_wait();
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f;
+    for (int k = threadIdx.x; k < p.parts; k += PT) {
+        const float4 v = p.part[static_cast<size_t>(blockIdx.y) * p.parts + k];
+        s0 += v.x; s1 += v.y; s2 += v.z;
+    }
+    s0 = warp_sum(s0); s1 = warp_sum(s1); s2 = warp_sum(s2);
+    const int w = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) { red[0][w] = s0; red[1][w] = s1; red[2][w] = s2; }
+    __syncthreads();
+    s0 = s1 = s2 = 0.f;
+    for (int k = 0; k < PT / 32; ++k) { s0 += red[0][k]; s1 += red[1][k]; s2 += red[2][k]; }
+    // x = (u f) / |u f|, f a power of two.  (A square sum below 2^-60 may have lost terms to underflow,
+    // one above 2^100 to overflow; the sums at the other scales are then within range.)
+    float f = 1.f, s = s0;
+    if (!(s0 >= 1.f / UP)) { f = UP; s = s1; }
+    else if (!(s0 <= UP * 1099511627776.f)) { f = DOWN; s = s2; }
+    // (a matrix of zeros stays one; an infinity or a NaN makes it NaN)
+    const float inv = s > 0.f ? (s <= 3.402823466e38f ? SX / sqrtf(s) : s - s) : s;
+    const long long n = static_cast<long long>(p.R) * p.C;
+    const size_t base = static_cast<size_t>(blockIdx.y) * n;
+    const long long lo = blockIdx.x * p.chunk, hi = min(n, lo + p.chunk);
+    for (long long i = lo + threadIdx.x * N; i < hi; i += PT * N) {
+        float u[N];
+        if (!p.m || p.nesterov) load_g<VEC>(p, base + i, u);
+        if (p.m) {
+            float m[N];
+            load_m<VEC>(p.m, base + i, m);
+#pragma unroll
+            for (int k = 0; k < N; ++k) u[k] = p.nesterov ? fmaf(p.mu, m[k], u[k]) : m[k];
+        }
+        const int r = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(r) * p.C);
+        const size_t at = (static_cast<size_t>(blockIdx.y) * p.R + r) * p.ld + c;
+        if constexpr (VEC) {
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float a = u[2 * k] * f * inv, b = u[2 * k + 1] * f * inv;
+                h[k] = f32x2_to_f16x2(b, a);
+                l[k] = f32x2_to_f16x2((b - f16_hi(h[k])) * SLO, (a - f16_lo(h[k])) * SLO);
+            }
+            *reinterpret_cast<uint4 *>(p.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(p.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        } else {
+            const float a = u[0] * f * inv;
+            const uint32_t h = f32x2_to_f16x2(0.f, a);
+            p.hi[at] = static_cast<uint16_t>(h);
+            p.lo[at] = static_cast<uint16_t>(f32x2_to_f16x2(0.f, (a - f16_lo(h)) * SLO));
+        }
+    }
+}
+
+// ------------------------------------------------------------------------ host side
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                   CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static const EncodeTiledFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(ptr);
+        return static_cast<EncodeTiledFn>(nullptr);
+    }();
+    return fn;
+}
+
+// fp16 [B][rows][cols] in rows of ld elements (a multiple of 8), boxes of box_rows x box_cols: 64
+// columns in the 128-byte swizzle, 32 in the 64-byte one.  What is outside reads as 0.
+bool encode(CUtensorMap *m, const void *base, int B, int rows, int cols, int ld, int box_rows, int box_cols)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(B)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2 * rows};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t al256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+int up8(int n) { return (n + 7) & ~7; }
+
+struct Layout {
+    int m, ld, ldm, parts;
+    long long chunk;
+    size_t part, hi[2], lo, A, P, bytes;
+};
+Layout layout(int B, int R, int C)
+{
+    Layout L{};
+    L.m = R < C ? R : C;
+    L.ld = up8(C);
+    L.ldm = up8(L.m);
+    const long long n = static_cast<long long>(R) * C;
+    // chunks of 16384 elements or more, MAX_PARTS at most
+    long long chunk = (n + MAX_PARTS - 1) / MAX_PARTS;
+    if (chunk < 16384) chunk = 16384;
+    L.chunk = (chunk + 7) / 8 * 8;
+    L.parts = static_cast<int>((n + L.chunk - 1) / L.chunk);
+    size_t o = 0;
+    auto take = [&](size_t b) { const size_t at = o; o += al256(b); return at; };
+    const size_t x = static_cast<size_t>(B) * R * L.ld * 2, a = static_cast<size_t>(B) * L.m * L.ldm * 2;
+    L.part = take(static_cast<size_t>(B) * L.parts * sizeof(float4));
+    L.hi[0] = take(x);
+    L.hi[1] = take(x);
+    L.lo = take(x);
+    L.A = take(a);
+    L.P = take(a);
+    L.bytes = o;
+    return L;
+}
+
+}  // namespace
+
+size_t ortho_bytes(int B, int R, int C) { return layout(B, R, C).bytes; }
+
+cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned long long timeout_ns, int inject,
+                         cudaStream_t s)
+{
+    const int B = f.B, R = f.R, C = f.C;
+    const Layout L = layout(B, R, C);
+    unsigned char *w = static_cast<unsigned char *>(scratch);
+    Prepare q{f.g, f.g_fp32, f.momentum, f.mu, f.nesterov, R, C, L.ld, L.chunk, L.parts,
+              reinterpret_cast<float4 *>(w + L.part), reinterpret_cast<uint16_t *>(w + L.hi[0]),
+              reinterpret_cast<uint16_t *>(w + L.lo)};
+    const bool vec = C % 8 == 0;
+    const dim3 grid(L.parts, B);
+    cudaError_t e = launch_pdl(vec ? ortho_momentum_kernel<true> : ortho_momentum_kernel<false>, grid, dim3(PT), 0, s, 1, q);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(vec ? ortho_scale_kernel<true> : ortho_scale_kernel<false>, grid, dim3(PT), 0, s, 1, q);
+    if (e != cudaSuccess) return e;
+
+    const bool tall = R > C;             // the smaller side is the columns
+    const int m = L.m;
+    void *A = w + L.A, *P = w + L.P;
+    Args g, sq, ap[2];
+    memset(&g, 0, sizeof g);
+    g.B = B;
+    g.status = status;
+    g.timeout_ns = timeout_ns;
+    g.inject = inject;
+    g.scale = f.scale;
+    g.out = static_cast<uint16_t *>(f.out);
+    sq = g;
+    ap[0] = g;
+    const auto tiles = [](int n) { return (n + TM - 1) / TM; };
+    // gram: [m][n] x [n][m]
+    g.mode = GRAM;
+    g.amn = g.bmn = tall ? 1 : 0;
+    g.M = g.N = m;
+    g.K = tall ? R : C;
+    g.nM = g.nN = tiles(m);
+    g.tiles = B * (g.nM * (g.nM + 1) / 2);
+    bool ok = encode(&g.s, A, B, m, m, L.ldm, 32, 32);
+    g.sm = g.s;
+    // square
+    sq.mode = SQUARE;
+    sq.M = sq.N = sq.K = m;
+    sq.nM = sq.nN = g.nM;
+    sq.tiles = g.tiles;
+    sq.add = static_cast<const uint16_t *>(A);
+    sq.ld = L.ldm;
+    ok = ok && encode(&sq.a, A, B, m, m, L.ldm, 128, 64) && encode(&sq.s, P, B, m, m, L.ldm, 32, 32);
+    sq.b = sq.a;
+    sq.sm = sq.s;
+    // apply: [m][m] x [m][n], or X P for tall matrices
+    ap[0].mode = APPLY;
+    ap[0].M = R;
+    ap[0].N = C;
+    ap[0].K = m;
+    ap[0].nM = tiles(R);
+    ap[0].nN = tiles(C);
+    ap[0].tiles = B * ap[0].nM * ap[0].nN;
+    ap[0].bmn = tall ? 0 : 1;
+    ap[0].ld = L.ld;
+    ap[0].add2 = reinterpret_cast<const uint16_t *>(w + L.lo);
+    ok = ok && encode(&ap[0].s2, w + L.lo, B, R, C, L.ld, 32, 32);
+    ap[1] = ap[0];
+    CUtensorMap gx[2];
+    for (int i = 0; i < 2; ++i) {        // from X in buffer i to the other one
+        void *x = w + L.hi[i];
+        ap[i].add = static_cast<const uint16_t *>(x);
+        ok = ok && encode(&ap[i].s, w + L.hi[1 - i], B, R, C, L.ld, 32, 32) &&
+             encode(&gx[i], x, B, R, C, L.ld, tall ? 64 : 128, 64);
+        if (tall)
+            ok = ok && encode(&ap[i].a, x, B, R, C, L.ld, 128, 64) && encode(&ap[i].b, P, B, m, m, L.ldm, 128, 64);
+        else
+            ok = ok && encode(&ap[i].a, P, B, m, m, L.ldm, 128, 64) && encode(&ap[i].b, x, B, R, C, L.ld, 64, 64);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + STAGES * STAGE + N_EPI * SLAB;
+    if ((e = ensure_smem(reinterpret_cast<const void *>(ortho_gemm_kernel), smem)) != cudaSuccess) return e;
+    const int most = num_sms() / 2;
+    auto run = [&](const Args &a) {
+        return launch_pdl(ortho_gemm_kernel, dim3(2 * (a.tiles < most ? a.tiles : most)), dim3(NT), smem, s, 2, a);
+    };
+    for (int k = 0; k < f.steps; ++k) {
+        const int i = k & 1;
+        g.a = g.b = gx[i];
+        sq.cb = f.coeffs[3 * k + 1];
+        sq.cc = f.coeffs[3 * k + 2];
+        ap[i].ca = f.coeffs[3 * k];
+        ap[i].mode = k + 1 < f.steps ? APPLY : LAST;
+        if ((e = run(g)) != cudaSuccess || (e = run(sq)) != cudaSuccess || (e = run(ap[i])) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace moe

@@ -78,8 +78,13 @@ __device__ __forceinline__ float4 col4(const float *p, int c, float absent)
 
 __device__ __forceinline__ float sum4(float4 v) { return (v.x + v.y) + (v.z + v.w); }
 __device__ __forceinline__ float dot4(float4 a, float4 b) { return fmaf(a.x, b.x, a.y * b.y) + fmaf(a.z, b.z, a.w * b.w); }
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
-__device__ __forceinline__ float4 scale4(float4 a, float s) { return make_float4(a.x * s, a.y * s, a.z * s, a.w * s); }
+// (rounded products, never part of an fma: which one the compiler forms would depend on the branch
+// around it, and dx and dy on which gradients are wanted)
+__device__ __forceinline__ float4 mul4(float4 a, float4 b)
+{
+    return make_float4(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y), __fmul_rn(a.z, b.z), __fmul_rn(a.w, b.w));
+}
+__device__ __forceinline__ float4 scale4(float4 a, float s) { return mul4(a, make_float4(s, s, s, s)); }
 __device__ __forceinline__ float4 norm4(float4 v, float m, float s)
 {
     return make_float4((v.x - m) * s, (v.y - m) * s, (v.z - m) * s, (v.w - m) * s);
@@ -214,7 +219,8 @@ __device__ __forceinline__ void stage_in(unsigned char *st, const void *p, int r
 }
 
 // ---------------------------------------------------------------------------- forward
-template <bool ONE, int MAXT>
+// PREG: the columns' parameters stay in registers (read once a CTA instead of once a row).
+template <bool ONE, int MAXT, bool PREG>
 __global__ void __launch_bounds__(MAXT) join_kernel(const __grid_constant__ Residual p)
 {
     extern __shared__ __align__(16) unsigned char stages[];
@@ -236,6 +242,23 @@ __global__ void __launch_bounds__(MAXT) join_kernel(const __grid_constant__ Resi
         copies_commit();
     };
     for (int s = 0; s < S; ++s) fetch(first + s * step, s);
+    // gate and norm of the branch as one scale and shift, the next norm's
+    auto scale = [&](int c) { return mul4(col4(o.gate, c, 1.f), col4(o.gamma_post, c, 1.f)); };
+    auto shift = [&](int c) {
+        return o.beta_post ? mul4(col4(o.gate, c, 1.f), col4(o.beta_post, c, 0.f)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    constexpr int PV = PREG ? VPT : 1;
+    float4 ps[PV], pt[PV], ns[PV], nt[PV];
+    if (PREG)
+#pragma unroll
+        for (int i = 0; i < PV; ++i) {
+            const int c = 4 * (w.tid + i * w.n);
+            if (c >= H) continue;
+            ps[i] = scale(c);
+            pt[i] = shift(c);
+            ns[i] = col4(o.gamma_pre, c, 1.f);
+            nt[i] = col4(o.beta_pre, c, 0.f);
+        }
     int s = 0;
     for (int row = first; row < p.T; row += step) {
         copies_wait(S - 1);
@@ -254,9 +277,7 @@ __global__ void __launch_bounds__(MAXT) join_kernel(const __grid_constant__ Resi
         for (int i = 0; i < VPT; ++i) {
             const int c = 4 * (w.tid + i * w.n);
             if (c >= H) continue;
-            float4 b = v[i];
-            if (o.post) b = fma4(norm4(b, sy.x, sy.y), col4(o.gamma_post, c, 1.f), col4(o.beta_post, c, 0.f));
-            if (o.gate) b = mul4(b, col4(o.gate, c, 1.f));
+            float4 b = fma4(norm4(v[i], sy.x, sy.y), PREG ? ps[i % PV] : scale(c), PREG ? pt[i % PV] : shift(c));
             const float4 x = ld4(st + p.off[0], c, xf);
             b = make_float4(fmaf(o.alpha, x.x, gt * b.x), fmaf(o.alpha, x.y, gt * b.y), fmaf(o.alpha, x.z, gt * b.z),
                             fmaf(o.alpha, x.w, gt * b.w));
@@ -274,7 +295,8 @@ __global__ void __launch_bounds__(MAXT) join_kernel(const __grid_constant__ Resi
             for (int i = 0; i < VPT; ++i) {
                 const int c = 4 * (w.tid + i * w.n);
                 if (c >= H) continue;
-                st4(p.n, base + c, false, fma4(norm4(v[i], sr.x, sr.y), col4(o.gamma_pre, c, 1.f), col4(o.beta_pre, c, 0.f)));
+                st4(p.n, base + c, false, fma4(norm4(v[i], sr.x, sr.y), PREG ? ns[i % PV] : col4(o.gamma_pre, c, 1.f),
+                                               PREG ? nt[i % PV] : col4(o.beta_pre, c, 0.f)));
             }
         }
         if (p.stats && w.tid == 0) p.stats[row] = make_float4(sy.x, sy.y, sr.x, sr.y);
@@ -283,8 +305,8 @@ __global__ void __launch_bounds__(MAXT) join_kernel(const __grid_constant__ Resi
 }
 
 // --------------------------------------------------------------------------- backward
-// Staged arrays: 0 dn, 1 r, 2 y, 3 dr.
-template <bool ONE, int MAXT>
+// Staged arrays: 0 dn, 1 r, 2 y, 3 dr.  S0: with beta_post, whose gradient and the gate's need those sums.  PREG as above.
+template <bool ONE, int MAXT, bool S0, bool PREG>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) join_bwd_kernel(const __grid_constant__ Residual p)
 {
     extern __shared__ __align__(16) unsigned char stages[];
@@ -308,9 +330,20 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) join_bwd_kernel(con
         copies_commit();
     };
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 p1[VPT], p0[VPT], s1[VPT], s0[VPT];
+    constexpr int PV = PREG ? VPT : 1, SV = S0 ? VPT : 1;
+    float4 p1[VPT], p0[VPT], s1[VPT], s0[SV], ga[PV], gb[PV];
+    auto scale = [&](int c) { return mul4(col4(o.gate, c, 1.f), col4(o.gamma_post, c, 1.f)); };
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) p1[i] = p0[i] = s1[i] = s0[i] = zero;
+    for (int i = 0; i < VPT; ++i) {
+        p1[i] = p0[i] = s1[i] = s0[i % SV] = zero;
+        const int c = 4 * (w.tid + i * w.n);
+        if (PREG && c < H) {
+            ga[i % PV] = col4(o.gamma_pre, c, 1.f);
+            gb[i % PV] = scale(c);
+        }
+    }
+    auto gamma = [&](int i, int c) { return PREG ? ga[i % PV] : col4(o.gamma_pre, c, 1.f); };
+    auto branch = [&](int i, int c) { return PREG ? gb[i % PV] : scale(c); };
     const float inv = 1.f / static_cast<float>(H);
     const bool token = p.d_token != nullptr;
     for (int s = 0; s < S; ++s) fetch(first + s * step, s);
@@ -338,7 +371,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) join_bwd_kernel(con
                 const float4 e = ld4(sm + p.off[0], c, false), h = norm4(ld4(sm + p.off[1], c, xf), st.z, st.w);
                 p1[i] = fma4(e, h, p1[i]);
                 p0[i] = make_float4(p0[i].x + e.x, p0[i].y + e.y, p0[i].z + e.z, p0[i].w + e.w);
-                const float4 a = mul4(e, col4(o.gamma_pre, c, 1.f));
+                const float4 a = mul4(e, gamma(i, c));
                 a0 += sum4(a);
                 a1 += dot4(a, h);
             }
@@ -350,7 +383,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) join_bwd_kernel(con
                 const int c = 4 * (w.tid + i * w.n);
                 if (c >= H) continue;
                 const float4 e = ld4(sm + p.off[0], c, false), h = norm4(ld4(sm + p.off[1], c, xf), st.z, st.w);
-                const float4 a = mul4(e, col4(o.gamma_pre, c, 1.f));
+                const float4 a = mul4(e, gamma(i, c));
                 d[i].x = fmaf(st.w, a.x - a0 - h.x * a1, d[i].x);
                 d[i].y = fmaf(st.w, a.y - a0 - h.y * a1, d[i].y);
                 d[i].z = fmaf(st.w, a.z - a0 - h.z * a1, d[i].z);
@@ -367,11 +400,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) join_bwd_kernel(con
             if (!p.y) continue;
             const float4 h = norm4(ld4(sm + p.off[2], c, yf), st.x, st.y), g = scale4(d[i], gt);
             s1[i] = fma4(g, h, s1[i]);
-            s0[i] = make_float4(s0[i].x + g.x, s0[i].y + g.y, s0[i].z + g.z, s0[i].w + g.w);
-            const float4 k = o.gate ? mul4(d[i], col4(o.gate, c, 1.f)) : d[i], f = mul4(k, col4(o.gamma_post, c, 1.f));
+            if (S0) s0[i % SV] = make_float4(s0[i % SV].x + g.x, s0[i % SV].y + g.y, s0[i % SV].z + g.z, s0[i % SV].w + g.w);
+            const float4 f = mul4(d[i], branch(i, c));
             a0 += sum4(f);
             a1 += dot4(f, h);
-            if (token && o.beta_post) a2 += dot4(k, col4(o.beta_post, c, 0.f));
+            if (token && o.beta_post) a2 += dot4(mul4(d[i], col4(o.gate, c, 1.f)), col4(o.beta_post, c, 0.f));
         }
         if (o.post || token) {
             w.sum3(a0, a1, a2);
@@ -386,10 +419,9 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) join_bwd_kernel(con
         for (int i = 0; i < VPT; ++i) {
             const int c = 4 * (w.tid + i * w.n);
             if (c >= H) continue;
-            float4 f = o.gate ? mul4(d[i], col4(o.gate, c, 1.f)) : d[i];
+            float4 f = mul4(d[i], branch(i, c));
             if (o.post) {
                 const float4 h = norm4(ld4(sm + p.off[2], c, yf), st.x, st.y);
-                f = mul4(f, col4(o.gamma_post, c, 1.f));
                 f = make_float4(f.x - a0 - h.x * a1, f.y - a0 - h.y * a1, f.z - a0 - h.z * a1, f.w - a0 - h.w * a1);
             }
             st4(p.dy, base + c, false, scale4(f, o.post ? rs : gt));
@@ -406,7 +438,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) join_bwd_kernel(con
             *reinterpret_cast<float4 *>(part + c) = p1[i];
             *reinterpret_cast<float4 *>(part + H + c) = p0[i];
             *reinterpret_cast<float4 *>(part + 2 * H + c) = s1[i];
-            *reinterpret_cast<float4 *>(part + 3 * H + c) = s0[i];
+            *reinterpret_cast<float4 *>(part + 3 * H + c) = s0[i % SV];
         }
         return;
     }
@@ -418,7 +450,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) join_bwd_kernel(con
         for (int i = 0; i < VPT; ++i) {
             const int c = 4 * (w.tid + 32 * i);
             __syncthreads();
-            comb[threadIdx.y][w.tid] = k == 0 ? p1[i] : k == 1 ? p0[i] : k == 2 ? s1[i] : s0[i];
+            comb[threadIdx.y][w.tid] = k == 0 ? p1[i] : k == 1 ? p0[i] : k == 2 ? s1[i] : s0[i % SV];
             __syncthreads();
             if (threadIdx.y == 0 && c < H) {
                 float4 t = comb[0][w.tid];
@@ -458,13 +490,6 @@ __global__ void __launch_bounds__(256) join_wgrad_kernel(const float *__restrict
     if (g.gate) g.gate[c] = fmaf(o.gamma_post ? o.gamma_post[c] : 1.f, v[2], o.beta_post ? o.beta_post[c] * v[3] : 0.f);
 }
 
-// The kernels' static arrays count against the 48 KB that need no attribute.
-cudaError_t allow_smem(const void *fn, size_t bytes)
-{
-    constexpr size_t PLAIN = 48 * 1024;
-    return ensure_smem(fn, bytes > PLAIN - 8 * 1024 && bytes <= PLAIN ? PLAIN + 16 : bytes);
-}
-
 int row_threads_of(int H) { return (H / 4 + VPT * 32 - 1) / (VPT * 32) * 32; }
 
 }  // namespace
@@ -490,30 +515,29 @@ cudaError_t launch_join(const ResidualOpts &o, const void *x, int x_fp32, const 
     p.off[1] = H * (x_fp32 ? 4 : 2);
     p.stage_bytes = p.off[1] + H * (y_fp32 ? 4 : 2);
     const bool one = H <= WARP_COLS;
-    const void *fn;
+    const int threads = row_threads_of(H);
     dim3 block, grid;
+    void (*kernel)(const Residual);
     if (one) {
         p.stages = 2;
         block = dim3(32, WARPS);
         const int units = (T + WARPS - 1) / WARPS, most = 4 * num_sms();
         grid = dim3(units < most ? units : most);
-        fn = reinterpret_cast<const void *>(join_kernel<true, 32 * WARPS>);
+        kernel = join_kernel<true, 32 * WARPS, false>;
     } else {
-        const int threads = row_threads_of(H), fit = static_cast<int>(ROOM / p.stage_bytes);
-        int ctas = 1024 / threads;
+        const int fit = static_cast<int>(ROOM / p.stage_bytes);
+        int ctas = 512 / threads;
         if (ctas > fit / 2) ctas = fit / 2;
         if (ctas < 1) ctas = 1;
         p.stages = fit / ctas > 3 ? 3 : fit / ctas;
         block = dim3(threads);
         grid = dim3(T < ctas * num_sms() ? T : ctas * num_sms());
-        fn = threads <= 512 ? reinterpret_cast<const void *>(join_kernel<false, 512>)
-                            : reinterpret_cast<const void *>(join_kernel<false, 1024>);
+        kernel = threads <= 512 ? join_kernel<false, 512, true> : join_kernel<false, 1024, false>;
     }
     const size_t smem = static_cast<size_t>(p.stages) * p.stage_bytes * (one ? WARPS : 1);
-    const cudaError_t e = allow_smem(fn, smem);
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
-    if (one) return launch_pdl(join_kernel<true, 32 * WARPS>, grid, block, smem, s, 1, p);
-    return launch_pdl(block.x <= 512 ? join_kernel<false, 512> : join_kernel<false, 1024>, grid, block, smem, s, 1, p);
+    return launch_pdl(kernel, grid, block, smem, s, 1, p);
 }
 
 cudaError_t launch_join_bwd(const ResidualOpts &o, const void *dn, const void *dr, const void *y, int y_fp32,
@@ -551,10 +575,14 @@ cudaError_t launch_join_bwd(const ResidualOpts &o, const void *dn, const void *d
     p.stages = fit < 1 ? 1 : (fit > 3 ? 3 : static_cast<int>(fit));
     const size_t smem = static_cast<size_t>(p.stages) * p.stage_bytes * (one ? WARPS : 1);
     const int threads = row_threads_of(H);
-    void (*kernel)(const Residual) = one ? join_bwd_kernel<true, 32 * WARPS>
-                                         : (threads <= 256 ? join_bwd_kernel<false, 256>
-                                            : threads <= 512 ? join_bwd_kernel<false, 512> : join_bwd_kernel<false, 1024>);
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
+    const bool s0 = o.beta_post != nullptr;
+    void (*kernel)(const Residual) =
+        one ? join_bwd_kernel<true, 32 * WARPS, true, false>
+        : threads <= 256 ? (s0 ? join_bwd_kernel<false, 256, true, true> : join_bwd_kernel<false, 256, false, true>)
+        : threads <= 448 ? (s0 ? join_bwd_kernel<false, 448, true, true> : join_bwd_kernel<false, 448, false, true>)
+        : threads <= 512 ? (s0 ? join_bwd_kernel<false, 512, true, false> : join_bwd_kernel<false, 512, false, true>)
+                         : join_bwd_kernel<false, 1024, true, false>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(ctas), one ? dim3(32, WARPS) : dim3(threads), smem, s, 1, p);
     if (e != cudaSuccess) return e;

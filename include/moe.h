@@ -145,19 +145,19 @@ int moe_read_status(void *ws, void *stream);
 /* Debugging hook: with on = 1, every later call that records device-side conditions in a
  * workspace status word (moe_router_topk, moe_router_topk_ex, moe_dispatch,
  * moe_expert_ffn, moe_layer_forward, moe_layer_forward_ex, moe_layer_forward_fp8,
- * moe_layer_norm_backward, moe_expert_ffn_backward) synchronises its stream after enqueueing
- * its work and returns that word, read and reset as by moe_read_status, in place of MOE_OK
- * -- except for an empty batch and inside a stream capture (a capture cannot be
+ * moe_layer_norm_backward, moe_expert_ffn_backward, moe_orthogonalize) synchronises its stream
+ * after enqueueing its work and returns that word, read and reset as by moe_read_status, in place
+ * of MOE_OK -- except for an empty batch and inside a stream capture (a capture cannot be
  * synchronised).  on = 0 (the default) restores the asynchronous calls.  Process-wide; not
  * for production use: it serialises the host with the GPU. */
 void moe_debug_set_sync_status(int on);
 
 /* Testing hook: sets the limit of the bounded device-side waits of the tensor-core FFN
- * kernels, forward and backward, and of moe_layer_norm and moe_layer_norm_backward (0 restores
- * the default of one second) and, with inject_stall = 1, makes the TMA producers of the FFN
- * kernels and the norms' copies of rows skip their work so that the waits run out and
- * MOE_ERR_DEVICE_TIMEOUT is recorded in the status word (no fault, no hang; moe_layer_norm has
- * none and reads the rows another way).  Affects later calls of these and of moe_layer_forward
+ * kernels, forward and backward, of moe_orthogonalize and of moe_layer_norm and
+ * moe_layer_norm_backward (0 restores the default of one second) and, with inject_stall = 1, makes
+ * the TMA producers of the FFN and moe_orthogonalize kernels and the norms' copies of rows skip
+ * their work so that the waits run out and MOE_ERR_DEVICE_TIMEOUT is recorded in the status word
+ * (no fault, no hang; moe_layer_norm has none and reads the rows another way).  Affects later calls of these and of moe_layer_forward
  * in the process; not for production use. */
 void moe_debug_set_wait_limit(unsigned long long limit_ns, int inject_stall);
 
@@ -560,6 +560,28 @@ int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, in
                                int x_fp32, const float *stats, const moe_residual_t *p, int T, int H,
                                void *dx, void *dy, const moe_residual_grads_t *grads, void *ws,
                                size_t ws_bytes, void *stream);
+
+/* Orthogonalised updates of a batch of weight matrices (the experts' [E, H, I] and [E, I, H]) by
+ * Newton-Schulz products, the update of the Muon optimiser.  Per matrix
+ *     momentum <- mu momentum + g;  u = g + mu momentum (nesterov), momentum, or g (no momentum)
+ *     X = u / |u|_F;  steps times  A = X X^T,  X <- a X + (b A + c A A) X;  out = scale X
+ * (A = X^T X and X <- a X + X (b A + c A A), the same matrix, where R > C).
+ *   g        [B, R, C], bf16 (g_fp32 == 0) or fp32 (g_fp32 == 1)
+ *   momentum fp32 [B, R, C], updated, or NULL (then mu is not read and nesterov must be 0)
+ *   coeffs   HOST array [steps][3] of a, b, c, read during the call, or NULL: 3.4445, -4.7750,
+ *            2.0315 in every step.  The iterates' singular values must stay below 8.
+ *   out      bf16 [B, R, C] (may be g's own memory where g is bf16)
+ *   ws       at least moe_orthogonalize_workspace_bytes(B, R, C) bytes (0 for an invalid shape):
+ *            about B (6 R C + 4 min(R, C)^2) bytes
+ * fp16 products with fp32 sums on the tensor cores; X is carried in 22 bits, so that directions with
+ * small singular values keep their precision; results are 0.2e-3 to 1.8e-3 off (2-norm) before
+ * out's rounding.  A matrix of zeros gives zeros; one with an infinity or a NaN gives NaN.  The
+ * results repeat bit for bit.  R, C <= 32768, B <= 65535, steps <= 32 (else
+ * MOE_ERR_UNSUPPORTED_SHAPE); any R and C from 1 on.  B == 0 enqueues nothing. */
+size_t moe_orthogonalize_workspace_bytes(int B, int R, int C);
+int moe_orthogonalize(const void *g, int g_fp32, float *momentum, float mu, int nesterov, int B, int R,
+                      int C, int steps, const float *coeffs, float scale, void *out, void *ws,
+                      size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------------------
  * GRACE-MoE placement planner ("GRACE-MoE" notes, Core Idea 1-3).  Host code on HOST

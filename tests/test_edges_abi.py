@@ -94,3 +94,26 @@ def test_bindings_check_types_and_sizes():
         B.moe_residual_norm(t(4, 64), t(4, 64), dict(gamma=t(64)), t(4, 64))
     with pytest.raises(ValueError, match="pre: group"):
         B.moe_residual_norm(t(4, 64), t(4, 64), dict(pre="group"), t(4, 64))
+
+
+def test_orthogonalize_refusals(lib):
+    def call(g=OK, f32=0, m=None, mu=0.95, nesterov=0, Bn=2, R=64, C=96, steps=5, co=None, scale=1.0, o=OK, ws=WS, n=BIG):
+        return lib.moe_orthogonalize(g, f32, m, mu, nesterov, Bn, R, C, steps, co, scale, o, ws, n, None)
+    nan = float("nan")
+    assert call(Bn=-1) == -1 and call(R=0) == -1 and call(C=-3) == -1 and call(f32=2) == -1 and call(nesterov=2, m=OK) == -1
+    assert call(steps=0) == -1 and call(nesterov=1) == -1 and call(mu=nan) == -1 and call(scale=nan) == -1
+    assert call(steps=33) == -2 and call(R=32769) == -2 and call(C=32769) == -2 and call(Bn=65536) == -2
+    assert call(co=ctypes.cast((ctypes.c_float * 15)(*[1.0] * 14, nan), P)) == -1
+    assert call(g=None) == -1 and call(o=None) == -1 and call(ws=None) == -1
+    assert call(g=BAD) == -3 and call(m=BAD) == -3 and call(o=BAD) == -3 and call(ws=P(0x100010)) == -3
+    need = B.moe_orthogonalize_workspace_bytes(2, 64, 96)
+    assert need > 0 and call(n=need - 1) == -4
+    assert call(Bn=0, g=None, o=None, ws=None) == 0
+    assert B.moe_orthogonalize_workspace_bytes(1, 0, 4) == 0 and B.moe_orthogonalize_workspace_bytes(1, 4, 32769) == 0
+    t = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype)
+    with pytest.raises(ValueError, match="out: dtype"):
+        B.moe_orthogonalize(t(4, 8), t(4, 8), t(256))
+    with pytest.raises(ValueError, match="momentum: 16 elements"):
+        B.moe_orthogonalize(t(4, 8), t(4, 8, dtype=torch.bfloat16), t(256), momentum=t(16))
+    with pytest.raises(ValueError, match="coeffs: 3 values, expected 6"):
+        B.moe_orthogonalize(t(4, 8), t(4, 8, dtype=torch.bfloat16), t(256), steps=2, coeffs=[(1, 2, 3)])
