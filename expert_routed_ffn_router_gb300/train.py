@@ -2,6 +2,10 @@
 
     out = x + sum_j w_j FFN_e(j)(n) + FFN_shared(n),   n = layer_norm(x)
 
+or, with a norm behind the experts, a gate for each channel or another scale of the stream,
+
+    out = alpha x + gate post_norm(sum_j w_j FFN_e(j)(n) + FFN_shared(n))
+
 with the routing weights w of a gate that is trained: logits = n W_gate^T in fp32.  Between the
 forward and the backward pass the block keeps x, the norm's statistics, the logits, the routing
 and its dispatch, and n in bf16, or with ``packed=True`` as an 8-bit checkpoint (E4M3 bytes and
@@ -24,7 +28,8 @@ bf16 once, the type moe_layer_norm_backward takes.
 
     python -m expert_routed_ffn_router_gb300.train --steps 30
 
-fits a small block to random targets and prints the loss.
+fits a small block to random targets and prints the loss; with ``--muon`` the experts' matrices take
+orthogonalised updates with momentum (Muon, below) in place of plain gradient descent.
 """
 from __future__ import annotations
 
@@ -41,10 +46,11 @@ EXPERTS = ("W1", "W3", "W2")
 class MoETrainBlock:
     """weights: gamma, beta fp32 [H]; W_gate fp32 [E, H]; bias fp32 [E] or None (selection
     only); W1, W3 bf16 [E, H, I], W2 bf16 [E, I, H]; optionally the shared expert's W1s, W3s
-    [H, Is], W2s [Is, H].  routing: as for moe_route_logits."""
+    [H, Is], W2s [Is, H], and gate fp32 [H], gamma_post and beta_post fp32 [H] (with post).  routing:
+    as for moe_route_logits; post, alpha: as for moe_residual_norm."""
 
     def __init__(self, weights: dict, T: int, K: int, routing=None, eps: float = 1e-5,
-                 packed: bool = False, x_dtype=F32):
+                 packed: bool = False, x_dtype=F32, post: str = "none", alpha: float = 1.0):
         self.w, self.T, self.K, self.eps, self.packed = weights, T, K, eps, packed
         self.routing = B.MoeRouting.make(**routing) if isinstance(routing, dict) else routing
         self.E, self.H, self.I = weights["W1"].shape
@@ -75,14 +81,22 @@ class MoETrainBlock:
         self.d_topk_w, self.d_logits = new(T, K), new(T, E)
         self.dn, self.dY, self.dx = new(T, H, dtype=BF16), new(T, H, dtype=BF16), new(T, H, dtype=x_dtype)
         self.dn_shared = new(T, H, dtype=BF16) if self.shared else None
+        # the branch's own norm, gate and scale: the stream is joined by one kernel each way then
+        ends = tuple(n for n in (("gamma_post", "beta_post") if post != "none" else ()) + ("gate",)
+                     if weights.get(n) is not None)
+        self.join = dict(post=post, alpha=alpha, eps_post=eps, **{n: weights[n] for n in ends})
+        self.joined = post != "none" or alpha != 1.0 or bool(ends)
+        self.stats = new(T, 4) if self.joined else None
         names = EXPERTS + (tuple(n + "s" for n in EXPERTS) if self.shared else ())
-        self.grads = {n: torch.empty_like(weights[n]) for n in ("gamma", "beta", "W_gate") + names}
+        self.grads = {n: torch.empty_like(weights[n]) for n in ("gamma", "beta", "W_gate") + names + ends}
+        self.join_grads = {n: self.grads[n] for n in ends}
         # the shared expert: one group that holds every token once, weight 1
         self.all_rows = torch.tensor([0, T], dtype=I32, device=dev)
         self.each_row = torch.arange(T, dtype=I32, device=dev).view(T, 1)
         nbytes = max(B.moe_workspace_bytes(T, H, E, K, I, Is), B.moe_expert_ffn_workspace_bytes(T * K, E, I),
                      B.moe_expert_ffn_backward_workspace_bytes(T, H, E, K, I),
                      B.moe_layer_norm_backward_workspace_bytes(T, H),
+                     B.moe_residual_norm_backward_workspace_bytes(T, H) if self.joined else 0,
                      B.moe_expert_ffn_workspace_bytes(T, 1, Is) if self.shared else 0,
                      B.moe_expert_ffn_backward_workspace_bytes(T, H, 1, 1, Is) if self.shared else 0)
         if nbytes == 0 or B.moe_expert_ffn_backward_workspace_bytes(T, H, E, K, I) == 0:
@@ -103,7 +117,10 @@ class MoETrainBlock:
         if self.shared:
             B.moe_expert_ffn(self.n, self.all_rows, 1, w["W1s"], w["W3s"], w["W2s"], self.Ysh, self.ws)
         B.moe_combine(self.Yp, self.slot_pos, self.topk_w, self.Ysh, self.Y)
-        torch.add(x, self.Y, out=self.out)
+        if self.joined:
+            B.moe_residual_norm(x, self.Y, self.join, self.out, None, self.stats)
+        else:
+            torch.add(x, self.Y, out=self.out)
         return self.out
 
     def backward(self, dout: torch.Tensor):
@@ -113,7 +130,13 @@ class MoETrainBlock:
             raise RuntimeError("backward() before forward()")
         w, g = self.w, self.grads
         rows, scale = (self.q, self.scale) if self.packed else (self.n, None)
-        self.dY.copy_(dout)
+        dres = dout
+        if self.joined:
+            dres = self.dx
+            B.moe_residual_norm_backward(None, dout, self.Y, None, self.stats, self.join, self.dx, self.dY,
+                                         self.join_grads, self.ws)
+        else:
+            self.dY.copy_(dout)
         B.moe_expert_ffn_backward(rows, scale, self.dY, self.offsets, self.slot_pos, self.topk_w, w["W1"],
                                   w["W3"], w["W2"], self.dn, self.d_topk_w, g["W1"], g["W3"], g["W2"], self.ws)
         B.moe_route_logits_backward(self.logits, self.routing, self.topk_idx, self.d_topk_w, self.d_logits)
@@ -125,9 +148,53 @@ class MoETrainBlock:
                                       w["W1s"][None], w["W3s"][None], w["W2s"][None], self.dn_shared, None,
                                       g["W1s"][None], g["W3s"][None], g["W2s"][None], self.ws)
             dn += self.dn_shared
-        B.moe_layer_norm_backward(dn.to(BF16), self.x, w["gamma"], self.mean, self.rstd, dout, self.dx,
+        B.moe_layer_norm_backward(dn.to(BF16), self.x, w["gamma"], self.mean, self.rstd, dres, self.dx,
                                   g["gamma"], g["beta"], self.ws)
         return self.dx, g
+
+    def status(self) -> int:
+        """Conditions the kernels recorded (moe_read_status; synchronises)."""
+        return B.moe_read_status(self.ws)
+
+
+class Muon:
+    """Orthogonalised updates with momentum for a block's matrices.
+
+        m <- mu m + g,  W <- (1 - lr decay) W - lr 0.2 sqrt(max(R, C)) orthogonalised(g + mu m)
+
+    The factor gives every entry of the update a mean square of about 0.2^2, whatever the matrix's
+    sides.  weights: the bf16 tensors by name, [R, C] or [E, R, C]; master copies in fp32 and the
+    momentum are kept here.  experts: matrices that one call orthogonalises (the workspace grows
+    with them; None: all of a tensor)."""
+
+    def __init__(self, weights: dict, lr: float = 0.02, mu: float = 0.95, decay: float = 0.0, experts=None):
+        self.weights, self.lr, self.mu, self.decay, self.experts = weights, lr, mu, decay, experts
+        self.master = {n: w.float() for n, w in weights.items()}
+        self.momentum = {n: torch.zeros_like(m) for n, m in self.master.items()}
+        self.update = {n: torch.empty_like(w, dtype=BF16) for n, w in weights.items()}
+        need = 256
+        for w in weights.values():
+            b, R, C = self._shape(w)
+            need = max(need, B.moe_orthogonalize_workspace_bytes(min(b, experts or b), R, C))
+        device = next(iter(weights.values())).device if weights else "cuda"
+        self.ws = torch.zeros(need, dtype=torch.uint8, device=device)
+
+    @staticmethod
+    def _shape(w):
+        return ((1,) + tuple(w.shape))[-3:]
+
+    def step(self, grads: dict) -> None:
+        """grads: the gradients by name (bf16 or fp32), of all or some of the weights."""
+        for n, g in grads.items():
+            b, R, C = self._shape(g)
+            k = min(b, self.experts or b)
+            v = [t.view(b, R, C) for t in (g, self.update[n], self.momentum[n])]
+            for i in range(0, b, k):
+                gi, ui, mi = (t[i:i + k] for t in v)
+                B.moe_orthogonalize(gi, ui, self.ws, momentum=mi, mu=self.mu, nesterov=True,
+                                    scale=0.2 * max(R, C) ** 0.5)
+            self.master[n].mul_(1 - self.lr * self.decay).sub_(self.update[n], alpha=self.lr)
+            self.weights[n].copy_(self.master[n])
 
     def status(self) -> int:
         """Conditions the kernels recorded (moe_read_status; synchronises)."""
@@ -149,23 +216,29 @@ def random_weights(H, E, I, Is, device, seed=0) -> dict:
     return w
 
 
-def fit(steps=30, T=512, H=256, E=16, K=2, I=128, Is=128, lr=2.0, seed=0, device="cuda", packed=False):
-    """Plain gradient descent on mean (out - target)^2 over one fixed batch; the losses."""
+def fit(steps=30, T=512, H=256, E=16, K=2, I=128, Is=128, lr=2.0, seed=0, device="cuda", packed=False,
+        muon=False):
+    """Plain gradient descent (muon: orthogonalised updates for the experts' matrices) on mean
+    (out - target)^2 over one fixed batch; the losses."""
     g = torch.Generator(device=device).manual_seed(seed + 1)
     x = torch.randn(T, H, generator=g, device=device)
     target = x + 0.5 * torch.randn(T, H, generator=g, device=device)
     weights = random_weights(H, E, I, Is, device, seed)
     block = MoETrainBlock(weights, T, K, packed=packed)
-    master = {n: weights[n].float() for n in block.grads}
+    matrices = [n for n in block.grads if n.rstrip("s") in EXPERTS] if muon else []
+    optimizer = Muon({n: weights[n] for n in matrices}, lr=0.01 * lr) if muon else None
+    master = {n: weights[n].float() for n in block.grads if n not in matrices}
     losses = []
     for _ in range(steps):
         diff = block.forward(x) - target
         losses.append(float(diff.square().mean()))
         _, grads = block.backward(2.0 / diff.numel() * diff)
-        for n, v in grads.items():
-            master[n] -= lr * v.float()
+        for n in master:
+            master[n] -= lr * grads[n].float()
             weights[n].copy_(master[n])
-    status = block.status()                      # (reading it resets it)
+        if muon:
+            optimizer.step({n: grads[n] for n in matrices})
+    status = block.status() or (optimizer.status() if muon else 0)       # (reading it resets it)
     if status != 0:
         raise B.MoeError("training step", status)
     return losses
@@ -179,8 +252,9 @@ def main(argv=None):
     rows = ap.add_mutually_exclusive_group()
     rows.add_argument("--packed", action="store_true", help="keep the token rows in 8 bits for the backward pass")
     rows.add_argument("--bf16-rows", action="store_true", help="keep them in bf16 (the default)")
+    ap.add_argument("--muon", action="store_true", help="orthogonalised updates for the experts' matrices")
     a = ap.parse_args(argv)
-    for i, v in enumerate(fit(steps=a.steps, T=a.T, lr=a.lr, packed=a.packed)):
+    for i, v in enumerate(fit(steps=a.steps, T=a.T, lr=a.lr, packed=a.packed, muon=a.muon)):
         print(f"step {i:3d}  loss {v:.6f}")
 
 
