@@ -875,7 +875,7 @@ int moe_orthogonalize(const void *g, int g_fp32, float *momentum, float mu, int 
                       int steps, const float *coeffs, float scale, void *out, void *ws, size_t ws_bytes,
                       void *stream)
 {
-    constexpr int kMost = 32;
+    constexpr int kMost = 32;    // (MAX_STEPS of the kernels)
     int rc = check_ortho(B, R, C);
     if (rc) return rc;
     if ((g_fp32 != 0 && g_fp32 != 1) || (nesterov != 0 && nesterov != 1)) return MOE_ERR_INVALID_ARG;

@@ -41,26 +41,29 @@ namespace {
 constexpr float SX = 4096.f, SA = 512.f;
 constexpr float SLO = 2048.f;             // the second number of X: its own power of two on top
 
-constexpr int TM = 256, TN = 256, BK = 64;
+constexpr int TM = 256, TN = 256, BK = 64;   // tiles of a cluster (at most)
 constexpr int N_EPI = 8, EPI0 = 4;
 constexpr int NT = 32 * (EPI0 + N_EPI);
 constexpr int HALF = 8192;                // 64 x 64 fp16
 constexpr int STAGE = 4 * HALF;
 constexpr int STAGES = 5;
-constexpr int SLAB = 8192;
+constexpr int PC = 32;                    // columns of an epilogue's piece
+constexpr int SLOT = 2 * 32 * PC * 2;     // its two arrays: the mirror image, or X's two numbers
+constexpr int SLOTS = 2;
+constexpr int SLAB = SLOTS * SLOT;        // an epilogue warp's buffers
 
 enum { GRAM, SQUARE, APPLY, LAST };
 
 struct Args {
     // loads: K-major operands in boxes of 128 x 64, MN-major ones in boxes of 64 x 64
     CUtensorMap a, b;
-    // stores: tiles of 32 x 64 (and of X's second numbers), mirror images of 64 x 32
-    CUtensorMap s, s2, sm;
+    // the epilogue's pieces of 32 rows: loads (SQUARE: A; APPLY: X's numbers), stores
+    CUtensorMap l, l2, s, s2;
     int mode, amn, bmn;           // operand rows (columns) contiguous
-    int B, M, N, K;               // products [M][K] x [K][N] of each matrix
+    int M, N, K;                  // products [M][K] x [K][N] of each matrix
     int nM, nN, tiles;            // tiles of a matrix in each direction, in all
-    const uint16_t *add, *add2;   // SQUARE: A; APPLY: X's numbers; rows of `ld`
-    int ld;
+    int tm, tn;                   // rows and columns of a tile that are kept
+    int tma_out;                  // LAST: rows of `out` are multiples of 16 bytes
     float ca, cb, cc;             // coefficients
     float scale;
     uint16_t *out;                // LAST: bf16 [B][M][N]
@@ -102,23 +105,28 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, 
 
 struct Tile { int b, m0, n0; };
 
+template <bool SYM>
 __device__ __forceinline__ Tile tile_at(const Args &p, int t)
 {
-    const int per = p.mode <= SQUARE ? p.nM * (p.nM + 1) / 2 : p.nM * p.nN;
+    const int per = SYM ? p.nM * (p.nM + 1) / 2 : p.nM * p.nN;
     const int b = t / per;
     int l = t - b * per, i, j;
-    if (p.mode <= SQUARE) {
+    if (SYM) {
         i = static_cast<int>((sqrtf(8.f * l + 1.f) - 1.f) * 0.5f);
         while (i * (i + 1) / 2 > l) --i;
         while ((i + 1) * (i + 2) / 2 <= l) ++i;
         j = l - i * (i + 1) / 2;
     } else {
-        j = l / p.nM;              // the rows of tiles innermost: they share columns of the larger operand
-        i = l - j * p.nM;
+        // the smaller side's tiles innermost: they share a part of X (rows innermost for tall matrices:
+        // 695 instead of 672 us for 16 of 7168 x 2048)
+        if (p.nM > p.nN) { i = l / p.nN; j = l - i * p.nN; }
+        else { j = l / p.nM; i = l - j * p.nM; }
     }
-    return Tile{b, i * TM, j * TN};
+    return Tile{b, i * p.tm, j * p.tn};
 }
 
+// SYM: GRAM and SQUARE, whose results are symmetric; else APPLY and LAST.
+template <bool SYM>
 __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant__ Args p)
 {
     constexpr int TCOLS = 512;
@@ -126,7 +134,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
     unsigned char *ring = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *slabs = ring + STAGES * STAGE;
-    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
+    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], piece[N_EPI][SLOTS], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     volatile int *abort_flag = &abort_s;
@@ -144,6 +152,8 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 2 * N_EPI);
         }
+        for (int w = 0; w < N_EPI; ++w)
+            for (int b = 0; b < SLOTS; ++b) mbar_init(&piece[w][b], 1);
         mbar_init(&drain, 1);
         abort_s = 0;
         fence_mbar_init();
@@ -169,8 +179,8 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             const int r = static_cast<int>(rank);
             bool good = true;
             for (int t = cluster; t < p.tiles && good; t += clusters) {
-                const Tile T = tile_at(p, t);
-                const int m = T.m0 + 128 * r, n = T.n0 + 128 * r;
+                const Tile T = tile_at<SYM>(p, t);
+                const int m = T.m0 + 128 * r, n = T.n0 + p.tn / 2 * r;
                 for (int kb = 0; kb < kbs; ++kb, ++it) {
                     if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
                     unsigned char *a = ring + s * STAGE, *b = a + 2 * HALF;
@@ -214,7 +224,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             const uint64_t ad0 = smem_desc_sw128(ring0, p.amn ? HALF : 16, 1024);
             const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, p.bmn ? HALF : 16, 1024);
             const uint32_t as = p.amn ? 128u : 2u, bs = p.bmn ? 128u : 2u;
-            const uint32_t id = idesc_f16_f32(TM, TN, p.amn, p.bmn);
+            const uint32_t id = idesc_f16_f32(TM, static_cast<uint32_t>(p.tn), p.amn, p.bmn);
             uint32_t s = 0, ph = 0, b = 0, tph = 0;
             bool good = true;
             for (int t = cluster; t < p.tiles && good; t += clusters) {
@@ -244,126 +254,178 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         }
     } else if (warp >= EPI0) {
         // ---------------------------------------------------------------- epilogue
+        // A warp's pieces of a tile, one after the other: what is added to the sums arrives ahead of time
+        // by TMA, and the results leave from the same buffer.
         const int q = warp & 3, half = (warp - EPI0) >> 2;   // lane quarter, half of the columns
         const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
         const int r0 = 128 * static_cast<int>(rank) + 32 * q;
         unsigned char *slab = slabs + (warp - EPI0) * SLAB;
-        uint32_t b = 0, tph = 0;
-        for (int t = cluster; t < p.tiles; t += clusters) {
-            const Tile T = tile_at(p, t);
-            bool good = true;
+        uint64_t *arrived = piece[warp - EPI0];
+        const int pieces = p.tn / PC, c0 = half ? (pieces + 1) / 2 : 0, c1 = half ? pieces : (pieces + 1) / 2;
+        const bool loads = p.mode != GRAM;
+        // the pieces of a tile that this warp has: from c0 on
+        auto last_piece = [&](const Tile &T) {
+            if (r0 >= p.tm || T.m0 + r0 >= p.M) return c0;
+            const int n = (p.N - T.n0 + PC - 1) / PC;
+            return c1 < n ? c1 : (n > c0 ? n : c0);
+        };
+        // the next piece to be loaded
+        int ft = cluster, fc = c0;
+        Tile F{};
+        auto settle = [&]() {                // to the first tile that has one
+            while (ft < p.tiles) {
+                F = tile_at<SYM>(p, ft);
+                if (fc < last_piece(F)) return;
+                ft += clusters;
+                fc = c0;
+            }
+        };
+        int issued = 0, taken = 0;
+        auto load_piece = [&](int slot) {    // lane 0
+            if (ft >= p.tiles) return;
+            ++issued;
+            unsigned char *d = slab + slot * SLOT;
+            const int col = F.n0 + PC * fc;
+            mbar_arrive_expect_tx(&arrived[slot], SYM ? SLOT / 2 : SLOT);
+            tma_load_3d(d, &p.l, &arrived[slot], col, F.m0 + r0, F.b);
+            if (!SYM) tma_load_3d(d + SLOT / 2, &p.l2, &arrived[slot], col, F.m0 + r0, F.b);
+            ++fc;
+            settle();
+        };
+        uint32_t b = 0, tph = 0, slot = 0, pph = 0;
+        if (loads && lane == 0 && !p.inject) {
+            settle();
+            for (int i = 0; i < SLOTS; ++i) load_piece(i);
+        }
+        bool good = true;
+        for (int t = cluster; t < p.tiles && good; t += clusters) {
+            const Tile T = tile_at<SYM>(p, t);
             if (lane == 0) good = mbar_wait(&tfull[b], tph, abort_flag, p.status, tmo);
             good = __shfl_sync(kFullMask, good, 0);
             if (!good) break;
             mbar_try_wait(&tfull[b], tph);
             tc_fence_after();
             const int m0 = T.m0 + r0, row = m0 + lane;
-            const bool mirror = p.mode <= SQUARE && T.m0 != T.n0;
-            const size_t at = (static_cast<size_t>(T.b) * p.M + row) * p.ld;
+            const bool mirror = SYM && T.m0 != T.n0;
+            const int end = last_piece(T);
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                const int lc = 128 * half + 32 * c, col = T.n0 + lc;
-                if (col >= p.N) break;
-                if (m0 >= p.M) break;
-                float v[32];
+            for (int c = c0; c < end; ++c) {
+                const int col = T.n0 + PC * c;
+                unsigned char *buf = slab + slot * SLOT;
                 __syncwarp();
-                tmem_ld32(tm0 + b * TN + lc, v);
-                uint4 h[4], l[4];
-                if (p.mode != GRAM && row < p.M) {
-                    // (the last columns of a row end within ld, a multiple of 8)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool in = col + 8 * i < p.N;
-                        h[i] = in ? *reinterpret_cast<const uint4 *>(p.add + at + col + 8 * i) : make_uint4(0, 0, 0, 0);
-                        if (p.mode >= APPLY)
-                            l[i] = in ? *reinterpret_cast<const uint4 *>(p.add2 + at + col + 8 * i) : make_uint4(0, 0, 0, 0);
+                if (lane == 0) {
+                    if (loads) {
+                        good = mbar_wait(&arrived[slot], pph, abort_flag, p.status, tmo);
+                        taken += good ? 1 : 0;
+                    } else {
+                        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
                     }
                 }
-                if (p.mode == GRAM) {
+                good = __shfl_sync(kFullMask, good, 0);
+                if (!good) break;
+                if (loads) mbar_try_wait(&arrived[slot], pph);
+                const bool direct = !SYM && p.mode == LAST && !p.tma_out;
+                float v[32];
+                tmem_ld32(tm0 + b * TN + PC * c, v);
+                // 16 bytes of the lane's row, in the 64-byte swizzle
+                auto at = [&](int i) -> uint4 * {
+                    return reinterpret_cast<uint4 *>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+                };
+                auto at2 = [&](int i) -> uint4 * { return at(i) + SLOT / 2 / 16; };
+                if (SYM && p.mode == GRAM) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] *= SA / (SX * SX);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint4 hv = h[i / 4], lv = p.mode >= APPLY ? l[i / 4] : make_uint4(0, 0, 0, 0);
-                        const uint32_t hw = (i & 3) == 0 ? hv.x : (i & 3) == 1 ? hv.y : (i & 3) == 2 ? hv.z : hv.w;
-                        const uint32_t lw = (i & 3) == 0 ? lv.x : (i & 3) == 1 ? lv.y : (i & 3) == 2 ? lv.z : lv.w;
-                        float x0 = f16_lo(hw), x1 = f16_hi(hw);
-                        if (p.mode >= APPLY) {
-                            x0 = fmaf(f16_lo(lw), 1.f / SLO, x0);
-                            x1 = fmaf(f16_hi(lw), 1.f / SLO, x1);
-                            v[2 * i] = fmaf(p.ca, x0, v[2 * i] * (1.f / SA));
-                            v[2 * i + 1] = fmaf(p.ca, x1, v[2 * i + 1] * (1.f / SA));
-                        } else {
-                            v[2 * i] = fmaf(p.cb, x0, v[2 * i] * (p.cc / SA));
-                            v[2 * i + 1] = fmaf(p.cb, x1, v[2 * i + 1] * (p.cc / SA));
-                        }
-                    }
-                }
-                if (p.mode == LAST) {
-                    if (row < p.M) {
-                        const float f = p.scale / SX;
-                        uint16_t *o = p.out + (static_cast<size_t>(T.b) * p.M + row) * p.N + col;
-                        if (p.N % 8 == 0) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (col + 8 * i < p.N)
-                                    reinterpret_cast<uint4 *>(o)[i] =
-                                        make_uint4(f32x2_to_bf16x2(v[8 * i + 1] * f, v[8 * i] * f), f32x2_to_bf16x2(v[8 * i + 3] * f, v[8 * i + 2] * f),
-                                                   f32x2_to_bf16x2(v[8 * i + 5] * f, v[8 * i + 4] * f), f32x2_to_bf16x2(v[8 * i + 7] * f, v[8 * i + 6] * f));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (col + i < p.N) o[i] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * f));
-                        }
-                    }
-                    continue;
-                }
-                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                __syncwarp();
-                // 32 columns of the lane's row, 64 bytes: the first numbers, and the second ones or
-                // the mirror image, each as 32 rows of 64 bytes in the 64-byte swizzle
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = f32x2_to_f16x2(v[2 * i + 1], v[2 * i]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4 *>(slab + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                if (p.mode == APPLY) {
-#pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint32_t y[4];
+                        const uint4 h = *at(i), l = SYM ? make_uint4(0, 0, 0, 0) : *at2(i);
+                        const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            y[k] = f32x2_to_f16x2((v[8 * i + 2 * k + 1] - f16_hi(w[4 * i + k])) * SLO,
-                                                  (v[8 * i + 2 * k] - f16_lo(w[4 * i + k])) * SLO);
-                        *reinterpret_cast<uint4 *>(slab + 2048 + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-                            make_uint4(y[0], y[1], y[2], y[3]);
+                        for (int k = 0; k < 4; ++k) {
+                            const int j = 8 * i + 2 * k;
+                            float x0 = f16_lo(hw[k]), x1 = f16_hi(hw[k]);
+                            if (SYM) {
+                                v[j] = fmaf(p.cb, x0, v[j] * (p.cc / SA));
+                                v[j + 1] = fmaf(p.cb, x1, v[j + 1] * (p.cc / SA));
+                            } else {
+                                x0 = fmaf(f16_lo(lw[k]), 1.f / SLO, x0);
+                                x1 = fmaf(f16_hi(lw[k]), 1.f / SLO, x1);
+                                v[j] = fmaf(p.ca, x0, v[j] * (1.f / SA));
+                                v[j + 1] = fmaf(p.ca, x1, v[j + 1] * (1.f / SA));
+                            }
+                        }
                     }
-                } else if (mirror) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        *reinterpret_cast<uint16_t *>(slab + 2048 + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2) =
-                            static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                const float f = p.scale / SX;
+                if (direct) {
+                    if (row < p.M) {
+                        uint16_t *o = p.out + (static_cast<size_t>(T.b) * p.M + row) * p.N + col;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (col + i < p.N) o[i] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * f));
+                    }
+                } else {
+                    uint32_t w[16];
+                    if (!SYM && p.mode == LAST) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = f32x2_to_bf16x2(v[2 * i + 1] * f, v[2 * i] * f);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = f32x2_to_f16x2(v[2 * i + 1], v[2 * i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) *at(i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    if (!SYM && p.mode == APPLY) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                y[k] = f32x2_to_f16x2((v[8 * i + 2 * k + 1] - f16_hi(w[4 * i + k])) * SLO,
+                                                      (v[8 * i + 2 * k] - f16_lo(w[4 * i + k])) * SLO);
+                            *at2(i) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    if (mirror) {
+                        // row j of the mirror image: this lane's number of column j
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            *reinterpret_cast<uint16_t *>(buf + SLOT / 2 + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2) =
+                                static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+                    }
+                }
+                if (!direct) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_3d(&p.s, slab, col, m0, T.b);
-                    if (p.mode == APPLY) tma_store_3d(&p.s2, slab + 2048, col, m0, T.b);
-                    else if (mirror) tma_store_3d(&p.sm, slab + 2048, m0, col, T.b);
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    if (!direct) {
+                        tma_store_3d(&p.s, buf, col, m0, T.b);
+                        if (!SYM && p.mode == APPLY) tma_store_3d(&p.s2, buf + SLOT / 2, col, m0, T.b);
+                        if (mirror) tma_store_3d(&p.s, buf + SLOT / 2, m0, col, T.b);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    if (loads) {             // the buffer's next piece, once this one has left it
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        load_piece(slot);
+                    }
                 }
+                if (++slot == SLOTS) { slot = 0; pph ^= 1u; }
             }
+            if (!good) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0 + 8u * b);
             b ^= 1u;
             if (b == 0) tph ^= 1u;
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0) {
+            // pieces still on their way (after a wait that ran out), and the last stores
+            for (; taken < issued; ++taken) {
+                int dummy = 0;
+                mbar_wait(&arrived[taken % SLOTS], (taken / SLOTS) & 1u, &dummy, nullptr, 20000000ull);
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncwarp();
@@ -379,6 +441,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
 // ------------------------------------------------------------------ momentum, norm, X
 constexpr int PT = 256;               // threads
 constexpr int MAX_PARTS = 256;        // chunks of a matrix
+constexpr int MAX_STEPS = 32;
 
 struct Prepare {
     const void *g;
@@ -438,6 +501,18 @@ __device__ __forceinline__ float warp_sum(float v)
 // Square sums of u, of 2^60 u and of 2^-80 u: one of them holds |u| to fp32's precision whatever the
 // size of the entries.
 constexpr float UP = 1152921504606846976.f, DOWN = 1.f / (UP * 1048576.f);
+
+// SX x = (u f) times the result, f a power of two, from the square sums.  (One of u below 2^-60 may have
+// lost terms to underflow, one above 2^100 to overflow; those at the other scales are then within
+// range.)  A matrix of zeros stays one; an infinity or a NaN makes it NaN.
+__device__ __forceinline__ float x_factor(float s0, float s1, float s2, float &f)
+{
+    float s = s0;
+    f = 1.f;
+    if (!(s0 >= 1.f / UP)) { f = UP; s = s1; }
+    else if (!(s0 <= UP * 1099511627776.f)) { f = DOWN; s = s2; }
+    return s > 0.f ? (s <= 3.402823466e38f ? SX / sqrtf(s) : s - s) : s;
+}
 
 // VEC: R C and C are multiples of 8.  CTA (part, matrix): the momentum, and the chunk's square sums.
 template <bool VEC>
@@ -505,13 +580,8 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
     __syncthreads();
     s0 = s1 = s2 = 0.f;
     for (int k = 0; k < PT / 32; ++k) { s0 += red[0][k]; s1 += red[1][k]; s2 += red[2][k]; }
-    // x = (u f) / |u f|, f a power of two.  (A square sum below 2^-60 may have lost terms to underflow,
-    // one above 2^100 to overflow; the sums at the other scales are then within range.)
-    float f = 1.f, s = s0;
-    if (!(s0 >= 1.f / UP)) { f = UP; s = s1; }
-    else if (!(s0 <= UP * 1099511627776.f)) { f = DOWN; s = s2; }
-    // (a matrix of zeros stays one; an infinity or a NaN makes it NaN)
-    const float inv = s > 0.f ? (s <= 3.402823466e38f ? SX / sqrtf(s) : s - s) : s;
+    float f;
+    const float inv = x_factor(s0, s1, s2, f);
     const long long n = static_cast<long long>(p.R) * p.C;
     const size_t base = static_cast<size_t>(blockIdx.y) * n;
     const long long lo = blockIdx.x * p.chunk, hi = min(n, lo + p.chunk);
@@ -542,6 +612,281 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
             p.hi[at] = static_cast<uint16_t>(h);
             p.lo[at] = static_cast<uint16_t>(f32x2_to_f16x2(0.f, (a - f16_lo(h)) * SLO));
         }
+    }
+}
+
+// ---------------------------------------------------------------------- small matrices
+// A CTA a matrix of up to 128 on the smaller side and 384 on the larger one, all steps in one launch:
+// X as the products' operand (fp16), A and P in shared memory, X itself (fp32) in tensor memory,
+// times a SA: the product with P is added to it there.  (The launches for large ones take 100 us for
+// 16 matrices of 256 x 128, this one @SMALL@.)
+constexpr int SM_SIDE = 128, SM_LONG = 384;
+constexpr int ST = 256;               // threads: two warps for each 32 rows, each half of the columns
+constexpr int CHUNK = 128 * 128;      // 128 rows x 64 fp16
+
+struct Small {
+    Prepare q;
+    int tall, m, n, np;               // sides of X (m <= n), n up to a multiple of 64
+    int steps;
+    float c[3 * MAX_STEPS];
+    float scale;
+    uint16_t *out;
+    int *status;
+    unsigned long long timeout_ns;
+    int inject;
+};
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+        ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+          "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+          "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+          "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// u of 32 columns of a row of X from c0 on (0 outside), after the momentum's update
+template <bool VEC>
+__device__ __forceinline__ void small_load(const Small &p, size_t base, int row, int c0, float (&v)[32])
+{
+    const Prepare &q = p.q;
+    if (VEC && !p.tall) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (row < p.m && c0 + 8 * i < p.n) {
+                const size_t at = base + static_cast<size_t>(row) * p.n + c0 + 8 * i;
+                load_g<true>(q, at, u);
+                if (q.m) {
+                    float m[8];
+                    load_m<true>(q.m, at, m);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        m[k] = fmaf(q.mu, m[k], u[k]);
+                        u[k] = q.nesterov ? fmaf(q.mu, m[k], u[k]) : m[k];
+                    }
+                    float4 *o = reinterpret_cast<float4 *>(q.m + at);
+                    o[0] = make_float4(m[0], m[1], m[2], m[3]);
+                    o[1] = make_float4(m[4], m[5], m[6], m[7]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[8 * i + k] = u[k];
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const int c = c0 + i;
+        float u[1] = {0.f};
+        if (row < p.m && c < p.n) {
+            const size_t at = base + (p.tall ? static_cast<size_t>(c) * p.m + row : static_cast<size_t>(row) * p.n + c);
+            load_g<false>(q, at, u);
+            if (q.m) {
+                const float m = fmaf(q.mu, q.m[at], u[0]);
+                q.m[at] = m;
+                u[0] = q.nesterov ? fmaf(q.mu, m, u[0]) : m;
+            }
+        }
+        v[i] = u[0];
+    }
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constant__ Small p)
+{
+    constexpr uint32_t TCOLS = 512, TD = SM_LONG;    // X, then the sums of A and A A
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sx = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char *sa = sx + p.np / 64 * CHUNK, *sp = sa + 2 * CHUNK;
+    __shared__ uint64_t done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ float red[3][ST / 32];
+    __shared__ int abort_s;
+    volatile int *abort_flag = &abort_s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        mbar_init(&done, 1);
+        abort_s = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_slot, TCOLS);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
+    const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const int nh = p.np / 2, x0 = half * nh;         // this thread's columns of X: x0 .. x0 + nh
+    const size_t base = static_cast<size_t>(blockIdx.x) * p.m * p.n;
+    // 32 numbers of the thread's row, from column c of an operand of 64-column chunks
+    auto put = [&](unsigned char *s, int c, const uint32_t (&w)[16]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(s + (c >> 6) * CHUNK + row * 128 + ((((c & 63) / 8 + i) ^ (row & 7)) << 4)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    };
+
+    // u to tensor memory, and its square sums (see ortho_momentum_kernel)
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f;
+    for (int c = x0; c < x0 + nh; c += 32) {
+        float v[32];
+        small_load<VEC>(p, base, row, c, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            s0 = fmaf(v[i], v[i], s0);
+            const float a = v[i] * UP, b = v[i] * DOWN;
+            s1 = fmaf(a, a, s1);
+            s2 = fmaf(b, b, s2);
+        }
+        __syncwarp();
+        tmem_st32(tm0 + c, v);
+    }
+    tmem_st_wait();
+    s0 = warp_sum(s0); s1 = warp_sum(s1); s2 = warp_sum(s2);
+    if (lane == 0) { red[0][warp] = s0; red[1][warp] = s1; red[2][warp] = s2; }
+    __syncthreads();
+    s0 = s1 = s2 = 0.f;
+    for (int k = 0; k < ST / 32; ++k) { s0 += red[0][k]; s1 += red[1][k]; s2 += red[2][k]; }
+    float f;
+    const float inv = x_factor(s0, s1, s2, f);
+
+    uint32_t ph = 0;
+    bool good = true;
+    // every MMA since the last call is done: its sums may be read, its operands overwritten
+    auto finished = [&]() {
+        good = mbar_wait(&done, ph, abort_flag, p.status, p.timeout_ns) && good;
+        ph ^= 1u;
+        __syncwarp();
+        tc_fence_after();
+    };
+    // operands and sums of all threads are in place for the next MMAs
+    auto in_place = [&]() {
+        tmem_st_wait();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        good = __syncthreads_and(good) != 0;
+        tc_fence_after();
+    };
+    const bool issuer = tid == 0 && !p.inject;
+    const uint32_t ux = smem_u32(sx), ua = smem_u32(sa), up = smem_u32(sp);
+    for (int k = 0; k <= p.steps; ++k) {
+        // X of this step: the operand, and a SA X in tensor memory; after the last one, the result
+        const bool last = k == p.steps;
+        const float take = k == 0 ? f : 1.f / SA, mul = k == 0 ? inv : 1.f, keep = last ? 0.f : p.c[3 * k] * SA;
+        for (int c = x0; c < x0 + nh; c += 32) {
+            float v[32];
+            __syncwarp();
+            tmem_ld32(tm0 + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = v[i] * take * mul;
+            if (!last) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = f32x2_to_f16x2(v[2 * i + 1], v[2 * i]);
+                put(sx, c, w);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= keep;
+                tmem_st32(tm0 + c, v);
+                continue;
+            }
+            if (row >= p.m) continue;
+            const float o = p.scale / SX;
+            if (VEC && !p.tall) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + 8 * i < p.n)
+                        *reinterpret_cast<uint4 *>(p.out + base + static_cast<size_t>(row) * p.n + c + 8 * i) =
+                            make_uint4(f32x2_to_bf16x2(v[8 * i + 1] * o, v[8 * i] * o), f32x2_to_bf16x2(v[8 * i + 3] * o, v[8 * i + 2] * o),
+                                       f32x2_to_bf16x2(v[8 * i + 5] * o, v[8 * i + 4] * o), f32x2_to_bf16x2(v[8 * i + 7] * o, v[8 * i + 6] * o));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c + i < p.n)
+                        p.out[base + (p.tall ? static_cast<size_t>(c + i) * p.m + row : static_cast<size_t>(row) * p.n + c + i)] =
+                            static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * o));
+            }
+        }
+        if (last) break;
+        in_place();
+        if (!good) break;
+        if (issuer) {                                // A = X X^T
+            const uint32_t id = idesc_f16_f32(128, 128, false, false);
+            for (int i = 0; i < p.np / 16; ++i) {
+                const uint64_t d = smem_desc_sw128(ux + (i >> 2) * CHUNK + (i & 3) * 32, 16, 1024);
+                tc_mma_bf16(tmem + TD, d, d, id, i > 0 ? 1u : 0u);
+            }
+            tc_commit(&done);
+        }
+        finished();
+        uint32_t a[2][16];                           // A of the thread's row, half of the columns
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float v[32];
+            __syncwarp();
+            tmem_ld32(tm0 + TD + 64 * half + 32 * j, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) a[j][i] = f32x2_to_f16x2(v[2 * i + 1] * (SA / (SX * SX)), v[2 * i] * (SA / (SX * SX)));
+            put(sa, 64 * half + 32 * j, a[j]);
+        }
+        in_place();
+        if (!good) break;
+        if (issuer) {                                // A A
+            const uint32_t id = idesc_f16_f32(128, 128, false, false);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t d = smem_desc_sw128(ua + (i >> 2) * CHUNK + (i & 3) * 32, 16, 1024);
+                tc_mma_bf16(tmem + TD, d, d, id, i > 0 ? 1u : 0u);
+            }
+            tc_commit(&done);
+        }
+        finished();
+        const float cb = p.c[3 * k + 1], cc = p.c[3 * k + 2] / SA;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float v[32];
+            __syncwarp();
+            tmem_ld32(tm0 + TD + 64 * half + 32 * j, v);
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = f32x2_to_f16x2(fmaf(cb, f16_hi(a[j][i]), v[2 * i + 1] * cc), fmaf(cb, f16_lo(a[j][i]), v[2 * i] * cc));
+            put(sp, 64 * half + 32 * j, w);
+        }
+        in_place();
+        if (!good) break;
+        if (issuer) {                                // a X + P X
+            for (int n0 = 0; n0 < p.np; n0 += 256) {
+                const int n = min(256, p.np - n0);
+                const uint32_t id = idesc_f16_f32(128, static_cast<uint32_t>(n), false, true);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    tc_mma_bf16(tmem + n0, smem_desc_sw128(up + (i >> 2) * CHUNK + (i & 3) * 32, 16, 1024),
+                                smem_desc_sw128(ux + (n0 >> 6) * CHUNK + i * 2048, CHUNK, 1024), id, 1u);
+            }
+            tc_commit(&done);
+        }
+        finished();
+    }
+    // (after a wait that ran out, MMAs still on their way)
+    if (!good && issuer) {
+        int dummy = 0;
+        mbar_wait(&done, ph ^ 1u, &dummy, nullptr, 20000000ull);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TCOLS);
     }
 }
 
@@ -628,75 +973,110 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
               reinterpret_cast<float4 *>(w + L.part), reinterpret_cast<uint16_t *>(w + L.hi[0]),
               reinterpret_cast<uint16_t *>(w + L.lo)};
     const bool vec = C % 8 == 0;
+    const bool tall = R > C;             // the smaller side is the columns
+    const int m = L.m, n = tall ? R : C;
+    cudaError_t e;
+    if (m <= SM_SIDE && n <= SM_LONG) {
+        Small p{};
+        p.q = q;
+        p.tall = tall;
+        p.m = m; p.n = n; p.np = (n + 63) / 64 * 64;
+        p.steps = f.steps;
+        memcpy(p.c, f.coeffs, 3 * f.steps * sizeof(float));
+        p.scale = f.scale;
+        p.out = static_cast<uint16_t *>(f.out);
+        p.status = status;
+        p.timeout_ns = timeout_ns;
+        p.inject = inject;
+        const size_t smem = 1024 + (p.np / 64 + 4) * CHUNK;
+        void (*kernel)(const Small) = vec ? ortho_small_kernel<true> : ortho_small_kernel<false>;
+        if ((e = ensure_smem(reinterpret_cast<const void *>(kernel), smem)) != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3(B), dim3(ST), smem, s, 1, p);
+    }
     const dim3 grid(L.parts, B);
-    cudaError_t e = launch_pdl(vec ? ortho_momentum_kernel<true> : ortho_momentum_kernel<false>, grid, dim3(PT), 0, s, 1, q);
+    e = launch_pdl(vec ? ortho_momentum_kernel<true> : ortho_momentum_kernel<false>, grid, dim3(PT), 0, s, 1, q);
     if (e != cudaSuccess) return e;
     e = launch_pdl(vec ? ortho_scale_kernel<true> : ortho_scale_kernel<false>, grid, dim3(PT), 0, s, 1, q);
     if (e != cudaSuccess) return e;
 
-    const bool tall = R > C;             // the smaller side is the columns
-    const int m = L.m;
     void *A = w + L.A, *P = w + L.P;
     Args g, sq, ap[2];
     memset(&g, 0, sizeof g);
-    g.B = B;
     g.status = status;
     g.timeout_ns = timeout_ns;
     g.inject = inject;
     g.scale = f.scale;
     g.out = static_cast<uint16_t *>(f.out);
-    sq = g;
     ap[0] = g;
-    const auto tiles = [](int n) { return (n + TM - 1) / TM; };
+    const int most = num_sms() / 2;      // clusters
+    const auto tiles = [](int n, int t) { return (n + t - 1) / t; };
+    // symmetric results: as many tiles as of 256, of equal sides (a multiple of 32)
+    const int side = (tiles(m, tiles(m, 256)) + 31) / 32 * 32;
+    // X: the width (a multiple of 32) whose rounds of tiles take least; a tile's fixed part is worth
+    // about 32 columns
+    const auto width = [&](int rows, int cols) {
+        int best = 0;
+        long long least = 0;
+        for (int k = tiles(cols, 256); k <= 4 * tiles(cols, 256); ++k) {
+            const int t = (tiles(cols, k) + 31) / 32 * 32;
+            const long long all = static_cast<long long>(B) * tiles(rows, TM) * tiles(cols, t);
+            const long long cost = (all + most - 1) / most * (t + 32);
+            if (!best || cost < least) { least = cost; best = t; }
+        }
+        return best;
+    };
     // gram: [m][n] x [n][m]
     g.mode = GRAM;
     g.amn = g.bmn = tall ? 1 : 0;
     g.M = g.N = m;
     g.K = tall ? R : C;
-    g.nM = g.nN = tiles(m);
+    g.tm = g.tn = side;
+    g.nM = g.nN = (m + g.tm - 1) / g.tm;
     g.tiles = B * (g.nM * (g.nM + 1) / 2);
     bool ok = encode(&g.s, A, B, m, m, L.ldm, 32, 32);
-    g.sm = g.s;
     // square
+    sq = g;
     sq.mode = SQUARE;
-    sq.M = sq.N = sq.K = m;
-    sq.nM = sq.nN = g.nM;
-    sq.tiles = g.tiles;
-    sq.add = static_cast<const uint16_t *>(A);
-    sq.ld = L.ldm;
+    sq.amn = sq.bmn = 0;
+    sq.K = m;
+    sq.l = g.s;
     ok = ok && encode(&sq.a, A, B, m, m, L.ldm, 128, 64) && encode(&sq.s, P, B, m, m, L.ldm, 32, 32);
     sq.b = sq.a;
-    sq.sm = sq.s;
     // apply: [m][m] x [m][n], or X P for tall matrices
     ap[0].mode = APPLY;
     ap[0].M = R;
     ap[0].N = C;
     ap[0].K = m;
-    ap[0].nM = tiles(R);
-    ap[0].nN = tiles(C);
+    ap[0].tm = TM;
+    ap[0].tn = width(R, C);
+    ap[0].nM = tiles(R, TM);
+    ap[0].nN = (C + ap[0].tn - 1) / ap[0].tn;
     ap[0].tiles = B * ap[0].nM * ap[0].nN;
     ap[0].bmn = tall ? 0 : 1;
-    ap[0].ld = L.ld;
-    ap[0].add2 = reinterpret_cast<const uint16_t *>(w + L.lo);
+    ap[0].tma_out = C % 8 == 0 ? 1 : 0;
     ok = ok && encode(&ap[0].s2, w + L.lo, B, R, C, L.ld, 32, 32);
+    ap[0].l2 = ap[0].s2;
     ap[1] = ap[0];
-    CUtensorMap gx[2];
+    CUtensorMap gx[2], out;
     for (int i = 0; i < 2; ++i) {        // from X in buffer i to the other one
         void *x = w + L.hi[i];
-        ap[i].add = static_cast<const uint16_t *>(x);
-        ok = ok && encode(&ap[i].s, w + L.hi[1 - i], B, R, C, L.ld, 32, 32) &&
-             encode(&gx[i], x, B, R, C, L.ld, tall ? 64 : 128, 64);
+        ok = ok && encode(&ap[i].l, x, B, R, C, L.ld, 32, 32) && encode(&gx[i], x, B, R, C, L.ld, tall ? 64 : 128, 64);
         if (tall)
             ok = ok && encode(&ap[i].a, x, B, R, C, L.ld, 128, 64) && encode(&ap[i].b, P, B, m, m, L.ldm, 128, 64);
         else
             ok = ok && encode(&ap[i].a, P, B, m, m, L.ldm, 128, 64) && encode(&ap[i].b, x, B, R, C, L.ld, 64, 64);
     }
+    ap[0].s = ap[1].l;
+    ap[1].s = ap[0].l;
+    if (ap[0].tma_out) ok = ok && encode(&out, f.out, B, R, C, C, 32, 32);
     if (!ok) return cudaErrorInvalidValue;
     const size_t smem = 1024 + STAGES * STAGE + N_EPI * SLAB;
-    if ((e = ensure_smem(reinterpret_cast<const void *>(ortho_gemm_kernel), smem)) != cudaSuccess) return e;
-    const int most = num_sms() / 2;
+    if ((e = ensure_smem(reinterpret_cast<const void *>(ortho_gemm_kernel<true>), smem)) != cudaSuccess ||
+        (e = ensure_smem(reinterpret_cast<const void *>(ortho_gemm_kernel<false>), smem)) != cudaSuccess)
+        return e;
     auto run = [&](const Args &a) {
-        return launch_pdl(ortho_gemm_kernel, dim3(2 * (a.tiles < most ? a.tiles : most)), dim3(NT), smem, s, 2, a);
+        return launch_pdl(a.mode <= SQUARE ? ortho_gemm_kernel<true> : ortho_gemm_kernel<false>,
+                          dim3(2 * (a.tiles < most ? a.tiles : most)), dim3(NT), smem, s, 2, a);
     };
     for (int k = 0; k < f.steps; ++k) {
         const int i = k & 1;
@@ -704,7 +1084,10 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
         sq.cb = f.coeffs[3 * k + 1];
         sq.cc = f.coeffs[3 * k + 2];
         ap[i].ca = f.coeffs[3 * k];
-        ap[i].mode = k + 1 < f.steps ? APPLY : LAST;
+        if (k + 1 == f.steps) {
+            ap[i].mode = LAST;
+            if (ap[i].tma_out) ap[i].s = out;
+        }
         if ((e = run(g)) != cudaSuccess || (e = run(sq)) != cudaSuccess || (e = run(ap[i])) != cudaSuccess) return e;
     }
     return cudaSuccess;

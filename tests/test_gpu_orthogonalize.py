@@ -68,7 +68,8 @@ def _off(got, ref):
 
 SHAPES = [(1, 1, 1), (3, 1, 40), (2, 40, 1), (2, 7, 9), (3, 33, 65), (4, 64, 64), (5, 129, 100), (2, 128, 256), (16, 256, 128),
           (1, 255, 257), (2, 257, 255), (3, 300, 520), (1, 1088, 2112), (2, 2112, 1088), (1, 1000, 1001), (2, 600, 130),
-          (1, 16, 7168), (1, 7168, 24), (700, 24, 17), (40, 192, 320)]
+          (1, 16, 7168), (1, 7168, 24), (700, 24, 17), (40, 192, 320), (2, 128, 384), (3, 383, 128), (2, 128, 392), (1, 136, 384),
+          (2, 96, 264), (2, 64, 321)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -166,9 +167,10 @@ def test_other_stream_and_graph():
     assert B.moe_read_status(ws) == 0
 
 
-def test_a_wait_that_runs_out_is_recorded():
-    g = _matrices(2, 128, 256).to(BF)
-    ws = torch.zeros(B.moe_orthogonalize_workspace_bytes(2, 128, 256), dtype=torch.uint8, device=DEV)
+@pytest.mark.parametrize("shape", [(2, 128, 256), (2, 300, 200)])
+def test_a_wait_that_runs_out_is_recorded(shape):
+    g = _matrices(*shape).to(BF)
+    ws = torch.zeros(B.moe_orthogonalize_workspace_bytes(*shape), dtype=torch.uint8, device=DEV)
     out = torch.empty_like(g)
     B.moe_debug_set_wait_limit(2_000_000, 1)
     try:
