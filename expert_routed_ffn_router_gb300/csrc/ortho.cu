@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
 // times a SA: the product with P is added to it there.  (The launches for large ones take 100 us for
 // 16 matrices of 256 x 128, this one @SMALL@.)
 constexpr int SM_SIDE = 128, SM_LONG = 384;
-constexpr int ST = 256;               // threads: two warps for each 32 rows, each half of the columns
+constexpr int ST = 512;               // threads: four warps for each 32 rows, which share the columns
 constexpr int CHUNK = 128 * 128;      // 128 rows x 64 fp16
 
 struct Small {
@@ -649,50 +649,26 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// u of 32 columns of a row of X from c0 on (0 outside), after the momentum's update
+// u at element i (8 of them from i on with VEC), after the momentum's update
 template <bool VEC>
-__device__ __forceinline__ void small_load(const Small &p, size_t base, int row, int c0, float (&v)[32])
+__device__ __forceinline__ void small_load(const Prepare &q, size_t i, float (&u)[Elements<VEC>::N])
 {
-    const Prepare &q = p.q;
-    if (VEC && !p.tall) {
+    constexpr int N = Elements<VEC>::N;
+    load_g<VEC>(q, i, u);
+    if (!q.m) return;
+    float m[N];
+    load_m<VEC>(q.m, i, m);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (row < p.m && c0 + 8 * i < p.n) {
-                const size_t at = base + static_cast<size_t>(row) * p.n + c0 + 8 * i;
-                load_g<true>(q, at, u);
-                if (q.m) {
-                    float m[8];
-                    load_m<true>(q.m, at, m);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        m[k] = fmaf(q.mu, m[k], u[k]);
-                        u[k] = q.nesterov ? fmaf(q.mu, m[k], u[k]) : m[k];
-                    }
-                    float4 *o = reinterpret_cast<float4 *>(q.m + at);
-                    o[0] = make_float4(m[0], m[1], m[2], m[3]);
-                    o[1] = make_float4(m[4], m[5], m[6], m[7]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[8 * i + k] = u[k];
-        }
-        return;
+    for (int k = 0; k < N; ++k) {
+        m[k] = fmaf(q.mu, m[k], u[k]);
+        u[k] = q.nesterov ? fmaf(q.mu, m[k], u[k]) : m[k];
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const int c = c0 + i;
-        float u[1] = {0.f};
-        if (row < p.m && c < p.n) {
-            const size_t at = base + (p.tall ? static_cast<size_t>(c) * p.m + row : static_cast<size_t>(row) * p.n + c);
-            load_g<false>(q, at, u);
-            if (q.m) {
-                const float m = fmaf(q.mu, q.m[at], u[0]);
-                q.m[at] = m;
-                u[0] = q.nesterov ? fmaf(q.mu, m, u[0]) : m;
-            }
-        }
-        v[i] = u[0];
+    if constexpr (VEC) {
+        float4 *o = reinterpret_cast<float4 *>(q.m + i);
+        o[0] = make_float4(m[0], m[1], m[2], m[3]);
+        o[1] = make_float4(m[4], m[5], m[6], m[7]);
+    } else {
+        q.m[i] = m[0];
     }
 }
 
@@ -724,9 +700,9 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
+    // this thread's row, and its columns: 32 from `col` on of every 128
+    const int q = warp & 3, col = 32 * (warp >> 2), row = 32 * q + lane;
     const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    const int nh = p.np / 2, x0 = half * nh;         // this thread's columns of X: x0 .. x0 + nh
     const size_t base = static_cast<size_t>(blockIdx.x) * p.m * p.n;
     // 32 numbers of the thread's row, from column c of an operand of 64-column chunks
     auto put = [&](unsigned char *s, int c, const uint32_t (&w)[16]) {
@@ -736,11 +712,42 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
                 make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     };
 
-    // u to tensor memory, and its square sums (see ortho_momentum_kernel)
+    // u to tensor memory, and its square sums (see ortho_momentum_kernel).  A tall matrix passes through
+    // shared memory, 128 of its rows (columns of X) at a time: [column][128 + 4 rows] of fp32.
     float s0 = 0.f, s1 = 0.f, s2 = 0.f;
-    for (int c = x0; c < x0 + nh; c += 32) {
+    float *turn = reinterpret_cast<float *>(sx);
+    constexpr int PITCH = 132, N = Elements<VEC>::N;
+    for (int c0 = 0; c0 < p.np; c0 += 128) {
+        if (p.tall) {
+            __syncthreads();
+            const int per = p.m / N;
+            for (int i = tid; i < 128 * per; i += ST) {
+                const int r = i / per, k = (i - r * per) * N;
+                if (c0 + r >= p.n) break;
+                float u[N];
+                small_load<VEC>(p.q, base + static_cast<size_t>(c0 + r) * p.m + k, u);
+#pragma unroll
+                for (int j = 0; j < N; ++j) turn[r * PITCH + k + j] = u[j];
+            }
+            __syncthreads();
+        }
+        const int c = c0 + col;
+        if (c >= p.np) continue;
         float v[32];
-        small_load<VEC>(p, base, row, c, v);
+        if (p.tall) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = row < p.m && c + i < p.n ? turn[(col + i) * PITCH + row] : 0.f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32 / N; ++i) {
+                float u[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k) u[k] = 0.f;
+                if (row < p.m && c + N * i < p.n) small_load<VEC>(p.q, base + static_cast<size_t>(row) * p.n + c + N * i, u);
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[N * i + k] = u[k];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             s0 = fmaf(v[i], v[i], s0);
@@ -783,7 +790,7 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
         // X of this step: the operand, and a SA X in tensor memory; after the last one, the result
         const bool last = k == p.steps;
         const float take = k == 0 ? f : 1.f / SA, mul = k == 0 ? inv : 1.f, keep = last ? 0.f : p.c[3 * k] * SA;
-        for (int c = x0; c < x0 + nh; c += 32) {
+        for (int c = col; c < p.np; c += 128) {
             float v[32];
             __syncwarp();
             tmem_ld32(tm0 + c, v);
@@ -799,21 +806,37 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
                 tmem_st32(tm0 + c, v);
                 continue;
             }
-            if (row >= p.m) continue;
             const float o = p.scale / SX;
-            if (VEC && !p.tall) {
+            if (p.tall) {            // [column][128 + 8 rows] of bf16 in shared memory
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    reinterpret_cast<uint16_t *>(sx)[(c + i) * 136 + row] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * o));
+                continue;
+            }
+            if (row >= p.m) continue;
+            uint16_t *to = p.out + base + static_cast<size_t>(row) * p.n + c;
+            if constexpr (VEC) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (c + 8 * i < p.n)
-                        *reinterpret_cast<uint4 *>(p.out + base + static_cast<size_t>(row) * p.n + c + 8 * i) =
+                        reinterpret_cast<uint4 *>(to)[i] =
                             make_uint4(f32x2_to_bf16x2(v[8 * i + 1] * o, v[8 * i] * o), f32x2_to_bf16x2(v[8 * i + 3] * o, v[8 * i + 2] * o),
                                        f32x2_to_bf16x2(v[8 * i + 5] * o, v[8 * i + 4] * o), f32x2_to_bf16x2(v[8 * i + 7] * o, v[8 * i + 6] * o));
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    if (c + i < p.n)
-                        p.out[base + (p.tall ? static_cast<size_t>(c + i) * p.m + row : static_cast<size_t>(row) * p.n + c + i)] =
-                            static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * o));
+                    if (c + i < p.n) to[i] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * o));
+            }
+        }
+        if (last && p.tall) {
+            __syncthreads();
+            const int per = p.m / N;
+            const uint16_t *from = reinterpret_cast<const uint16_t *>(sx);
+            for (int i = tid; i < p.n * per; i += ST) {
+                const int r = i / per, k = (i - r * per) * N;
+                uint16_t *to = p.out + base + static_cast<size_t>(r) * p.m + k;
+                if constexpr (VEC) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + r * 136 + k);
+                else *to = from[r * 136 + k];
             }
         }
         if (last) break;
@@ -828,16 +851,12 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
             tc_commit(&done);
         }
         finished();
-        uint32_t a[2][16];                           // A of the thread's row, half of the columns
+        uint32_t a[16];                              // A, of the thread's row and columns
+        float v[32];
+        tmem_ld32(tm0 + TD + col, v);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float v[32];
-            __syncwarp();
-            tmem_ld32(tm0 + TD + 64 * half + 32 * j, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) a[j][i] = f32x2_to_f16x2(v[2 * i + 1] * (SA / (SX * SX)), v[2 * i] * (SA / (SX * SX)));
-            put(sa, 64 * half + 32 * j, a[j]);
-        }
+        for (int i = 0; i < 16; ++i) a[i] = f32x2_to_f16x2(v[2 * i + 1] * (SA / (SX * SX)), v[2 * i] * (SA / (SX * SX)));
+        put(sa, col, a);
         in_place();
         if (!good) break;
         if (issuer) {                                // A A
@@ -851,17 +870,12 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
         }
         finished();
         const float cb = p.c[3 * k + 1], cc = p.c[3 * k + 2] / SA;
+        tmem_ld32(tm0 + TD + col, v);
+        uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float v[32];
-            __syncwarp();
-            tmem_ld32(tm0 + TD + 64 * half + 32 * j, v);
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                w[i] = f32x2_to_f16x2(fmaf(cb, f16_hi(a[j][i]), v[2 * i + 1] * cc), fmaf(cb, f16_lo(a[j][i]), v[2 * i] * cc));
-            put(sp, 64 * half + 32 * j, w);
-        }
+        for (int i = 0; i < 16; ++i)
+            w[i] = f32x2_to_f16x2(fmaf(cb, f16_hi(a[i]), v[2 * i + 1] * cc), fmaf(cb, f16_lo(a[i]), v[2 * i] * cc));
+        put(sp, col, w);
         in_place();
         if (!good) break;
         if (issuer) {                                // a X + P X
