@@ -110,7 +110,7 @@ struct ResidualGrads {             // each nullable
 };
 cudaError_t launch_join(const ResidualOpts &o, const void *x, int x_fp32, const void *y, int y_fp32, int T, int H,
                         void *r, void *n, float *stats, cudaStream_t s);
-// CTAs of the backward launch; each leaves 4 H partial sums in `part`.
+// CTAs of the backward launch at most; each leaves 4 H partial sums in `part`.
 int join_bwd_ctas(int T, int H);
 cudaError_t launch_join_bwd(const ResidualOpts &o, const void *dn, const void *dr, const void *y, int y_fp32,
                             const void *r, int x_fp32, const float *stats, int T, int H, void *dx, void *dy,

@@ -28,7 +28,8 @@ namespace residual {
 constexpr int VPT = 4;               // vectors of 4 columns a thread
 constexpr int WARP_COLS = 32 * 4 * VPT;   // longest row of one warp
 constexpr int WARPS = 8;             // rows of a CTA then
-constexpr size_t ROOM = 220 * 1024;  // shared memory of an SM for the staged rows
+constexpr size_t ROOM = 220 * 1024;  // shared memory of an SM for the staged rows of several CTAs
+constexpr size_t MOST = 225 * 1024;  // of one CTA, beside its static arrays
 
 struct Args {
     ResidualOpts o;
@@ -41,8 +42,10 @@ struct Args {
     void *dx;
     uint16_t *dy;
     float *d_token, *part;           // part [CTAs][4][H]: dgamma_pre, dbeta_pre, S1, S0
-    int stages, stage_bytes;         // of a CTA (of a warp: short rows)
+    int stages, stage_bytes;         // of a row's threads
+    int row_bytes, dr_once;          // backward: shared memory of a row's threads; dr is staged once
     int off[4];                      // the staged arrays in a stage, -1: read directly
+    int sum[2];                      // backward: two of the sums in shared memory
 };
 
 // The type of an array: known to the kernel, or (RUNTIME) told by a flag.
@@ -103,12 +106,15 @@ __device__ __forceinline__ float4 col4(const float *p, int tid, int k, float abs
 }
 
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// The copies of all groups but the last `left` (at most 2) have arrived.
+// The copies of all groups but the last `left` (at most 5) have arrived.
 __device__ __forceinline__ void copies_wait(int left)
 {
     if (left == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
     else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (left == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (left == 4) asm volatile("cp.async.wait_group 4;" ::: "memory");
+    else asm volatile("cp.async.wait_group 5;" ::: "memory");
 }
 
 template <int BYTES, int OFF>
@@ -120,11 +126,10 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
         asm volatile("cp.async.ca.shared.global [%0 + %2], [%1 + %2], 8;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
 }
 
-// The columns' vectors that a thread has: the first `sure` ones always (a row is longer than half of
-// what the threads have room for, or N is that of short rows)
+// The columns' vectors that a thread has: the first SURE ones always (row_threads)
 template <int N>
 struct Columns {
-    static constexpr int SURE = N == 32 ? 0 : (N == 128 ? 1 : 2);
+    static constexpr int SURE = N == 32 ? 0 : (N == 448 ? 3 : 2);
     int vec, tid;                    // vectors of a row, thread in the row
     __device__ __forceinline__ bool operator()(int k) const { return k < SURE || tid + k * N < vec; }
 };
@@ -154,36 +159,43 @@ __device__ __forceinline__ const unsigned char *staged(const unsigned char *st, 
     return st + tid * (wide<TY>(fp32) ? 16 : 8);
 }
 
-template <int M>
-__device__ __forceinline__ void warp_sums(float (&v)[M])
+// Sums of a and of b over the warp: that of a ends up in lanes 0 .. 15, that of b in lanes 16 .. 31 (half
+// the shuffles of two sums).
+__device__ __forceinline__ float warp_pair(float a, float b)
 {
+    const bool up = threadIdx.x & 16;
+    float t = (up ? b : a) + __shfl_xor_sync(kFullMask, up ? a : b, 16);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(kFullMask, v[i], o);
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(kFullMask, t, o);
+    return t;
+}
+// Both sums on every lane
+__device__ __forceinline__ float2 warp_pair_all(float a, float b)
+{
+    const float t = warp_pair(a, b), u = __shfl_xor_sync(kFullMask, t, 16);
+    return threadIdx.x & 16 ? make_float2(u, t) : make_float2(t, u);
 }
 
-// The warps of a row exchange their sums through `red`, two buffers in turn: one barrier.
+// The warps of a row exchange four numbers each, through two buffers in turn: one barrier.
 template <int N>
 struct Exchange {
-    static constexpr int NW = N / 32;
-    float (*red)[5][NW];
+    float4 (*red)[N / 32];
+    int tid;
     int turn = 0;
 
-    // v of a warp (on every lane) -> on lane w that of warp w, 0 beyond the last warp
-    template <int M>
-    __device__ __forceinline__ void operator()(float (&v)[M])
+    // x, y: of lane 0 and of lane 16; z, w: likewise -> on lane k those of warp k, 0 beyond the last warp
+    __device__ __forceinline__ float4 operator()(float xy, float zw)
     {
-        if (NW == 1) return;
-        float (*r)[NW] = red[turn];
-        turn ^= 1;
-        const int lane = threadIdx.x & 31;
-        if (lane == 0)
-#pragma unroll
-            for (int i = 0; i < M; ++i) r[i][threadIdx.x >> 5] = v[i];
+        float *r = reinterpret_cast<float *>(&red[turn][tid >> 5]);
+        const int lane = tid & 31;
+        if ((lane & 15) == 0) {
+            r[lane >> 4] = xy;
+            r[2 + (lane >> 4)] = zw;
+        }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = lane < NW ? r[i][lane] : 0.f;
+        const float4 got = lane < N / 32 ? red[turn][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        turn ^= 1;
+        return got;
     }
 };
 
@@ -198,7 +210,7 @@ __device__ __forceinline__ float warp_columns(int H, int w)
 }
 
 // Threads of a row
-inline int row_threads(int H) { return H <= WARP_COLS ? 32 : H <= 2048 ? 128 : H <= 4096 ? 256 : H <= 8192 ? 512 : 1024; }
+inline int row_threads(int H) { return H <= WARP_COLS ? 32 : H <= 1024 ? 64 : H <= 2048 ? 128 : H <= 4096 ? 256 : H <= 8192 ? 512 : 1024; }
 
 }  // namespace residual
 }  // namespace moe

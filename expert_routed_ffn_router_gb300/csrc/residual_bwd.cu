@@ -8,30 +8,41 @@
 // of its columns in registers; the CTAs' sums go to the workspace ([CTA][4][H]) and a second
 // launch adds them in CTA order.  No atomics: the result depends on the sizes alone.
 //
-// What bounds it: @BWD@
+// What bounds it: memory in fp32 (16384 x 7168, RMS norm of y, layer norm of r: 350 us, 6.7 TB/s, 99% of
+// the copy bandwidth), instructions in bf16 (302 us, 4.7 TB/s).  Two stages at most: with three of bf16
+// rows that call takes 386 us.
 #include "residual.cuh"
 
 namespace moe {
 namespace residual {
 namespace {
 
-// Staged arrays: 0 dn, 1 r, 2 dr (of a row's first part), 3 y (of its second one).  N: threads of a row
-// (32: a warp, with WARPS rows a CTA).  S0: with beta_post, whose gradient and the gate's need those
-// sums.  PREG: the columns' parameters stay in registers (read once a CTA instead of once a row).
-template <int N, bool S0, bool PREG, int XT, int YT>
+// Staged arrays: 0 dn, 1 r, 2 dr (of a row's first part), 3 y (of its second one).  Where dr does not fit
+// `stages` times with the others it is staged once (dr_once): a row's is read at the end of a turn, and
+// the next one has a turn to arrive.  N: threads of a row (32: a warp, with WARPS rows a CTA).
+// The columns' parameters stay in registers, and with them the sums p1 and s1; those of plain rows, p0 and
+// (BOTH: with beta_post) s0, in shared memory, every thread its own columns.  Where that is full
+// (IN_MEMORY) all sums are in registers and the parameters in memory.  (Everything in registers spills, and
+// with most of an SM's L1 taken as shared memory spills go to L2: 16384 x 7168 in fp32, RMS norm and layer
+// norm, two spilled registers: 592 us, 350 us so; with beta_post and gates of both kinds 693 us with
+// IN_MEMORY, 1000 us with spills, 490 us with BOTH.)
+enum { ONE_SHARED, BOTH, IN_MEMORY };
+
+template <int N, int SUMS, int XT, int YT>
 __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N == 32 ? 256 : N) : 1)
     join_bwd_kernel(const __grid_constant__ Args p)
 {
-    constexpr bool ONE = N == 32;
+    constexpr bool ONE = N == 32, S0 = SUMS != ONE_SHARED, PREG = SUMS != IN_MEMORY;
     extern __shared__ __align__(16) unsigned char stages[];
-    __shared__ float red[2][5][N / 32];
+    __shared__ float4 red[2][N / 32];
+    __shared__ float red_token[2][N / 32];
     const int H = p.H, S = p.stages;
     const bool xf = p.x_fp32, yf = p.y_fp32;
     const ResidualOpts &o = p.o;
     const Columns<N> in{H / 4, static_cast<int>(threadIdx.x)};
     const int tid = in.tid;
-    Exchange<N> exchange{red};
-    unsigned char *ring = stages + (ONE ? threadIdx.y * S * p.stage_bytes : 0);
+    Exchange<N> exchange{red, tid};
+    unsigned char *ring = stages + (ONE ? threadIdx.y * p.row_bytes : 0);
     const uint32_t ring_at = smem_u32(ring);
     const int first = ONE ? blockIdx.x * WARPS + threadIdx.y : blockIdx.x, step = ONE ? gridDim.x * WARPS : gridDim.x;
     pdl_wait();
@@ -40,17 +51,26 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
         const uint32_t st = ring_at + s * p.stage_bytes;
         if (p.off[0] >= 0) stage_in<BF16, N>(st + p.off[0], p.dn, row, H, false, in);
         if (p.off[1] >= 0) stage_in<XT, N>(st + p.off[1], p.r, row, H, xf, in);
-        if (p.off[2] >= 0) stage_in<XT, N>(st + p.off[2], p.dr, row, H, xf, in);
+        if (p.off[2] >= 0 && !p.dr_once) stage_in<XT, N>(st + p.off[2], p.dr, row, H, xf, in);
+    };
+    auto fetch_dr = [&](int row) {
+        if (row < p.T && p.dr_once) stage_in<XT, N>(ring_at + p.off[2], p.dr, row, H, xf, in);
+        copies_commit();
     };
     auto fetch_second = [&](int row, int s) {
         if (row < p.T && p.off[3] >= 0) stage_in<YT, N>(ring_at + s * p.stage_bytes + p.off[3], p.y, row, H, yf, in);
     };
-    constexpr int PV = PREG ? VPT : 1, SV = S0 ? VPT : 1;
-    float4 p1[VPT], p0[VPT], s1[VPT], s0[SV], ga[PV], gb[PV];
+    constexpr int PV = PREG ? VPT : 1, SV = SUMS == IN_MEMORY ? VPT : 1;
+    float4 p1[VPT], p0[SV], s1[VPT], s0[SV], ga[PV], gb[PV];
+    float4 *p0s = reinterpret_cast<float4 *>(ring + p.sum[0]) + tid, *s0s = reinterpret_cast<float4 *>(ring + p.sum[1]) + tid;
     auto scale = [&](int k) { return mul4(col4<N>(o.gate, tid, k, 1.f), col4<N>(o.gamma_post, tid, k, 1.f)); };
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        p1[k] = p0[k] = s1[k] = s0[k % SV] = all4(0.f);
+        p1[k] = p0[k % SV] = s1[k] = s0[k % SV] = all4(0.f);
+        if (PREG && in(k)) {
+            p0s[k * N] = all4(0.f);
+            if (S0) s0s[k * N] = all4(0.f);
+        }
         if (PREG && in(k)) {
             ga[k % PV] = col4<N>(o.gamma_pre, tid, k, 1.f);
             gb[k % PV] = scale(k);
@@ -62,9 +82,11 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
     const bool token = p.d_token != nullptr, sums = o.pre || o.post || token, y = p.y != nullptr;
     const float ly = o.post == 1 ? inv : 0.f, py = o.post ? inv : 0.f, lr = o.pre == 1 ? inv : 0.f;
 
-    // With each group of copies, the first part of one row and the second part of the row S - 1 before it
-    // go to the places that a turn has just read.
+    // A turn's copies, to the places that it has just read: dr of the row after the next one; the first part
+    // of the row S further on with the second part of the one before that.
     for (int s = 0; s < S; ++s) {
+        if (s == S - 1) fetch_dr(first);
+        else copies_commit();
         fetch_first(first + s * step, s);
         if (s > 0) fetch_second(first + (s - 1) * step, s - 1);
         copies_commit();
@@ -86,7 +108,7 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
         const unsigned char *sm = ring + s * p.stage_bytes;
         const unsigned char *gs = staged<BF16>(sm + p.off[0], tid, false), *rs = staged<XT>(sm + p.off[1], tid, xf);
         const unsigned char *ys = staged<YT>(ring + sp * p.stage_bytes + p.off[3], tid, yf);
-        copies_wait(S - 1);
+        copies_wait(2 * (S - 1));
         float e[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
         if (more && o.pre) {
 #pragma unroll
@@ -94,7 +116,8 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
                 if (!in(k)) continue;
                 const float4 g = ld4<BF16, N>(gs, k, false), h = norm4(ld4<XT, N>(rs, k, xf), st_next.z, st_next.w);
                 p1[k] = fma4(g, h, p1[k]);
-                p0[k] = add4(p0[k], g);
+                if (PREG) p0s[k * N] = add4(p0s[k * N], g);
+                else p0[k % SV] = add4(p0[k % SV], g);
                 const float4 a = mul4(g, gamma(k));
                 e[0] += sum4(a);
                 e[1] += dot4(a, h);
@@ -111,7 +134,8 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
                     if (!in(k)) continue;
                     const float4 h = norm4(ld4<YT, N>(ys, k, yf), st.x, st.y), g = scale4(d[k], gt);
                     s1[k] = fma4(g, h, s1[k]);
-                    if (S0) s0[k % SV] = add4(s0[k % SV], g);
+                    if (SUMS == BOTH) s0s[k * N] = add4(s0s[k * N], g);
+                    else if (S0) s0[k % SV] = add4(s0[k % SV], g);
                     const float4 f = mul4(d[k], branch(k));
                     e[2] += sum4(f);
                     e[3] += dot4(f, h);
@@ -124,10 +148,20 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
             }
         }
         if (sums) {
-            warp_sums(e);
-            if (!ONE) {
-                exchange(e);
-                warp_sums(e);
+            if (ONE) {
+                const float2 a = warp_pair_all(e[0], e[1]), f = warp_pair_all(e[2], e[3]);
+                e[0] = a.x; e[1] = a.y; e[2] = f.x; e[3] = f.y;
+                if (S0 && token) e[4] = warp_pair_all(e[4], 0.f).x;
+            } else {
+                if (S0 && token) {
+                    e[4] = warp_pair(e[4], 0.f);
+                    if ((tid & 31) == 0) red_token[exchange.turn][tid >> 5] = e[4];
+                }
+                const int turn = exchange.turn;
+                const float4 w = exchange(warp_pair(e[0], e[1]), warp_pair(e[2], e[3]));
+                const float2 a = warp_pair_all(w.x, w.y), f = warp_pair_all(w.z, w.w);
+                e[0] = a.x; e[1] = a.y; e[2] = f.x; e[3] = f.y;
+                if (S0 && token) e[4] = warp_pair_all((tid & 31) < N / 32 ? red_token[turn][tid & 31] : 0.f, 0.f).x;
             }
         }
         if (has) {
@@ -147,7 +181,9 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
         }
         if (more) {
             // (a row of dr that is not staged comes from memory)
-            const unsigned char *ds = p.off[2] >= 0 ? staged<XT>(sm + p.off[2], tid, xf) : row_at<XT>(p.dr, next, H, tid, xf);
+            const unsigned char *ds = p.off[2] < 0 ? row_at<XT>(p.dr, next, H, tid, xf)
+                                                   : staged<XT>((p.dr_once ? ring : sm) + p.off[2], tid, xf);
+            if (p.dr_once) copies_wait(1);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) d[k] = p.dr && in(k) ? ld4<XT, N>(ds, k, xf) : all4(0.f);
             if (o.pre) {
@@ -167,6 +203,7 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
         gt = gt_next;
         st_next = row_stats(next + step);
         gt_next = row_gate(next + step);
+        fetch_dr(next + step);
         fetch_first(next + S * step, s);
         fetch_second(next + (S - 1) * step, sp);
         copies_commit();
@@ -181,9 +218,9 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
         for (int k = 0; k < VPT; ++k) {
             if (!in(k)) continue;
             part[k * N] = p1[k];
-            part[vec + k * N] = p0[k];
+            part[vec + k * N] = PREG ? p0s[k * N] : p0[k % SV];
             part[2 * vec + k * N] = s1[k];
-            part[3 * vec + k * N] = s0[k % SV];
+            part[3 * vec + k * N] = SUMS == BOTH ? s0s[k * N] : s0[k % SV];
         }
     } else {
         // the warps' sums, added in their order
@@ -193,7 +230,7 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N, N <= 512 ? 512 / (N 
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 __syncthreads();
-                comb[threadIdx.y][tid] = j == 0 ? p1[k] : j == 1 ? p0[k] : j == 2 ? s1[k] : s0[k % SV];
+                comb[threadIdx.y][tid] = j == 0 ? p1[k] : j == 1 ? p0[k % SV] : j == 2 ? s1[k] : s0[k % SV];
                 __syncthreads();
                 if (threadIdx.y == 0 && in(k)) {
                     float4 t = comb[0][tid];
@@ -233,27 +270,27 @@ __global__ void __launch_bounds__(256) join_wgrad_kernel(const float *__restrict
 
 using Kernel = void (*)(const Args);
 
-template <int N, bool S0, bool PREG>
+template <int N, int SUMS>
 Kernel of_types(int x_fp32, int y_fp32)
 {
-    return x_fp32 ? (y_fp32 ? join_bwd_kernel<N, S0, PREG, FP32, FP32> : join_bwd_kernel<N, S0, PREG, FP32, BF16>)
-                  : (y_fp32 ? join_bwd_kernel<N, S0, PREG, BF16, FP32> : join_bwd_kernel<N, S0, PREG, BF16, BF16>);
+    return x_fp32 ? (y_fp32 ? join_bwd_kernel<N, SUMS, FP32, FP32> : join_bwd_kernel<N, SUMS, FP32, BF16>)
+                  : (y_fp32 ? join_bwd_kernel<N, SUMS, BF16, FP32> : join_bwd_kernel<N, SUMS, BF16, BF16>);
 }
 
 template <int N>
-Kernel of_rows(bool s0, int x_fp32, int y_fp32)
+Kernel of_rows(int sums, int x_fp32, int y_fp32)
 {
-    // (with the sums for beta_post there is no room for the parameters in registers)
-    return s0 ? of_types<N, true, false>(x_fp32, y_fp32) : of_types<N, false, true>(x_fp32, y_fp32);
+    return sums == ONE_SHARED ? of_types<N, ONE_SHARED>(x_fp32, y_fp32)
+           : sums == BOTH     ? of_types<N, BOTH>(x_fp32, y_fp32) : of_types<N, IN_MEMORY>(x_fp32, y_fp32);
 }
 
-// CTAs that share an SM
+// CTAs that share an SM, at most
 int per_sm(int H) { const int n = row_threads(H); return n == 32 ? 2 : (n < 512 ? 512 / n : 1); }
 
 }  // namespace
 }  // namespace residual
 
-// CTAs of the backward launch (each leaves 16 H bytes of partial sums).
+// CTAs of the backward launch at most (each leaves 16 H bytes of partial sums).
 int join_bwd_ctas(int T, int H)
 {
     using namespace residual;
@@ -288,25 +325,47 @@ cudaError_t launch_join_bwd(const ResidualOpts &o, const void *dn, const void *d
     };
     const int threads = row_threads(H);
     const bool one = threads == 32;
-    const size_t room = ROOM / (per_sm(H) * (one ? WARPS : 1));
     p.off[0] = take(o.pre != 0, H * 2);
     p.off[1] = take(o.pre != 0, xb);
     p.off[3] = take(p.y != nullptr, yb);
-    // dr is staged with the others where two stages fit so
-    p.off[2] = take(dr && 2 * static_cast<size_t>(at + xb) <= room, xb);
+    // As many CTAs an SM as have room for two stages, dr and the sums of plain rows.  Then dr in every stage
+    // where two fit so, else once, else not at all.
+    const size_t own = (o.beta_post ? 8 : 4) * static_cast<size_t>(H);
+    auto room_of = [&](int k) { return (k == 1 ? MOST : ROOM) / (k * (one ? WARPS : 1)); };
+    int ctas_sm = per_sm(H), sums = IN_MEMORY;
+    for (int k = ctas_sm; !one && threads <= 512 && k >= 1 && sums == IN_MEMORY; --k)
+        if (2 * static_cast<size_t>(at) + (dr ? xb : 0) + own <= room_of(k)) {
+            sums = o.beta_post ? BOTH : ONE_SHARED;
+            ctas_sm = k;
+        }
+    const size_t room = room_of(ctas_sm), rows = room - (sums != IN_MEMORY ? own : 0);
+    p.off[2] = -1;
+    if (dr && 2 * static_cast<size_t>(at + xb) <= rows) {
+        p.off[2] = take(true, xb);
+    } else if (dr && static_cast<size_t>(at + xb) <= rows) {
+        p.dr_once = 1;
+    }
     p.stage_bytes = at > 0 ? at : 16;
-    const size_t fit = room / p.stage_bytes;
-    p.stages = fit < 1 ? 1 : (fit > 3 ? 3 : static_cast<int>(fit));
-    const size_t smem = static_cast<size_t>(p.stages) * p.stage_bytes * (one ? WARPS : 1);
-    const bool s0 = o.beta_post != nullptr;
-    const Kernel kernel = threads == 32    ? of_types<32, true, false>(x_fp32, y_fp32)
-                          : threads == 128 ? of_rows<128>(s0, x_fp32, y_fp32)
-                          : threads == 256 ? of_rows<256>(s0, x_fp32, y_fp32)
-                          : threads == 512 ? of_rows<512>(s0, x_fp32, y_fp32)
-                                           : join_bwd_kernel<1024, true, false, RUNTIME, RUNTIME>;
+    const size_t fit = (rows - (p.dr_once ? xb : 0)) / p.stage_bytes;
+    p.stages = fit > 2 ? 2 : static_cast<int>(fit);
+    int end = p.stages * p.stage_bytes;
+    if (p.dr_once) { p.off[2] = end; end += xb; }
+    if (sums != IN_MEMORY) {
+        p.sum[0] = end;
+        p.sum[1] = end + 4 * H;
+        end += static_cast<int>(own);
+    }
+    p.row_bytes = end;
+    const size_t smem = static_cast<size_t>(end) * (one ? WARPS : 1);
+    const Kernel kernel = threads == 32    ? of_types<32, IN_MEMORY>(x_fp32, y_fp32)
+                          : threads == 64  ? of_rows<64>(sums, x_fp32, y_fp32)
+                          : threads == 128 ? of_rows<128>(sums, x_fp32, y_fp32)
+                          : threads == 256 ? of_rows<256>(sums, x_fp32, y_fp32)
+                          : threads == 512 ? of_rows<512>(sums, x_fp32, y_fp32)
+                                           : join_bwd_kernel<1024, IN_MEMORY, RUNTIME, RUNTIME>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
-    const int ctas = join_bwd_ctas(T, H);
+    const int units = one ? (T + WARPS - 1) / WARPS : T, ctas = units < ctas_sm * num_sms() ? units : ctas_sm * num_sms();
     e = launch_pdl(kernel, dim3(ctas), one ? dim3(32, WARPS) : dim3(threads), smem, s, 1, p);
     if (e != cudaSuccess) return e;
     if (!g.gamma_post && !g.beta_post && !g.gate && !g.gamma_pre && !g.beta_pre) return cudaSuccess;

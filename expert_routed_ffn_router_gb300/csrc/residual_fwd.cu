@@ -6,7 +6,10 @@
 // (sum of n_w (m_w - mean)^2): the variance is that of centred values, as in norm.cu.  A turn of the loop
 // takes the statistics of y of one row and of r of the row before it through the same exchange: a
 // row costs one barrier, and the two chains of shuffles around it run side by side (16384 x 7168 in
-// fp32 with two norms: 326 us with an exchange for each, @FWD@ so).
+// fp32 with two norms: 326 us with an exchange for each, 277 us so).
+//
+// What bounds it: memory in fp32 (16384 x 7168, RMS norm of y, layer norm of r: 240 us, 6.8 TB/s, the copy
+// bandwidth), instructions in bf16 (180-190 us, 5.2 TB/s).
 //
 // The next norm's statistics are those of r as it is stored: with a bf16 stream, what the backward
 // pass reads.
@@ -16,53 +19,59 @@ namespace moe {
 namespace residual {
 namespace {
 
-// N: threads of a row (32: a warp, with WARPS rows a CTA).  PREG: the columns' parameters stay in
-// registers (read once a CTA instead of once a row).
-template <int N, bool PREG, int XT, int YT>
+// N: threads of a row (32: a warp, with WARPS rows a CTA); the columns' parameters stay in registers, from
+// 64 to 512 (read once a CTA instead of once a row).  CY, CR: the norm of y, of r is centred (a layer
+// norm).
+template <int N, int XT, int YT, int CY, int CR>
 __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N) join_kernel(const __grid_constant__ Args p)
 {
-    constexpr bool ONE = N == 32;
-    extern __shared__ __align__(16) unsigned char stages[];
-    __shared__ float red[2][5][N / 32];
+    constexpr bool ONE = N == 32, PREG = N >= 64 && N <= 512;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float4 red[2][N / 32];
     const int H = p.H, S = p.stages, lane = threadIdx.x & 31;
     const bool xf = p.x_fp32, yf = p.y_fp32;
     const ResidualOpts &o = p.o;
-    const Columns<N> in{H / 4, static_cast<int>(threadIdx.x)};
-    const int tid = in.tid;
-    Exchange<N> exchange{red};
+    const int tid = threadIdx.x;
+    const Columns<N> in{H / 4, tid};
+    Exchange<N> exchange{red, tid};
     const float n_w = warp_columns<N>(H, tid >> 5), n_l = warp_columns<N>(H, lane);   // of this warp, of warp `lane`
-    unsigned char *ring = stages + (ONE ? threadIdx.y * S * p.stage_bytes : 0);
+    unsigned char *ring = smem + (ONE ? threadIdx.y * S * p.stage_bytes : 0);
     const uint32_t ring_at = smem_u32(ring);
     const int first = ONE ? blockIdx.x * WARPS + threadIdx.y : blockIdx.x, step = ONE ? gridDim.x * WARPS : gridDim.x;
     pdl_wait();
-    auto fetch = [&](int row, int s) {
-        if (row < p.T) {
-            const uint32_t st = ring_at + s * p.stage_bytes;
-            stage_in<XT, N>(st + p.off[0], p.x, row, H, xf, in);
-            stage_in<YT, N>(st + p.off[1], p.y, row, H, yf, in);
-        }
+    // (a thread's copies of x and y are groups of their own, in turn: 2 S - 1 are behind the one it needs)
+    auto fetch_x = [&](int row, int s) {
+        if (row < p.T) stage_in<XT, N>(ring_at + s * p.stage_bytes + p.off[0], p.x, row, H, xf, in);
         copies_commit();
     };
-    for (int s = 0; s < S; ++s) fetch(first + s * step, s);
+    auto fetch_y = [&](int row, int s) {
+        if (row < p.T) stage_in<YT, N>(ring_at + s * p.stage_bytes + p.off[1], p.y, row, H, yf, in);
+        copies_commit();
+    };
+    for (int s = 0; s < S; ++s) {
+        fetch_y(first + s * step, s);
+        fetch_x(first + s * step, s);
+    }
     // gate and norm of the branch as one scale and shift, the next norm's
     auto scale = [&](int k) { return mul4(col4<N>(o.gate, tid, k, 1.f), col4<N>(o.gamma_post, tid, k, 1.f)); };
     auto shift = [&](int k) {
         return o.beta_post ? mul4(col4<N>(o.gate, tid, k, 1.f), col4<N>(o.beta_post, tid, k, 0.f)) : all4(0.f);
     };
-    constexpr int PV = PREG ? VPT : 1;
-    float4 ps[PV], pt[PV], ns[PV], nt[PV];
-    if (PREG)
+    auto param = [&](int j, int k) {
+        return j == 0 ? scale(k) : j == 1 ? shift(k) : j == 2 ? col4<N>(o.gamma_pre, tid, k, 1.f) : col4<N>(o.beta_pre, tid, k, 0.f);
+    };
+    constexpr int PJ = PREG ? 4 : 1, PK = PREG ? VPT : 1;
+    float4 reg[PJ][PK];
+    if (PREG) {
 #pragma unroll
-        for (int k = 0; k < PV; ++k) {
-            if (!in(k)) continue;
-            ps[k] = scale(k);
-            pt[k] = shift(k);
-            ns[k] = col4<N>(o.gamma_pre, tid, k, 1.f);
-            nt[k] = col4<N>(o.beta_pre, tid, k, 0.f);
-        }
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                if (in(k)) reg[j % PJ][k % PK] = param(j, k);
+    }
+    auto take = [&](int j, int k) -> float4 { return PREG ? reg[j % PJ][k % PK] : param(j, k); };
     const float inv = 1.f / static_cast<float>(H), n_inv = n_w > 0.f ? 1.f / n_w : 0.f;
-    const bool stat = o.post || o.pre, centred = o.post == 1 || o.pre == 1;
-    const float ly = o.post == 1 ? 1.f : 0.f, lr = o.pre == 1 ? 1.f : 0.f;
+    const bool stat = o.post || o.pre;
     float4 u[VPT];                           // r of the row before
 #pragma unroll
     for (int k = 0; k < VPT; ++k) u[k] = all4(0.f);
@@ -74,55 +83,54 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N) join_kernel(const __
         float gt = 1.f;
         float4 v[VPT];
         if (now) {
-            copies_wait(S - 1);
+            copies_wait(2 * S - 1);
             if (o.gate_token) gt = o.gate_token[row];
         }
         const unsigned char *ys = staged<YT>(st + p.off[1], tid, yf);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) v[k] = now && in(k) ? ld4<YT, N>(ys, k, yf) : all4(0.f);
+        if (now) fetch_y(row + S * step, s);
         float2 sy = make_float2(0.f, 1.f), sr = sy;
         if (stat) {
             // of this warp's columns: the means (of y, of r before), then the square sums around them
-            float m[2] = {0.f, 0.f}, q[2] = {0.f, 0.f};
-            if (centred) {
+            float2 m = make_float2(0.f, 0.f), q = m;
+            if (CY || CR) {
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) {
-                    m[0] += sum4(v[k]);
-                    m[1] += sum4(u[k]);
+                    if (CY) m.x += sum4(v[k]);
+                    if (CR) m.y += sum4(u[k]);
                 }
-                warp_sums(m);
-                m[0] *= n_inv * ly;
-                m[1] *= n_inv * lr;
+                m = warp_pair_all(m.x, m.y);
+                m.x *= n_inv;
+                m.y *= n_inv;
             }
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 if (!in(k)) continue;
-                const float4 a = make_float4(v[k].x - m[0], v[k].y - m[0], v[k].z - m[0], v[k].w - m[0]);
-                const float4 b = make_float4(u[k].x - m[1], u[k].y - m[1], u[k].z - m[1], u[k].w - m[1]);
-                q[0] += dot4(a, a);
-                q[1] += dot4(b, b);
+                const float4 a = CY ? make_float4(v[k].x - m.x, v[k].y - m.x, v[k].z - m.x, v[k].w - m.x) : v[k];
+                const float4 b = CR ? make_float4(u[k].x - m.y, u[k].y - m.y, u[k].z - m.y, u[k].w - m.y) : u[k];
+                q.x += dot4(a, a);
+                q.y += dot4(b, b);
             }
-            warp_sums(q);
-            if (!ONE) {
-                float e[4] = {m[0], m[1], q[0], q[1]};
-                exchange(e);
-                q[0] = e[2];
-                q[1] = e[3];
-                if (centred) {
-                    m[0] = e[0] * n_l;
-                    m[1] = e[1] * n_l;
-                    warp_sums(m);
-                    m[0] *= inv;
-                    m[1] *= inv;
+            if (ONE) {
+                q = warp_pair_all(q.x, q.y);
+            } else {
+                // the warps' means and square sums
+                const float4 w = exchange(threadIdx.x & 16 ? m.y : m.x, warp_pair(q.x, q.y));
+                q = make_float2(w.z, w.w);
+                if (CY || CR) {
+                    m = warp_pair_all(w.x * n_l, w.y * n_l);
+                    m.x *= inv;
+                    m.y *= inv;
                     if (lane < N / 32) {
-                        q[0] = fmaf(n_l * ly * (e[0] - m[0]), e[0] - m[0], q[0]);
-                        q[1] = fmaf(n_l * lr * (e[1] - m[1]), e[1] - m[1], q[1]);
+                        if (CY) q.x = fmaf(n_l * (w.x - m.x), w.x - m.x, q.x);
+                        if (CR) q.y = fmaf(n_l * (w.y - m.y), w.y - m.y, q.y);
                     }
                 }
-                warp_sums(q);
+                q = warp_pair_all(q.x, q.y);
             }
-            if (o.post) sy = make_float2(m[0], 1.f / sqrtf(q[0] * inv + o.eps_post));
-            if (o.pre) sr = make_float2(m[1], 1.f / sqrtf(q[1] * inv + o.eps_pre));
+            if (o.post) sy = make_float2(CY ? m.x : 0.f, 1.f / sqrtf(q.x * inv + o.eps_post));
+            if (o.pre) sr = make_float2(CR ? m.y : 0.f, 1.f / sqrtf(q.y * inv + o.eps_pre));
         }
         if (before >= 0) {                   // the row before: its norm
             if (o.pre) {
@@ -130,19 +138,19 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N) join_kernel(const __
 #pragma unroll
                 for (int k = 0; k < VPT; ++k)
                     if (in(k))
-                        st4<BF16, N>(to, k, false, fma4(norm4(u[k], sr.x, sr.y), PREG ? ns[k % PV] : col4<N>(o.gamma_pre, tid, k, 1.f),
-                                                        PREG ? nt[k % PV] : col4<N>(o.beta_pre, tid, k, 0.f)));
+                        st4<BF16, N>(to, k, false, fma4(norm4(u[k], sr.x, sr.y), take(2, k), take(3, k)));
             }
             if (p.stats && tid == 0) p.stats[before] = make_float4(sy_before.x, sy_before.y, sr.x, sr.y);
         }
         before = -1;
         if (!now) continue;
+        copies_wait(2 * S - 1);
         const unsigned char *xs = staged<XT>(st + p.off[0], tid, xf);
         unsigned char *to = row_at<XT>(p.r, row, H, tid, xf);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             if (!in(k)) continue;
-            float4 b = fma4(norm4(v[k], sy.x, sy.y), PREG ? ps[k % PV] : scale(k), PREG ? pt[k % PV] : shift(k));
+            float4 b = fma4(norm4(v[k], sy.x, sy.y), take(0, k), take(1, k));
             const float4 x = ld4<XT, N>(xs, k, xf);
             b = make_float4(fmaf(o.alpha, x.x, gt * b.x), fmaf(o.alpha, x.y, gt * b.y), fmaf(o.alpha, x.z, gt * b.z),
                             fmaf(o.alpha, x.w, gt * b.w));
@@ -153,7 +161,7 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N) join_kernel(const __
             st4<XT, N>(to, k, xf, b);
             u[k] = b;
         }
-        fetch(row + S * step, s);
+        fetch_x(row + S * step, s);
         if (++s == S) s = 0;
         before = row;
         sy_before = sy;
@@ -162,11 +170,22 @@ __global__ void __launch_bounds__(N == 32 ? 32 * WARPS : N) join_kernel(const __
 
 using Kernel = void (*)(const Args);
 
-template <int N, bool PREG>
+template <int N, int CY, int CR>
 Kernel of_types(int x_fp32, int y_fp32)
 {
-    return x_fp32 ? (y_fp32 ? join_kernel<N, PREG, FP32, FP32> : join_kernel<N, PREG, FP32, BF16>)
-                  : (y_fp32 ? join_kernel<N, PREG, BF16, FP32> : join_kernel<N, PREG, BF16, BF16>);
+    return x_fp32 ? (y_fp32 ? join_kernel<N, FP32, FP32, CY, CR> : join_kernel<N, FP32, BF16, CY, CR>)
+                  : (y_fp32 ? join_kernel<N, BF16, FP32, CY, CR> : join_kernel<N, BF16, BF16, CY, CR>);
+}
+
+template <int N>
+Kernel of_kinds(const ResidualOpts &o, int x_fp32, int y_fp32)
+{
+    if constexpr (N == 1024)
+        return o.post == 1 ? (o.pre == 1 ? join_kernel<N, RUNTIME, RUNTIME, 1, 1> : join_kernel<N, RUNTIME, RUNTIME, 1, 0>)
+                           : (o.pre == 1 ? join_kernel<N, RUNTIME, RUNTIME, 0, 1> : join_kernel<N, RUNTIME, RUNTIME, 0, 0>);
+    else
+        return o.post == 1 ? (o.pre == 1 ? of_types<N, 1, 1>(x_fp32, y_fp32) : of_types<N, 1, 0>(x_fp32, y_fp32))
+                           : (o.pre == 1 ? of_types<N, 0, 1>(x_fp32, y_fp32) : of_types<N, 0, 0>(x_fp32, y_fp32));
 }
 
 }  // namespace
@@ -184,29 +203,27 @@ cudaError_t launch_join(const ResidualOpts &o, const void *x, int x_fp32, const 
     p.off[0] = 0;
     p.off[1] = H * (x_fp32 ? 4 : 2);
     p.stage_bytes = p.off[1] + H * (y_fp32 ? 4 : 2);
-    const int threads = row_threads(H);
+    // (448 where every thread has four vectors then)
+    const int threads = H > 6144 && H <= 7168 ? 448 : row_threads(H);
     const bool one = threads == 32;
-    dim3 block, grid;
-    if (one) {
-        p.stages = 2;
-        block = dim3(32, WARPS);
-        const int units = (T + WARPS - 1) / WARPS, most = 4 * num_sms();
-        grid = dim3(units < most ? units : most);
-    } else {
-        const int fit = static_cast<int>(ROOM / p.stage_bytes);
-        int ctas = 512 / threads;
-        if (ctas > fit / 2) ctas = fit / 2;
-        if (ctas < 1) ctas = 1;
-        p.stages = fit / ctas > 3 ? 3 : fit / ctas;
-        block = dim3(threads);
-        grid = dim3(T < ctas * num_sms() ? T : ctas * num_sms());
-    }
-    const Kernel kernel = threads == 32    ? of_types<32, false>(x_fp32, y_fp32)
-                          : threads == 128 ? of_types<128, true>(x_fp32, y_fp32)
-                          : threads == 256 ? of_types<256, true>(x_fp32, y_fp32)
-                          : threads == 512 ? of_types<512, true>(x_fp32, y_fp32)
-                                           : join_kernel<1024, false, RUNTIME, RUNTIME>;
+    // Rows on their way: about AHEAD bytes an SM.  More of them cost bandwidth (16384 x 7168 in fp32, without and
+    // with a norm of y, n by RMS norm and layer norm: 281 and 271 us with three stages of 57 KB, 254 and
+    // 241 us with one; in bf16 153 and 190 us with two stages of 29 KB, 165 and 191 us with one).
+    constexpr size_t AHEAD = 72 * 1024;
+    const size_t unit = static_cast<size_t>(p.stage_bytes) * (one ? WARPS : 1);     // a stage of a CTA
+    const int units = one ? (T + WARPS - 1) / WARPS : T, room = one ? 4 : 512 / threads;
+    int ctas = static_cast<int>(AHEAD / unit);
+    ctas = ctas < 1 ? 1 : (ctas > room ? (room < 1 ? 1 : room) : ctas);
+    const int fit = static_cast<int>(AHEAD / (unit * ctas));
+    p.stages = fit < 1 ? 1 : (fit > 3 ? 3 : fit);
+    const dim3 block = one ? dim3(32, WARPS) : dim3(threads), grid(units < ctas * num_sms() ? units : ctas * num_sms());
     const size_t smem = static_cast<size_t>(p.stages) * p.stage_bytes * (one ? WARPS : 1);
+    const Kernel kernel = threads == 32    ? of_kinds<32>(o, x_fp32, y_fp32)
+                          : threads == 64  ? of_kinds<64>(o, x_fp32, y_fp32)
+                          : threads == 128 ? of_kinds<128>(o, x_fp32, y_fp32)
+                          : threads == 256 ? of_kinds<256>(o, x_fp32, y_fp32)
+                          : threads == 448 ? of_kinds<448>(o, x_fp32, y_fp32)
+                          : threads == 512 ? of_kinds<512>(o, x_fp32, y_fp32) : of_kinds<1024>(o, x_fp32, y_fp32);
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, grid, block, smem, s, 1, p);

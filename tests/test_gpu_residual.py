@@ -313,6 +313,24 @@ def test_infinities_and_nan_stay_in_their_rows():
     assert bool(torch.isnan(r[4]).any()) and not bool(torch.isfinite(r[2]).all())
 
 
+@pytest.mark.parametrize("kinds", [("rms", "layer", True, False, False), ("layer", "rms", True, True, True), ("none", "none", False, True, True)])
+@pytest.mark.parametrize("T,H,xt,yt", [(9801, 1088, F32, F32), (9803, 576, F32, BF), (9901, 960, BF, F32), (9801, 1984, BF, BF), (4900, 2112, F32, BF), (5001, 4096, BF, F32),
+                                       (2501, 7168, BF, BF), (2499, 7168, F32, F32), (2433, 8192, F32, F32), (700, 8192, BF, F32)])
+def test_several_rows_a_cta(T, H, xt, yt, kinds):
+    # batches long enough for CTAs that take several rows at a time, and for every stage of the rings
+    x, y, p, dn, dr = _inputs(T, H, xt, yt, *kinds)
+    r, n, stats = _forward(x, y, p)
+    _check_forward(x, y, p, r, n, stats)
+    stats = _rounded_stats(y, r, p)
+    dx, dy, grads = _backward(dn, dr, y, r, stats, p)
+    rdx, rdy, ref = _reference(dn, dr, y, r, stats, p)
+    assert _near(dx, *rdx) and _near(dy, *rdy)
+    # (up to T / 152 rows a strand: 8 of the bound's 62 roundings become T / 152 + 8)
+    for k, g in grads.items():
+        w, t = ref[k]
+        assert _near(g, w, t * (T / 152 + 62) / 62), k
+
+
 FIRST = """
 import torch
 from expert_routed_ffn_router_gb300 import binding as B
