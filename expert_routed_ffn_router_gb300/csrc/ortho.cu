@@ -8,10 +8,14 @@
 // X P: A and P are symmetric, so the matrices stay as they lie).  A step's polynomial a s + b s^3 +
 // c s^5 acts on every singular value s of X.
 //
-// Launches: the momentum, partial square sums; X from them; three products a step:
+// Launches: the momentum, partial square sums; X from them; one persistent launch over all steps' products,
+// a list of tiles claimed in order:
 //   gram     A: the tiles on and below the diagonal, each stored twice (the mirror image too)
 //   square   P: likewise, with b A added as the tile leaves tensor memory
 //   apply    X: with a X added likewise; the last step's writes `out`
+// A matrix's tiles of one product start when those of the one before are stored (a counter a matrix);
+// they come earlier in the list, so whoever waits holds nothing that they need.  Other matrices' tiles
+// fill the gaps.  (A launch for each product: @LAUNCHES@.)
 //
 // Numbers.  The products take fp16 operands (11 bits; entries of X are at most 1.2 and typically
 // (rows columns)^-1/2, so a fixed power of two keeps them normal) with fp32 sums.  What is carried
@@ -24,8 +28,9 @@
 //
 // Tiles, roles and waits as in ffn_bwd.cu: clusters of two CTAs, 2-SM MMAs of 256 x 256, 64 deep
 // stages of 32 KB a CTA, two accumulators in tensor memory, eight epilogue warps, all waits
-// bounded (MOE_ERR_DEVICE_TIMEOUT in the status word).  A cluster's tiles are known beforehand
-// (tile, + clusters, ...), tiles of one matrix side by side.
+// bounded (MOE_ERR_DEVICE_TIMEOUT in the status word).
+//
+// What bounds it: @BOUND@
 #include <cuda.h>
 
 #include <cstring>
@@ -54,19 +59,27 @@ constexpr int SLAB = SLOTS * SLOT;        // an epilogue warp's buffers
 
 enum { GRAM, SQUARE, APPLY, LAST };
 
+constexpr int TQ = 4;                     // slots that hand claimed tiles to the roles
+constexpr int AHEAD = 24;                 // stages left to load of a tile when the next one is claimed
+constexpr int CLAIM_WARP = 2;
+constexpr int MAX_STEPS = 32;
+
 struct Args {
-    // loads: K-major operands in boxes of 128 x 64, MN-major ones in boxes of 64 x 64
-    CUtensorMap a, b;
-    // the epilogue's pieces of 32 rows: loads (SQUARE: A; APPLY: X's numbers), stores
-    CUtensorMap l, l2, s, s2;
-    int mode, amn, bmn;           // operand rows (columns) contiguous
-    int M, N, K;                  // products [M][K] x [K][N] of each matrix
-    int nM, nN, tiles;            // tiles of a matrix in each direction, in all
-    int tm, tn;                   // rows and columns of a tile that are kept
-    int tma_out;                  // LAST: rows of `out` are multiples of 16 bytes
-    float ca, cb, cc;             // coefficients
+    // loads: X of either buffer as the operand of gram and of apply, A, P; K-major operands in boxes
+    // of 128 x 64, MN-major ones (gram's X of tall matrices, apply's X of others) of 64 x 64
+    CUtensorMap xg[2], xa[2], a, p;
+    // the epilogue's pieces of 32 x 32, both ways: A, P, X's numbers, out
+    CUtensorMap pa, pp, px[2], pl, po;
+    int tall, steps, B, m, R, C;  // m: the smaller side
+    int side, n_side;             // tiles of A and P: rows and columns that are kept, tiles of a side
+    int tn, nM, nN;               // tiles of X: columns that are kept, tiles in each direction
+    int sym, app, units;          // tiles of A (or P), of X of a matrix; in all
+    int tma_out;                  // rows of `out` are multiples of 16 bytes
+    float c[3 * MAX_STEPS];
     float scale;
-    uint16_t *out;                // LAST: bf16 [B][M][N]
+    uint16_t *out;                // bf16 [B][R][C]
+    unsigned *count;              // [B] epilogue warps that are done with a tile (zeroed)
+    int *next;                    // the next tile to be claimed (zeroed)
     int *status;
     unsigned long long timeout_ns;
     int inject;
@@ -103,30 +116,52 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, 
                  ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src)) : "memory");
 }
 
-struct Tile { int b, m0, n0; };
-
-template <bool SYM>
-__device__ __forceinline__ Tile tile_at(const Args &p, int t)
+__device__ __forceinline__ unsigned ld_acquire(const unsigned *p)
 {
-    const int per = SYM ? p.nM * (p.nM + 1) / 2 : p.nM * p.nN;
-    const int b = t / per;
-    int l = t - b * per, i, j;
-    if (SYM) {
-        i = static_cast<int>((sqrtf(8.f * l + 1.f) - 1.f) * 0.5f);
-        while (i * (i + 1) / 2 > l) --i;
-        while ((i + 1) * (i + 2) / 2 <= l) ++i;
-        j = l - i * (i + 1) / 2;
-    } else {
-        // the smaller side's tiles innermost: they share a part of X (rows innermost for tall matrices:
-        // 695 instead of 672 us for 16 of 7168 x 2048)
-        if (p.nM > p.nN) { i = l / p.nN; j = l - i * p.nN; }
-        else { j = l / p.nM; i = l - j * p.nM; }
-    }
-    return Tile{b, i * p.tm, j * p.tn};
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
 }
 
-// SYM: GRAM and SQUARE, whose results are symmetric; else APPLY and LAST.
-template <bool SYM>
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// The tile's product and step, matrix and place, and the arrivals at the matrix's counter that it needs.
+struct Tile { int mode, k, b, m0, n0; unsigned need; };
+
+__device__ __forceinline__ Tile tile_at(const Args &p, int t)
+{
+    Tile T;
+    const int per = 2 * p.sym + p.app, step = p.B * per;
+    T.k = t / step;
+    int l = t - T.k * step;
+    T.need = 2 * N_EPI * static_cast<unsigned>(T.k * per);
+    if (l < 2 * p.B * p.sym) {
+        T.mode = l < p.B * p.sym ? GRAM : SQUARE;
+        if (T.mode == SQUARE) { l -= p.B * p.sym; T.need += 2 * N_EPI * p.sym; }
+        T.b = l / p.sym;
+        l -= T.b * p.sym;
+        int i = static_cast<int>((sqrtf(8.f * l + 1.f) - 1.f) * 0.5f);
+        while (i * (i + 1) / 2 > l) --i;
+        while ((i + 1) * (i + 2) / 2 <= l) ++i;
+        T.m0 = i * p.side;
+        T.n0 = (l - i * (i + 1) / 2) * p.side;
+        return T;
+    }
+    l -= 2 * p.B * p.sym;
+    T.mode = T.k + 1 < p.steps ? APPLY : LAST;
+    T.need += 2 * N_EPI * 2 * p.sym;
+    T.b = l / p.app;
+    l -= T.b * p.app;
+    // the smaller side's tiles innermost: they share a part of X (rows innermost for tall matrices:
+    // 695 instead of 672 us for 16 of 7168 x 2048)
+    int i, j;
+    if (p.nM > p.nN) { i = l / p.nN; j = l - i * p.nN; }
+    else { j = l / p.nM; i = l - j * p.nM; }
+    T.m0 = i * TM;
+    T.n0 = j * p.tn;
+    return T;
+}
+
 __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant__ Args p)
 {
     constexpr int TCOLS = 512;
@@ -134,7 +169,8 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
     unsigned char *ring = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *slabs = ring + STAGES * STAGE;
-    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], piece[N_EPI][SLOTS], drain;
+    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], piece[N_EPI][SLOTS], want, drain;
+    __shared__ int tq[TQ];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     volatile int *abort_flag = &abort_s;
@@ -152,8 +188,13 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 2 * N_EPI);
         }
+        for (int q = 0; q < TQ; ++q) {
+            mbar_init(&tqf[q], 1);
+            mbar_init(&tqe[q], 2 * N_EPI + 3);   // both epilogues and producers, the MMA issuer
+        }
         for (int w = 0; w < N_EPI; ++w)
             for (int b = 0; b < SLOTS; ++b) mbar_init(&piece[w][b], 1);
+        mbar_init(&want, 1);
         mbar_init(&drain, 1);
         abort_s = 0;
         fence_mbar_init();
@@ -168,36 +209,75 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-    const int kbs = (p.K + BK - 1) / BK;
+    const int gram_kbs = ((p.tall ? p.R : p.C) + BK - 1) / BK, m_kbs = (p.m + BK - 1) / BK;
+
+    // Tiles are claimed from a counter by a warp of the even CTA and handed to every role of both CTAs
+    // through TQ slots (-1 ends), the next one when that at hand has AHEAD stages left to load.
+    auto slot_done = [&](int q) {
+        if (leader) mbar_arrive(&tqe[q]);
+        else mbar_arrive_cluster(mapa_shared(smem_u32(&tqe[q]), 0));
+    };
+    // The tiles that this one builds on are stored.
+    auto ready = [&](const Tile &T) -> bool {
+        const unsigned *n = p.count + T.b;
+        if (T.need && ld_acquire(n) < T.need) {
+            const uint64_t t0 = globaltimer_ns();
+            while (ld_acquire(n) < T.need) {
+                if (*abort_flag) return false;
+                if (globaltimer_ns() - t0 > tmo) {
+                    *abort_flag = 1;
+                    report(p.status, MOE_ERR_DEVICE_TIMEOUT);
+                    return false;
+                }
+                __nanosleep(64);
+            }
+        }
+        fence_proxy_async_global();
+        return true;
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0 && !p.inject) {
-            uint32_t s = 0, ph = 0, it = 0;
+            uint32_t s = 0, ph = 0, it = 0, qs = 0, qph = 0;
             const uint32_t full0 = mapa_shared(smem_u32(full), 0);
             const int r = static_cast<int>(rank);
             bool good = true;
-            for (int t = cluster; t < p.tiles && good; t += clusters) {
-                const Tile T = tile_at<SYM>(p, t);
-                const int m = T.m0 + 128 * r, n = T.n0 + p.tn / 2 * r;
+            while (good) {
+                if (!mbar_wait_cluster(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
+                const int t = tq[qs];
+                slot_done(qs);
+                if (++qs == TQ) { qs = 0; qph ^= 1u; }
+                if (t < 0) break;
+                const Tile T = tile_at(p, t);
+                if (!ready(T)) break;
+                const bool sym = T.mode <= SQUARE;
+                const int m = T.m0 + 128 * r, n = T.n0 + (sym ? p.side : p.tn) / 2 * r, kbs = T.mode == GRAM ? gram_kbs : m_kbs;
+                const CUtensorMap *am, *bm;
+                bool amn = false, bmn = false;
+                if (T.mode == GRAM) { am = bm = &p.xg[T.k & 1]; amn = bmn = p.tall; }
+                else if (T.mode == SQUARE) { am = bm = &p.a; }
+                else if (p.tall) { am = &p.xa[T.k & 1]; bm = &p.p; }
+                else { am = &p.p; bm = &p.xa[T.k & 1]; bmn = true; }
+                bool asked = !leader;
                 for (int kb = 0; kb < kbs; ++kb, ++it) {
+                    if (!asked && kbs - kb <= AHEAD) { mbar_arrive(&want); asked = true; }
                     if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, tmo)) { good = false; break; }
                     unsigned char *a = ring + s * STAGE, *b = a + 2 * HALF;
                     const uint32_t fb = full0 + 8u * s;
                     if (leader) mbar_arrive_expect_tx(&full[s], 2u * STAGE);
                     const int k = kb * BK;
-                    if (p.amn) {
-                        tma_load_3d_pair(a, &p.a, fb, m, k, T.b);
-                        tma_load_3d_pair(a + HALF, &p.a, fb, m + 64, k, T.b);
+                    if (amn) {
+                        tma_load_3d_pair(a, am, fb, m, k, T.b);
+                        tma_load_3d_pair(a + HALF, am, fb, m + 64, k, T.b);
                     } else {
-                        tma_load_3d_pair(a, &p.a, fb, k, m, T.b);
+                        tma_load_3d_pair(a, am, fb, k, m, T.b);
                     }
-                    if (p.bmn) {
-                        tma_load_3d_pair(b, &p.b, fb, n, k, T.b);
-                        tma_load_3d_pair(b + HALF, &p.b, fb, n + 64, k, T.b);
+                    if (bmn) {
+                        tma_load_3d_pair(b, bm, fb, n, k, T.b);
+                        tma_load_3d_pair(b + HALF, bm, fb, n + 64, k, T.b);
                     } else {
-                        tma_load_3d_pair(b, &p.b, fb, k, n, T.b);
+                        tma_load_3d_pair(b, bm, fb, k, n, T.b);
                     }
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
@@ -221,13 +301,21 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         // -------------------------------------------------------------- MMA issuer
         if (lane == 0 && leader) {
             const uint32_t ring0 = smem_u32(ring);
-            const uint64_t ad0 = smem_desc_sw128(ring0, p.amn ? HALF : 16, 1024);
-            const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, p.bmn ? HALF : 16, 1024);
-            const uint32_t as = p.amn ? 128u : 2u, bs = p.bmn ? 128u : 2u;
-            const uint32_t id = idesc_f16_f32(TM, static_cast<uint32_t>(p.tn), p.amn, p.bmn);
-            uint32_t s = 0, ph = 0, b = 0, tph = 0;
+            uint32_t s = 0, ph = 0, b = 0, tph = 0, qs = 0, qph = 0;
             bool good = true;
-            for (int t = cluster; t < p.tiles && good; t += clusters) {
+            while (good) {
+                if (!mbar_wait(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
+                const int t = tq[qs];
+                slot_done(qs);
+                if (++qs == TQ) { qs = 0; qph ^= 1u; }
+                if (t < 0) break;
+                const Tile T = tile_at(p, t);
+                const bool amn = T.mode == GRAM && p.tall, bmn = amn || (T.mode >= APPLY && !p.tall);
+                const uint64_t ad0 = smem_desc_sw128(ring0, amn ? HALF : 16, 1024);
+                const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, bmn ? HALF : 16, 1024);
+                const uint32_t as = amn ? 128u : 2u, bs = bmn ? 128u : 2u;
+                const uint32_t id = idesc_f16_f32(TM, static_cast<uint32_t>(T.mode <= SQUARE ? p.side : p.tn), amn, bmn);
+                const int kbs = T.mode == GRAM ? gram_kbs : m_kbs;
                 if (!mbar_wait(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + b * TN;
@@ -252,6 +340,24 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             int dummy = 0;
             mbar_wait(&drain, 0, &dummy, nullptr, 20000000ull);
         }
+    } else if (warp == CLAIM_WARP) {
+        // ------------------------------------------------------------------ claims
+        if (lane == 0 && leader) {
+            uint32_t qs = 0, qph = 0, wph = 1;       // (the first claim waits for nothing)
+            int t = 0;
+            while (t >= 0) {
+                if (!mbar_wait(&want, wph, abort_flag, p.status, tmo)) break;
+                wph ^= 1u;
+                if (!mbar_wait_cluster(&tqe[qs], qph ^ 1u, abort_flag, p.status, tmo)) break;
+                t = atomicAdd(p.next, 1);
+                if (t >= p.units) t = -1;
+                tq[qs] = t;
+                st_shared_cluster(mapa_shared(smem_u32(&tq[qs]), 1), t);
+                mbar_arrive(&tqf[qs]);
+                mbar_arrive_cluster(mapa_shared(smem_u32(&tqf[qs]), 1));
+                if (++qs == TQ) { qs = 0; qph ^= 1u; }
+            }
+        }
     } else if (warp >= EPI0) {
         // ---------------------------------------------------------------- epilogue
         // A warp's pieces of a tile, one after the other: what is added to the sums arrives ahead of time
@@ -262,70 +368,76 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         const int r0 = 128 * static_cast<int>(rank) + 32 * q;
         unsigned char *slab = slabs + (warp - EPI0) * SLAB;
         uint64_t *arrived = piece[warp - EPI0];
-        const int pieces = p.tn / PC, c0 = half ? (pieces + 1) / 2 : 0, c1 = half ? pieces : (pieces + 1) / 2;
-        const bool loads = p.mode != GRAM;
-        // the pieces of a tile that this warp has: from c0 on
-        auto last_piece = [&](const Tile &T) {
-            if (r0 >= p.tm || T.m0 + r0 >= p.M) return c0;
-            const int n = (p.N - T.n0 + PC - 1) / PC;
-            return c1 < n ? c1 : (n > c0 ? n : c0);
-        };
-        // the next piece to be loaded
-        int ft = cluster, fc = c0;
-        Tile F{};
-        auto settle = [&]() {                // to the first tile that has one
-            while (ft < p.tiles) {
-                F = tile_at<SYM>(p, ft);
-                if (fc < last_piece(F)) return;
-                ft += clusters;
-                fc = c0;
-            }
-        };
-        int issued = 0, taken = 0;
-        auto load_piece = [&](int slot) {    // lane 0
-            if (ft >= p.tiles) return;
-            ++issued;
-            unsigned char *d = slab + slot * SLOT;
-            const int col = F.n0 + PC * fc;
-            mbar_arrive_expect_tx(&arrived[slot], SYM ? SLOT / 2 : SLOT);
-            tma_load_3d(d, &p.l, &arrived[slot], col, F.m0 + r0, F.b);
-            if (!SYM) tma_load_3d(d + SLOT / 2, &p.l2, &arrived[slot], col, F.m0 + r0, F.b);
-            ++fc;
-            settle();
-        };
-        uint32_t b = 0, tph = 0, slot = 0, pph = 0;
-        if (loads && lane == 0 && !p.inject) {
-            settle();
-            for (int i = 0; i < SLOTS; ++i) load_piece(i);
-        }
-        bool good = true;
-        for (int t = cluster; t < p.tiles && good; t += clusters) {
-            const Tile T = tile_at<SYM>(p, t);
-            if (lane == 0) good = mbar_wait(&tfull[b], tph, abort_flag, p.status, tmo);
+        uint32_t b = 0, tph = 0, qs = 0, qph = 0, pph = 0;   // pph: phases of the buffers' barriers
+        uint32_t flight = 0;                         // buffers that a copy is on its way to (lane 0)
+        // a wait by one lane (every lane then observes the phase itself)
+        auto wait_all = [&](uint64_t *bar, uint32_t parity, bool cluster) -> bool {
+            bool good = true;
+            if (lane == 0)
+                good = cluster ? mbar_wait_cluster(bar, parity, abort_flag, p.status, tmo)
+                               : mbar_wait(bar, parity, abort_flag, p.status, tmo);
             good = __shfl_sync(kFullMask, good, 0);
-            if (!good) break;
-            mbar_try_wait(&tfull[b], tph);
-            tc_fence_after();
+            if (good) {
+                if (cluster) mbar_try_wait_cluster(bar, parity);
+                else mbar_try_wait(bar, parity);
+            }
+            return good;
+        };
+        bool good = true;
+        while (good) {
+            if (!wait_all(&tqf[qs], qph, true)) break;
+            const int t = tq[qs];
+            __syncwarp();
+            if (lane == 0) slot_done(qs);
+            if (++qs == TQ) { qs = 0; qph ^= 1u; }
+            if (t < 0) break;
+            const Tile T = tile_at(p, t);
+            const bool sym = T.mode <= SQUARE, two = !sym, loads = T.mode != GRAM;
+            const int M = sym ? p.m : p.R, N = sym ? p.m : p.C, width = sym ? p.side : p.tn;
             const int m0 = T.m0 + r0, row = m0 + lane;
-            const bool mirror = SYM && T.m0 != T.n0;
-            const int end = last_piece(T);
-#pragma unroll 1
-            for (int c = c0; c < end; ++c) {
-                const int col = T.n0 + PC * c;
-                unsigned char *buf = slab + slot * SLOT;
-                __syncwarp();
+            const bool mirror = sym && T.m0 != T.n0;
+            // this warp's pieces: c0 .. end
+            const int pieces = width / PC, c0 = half ? (pieces + 1) / 2 : 0;
+            int end = half ? pieces : (pieces + 1) / 2;
+            if ((sym && r0 >= p.side) || m0 >= M) end = c0;
+            end = max(c0, min(end, (N - T.n0 + PC - 1) / PC));
+            const CUtensorMap *lm = sym ? &p.pa : &p.px[T.k & 1];
+            const CUtensorMap *sm = T.mode == GRAM ? &p.pa : T.mode == SQUARE ? &p.pp : T.mode == APPLY ? &p.px[(T.k + 1) & 1] : &p.po;
+            auto load_piece = [&](int c) {           // lane 0
+                const int slot = (c - c0) & 1;
+                unsigned char *d = slab + slot * SLOT;
+                mbar_arrive_expect_tx(&arrived[slot], two ? SLOT : SLOT / 2);
+                tma_load_3d(d, lm, &arrived[slot], T.n0 + PC * c, m0, T.b);
+                if (two) tma_load_3d(d + SLOT / 2, &p.pl, &arrived[slot], T.n0 + PC * c, m0, T.b);
+                flight |= 1u << slot;
+            };
+            if (loads && c0 < end) {
+                // (the producer has seen the same: this wait orders what this thread loads)
                 if (lane == 0) {
-                    if (loads) {
-                        good = mbar_wait(&arrived[slot], pph, abort_flag, p.status, tmo);
-                        taken += good ? 1 : 0;
-                    } else {
-                        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
-                    }
+                    good = ready(T);
+                    if (good && !p.inject)
+                        for (int c = c0; c < end && c < c0 + SLOTS; ++c) load_piece(c);
                 }
                 good = __shfl_sync(kFullMask, good, 0);
                 if (!good) break;
-                if (loads) mbar_try_wait(&arrived[slot], pph);
-                const bool direct = !SYM && p.mode == LAST && !p.tma_out;
+            }
+            if (!wait_all(&tfull[b], tph, false)) break;
+            tc_fence_after();
+            const bool direct = T.mode == LAST && !p.tma_out;
+            const float ca = p.c[3 * T.k], cb = p.c[3 * T.k + 1], cc = p.c[3 * T.k + 2] / SA;
+#pragma unroll 1
+            for (int c = c0; c < end; ++c) {
+                const int slot = (c - c0) & 1, col = T.n0 + PC * c;
+                unsigned char *buf = slab + slot * SLOT;
+                __syncwarp();
+                if (loads) {
+                    if (!wait_all(&arrived[slot], (pph >> slot) & 1u, false)) { good = false; break; }
+                    pph ^= 1u << slot;
+                    flight &= ~(1u << slot);
+                } else {
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
+                    __syncwarp();
+                }
                 float v[32];
                 tmem_ld32(tm0 + b * TN + PC * c, v);
                 // 16 bytes of the lane's row, in the 64-byte swizzle
@@ -333,41 +445,45 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                     return reinterpret_cast<uint4 *>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
                 };
                 auto at2 = [&](int i) -> uint4 * { return at(i) + SLOT / 2 / 16; };
-                if (SYM && p.mode == GRAM) {
+                if (T.mode == GRAM) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] *= SA / (SX * SX);
+                } else if (T.mode == SQUARE) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 h = *at(i);
+                        const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int j = 8 * i + 2 * k;
+                            v[j] = fmaf(cb, f16_lo(hw[k]), v[j] * cc);
+                            v[j + 1] = fmaf(cb, f16_hi(hw[k]), v[j + 1] * cc);
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 h = *at(i), l = SYM ? make_uint4(0, 0, 0, 0) : *at2(i);
+                        const uint4 h = *at(i), l = *at2(i);
                         const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int j = 8 * i + 2 * k;
-                            float x0 = f16_lo(hw[k]), x1 = f16_hi(hw[k]);
-                            if (SYM) {
-                                v[j] = fmaf(p.cb, x0, v[j] * (p.cc / SA));
-                                v[j + 1] = fmaf(p.cb, x1, v[j + 1] * (p.cc / SA));
-                            } else {
-                                x0 = fmaf(f16_lo(lw[k]), 1.f / SLO, x0);
-                                x1 = fmaf(f16_hi(lw[k]), 1.f / SLO, x1);
-                                v[j] = fmaf(p.ca, x0, v[j] * (1.f / SA));
-                                v[j + 1] = fmaf(p.ca, x1, v[j + 1] * (1.f / SA));
-                            }
+                            v[j] = fmaf(ca, fmaf(f16_lo(lw[k]), 1.f / SLO, f16_lo(hw[k])), v[j] * (1.f / SA));
+                            v[j + 1] = fmaf(ca, fmaf(f16_hi(lw[k]), 1.f / SLO, f16_hi(hw[k])), v[j + 1] * (1.f / SA));
                         }
                     }
                 }
                 const float f = p.scale / SX;
                 if (direct) {
-                    if (row < p.M) {
-                        uint16_t *o = p.out + (static_cast<size_t>(T.b) * p.M + row) * p.N + col;
+                    if (row < M) {
+                        uint16_t *o = p.out + (static_cast<size_t>(T.b) * M + row) * N + col;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (col + i < p.N) o[i] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * f));
+                            if (col + i < N) o[i] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * f));
                     }
                 } else {
                     uint32_t w[16];
-                    if (!SYM && p.mode == LAST) {
+                    if (T.mode == LAST) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) w[i] = f32x2_to_bf16x2(v[2 * i + 1] * f, v[2 * i] * f);
                     } else {
@@ -376,7 +492,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) *at(i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                    if (!SYM && p.mode == APPLY) {
+                    if (T.mode == APPLY) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t y[4];
@@ -386,43 +502,53 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                                                       (v[8 * i + 2 * k] - f16_lo(w[4 * i + k])) * SLO);
                             *at2(i) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
-                    }
-                    if (mirror) {
+                    } else if (mirror) {
                         // row j of the mirror image: this lane's number of column j
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             *reinterpret_cast<uint16_t *>(buf + SLOT / 2 + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2) =
                                 static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
                     }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                if (!direct) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
                     if (!direct) {
-                        tma_store_3d(&p.s, buf, col, m0, T.b);
-                        if (!SYM && p.mode == APPLY) tma_store_3d(&p.s2, buf + SLOT / 2, col, m0, T.b);
-                        if (mirror) tma_store_3d(&p.s, buf + SLOT / 2, m0, col, T.b);
+                        tma_store_3d(sm, buf, col, m0, T.b);
+                        if (T.mode == APPLY) tma_store_3d(&p.pl, buf + SLOT / 2, col, m0, T.b);
+                        else if (mirror) tma_store_3d(sm, buf + SLOT / 2, m0, col, T.b);
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
-                    if (loads) {             // the buffer's next piece, once this one has left it
+                    if (loads && c + SLOTS < end) {  // the buffer's next piece, once this one has left it
                         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        load_piece(slot);
+                        load_piece(c + SLOTS);
                     }
                 }
-                if (++slot == SLOTS) { slot = 0; pph ^= 1u; }
             }
             if (!good) break;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty0 + 8u * b);
+            if (lane == 0) {
+                mbar_arrive_cluster(tempty0 + 8u * b);
+                if (T.mode != LAST) {
+                    // the warp's part of the tile is in global memory: tell who builds on it
+                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                    fence_proxy_async_global();
+                    __threadfence();
+                    atomicAdd(p.count + T.b, 1u);
+                } else {
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+            }
+            __syncwarp();
             b ^= 1u;
             if (b == 0) tph ^= 1u;
         }
         if (lane == 0) {
             // pieces still on their way (after a wait that ran out), and the last stores
-            for (; taken < issued; ++taken) {
+            for (int i = 0; i < SLOTS; ++i) {
                 int dummy = 0;
-                mbar_wait(&arrived[taken % SLOTS], (taken / SLOTS) & 1u, &dummy, nullptr, 20000000ull);
+                if (flight >> i & 1u) mbar_wait(&arrived[i], (pph >> i) & 1u, &dummy, nullptr, 20000000ull);
             }
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         }
@@ -441,7 +567,6 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
 // ------------------------------------------------------------------ momentum, norm, X
 constexpr int PT = 256;               // threads
 constexpr int MAX_PARTS = 256;        // chunks of a matrix
-constexpr int MAX_STEPS = 32;
 
 struct Prepare {
     const void *g;
@@ -454,6 +579,7 @@ struct Prepare {
     int parts;
     float4 *part;                     // [B][parts]: square sums at three scales
     uint16_t *hi, *lo;                // [B][R][ld]
+    unsigned *count;                  // [B] and the next tile to be claimed: zeroed here
 };
 
 template <bool VEC>
@@ -521,6 +647,10 @@ __global__ void __launch_bounds__(PT) ortho_momentum_kernel(const Prepare p)
     constexpr int N = Elements<VEC>::N;
     __shared__ float red[3][PT / 32];
     pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.count[blockIdx.y] = 0;
+        if (blockIdx.y == 0) p.count[gridDim.y] = 0;
+    }
     const long long n = static_cast<long long>(p.R) * p.C;
     const size_t base = static_cast<size_t>(blockIdx.y) * n;
     const long long lo = blockIdx.x * p.chunk, hi = min(n, lo + p.chunk);
@@ -946,7 +1076,7 @@ int up8(int n) { return (n + 7) & ~7; }
 struct Layout {
     int m, ld, ldm, parts;
     long long chunk;
-    size_t part, hi[2], lo, A, P, bytes;
+    size_t count, part, hi[2], lo, A, P, bytes;
 };
 Layout layout(int B, int R, int C)
 {
@@ -963,6 +1093,7 @@ Layout layout(int B, int R, int C)
     size_t o = 0;
     auto take = [&](size_t b) { const size_t at = o; o += al256(b); return at; };
     const size_t x = static_cast<size_t>(B) * R * L.ld * 2, a = static_cast<size_t>(B) * L.m * L.ldm * 2;
+    L.count = take((static_cast<size_t>(B) + 1) * sizeof(unsigned));
     L.part = take(static_cast<size_t>(B) * L.parts * sizeof(float4));
     L.hi[0] = take(x);
     L.hi[1] = take(x);
@@ -985,7 +1116,7 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     unsigned char *w = static_cast<unsigned char *>(scratch);
     Prepare q{f.g, f.g_fp32, f.momentum, f.mu, f.nesterov, R, C, L.ld, L.chunk, L.parts,
               reinterpret_cast<float4 *>(w + L.part), reinterpret_cast<uint16_t *>(w + L.hi[0]),
-              reinterpret_cast<uint16_t *>(w + L.lo)};
+              reinterpret_cast<uint16_t *>(w + L.lo), reinterpret_cast<unsigned *>(w + L.count)};
     const bool vec = C % 8 == 0;
     const bool tall = R > C;             // the smaller side is the columns
     const int m = L.m, n = tall ? R : C;
@@ -1014,97 +1145,55 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     if (e != cudaSuccess) return e;
 
     void *A = w + L.A, *P = w + L.P;
-    Args g, sq, ap[2];
-    memset(&g, 0, sizeof g);
-    g.status = status;
-    g.timeout_ns = timeout_ns;
-    g.inject = inject;
-    g.scale = f.scale;
-    g.out = static_cast<uint16_t *>(f.out);
-    ap[0] = g;
+    Args a;
+    memset(&a, 0, sizeof a);
     const int most = num_sms() / 2;      // clusters
     const auto tiles = [](int n, int t) { return (n + t - 1) / t; };
+    a.tall = tall;
+    a.steps = f.steps;
+    a.B = B; a.m = m; a.R = R; a.C = C;
     // symmetric results: as many tiles as of 256, of equal sides (a multiple of 32)
-    const int side = (tiles(m, tiles(m, 256)) + 31) / 32 * 32;
-    // X: the width (a multiple of 32) whose rounds of tiles take least; a tile's fixed part is worth
-    // about 32 columns
-    const auto width = [&](int rows, int cols) {
-        int best = 0;
-        long long least = 0;
-        for (int k = tiles(cols, 256); k <= 4 * tiles(cols, 256); ++k) {
-            const int t = (tiles(cols, k) + 31) / 32 * 32;
-            const long long all = static_cast<long long>(B) * tiles(rows, TM) * tiles(cols, t);
-            const long long cost = (all + most - 1) / most * (t + 32);
-            if (!best || cost < least) { least = cost; best = t; }
-        }
-        return best;
-    };
-    // gram: [m][n] x [n][m]
-    g.mode = GRAM;
-    g.amn = g.bmn = tall ? 1 : 0;
-    g.M = g.N = m;
-    g.K = tall ? R : C;
-    g.tm = g.tn = side;
-    g.nM = g.nN = (m + g.tm - 1) / g.tm;
-    g.tiles = B * (g.nM * (g.nM + 1) / 2);
-    bool ok = encode(&g.s, A, B, m, m, L.ldm, 32, 32);
-    // square
-    sq = g;
-    sq.mode = SQUARE;
-    sq.amn = sq.bmn = 0;
-    sq.K = m;
-    sq.l = g.s;
-    ok = ok && encode(&sq.a, A, B, m, m, L.ldm, 128, 64) && encode(&sq.s, P, B, m, m, L.ldm, 32, 32);
-    sq.b = sq.a;
-    // apply: [m][m] x [m][n], or X P for tall matrices
-    ap[0].mode = APPLY;
-    ap[0].M = R;
-    ap[0].N = C;
-    ap[0].K = m;
-    ap[0].tm = TM;
-    ap[0].tn = width(R, C);
-    ap[0].nM = tiles(R, TM);
-    ap[0].nN = (C + ap[0].tn - 1) / ap[0].tn;
-    ap[0].tiles = B * ap[0].nM * ap[0].nN;
-    ap[0].bmn = tall ? 0 : 1;
-    ap[0].tma_out = C % 8 == 0 ? 1 : 0;
-    ok = ok && encode(&ap[0].s2, w + L.lo, B, R, C, L.ld, 32, 32);
-    ap[0].l2 = ap[0].s2;
-    ap[1] = ap[0];
-    CUtensorMap gx[2], out;
-    for (int i = 0; i < 2; ++i) {        // from X in buffer i to the other one
-        void *x = w + L.hi[i];
-        ok = ok && encode(&ap[i].l, x, B, R, C, L.ld, 32, 32) && encode(&gx[i], x, B, R, C, L.ld, tall ? 64 : 128, 64);
-        if (tall)
-            ok = ok && encode(&ap[i].a, x, B, R, C, L.ld, 128, 64) && encode(&ap[i].b, P, B, m, m, L.ldm, 128, 64);
-        else
-            ok = ok && encode(&ap[i].a, P, B, m, m, L.ldm, 128, 64) && encode(&ap[i].b, x, B, R, C, L.ld, 64, 64);
+    a.side = (tiles(m, tiles(m, 256)) + 31) / 32 * 32;
+    a.n_side = tiles(m, a.side);
+    a.sym = a.n_side * (a.n_side + 1) / 2;
+    // X: the width (a multiple of 32) whose tiles take least; a tile's fixed part is worth about 32 columns.
+    // Few matrices' products follow each other in rounds of the clusters.
+    a.nM = tiles(R, TM);
+    double least = 0;
+    for (int k = tiles(C, 256); k <= 4 * tiles(C, 256); ++k) {
+        const int t = (tiles(C, k) + 31) / 32 * 32;
+        const long long all = static_cast<long long>(B) * a.nM * tiles(C, t);
+        const double rounds = B < 4 || all < most ? static_cast<double>((all + most - 1) / most) : static_cast<double>(all) / most;
+        if (!a.tn || rounds * (t + 32) < least) { least = rounds * (t + 32); a.tn = t; }
     }
-    ap[0].s = ap[1].l;
-    ap[1].s = ap[0].l;
-    if (ap[0].tma_out) ok = ok && encode(&out, f.out, B, R, C, C, 32, 32);
+    a.nN = tiles(C, a.tn);
+    a.app = a.nM * a.nN;
+    const long long units = static_cast<long long>(f.steps) * B * (2 * a.sym + a.app);
+    if (units >= (1ll << 31) - 65536) return cudaErrorInvalidValue;
+    a.units = static_cast<int>(units);
+    a.tma_out = C % 8 == 0 ? 1 : 0;
+    memcpy(a.c, f.coeffs, 3 * f.steps * sizeof(float));
+    a.scale = f.scale;
+    a.out = static_cast<uint16_t *>(f.out);
+    a.count = q.count;
+    a.next = reinterpret_cast<int *>(q.count + B);
+    a.status = status;
+    a.timeout_ns = timeout_ns;
+    a.inject = inject;
+    bool ok = encode(&a.a, A, B, m, m, L.ldm, 128, 64) && encode(&a.p, P, B, m, m, L.ldm, 128, 64) &&
+              encode(&a.pa, A, B, m, m, L.ldm, 32, 32) && encode(&a.pp, P, B, m, m, L.ldm, 32, 32) &&
+              encode(&a.pl, w + L.lo, B, R, C, L.ld, 32, 32);
+    for (int i = 0; i < 2; ++i) {
+        void *x = w + L.hi[i];
+        ok = ok && encode(&a.xg[i], x, B, R, C, L.ld, tall ? 64 : 128, 64) &&
+             encode(&a.xa[i], x, B, R, C, L.ld, tall ? 128 : 64, 64) && encode(&a.px[i], x, B, R, C, L.ld, 32, 32);
+    }
+    if (a.tma_out) ok = ok && encode(&a.po, f.out, B, R, C, C, 32, 32);
     if (!ok) return cudaErrorInvalidValue;
     const size_t smem = 1024 + STAGES * STAGE + N_EPI * SLAB;
-    if ((e = ensure_smem(reinterpret_cast<const void *>(ortho_gemm_kernel<true>), smem)) != cudaSuccess ||
-        (e = ensure_smem(reinterpret_cast<const void *>(ortho_gemm_kernel<false>), smem)) != cudaSuccess)
-        return e;
-    auto run = [&](const Args &a) {
-        return launch_pdl(a.mode <= SQUARE ? ortho_gemm_kernel<true> : ortho_gemm_kernel<false>,
-                          dim3(2 * (a.tiles < most ? a.tiles : most)), dim3(NT), smem, s, 2, a);
-    };
-    for (int k = 0; k < f.steps; ++k) {
-        const int i = k & 1;
-        g.a = g.b = gx[i];
-        sq.cb = f.coeffs[3 * k + 1];
-        sq.cc = f.coeffs[3 * k + 2];
-        ap[i].ca = f.coeffs[3 * k];
-        if (k + 1 == f.steps) {
-            ap[i].mode = LAST;
-            if (ap[i].tma_out) ap[i].s = out;
-        }
-        if ((e = run(g)) != cudaSuccess || (e = run(sq)) != cudaSuccess || (e = run(ap[i])) != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    if ((e = ensure_smem(reinterpret_cast<const void *>(ortho_gemm_kernel), smem)) != cudaSuccess) return e;
+    const int widest = B * (a.sym > a.app ? a.sym : a.app);
+    return launch_pdl(ortho_gemm_kernel, dim3(2 * (widest < most ? widest : most)), dim3(NT), smem, s, 2, a);
 }
 
 }  // namespace moe
