@@ -2,17 +2,17 @@
 // of the Muon optimiser), on the 5th-generation tensor cores.
 //
 //   m <- mu m + g,  u = m or g + mu m (with momentum), else g
-//   X = u / |u|_F;  every step:  A = X X^T,  P = b A + c A A,  X <- a X + P X;   out = scale X
+//   X = u / |u|_F;  every step:  A = X X^T,  P = b A + c A A,  X <- (a I + P) X;   out = scale X
 //
-// with A on the smaller side (for matrices with more rows than columns A = X^T X and X <- a X +
-// X P: A and P are symmetric, so the matrices stay as they lie).  A step's polynomial a s + b s^3 +
+// with A on the smaller side (for matrices with more rows than columns A = X^T X and X <- X
+// (a I + P): A and P are symmetric, so the matrices stay as they lie).  A step's polynomial a s + b s^3 +
 // c s^5 acts on every singular value s of X.
 //
 // Launches: the momentum, partial square sums; X from them; one persistent launch over all steps' products,
 // a list of tiles claimed in order:
 //   gram     A: the tiles on and below the diagonal, each stored twice (the mirror image too)
-//   square   P: likewise, with b A added as the tile leaves tensor memory
-//   apply    X: with a X added likewise; the last step's writes `out`
+//   square   a I + P: likewise, with a I + b A added as the tile leaves tensor memory
+//   apply    X: the product of a I + P and X, the last step's into `out`
 // A matrix's tiles of one product start when those of the one before are stored (a counter a matrix);
 // they come earlier in the list, so whoever waits holds nothing that they need.  Other matrices' tiles
 // fill the gaps.  (A launch for each product: @LAUNCHES@.)
@@ -20,11 +20,13 @@
 // Numbers.  The products take fp16 operands (11 bits; entries of X are at most 1.2 and typically
 // (rows columns)^-1/2, so a fixed power of two keeps them normal) with fp32 sums.  What is carried
 // from step to step is X in two fp16 numbers, 22 bits: a direction with a small singular value
-// is multiplied by a = 3.4 in every step, 485 over five, and a rounding of X with it.  (Rounded to
-// fp16 once a step, gradients of rank 16 come out 3e-2 off, in bf16 0.2; so they are 4e-4 off.)
-// A and P are rounded to fp16 once each: their error acts through products with X alone, and
-// what X has not is not amplified.  In all 2e-4 to 1.8e-3 off, the largest for flat spectra; the
-// rounding of the bf16 result is 1.7e-3.
+// is multiplied by a = 3.4 in every step, 485 over five, and a rounding of X with it.  The products take
+// the first number; of the second one, a times itself is added (what P would make of it is small).
+// The last step does without: its factor of 3.4 on a rounding does not show.  (Rounded to fp16 in every
+// step, gradients of rank 16 come out 3e-2 off, in bf16 0.2; so they are 1.5e-3 off.)  A and a I + P are
+// rounded to fp16 once each: their error acts through products with X alone, and what X has not is not
+// amplified.  In all 0.5e-3 to 1.7e-3 off, the largest for flat spectra and for ranks far below the
+// sides; the rounding of the bf16 result is 1.7e-3.
 //
 // Tiles, roles and waits as in ffn_bwd.cu: clusters of two CTAs, 2-SM MMAs of 256 x 256, 64 deep
 // stages of 32 KB a CTA, two accumulators in tensor memory, eight epilogue warps, all waits
@@ -51,11 +53,12 @@ constexpr int N_EPI = 8, EPI0 = 4;
 constexpr int NT = 32 * (EPI0 + N_EPI);
 constexpr int HALF = 8192;                // 64 x 64 fp16
 constexpr int STAGE = 4 * HALF;
-constexpr int STAGES = 5;
+constexpr int STAGES = 4;
 constexpr int PC = 32;                    // columns of an epilogue's piece
-constexpr int SLOT = 2 * 32 * PC * 2;     // its two arrays: the mirror image, or X's two numbers
-constexpr int SLOTS = 2;
-constexpr int SLAB = SLOTS * SLOT;        // an epilogue warp's buffers
+constexpr int PIECES = 4;                 // of a warp's part of a tile, at most
+constexpr int PIECE = 32 * PC * 2;
+constexpr int SIDE = 2;                   // buffers for what leaves beside a piece, in turn
+constexpr int SLAB = (PIECES + SIDE) * PIECE;   // an epilogue warp's buffers
 
 enum { GRAM, SQUARE, APPLY, LAST };
 
@@ -68,7 +71,7 @@ struct Args {
     // loads: X of either buffer as the operand of gram and of apply, A, P; K-major operands in boxes
     // of 128 x 64, MN-major ones (gram's X of tall matrices, apply's X of others) of 64 x 64
     CUtensorMap xg[2], xa[2], a, p;
-    // the epilogue's pieces of 32 x 32, both ways: A, P, X's numbers, out
+    // the epilogue's pieces of 32 x 32, both ways: A, P, X's first and second numbers, out
     CUtensorMap pa, pp, px[2], pl, po;
     int tall, steps, B, m, R, C;  // m: the smaller side
     int side, n_side;             // tiles of A and P: rows and columns that are kept, tiles of a side
@@ -123,6 +126,15 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned *p)
     return v;
 }
 
+// Whether a phase is complete, without waiting (try_wait may suspend the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // The tile's product and step, matrix and place, and the arrivals at the matrix's counter that it needs.
@@ -169,8 +181,8 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
     unsigned char *ring = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *slabs = ring + STAGES * STAGE;
-    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], piece[N_EPI][SLOTS], want, drain;
-    __shared__ int tq[TQ];
+    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], piece[N_EPI][PIECES], want, drain;
+    __shared__ int tq[TQ][5];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     volatile int *abort_flag = &abort_s;
@@ -193,7 +205,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             mbar_init(&tqe[q], 2 * N_EPI + 3);   // both epilogues and producers, the MMA issuer
         }
         for (int w = 0; w < N_EPI; ++w)
-            for (int b = 0; b < SLOTS; ++b) mbar_init(&piece[w][b], 1);
+            for (int b = 0; b < PIECES; ++b) mbar_init(&piece[w][b], 1);
         mbar_init(&want, 1);
         mbar_init(&drain, 1);
         abort_s = 0;
@@ -211,30 +223,14 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
     const uint32_t tmem = tmem_slot;
     const int gram_kbs = ((p.tall ? p.R : p.C) + BK - 1) / BK, m_kbs = (p.m + BK - 1) / BK;
 
-    // Tiles are claimed from a counter by a warp of the even CTA and handed to every role of both CTAs
-    // through TQ slots (-1 ends), the next one when that at hand has AHEAD stages left to load.
+    // Tiles are claimed from a counter by a warp of the even CTA, the next one when that at hand has AHEAD
+    // stages left to load.  It decodes them, waits for what they build on, and hands them to every role of
+    // both CTAs through TQ slots (mode -1 ends).
     auto slot_done = [&](int q) {
         if (leader) mbar_arrive(&tqe[q]);
         else mbar_arrive_cluster(mapa_shared(smem_u32(&tqe[q]), 0));
     };
-    // The tiles that this one builds on are stored.
-    auto ready = [&](const Tile &T) -> bool {
-        const unsigned *n = p.count + T.b;
-        if (T.need && ld_acquire(n) < T.need) {
-            const uint64_t t0 = globaltimer_ns();
-            while (ld_acquire(n) < T.need) {
-                if (*abort_flag) return false;
-                if (globaltimer_ns() - t0 > tmo) {
-                    *abort_flag = 1;
-                    report(p.status, MOE_ERR_DEVICE_TIMEOUT);
-                    return false;
-                }
-                __nanosleep(64);
-            }
-        }
-        fence_proxy_async_global();
-        return true;
-    };
+    auto slot_read = [&](int q) { return Tile{tq[q][0], tq[q][1], tq[q][2], tq[q][3], tq[q][4], 0u}; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
@@ -245,12 +241,11 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             bool good = true;
             while (good) {
                 if (!mbar_wait_cluster(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
-                const int t = tq[qs];
+                const Tile T = slot_read(qs);
                 slot_done(qs);
                 if (++qs == TQ) { qs = 0; qph ^= 1u; }
-                if (t < 0) break;
-                const Tile T = tile_at(p, t);
-                if (!ready(T)) break;
+                if (T.mode < 0) break;
+                fence_proxy_async_global();
                 const bool sym = T.mode <= SQUARE;
                 const int m = T.m0 + 128 * r, n = T.n0 + (sym ? p.side : p.tn) / 2 * r, kbs = T.mode == GRAM ? gram_kbs : m_kbs;
                 const CUtensorMap *am, *bm;
@@ -305,11 +300,10 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             bool good = true;
             while (good) {
                 if (!mbar_wait(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
-                const int t = tq[qs];
+                const Tile T = slot_read(qs);
                 slot_done(qs);
                 if (++qs == TQ) { qs = 0; qph ^= 1u; }
-                if (t < 0) break;
-                const Tile T = tile_at(p, t);
+                if (T.mode < 0) break;
                 const bool amn = T.mode == GRAM && p.tall, bmn = amn || (T.mode >= APPLY && !p.tall);
                 const uint64_t ad0 = smem_desc_sw128(ring0, amn ? HALF : 16, 1024);
                 const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, bmn ? HALF : 16, 1024);
@@ -344,15 +338,39 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         // ------------------------------------------------------------------ claims
         if (lane == 0 && leader) {
             uint32_t qs = 0, qph = 0, wph = 1;       // (the first claim waits for nothing)
-            int t = 0;
-            while (t >= 0) {
+            bool more = true;
+            while (more) {
                 if (!mbar_wait(&want, wph, abort_flag, p.status, tmo)) break;
                 wph ^= 1u;
+                const int t = atomicAdd(p.next, 1);
+                more = t < p.units;
+                Tile T{-1, 0, 0, 0, 0, 0u};
+                if (more) {
+                    T = tile_at(p, t);
+                    // the tiles that it builds on are stored
+                    const unsigned *n = p.count + T.b;
+                    if (T.need && ld_acquire(n) < T.need) {
+                        const uint64_t t0 = globaltimer_ns();
+                        bool good = true;
+                        while (good && ld_acquire(n) < T.need) {
+                            if (*abort_flag) good = false;
+                            else if (globaltimer_ns() - t0 > tmo) {
+                                *abort_flag = 1;
+                                report(p.status, MOE_ERR_DEVICE_TIMEOUT);
+                                good = false;
+                            }
+                        }
+                        if (!good) break;
+                    }
+                }
                 if (!mbar_wait_cluster(&tqe[qs], qph ^ 1u, abort_flag, p.status, tmo)) break;
-                t = atomicAdd(p.next, 1);
-                if (t >= p.units) t = -1;
-                tq[qs] = t;
-                st_shared_cluster(mapa_shared(smem_u32(&tq[qs]), 1), t);
+                const int vals[5] = {T.mode, T.k, T.b, T.m0, T.n0};
+                const uint32_t other = mapa_shared(smem_u32(tq[qs]), 1);
+#pragma unroll
+                for (int j = 0; j < 5; ++j) {
+                    tq[qs][j] = vals[j];
+                    st_shared_cluster(other + 4u * j, vals[j]);
+                }
                 mbar_arrive(&tqf[qs]);
                 mbar_arrive_cluster(mapa_shared(smem_u32(&tqf[qs]), 1));
                 if (++qs == TQ) { qs = 0; qph ^= 1u; }
@@ -360,8 +378,9 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         }
     } else if (warp >= EPI0) {
         // ---------------------------------------------------------------- epilogue
-        // A warp's pieces of a tile, one after the other: what is added to the sums arrives ahead of time
-        // by TMA, and the results leave from the same buffer.
+        // A warp's pieces of a tile, a buffer each: what is added to the sums (SQUARE: A; APPLY: X's second
+        // number) arrives there by TMA while the products run, and the results leave from there; what
+        // goes beside them (the mirror image; X's first number) leaves from two more buffers in turn.
         const int q = warp & 3, half = (warp - EPI0) >> 2;   // lane quarter, half of the columns
         const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
@@ -370,6 +389,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         uint64_t *arrived = piece[warp - EPI0];
         uint32_t b = 0, tph = 0, qs = 0, qph = 0, pph = 0;   // pph: phases of the buffers' barriers
         uint32_t flight = 0;                         // buffers that a copy is on its way to (lane 0)
+        int pending = -1;                            // matrix of the last tile, if nobody has been told of it
         // a wait by one lane (every lane then observes the phase itself)
         auto wait_all = [&](uint64_t *bar, uint32_t parity, bool cluster) -> bool {
             bool good = true;
@@ -383,75 +403,84 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             }
             return good;
         };
+        // The warp's part of its last tile is in global memory: tell who builds on it (lane 0).
+        auto tell = [&]() {
+            if (pending < 0) return;
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            fence_proxy_async_global();
+            __threadfence();
+            atomicAdd(p.count + pending, 1u);
+            pending = -1;
+        };
         bool good = true;
         while (good) {
+            // (the next tile may wait for the one that nobody has been told of)
+            if (lane == 0 && pending >= 0 && !mbar_test(&tqf[qs], qph)) tell();
             if (!wait_all(&tqf[qs], qph, true)) break;
-            const int t = tq[qs];
+            const Tile T = slot_read(qs);
             __syncwarp();
             if (lane == 0) slot_done(qs);
             if (++qs == TQ) { qs = 0; qph ^= 1u; }
-            if (t < 0) break;
-            const Tile T = tile_at(p, t);
-            const bool sym = T.mode <= SQUARE, two = !sym, loads = T.mode != GRAM;
+            if (T.mode < 0) {
+                if (lane == 0) tell();
+                break;
+            }
+            const bool sym = T.mode <= SQUARE, loads = T.mode == SQUARE || T.mode == APPLY;
             const int M = sym ? p.m : p.R, N = sym ? p.m : p.C, width = sym ? p.side : p.tn;
             const int m0 = T.m0 + r0, row = m0 + lane;
             const bool mirror = sym && T.m0 != T.n0;
+            // X of the step before the last one goes on in its first number alone
+            const bool second = T.mode == APPLY && T.k + 2 < p.steps;
             // this warp's pieces: c0 .. end
             const int pieces = width / PC, c0 = half ? (pieces + 1) / 2 : 0;
             int end = half ? pieces : (pieces + 1) / 2;
             if ((sym && r0 >= p.side) || m0 >= M) end = c0;
             end = max(c0, min(end, (N - T.n0 + PC - 1) / PC));
-            const CUtensorMap *lm = sym ? &p.pa : &p.px[T.k & 1];
-            const CUtensorMap *sm = T.mode == GRAM ? &p.pa : T.mode == SQUARE ? &p.pp : T.mode == APPLY ? &p.px[(T.k + 1) & 1] : &p.po;
-            auto load_piece = [&](int c) {           // lane 0
-                const int slot = (c - c0) & 1;
-                unsigned char *d = slab + slot * SLOT;
-                mbar_arrive_expect_tx(&arrived[slot], two ? SLOT : SLOT / 2);
-                tma_load_3d(d, lm, &arrived[slot], T.n0 + PC * c, m0, T.b);
-                if (two) tma_load_3d(d + SLOT / 2, &p.pl, &arrived[slot], T.n0 + PC * c, m0, T.b);
-                flight |= 1u << slot;
-            };
-            if (loads && c0 < end) {
-                // (the producer has seen the same: this wait orders what this thread loads)
-                if (lane == 0) {
-                    good = ready(T);
-                    if (good && !p.inject)
-                        for (int c = c0; c < end && c < c0 + SLOTS; ++c) load_piece(c);
+            if (lane == 0) {
+                // (what left the buffers for the tile before has left them)
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                if (loads && c0 < end && !p.inject) {
+                    fence_proxy_async_global();
+                    for (int c = c0; c < end; ++c) {
+                        mbar_arrive_expect_tx(&arrived[c - c0], PIECE);
+                        tma_load_3d(slab + (c - c0) * PIECE, T.mode == SQUARE ? &p.pa : &p.pl, &arrived[c - c0], T.n0 + PC * c, m0, T.b);
+                        flight |= 1u << (c - c0);
+                    }
                 }
-                good = __shfl_sync(kFullMask, good, 0);
-                if (!good) break;
+                tell();
             }
+            __syncwarp();
             if (!wait_all(&tfull[b], tph, false)) break;
             tc_fence_after();
             const bool direct = T.mode == LAST && !p.tma_out;
             const float ca = p.c[3 * T.k], cb = p.c[3 * T.k + 1], cc = p.c[3 * T.k + 2] / SA;
+            const CUtensorMap *sm = T.mode == GRAM ? &p.pa : T.mode == SQUARE ? &p.pp : T.mode == APPLY ? &p.px[(T.k + 1) & 1] : &p.po;
 #pragma unroll 1
             for (int c = c0; c < end; ++c) {
-                const int slot = (c - c0) & 1, col = T.n0 + PC * c;
-                unsigned char *buf = slab + slot * SLOT;
+                const int col = T.n0 + PC * c;
+                // (an address in the 64-byte swizzle goes by the lane's row: 16 bytes i of 64)
+                unsigned char *main = slab + (c - c0) * PIECE, *side = slab + (PIECES + ((c - c0) & 1)) * PIECE;
+                auto at = [&](unsigned char *s, int i) -> uint4 * {
+                    return reinterpret_cast<uint4 *>(s + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+                };
                 __syncwarp();
                 if (loads) {
-                    if (!wait_all(&arrived[slot], (pph >> slot) & 1u, false)) { good = false; break; }
-                    pph ^= 1u << slot;
-                    flight &= ~(1u << slot);
-                } else {
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
-                    __syncwarp();
+                    if (!wait_all(&arrived[c - c0], (pph >> (c - c0)) & 1u, false)) { good = false; break; }
+                    pph ^= 1u << (c - c0);
+                    flight &= ~(1u << (c - c0));
                 }
+                // (the side buffer's last group but one has left it)
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                __syncwarp();
                 float v[32];
                 tmem_ld32(tm0 + b * TN + PC * c, v);
-                // 16 bytes of the lane's row, in the 64-byte swizzle
-                auto at = [&](int i) -> uint4 * {
-                    return reinterpret_cast<uint4 *>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
-                };
-                auto at2 = [&](int i) -> uint4 * { return at(i) + SLOT / 2 / 16; };
                 if (T.mode == GRAM) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] *= SA / (SX * SX);
                 } else if (T.mode == SQUARE) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 h = *at(i);
+                        const uint4 h = *at(main, i);
                         const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -460,16 +489,24 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                             v[j + 1] = fmaf(cb, f16_hi(hw[k]), v[j + 1] * cc);
                         }
                     }
+                    if (!mirror) {                   // on the diagonal
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (col + i == row) v[i] = fmaf(ca, SA, v[i]);
+                    }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 h = *at(i), l = *at2(i);
-                        const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+                    for (int i = 0; i < 32; ++i) v[i] *= 1.f / SA;
+                    if (T.mode == APPLY) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int j = 8 * i + 2 * k;
-                            v[j] = fmaf(ca, fmaf(f16_lo(lw[k]), 1.f / SLO, f16_lo(hw[k])), v[j] * (1.f / SA));
-                            v[j + 1] = fmaf(ca, fmaf(f16_hi(lw[k]), 1.f / SLO, f16_hi(hw[k])), v[j + 1] * (1.f / SA));
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 l = *at(main, i);
+                            const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                v[8 * i + 2 * k] = fmaf(ca / SLO, f16_lo(lw[k]), v[8 * i + 2 * k]);
+                                v[8 * i + 2 * k + 1] = fmaf(ca / SLO, f16_hi(lw[k]), v[8 * i + 2 * k + 1]);
+                            }
                         }
                     }
                 }
@@ -481,48 +518,44 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                         for (int i = 0; i < 32; ++i)
                             if (col + i < N) o[i] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * f));
                     }
-                } else {
-                    uint32_t w[16];
-                    if (T.mode == LAST) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = f32x2_to_bf16x2(v[2 * i + 1] * f, v[2 * i] * f);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = f32x2_to_f16x2(v[2 * i + 1], v[2 * i]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) *at(i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                    if (T.mode == APPLY) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t y[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                y[k] = f32x2_to_f16x2((v[8 * i + 2 * k + 1] - f16_hi(w[4 * i + k])) * SLO,
-                                                      (v[8 * i + 2 * k] - f16_lo(w[4 * i + k])) * SLO);
-                            *at2(i) = make_uint4(y[0], y[1], y[2], y[3]);
-                        }
-                    } else if (mirror) {
-                        // row j of the mirror image: this lane's number of column j
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            *reinterpret_cast<uint16_t *>(buf + SLOT / 2 + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2) =
-                                static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    continue;
                 }
+                uint32_t w[16];
+                if (T.mode == LAST) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = f32x2_to_bf16x2(v[2 * i + 1] * f, v[2 * i] * f);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = f32x2_to_f16x2(v[2 * i + 1], v[2 * i]);
+                }
+                unsigned char *first = T.mode == APPLY ? side : main;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) *at(first, i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                if (second) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = f32x2_to_f16x2((v[8 * i + 2 * k + 1] - f16_hi(w[4 * i + k])) * SLO,
+                                                  (v[8 * i + 2 * k] - f16_lo(w[4 * i + k])) * SLO);
+                        *at(main, i) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+                if (mirror) {
+                    // row j of the mirror image: this lane's number of column j
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        *reinterpret_cast<uint16_t *>(side + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2) =
+                            static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    if (!direct) {
-                        tma_store_3d(sm, buf, col, m0, T.b);
-                        if (T.mode == APPLY) tma_store_3d(&p.pl, buf + SLOT / 2, col, m0, T.b);
-                        else if (mirror) tma_store_3d(sm, buf + SLOT / 2, m0, col, T.b);
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    }
-                    if (loads && c + SLOTS < end) {  // the buffer's next piece, once this one has left it
-                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        load_piece(c + SLOTS);
-                    }
+                    tma_store_3d(sm, first, col, m0, T.b);
+                    if (second) tma_store_3d(&p.pl, main, col, m0, T.b);
+                    if (mirror) tma_store_3d(sm, side, m0, col, T.b);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
             if (!good) break;
@@ -530,15 +563,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive_cluster(tempty0 + 8u * b);
-                if (T.mode != LAST) {
-                    // the warp's part of the tile is in global memory: tell who builds on it
-                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-                    fence_proxy_async_global();
-                    __threadfence();
-                    atomicAdd(p.count + T.b, 1u);
-                } else {
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                }
+                if (T.mode != LAST) pending = T.b;
             }
             __syncwarp();
             b ^= 1u;
@@ -546,7 +571,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         }
         if (lane == 0) {
             // pieces still on their way (after a wait that ran out), and the last stores
-            for (int i = 0; i < SLOTS; ++i) {
+            for (int i = 0; i < PIECES; ++i) {
                 int dummy = 0;
                 if (flight >> i & 1u) mbar_wait(&arrived[i], (pph >> i) & 1u, &dummy, nullptr, 20000000ull);
             }
@@ -1152,20 +1177,25 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     a.tall = tall;
     a.steps = f.steps;
     a.B = B; a.m = m; a.R = R; a.C = C;
-    // symmetric results: as many tiles as of 256, of equal sides (a multiple of 32)
-    a.side = (tiles(m, tiles(m, 256)) + 31) / 32 * 32;
+    // Sides of the symmetric results' tiles and widths of X's: multiples of 32 up to 256, those whose tiles
+    // take least.  A tile's fixed part is worth about 32 columns; the tiles of few matrices follow each other
+    // in rounds of the clusters.
+    const auto pick = [&](int n, auto count) {
+        int best = 0;
+        double least = 0;
+        for (int k = tiles(n, 256); k <= 4 * tiles(n, 256); ++k) {
+            const int t = (tiles(n, k) + 31) / 32 * 32;
+            const long long all = static_cast<long long>(B) * count(tiles(n, t));
+            const double rounds = B < 4 || all < most ? static_cast<double>((all + most - 1) / most) : static_cast<double>(all) / most;
+            if (!best || rounds * (t + 32) < least) { least = rounds * (t + 32); best = t; }
+        }
+        return best;
+    };
+    a.side = pick(m, [](long long k) { return k * (k + 1) / 2; });
     a.n_side = tiles(m, a.side);
     a.sym = a.n_side * (a.n_side + 1) / 2;
-    // X: the width (a multiple of 32) whose tiles take least; a tile's fixed part is worth about 32 columns.
-    // Few matrices' products follow each other in rounds of the clusters.
     a.nM = tiles(R, TM);
-    double least = 0;
-    for (int k = tiles(C, 256); k <= 4 * tiles(C, 256); ++k) {
-        const int t = (tiles(C, k) + 31) / 32 * 32;
-        const long long all = static_cast<long long>(B) * a.nM * tiles(C, t);
-        const double rounds = B < 4 || all < most ? static_cast<double>((all + most - 1) / most) : static_cast<double>(all) / most;
-        if (!a.tn || rounds * (t + 32) < least) { least = rounds * (t + 32); a.tn = t; }
-    }
+    a.tn = pick(C, [&](long long k) { return k * a.nM; });
     a.nN = tiles(C, a.tn);
     a.app = a.nM * a.nN;
     const long long units = static_cast<long long>(f.steps) * B * (2 * a.sym + a.app);
