@@ -561,23 +561,39 @@ def moe_dispatch_backward(dXp, slot_pos, dres, dX, stream=None):
 
 
 _NORMS = {"none": 0, "layer": 1, "rms": 2}
-_RESIDUAL_SCALARS = ("post", "pre", "alpha", "eps_post", "eps_pre")
-_RESIDUAL_COLUMNS = ("gamma_post", "beta_post", "gate", "gate_token", "gamma_pre", "beta_pre")
+_COLUMN_KEYS = frozenset(("gamma_post", "beta_post", "gate", "gate_token", "gamma_pre", "beta_pre"))
+_RESIDUAL_KEYS = _COLUMN_KEYS | {"post", "pre", "alpha", "eps_post", "eps_pre"}
 
 
-def _column_specs(d, T, H, scalars=(), prefix=""):
-    for n in d:
-        if n not in _RESIDUAL_COLUMNS and n not in scalars:
-            raise ValueError(f"{prefix}{n}: unknown, expected some of {_RESIDUAL_COLUMNS}")
-    for n in ("post", "pre"):
-        if d.get(n, "none") not in _NORMS:
-            raise ValueError(f"{n}: {d[n]}, expected one of {tuple(_NORMS)}")
-    return [(d.get(n), F32, T if n == "gate_token" else H, prefix + n) for n in _RESIDUAL_COLUMNS]
+def _param_specs(p, T, H):
+    """Specs of a joined residual's parameters for _ptrs."""
+    if not _RESIDUAL_KEYS.issuperset(p):
+        raise ValueError(f"{next(n for n in p if n not in _RESIDUAL_KEYS)}: unknown, expected some of {sorted(_RESIDUAL_KEYS)}")
+    get = p.get
+    return ((get("gamma_post"), F32, H, "gamma_post"), (get("beta_post"), F32, H, "beta_post"), (get("gate"), F32, H, "gate"),
+            (get("gate_token"), F32, T, "gate_token"), (get("gamma_pre"), F32, H, "gamma_pre"),
+            (get("beta_pre"), F32, H, "beta_pre"))
 
 
-def _residual(p, columns):
-    return MoeResidual(_NORMS[p.get("post", "none")], _NORMS[p.get("pre", "none")], float(p.get("alpha", 1.0)),
-                       float(p.get("eps_post", 1e-5)), float(p.get("eps_pre", 1e-5)), *columns)
+def _grad_specs(g, T, H):
+    if not _COLUMN_KEYS.issuperset(g):
+        raise ValueError(f"{next(n for n in g if n not in _COLUMN_KEYS)}: unknown gradient, expected some of {sorted(_COLUMN_KEYS)}")
+    get = g.get
+    return ((get("gamma_post"), F32, H, "gradient of gamma_post"), (get("beta_post"), F32, H, "gradient of beta_post"),
+            (get("gate"), F32, H, "gradient of gate"), (get("gate_token"), F32, T, "gradient of gate_token"),
+            (get("gamma_pre"), F32, H, "gradient of gamma_pre"), (get("beta_pre"), F32, H, "gradient of beta_pre"))
+
+
+def _norm_kind(p, name):
+    kind = p.get(name, "none")
+    if kind not in _NORMS:
+        raise ValueError(f"{name}: {kind}, expected one of {tuple(_NORMS)}")
+    return _NORMS[kind]
+
+
+def _residual(p, post, pre, columns):
+    get = p.get
+    return ctypes.byref(MoeResidual(post, pre, get("alpha", 1.0), get("eps_post", 1e-5), get("eps_pre", 1e-5), *columns))
 
 
 def moe_residual_norm(x, y, p, r, n=None, stats=None, stream=None):
@@ -585,12 +601,12 @@ def moe_residual_norm(x, y, p, r, n=None, stats=None, stream=None):
     eps_post, eps_pre (default 1e-5) and the fp32 parameters gamma_post, beta_post, gate, gamma_pre,
     beta_pre [H] and gate_token [T], each of which may be missing or None."""
     T, H = x.shape
-    fx, fy = _fp32_flag(x, "x"), _fp32_flag(y, "y")
+    fx, fy, post, pre, k = _fp32_flag(x, "x"), _fp32_flag(y, "y"), _norm_kind(p, "post"), _norm_kind(p, "pre"), T * H
     xp, yp, rp, np_, sp, *cols = _ptrs(
-        (x, x.dtype, T * H, "x"), (y, y.dtype, T * H, "y"), (r, x.dtype, T * H, "r"), (n, BF16, T * H, "n"),
-        (stats, F32, 4 * T, "stats"), *_column_specs(p, T, H, _RESIDUAL_SCALARS))
-    _check("moe_residual_norm", load().moe_residual_norm(xp, fx, yp, fy, ctypes.byref(_residual(p, cols)), T, H, rp,
-                                                         np_, sp, _stream(stream)))
+        (x, x.dtype, k, "x"), (y, y.dtype, k, "y"), (r, x.dtype, k, "r"), (n, BF16, k, "n"),
+        (stats, F32, 4 * T, "stats"), *_param_specs(p, T, H))
+    _check("moe_residual_norm", load().moe_residual_norm(xp, fx, yp, fy, _residual(p, post, pre, cols), T, H, rp, np_, sp,
+                                                         _stream(stream)))
 
 
 def moe_residual_norm_backward_workspace_bytes(T: int, H: int) -> int:
@@ -601,13 +617,14 @@ def moe_residual_norm_backward(dn, dr, y, r, stats, p, dx, dy, grads, ws, stream
     """p as in the forward call; grads: dict of the wanted parameters' gradients by the
     parameters' names.  dn (without pre), dr, y and r (see the header) may be None."""
     T, H = dx.shape
-    fx, fy = _fp32_flag(dx, "dx"), 0 if y is None else _fp32_flag(y, "y")
+    fx, fy, post, pre = _fp32_flag(dx, "dx"), 0 if y is None else _fp32_flag(y, "y"), _norm_kind(p, "post"), _norm_kind(p, "pre")
+    k, xt = T * H, dx.dtype
     d, e, yp, rp, sp, dxp, dyp, *cols = _ptrs(
-        (dn, BF16, T * H, "dn"), (dr, dx.dtype, T * H, "dr"), (y, F32 if fy else BF16, T * H, "y"),
-        (r, dx.dtype, T * H, "r"), (stats, F32, 4 * T, "stats"), (dx, dx.dtype, T * H, "dx"), (dy, BF16, T * H, "dy"),
-        *_column_specs(p, T, H, _RESIDUAL_SCALARS), *_column_specs(grads, T, H, prefix="gradient of "))
+        (dn, BF16, k, "dn"), (dr, xt, k, "dr"), (y, F32 if fy else BF16, k, "y"), (r, xt, k, "r"),
+        (stats, F32, 4 * T, "stats"), (dx, xt, k, "dx"), (dy, BF16, k, "dy"), *_param_specs(p, T, H),
+        *_grad_specs(grads, T, H))
     _check("moe_residual_norm_backward", load().moe_residual_norm_backward(
-        d, e, yp, fy, rp, fx, sp, ctypes.byref(_residual(p, cols[:6])), T, H, dxp, dyp,
+        d, e, yp, fy, rp, fx, sp, _residual(p, post, pre, cols[:6]), T, H, dxp, dyp,
         ctypes.byref(MoeResidualGrads(*cols[6:])), *_ws(ws), _stream(stream)))
 
 

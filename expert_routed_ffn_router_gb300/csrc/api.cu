@@ -30,7 +30,7 @@ cudaError_t ensure_smem(const void *func, size_t bytes)
     // small table of (function, device) -> largest limit set so far; host threads making
     // their first calls at the same time share it, hence the lock
     struct Entry { const void *f; int dev; size_t bytes; };
-    static Entry tab[64];
+    static Entry tab[512];
     static int n = 0;
     static std::mutex mu;
     // 48 KB need no attribute, a kernel's static arrays among them (at most 8 KB)
@@ -46,7 +46,7 @@ cudaError_t ensure_smem(const void *func, size_t bytes)
     if (e != cudaSuccess) return e;
     for (int i = 0; i < n; ++i)
         if (tab[i].f == func && tab[i].dev == dev) { tab[i].bytes = bytes; return cudaSuccess; }
-    if (n < 64) tab[n++] = Entry{func, dev, bytes};
+    if (n < 512) tab[n++] = Entry{func, dev, bytes};
     return cudaSuccess;
 }
 
