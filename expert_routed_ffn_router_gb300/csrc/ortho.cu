@@ -8,8 +8,9 @@
 // (a I + P): A and P are symmetric, so the matrices stay as they lie).  A step's polynomial a s + b s^3 +
 // c s^5 acts on every singular value s of X.
 //
-// Launches: the momentum, partial square sums; X from them; one persistent launch over all steps' products,
-// a list of tiles claimed in order:
+// Launches: the size of u from a sample; the momentum, u as two fp16 numbers at the power of two that the
+// sample gives, and its norm (what is left of it, a factor near 1, goes into the first step); one
+// persistent launch over all steps' products, a list of tiles claimed in order:
 //   gram     A: the tiles on and below the diagonal, each stored twice (the mirror image too)
 //   square   a I + P: likewise, with a I + b A added as the tile leaves tensor memory
 //   apply    X: the product of a I + P and X, the last step's into `out`
@@ -81,6 +82,7 @@ struct Args {
     float c[3 * MAX_STEPS];
     float scale;
     uint16_t *out;                // bf16 [B][R][C]
+    const float *rest;            // [B] what the first X still has to be multiplied by
     unsigned *count;              // [B] epilogue warps that are done with a tile (zeroed)
     int *next;                    // the next tile to be claimed (zeroed)
     int *status;
@@ -453,7 +455,9 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             if (!wait_all(&tfull[b], tph, false)) break;
             tc_fence_after();
             const bool direct = T.mode == LAST && !p.tma_out;
+            const float rest = T.k == 0 ? p.rest[T.b] : 1.f;
             const float ca = p.c[3 * T.k], cb = p.c[3 * T.k + 1], cc = p.c[3 * T.k + 2] / SA;
+            const float gram = SA / (SX * SX) * rest * rest, apply = rest / SA, again = ca / SLO * rest;
             const CUtensorMap *sm = T.mode == GRAM ? &p.pa : T.mode == SQUARE ? &p.pp : T.mode == APPLY ? &p.px[(T.k + 1) & 1] : &p.po;
 #pragma unroll 1
             for (int c = c0; c < end; ++c) {
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 tmem_ld32(tm0 + b * TN + PC * c, v);
                 if (T.mode == GRAM) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= SA / (SX * SX);
+                    for (int i = 0; i < 32; ++i) v[i] *= gram;
                 } else if (T.mode == SQUARE) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= 1.f / SA;
+                    for (int i = 0; i < 32; ++i) v[i] *= apply;
                     if (T.mode == APPLY) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -504,8 +508,8 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                             const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                v[8 * i + 2 * k] = fmaf(ca / SLO, f16_lo(lw[k]), v[8 * i + 2 * k]);
-                                v[8 * i + 2 * k + 1] = fmaf(ca / SLO, f16_hi(lw[k]), v[8 * i + 2 * k + 1]);
+                                v[8 * i + 2 * k] = fmaf(again, f16_lo(lw[k]), v[8 * i + 2 * k]);
+                                v[8 * i + 2 * k + 1] = fmaf(again, f16_hi(lw[k]), v[8 * i + 2 * k + 1]);
                             }
                         }
                     }
@@ -605,6 +609,8 @@ struct Prepare {
     float4 *part;                     // [B][parts]: square sums at three scales
     uint16_t *hi, *lo;                // [B][R][ld]
     unsigned *count;                  // [B] and the next tile to be claimed: zeroed here
+    float2 *size;                     // [B] the sample's factor, in two
+    float *rest;                      // [B] what X's numbers still have to be multiplied by
 };
 
 template <bool VEC>
@@ -665,21 +671,96 @@ __device__ __forceinline__ float x_factor(float s0, float s1, float s2, float &f
     return s > 0.f ? (s <= 3.402823466e38f ? SX / sqrtf(s) : s - s) : s;
 }
 
-// VEC: R C and C are multiples of 8.  CTA (part, matrix): the momentum, and the chunk's square sums.
+// Sums over the CTA's PT threads (and the largest d) to all of them
+__device__ __forceinline__ float4 cta_sums(float a, float b, float c, float d)
+{
+    __shared__ float4 red[PT / 32];
+    a = warp_sum(a); b = warp_sum(b); c = warp_sum(c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d = fmaxf(d, __shfl_xor_sync(kFullMask, d, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float4(a, b, c, d);
+    __syncthreads();
+    float4 t = red[0];
+    for (int k = 1; k < PT / 32; ++k) t = make_float4(t.x + red[k].x, t.y + red[k].y, t.z + red[k].z, fmaxf(t.w, red[k].w));
+    return t;
+}
+
+__device__ __forceinline__ void add_squares(float u, float &s0, float &s1, float &s2)
+{
+    s0 = fmaf(u, u, s0);
+    const float a = u * UP, b = u * DOWN;
+    s1 = fmaf(a, a, s1);
+    s2 = fmaf(b, b, s2);
+}
+
+// CTA a matrix: a power of two that brings u to the size of SX X, by SAMPLE of its entries.
+constexpr int SAMPLE = 8 * PT;
+__global__ void __launch_bounds__(PT) ortho_sample_kernel(const Prepare p)
+{
+    pdl_wait();
+    const unsigned long long n = static_cast<unsigned long long>(p.R) * p.C;
+    const size_t base = static_cast<size_t>(blockIdx.x) * n;
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < SAMPLE / PT; ++k) {
+        // (multiples of the golden ratio, modulo 1: even over the matrix, no row or column preferred)
+        const size_t i = base + __umul64hi((k * PT + threadIdx.x + 1) * 0x9E3779B97F4A7C15ull, n);
+        float u[1];
+        load_g<false>(p, i, u);
+        if (p.m) {
+            const float m = fmaf(p.mu, p.m[i], u[0]);
+            u[0] = p.nesterov ? fmaf(p.mu, m, u[0]) : m;
+        }
+        add_squares(u[0], s0, s1, s2);
+    }
+    const float4 t = cta_sums(s0, s1, s2, 0.f);
+    if (threadIdx.x != 0) return;
+    float f;
+    const float inv = x_factor(t.x, t.y, t.z, f) * sqrtf(static_cast<float>(SAMPLE) / static_cast<float>(n));   // SX / |u f|
+    int e = 0, g = 0;
+    if (inv > 0.f && inv <= 3.402823466e38f) {
+        frexpf(inv, &e);
+        frexpf(f, &g);
+        e += g - 2;
+    }
+    e = max(-200, min(200, e));
+    p.size[blockIdx.x] = make_float2(pow2f(e / 2), pow2f(e - e / 2));
+    p.count[blockIdx.x] = 0;
+    if (blockIdx.x == 0) p.count[gridDim.x] = 0;
+}
+
+// N numbers from `at` on as two fp16 numbers each
+template <int N>
+__device__ __forceinline__ void store_numbers(const Prepare &p, size_t at, const float (&v)[N])
+{
+    if constexpr (N == 8) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = f32x2_to_f16x2(v[2 * k + 1], v[2 * k]);
+            l[k] = f32x2_to_f16x2((v[2 * k + 1] - f16_hi(h[k])) * SLO, (v[2 * k] - f16_lo(h[k])) * SLO);
+        }
+        *reinterpret_cast<uint4 *>(p.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(p.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    } else {
+        const uint32_t h = f32x2_to_f16x2(0.f, v[0]);
+        p.hi[at] = static_cast<uint16_t>(h);
+        p.lo[at] = static_cast<uint16_t>(f32x2_to_f16x2(0.f, (v[0] - f16_lo(h)) * SLO));
+    }
+}
+
+// VEC: R C and C are multiples of 8.  CTA (part, matrix): the momentum, u times the sample's factor, and the
+// chunk's square sums.
 template <bool VEC>
 __global__ void __launch_bounds__(PT) ortho_momentum_kernel(const Prepare p)
 {
     constexpr int N = Elements<VEC>::N;
-    __shared__ float red[3][PT / 32];
     pdl_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        p.count[blockIdx.y] = 0;
-        if (blockIdx.y == 0) p.count[gridDim.y] = 0;
-    }
     const long long n = static_cast<long long>(p.R) * p.C;
     const size_t base = static_cast<size_t>(blockIdx.y) * n;
     const long long lo = blockIdx.x * p.chunk, hi = min(n, lo + p.chunk);
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f;
+    const float2 size = p.size[blockIdx.y];
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, most = 0.f;
     for (long long i = lo + threadIdx.x * N; i < hi; i += PT * N) {
         float u[N];
         load_g<VEC>(p, base + i, u);
@@ -699,44 +780,41 @@ __global__ void __launch_bounds__(PT) ortho_momentum_kernel(const Prepare p)
                 p.m[base + i] = m[0];
             }
         }
+        float v[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            s0 = fmaf(u[k], u[k], s0);
-            const float a = u[k] * UP, b = u[k] * DOWN;
-            s1 = fmaf(a, a, s1);
-            s2 = fmaf(b, b, s2);
+            add_squares(u[k], s0, s1, s2);
+            v[k] = u[k] * size.x * size.y;
+            most = fmaxf(most, fabsf(v[k]));
         }
+        const int r = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(r) * p.C);
+        store_numbers(p, (static_cast<size_t>(blockIdx.y) * p.R + r) * p.ld + c, v);
     }
-    s0 = warp_sum(s0); s1 = warp_sum(s1); s2 = warp_sum(s2);
-    const int w = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) { red[0][w] = s0; red[1][w] = s1; red[2][w] = s2; }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int k = 1; k < PT / 32; ++k) { s0 += red[0][k]; s1 += red[1][k]; s2 += red[2][k]; }
-        p.part[static_cast<size_t>(blockIdx.y) * p.parts + blockIdx.x] = make_float4(s0, s1, s2, 0.f);
-    }
+    const float4 t = cta_sums(s0, s1, s2, most);
+    if (threadIdx.x == 0) p.part[static_cast<size_t>(blockIdx.y) * p.parts + blockIdx.x] = t;
 }
 
-// CTA (part, matrix): X = u / |u| of the chunk, as two fp16 numbers.
+// CTA (part, matrix): the factor that is left.  Where the sample was so far off that X's numbers have left
+// fp16's range or come near its end, the chunk's are made again.
 template <bool VEC>
 __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
 {
     constexpr int N = Elements<VEC>::N;
-    __shared__ float red[3][PT / 32];
     pdl_wait();
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f;
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, most = 0.f;
     for (int k = threadIdx.x; k < p.parts; k += PT) {
         const float4 v = p.part[static_cast<size_t>(blockIdx.y) * p.parts + k];
         s0 += v.x; s1 += v.y; s2 += v.z;
+        most = fmaxf(most, v.w);
     }
-    s0 = warp_sum(s0); s1 = warp_sum(s1); s2 = warp_sum(s2);
-    const int w = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) { red[0][w] = s0; red[1][w] = s1; red[2][w] = s2; }
-    __syncthreads();
-    s0 = s1 = s2 = 0.f;
-    for (int k = 0; k < PT / 32; ++k) { s0 += red[0][k]; s1 += red[1][k]; s2 += red[2][k]; }
+    const float4 t = cta_sums(s0, s1, s2, most);
+    const float2 size = p.size[blockIdx.y];
     float f;
-    const float inv = x_factor(s0, s1, s2, f);
+    const float inv = x_factor(t.x, t.y, t.z, f), rest = inv * (f / size.x) / size.y;
+    // (a matrix of zeros: 0; one that holds a NaN or an infinity: NaN)
+    const bool far = inv > 0.f && !(rest >= 1.f / 16 && rest <= 16.f && t.w <= 60000.f);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.rest[blockIdx.y] = far ? 1.f : (inv > 0.f ? rest : inv);
+    if (!far) return;
     const long long n = static_cast<long long>(p.R) * p.C;
     const size_t base = static_cast<size_t>(blockIdx.y) * n;
     const long long lo = blockIdx.x * p.chunk, hi = min(n, lo + p.chunk);
@@ -749,24 +827,10 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
 #pragma unroll
             for (int k = 0; k < N; ++k) u[k] = p.nesterov ? fmaf(p.mu, m[k], u[k]) : m[k];
         }
-        const int r = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(r) * p.C);
-        const size_t at = (static_cast<size_t>(blockIdx.y) * p.R + r) * p.ld + c;
-        if constexpr (VEC) {
-            uint32_t h[4], l[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float a = u[2 * k] * f * inv, b = u[2 * k + 1] * f * inv;
-                h[k] = f32x2_to_f16x2(b, a);
-                l[k] = f32x2_to_f16x2((b - f16_hi(h[k])) * SLO, (a - f16_lo(h[k])) * SLO);
-            }
-            *reinterpret_cast<uint4 *>(p.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(p.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
-        } else {
-            const float a = u[0] * f * inv;
-            const uint32_t h = f32x2_to_f16x2(0.f, a);
-            p.hi[at] = static_cast<uint16_t>(h);
-            p.lo[at] = static_cast<uint16_t>(f32x2_to_f16x2(0.f, (a - f16_lo(h)) * SLO));
-        }
+        for (int k = 0; k < N; ++k) u[k] = u[k] * f * inv;
+        const int r = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(r) * p.C);
+        store_numbers(p, (static_cast<size_t>(blockIdx.y) * p.R + r) * p.ld + c, u);
     }
 }
 
@@ -867,7 +931,7 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
                 make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     };
 
-    // u to tensor memory, and its square sums (see ortho_momentum_kernel).  A tall matrix passes through
+    // u to tensor memory, and its square sums (see UP).  A tall matrix passes through
     // shared memory, 128 of its rows (columns of X) at a time: [column][128 + 4 rows] of fp32.
     float s0 = 0.f, s1 = 0.f, s2 = 0.f;
     float *turn = reinterpret_cast<float *>(sx);
@@ -904,12 +968,7 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
             }
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            s0 = fmaf(v[i], v[i], s0);
-            const float a = v[i] * UP, b = v[i] * DOWN;
-            s1 = fmaf(a, a, s1);
-            s2 = fmaf(b, b, s2);
-        }
+        for (int i = 0; i < 32; ++i) add_squares(v[i], s0, s1, s2);
         __syncwarp();
         tmem_st32(tm0 + c, v);
     }
@@ -1101,7 +1160,7 @@ int up8(int n) { return (n + 7) & ~7; }
 struct Layout {
     int m, ld, ldm, parts;
     long long chunk;
-    size_t count, part, hi[2], lo, A, P, bytes;
+    size_t count, size, rest, part, hi[2], lo, A, P, bytes;
 };
 Layout layout(int B, int R, int C)
 {
@@ -1119,6 +1178,8 @@ Layout layout(int B, int R, int C)
     auto take = [&](size_t b) { const size_t at = o; o += al256(b); return at; };
     const size_t x = static_cast<size_t>(B) * R * L.ld * 2, a = static_cast<size_t>(B) * L.m * L.ldm * 2;
     L.count = take((static_cast<size_t>(B) + 1) * sizeof(unsigned));
+    L.size = take(static_cast<size_t>(B) * sizeof(float2));
+    L.rest = take(static_cast<size_t>(B) * sizeof(float));
     L.part = take(static_cast<size_t>(B) * L.parts * sizeof(float4));
     L.hi[0] = take(x);
     L.hi[1] = take(x);
@@ -1141,7 +1202,8 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     unsigned char *w = static_cast<unsigned char *>(scratch);
     Prepare q{f.g, f.g_fp32, f.momentum, f.mu, f.nesterov, R, C, L.ld, L.chunk, L.parts,
               reinterpret_cast<float4 *>(w + L.part), reinterpret_cast<uint16_t *>(w + L.hi[0]),
-              reinterpret_cast<uint16_t *>(w + L.lo), reinterpret_cast<unsigned *>(w + L.count)};
+              reinterpret_cast<uint16_t *>(w + L.lo), reinterpret_cast<unsigned *>(w + L.count),
+              reinterpret_cast<float2 *>(w + L.size), reinterpret_cast<float *>(w + L.rest)};
     const bool vec = C % 8 == 0;
     const bool tall = R > C;             // the smaller side is the columns
     const int m = L.m, n = tall ? R : C;
@@ -1164,6 +1226,7 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
         return launch_pdl(kernel, dim3(B), dim3(ST), smem, s, 1, p);
     }
     const dim3 grid(L.parts, B);
+    if ((e = launch_pdl(ortho_sample_kernel, dim3(B), dim3(PT), 0, s, 1, q)) != cudaSuccess) return e;
     e = launch_pdl(vec ? ortho_momentum_kernel<true> : ortho_momentum_kernel<false>, grid, dim3(PT), 0, s, 1, q);
     if (e != cudaSuccess) return e;
     e = launch_pdl(vec ? ortho_scale_kernel<true> : ortho_scale_kernel<false>, grid, dim3(PT), 0, s, 1, q);
@@ -1205,6 +1268,7 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     memcpy(a.c, f.coeffs, 3 * f.steps * sizeof(float));
     a.scale = f.scale;
     a.out = static_cast<uint16_t *>(f.out);
+    a.rest = q.rest;
     a.count = q.count;
     a.next = reinterpret_cast<int *>(q.count + B);
     a.status = status;

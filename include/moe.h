@@ -569,12 +569,13 @@ int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, in
  *   g        [B, R, C], bf16 (g_fp32 == 0) or fp32 (g_fp32 == 1)
  *   momentum fp32 [B, R, C], updated, or NULL (then mu is not read and nesterov must be 0)
  *   coeffs   HOST array [steps][3] of a, b, c, read during the call, or NULL: 3.4445, -4.7750,
- *            2.0315 in every step.  The iterates' singular values must stay below 8.
+ *            2.0315 in every step.  The iterates' singular values s must stay below 8, and |a| +
+ *            |b| s^2 + |c| s^4 below 120 (fp16's range).
  *   out      bf16 [B, R, C] (may be g's own memory where g is bf16)
  *   ws       at least moe_orthogonalize_workspace_bytes(B, R, C) bytes (0 for an invalid shape):
  *            about B (6 R C + 4 min(R, C)^2) bytes
  * fp16 products with fp32 sums on the tensor cores; X is carried in 22 bits, so that directions with
- * small singular values keep their precision; results are 0.2e-3 to 1.8e-3 off (2-norm) before
+ * small singular values keep their precision; results are 0.3e-3 to 1.8e-3 off (2-norm) before
  * out's rounding.  A matrix of zeros gives zeros; one with an infinity or a NaN gives NaN.  The
  * results repeat bit for bit.  R, C <= 32768, B <= 65535, steps <= 32 (else
  * MOE_ERR_UNSUPPORTED_SHAPE); any R and C from 1 on.  B == 0 enqueues nothing. */
