@@ -16,7 +16,8 @@
 //   apply    X: the product of a I + P and X, the last step's into `out`
 // A matrix's tiles of one product start when those of the one before are stored (a counter a matrix);
 // they come earlier in the list, so whoever waits holds nothing that they need.  Other matrices' tiles
-// fill the gaps.  (A launch for each product: @LAUNCHES@.)
+// fill the gaps.  (With a launch for each product: 6.9 ms for 16 matrices of 7168 x 2048, 1.42 ms for 24 of
+// 2112 x 1088; with this 6.7 and 1.34 ms.)
 //
 // Numbers.  The products take fp16 operands (11 bits; entries of X are at most 1.2 and typically
 // (rows columns)^-1/2, so a fixed power of two keeps them normal) with fp32 sums.  What is carried
@@ -33,7 +34,11 @@
 // stages of 32 KB a CTA, two accumulators in tensor memory, eight epilogue warps, all waits
 // bounded (MOE_ERR_DEVICE_TIMEOUT in the status word).
 //
-// What bounds it: @BOUND@
+// What bounds it: large matrices the tensor cores (16 of 7168 x 2048: 5.2 ms in the products of one call,
+// 1610 TFLOP/s with the diagonal tiles computed whole; 5.8 ms in calls one after the other, under the power
+// cap, where the measured library rate is 1.05 of that) and 0.53 ms of memory before them; 24 of 2112 x 1088:
+// 1.06 ms in the products, tiles of 17 stages and the shared memory's loads from L2 (13 TB/s); few
+// matrices: 7 us a product, in turn.
 #include <cuda.h>
 
 #include <cstring>
@@ -835,17 +840,19 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
 }
 
 // ---------------------------------------------------------------------- small matrices
-// A CTA a matrix of up to 128 on the smaller side and 384 on the larger one, all steps in one launch:
-// X as the products' operand (fp16), A and P in shared memory, X itself (fp32) in tensor memory,
-// times a SA: the product with P is added to it there.  (The launches for large ones take 100 us for
-// 16 matrices of 256 x 128, this one @SMALL@.)
-constexpr int SM_SIDE = 128, SM_LONG = 384;
+// Matrices of up to 128 on the smaller side and 3072 on the larger one: a cluster of CL CTAs a matrix, each
+// with up to 384 columns of X, all steps in one launch.  X as the products' operand (fp16), A and P lie
+// in shared memory, X itself (fp32) in tensor memory, times a SA: the product with P is added to it there.
+// With several CTAs, each takes the sums of a part of A's rows from all of them and gives it to all: two
+// barriers of the cluster a step.  (16 matrices of 256 x 128: 100 us with the launches for large ones, 27 us
+// with this; one of 128 x 1000: 116 and 43 us; 76 of 128 x 1536: 303 and 174 us.)
+constexpr int SM_SIDE = 128, SM_LONG = 384, SM_CTAS = 8;
 constexpr int ST = 512;               // threads: four warps for each 32 rows, which share the columns
 constexpr int CHUNK = 128 * 128;      // 128 rows x 64 fp16
 
 struct Small {
     Prepare q;
-    int tall, m, n, np;               // sides of X (m <= n), n up to a multiple of 64
+    int tall, m, n, np;               // sides of X (m <= n), columns of a CTA (a multiple of 64)
     int steps;
     float c[3 * MAX_STEPS];
     float scale;
@@ -891,7 +898,14 @@ __device__ __forceinline__ void small_load(const Prepare &q, size_t i, float (&u
     }
 }
 
-template <bool VEC>
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+template <bool VEC, int CL>
 __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constant__ Small p)
 {
     constexpr uint32_t TCOLS = 512, TD = SM_LONG;    // X, then the sums of A and A A
@@ -899,9 +913,11 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
     unsigned char *sx = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *sa = sx + p.np / 64 * CHUNK, *sp = sa + 2 * CHUNK;
+    unsigned char *part = sp + 2 * CHUNK;            // CL > 1: this CTA's sums of A, fp32 [128][128]
     __shared__ uint64_t done;
     __shared__ uint32_t tmem_slot;
     __shared__ float red[3][ST / 32];
+    __shared__ __align__(16) float total[4];
     __shared__ int abort_s;
     volatile int *abort_flag = &abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -922,7 +938,9 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
     // this thread's row, and its columns: 32 from `col` on of every 128
     const int q = warp & 3, col = 32 * (warp >> 2), row = 32 * q + lane;
     const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    const size_t base = static_cast<size_t>(blockIdx.x) * p.m * p.n;
+    const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int x0 = rank * p.np, own = max(0, min(p.np, p.n - x0));   // this CTA's columns of X
+    const size_t base = static_cast<size_t>(blockIdx.x / CL) * p.m * p.n;
     // 32 numbers of the thread's row, from column c of an operand of 64-column chunks
     auto put = [&](unsigned char *s, int c, const uint32_t (&w)[16]) {
 #pragma unroll
@@ -942,9 +960,9 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
             const int per = p.m / N;
             for (int i = tid; i < 128 * per; i += ST) {
                 const int r = i / per, k = (i - r * per) * N;
-                if (c0 + r >= p.n) break;
+                if (c0 + r >= own) break;
                 float u[N];
-                small_load<VEC>(p.q, base + static_cast<size_t>(c0 + r) * p.m + k, u);
+                small_load<VEC>(p.q, base + static_cast<size_t>(x0 + c0 + r) * p.m + k, u);
 #pragma unroll
                 for (int j = 0; j < N; ++j) turn[r * PITCH + k + j] = u[j];
             }
@@ -955,14 +973,14 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
         float v[32];
         if (p.tall) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = row < p.m && c + i < p.n ? turn[(col + i) * PITCH + row] : 0.f;
+            for (int i = 0; i < 32; ++i) v[i] = row < p.m && c + i < own ? turn[(col + i) * PITCH + row] : 0.f;
         } else {
 #pragma unroll
             for (int i = 0; i < 32 / N; ++i) {
                 float u[N];
 #pragma unroll
                 for (int k = 0; k < N; ++k) u[k] = 0.f;
-                if (row < p.m && c + N * i < p.n) small_load<VEC>(p.q, base + static_cast<size_t>(row) * p.n + c + N * i, u);
+                if (row < p.m && c + N * i < own) small_load<VEC>(p.q, base + static_cast<size_t>(row) * p.n + x0 + c + N * i, u);
 #pragma unroll
                 for (int k = 0; k < N; ++k) v[N * i + k] = u[k];
             }
@@ -978,9 +996,21 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
     __syncthreads();
     s0 = s1 = s2 = 0.f;
     for (int k = 0; k < ST / 32; ++k) { s0 += red[0][k]; s1 += red[1][k]; s2 += red[2][k]; }
+    if (CL > 1) {
+        if (tid == 0) { total[0] = s0; total[1] = s1; total[2] = s2; total[3] = 0.f; }
+        __syncwarp();
+        cluster_sync();
+        s0 = s1 = s2 = 0.f;
+        for (int r = 0; r < CL; ++r) {
+            const float4 t = ld_cluster(mapa_shared(smem_u32(total), r));
+            s0 += t.x; s1 += t.y; s2 += t.z;
+        }
+    }
     float f;
     const float inv = x_factor(s0, s1, s2, f);
 
+    // (Several CTAs: every one goes through all steps, whatever it waited for in vain, so that they meet at
+    // the barriers.)
     uint32_t ph = 0;
     bool good = true;
     // every MMA since the last call is done: its sums may be read, its operands overwritten
@@ -1028,35 +1058,35 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
                 continue;
             }
             if (row >= p.m) continue;
-            uint16_t *to = p.out + base + static_cast<size_t>(row) * p.n + c;
+            uint16_t *to = p.out + base + static_cast<size_t>(row) * p.n + x0 + c;
             if constexpr (VEC) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (c + 8 * i < p.n)
+                    if (c + 8 * i < own)
                         reinterpret_cast<uint4 *>(to)[i] =
                             make_uint4(f32x2_to_bf16x2(v[8 * i + 1] * o, v[8 * i] * o), f32x2_to_bf16x2(v[8 * i + 3] * o, v[8 * i + 2] * o),
                                        f32x2_to_bf16x2(v[8 * i + 5] * o, v[8 * i + 4] * o), f32x2_to_bf16x2(v[8 * i + 7] * o, v[8 * i + 6] * o));
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    if (c + i < p.n) to[i] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * o));
+                    if (c + i < own) to[i] = static_cast<uint16_t>(f32x2_to_bf16x2(0.f, v[i] * o));
             }
         }
         if (last && p.tall) {
             __syncthreads();
             const int per = p.m / N;
             const uint16_t *from = reinterpret_cast<const uint16_t *>(sx);
-            for (int i = tid; i < p.n * per; i += ST) {
+            for (int i = tid; i < own * per; i += ST) {
                 const int r = i / per, k = (i - r * per) * N;
-                uint16_t *to = p.out + base + static_cast<size_t>(r) * p.m + k;
+                uint16_t *to = p.out + base + static_cast<size_t>(x0 + r) * p.m + k;
                 if constexpr (VEC) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + r * 136 + k);
                 else *to = from[r * 136 + k];
             }
         }
         if (last) break;
         in_place();
-        if (!good) break;
-        if (issuer) {                                // A = X X^T
+        if (CL == 1 && !good) break;
+        if (issuer && good) {                        // A = X X^T
             const uint32_t id = idesc_f16_f32(128, 128, false, false);
             for (int i = 0; i < p.np / 16; ++i) {
                 const uint64_t d = smem_desc_sw128(ux + (i >> 2) * CHUNK + (i & 3) * 32, 16, 1024);
@@ -1068,12 +1098,46 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
         uint32_t a[16];                              // A, of the thread's row and columns
         float v[32];
         tmem_ld32(tm0 + TD + col, v);
+        if (CL == 1) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] = f32x2_to_f16x2(v[2 * i + 1] * (SA / (SX * SX)), v[2 * i] * (SA / (SX * SX)));
-        put(sa, col, a);
+            for (int i = 0; i < 16; ++i) a[i] = f32x2_to_f16x2(v[2 * i + 1] * (SA / (SX * SX)), v[2 * i] * (SA / (SX * SX)));
+            put(sa, col, a);
+        } else {
+            // vector j of 4 columns of a row lies at j ^ row (modulo 32)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4 *>(part + row * 512 + (((col / 4 + i) ^ (row & 31)) << 4)) =
+                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            __syncwarp();
+            cluster_sync();
+#pragma unroll
+            for (int j = 0; j < 128 / CL * 32 / ST; ++j) {
+                const int r = rank * (128 / CL) + j * (ST / 32) + warp;      // a row of this CTA's, vector `lane`
+                const uint32_t at = smem_u32(part) + r * 512 + ((lane ^ (r & 31)) << 4);
+                float4 t[CL];
+#pragma unroll
+                for (int k2 = 0; k2 < CL; ++k2) t[k2] = ld_cluster(mapa_shared(at, k2));
+#pragma unroll
+                for (int k2 = 1; k2 < CL; ++k2) t[0] = make_float4(t[0].x + t[k2].x, t[0].y + t[k2].y, t[0].z + t[k2].z, t[0].w + t[k2].w);
+                constexpr float S = SA / (SX * SX);
+                const uint32_t lo = f32x2_to_f16x2(t[0].y * S, t[0].x * S), hi = f32x2_to_f16x2(t[0].w * S, t[0].z * S);
+                const uint32_t to = ua + (lane >> 4) * CHUNK + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+#pragma unroll
+                for (int k2 = 0; k2 < CL; ++k2)
+                    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(mapa_shared(to, k2)), "r"(lo), "r"(hi) : "memory");
+            }
+            asm volatile("fence.proxy.async;" ::: "memory");
+            __syncwarp();
+            cluster_sync();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(sa + (col >> 6) * CHUNK + row * 128 + ((((col & 63) / 8 + i) ^ (row & 7)) << 4));
+                a[4 * i] = u.x; a[4 * i + 1] = u.y; a[4 * i + 2] = u.z; a[4 * i + 3] = u.w;
+            }
+        }
         in_place();
-        if (!good) break;
-        if (issuer) {                                // A A
+        if (CL == 1 && !good) break;
+        if (issuer && good) {                        // A A
             const uint32_t id = idesc_f16_f32(128, 128, false, false);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -1091,8 +1155,8 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
             w[i] = f32x2_to_f16x2(fmaf(cb, f16_hi(a[i]), v[2 * i + 1] * cc), fmaf(cb, f16_lo(a[i]), v[2 * i] * cc));
         put(sp, col, w);
         in_place();
-        if (!good) break;
-        if (issuer) {                                // a X + P X
+        if (CL == 1 && !good) break;
+        if (issuer && good) {                        // a X + P X
             for (int n0 = 0; n0 < p.np; n0 += 256) {
                 const int n = min(256, p.np - n0);
                 const uint32_t id = idesc_f16_f32(128, static_cast<uint32_t>(n), false, true);
@@ -1208,11 +1272,12 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     const bool tall = R > C;             // the smaller side is the columns
     const int m = L.m, n = tall ? R : C;
     cudaError_t e;
-    if (m <= SM_SIDE && n <= SM_LONG) {
+    if (m <= SM_SIDE && n <= SM_CTAS * SM_LONG) {
+        const int cl = n <= SM_LONG ? 1 : n <= 2 * SM_LONG ? 2 : n <= 4 * SM_LONG ? 4 : SM_CTAS;
         Small p{};
         p.q = q;
         p.tall = tall;
-        p.m = m; p.n = n; p.np = (n + 63) / 64 * 64;
+        p.m = m; p.n = n; p.np = ((n + cl - 1) / cl + 63) / 64 * 64;
         p.steps = f.steps;
         memcpy(p.c, f.coeffs, 3 * f.steps * sizeof(float));
         p.scale = f.scale;
@@ -1220,10 +1285,13 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
         p.status = status;
         p.timeout_ns = timeout_ns;
         p.inject = inject;
-        const size_t smem = 1024 + (p.np / 64 + 4) * CHUNK;
-        void (*kernel)(const Small) = vec ? ortho_small_kernel<true> : ortho_small_kernel<false>;
+        const size_t smem = 1024 + (p.np / 64 + 4 + (cl > 1 ? 4 : 0)) * CHUNK;
+        void (*kernel)(const Small) = cl == 1   ? (vec ? ortho_small_kernel<true, 1> : ortho_small_kernel<false, 1>)
+                                      : cl == 2 ? (vec ? ortho_small_kernel<true, 2> : ortho_small_kernel<false, 2>)
+                                      : cl == 4 ? (vec ? ortho_small_kernel<true, 4> : ortho_small_kernel<false, 4>)
+                                                : (vec ? ortho_small_kernel<true, 8> : ortho_small_kernel<false, 8>);
         if ((e = ensure_smem(reinterpret_cast<const void *>(kernel), smem)) != cudaSuccess) return e;
-        return launch_pdl(kernel, dim3(B), dim3(ST), smem, s, 1, p);
+        return launch_pdl(kernel, dim3(B * cl), dim3(ST), smem, s, cl, p);
     }
     const dim3 grid(L.parts, B);
     if ((e = launch_pdl(ortho_sample_kernel, dim3(B), dim3(PT), 0, s, 1, q)) != cudaSuccess) return e;

@@ -69,7 +69,8 @@ def _off(got, ref):
 SHAPES = [(1, 1, 1), (3, 1, 40), (2, 40, 1), (2, 7, 9), (3, 33, 65), (4, 64, 64), (5, 129, 100), (2, 128, 256), (16, 256, 128),
           (1, 255, 257), (2, 257, 255), (3, 300, 520), (1, 1088, 2112), (2, 2112, 1088), (1, 1000, 1001), (2, 600, 130),
           (1, 16, 7168), (1, 7168, 24), (700, 24, 17), (40, 192, 320), (2, 128, 384), (3, 383, 128), (2, 128, 392), (1, 136, 384),
-          (2, 96, 264), (2, 64, 321)]
+          (2, 96, 264), (2, 64, 321), (2, 1, 1000), (1, 1000, 1), (3, 5, 385), (2, 768, 128), (2, 128, 769), (3, 1537, 100),
+          (2, 77, 1531), (40, 128, 1024), (1, 128, 3072), (2, 3001, 57), (1, 120, 3073), (2, 129, 1500)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -90,7 +91,7 @@ def test_full_width():
         assert _off(_run(g), _reference(g)) <= (NEAR ** 2 + 2.0 ** -16) ** 0.5
 
 
-@pytest.mark.parametrize("shape", [(3, 33, 65), (2, 256, 128), (2, 264, 136)])
+@pytest.mark.parametrize("shape", [(3, 33, 65), (2, 256, 128), (2, 264, 136), (2, 1001, 65), (2, 128, 800)])
 @pytest.mark.parametrize("nesterov", [False, True])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_momentum(shape, nesterov, dt):
@@ -112,10 +113,16 @@ def test_coefficients_scale_steps_and_own_memory():
     assert _off(out, ref) <= (NEAR ** 2 + 2.0 ** -16) ** 0.5
     same = g.clone()
     assert torch.equal(_run(same, steps=3, coeffs=co, scale=0.2, out=same), out)
+    g = _matrices(2, 300, 200, "flat").to(BF)
+    same = g.clone()
+    assert torch.equal(_run(same, out=same), _run(g))
+    for steps in (1, 2):                        # (the last and the last but one carry X in fewer numbers)
+        assert _off(_run(g, steps=steps), _reference(g, steps)) <= (NEAR ** 2 + 2.0 ** -16) ** 0.5
+    g = g[:, :96].contiguous()
     assert _off(_run(g, steps=1), _reference(g, 1)) <= (NEAR ** 2 + 2.0 ** -16) ** 0.5
 
 
-@pytest.mark.parametrize("shape", [(6, 40, 56), (6, 41, 57)])
+@pytest.mark.parametrize("shape", [(6, 40, 56), (6, 41, 57), (6, 60, 1000), (6, 333, 250)])
 def test_sizes_zeros_infinities_and_nan(shape):
     g = _matrices(*shape, "flat")
     ref = _reference(g)
@@ -186,7 +193,7 @@ def test_other_stream_and_graph():
     assert B.moe_read_status(ws) == 0
 
 
-@pytest.mark.parametrize("shape", [(2, 128, 256), (2, 300, 200)])
+@pytest.mark.parametrize("shape", [(2, 128, 256), (2, 2500, 96), (2, 300, 200)])
 def test_a_wait_that_runs_out_is_recorded(shape):
     g = _matrices(*shape).to(BF)
     ws = torch.zeros(B.moe_orthogonalize_workspace_bytes(*shape), dtype=torch.uint8, device=DEV)
