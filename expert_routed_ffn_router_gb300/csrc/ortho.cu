@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
 }
 
 // ---------------------------------------------------------------------- small matrices
-// Matrices of up to 128 on the smaller side and 3072 on the larger one: a cluster of CL CTAs a matrix, each
+// Matrices of up to 128 on the smaller side and eight times 384 on the larger: a cluster of CL CTAs a matrix, each
 // with up to 384 columns of X, all steps in one launch.  X as the products' operand (fp16), A and P lie
 // in shared memory, X itself (fp32) in tensor memory, times a SA: the product with P is added to it there.
 // With several CTAs, each takes the sums of a part of A's rows from all of them and gives it to all: two

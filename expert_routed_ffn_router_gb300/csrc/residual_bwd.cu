@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(256) join_wgrad_kernel(const float *__restrict
     pdl_wait();
     const int c = blockIdx.x * 32 + threadIdx.x;     // (H is a multiple of 32)
     float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int r = threadIdx.y; r < n; r += 8)
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] += part[(static_cast<size_t>(r) * 4 + k) * H + c];

@@ -70,7 +70,7 @@ SHAPES = [(1, 1, 1), (3, 1, 40), (2, 40, 1), (2, 7, 9), (3, 33, 65), (4, 64, 64)
           (1, 255, 257), (2, 257, 255), (3, 300, 520), (1, 1088, 2112), (2, 2112, 1088), (1, 1000, 1001), (2, 600, 130),
           (1, 16, 7168), (1, 7168, 24), (700, 24, 17), (40, 192, 320), (2, 128, 384), (3, 383, 128), (2, 128, 392), (1, 136, 384),
           (2, 96, 264), (2, 64, 321), (2, 1, 1000), (1, 1000, 1), (3, 5, 385), (2, 768, 128), (2, 128, 769), (3, 1537, 100),
-          (2, 77, 1531), (40, 128, 1024), (1, 128, 3072), (2, 3001, 57), (1, 120, 3073), (2, 129, 1500)]
+          (2, 77, 1531), (40, 128, 1024), (1, 128, 3000), (2, 3001, 57), (1, 120, 3090), (2, 129, 1500)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
