@@ -45,9 +45,10 @@ __device__ __forceinline__ void load8(const void *p, size_t off, float (&v)[8])
 }
 
 // ---------------------------------------------------------------------------- combine
-// A CTA a token: each thread holds CV vectors of 8 columns of dY (as many as the row needs, 4 at most, in
-// turns beyond) and goes through the token's slots with them; the row of the next slot is loaded before the one at hand is stored.  (dYp may be
-// Yp's own memory: a thread has read what it overwrites, and no other one touches it.)
+// A CTA a token: each thread holds CV vectors of 8 columns of dY (as many as the row needs, 4 at most,
+// in turns beyond: 1777 x 2112, 3 slots: 15.4 us with 4, 11.7 us with the 2 that it needs) and goes through
+// the token's slots with them; the row of the next slot is loaded before the one at hand is stored.  (dYp may
+// be Yp's own memory: a thread has read what it overwrites, and no other one touches it.)
 constexpr int CT = 256;
 
 template <bool F32, bool DOT, int CV>
