@@ -83,6 +83,7 @@ struct Args {
     int side, n_side;             // tiles of A and P: rows and columns that are kept, tiles of a side
     int tn, nM, nN;               // tiles of X: columns that are kept, tiles in each direction
     int sym, app, units;          // tiles of A (or P), of X of a matrix; in all
+    int group;                    // matrices that go through the steps together
     int tma_out;                  // rows of `out` are multiples of 16 bytes
     float c[3 * MAX_STEPS];
     float scale;
@@ -150,15 +151,18 @@ struct Tile { int mode, k, b, m0, n0; unsigned need; };
 __device__ __forceinline__ Tile tile_at(const Args &p, int t)
 {
     Tile T;
-    const int per = 2 * p.sym + p.app, step = p.B * per;
+    const int per = 2 * p.sym + p.app, all = p.steps * p.group * per;
+    const int g0 = t / all * p.group, n = min(p.group, p.B - g0), step = n * per;
+    t -= g0 * p.steps * per;
     T.k = t / step;
     int l = t - T.k * step;
     T.need = 2 * N_EPI * static_cast<unsigned>(T.k * per);
-    if (l < 2 * p.B * p.sym) {
-        T.mode = l < p.B * p.sym ? GRAM : SQUARE;
-        if (T.mode == SQUARE) { l -= p.B * p.sym; T.need += 2 * N_EPI * p.sym; }
+    if (l < 2 * n * p.sym) {
+        T.mode = l < n * p.sym ? GRAM : SQUARE;
+        if (T.mode == SQUARE) { l -= n * p.sym; T.need += 2 * N_EPI * p.sym; }
         T.b = l / p.sym;
         l -= T.b * p.sym;
+        T.b += g0;
         int i = static_cast<int>((sqrtf(8.f * l + 1.f) - 1.f) * 0.5f);
         while (i * (i + 1) / 2 > l) --i;
         while ((i + 1) * (i + 2) / 2 <= l) ++i;
@@ -166,11 +170,12 @@ __device__ __forceinline__ Tile tile_at(const Args &p, int t)
         T.n0 = (l - i * (i + 1) / 2) * p.side;
         return T;
     }
-    l -= 2 * p.B * p.sym;
+    l -= 2 * n * p.sym;
     T.mode = T.k + 1 < p.steps ? APPLY : LAST;
     T.need += 2 * N_EPI * 2 * p.sym;
     T.b = l / p.app;
     l -= T.b * p.app;
+    T.b += g0;
     // the smaller side's tiles innermost: they share a part of X (rows innermost for tall matrices:
     // 695 instead of 672 us for 16 of 7168 x 2048)
     int i, j;
@@ -734,6 +739,15 @@ __global__ void __launch_bounds__(PT) ortho_sample_kernel(const Prepare p)
     if (blockIdx.x == 0) p.count[gridDim.x] = 0;
 }
 
+// Where element i of matrix `b` lies in X's arrays (their rows are as long as the matrix's where it is VEC).
+template <bool VEC>
+__device__ __forceinline__ size_t x_at(const Prepare &p, int b, size_t base, long long i)
+{
+    if constexpr (VEC) return base + i;
+    const long long r = i / p.C;
+    return (static_cast<size_t>(b) * p.R + r) * p.ld + (i - r * p.C);
+}
+
 // N numbers from `at` on as two fp16 numbers each
 template <int N>
 __device__ __forceinline__ void store_numbers(const Prepare &p, size_t at, const float (&v)[N])
@@ -792,15 +806,14 @@ __global__ void __launch_bounds__(PT) ortho_momentum_kernel(const Prepare p)
             v[k] = u[k] * size.x * size.y;
             most = fmaxf(most, fabsf(v[k]));
         }
-        const int r = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(r) * p.C);
-        store_numbers(p, (static_cast<size_t>(blockIdx.y) * p.R + r) * p.ld + c, v);
+        store_numbers(p, x_at<VEC>(p, blockIdx.y, base, i), v);
     }
     const float4 t = cta_sums(s0, s1, s2, most);
     if (threadIdx.x == 0) p.part[static_cast<size_t>(blockIdx.y) * p.parts + blockIdx.x] = t;
 }
 
-// CTA (part, matrix): the factor that is left.  Where the sample was so far off that X's numbers have left
-// fp16's range or come near its end, the chunk's are made again.
+// CTAs of a matrix: the factor that is left.  Where the sample was so far off that X's numbers have left
+// fp16's range or come near its end, they are made again.
 template <bool VEC>
 __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
 {
@@ -822,8 +835,8 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
     if (!far) return;
     const long long n = static_cast<long long>(p.R) * p.C;
     const size_t base = static_cast<size_t>(blockIdx.y) * n;
-    const long long lo = blockIdx.x * p.chunk, hi = min(n, lo + p.chunk);
-    for (long long i = lo + threadIdx.x * N; i < hi; i += PT * N) {
+    const long long step = static_cast<long long>(gridDim.x) * PT * N;
+    for (long long i = (static_cast<long long>(blockIdx.x) * PT + threadIdx.x) * N; i < n; i += step) {
         float u[N];
         if (!p.m || p.nesterov) load_g<VEC>(p, base + i, u);
         if (p.m) {
@@ -834,8 +847,7 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) u[k] = u[k] * f * inv;
-        const int r = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(r) * p.C);
-        store_numbers(p, (static_cast<size_t>(blockIdx.y) * p.R + r) * p.ld + c, u);
+        store_numbers(p, x_at<VEC>(p, blockIdx.y, base, i), u);
     }
 }
 
@@ -1297,7 +1309,9 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     if ((e = launch_pdl(ortho_sample_kernel, dim3(B), dim3(PT), 0, s, 1, q)) != cudaSuccess) return e;
     e = launch_pdl(vec ? ortho_momentum_kernel<true> : ortho_momentum_kernel<false>, grid, dim3(PT), 0, s, 1, q);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(vec ? ortho_scale_kernel<true> : ortho_scale_kernel<false>, grid, dim3(PT), 0, s, 1, q);
+    const int rest = (2 * num_sms() + B - 1) / B;
+    e = launch_pdl(vec ? ortho_scale_kernel<true> : ortho_scale_kernel<false>, dim3(L.parts < rest ? L.parts : rest, B),
+                   dim3(PT), 0, s, 1, q);
     if (e != cudaSuccess) return e;
 
     void *A = w + L.A, *P = w + L.P;
@@ -1329,6 +1343,14 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     a.tn = pick(C, [&](long long k) { return k * a.nM; });
     a.nN = tiles(C, a.tn);
     a.app = a.nM * a.nN;
+    // Matrices go through all steps in groups: what a group's products hand on is more often still in L2 (16 of
+    // 7168 x 2048, without momentum: 5.88 ms in one group, 5.67 in two or in four; 1% in calls one after the
+    // other, under the power cap).  A group's tiles of A go around the clusters 2.5 times, or the next product
+    // waits (24 of 2112 x 1088: 1.13 ms in one or two groups, 1.22 in three, 1.32 in four; 48: 2.33 ms in
+    // one, 2.25 in three); a rest of few matrices would, too.
+    const int least = static_cast<int>((5ll * most / 2 + a.sym - 1) / a.sym);
+    a.group = B < 2 * least ? B : (B + B / least - 1) / (B / least);
+    while (B % a.group && B % a.group < least) ++a.group;
     const long long units = static_cast<long long>(f.steps) * B * (2 * a.sym + a.app);
     if (units >= (1ll << 31) - 65536) return cudaErrorInvalidValue;
     a.units = static_cast<int>(units);
