@@ -748,7 +748,8 @@ constexpr int kMaxRows = 0x7fffffff - (1 << 20);
 static int check_rows(int T, int H, int K)
 {
     if (T < 0 || H <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
-    if (H % 64 || K > 32 || static_cast<long long>(T) * K >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    // (H: the dispatch's grid has a CTA for each 1024 columns)
+    if (H % 64 || H > (1 << 25) || K > 32 || static_cast<long long>(T) * K >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
 }
 

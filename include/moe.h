@@ -484,7 +484,8 @@ int moe_expert_ffn_backward(const void *x, const int8_t *x_scale, const void *dY
 /* Gradients of the layer's two row movements, for experts whose own backward pass the caller has
  * (moe_expert_ffn_backward holds both for the library's experts).  slot_pos as moe_dispatch left
  * it, its rows distinct; an entry outside [0, T*K) -- -1, a pair without a row -- contributes
- * nothing.  K <= 32.  No sum crosses tokens: the results repeat bit for bit.
+ * nothing.  K <= 32, H a multiple of 64 up to 2^25, T K < 2^31 (else MOE_ERR_UNSUPPORTED_SHAPE).  No
+ * sum crosses tokens: the results repeat bit for bit.
  *
  * Of moe_combine's Y[t] = sum_j topk_w[t, j] Yp[slot_pos[t, j]] (+ Ysh[t], whose gradient is dY):
  *     dYp[slot_pos[t, j]] = topk_w[t, j] dY[t],   d_topk_w[t, j] = <dY[t], Yp[slot_pos[t, j]]>

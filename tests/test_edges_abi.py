@@ -117,3 +117,8 @@ def test_orthogonalize_refusals(lib):
         B.moe_orthogonalize(t(4, 8), t(4, 8, dtype=torch.bfloat16), t(256), momentum=t(16))
     with pytest.raises(ValueError, match="coeffs: 3 values, expected 6"):
         B.moe_orthogonalize(t(4, 8), t(4, 8, dtype=torch.bfloat16), t(256), steps=2, coeffs=[(1, 2, 3)])
+
+
+def test_rows_longer_than_the_grid_are_refused(lib):
+    assert lib.moe_combine_backward(OK, 0, OK, OK, OK, 1, (1 << 25) + 64, 1, OK, OK, None) == -2
+    assert lib.moe_dispatch_backward(OK, OK, None, 1, (1 << 26) + 64, 1, OK, 0, None) == -2
