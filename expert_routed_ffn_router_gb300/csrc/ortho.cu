@@ -41,6 +41,7 @@
 // matrices: 7 us a product, in turn.
 #include <cuda.h>
 
+#include <cmath>
 #include <cstring>
 
 #include "common.cuh"
@@ -84,6 +85,7 @@ struct Args {
     int tn, nM, nN;               // tiles of X: columns that are kept, tiles in each direction
     int sym, app, units;          // tiles of A (or P), of X of a matrix; in all
     int group;                    // matrices that go through the steps together
+    int split;                    // parts of gram's sums
     int tma_out;                  // rows of `out` are multiples of 16 bytes
     float c[3 * MAX_STEPS];
     float scale;
@@ -91,6 +93,8 @@ struct Args {
     const float *rest;            // [B] what the first X still has to be multiplied by
     unsigned *count;              // [B] epilogue warps that are done with a tile (zeroed)
     int *next;                    // the next tile to be claimed (zeroed)
+    float *sums;                  // [B][tiles of A][split][2][N_EPI] parts of the sums, PIECES 32 x 32 each
+    unsigned *ticket;             // [B][tiles of A][2][N_EPI] how many of them are there (zeroed)
     int *status;
     unsigned long long timeout_ns;
     int inject;
@@ -145,21 +149,31 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
 
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-// The tile's product and step, matrix and place, and the arrivals at the matrix's counter that it needs.
-struct Tile { int mode, k, b, m0, n0; unsigned need; };
+// The tile's product and step, matrix and place, part of the sums, and the arrivals at the matrix's counter that
+// it needs.
+struct Tile { int mode, k, b, m0, n0, part; unsigned need; };
 
 __device__ __forceinline__ Tile tile_at(const Args &p, int t)
 {
     Tile T;
-    const int per = 2 * p.sym + p.app, all = p.steps * p.group * per;
+    const int per = (p.split + 1) * p.sym + p.app, all = p.steps * p.group * per;
     const int g0 = t / all * p.group, n = min(p.group, p.B - g0), step = n * per;
     t -= g0 * p.steps * per;
     T.k = t / step;
     int l = t - T.k * step;
-    T.need = 2 * N_EPI * static_cast<unsigned>(T.k * per);
-    if (l < 2 * n * p.sym) {
-        T.mode = l < n * p.sym ? GRAM : SQUARE;
-        if (T.mode == SQUARE) { l -= n * p.sym; T.need += 2 * N_EPI * p.sym; }
+    T.need = 2 * N_EPI * static_cast<unsigned>(T.k * (2 * p.sym + p.app));
+    T.part = 0;
+    const int gram = n * p.sym * p.split;
+    if (l < gram + n * p.sym) {
+        if (l < gram) {
+            T.mode = GRAM;
+            T.part = l % p.split;
+            l /= p.split;
+        } else {
+            T.mode = SQUARE;
+            T.need += 2 * N_EPI * p.sym;
+            l -= gram;
+        }
         T.b = l / p.sym;
         l -= T.b * p.sym;
         T.b += g0;
@@ -170,7 +184,7 @@ __device__ __forceinline__ Tile tile_at(const Args &p, int t)
         T.n0 = (l - i * (i + 1) / 2) * p.side;
         return T;
     }
-    l -= 2 * n * p.sym;
+    l -= gram + n * p.sym;
     T.mode = T.k + 1 < p.steps ? APPLY : LAST;
     T.need += 2 * N_EPI * 2 * p.sym;
     T.b = l / p.app;
@@ -194,7 +208,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *slabs = ring + STAGES * STAGE;
     __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], piece[N_EPI][PIECES], want, drain;
-    __shared__ int tq[TQ][5];
+    __shared__ int tq[TQ][6];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     volatile int *abort_flag = &abort_s;
@@ -242,7 +256,9 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         if (leader) mbar_arrive(&tqe[q]);
         else mbar_arrive_cluster(mapa_shared(smem_u32(&tqe[q]), 0));
     };
-    auto slot_read = [&](int q) { return Tile{tq[q][0], tq[q][1], tq[q][2], tq[q][3], tq[q][4], 0u}; };
+    auto slot_read = [&](int q) { return Tile{tq[q][0], tq[q][1], tq[q][2], tq[q][3], tq[q][4], tq[q][5], 0u}; };
+    // the stages of a part of gram's sums
+    auto first_stage = [&](int part) { return gram_kbs * part / p.split; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
@@ -259,7 +275,8 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 if (T.mode < 0) break;
                 fence_proxy_async_global();
                 const bool sym = T.mode <= SQUARE;
-                const int m = T.m0 + 128 * r, n = T.n0 + (sym ? p.side : p.tn) / 2 * r, kbs = T.mode == GRAM ? gram_kbs : m_kbs;
+                const int m = T.m0 + 128 * r, n = T.n0 + (sym ? p.side : p.tn) / 2 * r, kb0 = T.mode == GRAM ? first_stage(T.part) : 0;
+                const int kbs = T.mode == GRAM ? first_stage(T.part + 1) - kb0 : m_kbs;
                 const CUtensorMap *am, *bm;
                 bool amn = false, bmn = false;
                 if (T.mode == GRAM) { am = bm = &p.xg[T.k & 1]; amn = bmn = p.tall; }
@@ -273,7 +290,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                     unsigned char *a = ring + s * STAGE, *b = a + 2 * HALF;
                     const uint32_t fb = full0 + 8u * s;
                     if (leader) mbar_arrive_expect_tx(&full[s], 2u * STAGE);
-                    const int k = kb * BK;
+                    const int k = (kb0 + kb) * BK;
                     if (amn) {
                         tma_load_3d_pair(a, am, fb, m, k, T.b);
                         tma_load_3d_pair(a + HALF, am, fb, m + 64, k, T.b);
@@ -321,7 +338,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, bmn ? HALF : 16, 1024);
                 const uint32_t as = amn ? 128u : 2u, bs = bmn ? 128u : 2u;
                 const uint32_t id = idesc_f16_f32(TM, static_cast<uint32_t>(T.mode <= SQUARE ? p.side : p.tn), amn, bmn);
-                const int kbs = T.mode == GRAM ? gram_kbs : m_kbs;
+                const int kbs = T.mode == GRAM ? first_stage(T.part + 1) - first_stage(T.part) : m_kbs;
                 if (!mbar_wait(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + b * TN;
@@ -356,7 +373,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 wph ^= 1u;
                 const int t = atomicAdd(p.next, 1);
                 more = t < p.units;
-                Tile T{-1, 0, 0, 0, 0, 0u};
+                Tile T{-1, 0, 0, 0, 0, 0, 0u};
                 if (more) {
                     T = tile_at(p, t);
                     // the tiles that it builds on are stored
@@ -376,10 +393,10 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                     }
                 }
                 if (!mbar_wait_cluster(&tqe[qs], qph ^ 1u, abort_flag, p.status, tmo)) break;
-                const int vals[5] = {T.mode, T.k, T.b, T.m0, T.n0};
+                const int vals[6] = {T.mode, T.k, T.b, T.m0, T.n0, T.part};
                 const uint32_t other = mapa_shared(smem_u32(tq[qs]), 1);
 #pragma unroll
-                for (int j = 0; j < 5; ++j) {
+                for (int j = 0; j < 6; ++j) {
                     tq[qs][j] = vals[j];
                     st_shared_cluster(other + 4u * j, vals[j]);
                 }
@@ -468,6 +485,38 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             const float rest = T.k == 0 ? p.rest[T.b] : 1.f;
             const float ca = p.c[3 * T.k], cb = p.c[3 * T.k + 1], cc = p.c[3 * T.k + 2] / SA;
             const float gram = SA / (SX * SX) * rest * rest, apply = rest / SA, again = ca / SLO * rest;
+            // A part of gram's sums goes to memory; the warp whose part is the last one there adds all of them, in
+            // their order.
+            const bool parts = T.mode == GRAM && p.split > 1;
+            float4 *sums = nullptr;
+            bool told = T.mode != LAST;
+            constexpr int REGION = PIECES * 32 * 32 / 4;
+            if (parts) {
+                const int i = T.m0 / p.side, tile = T.b * p.sym + i * (i + 1) / 2 + T.n0 / p.side;
+                const int who = static_cast<int>(rank) * N_EPI + warp - EPI0;
+                sums = reinterpret_cast<float4 *>(p.sums) + (static_cast<size_t>(tile) * p.split * 2 * N_EPI + who) * REGION + lane;
+                float4 *mine = sums + static_cast<size_t>(T.part) * 2 * N_EPI * REGION;
+#pragma unroll 1
+                for (int c = c0; c < end; ++c) {
+                    float v[32];
+                    tmem_ld32(tm0 + b * TN + PC * c, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        __stcg(mine + (c - c0) * 256 + i * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                }
+                __threadfence();
+                __syncwarp();
+                unsigned *ticket = p.ticket + tile * 2 * N_EPI + who;
+                unsigned there = lane == 0 ? atomicAdd(ticket, 1u) + 1 : 0u;
+                there = __shfl_sync(kFullMask, there, 0);
+                __threadfence();
+                if (there == static_cast<unsigned>(p.split)) {
+                    if (lane == 0) *ticket = 0;      // (for the next step, which comes after this tile is stored)
+                } else {
+                    told = false;
+                    end = c0;
+                }
+            }
             const CUtensorMap *sm = T.mode == GRAM ? &p.pa : T.mode == SQUARE ? &p.pp : T.mode == APPLY ? &p.px[(T.k + 1) & 1] : &p.po;
 #pragma unroll 1
             for (int c = c0; c < end; ++c) {
@@ -487,7 +536,21 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                 __syncwarp();
                 float v[32];
-                tmem_ld32(tm0 + b * TN + PC * c, v);
+                if (!parts) {
+                    tmem_ld32(tm0 + b * TN + PC * c, v);
+                } else {
+                    const float4 *q = sums + (c - c0) * 256;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 2
+                    for (int s = 0; s < p.split; ++s, q += 2 * N_EPI * REGION) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 w = __ldcg(q + i * 32);
+                            v[4 * i] += w.x; v[4 * i + 1] += w.y; v[4 * i + 2] += w.z; v[4 * i + 3] += w.w;
+                        }
+                    }
+                }
                 if (T.mode == GRAM) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] *= gram;
@@ -577,7 +640,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive_cluster(tempty0 + 8u * b);
-                if (T.mode != LAST) pending = T.b;
+                if (told) pending = T.b;
             }
             __syncwarp();
             b ^= 1u;
@@ -619,6 +682,8 @@ struct Prepare {
     float4 *part;                     // [B][parts]: square sums at three scales
     uint16_t *hi, *lo;                // [B][R][ld]
     unsigned *count;                  // [B] and the next tile to be claimed: zeroed here
+    unsigned *ticket;                 // `tickets` for each matrix: zeroed here
+    int tickets;
     float2 *size;                     // [B] the sample's factor, in two
     float *rest;                      // [B] what X's numbers still have to be multiplied by
 };
@@ -708,6 +773,7 @@ constexpr int SAMPLE = 8 * PT;
 __global__ void __launch_bounds__(PT) ortho_sample_kernel(const Prepare p)
 {
     pdl_wait();
+    for (int i = threadIdx.x; i < p.tickets; i += PT) p.ticket[static_cast<size_t>(blockIdx.x) * p.tickets + i] = 0;
     const unsigned long long n = static_cast<unsigned long long>(p.R) * p.C;
     const size_t base = static_cast<size_t>(blockIdx.x) * n;
     float s0 = 0.f, s1 = 0.f, s2 = 0.f;
@@ -1233,12 +1299,79 @@ bool encode(CUtensorMap *m, const void *base, int B, int rows, int cols, int ld,
 size_t al256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 int up8(int n) { return (n + 7) & ~7; }
 
+bool is_small(int m, int n) { return m <= SM_SIDE && n <= SM_CTAS * SM_LONG; }
+int tiles_of(int n, int t) { return (n + t - 1) / t; }
+
+// Tiles of a call's products (Args).
+struct Plan { int side, n_side, sym, tn, nM, nN, app, group, split; };
+Plan plan_of(int B, int R, int C)
+{
+    Plan a{};
+    const int most = num_sms() / 2;      // clusters
+    const int m = R < C ? R : C, n = R < C ? C : R;
+    // Sides of the symmetric results' tiles and widths of X's: multiples of 32 up to 256, those whose tiles
+    // take least.  A tile's fixed part is worth about 32 columns; the tiles of few matrices follow each other
+    // in rounds of the clusters.
+    const auto pick = [&](int n, auto count) {
+        int best = 0;
+        double least = 0;
+        for (int k = tiles_of(n, 256); k <= 4 * tiles_of(n, 256); ++k) {
+            const int t = (tiles_of(n, k) + 31) / 32 * 32;
+            const long long all = static_cast<long long>(B) * count(tiles_of(n, t));
+            const double rounds = B < 4 || all < most ? static_cast<double>((all + most - 1) / most) : static_cast<double>(all) / most;
+            if (!best || rounds * (t + 32) < least) { least = rounds * (t + 32); best = t; }
+        }
+        return best;
+    };
+    const auto triangle = [](long long k) { return k * (k + 1) / 2; };
+    a.split = 1;
+    if (B * triangle(tiles_of(m, 256)) >= most || is_small(m, n)) {
+        a.side = pick(m, triangle);
+    } else {
+        // A round holds all of A's tiles, and gram's sums may go in parts.  Microseconds: a stage about 0.3 whatever
+        // the width (latency: four are on their way), a piece of 32 columns 0.7, a part 2 in all and 0.4 for a
+        // piece.  (1 of 7168 x 100: 391 us in whole sums, 180 in parts; 6 of 7168 x 200: 422 and 264; 1 of 7168 x
+        // 512: 313 and 211; 1 of 7168 x 2048: 562 and 527.)
+        const int gram = tiles_of(n, BK), square = tiles_of(m, BK);
+        double least = 0;
+        for (int k = tiles_of(m, 256); k <= 4 * tiles_of(m, 256); ++k) {
+            const int t = (tiles_of(m, k) + 31) / 32 * 32, pieces = (t / PC + 1) / 2;
+            const long long all = B * triangle(tiles_of(m, t));
+            if (all > most) break;
+            int split = static_cast<int>(sqrt(0.75 * gram / pieces));
+            if (split > most / all) split = static_cast<int>(most / all);
+            if (split > gram / 4) split = gram / 4;
+            for (int i = 0; i < 2; ++i, split = 1) {
+                const int parts = split < 2 ? 1 : split;
+                const double us = (tiles_of(gram, parts) + square) * (0.26 + 0.0003 * t) + 1.4 * pieces +
+                                  (parts > 1 ? 2 + 0.4 * parts * pieces : 0);
+                if (!least || us < least) { least = us; a.side = t; a.split = parts; }
+            }
+        }
+    }
+    a.n_side = tiles_of(m, a.side);
+    a.sym = a.n_side * (a.n_side + 1) / 2;
+    a.nM = tiles_of(R, TM);
+    a.tn = pick(C, [&](long long k) { return k * a.nM; });
+    a.nN = tiles_of(C, a.tn);
+    a.app = a.nM * a.nN;
+    // Matrices go through all steps in groups: what a group's products hand on is more often still in L2 (16 of
+    // 7168 x 2048, without momentum: 5.88 ms in one group, 5.67 in two or in four; 1% in calls one after the
+    // other, under the power cap).  A group's tiles of A go around the clusters 2.5 times, or the next product
+    // waits (24 of 2112 x 1088: 1.13 ms in one or two groups, 1.22 in three, 1.32 in four; 48: 2.33 ms in
+    // one, 2.25 in three); a rest of few matrices would, too.
+    const int least = static_cast<int>((5ll * most / 2 + a.sym - 1) / a.sym);
+    a.group = B < 2 * least ? B : (B + B / least - 1) / (B / least);
+    while (B % a.group && B % a.group < least) ++a.group;
+    return a;
+}
+
 struct Layout {
     int m, ld, ldm, parts;
     long long chunk;
-    size_t count, size, rest, part, hi[2], lo, A, P, bytes;
+    size_t count, size, rest, part, hi[2], lo, A, P, ticket, sums, bytes;
 };
-Layout layout(int B, int R, int C)
+Layout layout(int B, int R, int C, const Plan &t)
 {
     Layout L{};
     L.m = R < C ? R : C;
@@ -1262,29 +1395,34 @@ Layout layout(int B, int R, int C)
     L.lo = take(x);
     L.A = take(a);
     L.P = take(a);
+    const size_t each = t.split > 1 ? static_cast<size_t>(B) * t.sym * 2 * N_EPI : 0;
+    L.ticket = take(each * sizeof(unsigned));
+    L.sums = take(each * t.split * PIECES * 32 * 32 * sizeof(float));
     L.bytes = o;
     return L;
 }
 
 }  // namespace
 
-size_t ortho_bytes(int B, int R, int C) { return layout(B, R, C).bytes; }
+size_t ortho_bytes(int B, int R, int C) { return layout(B, R, C, plan_of(B, R, C)).bytes; }
 
 cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned long long timeout_ns, int inject,
                          cudaStream_t s)
 {
     const int B = f.B, R = f.R, C = f.C;
-    const Layout L = layout(B, R, C);
+    const Plan t = plan_of(B, R, C);
+    const Layout L = layout(B, R, C, t);
     unsigned char *w = static_cast<unsigned char *>(scratch);
     Prepare q{f.g, f.g_fp32, f.momentum, f.mu, f.nesterov, R, C, L.ld, L.chunk, L.parts,
               reinterpret_cast<float4 *>(w + L.part), reinterpret_cast<uint16_t *>(w + L.hi[0]),
               reinterpret_cast<uint16_t *>(w + L.lo), reinterpret_cast<unsigned *>(w + L.count),
+              reinterpret_cast<unsigned *>(w + L.ticket), t.split > 1 ? t.sym * 2 * N_EPI : 0,
               reinterpret_cast<float2 *>(w + L.size), reinterpret_cast<float *>(w + L.rest)};
     const bool vec = C % 8 == 0;
     const bool tall = R > C;             // the smaller side is the columns
     const int m = L.m, n = tall ? R : C;
     cudaError_t e;
-    if (m <= SM_SIDE && n <= SM_CTAS * SM_LONG) {
+    if (is_small(m, n)) {
         const int cl = n <= SM_LONG ? 1 : n <= 2 * SM_LONG ? 2 : n <= 4 * SM_LONG ? 4 : SM_CTAS;
         Small p{};
         p.q = q;
@@ -1318,40 +1456,13 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     Args a;
     memset(&a, 0, sizeof a);
     const int most = num_sms() / 2;      // clusters
-    const auto tiles = [](int n, int t) { return (n + t - 1) / t; };
     a.tall = tall;
     a.steps = f.steps;
     a.B = B; a.m = m; a.R = R; a.C = C;
-    // Sides of the symmetric results' tiles and widths of X's: multiples of 32 up to 256, those whose tiles
-    // take least.  A tile's fixed part is worth about 32 columns; the tiles of few matrices follow each other
-    // in rounds of the clusters.
-    const auto pick = [&](int n, auto count) {
-        int best = 0;
-        double least = 0;
-        for (int k = tiles(n, 256); k <= 4 * tiles(n, 256); ++k) {
-            const int t = (tiles(n, k) + 31) / 32 * 32;
-            const long long all = static_cast<long long>(B) * count(tiles(n, t));
-            const double rounds = B < 4 || all < most ? static_cast<double>((all + most - 1) / most) : static_cast<double>(all) / most;
-            if (!best || rounds * (t + 32) < least) { least = rounds * (t + 32); best = t; }
-        }
-        return best;
-    };
-    a.side = pick(m, [](long long k) { return k * (k + 1) / 2; });
-    a.n_side = tiles(m, a.side);
-    a.sym = a.n_side * (a.n_side + 1) / 2;
-    a.nM = tiles(R, TM);
-    a.tn = pick(C, [&](long long k) { return k * a.nM; });
-    a.nN = tiles(C, a.tn);
-    a.app = a.nM * a.nN;
-    // Matrices go through all steps in groups: what a group's products hand on is more often still in L2 (16 of
-    // 7168 x 2048, without momentum: 5.88 ms in one group, 5.67 in two or in four; 1% in calls one after the
-    // other, under the power cap).  A group's tiles of A go around the clusters 2.5 times, or the next product
-    // waits (24 of 2112 x 1088: 1.13 ms in one or two groups, 1.22 in three, 1.32 in four; 48: 2.33 ms in
-    // one, 2.25 in three); a rest of few matrices would, too.
-    const int least = static_cast<int>((5ll * most / 2 + a.sym - 1) / a.sym);
-    a.group = B < 2 * least ? B : (B + B / least - 1) / (B / least);
-    while (B % a.group && B % a.group < least) ++a.group;
-    const long long units = static_cast<long long>(f.steps) * B * (2 * a.sym + a.app);
+    a.side = t.side; a.n_side = t.n_side; a.sym = t.sym;
+    a.tn = t.tn; a.nM = t.nM; a.nN = t.nN; a.app = t.app;
+    a.group = t.group; a.split = t.split;
+    const long long units = static_cast<long long>(f.steps) * B * ((a.split + 1) * a.sym + a.app);
     if (units >= (1ll << 31) - 65536) return cudaErrorInvalidValue;
     a.units = static_cast<int>(units);
     a.tma_out = C % 8 == 0 ? 1 : 0;
@@ -1361,6 +1472,8 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     a.rest = q.rest;
     a.count = q.count;
     a.next = reinterpret_cast<int *>(q.count + B);
+    a.sums = reinterpret_cast<float *>(w + L.sums);
+    a.ticket = q.ticket;
     a.status = status;
     a.timeout_ns = timeout_ns;
     a.inject = inject;
@@ -1376,7 +1489,7 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     if (!ok) return cudaErrorInvalidValue;
     const size_t smem = 1024 + STAGES * STAGE + N_EPI * SLAB;
     if ((e = ensure_smem(reinterpret_cast<const void *>(ortho_gemm_kernel), smem)) != cudaSuccess) return e;
-    const int widest = B * (a.sym > a.app ? a.sym : a.app);
+    const int gram = a.split * a.sym, widest = B * (gram > a.app ? gram : a.app);
     return launch_pdl(ortho_gemm_kernel, dim3(2 * (widest < most ? widest : most)), dim3(NT), smem, s, 2, a);
 }
 

@@ -578,7 +578,8 @@ int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, in
  * fp16 products with fp32 sums on the tensor cores; X is carried in 22 bits, so that directions with
  * small singular values keep their precision; results are 0.3e-3 to 1.8e-3 off (2-norm) before
  * out's rounding.  A matrix of zeros gives zeros; one with an infinity or a NaN gives NaN.  The
- * results repeat bit for bit.  R, C <= 32768, B <= 65535, steps <= 32 (else
+ * results repeat bit for bit (a matrix's may differ in their last bits with the number of matrices
+ * beside it: long sums of few matrices are formed in parts).  R, C <= 32768, B <= 65535, steps <= 32 (else
  * MOE_ERR_UNSUPPORTED_SHAPE); any R and C from 1 on.  B == 0 enqueues nothing. */
 size_t moe_orthogonalize_workspace_bytes(int B, int R, int C);
 int moe_orthogonalize(const void *g, int g_fp32, float *momentum, float mu, int nesterov, int B, int R,

@@ -170,6 +170,58 @@ def test_repeats_and_batches_bit_for_bit():
     assert torch.equal(flat, out[0])
 
 
+# (few matrices with long sums: A = X X^T in parts that the last one adds)
+LONG = [(1, 7168, 100), (4, 100, 7168), (1, 5001, 300), (6, 200, 2100), (1, 257, 4100), (1, 7168, 24), (2, 1024, 4096), (30, 7168, 64)]
+
+
+@pytest.mark.parametrize("shape", LONG)
+@pytest.mark.parametrize("kind", ["flat", "low"])
+def test_long_sums_of_few_matrices(shape, kind):
+    g = _matrices(*shape, kind).to(BF)
+    ws = torch.full((B.moe_orthogonalize_workspace_bytes(*shape),), 255, dtype=torch.uint8, device=DEV)
+    ws[:256] = 0                                # (the status word; the rest is the call's own)
+    out = _run(g, ws=ws)
+    assert _off(out, _reference(g)) <= (NEAR ** 2 + 2.0 ** -16) ** 0.5
+    for _ in range(3):                          # whichever part comes last
+        assert torch.equal(_run(g, ws=ws), out)
+    graph, again = torch.cuda.CUDAGraph(), torch.empty_like(out)
+    with torch.cuda.graph(graph):
+        _run(g, out=again, ws=ws)
+    for _ in range(2):
+        again.zero_()
+        graph.replay()
+        assert torch.equal(again, out)
+
+
+def test_two_calls_at_once():
+    shapes = [(1, 7168, 100), (2, 600, 2100)]
+    gs = [_matrices(*s, "fall").to(BF) for s in shapes]
+    want = [_run(g) for g in gs]
+    wss = [torch.zeros(B.moe_orthogonalize_workspace_bytes(*s), dtype=torch.uint8, device=DEV) for s in shapes]
+    outs = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in shapes]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, o, ws, st in zip(gs, outs, wss, streams):
+            _run(g, stream=st, out=o, ws=ws)
+    torch.cuda.synchronize()
+    for o, w, ws in zip(outs, want, wss):
+        assert torch.equal(o, w) and B.moe_read_status(ws) == 0
+
+
+def test_a_wait_that_runs_out_with_sums_in_parts():
+    g = _matrices(1, 7168, 100).to(BF)
+    ws = torch.zeros(B.moe_orthogonalize_workspace_bytes(1, 7168, 100), dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(g)
+    B.moe_debug_set_wait_limit(2_000_000, 1)
+    try:
+        B.moe_orthogonalize(g, out, ws)
+        assert B.moe_read_status(ws) == B.MOE_ERR_DEVICE_TIMEOUT
+    finally:
+        B.moe_debug_set_wait_limit(0, 0)
+    assert _off(_run(g, ws=ws), _reference(g)) <= (NEAR ** 2 + 2.0 ** -16) ** 0.5
+
+
 def test_other_stream_and_graph():
     g, m0 = _matrices(3, 130, 70, "fall"), _matrices(3, 130, 70, "flat", seed=2)
     m = m0.clone()
