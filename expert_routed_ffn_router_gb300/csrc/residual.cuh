@@ -42,6 +42,8 @@ struct Args {
     void *dx;
     uint16_t *dy;
     float *d_token, *part;           // part [CTAs][4][H]: dgamma_pre, dbeta_pre, S1, S0
+    ResidualGrads g;                 // backward: the CTAs are one cluster, which adds its own sums (joined)
+    int joined;
     int stages, stage_bytes;         // of a row's threads
     int row_bytes, dr_once;          // backward: shared memory of a row's threads; dr is staged once
     int off[4];                      // the staged arrays in a stage, -1: read directly

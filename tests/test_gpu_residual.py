@@ -206,6 +206,36 @@ def test_backward(T, H, kinds, xt, yt, with_dr):
         assert torch.equal(dx2, dx) and torch.equal(dy2, dy)
 
 
+# (up to eight CTAs are a cluster that adds its own column sums; one more and a second launch does)
+@pytest.mark.parametrize("T,H", [(T, H) for H in (64, 320) for T in (1, 8, 9, 31, 40, 63, 64, 65)] +
+                         [(T, H) for H in (576, 7168, 16384) for T in (1, 2, 3, 6, 8, 9)])
+def test_column_gradients_of_few_rows(T, H):
+    for kinds in (KINDS[3], KINDS[1], KINDS[4]):
+        x, y, p, dn, dr = _inputs(T, H, F32, F32, *kinds)
+        r, _, _ = _forward(x, y, p)
+        stats = _rounded_stats(y, r, p)
+        ref = _reference(dn, dr, y, r, stats, p)[2]
+        grads = {k: torch.full_like(v, 7.0) for k, v in p.items() if torch.is_tensor(v)}
+        n = B.moe_residual_norm_backward_workspace_bytes(T, H)
+        ws = torch.full((n + 256,), 255, dtype=torch.uint8, device=DEV)
+        dx, dy = torch.empty_like(r), torch.empty(T, H, device=DEV, dtype=BF)
+
+        def call():
+            B.moe_residual_norm_backward(dn if p["pre"] != "none" else None, dr, y, r, stats, p, dx, dy, grads, ws[:n])
+        call()
+        for q, g in grads.items():
+            assert _near(g, *ref[q]), q
+        assert bool((ws[n:] == 255).all())
+        kept = {q: g.clone() for q, g in grads.items()}
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        for g in grads.values():
+            g.zero_()
+        graph.replay()
+        assert all(torch.equal(grads[q], kept[q]) for q in kept)
+
+
 def test_formula_against_differences():
     # the reference's own gradients: central differences of the definition in 64 bits
     T, H = 4, 64
