@@ -1310,8 +1310,10 @@ Plan plan_of(int B, int R, int C)
     const int most = num_sms() / 2;      // clusters
     const int m = R < C ? R : C, n = R < C ? C : R;
     // Sides of the symmetric results' tiles and widths of X's: multiples of 32 up to 256, those whose tiles
-    // take least.  A tile's fixed part is worth about 32 columns; the tiles of few matrices follow each other
-    // in rounds of the clusters.
+    // take least.  What a tile takes beside its columns is worth about 200 of them (24 of 2112 x 1088, widths
+    // of X's tiles 224, 192, 128: 1.13, 1.18, 1.40 ms), and 224 columns take as long as 256 (24 of 1088 x 2112:
+    // 1.17 ms with ten tiles of 224, 1.12 with nine of 256).  The tiles of few matrices follow each other in
+    // rounds of the clusters.
     const auto pick = [&](int n, auto count) {
         int best = 0;
         double least = 0;
@@ -1319,7 +1321,8 @@ Plan plan_of(int B, int R, int C)
             const int t = (tiles_of(n, k) + 31) / 32 * 32;
             const long long all = static_cast<long long>(B) * count(tiles_of(n, t));
             const double rounds = B < 4 || all < most ? static_cast<double>((all + most - 1) / most) : static_cast<double>(all) / most;
-            if (!best || rounds * (t + 32) < least) { least = rounds * (t + 32); best = t; }
+            const double cost = rounds * ((t > 192 ? 256 : t) + 200);
+            if (!best || cost < least) { least = cost; best = t; }
         }
         return best;
     };
