@@ -69,9 +69,10 @@ constexpr int SLAB = (PIECES + SIDE) * PIECE;   // an epilogue warp's buffers
 
 enum { GRAM, SQUARE, APPLY, LAST };
 
-constexpr int TQ = 4;                     // slots that hand claimed tiles to the roles
+constexpr int TQ = 8;                     // slots that hand claimed tiles to the roles
 constexpr int AHEAD = 24;                 // stages left to load of a tile when the next one is claimed
-constexpr int CLAIM_WARP = 2;
+constexpr int CLAIM_WARP = 2, TELL_WARP = 3;
+constexpr int DONE = 4;                   // tiles that the epilogue's warps may be apart
 constexpr int MAX_STEPS = 32;
 
 struct Args {
@@ -208,6 +209,8 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *slabs = ring + STAGES * STAGE;
     __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], piece[N_EPI][PIECES], want, drain;
+    __shared__ uint64_t drained[2], done[DONE];
+    __shared__ unsigned told[DONE];
     __shared__ int tq[TQ][6];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
@@ -224,11 +227,16 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 2 * N_EPI);
+            mbar_init(&tempty[b], 2);
+            mbar_init(&drained[b], N_EPI);
+        }
+        for (int i = 0; i < DONE; ++i) {
+            mbar_init(&done[i], N_EPI);
+            told[i] = 0;
         }
         for (int q = 0; q < TQ; ++q) {
             mbar_init(&tqf[q], 1);
-            mbar_init(&tqe[q], 2 * N_EPI + 3);   // both epilogues and producers, the MMA issuer
+            mbar_init(&tqe[q], 5);       // both producers, the MMA issuer, both warps that tell
         }
         for (int w = 0; w < N_EPI; ++w)
             for (int b = 0; b < PIECES; ++b) mbar_init(&piece[w][b], 1);
@@ -405,6 +413,37 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 if (++qs == TQ) { qs = 0; qph ^= 1u; }
             }
         }
+    } else if (warp == TELL_WARP) {
+        // -------------------------------------------------------------------- news
+        // What the epilogue has to tell other CTAs: that a tile's accumulator and slot are free, and that its
+        // results are in memory.  (Arrivals and counts at those scopes hold up a thread for 1 to 3 thousand cycles;
+        // with the epilogue's own threads telling, 24 of 2112 x 1088 took BEFORE us, AFTER so.)
+        if (lane == 0) {
+            uint32_t qs = 0, qph = 0, b = 0, bph = 0, i = 0, iph = 0;
+            const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+            while (true) {
+                if (!mbar_wait_cluster(&tqf[qs], qph, abort_flag, p.status, tmo)) break;
+                const Tile T = slot_read(qs);
+                if (T.mode < 0) break;
+                if (!mbar_wait(&drained[b], bph, abort_flag, p.status, tmo)) break;
+                tc_fence_after();
+                tc_fence_before();
+                mbar_arrive_cluster(tempty0 + 8u * b);
+                slot_done(qs);
+                if (++qs == TQ) { qs = 0; qph ^= 1u; }
+                b ^= 1u;
+                if (b == 0) bph ^= 1u;
+                if (!mbar_wait(&done[i], iph, abort_flag, p.status, tmo)) break;
+                const unsigned n = told[i];
+                told[i] = 0;
+                if (n) {
+                    fence_proxy_async_global();
+                    __threadfence();
+                    atomicAdd(p.count + T.b, n);
+                }
+                if (++i == DONE) { i = 0; iph ^= 1u; }
+            }
+        }
     } else if (warp >= EPI0) {
         // ---------------------------------------------------------------- epilogue
         // A warp's pieces of a tile, a buffer each: what is added to the sums (SQUARE: A; APPLY: X's second
@@ -412,13 +451,14 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         // goes beside them (the mirror image; X's first number) leaves from two more buffers in turn.
         const int q = warp & 3, half = (warp - EPI0) >> 2;   // lane quarter, half of the columns
         const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
-        const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
         const int r0 = 128 * static_cast<int>(rank) + 32 * q;
         unsigned char *slab = slabs + (warp - EPI0) * SLAB;
         uint64_t *arrived = piece[warp - EPI0];
         uint32_t b = 0, tph = 0, qs = 0, qph = 0, pph = 0;   // pph: phases of the buffers' barriers
         uint32_t flight = 0;                         // buffers that a copy is on its way to (lane 0)
-        int pending = -1;                            // matrix of the last tile, if nobody has been told of it
+        uint32_t tile = 0;
+        int owed = -1;                               // the last tile's place in done, if it is not arrived at (lane 0)
+        bool counts = false;                         // whether that tile counts
         // a wait by one lane (every lane then observes the phase itself)
         auto wait_all = [&](uint64_t *bar, uint32_t parity, bool cluster) -> bool {
             bool good = true;
@@ -432,26 +472,27 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             }
             return good;
         };
-        // The warp's part of its last tile is in global memory: tell who builds on it (lane 0).
-        auto tell = [&]() {
-            if (pending < 0) return;
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-            fence_proxy_async_global();
-            __threadfence();
-            atomicAdd(p.count + pending, 1u);
-            pending = -1;
+        // The warp's part of its last tile is in memory (lane 0, which has committed `newer` groups since).
+        auto settle = [&](int newer) {
+            if (owed < 0) return;
+            if (newer == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            else if (newer == 1) asm volatile("cp.async.bulk.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.bulk.wait_group 2;" ::: "memory");
+            if (counts) atomicAdd(&told[owed], 1u);
+            mbar_arrive(&done[owed]);
+            owed = -1;
         };
         bool good = true;
         while (good) {
-            // (the next tile may wait for the one that nobody has been told of)
-            if (lane == 0 && pending >= 0 && !mbar_test(&tqf[qs], qph)) tell();
+            // (the next tile may wait for the last one; else that is seen to while this one's sums are formed, or
+            // after its second piece)
+            if (lane == 0 && owed >= 0 && !mbar_test(&tqf[qs], qph)) settle(0);
             if (!wait_all(&tqf[qs], qph, true)) break;
             const Tile T = slot_read(qs);
             __syncwarp();
-            if (lane == 0) slot_done(qs);
             if (++qs == TQ) { qs = 0; qph ^= 1u; }
             if (T.mode < 0) {
-                if (lane == 0) tell();
+                if (lane == 0) settle(0);
                 break;
             }
             const bool sym = T.mode <= SQUARE, loads = T.mode == SQUARE || T.mode == APPLY;
@@ -476,7 +517,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                         flight |= 1u << (c - c0);
                     }
                 }
-                tell();
+                if (owed >= 0 && !mbar_test(&tfull[b], tph)) settle(0);
             }
             __syncwarp();
             if (!wait_all(&tfull[b], tph, false)) break;
@@ -489,7 +530,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             // their order.
             const bool parts = T.mode == GRAM && p.split > 1;
             float4 *sums = nullptr;
-            bool told = T.mode != LAST;
+            bool last = T.mode != LAST;              // whether the tile is done with this one
             constexpr int REGION = PIECES * 32 * 32 / 4;
             if (parts) {
                 const int i = T.m0 / p.side, tile = T.b * p.sym + i * (i + 1) / 2 + T.n0 / p.side;
@@ -513,7 +554,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 if (there == static_cast<unsigned>(p.split)) {
                     if (lane == 0) *ticket = 0;      // (for the next step, which comes after this tile is stored)
                 } else {
-                    told = false;
+                    last = false;
                     end = c0;
                 }
             }
@@ -633,16 +674,20 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                     if (second) tma_store_3d(&p.pl, main, col, m0, T.b);
                     if (mirror) tma_store_3d(sm, side, m0, col, T.b);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    if (c == c0 + 1) settle(2);
                 }
             }
             if (!good) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive_cluster(tempty0 + 8u * b);
-                if (told) pending = T.b;
+                mbar_arrive(&drained[b]);
+                settle(direct || end == c0 ? 0 : 1);
+                owed = static_cast<int>(tile % DONE);
+                counts = last;
             }
             __syncwarp();
+            ++tile;
             b ^= 1u;
             if (b == 0) tph ^= 1u;
         }
