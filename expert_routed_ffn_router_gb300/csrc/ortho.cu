@@ -60,12 +60,20 @@ constexpr int N_EPI = 8, EPI0 = 4;
 constexpr int NT = 32 * (EPI0 + N_EPI);
 constexpr int HALF = 8192;                // 64 x 64 fp16
 constexpr int STAGE = 4 * HALF;
-constexpr int STAGES = 4;
 constexpr int PC = 32;                    // columns of an epilogue's piece
 constexpr int PIECES = 4;                 // of a warp's part of a tile, at most
 constexpr int PIECE = 32 * PC * 2;
-constexpr int SIDE = 2;                   // buffers for what leaves beside a piece, in turn
-constexpr int SLAB = (PIECES + SIDE) * PIECE;   // an epilogue warp's buffers
+// The ring's stages, and an epilogue warp's buffers: ARRIVE that pieces arrive in, two that leave.  With 5 stages
+// two pieces arrive ahead of time, with 4 all of them: long sums gain by the stages (24 of 2112 x 1088: 1.09 and
+// 1.05 ms, 8 of 1536 x 4096: 1.02 and 0.98), short ones lose by the pieces (30 of 300 x 700: 315 and 329 us, 20
+// of 600 x 1300: 579 and 586).
+template <int STAGES>
+struct Ring {
+    static constexpr int ARRIVE = STAGES == 5 ? 2 : 4;
+    static constexpr int SLAB = (ARRIVE + 2) * PIECE;
+    static constexpr int BYTES = 1024 + STAGES * STAGE + N_EPI * SLAB;
+};
+constexpr int LONG_SUMS = 1024;           // the smaller side from which on there are 5 stages
 
 enum { GRAM, SQUARE, APPLY, LAST };
 
@@ -201,14 +209,16 @@ __device__ __forceinline__ Tile tile_at(const Args &p, int t)
     return T;
 }
 
+template <int STAGES>
 __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant__ Args p)
 {
+    constexpr int ARRIVE = Ring<STAGES>::ARRIVE, SLAB = Ring<STAGES>::SLAB;
     constexpr int TCOLS = 512;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *slabs = ring + STAGES * STAGE;
-    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], piece[N_EPI][PIECES], want, drain;
+    __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], tqf[TQ], tqe[TQ], piece[N_EPI][ARRIVE], want, drain;
     __shared__ uint64_t drained[2], done[DONE];
     __shared__ unsigned told[DONE];
     __shared__ int tq[TQ][6];
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             mbar_init(&tqe[q], 5);       // both producers, the MMA issuer, both warps that tell
         }
         for (int w = 0; w < N_EPI; ++w)
-            for (int b = 0; b < PIECES; ++b) mbar_init(&piece[w][b], 1);
+            for (int b = 0; b < ARRIVE; ++b) mbar_init(&piece[w][b], 1);
         mbar_init(&want, 1);
         mbar_init(&drain, 1);
         abort_s = 0;
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         // -------------------------------------------------------------------- news
         // What the epilogue has to tell other CTAs: that a tile's accumulator and slot are free, and that its
         // results are in memory.  (Arrivals and counts at those scopes hold up a thread for 1 to 3 thousand cycles;
-        // with the epilogue's own threads telling, 24 of 2112 x 1088 took BEFORE us, AFTER so.)
+        // with the epilogue's own threads telling, 24 of 2112 x 1088 took 1.12 ms, 1.09 so.)
         if (lane == 0) {
             uint32_t qs = 0, qph = 0, b = 0, bph = 0, i = 0, iph = 0;
             const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
@@ -446,9 +456,8 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         }
     } else if (warp >= EPI0) {
         // ---------------------------------------------------------------- epilogue
-        // A warp's pieces of a tile, a buffer each: what is added to the sums (SQUARE: A; APPLY: X's second
-        // number) arrives there by TMA while the products run, and the results leave from there; what
-        // goes beside them (the mirror image; X's first number) leaves from two more buffers in turn.
+        // What is added to a piece's sums (SQUARE: A; APPLY: X's second number) arrives by TMA, ARRIVE pieces ahead;
+        // the result and what goes beside it (the mirror image; X's second number) leave from a buffer each.
         const int q = warp & 3, half = (warp - EPI0) >> 2;   // lane quarter, half of the columns
         const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
         const int r0 = 128 * static_cast<int>(rank) + 32 * q;
@@ -506,16 +515,17 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             int end = half ? pieces : (pieces + 1) / 2;
             if ((sym && r0 >= p.side) || m0 >= M) end = c0;
             end = max(c0, min(end, (N - T.n0 + PC - 1) / PC));
+            // (lane 0; the warp has read what the buffer held)
+            auto load = [&](int c) {
+                const int i = (c - c0) % ARRIVE;
+                mbar_arrive_expect_tx(&arrived[i], PIECE);
+                tma_load_3d(slab + i * PIECE, T.mode == SQUARE ? &p.pa : &p.pl, &arrived[i], T.n0 + PC * c, m0, T.b);
+                flight |= 1u << i;
+            };
             if (lane == 0) {
-                // (what left the buffers for the tile before has left them)
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 if (loads && c0 < end && !p.inject) {
                     fence_proxy_async_global();
-                    for (int c = c0; c < end; ++c) {
-                        mbar_arrive_expect_tx(&arrived[c - c0], PIECE);
-                        tma_load_3d(slab + (c - c0) * PIECE, T.mode == SQUARE ? &p.pa : &p.pl, &arrived[c - c0], T.n0 + PC * c, m0, T.b);
-                        flight |= 1u << (c - c0);
-                    }
+                    for (int c = c0; c < min(end, c0 + ARRIVE); ++c) load(c);
                 }
                 if (owed >= 0 && !mbar_test(&tfull[b], tph)) settle(0);
             }
@@ -563,19 +573,17 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             for (int c = c0; c < end; ++c) {
                 const int col = T.n0 + PC * c;
                 // (an address in the 64-byte swizzle goes by the lane's row: 16 bytes i of 64)
-                unsigned char *main = slab + (c - c0) * PIECE, *side = slab + (PIECES + ((c - c0) & 1)) * PIECE;
+                unsigned char *in = slab + (c - c0) % ARRIVE * PIECE, *first = slab + ARRIVE * PIECE, *side = first + PIECE;
                 auto at = [&](unsigned char *s, int i) -> uint4 * {
                     return reinterpret_cast<uint4 *>(s + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
                 };
                 __syncwarp();
                 if (loads) {
-                    if (!wait_all(&arrived[c - c0], (pph >> (c - c0)) & 1u, false)) { good = false; break; }
-                    pph ^= 1u << (c - c0);
-                    flight &= ~(1u << (c - c0));
+                    const int i = (c - c0) % ARRIVE;
+                    if (!wait_all(&arrived[i], (pph >> i) & 1u, false)) { good = false; break; }
+                    pph ^= 1u << i;
+                    flight &= ~(1u << i);
                 }
-                // (the side buffer's last group but one has left it)
-                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                __syncwarp();
                 float v[32];
                 if (!parts) {
                     tmem_ld32(tm0 + b * TN + PC * c, v);
@@ -598,7 +606,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 } else if (T.mode == SQUARE) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 h = *at(main, i);
+                        const uint4 h = *at(in, i);
                         const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -618,7 +626,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                     if (T.mode == APPLY) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint4 l = *at(main, i);
+                            const uint4 l = *at(in, i);
                             const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -628,6 +636,13 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                         }
                     }
                 }
+                // (what the piece before left in its buffers has left them)
+                __syncwarp();
+                if (lane == 0) {
+                    if (loads && c + ARRIVE < end && !p.inject) load(c + ARRIVE);
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+                __syncwarp();
                 const float f = p.scale / SX;
                 if (direct) {
                     if (row < M) {
@@ -646,7 +661,6 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
 #pragma unroll
                     for (int i = 0; i < 16; ++i) w[i] = f32x2_to_f16x2(v[2 * i + 1], v[2 * i]);
                 }
-                unsigned char *first = T.mode == APPLY ? side : main;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) *at(first, i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 if (second) {
@@ -657,7 +671,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                         for (int k = 0; k < 4; ++k)
                             y[k] = f32x2_to_f16x2((v[8 * i + 2 * k + 1] - f16_hi(w[4 * i + k])) * SLO,
                                                   (v[8 * i + 2 * k] - f16_lo(w[4 * i + k])) * SLO);
-                        *at(main, i) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *at(side, i) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
                 if (mirror) {
@@ -671,7 +685,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 __syncwarp();
                 if (lane == 0) {
                     tma_store_3d(sm, first, col, m0, T.b);
-                    if (second) tma_store_3d(&p.pl, main, col, m0, T.b);
+                    if (second) tma_store_3d(&p.pl, side, col, m0, T.b);
                     if (mirror) tma_store_3d(sm, side, m0, col, T.b);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     if (c == c0 + 1) settle(2);
@@ -693,7 +707,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         }
         if (lane == 0) {
             // pieces still on their way (after a wait that ran out), and the last stores
-            for (int i = 0; i < PIECES; ++i) {
+            for (int i = 0; i < ARRIVE; ++i) {
                 int dummy = 0;
                 if (flight >> i & 1u) mbar_wait(&arrived[i], (pph >> i) & 1u, &dummy, nullptr, 20000000ull);
             }
@@ -1535,10 +1549,12 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
     }
     if (a.tma_out) ok = ok && encode(&a.po, f.out, B, R, C, C, 32, 32);
     if (!ok) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + STAGES * STAGE + N_EPI * SLAB;
-    if ((e = ensure_smem(reinterpret_cast<const void *>(ortho_gemm_kernel), smem)) != cudaSuccess) return e;
+    const bool longer = m >= LONG_SUMS;
+    void (*kernel)(const Args) = longer ? ortho_gemm_kernel<5> : ortho_gemm_kernel<4>;
+    const size_t smem = longer ? Ring<5>::BYTES : Ring<4>::BYTES;
+    if ((e = ensure_smem(reinterpret_cast<const void *>(kernel), smem)) != cudaSuccess) return e;
     const int gram = a.split * a.sym, widest = B * (gram > a.app ? gram : a.app);
-    return launch_pdl(ortho_gemm_kernel, dim3(2 * (widest < most ? widest : most)), dim3(NT), smem, s, 2, a);
+    return launch_pdl(kernel, dim3(2 * (widest < most ? widest : most)), dim3(NT), smem, s, 2, a);
 }
 
 }  // namespace moe
