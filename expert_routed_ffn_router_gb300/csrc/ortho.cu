@@ -17,7 +17,7 @@
 // A matrix's tiles of one product start when those of the one before are stored (a counter a matrix);
 // they come earlier in the list, so whoever waits holds nothing that they need.  Other matrices' tiles
 // fill the gaps.  (With a launch for each product: 6.9 ms for 16 matrices of 7168 x 2048, 1.42 ms for 24 of
-// 2112 x 1088; with this 6.7 and 1.34 ms.)
+// 2112 x 1088; with this 6.7 and 1.34 ms, before the steps noted below.)
 //
 // Numbers.  The products take fp16 operands (11 bits; entries of X are at most 1.2 and typically
 // (rows columns)^-1/2, so a fixed power of two keeps them normal) with fp32 sums.  What is carried
@@ -34,11 +34,11 @@
 // stages of 32 KB a CTA, two accumulators in tensor memory, eight epilogue warps, all waits
 // bounded (MOE_ERR_DEVICE_TIMEOUT in the status word).
 //
-// What bounds it: large matrices the tensor cores (16 of 7168 x 2048: 5.2 ms in the products of one call,
-// 1610 TFLOP/s with the diagonal tiles computed whole; 5.8 ms in calls one after the other, under the power
-// cap, where the measured library rate is 1.05 of that) and 0.53 ms of memory before them; 24 of 2112 x 1088:
-// 1.06 ms in the products, tiles of 17 stages and the shared memory's loads from L2 (13 TB/s); few
-// matrices: 7 us a product, in turn.
+// What bounds it: large matrices the tensor cores (16 of 7168 x 2048: 5.1 ms in the products of one call,
+// 1630 TFLOP/s with the diagonal tiles computed whole; 5.8 ms in calls one after the other, under the power
+// cap at 1500 MHz, where the library's products are 5% faster) and 0.5 ms of memory before them; 24 of 2112 x
+// 1088: 1.0 ms in the products, operands that come late from L2 and tiles of 17 stages; few matrices: 7 us a
+// product, in turn.
 #include <cuda.h>
 
 #include <cmath>
