@@ -392,24 +392,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 const int t = atomicAdd(p.next, 1);
                 more = t < p.units;
                 Tile T{-1, 0, 0, 0, 0, 0, 0u};
-                if (more) {
-                    T = tile_at(p, t);
-                    // the tiles that it builds on are stored
-                    const unsigned *n = p.count + T.b;
-                    if (T.need && ld_acquire(n) < T.need) {
-                        const uint64_t t0 = globaltimer_ns();
-                        bool good = true;
-                        while (good && ld_acquire(n) < T.need) {
-                            if (*abort_flag) good = false;
-                            else if (globaltimer_ns() - t0 > tmo) {
-                                *abort_flag = 1;
-                                report(p.status, MOE_ERR_DEVICE_TIMEOUT);
-                                good = false;
-                            }
-                        }
-                        if (!good) break;
-                    }
-                }
+                if (more) T = tile_at(p, t);
                 if (!mbar_wait_cluster(&tqe[qs], qph ^ 1u, abort_flag, p.status, tmo)) break;
                 const int vals[6] = {T.mode, T.k, T.b, T.m0, T.n0, T.part};
                 const uint32_t other = mapa_shared(smem_u32(tq[qs]), 1);
@@ -417,6 +400,22 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 for (int j = 0; j < 6; ++j) {
                     tq[qs][j] = vals[j];
                     st_shared_cluster(other + 4u * j, vals[j]);
+                }
+                // The tiles that it builds on are stored.  (Waited for after the slot is written: the arrival in the
+                // other CTA then has no store to wait for.)
+                const unsigned *n = p.count + T.b;
+                if (T.need && ld_acquire(n) < T.need) {
+                    const uint64_t t0 = globaltimer_ns();
+                    bool good = true;
+                    for (int i = 1; good && ld_acquire(n) < T.need; ++i) {
+                        if (*abort_flag) good = false;
+                        else if (i % 16 == 0 && globaltimer_ns() - t0 > tmo) {
+                            *abort_flag = 1;
+                            report(p.status, MOE_ERR_DEVICE_TIMEOUT);
+                            good = false;
+                        }
+                    }
+                    if (!good) break;
                 }
                 mbar_arrive(&tqf[qs]);
                 mbar_arrive_cluster(mapa_shared(smem_u32(&tqf[qs]), 1));
