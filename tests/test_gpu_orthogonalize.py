@@ -193,6 +193,14 @@ def test_long_sums_of_few_matrices(shape, kind):
         assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("shape", [(40, 1100, 1024), (2, 1023, 1024), (2, 1024, 1024), (3, 1025, 1100)])
+def test_groups_of_matrices_and_both_rings(shape):
+    g = _matrices(*shape, "fall").to(BF)
+    out = _run(g)
+    assert _off(out, _reference(g)) <= (NEAR ** 2 + 2.0 ** -16) ** 0.5
+    assert torch.equal(_run(g), out)
+
+
 def test_two_calls_at_once():
     shapes = [(1, 7168, 100), (2, 600, 2100)]
     gs = [_matrices(*s, "fall").to(BF) for s in shapes]
