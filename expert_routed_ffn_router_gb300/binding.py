@@ -205,6 +205,31 @@ def _ptrs(*specs):
     return [_ptr(*spec) for spec in specs]
 
 
+def _ptrs_here(ref, *specs):
+    """As _ptrs, for tensors that have to lie on the current device (ref is one of them)."""
+    dev, out = ref.get_device(), []
+    for t, dtype, numel, name in specs:
+        if t is None:
+            out.append(None)
+        elif t.dtype is dtype and t.get_device() == dev and t.numel() == numel and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            break
+    else:
+        if dev >= 0 and dev == _current_device():    # (-1: host memory)
+            return out
+    out = _ptrs(*specs)
+    for t, _, _, name in specs:
+        if t is not None:
+            _here(t, name)
+    return out
+
+
+def _here(t, name):
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name}: on device {t.get_device()}, the current one is {_current_device()}")
+
+
 def _wstruct(cls, weights: dict, specs, io_specs):
     """A weights structure from (name, dtype, numel) specs (a missing name stays NULL), with
     the layer's input / output tensors (io_specs): every type and size is checked first."""
@@ -227,12 +252,30 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
+_current_device = _raw_device or torch.cuda.current_device
+
+
+def _ws_here(ws):
+    if ws.get_device() == _current_device() and ws.is_contiguous():
+        return ws.data_ptr(), ws.nbytes
+    out = _ws(ws)
+    _here(ws, "ws")
+    return out
+
+
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
         return _raw_stream(_raw_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _stream_here(stream):
+    """As _stream, behind _ptrs_here (CUDA is initialised)."""
+    if stream is None and _raw_stream is not None and _raw_device is not None:
+        return _raw_stream(_raw_device())
+    return _stream(stream)
 
 
 def _check(fn, rc):
@@ -545,19 +588,20 @@ def moe_combine_backward(dY, Yp, slot_pos, topk_w, dYp, d_topk_w=None, stream=No
     """dY bf16 or fp32 [T, H]; topk_w (all 1), d_topk_w (not wanted) and with it Yp may be None."""
     T, K = slot_pos.shape
     H, f = dY.shape[1], _fp32_flag(dY, "dY")
-    d, y, s, w, o, dw = _ptrs((dY, dY.dtype, T * H, "dY"), (Yp, BF16, T * K * H, "Yp"), (slot_pos, I32, T * K, "slot_pos"),
-                              (topk_w, F32, T * K, "topk_w"), (dYp, BF16, T * K * H, "dYp"),
-                              (d_topk_w, F32, T * K, "d_topk_w"))
-    _check("moe_combine_backward", load().moe_combine_backward(d, f, y, s, w, T, H, K, o, dw, _stream(stream)))
+    d, y, s, w, o, dw = _ptrs_here(
+        dY, (dY, dY.dtype, T * H, "dY"), (Yp, BF16, T * K * H, "Yp"), (slot_pos, I32, T * K, "slot_pos"),
+        (topk_w, F32, T * K, "topk_w"), (dYp, BF16, T * K * H, "dYp"), (d_topk_w, F32, T * K, "d_topk_w"))
+    _check("moe_combine_backward", load().moe_combine_backward(d, f, y, s, w, T, H, K, o, dw, _stream_here(stream)))
 
 
 def moe_dispatch_backward(dXp, slot_pos, dres, dX, stream=None):
     """dX bf16 or fp32 [T, H]; dres of its type, or None."""
     T, K = slot_pos.shape
     H, f = dX.shape[1], _fp32_flag(dX, "dX")
-    p, s, r, o = _ptrs((dXp, BF16, T * K * H, "dXp"), (slot_pos, I32, T * K, "slot_pos"),
-                       (dres, dX.dtype, T * H, "dres"), (dX, dX.dtype, T * H, "dX"))
-    _check("moe_dispatch_backward", load().moe_dispatch_backward(p, s, r, T, H, K, o, f, _stream(stream)))
+    p, s, r, o = _ptrs_here(
+        dX, (dXp, BF16, T * K * H, "dXp"), (slot_pos, I32, T * K, "slot_pos"), (dres, dX.dtype, T * H, "dres"),
+        (dX, dX.dtype, T * H, "dX"))
+    _check("moe_dispatch_backward", load().moe_dispatch_backward(p, s, r, T, H, K, o, f, _stream_here(stream)))
 
 
 _NORMS = {"none": 0, "layer": 1, "rms": 2}
@@ -585,10 +629,10 @@ def _grad_specs(g, T, H):
 
 
 def _norm_kind(p, name):
-    kind = p.get(name, "none")
-    if kind not in _NORMS:
-        raise ValueError(f"{name}: {kind}, expected one of {tuple(_NORMS)}")
-    return _NORMS[kind]
+    kind = _NORMS.get(p.get(name, "none"))
+    if kind is None:
+        raise ValueError(f"{name}: {p[name]}, expected one of {tuple(_NORMS)}")
+    return kind
 
 
 def _residual(p, post, pre, columns):
@@ -602,11 +646,11 @@ def moe_residual_norm(x, y, p, r, n=None, stats=None, stream=None):
     beta_pre [H] and gate_token [T], each of which may be missing or None."""
     T, H = x.shape
     fx, fy, post, pre, k = _fp32_flag(x, "x"), _fp32_flag(y, "y"), _norm_kind(p, "post"), _norm_kind(p, "pre"), T * H
-    xp, yp, rp, np_, sp, *cols = _ptrs(
-        (x, x.dtype, k, "x"), (y, y.dtype, k, "y"), (r, x.dtype, k, "r"), (n, BF16, k, "n"),
+    xp, yp, rp, np_, sp, *cols = _ptrs_here(
+        x, (x, x.dtype, k, "x"), (y, y.dtype, k, "y"), (r, x.dtype, k, "r"), (n, BF16, k, "n"),
         (stats, F32, 4 * T, "stats"), *_param_specs(p, T, H))
     _check("moe_residual_norm", load().moe_residual_norm(xp, fx, yp, fy, _residual(p, post, pre, cols), T, H, rp, np_, sp,
-                                                         _stream(stream)))
+                                                         _stream_here(stream)))
 
 
 def moe_residual_norm_backward_workspace_bytes(T: int, H: int) -> int:
@@ -619,13 +663,13 @@ def moe_residual_norm_backward(dn, dr, y, r, stats, p, dx, dy, grads, ws, stream
     T, H = dx.shape
     fx, fy, post, pre = _fp32_flag(dx, "dx"), 0 if y is None else _fp32_flag(y, "y"), _norm_kind(p, "post"), _norm_kind(p, "pre")
     k, xt = T * H, dx.dtype
-    d, e, yp, rp, sp, dxp, dyp, *cols = _ptrs(
-        (dn, BF16, k, "dn"), (dr, xt, k, "dr"), (y, F32 if fy else BF16, k, "y"), (r, xt, k, "r"),
+    d, e, yp, rp, sp, dxp, dyp, *cols = _ptrs_here(
+        dx, (dn, BF16, k, "dn"), (dr, xt, k, "dr"), (y, F32 if fy else BF16, k, "y"), (r, xt, k, "r"),
         (stats, F32, 4 * T, "stats"), (dx, xt, k, "dx"), (dy, BF16, k, "dy"), *_param_specs(p, T, H),
         *_grad_specs(grads, T, H))
     _check("moe_residual_norm_backward", load().moe_residual_norm_backward(
         d, e, yp, fy, rp, fx, sp, _residual(p, post, pre, cols[:6]), T, H, dxp, dyp,
-        ctypes.byref(MoeResidualGrads(*cols[6:])), *_ws(ws), _stream(stream)))
+        ctypes.byref(MoeResidualGrads(*cols[6:])), *_ws_here(ws), _stream_here(stream)))
 
 
 def moe_orthogonalize_workspace_bytes(B: int, R: int, C: int) -> int:
@@ -644,10 +688,10 @@ def moe_orthogonalize(g, out, ws, momentum=None, mu=0.95, nesterov=False, steps=
         if len(flat) != 3 * int(steps):
             raise ValueError(f"coeffs: {len(flat)} values, expected {3 * int(steps)}")
         arr = (ctypes.c_float * len(flat))(*flat)
-    gp, m, o = _ptrs((g, g.dtype, n, "g"), (momentum, F32, n, "momentum"), (out, BF16, n, "out"))
+    gp, m, o = _ptrs_here(g, (g, g.dtype, n, "g"), (momentum, F32, n, "momentum"), (out, BF16, n, "out"))
     _check("moe_orthogonalize", load().moe_orthogonalize(
-        gp, f, m, float(mu), 1 if nesterov else 0, b, R, C, int(steps), arr, float(scale), o, *_ws(ws),
-        _stream(stream)))
+        gp, f, m, float(mu), 1 if nesterov else 0, b, R, C, int(steps), arr, float(scale), o, *_ws_here(ws),
+        _stream_here(stream)))
 
 
 # ------------------------------------------------------------------- convenience wrapper

@@ -191,3 +191,26 @@ def test_muon_step_and_fit():
         assert torch.equal(w[k], opt.master[k].to(BF))
     losses = train.fit(steps=3, T=64, muon=True)
     assert len(losses) == 3 and all(v == v for v in losses)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    # (the current device is said to be another one: nothing is launched)
+    T, H, K = 4, 128, 2
+    x, y = torch.zeros(T, H, device=DEV), torch.zeros(T * K, H, device=DEV, dtype=torch.bfloat16)
+    slot = torch.arange(T * K, device=DEV, dtype=torch.int32).view(T, K)
+    n, stats, ws = y[:T], torch.zeros(T, 4, device=DEV), torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+    calls = [lambda: B.moe_combine_backward(x, y, slot, None, y),
+             lambda: B.moe_dispatch_backward(y, slot, None, x),
+             lambda: B.moe_residual_norm(x, x, {}, x),
+             lambda: B.moe_residual_norm_backward(None, x, None, x, stats, {}, x, n, {}, ws),
+             lambda: B.moe_orthogonalize(n, n, ws)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    for call in (lambda: B.moe_orthogonalize(n, n, ws.cpu()), lambda: B.moe_dispatch_backward(y, slot.cpu(), None, x)):
+        with pytest.raises(ValueError, match="device tensors"):
+            call()
+    monkeypatch.setattr(B, "_current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="current one is 1"):
+            call()
