@@ -1360,7 +1360,7 @@ int up8(int n) { return (n + 7) & ~7; }
 bool is_small(int m, int n) { return m <= SM_SIDE && n <= SM_CTAS * SM_LONG; }
 int tiles_of(int n, int t) { return (n + t - 1) / t; }
 
-// Tiles of a call's products (Args).
+// Tiles of a call's products (Args); B > 0.
 struct Plan { int side, n_side, sym, tn, nM, nN, app, group, split; };
 Plan plan_of(int B, int R, int C)
 {
@@ -1465,7 +1465,7 @@ Layout layout(int B, int R, int C, const Plan &t)
 
 }  // namespace
 
-size_t ortho_bytes(int B, int R, int C) { return layout(B, R, C, plan_of(B, R, C)).bytes; }
+size_t ortho_bytes(int B, int R, int C) { return B > 0 ? layout(B, R, C, plan_of(B, R, C)).bytes : 0; }
 
 cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned long long timeout_ns, int inject,
                          cudaStream_t s)
