@@ -175,7 +175,9 @@ class Muon:
         need = 256
         for w in weights.values():
             b, R, C = self._shape(w)
-            need = max(need, B.moe_orthogonalize_workspace_bytes(min(b, experts or b), R, C))
+            k = max(1, min(b, experts or b))
+            # (of the last call too, which has the rest: fewer matrices may need more)
+            need = max(need, *(B.moe_orthogonalize_workspace_bytes(n, R, C) for n in (k, b % k) if n))
         device = next(iter(weights.values())).device if weights else "cuda"
         self.ws = torch.zeros(need, dtype=torch.uint8, device=device)
 

@@ -575,6 +575,7 @@ int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, in
  *   out      bf16 [B, R, C] (may be g's own memory where g is bf16)
  *   ws       at least moe_orthogonalize_workspace_bytes(B, R, C) bytes (0 for an invalid shape):
  *            about B (6 R C + 4 min(R, C)^2) bytes, and up to 20 MB for few matrices with long sums
+ *            (so fewer matrices may need more than many)
  * fp16 products with fp32 sums on the tensor cores; X is carried in 22 bits, so that directions with
  * small singular values keep their precision; results are 0.3e-3 to 1.8e-3 off (2-norm) before
  * out's rounding.  A matrix of zeros gives zeros; one with an infinity or a NaN gives NaN.  The

@@ -4,6 +4,12 @@ import os
 import subprocess
 import sys
 
+import pytest
+import torch
+
+from expert_routed_ffn_router_gb300 import binding as B
+from expert_routed_ffn_router_gb300 import train
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SHAPES = [(64, 96), (128, 3000), (128, 3100), (300, 520), (7168, 100), (100, 7168), (2112, 1088), (512, 2048), (1, 32768),
           (32768, 32768)]
@@ -14,3 +20,28 @@ def test_workspace_of_no_matrices():
     code = ("from expert_routed_ffn_router_gb300 import binding as B\n"
             f"for s in {SHAPES!r}: assert 0 < B.moe_orthogonalize_workspace_bytes(0, *s) <= 4096, s\n")
     assert subprocess.run([sys.executable, "-c", code], timeout=300, cwd=ROOT).returncode == 0
+
+
+def _calls(monkeypatch):
+    """Every call's matrices, bytes of workspace and addresses, in place of the kernels."""
+    seen = []
+
+    def call(g, out, ws, momentum=None, **k):
+        out.fill_(1.0)
+        momentum.add_(g)
+        seen.append((g.shape, ws.numel(), [t.data_ptr() for t in (g, out, momentum)]))
+    monkeypatch.setattr(B, "moe_orthogonalize", call)
+    return seen
+
+
+# (fewer matrices may need more: their sums are formed in parts)
+@pytest.mark.parametrize("shape,experts", [((3, 512, 2048), 2), ((7, 256, 2048), 4), ((9, 200, 2100), 5), ((5, 64, 96), 2),
+                                           ((512, 2048), 1), ((4, 300, 520), None)])
+def test_muon_has_the_workspace_of_its_last_call_too(monkeypatch, shape, experts):
+    w = torch.zeros(shape, dtype=torch.bfloat16)
+    opt = train.Muon({"W": w}, experts=experts)
+    seen = _calls(monkeypatch)
+    opt.step({"W": torch.ones_like(w)})
+    assert sum(s[0] for s, _, _ in seen) == (shape[0] if len(shape) == 3 else 1)
+    for s, have, _ in seen:
+        assert have >= B.moe_orthogonalize_workspace_bytes(*s), s
