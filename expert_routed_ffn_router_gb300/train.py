@@ -34,6 +34,7 @@ orthogonalised updates with momentum (Muon, below) in place of plain gradient de
 from __future__ import annotations
 
 import argparse
+import math
 
 import torch
 
@@ -164,10 +165,14 @@ class Muon:
 
     The factor gives every entry of the update a mean square of about 0.2^2, whatever the matrix's
     sides.  weights: the bf16 tensors by name, [R, C] or [E, R, C]; master copies in fp32 and the
-    momentum are kept here.  experts: matrices that one call orthogonalises (the workspace grows
-    with them; None: all of a tensor)."""
+    momentum are kept here.  experts: matrices that one call orthogonalises, at most (the workspace
+    grows with them; None: all of a tensor); a call starts on a boundary of 16 bytes, which takes up
+    to eight matrices where R C is no multiple of 8."""
 
     def __init__(self, weights: dict, lr: float = 0.02, mu: float = 0.95, decay: float = 0.0, experts=None):
+        if experts is not None and (int(experts) != experts or experts < 1):
+            raise ValueError(f"experts: {experts!r}, expected a number of matrices from 1 on, or None")
+        experts = None if experts is None else int(experts)
         self.weights, self.lr, self.mu, self.decay, self.experts = weights, lr, mu, decay, experts
         self.master = {n: w.float() for n, w in weights.items()}
         self.momentum = {n: torch.zeros_like(m) for n, m in self.master.items()}
@@ -175,7 +180,7 @@ class Muon:
         need = 256
         for w in weights.values():
             b, R, C = self._shape(w)
-            k = max(1, min(b, experts or b))
+            k = self._chunk(b, R, C)
             # (of the last call too, which has the rest: fewer matrices may need more)
             need = max(need, *(B.moe_orthogonalize_workspace_bytes(n, R, C) for n in (k, b % k) if n))
         device = next(iter(weights.values())).device if weights else "cuda"
@@ -185,11 +190,20 @@ class Muon:
     def _shape(w):
         return ((1,) + tuple(w.shape))[-3:]
 
+    def _chunk(self, b, R, C):
+        """Matrices of a call: b, or as many up to `experts` as end on a boundary of 16 bytes."""
+        if self.experts is None or self.experts >= b:
+            return max(1, b)
+        each = 8 // math.gcd(R * C, 8)
+        if self.experts < each:
+            raise ValueError(f"experts: {self.experts}, matrices of {R} x {C} take a multiple of {each}")
+        return self.experts // each * each
+
     def step(self, grads: dict) -> None:
         """grads: the gradients by name (bf16 or fp32), of all or some of the weights."""
         for n, g in grads.items():
             b, R, C = self._shape(g)
-            k = min(b, self.experts or b)
+            k = self._chunk(b, R, C)
             v = [t.view(b, R, C) for t in (g, self.update[n], self.momentum[n])]
             for i in range(0, b, k):
                 gi, ui, mi = (t[i:i + k] for t in v)

@@ -45,3 +45,31 @@ def test_muon_has_the_workspace_of_its_last_call_too(monkeypatch, shape, experts
     assert sum(s[0] for s, _, _ in seen) == (shape[0] if len(shape) == 3 else 1)
     for s, have, _ in seen:
         assert have >= B.moe_orthogonalize_workspace_bytes(*s), s
+
+
+def test_muon_refuses_numbers_of_matrices_that_it_cannot_take(monkeypatch):
+    w = torch.zeros(6, 64, 96, dtype=torch.bfloat16)
+    for bad in (0, -1, -4, 1.5, "2"):      # (-1 took no step at all, 0 all matrices)
+        with pytest.raises(ValueError, match="experts"):
+            train.Muon({"W": w}, experts=bad)
+
+
+# bf16 matrices of 35, 12 and 4 entries: 8, 2 and 2 of them end on a boundary of 16 bytes
+@pytest.mark.parametrize("shape,experts,sizes", [((20, 5, 7), 9, [8, 8, 4]), ((5, 3, 4), 3, [2, 2, 1]), ((9, 2, 2), 2, [2] * 4 + [1]),
+                                                 ((3, 5, 7), 8, [3]), ((3, 5, 7), None, [3]), ((5, 64, 96), 2, [2, 2, 1])])
+def test_muon_takes_matrices_from_aligned_addresses_on(monkeypatch, shape, experts, sizes):
+    w = torch.zeros(shape, dtype=torch.bfloat16)
+    opt = train.Muon({"W": w}, experts=experts)
+    seen = _calls(monkeypatch)
+    opt.step({"W": torch.ones_like(w)})
+    assert [s[0] for s, _, _ in seen] == sizes
+    for s, have, at in seen:
+        assert all(a % 16 == 0 for a in at) and have >= B.moe_orthogonalize_workspace_bytes(*s)
+    assert bool((opt.momentum["W"] == 1).all())
+
+
+@pytest.mark.parametrize("shape,experts", [((3, 5, 7), 2), ((20, 5, 7), 7), ((5, 3, 4), 1), ((2, 1, 1), 1)])
+def test_muon_refuses_chunks_between_boundaries(shape, experts):
+    # (refused by the second call of a step, after the first one's momentum, before)
+    with pytest.raises(ValueError, match="experts"):
+        train.Muon({"W": torch.zeros(shape, dtype=torch.bfloat16)}, experts=experts)
