@@ -982,9 +982,33 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
 // With several CTAs, each takes the sums of a part of A's rows from all of them and gives it to all: two
 // barriers of the cluster a step.  (16 matrices of 256 x 128: 100 us with the launches for large ones, 27 us
 // with this; one of 128 x 1000: 116 and 43 us; 76 of 128 x 1536: 303 and 174 us.)
-constexpr int SM_SIDE = 128, SM_LONG = 384, SM_CTAS = 8;
+//
+// SIDE 64: up to FEW on the smaller side, every operand is two fp16 numbers, hi + lo (22 bits; lo at hi's power
+// of two, where its last bit is 2^-24 / SX or less), and a product is hi hi + hi lo + lo hi.  With one number
+// the roundings of X, A and P do not average out over few directions: of 64 random matrices of 2 x 2 the worst
+// comes out 9.8e-3 off, of 4 x 3000 7.3e-3, of 32 x 3000 3.5e-3; so 1e-5, and 2e-4 with ranks far below the sides
+// (700 of 24 x 17: 74 us with one number, 89 so; 16 of 64 x 256 24 and 34 us; 8 of 64 x 3000, a cluster of
+// eight each, 55 and 53).  A chunk of an operand is 64 rows then: as the first operand of a product of 128 rows
+// it reads on into what lies behind it, for rows of the sums that nothing reads.
+constexpr int SM_SIDE = 128, SM_LONG = 384, SM_CTAS = 8, FEW = 64;
 constexpr int ST = 512;               // threads: four warps for each 32 rows, which share the columns
-constexpr int CHUNK = 128 * 128;      // 128 rows x 64 fp16
+constexpr int PITCH = 132;            // of 128 rows of a tall matrix on their way, in fp32
+
+// Shared memory from its first multiple of 1024 on: X (SIDE 64: its second numbers), A and P (likewise), this CTA's
+// sums of A where there are several CTAs, fp32 [SIDE][SIDE], and what a chunk of 64 rows is read on into.
+template <int SIDE>
+struct Places {
+    static constexpr int NUMBERS = SIDE == 64 ? 2 : 1;
+    static constexpr int CHUNK = SIDE * 128;             // SIDE rows x 64 fp16
+    static constexpr int SQUARE_OF = SIDE / 64 * CHUNK;  // one number of A or P
+    static constexpr int x(int np) { return np / 64 * CHUNK; }
+    static constexpr size_t bytes(int np, int cl)
+    {
+        const size_t all = NUMBERS * (x(np) + 2 * SQUARE_OF) + (cl > 1 ? SIDE * SIDE * 4 : 0) + (SIDE == 64 ? CHUNK : 0);
+        const size_t turn = SIDE == 64 ? 128 * PITCH * 4 : 0;    // (within the rest for 128)
+        return 1024 + (all > turn ? all : turn);
+    }
+};
 
 struct Small {
     Prepare q;
@@ -1041,15 +1065,25 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr)
     return v;
 }
 
-template <bool VEC, int CL>
+// Two numbers of fp16, of each of a pair
+__device__ __forceinline__ void two_numbers(float v1, float v0, uint32_t &hi, uint32_t &lo)
+{
+    hi = f32x2_to_f16x2(v1, v0);
+    lo = f32x2_to_f16x2(v1 - f16_hi(hi), v0 - f16_lo(hi));
+}
+
+template <bool VEC, int CL, int SIDE>
 __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constant__ Small p)
 {
     constexpr uint32_t TCOLS = 512, TD = SM_LONG;    // X, then the sums of A and A A
+    constexpr bool TWO = SIDE == 64;
+    constexpr int CHUNK = Places<SIDE>::CHUNK, ALO = Places<SIDE>::SQUARE_OF, TERMS = TWO ? 3 : 1;
+    const int XLO = Places<SIDE>::x(p.np);
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sx = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char *sa = sx + p.np / 64 * CHUNK, *sp = sa + 2 * CHUNK;
-    unsigned char *part = sp + 2 * CHUNK;            // CL > 1: this CTA's sums of A, fp32 [128][128]
+    unsigned char *sa = sx + Places<SIDE>::NUMBERS * XLO, *sp = sa + Places<SIDE>::NUMBERS * ALO;
+    unsigned char *part = sp + Places<SIDE>::NUMBERS * ALO;      // CL > 1: this CTA's sums of A
     __shared__ uint64_t done;
     __shared__ uint32_t tmem_slot;
     __shared__ float red[3][ST / 32];
@@ -1073,6 +1107,7 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
     const uint32_t tmem = tmem_slot;
     // this thread's row, and its columns: 32 from `col` on of every 128
     const int q = warp & 3, col = 32 * (warp >> 2), row = 32 * q + lane;
+    const bool rows = 32 * q < SIDE, square = rows && col < SIDE;    // whether it has numbers of X, of A and P
     const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int x0 = rank * p.np, own = max(0, min(p.np, p.n - x0));   // this CTA's columns of X
@@ -1089,7 +1124,7 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
     // shared memory, 128 of its rows (columns of X) at a time: [column][128 + 4 rows] of fp32.
     float s0 = 0.f, s1 = 0.f, s2 = 0.f;
     float *turn = reinterpret_cast<float *>(sx);
-    constexpr int PITCH = 132, N = Elements<VEC>::N;
+    constexpr int N = Elements<VEC>::N;
     for (int c0 = 0; c0 < p.np; c0 += 128) {
         if (p.tall) {
             __syncthreads();
@@ -1170,17 +1205,18 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
         // X of this step: the operand, and a SA X in tensor memory; after the last one, the result
         const bool last = k == p.steps;
         const float take = k == 0 ? f : 1.f / SA, mul = k == 0 ? inv : 1.f, keep = last ? 0.f : p.c[3 * k] * SA;
-        for (int c = col; c < p.np; c += 128) {
+        for (int c = rows ? col : p.np; c < p.np; c += 128) {
             float v[32];
             __syncwarp();
             tmem_ld32(tm0 + c, v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = v[i] * take * mul;
             if (!last) {
-                uint32_t w[16];
+                uint32_t w[16], l[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = f32x2_to_f16x2(v[2 * i + 1], v[2 * i]);
+                for (int i = 0; i < 16; ++i) two_numbers(v[2 * i + 1], v[2 * i], w[i], l[i]);
                 put(sx, c, w);
+                if (TWO) put(sx + XLO, c, l);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= keep;
                 tmem_st32(tm0 + c, v);
@@ -1223,73 +1259,109 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
         in_place();
         if (CL == 1 && !good) break;
         if (issuer && good) {                        // A = X X^T
-            const uint32_t id = idesc_f16_f32(128, 128, false, false);
+            const uint32_t id = idesc_f16_f32(128, SIDE, false, false);
             for (int i = 0; i < p.np / 16; ++i) {
-                const uint64_t d = smem_desc_sw128(ux + (i >> 2) * CHUNK + (i & 3) * 32, 16, 1024);
+                const uint32_t at = ux + (i >> 2) * CHUNK + (i & 3) * 32;
+                const uint64_t d = smem_desc_sw128(at, 16, 1024);
                 tc_mma_bf16(tmem + TD, d, d, id, i > 0 ? 1u : 0u);
+                if (TWO) {
+                    const uint64_t l = smem_desc_sw128(at + XLO, 16, 1024);
+                    tc_mma_bf16(tmem + TD, d, l, id, 1u);
+                    tc_mma_bf16(tmem + TD, l, d, id, 1u);
+                }
             }
             tc_commit(&done);
         }
         finished();
-        uint32_t a[16];                              // A, of the thread's row and columns
+        constexpr float S = SA / (SX * SX);
+        uint32_t a[16], al[16];                      // A, of the thread's row and columns
         float v[32];
-        tmem_ld32(tm0 + TD + col, v);
+        if (square) tmem_ld32(tm0 + TD + col, v);
         if (CL == 1) {
+            if (square) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) a[i] = f32x2_to_f16x2(v[2 * i + 1] * (SA / (SX * SX)), v[2 * i] * (SA / (SX * SX)));
-            put(sa, col, a);
+                for (int i = 0; i < 16; ++i) two_numbers(v[2 * i + 1] * S, v[2 * i] * S, a[i], al[i]);
+                put(sa, col, a);
+                if (TWO) put(sa + ALO, col, al);
+            }
         } else {
-            // vector j of 4 columns of a row lies at j ^ row (modulo 32)
+            // vector j of 4 columns of a row lies at j ^ row (modulo the vectors)
+            constexpr int V = SIDE / 4;
+            if (square)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4 *>(part + row * 512 + (((col / 4 + i) ^ (row & 31)) << 4)) =
-                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<float4 *>(part + row * (SIDE * 4) + (((col / 4 + i) ^ (row & (V - 1))) << 4)) =
+                        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             __syncwarp();
             cluster_sync();
+            constexpr int MINE = SIDE / CL * V;      // vectors of this CTA's rows
 #pragma unroll
-            for (int j = 0; j < 128 / CL * 32 / ST; ++j) {
-                const int r = rank * (128 / CL) + j * (ST / 32) + warp;      // a row of this CTA's, vector `lane`
-                const uint32_t at = smem_u32(part) + r * 512 + ((lane ^ (r & 31)) << 4);
+            for (int j = 0; j < (MINE + ST - 1) / ST; ++j) {
+                const int e = j * ST + tid, r = rank * (SIDE / CL) + e / V, n = e % V;
+                if (MINE % ST && e >= MINE) break;
+                const uint32_t at = smem_u32(part) + r * (SIDE * 4) + ((n ^ (r & (V - 1))) << 4);
                 float4 t[CL];
 #pragma unroll
                 for (int k2 = 0; k2 < CL; ++k2) t[k2] = ld_cluster(mapa_shared(at, k2));
 #pragma unroll
                 for (int k2 = 1; k2 < CL; ++k2) t[0] = make_float4(t[0].x + t[k2].x, t[0].y + t[k2].y, t[0].z + t[k2].z, t[0].w + t[k2].w);
-                constexpr float S = SA / (SX * SX);
-                const uint32_t lo = f32x2_to_f16x2(t[0].y * S, t[0].x * S), hi = f32x2_to_f16x2(t[0].w * S, t[0].z * S);
-                const uint32_t to = ua + (lane >> 4) * CHUNK + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+                uint32_t h0, h1, l0, l1;
+                two_numbers(t[0].y * S, t[0].x * S, h0, l0);
+                two_numbers(t[0].w * S, t[0].z * S, h1, l1);
+                const uint32_t to = ua + (n >> 4) * CHUNK + r * 128 + ((((n & 15) >> 1) ^ (r & 7)) << 4) + (n & 1) * 8;
 #pragma unroll
-                for (int k2 = 0; k2 < CL; ++k2)
-                    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(mapa_shared(to, k2)), "r"(lo), "r"(hi) : "memory");
+                for (int k2 = 0; k2 < CL; ++k2) {
+                    const uint32_t there = mapa_shared(to, k2);
+                    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(there), "r"(h0), "r"(h1) : "memory");
+                    if (TWO) asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(there + ALO), "r"(l0), "r"(l1) : "memory");
+                }
             }
             asm volatile("fence.proxy.async;" ::: "memory");
             __syncwarp();
             cluster_sync();
+            auto get = [&](const unsigned char *s, uint32_t (&w)[16]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(sa + (col >> 6) * CHUNK + row * 128 + ((((col & 63) / 8 + i) ^ (row & 7)) << 4));
-                a[4 * i] = u.x; a[4 * i + 1] = u.y; a[4 * i + 2] = u.z; a[4 * i + 3] = u.w;
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(s + (col >> 6) * CHUNK + row * 128 + ((((col & 63) / 8 + i) ^ (row & 7)) << 4));
+                    w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+                }
+            };
+            if (square) {
+                get(sa, a);
+                if (TWO) get(sa + ALO, al);
             }
         }
         in_place();
         if (CL == 1 && !good) break;
         if (issuer && good) {                        // A A
-            const uint32_t id = idesc_f16_f32(128, 128, false, false);
+            const uint32_t id = idesc_f16_f32(128, SIDE, false, false);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint64_t d = smem_desc_sw128(ua + (i >> 2) * CHUNK + (i & 3) * 32, 16, 1024);
+            for (int i = 0; i < SIDE / 16; ++i) {
+                const uint32_t at = ua + (i >> 2) * CHUNK + (i & 3) * 32;
+                const uint64_t d = smem_desc_sw128(at, 16, 1024);
                 tc_mma_bf16(tmem + TD, d, d, id, i > 0 ? 1u : 0u);
+                if (TWO) {
+                    const uint64_t l = smem_desc_sw128(at + ALO, 16, 1024);
+                    tc_mma_bf16(tmem + TD, d, l, id, 1u);
+                    tc_mma_bf16(tmem + TD, l, d, id, 1u);
+                }
             }
             tc_commit(&done);
         }
         finished();
         const float cb = p.c[3 * k + 1], cc = p.c[3 * k + 2] / SA;
-        tmem_ld32(tm0 + TD + col, v);
-        uint32_t w[16];
+        if (square) {
+            tmem_ld32(tm0 + TD + col, v);
+            uint32_t w[16], l[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            w[i] = f32x2_to_f16x2(fmaf(cb, f16_hi(a[i]), v[2 * i + 1] * cc), fmaf(cb, f16_lo(a[i]), v[2 * i] * cc));
-        put(sp, col, w);
+            for (int i = 0; i < 16; ++i) {
+                float a1 = f16_hi(a[i]), a0 = f16_lo(a[i]);
+                if (TWO) { a1 += f16_hi(al[i]); a0 += f16_lo(al[i]); }
+                two_numbers(fmaf(cb, a1, v[2 * i + 1] * cc), fmaf(cb, a0, v[2 * i] * cc), w[i], l[i]);
+            }
+            put(sp, col, w);
+            if (TWO) put(sp + ALO, col, l);
+        }
         in_place();
         if (CL == 1 && !good) break;
         if (issuer && good) {                        // a X + P X
@@ -1297,9 +1369,11 @@ __global__ void __launch_bounds__(ST, 1) ortho_small_kernel(const __grid_constan
                 const int n = min(256, p.np - n0);
                 const uint32_t id = idesc_f16_f32(128, static_cast<uint32_t>(n), false, true);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    tc_mma_bf16(tmem + n0, smem_desc_sw128(up + (i >> 2) * CHUNK + (i & 3) * 32, 16, 1024),
-                                smem_desc_sw128(ux + (n0 >> 6) * CHUNK + i * 2048, CHUNK, 1024), id, 1u);
+                for (int t = 0; t < TERMS; ++t)      // P X, P lo X, P X lo
+#pragma unroll
+                    for (int i = 0; i < SIDE / 16; ++i)
+                        tc_mma_bf16(tmem + n0, smem_desc_sw128(up + (t == 1 ? ALO : 0) + (i >> 2) * CHUNK + (i & 3) * 32, 16, 1024),
+                                    smem_desc_sw128(ux + (t == 2 ? XLO : 0) + (n0 >> 6) * CHUNK + i * 2048, CHUNK, 1024), id, 1u);
             }
             tc_commit(&done);
         }
@@ -1356,6 +1430,14 @@ bool encode(CUtensorMap *m, const void *base, int B, int rows, int cols, int ld,
 
 size_t al256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 int up8(int n) { return (n + 7) & ~7; }
+
+template <bool VEC, int SIDE>
+auto small_kernel(int cl) -> void (*)(const Small)
+{
+    return cl == 1   ? ortho_small_kernel<VEC, 1, SIDE>
+           : cl == 2 ? ortho_small_kernel<VEC, 2, SIDE>
+           : cl == 4 ? ortho_small_kernel<VEC, 4, SIDE> : ortho_small_kernel<VEC, 8, SIDE>;
+}
 
 bool is_small(int m, int n) { return m <= SM_SIDE && n <= SM_CTAS * SM_LONG; }
 int tiles_of(int n, int t) { return (n + t - 1) / t; }
@@ -1496,11 +1578,9 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
         p.status = status;
         p.timeout_ns = timeout_ns;
         p.inject = inject;
-        const size_t smem = 1024 + (p.np / 64 + 4 + (cl > 1 ? 4 : 0)) * CHUNK;
-        void (*kernel)(const Small) = cl == 1   ? (vec ? ortho_small_kernel<true, 1> : ortho_small_kernel<false, 1>)
-                                      : cl == 2 ? (vec ? ortho_small_kernel<true, 2> : ortho_small_kernel<false, 2>)
-                                      : cl == 4 ? (vec ? ortho_small_kernel<true, 4> : ortho_small_kernel<false, 4>)
-                                                : (vec ? ortho_small_kernel<true, 8> : ortho_small_kernel<false, 8>);
+        const size_t smem = m <= FEW ? Places<64>::bytes(p.np, cl) : Places<128>::bytes(p.np, cl);
+        void (*kernel)(const Small) = m <= FEW ? (vec ? small_kernel<true, 64>(cl) : small_kernel<false, 64>(cl))
+                                               : (vec ? small_kernel<true, 128>(cl) : small_kernel<false, 128>(cl));
         if ((e = ensure_smem(reinterpret_cast<const void *>(kernel), smem)) != cudaSuccess) return e;
         return launch_pdl(kernel, dim3(B * cl), dim3(ST), smem, s, cl, p);
     }

@@ -1,0 +1,99 @@
+"""Orthogonalised updates on the GPU with few rows or columns, where roundings do not average out: what is off
+before the result's own rounding.
+
+That rounding is averaged away: `out` is called for with N scales s = 2^(j / N), and out / s averaged.  A
+rounding to bf16 is off by at most 2^-8 of a value, evenly, so at most 2^-8 / sqrt(3) in the mean square; the N
+roundings of an entry fall on different places between neighbours, so the mean is 2^-8 / sqrt(3 N) off, in a
+2-norm over k entries up to (1 + 5 / sqrt(k)) times that (five standard deviations).
+
+Up to 64 on the smaller side every operand is two fp16 numbers, 22 bits: an entry is off by at most 2^-22, 2^-22 /
+sqrt(3) in the mean square.  With |X|_2 <= 1.2 and the default coefficients the products b A X + c A A X carry
+that with at most 6.9 + 4.2 = 11.1, for X, for A twice and for P: sqrt(1 + 4 + 1) in the mean square, 3.8e-6 |X|_F a
+step.  What of it lies in directions that X lacks grows by a = 3.44 in every step that follows: 141, 41, 12, 3.4
+and 1 times, 147 in the mean square: FEW = 147 * 3.8e-6 = 5.6e-4."""
+import pytest
+import torch
+
+from expert_routed_ffn_router_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+FEW = 5.6e-4
+KINDS = ["flat", "fall", "low", "one"]
+
+
+def _matrices(Bn, R, C, kind, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    k = min(R, C)
+    if kind == "flat":
+        return r(Bn, R, C)
+    if kind in ("low", "one"):                  # rank far below the sides
+        q = max(1, k // 16) if kind == "low" else 1
+        return r(Bn, R, q) @ r(Bn, q, C)
+    fall = torch.arange(1, k + 1, device=DEV, dtype=F32) ** -1.0
+    return (r(Bn, R, k) * fall) @ r(Bn, k, C) + 0.01 * r(Bn, R, C)
+
+
+def _reference(u, steps=5):
+    u = u.to(F64)
+    x = u.mT if u.shape[1] > u.shape[2] else u
+    n = torch.linalg.vector_norm(x, dim=(1, 2), keepdim=True)
+    x = x / torch.where(n > 0, n, torch.ones_like(n))
+    for _ in range(steps):
+        A = x @ x.mT
+        x = 3.4445 * x + (-4.7750 * A + 2.0315 * (A @ A)) @ x
+    return x.mT if u.shape[1] > u.shape[2] else x
+
+
+def _workspace(shape, fill=0):
+    ws = torch.full((B.moe_orthogonalize_workspace_bytes(*shape),), fill, dtype=torch.uint8, device=DEV)
+    ws[:256] = 0
+    return ws
+
+
+def _off_before_rounding(g, ref, N=64):
+    """-> 2-norms relative to the matrices', and what the mean of the roundings may have left in them"""
+    ws, out = _workspace(g.shape), torch.empty(g.shape, device=DEV, dtype=BF)
+    mean = torch.zeros(g.shape, device=DEV, dtype=F64)
+    for j in range(N):
+        s = torch.tensor(2.0 ** (j / N), dtype=F32).item()
+        B.moe_orthogonalize(g, out, ws, scale=s)
+        mean += out.to(F64) / s
+    assert B.moe_read_status(ws) == 0
+    d = torch.linalg.vector_norm(mean / N - ref, dim=(1, 2)) / torch.linalg.vector_norm(ref, dim=(1, 2))
+    k = g.shape[1] * g.shape[2]
+    return float(d.max()), 2.0 ** -8 / (3 * N) ** 0.5 * (1 + 5 / k ** 0.5)
+
+
+# one CTA a matrix, and clusters of two, four and eight
+SHAPES = [(64, 1, 1), (64, 1, 40), (64, 2, 2), (64, 4, 4), (64, 8, 8), (64, 5, 3), (64, 16, 16), (64, 40, 40), (64, 64, 64),
+          (64, 63, 65), (64, 200, 33), (64, 384, 64), (64, 64, 128), (64, 2, 385), (64, 32, 500), (64, 64, 768), (64, 777, 17),
+          (64, 1500, 4), (64, 64, 1531), (64, 4, 3000), (64, 32, 3000), (64, 3000, 8), (64, 57, 3001), (64, 64, 2500)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("kind", KINDS)
+def test_few_rows_or_columns(shape, kind):
+    g = _matrices(*shape, kind)
+    off, left = _off_before_rounding(g, _reference(g))
+    assert off <= FEW + left
+
+
+@pytest.mark.parametrize("shape", [(5, 24, 40), (5, 300, 64), (5, 30, 700), (5, 2900, 9)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_momentum_steps_zeros_and_nan_with_few_rows(shape, dt):
+    g, m = _matrices(*shape, "flat").to(dt), _matrices(*shape, "fall", seed=1)
+    g[1], m[1] = 0.0, 0.0
+    g[2, 0, 0] = float("nan")
+    g[3, 1, 2] = float("inf")
+    u = g.to(F64) + 0.9 * (0.9 * m.to(F64) + g.to(F64))
+    for steps in (1, 2, 5):
+        ws, out, mo = _workspace(shape), torch.full(shape, 7.0, device=DEV, dtype=BF), m.clone()
+        B.moe_orthogonalize(g, out, ws, momentum=mo, mu=0.9, nesterov=True, steps=steps)
+        assert B.moe_read_status(ws) == 0 and float(out[1].abs().max()) == 0.0
+        assert bool(torch.isnan(out[2]).all()) and bool(torch.isnan(out[3]).all())
+        for i in (0, 4):
+            ref = _reference(u[i:i + 1], steps)
+            assert float((out[i].to(F64) - ref[0]).norm()) <= (FEW + 2.0 ** -8) * float(ref.norm())
