@@ -89,6 +89,7 @@ struct Args {
     CUtensorMap xg[2], xa[2], a, p;
     // the epilogue's pieces of 32 x 32, both ways: A, P, X's first and second numbers, out
     CUtensorMap pa, pp, px[2], pl, po;
+    CUtensorMap a2, p2, pa2, pp2;     // second numbers of A and P (TWO), likewise
     int tall, steps, B, m, R, C;  // m: the smaller side
     int side, n_side;             // tiles of A and P: rows and columns that are kept, tiles of a side
     int tn, nM, nN;               // tiles of X: columns that are kept, tiles in each direction
@@ -209,7 +210,16 @@ __device__ __forceinline__ Tile tile_at(const Args &p, int t)
     return T;
 }
 
-template <int STAGES>
+// Products that follow one another in a tile's sums: where A and P are two numbers each (TWO), A A is A A + A A2 + A2 A
+// and P X is P X + P2 X.
+template <bool TWO>
+__device__ __forceinline__ int terms_of(int mode) { return !TWO || mode == GRAM ? 1 : mode == SQUARE ? 3 : 2; }
+
+// TWO: A and P in two fp16 numbers at the same power of two (up to FEW on the smaller side, whose single tile they
+// are).  Their roundings do not average out over few directions: with one number, the worst of 64 random matrices of
+// 4 x 4096 is 8.2e-3 off, of 16 of 4096 x 33 3.6e-3; so 1.3e-3 at most, what X's rounding leaves (1 of 7168 x 24:
+// 117 us with one number, 129 so; 30 of 7168 x 64 304 and 317).  X in two numbers as well: 1e-4, and 165 and 499 us.
+template <int STAGES, bool TWO>
 __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant__ Args p)
 {
     constexpr int ARRIVE = Ring<STAGES>::ARRIVE, SLAB = Ring<STAGES>::SLAB;
@@ -294,7 +304,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 fence_proxy_async_global();
                 const bool sym = T.mode <= SQUARE;
                 const int m = T.m0 + 128 * r, n = T.n0 + (sym ? p.side : p.tn) / 2 * r, kb0 = T.mode == GRAM ? first_stage(T.part) : 0;
-                const int kbs = T.mode == GRAM ? first_stage(T.part + 1) - kb0 : m_kbs;
+                const int each = T.mode == GRAM ? first_stage(T.part + 1) - kb0 : m_kbs, kbs = terms_of<TWO>(T.mode) * each;
                 const CUtensorMap *am, *bm;
                 bool amn = false, bmn = false;
                 if (T.mode == GRAM) { am = bm = &p.xg[T.k & 1]; amn = bmn = p.tall; }
@@ -308,7 +318,17 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                     unsigned char *a = ring + s * STAGE, *b = a + 2 * HALF;
                     const uint32_t fb = full0 + 8u * s;
                     if (leader) mbar_arrive_expect_tx(&full[s], 2u * STAGE);
-                    const int k = (kb0 + kb) * BK;
+                    int k = (kb0 + kb) * BK;
+                    if (TWO && T.mode != GRAM) {
+                        const int term = kb / each;
+                        k -= term * each * BK;
+                        if (T.mode == SQUARE) {
+                            am = term == 2 ? &p.a2 : &p.a;
+                            bm = term == 1 ? &p.a2 : &p.a;
+                        } else {
+                            (p.tall ? bm : am) = term == 1 ? &p.p2 : &p.p;
+                        }
+                    }
                     if (amn) {
                         tma_load_3d_pair(a, am, fb, m, k, T.b);
                         tma_load_3d_pair(a + HALF, am, fb, m + 64, k, T.b);
@@ -356,7 +376,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 const uint64_t bd0 = smem_desc_sw128(ring0 + 2 * HALF, bmn ? HALF : 16, 1024);
                 const uint32_t as = amn ? 128u : 2u, bs = bmn ? 128u : 2u;
                 const uint32_t id = idesc_f16_f32(TM, static_cast<uint32_t>(T.mode <= SQUARE ? p.side : p.tn), amn, bmn);
-                const int kbs = T.mode == GRAM ? first_stage(T.part + 1) - first_stage(T.part) : m_kbs;
+                const int kbs = terms_of<TWO>(T.mode) * (T.mode == GRAM ? first_stage(T.part + 1) - first_stage(T.part) : m_kbs);
                 if (!mbar_wait(&tempty[b], tph ^ 1u, abort_flag, p.status, tmo)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + b * TN;
@@ -455,8 +475,9 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
         }
     } else if (warp >= EPI0) {
         // ---------------------------------------------------------------- epilogue
-        // What is added to a piece's sums (SQUARE: A; APPLY: X's second number) arrives by TMA, ARRIVE pieces ahead;
-        // the result and what goes beside it (the mirror image; X's second number) leave from a buffer each.
+        // What is added to a piece's sums (SQUARE: A; APPLY: X's second number) arrives by TMA, NEXT pieces ahead;
+        // the result and what goes beside it (the mirror image; a second number) leave from a buffer each.
+        constexpr int EACH = TWO ? 2 : 1, NEXT = ARRIVE / EACH;      // buffers of a piece, pieces
         const int q = warp & 3, half = (warp - EPI0) >> 2;   // lane quarter, half of the columns
         const uint32_t tm0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
         const int r0 = 128 * static_cast<int>(rank) + 32 * q;
@@ -506,9 +527,9 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             const bool sym = T.mode <= SQUARE, loads = T.mode == SQUARE || T.mode == APPLY;
             const int M = sym ? p.m : p.R, N = sym ? p.m : p.C, width = sym ? p.side : p.tn;
             const int m0 = T.m0 + r0, row = m0 + lane;
-            const bool mirror = sym && T.m0 != T.n0;
+            const bool mirror = !TWO && sym && T.m0 != T.n0;
             // X of the step before the last one goes on in its first number alone
-            const bool second = T.mode == APPLY && T.k + 2 < p.steps;
+            const bool second = (T.mode == APPLY && T.k + 2 < p.steps) || (TWO && sym);
             // this warp's pieces: c0 .. end
             const int pieces = width / PC, c0 = half ? (pieces + 1) / 2 : 0;
             int end = half ? pieces : (pieces + 1) / 2;
@@ -516,15 +537,20 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             end = max(c0, min(end, (N - T.n0 + PC - 1) / PC));
             // (lane 0; the warp has read what the buffer held)
             auto load = [&](int c) {
-                const int i = (c - c0) % ARRIVE;
+                const int i = (c - c0) % NEXT * EACH;
                 mbar_arrive_expect_tx(&arrived[i], PIECE);
                 tma_load_3d(slab + i * PIECE, T.mode == SQUARE ? &p.pa : &p.pl, &arrived[i], T.n0 + PC * c, m0, T.b);
                 flight |= 1u << i;
+                if (TWO && sym) {
+                    mbar_arrive_expect_tx(&arrived[i + 1], PIECE);
+                    tma_load_3d(slab + (i + 1) * PIECE, &p.pa2, &arrived[i + 1], T.n0 + PC * c, m0, T.b);
+                    flight |= 2u << i;
+                }
             };
             if (lane == 0) {
                 if (loads && c0 < end && !p.inject) {
                     fence_proxy_async_global();
-                    for (int c = c0; c < min(end, c0 + ARRIVE); ++c) load(c);
+                    for (int c = c0; c < min(end, c0 + NEXT); ++c) load(c);
                 }
                 if (owed >= 0 && !mbar_test(&tfull[b], tph)) settle(0);
             }
@@ -572,16 +598,21 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
             for (int c = c0; c < end; ++c) {
                 const int col = T.n0 + PC * c;
                 // (an address in the 64-byte swizzle goes by the lane's row: 16 bytes i of 64)
-                unsigned char *in = slab + (c - c0) % ARRIVE * PIECE, *first = slab + ARRIVE * PIECE, *side = first + PIECE;
+                unsigned char *in = slab + (c - c0) % NEXT * EACH * PIECE, *first = slab + ARRIVE * PIECE, *side = first + PIECE;
                 auto at = [&](unsigned char *s, int i) -> uint4 * {
                     return reinterpret_cast<uint4 *>(s + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
                 };
                 __syncwarp();
                 if (loads) {
-                    const int i = (c - c0) % ARRIVE;
+                    const int i = (c - c0) % NEXT * EACH;
                     if (!wait_all(&arrived[i], (pph >> i) & 1u, false)) { good = false; break; }
                     pph ^= 1u << i;
                     flight &= ~(1u << i);
+                    if (TWO && sym) {
+                        if (!wait_all(&arrived[i + 1], (pph >> (i + 1)) & 1u, false)) { good = false; break; }
+                        pph ^= 2u << i;
+                        flight &= ~(2u << i);
+                    }
                 }
                 float v[32];
                 if (!parts) {
@@ -605,13 +636,13 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 } else if (T.mode == SQUARE) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 h = *at(in, i);
-                        const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+                        const uint4 h = *at(in, i), l = TWO ? *at(in + PIECE, i) : make_uint4(0, 0, 0, 0);
+                        const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int j = 8 * i + 2 * k;
-                            v[j] = fmaf(cb, f16_lo(hw[k]), v[j] * cc);
-                            v[j + 1] = fmaf(cb, f16_hi(hw[k]), v[j + 1] * cc);
+                            v[j] = fmaf(cb, TWO ? f16_lo(hw[k]) + f16_lo(lw[k]) : f16_lo(hw[k]), v[j] * cc);
+                            v[j + 1] = fmaf(cb, TWO ? f16_hi(hw[k]) + f16_hi(lw[k]) : f16_hi(hw[k]), v[j + 1] * cc);
                         }
                     }
                     if (!mirror) {                   // on the diagonal
@@ -638,7 +669,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 // (what the piece before left in its buffers has left them)
                 __syncwarp();
                 if (lane == 0) {
-                    if (loads && c + ARRIVE < end && !p.inject) load(c + ARRIVE);
+                    if (loads && c + NEXT < end && !p.inject) load(c + NEXT);
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 }
                 __syncwarp();
@@ -663,13 +694,14 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
 #pragma unroll
                 for (int i = 0; i < 4; ++i) *at(first, i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 if (second) {
+                    const float up = TWO && sym ? 1.f : SLO;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t y[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            y[k] = f32x2_to_f16x2((v[8 * i + 2 * k + 1] - f16_hi(w[4 * i + k])) * SLO,
-                                                  (v[8 * i + 2 * k] - f16_lo(w[4 * i + k])) * SLO);
+                            y[k] = f32x2_to_f16x2((v[8 * i + 2 * k + 1] - f16_hi(w[4 * i + k])) * up,
+                                                  (v[8 * i + 2 * k] - f16_lo(w[4 * i + k])) * up);
                         *at(side, i) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
@@ -684,7 +716,7 @@ __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant
                 __syncwarp();
                 if (lane == 0) {
                     tma_store_3d(sm, first, col, m0, T.b);
-                    if (second) tma_store_3d(&p.pl, side, col, m0, T.b);
+                    if (second) tma_store_3d(T.mode == APPLY ? &p.pl : T.mode == GRAM ? &p.pa2 : &p.pp2, side, col, m0, T.b);
                     if (mirror) tma_store_3d(sm, side, m0, col, T.b);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     if (c == c0 + 1) settle(2);
@@ -1443,12 +1475,13 @@ bool is_small(int m, int n) { return m <= SM_SIDE && n <= SM_CTAS * SM_LONG; }
 int tiles_of(int n, int t) { return (n + t - 1) / t; }
 
 // Tiles of a call's products (Args); B > 0.
-struct Plan { int side, n_side, sym, tn, nM, nN, app, group, split; };
+struct Plan { int side, n_side, sym, tn, nM, nN, app, group, split, two; };
 Plan plan_of(int B, int R, int C)
 {
     Plan a{};
     const int most = num_sms() / 2;      // clusters
     const int m = R < C ? R : C, n = R < C ? C : R;
+    a.two = m <= FEW && !is_small(m, n);
     // Sides of the symmetric results' tiles and widths of X's: multiples of 32 up to 256, those whose tiles
     // take least.  What a tile takes beside its columns is worth about 200 of them (24 of 2112 x 1088, widths
     // of X's tiles 224, 192, 128: 1.13, 1.18, 1.40 ms), and 224 columns take as long as 256 (24 of 1088 x 2112:
@@ -1469,15 +1502,15 @@ Plan plan_of(int B, int R, int C)
     const auto triangle = [](long long k) { return k * (k + 1) / 2; };
     a.split = 1;
     if (B * triangle(tiles_of(m, 256)) >= most || is_small(m, n)) {
-        a.side = pick(m, triangle);
+        a.side = a.two ? tiles_of(m, 32) * 32 : pick(m, triangle);
     } else {
         // A round holds all of A's tiles, and gram's sums may go in parts.  Microseconds: a stage about 0.3 whatever
         // the width (latency: four are on their way), a piece of 32 columns 0.7, a part 2 in all and 0.4 for a
         // piece.  (1 of 7168 x 100: 391 us in whole sums, 180 in parts; 6 of 7168 x 200: 422 and 264; 1 of 7168 x
         // 512: 313 and 211; 1 of 7168 x 2048: 562 and 527.)
-        const int gram = tiles_of(n, BK), square = tiles_of(m, BK);
+        const int gram = tiles_of(n, BK), square = (a.two ? 3 : 1) * tiles_of(m, BK);
         double least = 0;
-        for (int k = tiles_of(m, 256); k <= 4 * tiles_of(m, 256); ++k) {
+        for (int k = tiles_of(m, 256); k <= (a.two ? 1 : 4 * tiles_of(m, 256)); ++k) {
             const int t = (tiles_of(m, k) + 31) / 32 * 32, pieces = (t / PC + 1) / 2;
             const long long all = B * triangle(tiles_of(m, t));
             if (all > most) break;
@@ -1512,7 +1545,7 @@ Plan plan_of(int B, int R, int C)
 struct Layout {
     int m, ld, ldm, parts;
     long long chunk;
-    size_t count, size, rest, part, hi[2], lo, A, P, ticket, sums, bytes;
+    size_t count, size, rest, part, hi[2], lo, A, P, A2, P2, ticket, sums, bytes;
 };
 Layout layout(int B, int R, int C, const Plan &t)
 {
@@ -1538,6 +1571,8 @@ Layout layout(int B, int R, int C, const Plan &t)
     L.lo = take(x);
     L.A = take(a);
     L.P = take(a);
+    L.A2 = take(t.two ? a : 0);
+    L.P2 = take(t.two ? a : 0);
     const size_t each = t.split > 1 ? static_cast<size_t>(B) * t.sym * 2 * N_EPI : 0;
     L.ticket = take(each * sizeof(unsigned));
     L.sums = take(each * t.split * PIECES * 32 * 32 * sizeof(float));
@@ -1626,10 +1661,13 @@ cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned lo
         ok = ok && encode(&a.xg[i], x, B, R, C, L.ld, tall ? 64 : 128, 64) &&
              encode(&a.xa[i], x, B, R, C, L.ld, tall ? 128 : 64, 64) && encode(&a.px[i], x, B, R, C, L.ld, 32, 32);
     }
+    if (t.two)
+        ok = ok && encode(&a.a2, w + L.A2, B, m, m, L.ldm, 128, 64) && encode(&a.p2, w + L.P2, B, m, m, L.ldm, 128, 64) &&
+             encode(&a.pa2, w + L.A2, B, m, m, L.ldm, 32, 32) && encode(&a.pp2, w + L.P2, B, m, m, L.ldm, 32, 32);
     if (a.tma_out) ok = ok && encode(&a.po, f.out, B, R, C, C, 32, 32);
     if (!ok) return cudaErrorInvalidValue;
     const bool longer = m >= LONG_SUMS;
-    void (*kernel)(const Args) = longer ? ortho_gemm_kernel<5> : ortho_gemm_kernel<4>;
+    void (*kernel)(const Args) = longer ? ortho_gemm_kernel<5, false> : t.two ? ortho_gemm_kernel<4, true> : ortho_gemm_kernel<4, false>;
     const size_t smem = longer ? Ring<5>::BYTES : Ring<4>::BYTES;
     if ((e = ensure_smem(reinterpret_cast<const void *>(kernel), smem)) != cudaSuccess) return e;
     const int gram = a.split * a.sym, widest = B * (gram > a.app ? gram : a.app);

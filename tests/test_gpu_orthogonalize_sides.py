@@ -81,7 +81,47 @@ def test_few_rows_or_columns(shape, kind):
     assert off <= FEW + left
 
 
-@pytest.mark.parametrize("shape", [(5, 24, 40), (5, 300, 64), (5, 30, 700), (5, 2900, 9)])
+# One shape to a launch over a list of tiles: A and P in two numbers, X in one for the products.  Its rounding, 2^-11
+# an entry and 2^-11 / sqrt(3) in the mean square, enters each product with P once and A in two places, over sums of
+# n > 3000 entries that average it out; so a step adds |P - a I| <= 11.1 times it at most where it does not
+# average, 3.1e-3 |X|_F, and five steps of random roundings sqrt(5) of that where all singular values lie at
+# |P - a I|'s largest, s = 1.2.  They lie around 1, where |P - a I| = 2.7: THIN = 2.7 * 2^-11 / sqrt(3) * sqrt(5) = 1.7e-3.
+THIN = 1.7e-3
+
+
+@pytest.mark.parametrize("shape", [(64, 1, 3100), (64, 2, 3100), (64, 4, 4096), (64, 8, 5000), (64, 3201, 16), (64, 32, 3300), (64, 4096, 33),
+                                   (16, 64, 5000), (2, 7168, 24), (1, 16, 7168), (3, 64, 7169), (30, 7168, 64), (2, 32768, 8), (1, 3, 32768)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_few_rows_or_columns_of_great_length(shape, kind):
+    g = _matrices(*shape, kind)
+    off, left = _off_before_rounding(g, _reference(g))
+    assert off <= THIN + left
+
+
+@pytest.mark.parametrize("shape", [(2, 4, 4096), (1, 7168, 24), (200, 64, 4000), (3, 3333, 63)])
+def test_great_length_repeats_in_a_graph_and_records_waits(shape):
+    g, ws = _matrices(*shape, "fall").to(BF), _workspace(shape, 255)
+    out, again = (torch.empty(shape, device=DEV, dtype=BF) for _ in range(2))
+    B.moe_orthogonalize(g, out, ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_orthogonalize(g, again, ws)
+    for _ in range(3):
+        again.zero_()
+        graph.replay()
+        assert torch.equal(again, out)
+    assert B.moe_read_status(ws) == 0
+    B.moe_debug_set_wait_limit(2_000_000, 1)
+    try:
+        B.moe_orthogonalize(g, again, ws)
+        assert B.moe_read_status(ws) == B.MOE_ERR_DEVICE_TIMEOUT
+    finally:
+        B.moe_debug_set_wait_limit(0, 0)
+    B.moe_orthogonalize(g, again, ws)
+    assert B.moe_read_status(ws) == 0 and torch.equal(again, out)
+
+
+@pytest.mark.parametrize("shape", [(5, 24, 40), (5, 300, 64), (5, 30, 700), (5, 2900, 9), (5, 6, 3200)])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_momentum_steps_zeros_and_nan_with_few_rows(shape, dt):
     g, m = _matrices(*shape, "flat").to(dt), _matrices(*shape, "fall", seed=1)
@@ -96,4 +136,4 @@ def test_momentum_steps_zeros_and_nan_with_few_rows(shape, dt):
         assert bool(torch.isnan(out[2]).all()) and bool(torch.isnan(out[3]).all())
         for i in (0, 4):
             ref = _reference(u[i:i + 1], steps)
-            assert float((out[i].to(F64) - ref[0]).norm()) <= (FEW + 2.0 ** -8) * float(ref.norm())
+            assert float((out[i].to(F64) - ref[0]).norm()) <= (THIN + 2.0 ** -8) * float(ref.norm())
