@@ -820,19 +820,20 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Square sums of u, of 2^60 u and of 2^-80 u: one of them holds |u| to fp32's precision whatever the
-// size of the entries.
-constexpr float UP = 1152921504606846976.f, DOWN = 1.f / (UP * 1048576.f);
+// Square sums of u, of 2^90 u and of 2^-80 u: one of them holds |u| to fp32's precision whatever the
+// size of the entries, subnormal ones too (2^-149 and up: the square of 2^90 u is 2^-118 then).
+constexpr float TWO_30 = 1073741824.f, TWO_40 = 1024.f * TWO_30, TWO_60 = TWO_30 * TWO_30;
+constexpr float UP = TWO_60 * TWO_30, DOWN = 1.f / (TWO_40 * TWO_40);
 
 // SX x = (u f) times the result, f a power of two, from the square sums.  (One of u below 2^-60 may have
 // lost terms to underflow, one above 2^100 to overflow; those at the other scales are then within
-// range.)  A matrix of zeros stays one; an infinity or a NaN makes it NaN.
+// range: that of 2^90 u below 2^120.)  A matrix of zeros stays one; an infinity or a NaN makes it NaN.
 __device__ __forceinline__ float x_factor(float s0, float s1, float s2, float &f)
 {
     float s = s0;
     f = 1.f;
-    if (!(s0 >= 1.f / UP)) { f = UP; s = s1; }
-    else if (!(s0 <= UP * 1099511627776.f)) { f = DOWN; s = s2; }
+    if (!(s0 >= 1.f / TWO_60)) { f = UP; s = s1; }
+    else if (!(s0 <= TWO_60 * TWO_40)) { f = DOWN; s = s2; }
     return s > 0.f ? (s <= 3.402823466e38f ? SX / sqrtf(s) : s - s) : s;
 }
 

@@ -137,3 +137,24 @@ def test_momentum_steps_zeros_and_nan_with_few_rows(shape, dt):
         for i in (0, 4):
             ref = _reference(u[i:i + 1], steps)
             assert float((out[i].to(F64) - ref[0]).norm()) <= (THIN + 2.0 ** -8) * float(ref.norm())
+
+
+@pytest.mark.parametrize("shape", [(4, 40, 56), (4, 41, 57), (4, 100, 90), (4, 60, 1000), (4, 333, 250), (4, 8, 3200)])
+@pytest.mark.parametrize("momentum", [False, True])
+def test_subnormal_entries(shape, momentum):
+    # (made on the host, so that nothing on the way takes them for zero; the reference takes them as they are)
+    g = _matrices(*shape, "flat").cpu().to(F64)
+    for i, size in enumerate((1e-39, 1e-41, 1e-43, 3e-45)):
+        g[i] *= size / float(g[i].abs().max())
+    for dt in (F32, BF):
+        u = g.to(F32).to(dt)
+        live = [i for i in range(4) if float(u[i].to(F64).abs().max()) > 0.0]
+        assert live == ([0, 1, 2, 3] if dt == F32 else [0])      # (bf16's smallest number is 9.2e-41)
+        ref = _reference(u.to(DEV))
+        ws, out = _workspace(shape), torch.full(shape, 7.0, device=DEV, dtype=BF)
+        m = torch.zeros(shape, device=DEV) if momentum else None
+        B.moe_orthogonalize(u.to(DEV), out, ws, momentum=m)
+        assert B.moe_read_status(ws) == 0
+        for i in range(4):
+            # (sides above 64: the updates' own error; 6.2e-3 bounds it)
+            assert float((out[i].to(F64) - ref[i]).norm()) <= (6.2e-3 + 2.0 ** -8) * float(ref[i].norm()), (dt, i)
