@@ -27,8 +27,10 @@
 // The last step does without: its factor of 3.4 on a rounding does not show.  (Rounded to fp16 in every
 // step, gradients of rank 16 come out 3e-2 off, in bf16 0.2; so they are 1.5e-3 off.)  A and a I + P are
 // rounded to fp16 once each: their error acts through products with X alone, and what X has not is not
-// amplified.  In all 0.5e-3 to 1.7e-3 off, the largest for flat spectra and for ranks far below the
-// sides; the rounding of the bf16 result is 1.7e-3.
+// amplified.  In all 0.5e-3 to 2.0e-3 off over random matrices with five default steps, the most for flat
+// spectra, and 2.1e-3 to 2.8e-3 with a rank of one; the rounding of the bf16 result is 1.7e-3.  Over few directions
+// A's and P's roundings do not average out: up to FEW on the smaller side these are two fp16 numbers each, and where
+// one launch does all steps X is too (TWO, SIDE 64 below).
 //
 // Tiles, roles and waits as in ffn_bwd.cu: clusters of two CTAs, 2-SM MMAs of 256 x 256, 64 deep
 // stages of 32 KB a CTA, two accumulators in tensor memory, eight epilogue warps, all waits
