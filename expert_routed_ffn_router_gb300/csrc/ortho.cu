@@ -1046,7 +1046,7 @@ struct Places {
 };
 
 struct Small {
-    Prepare q;
+    Prepare q;                        // of it: the matrices and the momentum
     int tall, m, n, np;               // sides of X (m <= n), columns of a CTA (a multiple of 64)
     int steps;
     float c[3 * MAX_STEPS];
@@ -1585,7 +1585,11 @@ Layout layout(int B, int R, int C, const Plan &t)
 
 }  // namespace
 
-size_t ortho_bytes(int B, int R, int C) { return B > 0 ? layout(B, R, C, plan_of(B, R, C)).bytes : 0; }
+// (small matrices need none: ortho_small_kernel)
+size_t ortho_bytes(int B, int R, int C)
+{
+    return B > 0 && !is_small(R < C ? R : C, R < C ? C : R) ? layout(B, R, C, plan_of(B, R, C)).bytes : 0;
+}
 
 cudaError_t launch_ortho(const Ortho &f, void *scratch, int *status, unsigned long long timeout_ns, int inject,
                          cudaStream_t s)

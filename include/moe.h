@@ -574,9 +574,10 @@ int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, in
  *            2.0315 in every step.  The iterates' singular values s must stay below 8, and |a| +
  *            |b| s^2 + |c| s^4 below 120 (fp16's range).
  *   out      bf16 [B, R, C] (may be g's own memory where g is bf16)
- *   ws       at least moe_orthogonalize_workspace_bytes(B, R, C) bytes (0 for an invalid shape):
- *            about B (6 R C + 4 min(R, C)^2) bytes, and up to 20 MB for few matrices with long sums
- *            (so fewer matrices may need more than many)
+ *   ws       at least moe_orthogonalize_workspace_bytes(B, R, C) bytes (0 for an invalid shape): 256
+ *            for up to 128 on the smaller side and 8 x 384 on the larger; else about B (6 R C + 4
+ *            min(R, C)^2) bytes, and up to 20 MB for few matrices with long sums (so fewer matrices
+ *            may need more than many)
  * fp16 products with fp32 sums on the tensor cores; X is carried in 22 bits, so that directions with
  * small singular values keep their precision.  With the default coefficients and five steps, a matrix is
  * off before out's rounding (2-norm, relative) by up to

@@ -22,6 +22,14 @@ def test_workspace_of_no_matrices():
     assert subprocess.run([sys.executable, "-c", code], timeout=300, cwd=ROOT).returncode == 0
 
 
+def test_workspace_of_matrices_that_stay_on_the_chip():
+    # up to 128 on the smaller side and 8 x 384 on the larger, all steps run in shared and tensor memory
+    for b, r, c in ((256, 128, 3000), (65535, 128, 128), (1, 1, 1), (3, 3071, 127), (700, 24, 17)):
+        assert 0 < B.moe_orthogonalize_workspace_bytes(b, r, c) <= 4096
+    for r, c in ((129, 130), (128, 3073), (3073, 1), (300, 520)):
+        assert B.moe_orthogonalize_workspace_bytes(2, r, c) > 2 * 6 * r * c
+
+
 def _calls(monkeypatch):
     """Every call's matrices, bytes of workspace and addresses, in place of the kernels."""
     seen = []
