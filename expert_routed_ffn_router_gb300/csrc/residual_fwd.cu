@@ -9,7 +9,7 @@
 // fp32 with two norms: 326 us with an exchange for each, 277 us so).
 //
 // What bounds it: memory in fp32 (16384 x 7168, RMS norm of y, layer norm of r: 240 us, 6.8 TB/s, the copy
-// bandwidth), instructions in bf16 (180-190 us, 5.2 TB/s).
+// bandwidth); in bf16 (180-190 us, 5.2 TB/s) memory is at three quarters and the schedulers at 59%.
 //
 // The next norm's statistics are those of r as it is stored: with a bf16 stream, what the backward
 // pass reads.

@@ -158,3 +158,43 @@ def test_subnormal_entries(shape, momentum):
         for i in range(4):
             # (sides above 64: the updates' own error; 6.2e-3 bounds it)
             assert float((out[i].to(F64) - ref[i]).norm()) <= (6.2e-3 + 2.0 ** -8) * float(ref[i].norm()), (dt, i)
+
+
+@pytest.mark.parametrize("shape", [(3, 40, 56), (3, 300, 64), (3, 30, 700), (3, 700, 21), (5, 64, 2999), (2, 6, 3200), (2, 3300, 64)])
+def test_few_rows_over_their_own_memory_and_in_graphs(shape):
+    g, ws = _matrices(*shape, "fall").to(BF), _workspace(shape, 255)
+    out, same = torch.empty_like(g), g.clone()
+    B.moe_orthogonalize(g, out, ws)
+    B.moe_orthogonalize(same, same, ws)
+    assert torch.equal(same, out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_orthogonalize(g, same, ws)
+    for _ in range(2):
+        same.zero_()
+        graph.replay()
+        assert torch.equal(same, out)
+    B.moe_debug_set_wait_limit(2_000_000, 1)
+    try:
+        B.moe_orthogonalize(g, same, ws)
+        assert B.moe_read_status(ws) == B.MOE_ERR_DEVICE_TIMEOUT
+    finally:
+        B.moe_debug_set_wait_limit(0, 0)
+    B.moe_orthogonalize(g, same, ws)
+    assert B.moe_read_status(ws) == 0 and torch.equal(same, out)
+
+
+def test_calls_of_every_kind_at_once():
+    shapes = [(64, 32, 3000), (200, 40, 40), (30, 700, 60), (40, 128, 1024), (3, 4096, 33), (6, 300, 520)]
+    gs = [_matrices(*s, "fall").to(BF) for s in shapes]
+    outs, wss, streams = [torch.empty_like(g) for g in gs], [_workspace(s) for s in shapes], [torch.cuda.Stream() for _ in shapes]
+    want = [torch.empty_like(g) for g in gs]
+    for g, o, ws in zip(gs, want, wss):
+        B.moe_orthogonalize(g, o, ws)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, o, ws, st in zip(gs, outs, wss, streams):
+            B.moe_orthogonalize(g, o, ws, stream=st)
+    torch.cuda.synchronize()
+    for o, w, ws in zip(outs, want, wss):
+        assert torch.equal(o, w) and B.moe_read_status(ws) == 0

@@ -126,3 +126,15 @@ def test_the_stated_accuracy(shape, kind):
     g = _matrices(*shape, kind)
     ref = _formula(g, [ABC] * 5, F64)
     assert _off(_mean(g, [ABC] * 5), ref) <= STATED + _left(g)
+
+
+# The last sizes of one launch (a cluster's CTAs all full but for a column) and the first of the other one; the borders
+# between operands in one and in two numbers.
+@pytest.mark.parametrize("shape", [(8, 128, 3071), (8, 3071, 128), (8, 120, 3073), (8, 3073, 128), (16, 64, 3071), (16, 3073, 64), (16, 65, 3071),
+                                   (16, 64, 384), (16, 385, 64), (16, 65, 385), (16, 128, 768), (16, 769, 128)])
+@pytest.mark.parametrize("kind", ["flat", "one"])
+def test_at_the_borders_of_the_ways(shape, kind):
+    g = _matrices(*shape, kind)
+    ref = _formula(g, [ABC] * 5, F64)
+    few, longer = min(shape[1:]) <= 64, max(shape[1:]) > 8 * 384
+    assert _off(_mean(g, [ABC] * 5), ref) <= (STATED if not few else 1.4e-3 if longer else 2e-4) + _left(g)
