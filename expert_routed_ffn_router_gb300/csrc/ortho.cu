@@ -219,7 +219,7 @@ __device__ __forceinline__ int terms_of(int mode) { return !TWO || mode == GRAM 
 
 // TWO: A and P in two fp16 numbers at the same power of two (up to FEW on the smaller side, whose single tile they
 // are).  Their roundings do not average out over few directions: with one number, the worst of 64 random matrices of
-// 4 x 4096 is 8.2e-3 off, of 16 of 4096 x 33 3.6e-3; so 1.3e-3 at most, what X's rounding leaves (1 of 7168 x 24:
+// 4 x 4096 is 8.2e-3 off, of 16 of 4096 x 33 3.6e-3; so 1.4e-3 at most, what X's rounding leaves (1 of 7168 x 24:
 // 117 us with one number, 129 so; 30 of 7168 x 64 304 and 317).  X in two numbers as well: 1e-4, and 165 and 499 us.
 template <int STAGES, bool TWO>
 __global__ void __launch_bounds__(NT, 1) ortho_gemm_kernel(const __grid_constant__ Args p)
@@ -1021,7 +1021,7 @@ __global__ void __launch_bounds__(PT) ortho_scale_kernel(const Prepare p)
 // SIDE 64: up to FEW on the smaller side, every operand is two fp16 numbers, hi + lo (22 bits; lo at hi's power
 // of two, where its last bit is 2^-24 / SX or less), and a product is hi hi + hi lo + lo hi.  With one number
 // the roundings of X, A and P do not average out over few directions: of 64 random matrices of 2 x 2 the worst
-// comes out 9.8e-3 off, of 4 x 3000 7.3e-3, of 32 x 3000 3.5e-3; so 1e-5, and 2e-4 with ranks far below the sides
+// comes out 9.8e-3 off, of 4 x 3000 7.3e-3, of 32 x 3000 3.5e-3; so 1e-5, and up to 3e-4 with ranks far below the sides
 // (700 of 24 x 17: 74 us with one number, 89 so; 16 of 64 x 256 24 and 34 us; 8 of 64 x 3000, a cluster of
 // eight each, 55 and 53).  A chunk of an operand is 64 rows then: as the first operand of a product of 128 rows
 // it reads on into what lies behind it, for rows of the sums that nothing reads.

@@ -581,8 +581,9 @@ int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, in
  * fp16 products with fp32 sums on the tensor cores; X is carried in 22 bits, so that directions with
  * small singular values keep their precision.  With the default coefficients and five steps, a matrix is
  * off before out's rounding (2-norm, relative) by up to
- *     2e-4    up to 64 on the smaller side and 8 x 384 on the larger: every operand in 22 bits
- *     1.4e-3  up to 64 and longer: A and b A + c A A in 22 bits
+ *     3e-4    up to 64 on the smaller side and 8 x 384 on the larger: every operand in 22 bits
+ *     1.4e-3  up to 64 and longer: A and b A + c A A in 22 bits (1.8e-3 for one row or column of bf16
+ *             numbers: few mantissas, each rounded one way)
  *     2.2e-3  else, typically 0.5e-3 to 2e-3; 2.8e-3 with a rank of one
  * More steps: above 64, 4.4e-3 with ten and 1e-2 with 32, where no singular value is far below the others.
  * What rounding leaves in directions that a matrix lacks grows by a in every step, in plain fp32 too: with a
@@ -590,9 +591,9 @@ int moe_residual_norm_backward(const void *dn, const void *dr, const void *y, in
  * 4e-3, up to 6e-2 in both with ten, and all of the result from about 16 on.
  * Other coefficients: an error of X grows by the slopes |a + 3 b s^2 + 5 c s^4| that its singular values s
  * meet.  (8.29, -23.6, 17.3) and four gentler steps: 2e-3 to 2.4e-2 above 64, 5e-2 for flat 16 x 3200.
- * A matrix of zeros gives zeros; one with an infinity or a NaN gives NaN.  The
- * results repeat bit for bit (a matrix's may differ in their last bits with the number of matrices
- * beside it: long sums of few matrices are formed in parts).  R, C <= 32768, B <= 65535, steps <= 32 (else
+ * A matrix of zeros gives zeros; one with an infinity or a NaN gives NaN.  The results repeat bit for
+ * bit (a matrix's may differ in their last bits with the number of matrices beside it: long sums of few
+ * matrices are formed in parts).  R, C <= 32768, B <= 65535, steps <= 32 (else
  * MOE_ERR_UNSUPPORTED_SHAPE); any R and C from 1 on.  B == 0 enqueues nothing. */
 size_t moe_orthogonalize_workspace_bytes(int B, int R, int C);
 int moe_orthogonalize(const void *g, int g_fp32, float *momentum, float mu, int nesterov, int B, int R,

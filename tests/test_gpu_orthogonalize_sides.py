@@ -98,6 +98,14 @@ def test_few_rows_or_columns_of_great_length(shape, kind):
     assert off <= THIN + left
 
 
+@pytest.mark.parametrize("shape", [(200, 1, 3100), (200, 4843, 1), (200, 2, 4000), (1, 24, 32768)])
+def test_few_mantissas_of_great_length(shape):
+    for kind in ("fall", "one"):
+        g = _matrices(*shape, kind).to(BF)
+        off, left = _off_before_rounding(g, _reference(g))
+        assert off <= THIN + left
+
+
 @pytest.mark.parametrize("shape", [(2, 4, 4096), (1, 7168, 24), (200, 64, 4000), (3, 3333, 63)])
 def test_great_length_repeats_in_a_graph_and_records_waits(shape):
     g, ws = _matrices(*shape, "fall").to(BF), _workspace(shape, 255)
